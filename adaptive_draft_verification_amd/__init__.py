@@ -21,13 +21,15 @@ LIB_PATH = os.path.join(_HERE, "libspecverify.so")
 
 SV_OK, SV_ERR_NULL, SV_ERR_SHAPE, SV_ERR_DTYPE, SV_ERR_VALUE, SV_ERR_WORKSPACE, SV_ERR_LAUNCH, \
     SV_ERR_CAPACITY, SV_ERR_DATA = range(9)
-SV_F32, SV_BF16 = 0, 1
+SV_F32, SV_BF16, SV_E4M3 = 0, 1, 2
 SV_STOCHASTIC, SV_GREEDY = 0, 1
 SV_DEV_BAD_CU_ROWS, SV_DEV_BAD_TOKEN, SV_DEV_NONFINITE = 1, 2, 4
 SV_DEV_BAD_DRAFT_LEN, SV_DEV_BAD_COST, SV_DEV_BAD_KEPT = 8, 16, 32
+SV_DEV_BAD_PAGE, SV_DEV_BAD_CTX = 64, 128
 SV_MAX_BUDGET_SLOTS, SV_MAX_DRAFT, SV_MAX_VOCAB = 8192, 64, 1048576
 SV_MAX_VERIFY_SLOTS = 524288
 SV_NOALLOC_WS_BYTES = 8388608
+SV_MAX_ATTEND_SLOTS, SV_MAX_APPEND_VALUES = 16777216, 1073741824
 
 EXPORTED = ["sv_status_str", "sv_budget_workspace_bytes", "sv_verify_workspace_bytes",
             "sv_cost_table_prepare", "sv_budget_select", "sv_budget_allocate",
@@ -35,7 +37,18 @@ EXPORTED = ["sv_status_str", "sv_budget_workspace_bytes", "sv_verify_workspace_b
             "sv_uniform_k_select", "sv_pack_varlen",
             "sv_verify",
             "sv_verify_stages", "sv_verify_noalloc", "sv_accept_stats", "sv_calibrate_update", "sv_calibrate_predict",
-            "sv_philox_uniforms"]
+            "sv_philox_uniforms",
+            "sv_cache_append", "sv_cache_attend", "sv_cache_attend_workspace_bytes"]
+
+
+class _Cache(ctypes.Structure):
+    """sv_cache of the C header."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("dtype", ctypes.c_int),
+                ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("page_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p)]
 
 
 class SvError(RuntimeError):
@@ -80,6 +93,11 @@ def _load():
         "sv_calibrate_update": (ctypes.c_int, [vp, vp, vp, vp, vp, vp, i32, i32, f32, vp, vp]),
         "sv_calibrate_predict": (ctypes.c_int, [vp, vp, vp, vp, i32, i32, vp, vp]),
         "sv_philox_uniforms": (ctypes.c_int, [u64, u64, i32, i32, vp, vp, vp]),
+        "sv_cache_append": (ctypes.c_int, [vp, vp, i32, vp, vp, i64, vp, vp, i32, vp, i32, vp,
+                                           vp]),
+        "sv_cache_attend_workspace_bytes": (sz, [i32, i32, i32, i32, i32, i32, i32]),
+        "sv_cache_attend": (ctypes.c_int, [vp, vp, i32, vp, i64, i64, i32, vp, vp, i32, i32, f32,
+                                           vp, i64, vp, vp, vp, sz, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -98,6 +116,38 @@ def _ptr(t):
 def _stream(stream):
     if stream is None:
         stream = torch.cuda.current_stream()
+    return ctypes.c_void_p(stream.cuda_stream)
+
+
+def _same_device(first, *others):
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise ValueError("every tensor must be on one device")
+
+
+class _on_device:
+    """Makes a tensor's device current for a launch on one of its streams."""
+
+    def __init__(self, t, stream):
+        if stream is not None and stream.device != t.device:
+            raise ValueError("the stream must be on the tensors' device")
+        self.want, self.back = t.device.index, None
+
+    def __enter__(self):
+        cur = torch.cuda.current_device()
+        if cur != self.want:
+            self.back = cur
+            torch.cuda.set_device(self.want)
+
+    def __exit__(self, *exc):
+        if self.back is not None:
+            torch.cuda.set_device(self.back)
+
+
+def _stream_on(t, stream):
+    """The stream given, else the current one of the tensor's device."""
+    if stream is None:
+        stream = torch.cuda.current_stream(t.device)
     return ctypes.c_void_p(stream.cuda_stream)
 
 
@@ -434,6 +484,108 @@ def sv_philox_uniforms(seed, step, u, v, stream=None):
     _check(_lib.sv_philox_uniforms(int(seed), int(step), n, n_pos, _ptr(u), _ptr(v),
                                    _stream(stream)),
            "sv_philox_uniforms")
+
+
+class PagedCache:
+    """A paged key-value cache: k and v [n_pages, page_size, n_kv_heads, head_dim] (bfloat16 or
+    float8_e4m3fn), any strides over pages, positions and heads that both share, the last
+    dimension contiguous; k_scale, v_scale [n_kv_heads] f32 (float8 caches)."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        if not (k.is_cuda and v.is_cuda) or k.device != v.device:
+            raise ValueError("k and v must be device tensors on one device")
+        if k.dtype not in _CACHE_DTYPES or v.dtype != k.dtype:
+            raise ValueError("k and v must both be bfloat16 or float8_e4m3fn")
+        if k.dim() != 4 or v.shape != k.shape or v.stride() != k.stride() or k.stride(3) != 1:
+            raise ValueError("k and v must be [n_pages, page_size, n_kv_heads, head_dim] with "
+                             "the same strides, the last dimension contiguous")
+        for name, s in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if s is None:
+                continue
+            if k.dtype == torch.bfloat16:
+                raise ValueError("scales belong to float8 caches")
+            _dev(s, torch.float32, name, 1)
+            if s.numel() != k.shape[2] or s.device != k.device:
+                raise ValueError(f"{name} must be [n_kv_heads] on the cache's device")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.n_kv_heads, self.head_dim = k.shape[2], k.shape[3]
+        self.page_size = k.shape[1]
+        addr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+        self._c = _Cache(k.data_ptr(), v.data_ptr(), _CACHE_DTYPES[k.dtype], *k.shape,
+                         *k.stride()[:3], addr(k_scale), addr(v_scale))
+
+
+_CACHE_DTYPES = {torch.bfloat16: SV_BF16, torch.float8_e4m3fn: SV_E4M3}
+
+
+def _rows(t, name, heads, dim):
+    """Row stride of a [rows, heads, dim] bfloat16 tensor whose rows are contiguous."""
+    if not t.is_cuda or t.dtype != torch.bfloat16 or t.dim() != 3 \
+            or (heads is not None and t.shape[1] != heads) or t.shape[2] != dim:
+        raise ValueError(f"{name} must be a bfloat16 device tensor "
+                         f"[rows, {heads or 'heads'}, {dim}]")
+    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != dim):
+        raise ValueError(f"{name} must have contiguous heads within a row")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * dim
+
+
+def sv_cache_append(cache, page_table, k, v, row_req, row_pos, ctx_len, dev_error=None,
+                    stream=None):
+    """Rows k, v [rows, n_kv_heads, head_dim] bf16 into the cache, row i at position
+    ctx_len[row_req[i]] + row_pos[i] (the maps pack_varlen writes; -1: skipped);
+    page_table [n, max_pages] i32, ctx_len [n] i32."""
+    _dev(page_table, torch.int32, "page_table", 2)
+    for name, t in (("row_req", row_req), ("row_pos", row_pos), ("ctx_len", ctx_len),
+                    ("dev_error", dev_error)):
+        _dev(t, torch.int32, name, 1)
+    ld = _rows(k, "k", cache.n_kv_heads, cache.head_dim)
+    if _rows(v, "v", cache.n_kv_heads, cache.head_dim) != ld or v.shape[0] != k.shape[0]:
+        raise ValueError("k and v must have the same rows and row stride")
+    n, max_pages = page_table.shape
+    if row_req.numel() != k.shape[0] or row_pos.numel() != k.shape[0] or ctx_len.numel() != n:
+        raise ValueError("row_req, row_pos need one entry a row, ctx_len one a request")
+    _same_device(cache.k, page_table, k, v, row_req, row_pos, ctx_len, dev_error)
+    with _on_device(cache.k, stream):
+        _check(_lib.sv_cache_append(ctypes.byref(cache._c), _ptr(page_table), max_pages, _ptr(k),
+                                    _ptr(v), ld, _ptr(row_req), _ptr(row_pos), k.shape[0],
+                                    _ptr(ctx_len), n, _ptr(dev_error),
+                                    _stream_on(cache.k, stream)),
+               "sv_cache_append")
+
+
+def sv_cache_attend_workspace_bytes(n_req, k_max, n_heads, n_kv_heads, head_dim, max_pages,
+                                    page_size):
+    return int(_lib.sv_cache_attend_workspace_bytes(n_req, k_max, n_heads, n_kv_heads, head_dim,
+                                                    max_pages, page_size))
+
+
+def sv_cache_attend(cache, page_table, q, cu_rows, ctx_len, k_max, scale, out, ws=None,
+                    out_lse=None, dev_error=None, stream=None):
+    """Packed rows q [rows, n_heads, head_dim] bf16 -> out (same shape): row j of request r
+    (packed row cu_rows[r] + j) sees the cache's positions 0 .. ctx_len[r] + j.
+    ws: uint8 device buffer of sv_cache_attend_workspace_bytes(...) bytes (None if 0);
+    out_lse [rows, n_heads] f32."""
+    _dev(page_table, torch.int32, "page_table", 2)
+    for name, t in (("cu_rows", cu_rows), ("ctx_len", ctx_len), ("dev_error", dev_error)):
+        _dev(t, torch.int32, name, 1)
+    _dev(out_lse, torch.float32, "out_lse", 2)
+    _dev(ws, torch.uint8, "ws", 1)
+    q_ld = _rows(q, "q", None, cache.head_dim)
+    heads = q.shape[1]
+    out_ld = _rows(out, "out", heads, cache.head_dim)
+    n, max_pages = page_table.shape
+    if out.shape != q.shape or cu_rows.numel() != n + 1 or ctx_len.numel() != n:
+        raise ValueError("out must have q's shape; cu_rows [n+1], ctx_len [n]")
+    if out_lse is not None and tuple(out_lse.shape) != (q.shape[0], heads):
+        raise ValueError("out_lse must be [rows, n_heads]")
+    _same_device(cache.k, page_table, q, cu_rows, ctx_len, out, ws, out_lse, dev_error)
+    with _on_device(cache.k, stream):
+        _check(_lib.sv_cache_attend(ctypes.byref(cache._c), _ptr(page_table), max_pages, _ptr(q),
+                                    q_ld, q.shape[0], heads, _ptr(cu_rows), _ptr(ctx_len), n,
+                                    int(k_max), float(scale), _ptr(out), out_ld, _ptr(out_lse),
+                                    _ptr(dev_error), _ptr(ws), 0 if ws is None else ws.numel(),
+                                    _stream_on(cache.k, stream)),
+               "sv_cache_attend")
 
 
 # ----------------------------------------------------------------------------

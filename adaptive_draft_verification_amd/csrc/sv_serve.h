@@ -1,0 +1,83 @@
+// Arguments and launchers of the paged cache (internal; sv_cache_api.cpp
+// validates before calling these).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "libspecverify.h"
+
+namespace sv {
+
+struct AppendArgs {
+    sv_cache cache;
+    const int32_t* page_table;
+    int max_pages;
+    const void* k;
+    const void* v;
+    int64_t kv_ld;
+    const int32_t* row_req;
+    const int32_t* row_pos;
+    int n_rows;
+    const int32_t* ctx_len;
+    int n_req;
+    int32_t* dev_error;
+};
+hipError_t launch_cache_append(const AppendArgs& a, hipStream_t stream);
+
+struct AttendArgs {
+    sv_cache cache;
+    const int32_t* page_table;
+    int max_pages;
+    const void* q;
+    int64_t q_ld;
+    int64_t q_rows;
+    int n_heads;
+    int group;  // query heads per kv head
+    const int32_t* cu_rows;
+    const int32_t* ctx_len;
+    int n_req;
+    int k_max;
+    float scale;
+    void* out;
+    int64_t out_ld;
+    float* out_lse;
+    int32_t* dev_error;
+    int slot_tiles, slot_blocks, parts;  // AttendPlan's
+    float* part_out;                     // parts > 1: [n_req, n_heads, k_max + 1, parts, head_dim]
+    float* part_ml;                      //            [..., parts, 2] maximum and sum
+};
+hipError_t launch_cache_attend(const AttendArgs& a, hipStream_t stream);
+
+// Positions in each part of a request's length: a multiple of 128 (four waves
+// of 32), so that short requests use fewer parts than the launch has.
+inline __host__ __device__ int part_len(int len, int parts) {
+    return ((len + parts - 1) / parts + 127) / 128 * 128;
+}
+
+// How an attend call is cut into workgroups: by host-known sizes alone.
+struct AttendPlan {
+    int slot_tiles;   // 16-slot tiles a workgroup takes: 1, 2 or 4
+    int slot_blocks;  // workgroups over a (request, kv head)'s query slots
+    int parts;        // workgroups over the cached positions
+    AttendPlan(int n_req, int k_max, int n_heads, int n_kv_heads, int head_dim, int64_t capacity) {
+        const int slots = (k_max + 1) * (n_heads / n_kv_heads);
+        slot_tiles = slots <= 16 ? 1 : slots <= 32 || head_dim > 128 ? 2 : 4;
+        slot_blocks = (slots + 16 * slot_tiles - 1) / (16 * slot_tiles);
+        const int64_t groups = (int64_t)n_req * n_kv_heads * slot_blocks;
+        const int64_t want = groups > 0 ? (2048 + groups - 1) / groups : 1;
+        const int64_t most = (capacity + 127) / 128;
+        const int64_t p = want < most ? want : most;
+        parts = (int)(p < 1 ? 1 : p > 128 ? 128 : p);
+    }
+    int64_t grid(int n_req, int n_kv_heads) const {
+        return (int64_t)n_req * n_kv_heads * slot_blocks * parts;
+    }
+    size_t bytes(int n_req, int k_max, int n_heads, int head_dim) const {
+        if (parts == 1) return 0;
+        return (size_t)n_req * n_heads * (k_max + 1) * parts * (head_dim + 2) * sizeof(float);
+    }
+};
+
+}  // namespace sv

@@ -75,6 +75,7 @@ typedef enum {
 typedef enum {
     SV_F32 = 0,
     SV_BF16 = 1,
+    SV_E4M3 = 2, /* 8 bits, 4 of exponent, largest 448, no infinity (cache only) */
     SV_DTYPE_RANGE_LO_ = -2147483647 - 1,
     SV_DTYPE_RANGE_HI_ = 2147483647
 } sv_dtype;
@@ -92,6 +93,8 @@ typedef enum {
 #define SV_DEV_BAD_DRAFT_LEN 8  /* a draft length is outside [0, k_max] (clamped)                */
 #define SV_DEV_BAD_COST      16 /* a consulted cost entry is not finite and > 0 (never chosen)   */
 #define SV_DEV_BAD_KEPT      32 /* a kept count is outside [0, k_max] (clamped)                  */
+#define SV_DEV_BAD_PAGE      64 /* a page id is outside [0, n_pages)                             */
+#define SV_DEV_BAD_CTX      128 /* a context length is negative or its rows pass the page table  */
 
 /* Limits checked on the host. */
 #define SV_MAX_BUDGET_SLOTS 8192   /* n_req and n_req * k_max for sv_budget_select (LDS-resident) */
@@ -484,6 +487,104 @@ sv_status sv_calibrate_update(float* theta, const float* q_draft, const float* q
 sv_status sv_calibrate_predict(const float* theta, const float* q_draft, const float* q_entropy,
                                const float* q_max, int32_t n_req, int32_t k_max, float* conf,
                                void* stream);
+
+/*
+ * The paged key-value cache of the packed batch.
+ *
+ * agentlens page, section "기술적 구현 및 CUDA Graphs", item Graph Capture: one
+ * decode shape holds 1 .. k+1 query tokens per request.  The target's layers
+ * run that shape on the layout sv_pack_varlen writes; the two calls below are
+ * the part of a layer that touches the cache.  Request r has ctx_len[r]
+ * positions cached; its packed row j is position ctx_len[r] + j.
+ *
+ * k, v:         position t of request r, kv head h, is the head_dim
+ *               consecutive values at page_table[r, t / page_size] *
+ *               page_stride + (t % page_size) * token_stride + h * head_stride
+ *               (strides in values, the same for k and v, so that either order
+ *               of heads and positions within a page works).
+ * dtype:        SV_BF16, or SV_E4M3: a stored value times its head's scale is
+ *               the value (k_scale, v_scale: [n_kv_heads] fp32, NULL = 1).
+ * head_dim:     64, 128 or 256.   page_size: any (attend reads pages of a
+ *               multiple of 16 positions faster).
+ * Alignment: k, v and every stride to 16 bytes.
+ * page_table:   [n_req, max_pages] int32; entries past a request's positions
+ *               are not read.
+ */
+typedef struct {
+    void* k;
+    void* v;
+    sv_dtype dtype;
+    int32_t n_pages, page_size, n_kv_heads, head_dim;
+    int64_t page_stride, token_stride, head_stride;
+    const float* k_scale;
+    const float* v_scale;
+} sv_cache;
+
+#define SV_MAX_ATTEND_SLOTS  16777216   /* n_req * n_heads * (k_max + 1) for sv_cache_attend */
+#define SV_MAX_APPEND_VALUES 1073741824 /* n_rows * n_kv_heads * head_dim for sv_cache_append */
+
+/*
+ * sv_cache_append — write a step's keys and values behind the contexts.
+ *
+ * k, v:    [n_rows, n_kv_heads, head_dim] bf16, rows kv_ld values apart (a
+ *          multiple of 8, 16-byte aligned).
+ * row_req, row_pos: [n_rows] int32 as sv_pack_varlen writes them (its capacity
+ *          n_req * (k_max + 1); rows of request -1 are skipped).
+ * ctx_len: [n_req] int32 positions cached before this step.
+ * An 8-bit cache stores x / scale taken in fp32 and rounded to the nearest
+ * (ties to even), held at +-448; NaN stays NaN.
+ * Rows of an unknown request (SV_DEV_BAD_CU_ROWS), past the page table
+ * (SV_DEV_BAD_CTX) or with a page id outside [0, n_pages) (SV_DEV_BAD_PAGE)
+ * are not written.
+ * Launch: one kernel, 16 bytes of input a thread.
+ * Errors: SV_ERR_NULL; SV_ERR_DTYPE; SV_ERR_SHAPE.
+ */
+sv_status sv_cache_append(const sv_cache* cache, const int32_t* page_table, int32_t max_pages,
+                          const void* k, const void* v, int64_t kv_ld, const int32_t* row_req,
+                          const int32_t* row_pos, int32_t n_rows, const int32_t* ctx_len,
+                          int32_t n_req, int32_t* dev_error, void* stream);
+
+/*
+ * sv_cache_attend — the packed rows attend to the cache.
+ *
+ * For row j of request r (position t = ctx_len[r] + j) and query head h, with
+ * kv head h / (n_heads / n_kv_heads) and the positions i = 0 .. t (the step's
+ * own rows among them, as sv_cache_append wrote them):
+ *   s_i = scale * <q, k_i>;  out = sum_i e^(s_i) v_i / sum_i e^(s_i);
+ *   lse = ln sum_i e^(s_i).
+ * q, out:  [q_rows, n_heads, head_dim] bf16, rows q_ld and out_ld values apart
+ *          (multiples of 8, 16-byte aligned).  Rows outside every request are
+ *          neither read nor written.
+ * cu_rows: [n_req + 1] int32 as sv_pack_varlen writes it; a request may have
+ *          0 .. k_max + 1 rows (k_max = 0: one new token each, plain decoding).
+ * out_lse: [q_rows, n_heads] fp32, or NULL.
+ * A position whose page id is outside [0, n_pages) counts as absent
+ * (SV_DEV_BAD_PAGE).  A row left with no position, or whose scores are all
+ * -inf, gives 0 and lse -inf.  A position a row does not see does not touch
+ * it, whatever it holds.  The rows of a request with bad offsets
+ * (SV_DEV_BAD_CU_ROWS) or a bad context length (SV_DEV_BAD_CTX) are not
+ * written.
+ * Numerics: products of bf16 values (an 8-bit cache's values are exact in
+ * bf16) summed in fp32; maxima, sums and merges in fp32; the weights e^(s_i -
+ * max) rounded to bf16 for the product with v.  Repeated calls agree bit for
+ * bit.
+ * ws:      sv_cache_attend_workspace_bytes(...) bytes, 16-byte aligned (0:
+ *          NULL will do), uninitialised.  Calls that overlap in time must not
+ *          share it.
+ * Launch: one kernel, four waves for each request, kv head, block of up to 64
+ * query slots and part of the length; a second one merges the parts if there
+ * are several (few requests, long tables).
+ * Errors: SV_ERR_NULL; SV_ERR_DTYPE; SV_ERR_SHAPE; SV_ERR_VALUE (scale not
+ * finite); SV_ERR_WORKSPACE.
+ */
+size_t sv_cache_attend_workspace_bytes(int32_t n_req, int32_t k_max, int32_t n_heads,
+                                       int32_t n_kv_heads, int32_t head_dim, int32_t max_pages,
+                                       int32_t page_size);
+sv_status sv_cache_attend(const sv_cache* cache, const int32_t* page_table, int32_t max_pages,
+                          const void* q, int64_t q_ld, int64_t q_rows, int32_t n_heads,
+                          const int32_t* cu_rows, const int32_t* ctx_len, int32_t n_req,
+                          int32_t k_max, float scale, void* out, int64_t out_ld, float* out_lse,
+                          int32_t* dev_error, void* ws, size_t ws_bytes, void* stream);
 
 /*
  * sv_philox_uniforms — the (u, v) pairs sv_verify draws, for inspection.
