@@ -12,6 +12,7 @@ torch's current stream unless one is given.  A non-OK status raises SvError.
 
 import ctypes
 import os
+from typing import NamedTuple, Optional
 
 import numpy as np
 import torch
@@ -25,11 +26,12 @@ SV_F32, SV_BF16, SV_E4M3 = 0, 1, 2
 SV_STOCHASTIC, SV_GREEDY = 0, 1
 SV_DEV_BAD_CU_ROWS, SV_DEV_BAD_TOKEN, SV_DEV_NONFINITE = 1, 2, 4
 SV_DEV_BAD_DRAFT_LEN, SV_DEV_BAD_COST, SV_DEV_BAD_KEPT = 8, 16, 32
-SV_DEV_BAD_PAGE, SV_DEV_BAD_CTX = 64, 128
+SV_DEV_BAD_PAGE, SV_DEV_BAD_CTX, SV_DEV_BAD_PARAM = 64, 128, 256
 SV_MAX_BUDGET_SLOTS, SV_MAX_DRAFT, SV_MAX_VOCAB = 8192, 64, 1048576
 SV_MAX_VERIFY_SLOTS = 524288
 SV_NOALLOC_WS_BYTES = 8388608
 SV_MAX_ATTEND_SLOTS, SV_MAX_APPEND_VALUES = 16777216, 1073741824
+SV_MAX_SAMPLE_ROWS = 4194303
 
 EXPORTED = ["sv_status_str", "sv_budget_workspace_bytes", "sv_verify_workspace_bytes",
             "sv_cost_table_prepare", "sv_budget_select", "sv_budget_allocate",
@@ -38,7 +40,8 @@ EXPORTED = ["sv_status_str", "sv_budget_workspace_bytes", "sv_verify_workspace_b
             "sv_verify",
             "sv_verify_stages", "sv_verify_noalloc", "sv_accept_stats", "sv_calibrate_update", "sv_calibrate_predict",
             "sv_philox_uniforms",
-            "sv_cache_append", "sv_cache_attend", "sv_cache_attend_workspace_bytes"]
+            "sv_cache_append", "sv_cache_attend", "sv_cache_attend_workspace_bytes",
+            "sv_sample", "sv_verify_truncated", "sv_verify_truncated_workspace_bytes"]
 
 
 class _Cache(ctypes.Structure):
@@ -49,6 +52,12 @@ class _Cache(ctypes.Structure):
                 ("page_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
                 ("head_stride", ctypes.c_int64), ("k_scale", ctypes.c_void_p),
                 ("v_scale", ctypes.c_void_p)]
+
+
+class _Law(ctypes.Structure):
+    """sv_sampling of the C header."""
+    _fields_ = [("temperature", ctypes.c_void_p), ("top_k", ctypes.c_void_p),
+                ("top_p", ctypes.c_void_p), ("min_p", ctypes.c_void_p)]
 
 
 class SvError(RuntimeError):
@@ -98,6 +107,11 @@ def _load():
         "sv_cache_attend_workspace_bytes": (sz, [i32, i32, i32, i32, i32, i32, i32]),
         "sv_cache_attend": (ctypes.c_int, [vp, vp, i32, vp, i64, i64, i32, vp, vp, i32, i32, f32,
                                            vp, i64, vp, vp, vp, sz, vp]),
+        "sv_sample": (ctypes.c_int, [vp, i64, i32, ctypes.c_int, i32, vp, vp, vp, vp, vp, vp, vp]),
+        "sv_verify_truncated_workspace_bytes": (sz, [i32, i32]),
+        "sv_verify_truncated": (ctypes.c_int, [vp, i64, i64, vp, i64, ctypes.c_int, i32, vp, vp,
+                                               i32, i32, vp, vp, u64, u64, vp, vp, vp, vp, vp, vp,
+                                               vp, sz, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -484,6 +498,112 @@ def sv_philox_uniforms(seed, step, u, v, stream=None):
     _check(_lib.sv_philox_uniforms(int(seed), int(step), n, n_pos, _ptr(u), _ptr(v),
                                    _stream(stream)),
            "sv_philox_uniforms")
+
+
+class Sampling(NamedTuple):
+    """Settings of truncated laws, one entry a row (sv_sample) or request
+    (sv_verify_truncated), each a device tensor or None: temperature f32 (None: 1; 0: greedy),
+    top_k i32 (None or <= 0: off), top_p f32 (None or >= 1: off), min_p f32 (None or 0: off)."""
+    temperature: Optional[torch.Tensor] = None
+    top_k: Optional[torch.Tensor] = None
+    top_p: Optional[torch.Tensor] = None
+    min_p: Optional[torch.Tensor] = None
+
+
+def _law(law, n, like, name="law"):
+    if law is None:
+        return None
+    for field, t, dtype in zip(law._fields, law, (torch.float32, torch.int32, torch.float32,
+                                                  torch.float32)):
+        _dev(t, dtype, f"{name}.{field}", 1)
+        if t is not None and t.numel() != n:
+            raise ValueError(f"{name}.{field} must have {n} entries")
+    _same_device(like, *law)
+    return ctypes.byref(_Law(*(None if t is None else t.data_ptr() for t in law)))
+
+
+def _logits(t, name):
+    """Row stride of a logit matrix: rows may lie further apart than they are long."""
+    if not t.is_cuda or t.dtype not in _DTYPES or t.dim() != 2:
+        raise ValueError(f"{name} must be a bfloat16 or float32 device matrix")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+        raise ValueError(f"{name}'s rows must not overlap")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def sv_sample(logits, u, law, out_tokens, out_prob=None, out_support=None, dev_error=None,
+              vocab=None, stream=None):
+    """logits [rows, >=V] (bf16 or f32), u [rows] f32 in [0, 1) -> out_tokens [rows] i32 drawn
+    under law (a Sampling or None), out_prob [rows] f32, out_support [rows] i32."""
+    ld = _logits(logits, "logits")
+    n = logits.shape[0]
+    _dev(u, torch.float32, "u", 1)
+    _dev(out_prob, torch.float32, "out_prob", 1)
+    for name, t in (("out_tokens", out_tokens), ("out_support", out_support),
+                    ("dev_error", dev_error)):
+        _dev(t, torch.int32, name, 1)
+    for t in (u, out_tokens, out_prob, out_support):
+        if t is not None and t.numel() != n:
+            raise ValueError("u, out_tokens, out_prob, out_support need one entry a row")
+    V = logits.shape[1] if vocab is None else int(vocab)
+    if V > logits.shape[1]:
+        raise ValueError("vocab must not pass the rows' width")
+    _same_device(logits, u, out_tokens, out_prob, out_support, dev_error)
+    with _on_device(logits, stream):
+        _check(_lib.sv_sample(_ptr(logits), ld, n, _DTYPES[logits.dtype], V,
+                              _law(law, n, logits), _ptr(u), _ptr(out_tokens), _ptr(out_prob),
+                              _ptr(out_support), _ptr(dev_error), _stream_on(logits, stream)),
+               "sv_sample")
+
+
+def sv_verify_truncated_workspace_bytes(n_req, k_max):
+    return int(_lib.sv_verify_truncated_workspace_bytes(n_req, k_max))
+
+
+def sv_verify_truncated(target, draft, draft_tokens, cu_rows, target_law, draft_law, seed, step,
+                        out_tokens, out_accepted, ws, out_p_draft=None, out_q_draft=None,
+                        out_residual_mass=None, dev_error=None, vocab=None, stream=None):
+    """sv_verify with each request's truncated laws: target [rows, >=V], draft [n*k_max, >=V]
+    (None if k_max is 0), target_law and draft_law a Sampling of [n] settings or None;
+    ws: uint8 device buffer of sv_verify_truncated_workspace_bytes(n, k_max) bytes."""
+    _dev(draft_tokens, torch.int32, "draft_tokens", 2)
+    _dev(out_tokens, torch.int32, "out_tokens", 2)
+    for name, t in (("cu_rows", cu_rows), ("out_accepted", out_accepted),
+                    ("dev_error", dev_error)):
+        _dev(t, torch.int32, name, 1)
+    _dev(ws, torch.uint8, "ws", 1)
+    _dev(out_residual_mass, torch.float32, "out_residual_mass", 1)
+    n, k_max = draft_tokens.shape
+    ld, V = _logits(target, "target"), target.shape[1] if vocab is None else int(vocab)
+    draft_ld = V
+    if draft is not None:
+        draft_ld = _logits(draft, "draft")
+        if draft.dtype != target.dtype or draft.shape[0] < n * k_max or V > draft.shape[1]:
+            raise ValueError("draft must hold n*k_max rows of the target's type and width")
+    if V > target.shape[1]:
+        raise ValueError("vocab must not pass the rows' width")
+    if cu_rows.numel() != n + 1 or tuple(out_tokens.shape) != (n, k_max + 1) \
+            or out_accepted.numel() != n:
+        raise ValueError("cu_rows [n+1], out_tokens [n, k_max+1], out_accepted [n]")
+    for name, t in (("out_p_draft", out_p_draft), ("out_q_draft", out_q_draft)):
+        _dev(t, torch.float32, name, 2)
+        if t is not None and tuple(t.shape) != (n, k_max):
+            raise ValueError(f"{name} must be [n, k_max]")
+    if out_residual_mass is not None and out_residual_mass.numel() != n:
+        raise ValueError("out_residual_mass must have n entries")
+    _same_device(target, draft, draft_tokens, cu_rows, out_tokens, out_accepted, ws, out_p_draft,
+                 out_q_draft, out_residual_mass, dev_error)
+    with _on_device(target, stream):
+        _check(_lib.sv_verify_truncated(
+            _ptr(target), ld, target.shape[0], _ptr(draft), draft_ld, _DTYPES[target.dtype], V,
+            _ptr(draft_tokens), _ptr(cu_rows), n, k_max, _law(target_law, n, target, "target_law"),
+            _law(draft_law, n, target, "draft_law"), int(seed), int(step), _ptr(out_tokens),
+            _ptr(out_accepted), _ptr(out_p_draft), _ptr(out_q_draft), _ptr(out_residual_mass),
+            _ptr(dev_error), _ptr(ws), 0 if ws is None else ws.numel(),
+            _stream_on(target, stream)),
+            "sv_verify_truncated")
 
 
 class PagedCache:

@@ -1,5 +1,6 @@
-// Arguments and launchers of the paged cache (internal; sv_cache_api.cpp
-// validates before calling these).
+// Arguments and launchers of the paged cache and of the truncated laws
+// (internal; sv_cache_api.cpp and sv_sample_api.cpp validate before calling
+// these).
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -79,5 +80,56 @@ struct AttendPlan {
         return (size_t)n_req * n_heads * (k_max + 1) * parts * (head_dim + 2) * sizeof(float);
     }
 };
+
+struct SampleArgs {
+    const void* logits;
+    int64_t ld;
+    int n_rows;
+    sv_dtype dtype;
+    int vocab;
+    sv_sampling law;
+    const float* u;
+    int32_t* out_tokens;
+    float* out_prob;
+    int32_t* out_support;
+    int32_t* dev_error;
+};
+hipError_t launch_sample(const SampleArgs& a, hipStream_t stream);
+
+// One row's law, from the first launch of sv_verify_truncated to the second.
+struct LawRecord {
+    double total;    // the support's weight
+    float top;       // the largest logit
+    uint32_t ckey;   // the support's last logit (ordered key) and last id of it
+    int32_t cid;
+    int32_t fault;   // SV_DEV_* bits
+    double drafted;  // the weight of the position's draft id (0: outside)
+};
+
+struct VerifyTruncatedArgs {
+    const void* target;
+    int64_t target_ld;
+    int64_t target_rows;
+    const void* draft;
+    int64_t draft_ld;
+    sv_dtype dtype;
+    int vocab;
+    const int32_t* draft_tokens;
+    const int32_t* cu_rows;
+    int n_req;
+    int k_max;
+    sv_sampling target_law;
+    sv_sampling draft_law;
+    uint64_t seed;
+    uint64_t step;
+    int32_t* out_tokens;
+    int32_t* out_accepted;
+    float* out_p_draft;
+    float* out_q_draft;
+    float* out_residual_mass;
+    int32_t* dev_error;
+    LawRecord* laws;  // [n_req, 2 k_max + 1]: target rows 0 .. k_max, draft rows
+};
+hipError_t launch_verify_truncated(const VerifyTruncatedArgs& a, hipStream_t stream);
 
 }  // namespace sv

@@ -94,6 +94,7 @@ typedef enum {
 #define SV_DEV_BAD_COST      16 /* a consulted cost entry is not finite and > 0 (never chosen)   */
 #define SV_DEV_BAD_KEPT      32 /* a kept count is outside [0, k_max] (clamped)                  */
 #define SV_DEV_BAD_PAGE      64 /* a page id is outside [0, n_pages)                             */
+#define SV_DEV_BAD_PARAM    256 /* a temperature, top_p, min_p or uniform is out of range        */
 #define SV_DEV_BAD_CTX      128 /* a context length is negative or its rows pass the page table  */
 
 /* Limits checked on the host. */
@@ -487,6 +488,92 @@ sv_status sv_calibrate_update(float* theta, const float* q_draft, const float* q
 sv_status sv_calibrate_predict(const float* theta, const float* q_draft, const float* q_entropy,
                                const float* q_max, int32_t n_req, int32_t k_max, float* conf,
                                void* stream);
+
+/*
+ * Truncated laws: what temperature, top-k, top-p and min-p leave of a row's
+ * softmax.  FOS page, section "속도, 메모리, 정확도에 주는 영향", row 정확도: the
+ * output law is the target's; a request that samples with these settings has
+ * the truncated law as its target, and its drafts are drawn from the drafter's
+ * truncated the same way.
+ *
+ * For logits z of a row, m = max z and w(x) = exp((z(x) - m) / T), the ids are
+ * ordered by z, larger first, ties to the lower id (ids of -inf take no part).
+ * The support is the first min(n_k, n_p, n_m) ids of that order:
+ *   n_k = top_k (every id where top_k <= 0 or >= vocab);
+ *   n_p = the fewest ids whose weights reach top_p of the sum of the first n_k
+ *         (at least 1; n_k where top_p >= 1);
+ *   n_m = the ids of weight >= min_p.
+ * The law is w over its sum on the support.  T = 0: the first id alone.
+ *
+ * Each array holds one entry a row (sv_sample) or a request
+ * (sv_verify_truncated); NULL: 1, off, 1 and 0.  A row or request whose
+ * temperature is negative or not finite, top_p negative or NaN, or min_p
+ * outside [0, 1] is faulty (SV_DEV_BAD_PARAM).
+ * Numerics: weights, sums and borders in 64 bits, whatever the logits' type.
+ */
+typedef struct {
+    const float* temperature;
+    const int32_t* top_k;
+    const float* top_p;
+    const float* min_p;
+} sv_sampling;
+
+#define SV_MAX_SAMPLE_ROWS 4194303  /* the grid stays below 2^32 work-items */
+
+/*
+ * sv_sample — one token a row from given random numbers.
+ *
+ * The drafter's draw (its probability is what sv_verify_truncated divides by),
+ * and plain decoding's.  Row i's token is the smallest id x with C(x) > u[i] *
+ * W, C the running sum of the support's weights over ascending ids and W its
+ * total, as sv_verify draws.
+ * logits:  [n_rows] rows of vocab values, ld apart; rows need no alignment.
+ * law:     host pointer to the settings, or NULL (softmax at temperature 1).
+ * u:       [n_rows] fp32 in [0, 1) (sv_philox_uniforms draws such).
+ * out_tokens: [n_rows] int32.   out_prob: [n_rows] fp32, the token's
+ *          probability under the law, or NULL.   out_support: [n_rows] int32,
+ *          how many ids the law leaves, or NULL.
+ * A row with NaN, +inf or only -inf (SV_DEV_NONFINITE), bad settings or a
+ * uniform outside [0, 1) (SV_DEV_BAD_PARAM) gives -1 in all of them.
+ * Repeated calls agree bit for bit.
+ * Launch: one kernel, one 1024-thread workgroup a row; no workspace.
+ * Errors: SV_ERR_NULL; SV_ERR_DTYPE; SV_ERR_SHAPE.
+ */
+sv_status sv_sample(const void* logits, int64_t ld, int32_t n_rows, sv_dtype dtype,
+                    int32_t vocab, const sv_sampling* law, const float* u, int32_t* out_tokens,
+                    float* out_prob, int32_t* out_support, int32_t* dev_error, void* stream);
+
+/*
+ * sv_verify_truncated — sv_verify with truncated laws.
+ *
+ * The same rule, layouts, uniforms, outputs and faults as sv_verify's
+ * stochastic mode, with p_j and q_j the truncated laws of target row j and
+ * draft row j under the request's own settings: d_j is accepted iff u_j <
+ * min(1, p_j(d_j) / q_j(d_j)) (q = 0: iff p > 0); the token at the first
+ * rejection is drawn from max(0, p - q) (p where that has no mass), after the
+ * last draft from p.  A temperature of 0 makes a request greedy, so one batch
+ * may mix greedy and sampled requests.
+ * target_law, draft_law: host pointers to the settings of p and q ([n_req]
+ *          arrays), or NULL; often the same.  Faults: SV_DEV_BAD_PARAM and
+ *          those of sv_verify; a faulty request writes -1 to all its outputs.
+ * Numerics: 64 bits up to the outputs; repeated calls agree bit for bit.
+ * ws:      sv_verify_truncated_workspace_bytes(n_req, k_max) bytes (a 32-byte
+ *          record for each of a request's 2 k_max + 1 row slots), 8-byte
+ *          aligned, uninitialised.  Calls that overlap in time must not share
+ *          it.
+ * Launch: two kernels: one 1024-thread workgroup per row slot, then one per
+ * request.
+ * Errors: SV_ERR_NULL; SV_ERR_DTYPE; SV_ERR_SHAPE; SV_ERR_WORKSPACE.
+ */
+size_t sv_verify_truncated_workspace_bytes(int32_t n_req, int32_t k_max);
+sv_status sv_verify_truncated(const void* target_logits, int64_t target_ld, int64_t target_rows,
+                              const void* draft_logits, int64_t draft_ld, sv_dtype dtype,
+                              int32_t vocab, const int32_t* draft_tokens, const int32_t* cu_rows,
+                              int32_t n_req, int32_t k_max, const sv_sampling* target_law,
+                              const sv_sampling* draft_law, uint64_t seed, uint64_t step,
+                              int32_t* out_tokens, int32_t* out_accepted, float* out_p_draft,
+                              float* out_q_draft, float* out_residual_mass, int32_t* dev_error,
+                              void* ws, size_t ws_bytes, void* stream);
 
 /*
  * The paged key-value cache of the packed batch.

@@ -1,0 +1,359 @@
+"""sv_sample and sv_verify_truncated on the GPU against the fp64 oracle.
+
+Tokens, support sizes and accepted lengths have to be equal: both sides work in
+64 bits, where a border or a draw falls within rounding (1e-13 of the total) of
+its neighbour in about one of 10^8 rows.  Probabilities and masses are 64-bit
+results rounded once to fp32: within 2^-24 of the value, plus the two sides' own
+rounding (1e-12 of the probabilities involved)."""
+
+import numpy as np
+import pytest
+import torch
+
+import adaptive_draft_verification_amd as sv
+from oracle.truncate import bad_settings, sample_row, verify_truncated
+
+pytestmark = pytest.mark.gpu
+
+BF, F32 = torch.bfloat16, torch.float32
+TOP_U = 1 - 2.0 ** -24
+
+
+@pytest.fixture(autouse=True, scope="module")
+def _need_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+def law_of(settings):
+    """[(t, k, p, s)] -> Sampling on the device."""
+    t, k, p, s = zip(*settings)
+    f = lambda x: torch.tensor(x, dtype=F32, device="cuda")  # noqa: E731
+    return sv.Sampling(f(t), torch.tensor(k, dtype=torch.int32, device="cuda"), f(p), f(s))
+
+
+def run_sample(z, u, law, vocab=None, stream=None):
+    n = z.shape[0]
+    tok = torch.full((n,), -7, dtype=torch.int32, device="cuda")
+    prob = torch.full((n,), -7.0, device="cuda")
+    size = torch.full((n,), -7, dtype=torch.int32, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    sv.sv_sample(z, torch.tensor(u, dtype=F32, device="cuda"), law, tok, prob, size, err, vocab,
+                 stream)
+    torch.cuda.synchronize()
+    return tok.cpu().numpy(), prob.cpu().numpy(), size.cpu().numpy(), int(err)
+
+
+def check_sample(z, u, settings, vocab=None):
+    """z: device logits [n, >= vocab]."""
+    tok, prob, size, err = run_sample(z, u, law_of(settings), vocab)
+    assert err == 0
+    zz = z.float().cpu().numpy()[:, :vocab]
+    for i, (uu, s) in enumerate(zip(u, settings)):
+        t, p, n = sample_row(zz[i], uu, *s)
+        assert (int(tok[i]), int(size[i])) == (t, n), (i, uu, s)
+        assert abs(prob[i] - p) <= (2.0 ** -24 + 1e-12) * p + 1e-45, (i, prob[i], p)
+    return tok
+
+
+SETTINGS = [(1.0, 0, 1.0, 0.0), (0.0, 0, 1.0, 0.0), (0.7, 1, 1.0, 0.0), (0.8, 40, 0.95, 0.0),
+            (1.3, 0, 0.9, 0.0), (0.6, 0, 0.5, 0.0), (1.0, 0, 1.0, 0.1), (0.9, 50, 0.9, 0.05),
+            (1.0, 1025, 1.0, 0.0), (1.0, 3000, 0.99, 0.0), (2.5, 700, 0.7, 0.001),
+            (1.0, 0, 0.9999, 1e-6), (0.3, 0, 0.999999, 0.0), (1.0, 5, 1e-7, 0.0),
+            (5.0, 0, 0.97, 0.0), (1.0, 0, 1.0, 1.0)]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("vocab", [1, 2, 7, 8, 9, 63, 1000, 8191, 32000, 70001])
+def test_sample_sizes_and_settings(dtype, vocab):
+    g = torch.Generator().manual_seed(vocab)
+    n = len(SETTINGS)
+    z = (torch.randn(n, vocab, generator=g) * 3).to(dtype).cuda()
+    u = torch.rand(n, generator=g).numpy()
+    u[0], u[4], u[7] = TOP_U, 0.0, 0.0
+    check_sample(z, [float(x) for x in u], SETTINGS)
+
+
+@pytest.mark.parametrize("dtype,vocab", [(BF, 129280), (F32, 256000), (BF, 1048576)])
+def test_sample_large_vocabularies(dtype, vocab):
+    g = torch.Generator().manual_seed(7)
+    s = [SETTINGS[i] for i in (0, 3, 4, 5, 9, 12, 14)]
+    z = (torch.randn(len(s), vocab, generator=g) * 3).to(dtype).cuda()
+    check_sample(z, torch.rand(len(s), generator=g).tolist(), s)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_sample_ties(dtype):
+    """Few distinct logits: every border falls inside a run of equal ones."""
+    g = torch.Generator().manual_seed(11)
+    rows = []
+    for vocab_kind in range(len(SETTINGS)):
+        rows.append(torch.randint(-3, 4, (20000,), generator=g).float() * 0.5)
+    z = torch.stack(rows)
+    z[3] = 0.0                       # one long run
+    z[4, ::2], z[4, 1::2] = 0.0, -0.0
+    z[5] = torch.where(torch.arange(20000) == 777, 4.0, 0.0)
+    check_sample(z.to(dtype).cuda(), torch.rand(len(SETTINGS), generator=g).tolist(), SETTINGS)
+    # constant rows: exact counts at exact borders
+    flat = torch.zeros(4, 6000, dtype=dtype, device="cuda")
+    got = check_sample(flat, [0.5, 0.0, TOP_U, 0.25],
+                       [(1.0, 0, 0.5, 0.0), (1.0, 0, 0.25, 0.0), (0.5, 0, 1.0, 1.0),
+                        (1.0, 3000, 0.5, 0.0)])
+    assert got.tolist() == [1500, 0, 5999, 375]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_sample_shapes_of_rows(dtype):
+    """Sorted, peaked, far apart, tiny and huge logits; ids of -inf."""
+    V = 30000
+    g = torch.Generator().manual_seed(13)
+    x = torch.randn(V, generator=g)
+    ninf = float("-inf")
+    half = torch.where(torch.rand(V, generator=g) < 0.5, ninf, 1.0) * 1.0
+    rows = [x.sort().values * 4, x.sort(descending=True).values * 4, x * 1e-3, x * 300,
+            torch.where(torch.arange(V) == V - 1, 80.0, x), -1e4 + x * 50,
+            torch.where(torch.isinf(half), ninf, x), torch.full((V,), ninf), x - 5000, x * 1e-30]
+    rows[7][[5, 29999]] = torch.tensor([-3.0, -3.0])
+    z = torch.stack(rows).to(dtype).cuda()
+    for s in SETTINGS:
+        check_sample(z, torch.rand(len(rows), generator=g).tolist(), [s] * len(rows))
+
+
+def test_sample_flat_tail_behind_a_peak():
+    """One id holds nearly all weight; top-p's border lies in a long flat tail whose
+    weights are far below the peak's (in fp32 and in coarse fixed point it is lost)."""
+    V = 50000
+    z = torch.zeros(6, V)
+    gaps = [12.0, 20.0, 25.0, 28.0, 12.0, 20.0]
+    for i, gap in enumerate(gaps):
+        z[i, 1234] = gap
+    ps = []
+    for gap in gaps:
+        w = np.exp(-gap) * (V - 1)
+        ps.append(float(np.float32(1 - 0.4 * w / (1 + w))))
+    settings = [(1.0, 0, p, 0.0) for p in ps]
+    settings[4] = (1.0, 40000, ps[4], 0.0)
+    check_sample(z.cuda(), [0.3, TOP_U, TOP_U, 0.999, TOP_U, 0.0], settings)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("shift", [1, 2, 3, 5, 7])
+def test_sample_rows_that_start_anywhere(dtype, shift):
+    """Rows off 16-byte alignment, with NaN around them that must not be read as theirs."""
+    g = torch.Generator().manual_seed(shift)
+    n, V = len(SETTINGS), 4003
+    wide = torch.full((n, 4096 + 3), float("nan"), dtype=dtype)
+    wide[:, shift:shift + V] = (torch.randn(n, V, generator=g) * 2).to(dtype)
+    wide = wide.cuda()
+    u = torch.rand(n, generator=g).tolist()
+    view = wide[:, shift:]
+    check_sample(view, u, SETTINGS, vocab=V)
+
+
+def test_sample_defaults_and_faults():
+    g = torch.Generator().manual_seed(17)
+    z = (torch.randn(8, 500, generator=g) * 2).cuda()
+    u = [0.1 * i for i in range(8)]
+    a = run_sample(z, u, None)
+    b = run_sample(z, u, law_of([(1.0, 0, 1.0, 0.0)] * 8))
+    for x, y in zip(a, b):
+        np.testing.assert_array_equal(x, y)
+    nan, inf = float("nan"), float("inf")
+    z[1, 3], z[2, 4], z[3] = nan, inf, -inf
+    z[4, 0] = -nan
+    tok, prob, size, err = run_sample(z, u, None)
+    assert err == sv.SV_DEV_NONFINITE
+    assert (tok[1:5] == -1).all() and (prob[1:5] == -1).all() and (size[1:5] == -1).all()
+    np.testing.assert_array_equal(tok[5:], a[0][5:])
+    z = (torch.randn(8, 500, generator=g) * 2).cuda()
+    bad = [(-1.0, 0, 1.0, 0.0), (nan, 0, 1.0, 0.0), (inf, 0, 1.0, 0.0), (1.0, 0, -0.1, 0.0),
+           (1.0, 0, nan, 0.0), (1.0, 0, 1.0, -0.5), (1.0, 0, 1.0, 1.5), (1.0, 0, 1.0, nan)]
+    assert all(bad_settings(*s) for s in bad)
+    tok, _, _, err = run_sample(z, u, law_of(bad))
+    assert err == sv.SV_DEV_BAD_PARAM and (tok == -1).all()
+    tok, _, _, err = run_sample(z, [0.0, 1.0, -0.1, nan, inf, 0.5, 0.5, 0.5], None)
+    assert err == sv.SV_DEV_BAD_PARAM
+    assert (tok[1:5] == -1).all() and (tok[[0, 5, 6, 7]] >= 0).all()
+    # odd but allowed settings
+    check_sample(z, u, [(1e-30, 0, 1.0, 0.0), (1e30, 0, 0.5, 0.0), (1.0, -5, 7.0, 0.0),
+                        (1.0, 10 ** 9, 1.0, 0.0), (0.0, 7, nan if False else 0.3, 0.9),
+                        (1e-30, 3, 0.5, 0.5), (1.0, 499, 1.0, 0.0), (1.0, 500, 0.0, 0.0)])
+
+
+def test_sample_repeats_streams_and_graph():
+    g = torch.Generator().manual_seed(19)
+    n = len(SETTINGS)
+    z = (torch.randn(n, 30001, generator=g) * 3).cuda()
+    u = torch.rand(n, generator=g).tolist()
+    law = law_of(SETTINGS)
+    want = run_sample(z, u, law)
+    for stream in (None, torch.cuda.Stream(), None):
+        for x, y in zip(run_sample(z, u, law, stream=stream), want):
+            np.testing.assert_array_equal(x, y)
+    ud = torch.tensor(u, device="cuda")
+    tok = torch.zeros(n, dtype=torch.int32, device="cuda")
+    prob = torch.zeros(n, device="cuda")
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side), torch.cuda.graph(graph, stream=side):
+        sv.sv_sample(z, ud, law, tok, prob)
+    for i in range(3):
+        z.copy_((torch.randn(n, 30001, generator=g) * 3))
+        ud.copy_(torch.rand(n, generator=g))
+        tok.fill_(-3)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = tok.cpu().numpy(), prob.cpu().numpy()
+        eager = run_sample(z, ud.tolist(), law)
+        np.testing.assert_array_equal(got[0], eager[0])
+        np.testing.assert_array_equal(got[1], eager[1])
+
+
+# ------------------------------------------------------------ verify_truncated
+
+def verify_case(seed, n, k, V, dtype, settings, draft_settings=None, rows=None, noise=1.0,
+                ld_extra=0):
+    g = torch.Generator().manual_seed(seed)
+    rng = np.random.default_rng(seed)
+    rows = rng.integers(1, k + 2, n) if rows is None else np.asarray(rows)
+    cu = np.concatenate([[0], np.cumsum(rows)]).astype(np.int32)
+    total = int(cu[-1])
+    target = (torch.randn(total, V + ld_extra, generator=g) * 3).to(dtype)
+    draft = torch.full((n * k, V + ld_extra), float("nan")).to(dtype)
+    toks = np.full((n, k), -1, np.int32)
+    ds = draft_settings or settings
+    for r in range(n):
+        for j in range(rows[r] - 1):
+            z = target[cu[r] + j].float() + noise * torch.randn(V + ld_extra, generator=g)
+            draft[r * k + j] = z.to(dtype)
+            toks[r, j] = sample_row(draft[r * k + j, :V].float().numpy(), float(rng.random()),
+                                    *ds[r])[0]
+    return target, draft, toks, cu, settings, ds
+
+
+def run_verify(target, draft, toks, cu, settings, ds, V, seed, step, stream=None):
+    n, k = toks.shape
+    full = lambda *s: torch.full(s, -7.0, device="cuda")  # noqa: E731
+    out = dict(tokens=full(n, k + 1).int(), accepted=full(n).int(), p_draft=full(n, k),
+               q_draft=full(n, k), residual_mass=full(n))
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ws = torch.full((sv.sv_verify_truncated_workspace_bytes(n, k),), 0xFF, dtype=torch.uint8,
+                    device="cuda")
+    sv.sv_verify_truncated(target.cuda(), draft.cuda() if k else None,
+                           torch.from_numpy(toks).cuda(), torch.from_numpy(cu).cuda(),
+                           law_of(settings), law_of(ds), seed, step, out["tokens"],
+                           out["accepted"], ws, out["p_draft"], out["q_draft"],
+                           out["residual_mass"], err, V, stream)
+    torch.cuda.synchronize()
+    g = {x: y.cpu().numpy() for x, y in out.items()}
+    g["dev_error"] = int(err)
+    return g
+
+
+def check_verify(case, V, seed, step):
+    g = run_verify(*case, V, seed, step)
+    target, draft, toks, cu, settings, ds = case
+    n, k = toks.shape
+    o = verify_truncated(target.float().numpy(), draft.float().numpy(), toks, cu, k, V, settings,
+                         ds, seed, step)
+    assert g["dev_error"] == o["dev_error"]
+    np.testing.assert_array_equal(g["accepted"], o["accepted"])
+    np.testing.assert_array_equal(g["tokens"], o["tokens"])
+    for key in ("p_draft", "q_draft", "residual_mass"):
+        tol = (2.0 ** -24 + 1e-12) * np.abs(o[key]) + (1e-12 if key == "residual_mass" else 1e-45)
+        assert (np.abs(g[key] - o[key]) <= tol).all(), key
+    return g
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("n,k,V", [(16, 3, 1000), (5, 7, 8001), (16, 1, 7), (1, 4, 32000)])
+def test_verify_truncated_matches_oracle(dtype, n, k, V):
+    settings = [SETTINGS[(3 * i + 1) % len(SETTINGS)] for i in range(n)]
+    g = check_verify(verify_case(n + V, n, k, V, dtype, settings), V, 21, 5)
+    assert (g["accepted"] >= 0).all()
+
+
+def test_verify_truncated_large():
+    settings = [SETTINGS[i] for i in (0, 1, 3, 4)]
+    check_verify(verify_case(31, 4, 3, 129280, BF, settings), 129280, 2 ** 40 + 3, 2 ** 33 + 1)
+
+
+def test_verify_truncated_laws_that_differ():
+    """A drafter with settings of its own; drafts outside the target's support."""
+    n = 12
+    settings = [(0.7, 5, 0.9, 0.0)] * n
+    ds = [(1.5, 0, 1.0, 0.0)] * n
+    case = verify_case(33, n, 4, 3001, F32, settings, ds, noise=2.0)
+    g = check_verify(case, 3001, 3, 9)
+    assert (g["p_draft"] == 0).any()
+
+
+def test_verify_truncated_equal_rows_accept_everything():
+    n, k, V = 4, 5, 2000
+    settings = [(0.8, 50, 0.95, 0.0)] * n
+    case = verify_case(35, n, k, V, BF, settings, rows=[k + 1] * n, noise=0.0)
+    g = check_verify(case, V, 1, 1)
+    assert (g["accepted"] == k).all() and (g["residual_mass"] == -1).all()
+
+
+def test_verify_truncated_k_of_64_and_of_0():
+    settings = [(1.0, 20, 1.0, 0.0)] * 3
+    check_verify(verify_case(37, 3, 64, 300, F32, settings, rows=[65, 65, 30], noise=0.0), 300, 4,
+                 4)
+    check_verify(verify_case(38, 3, 0, 300, BF, settings, rows=[1, 1, 1]), 300, 4, 4)
+
+
+def test_verify_truncated_unaligned_rows():
+    n, k, V = 6, 3, 4001
+    settings = [SETTINGS[i] for i in (0, 3, 4, 6, 7, 8)]
+    check_verify(verify_case(39, n, k, V, BF, settings, ld_extra=2), V, 8, 8)
+
+
+def test_verify_truncated_faults():
+    n, k, V = 8, 3, 500
+    settings = [(0.9, 30, 0.9, 0.0)] * n
+    t, d, toks, cu, s, ds = verify_case(41, n, k, V, F32, settings, rows=[4] * n)
+    t[cu[1] + 3, 7] = float("nan")           # the bonus row
+    d[2 * k + 1, 0] = float("inf")
+    toks[3, 2] = V
+    s, ds = list(s), list(ds)
+    s[4] = (-1.0, 0, 1.0, 0.0)
+    ds[5] = (1.0, 0, 1.0, 2.0)
+    cu = cu.copy()
+    g = check_verify((t, d, toks, cu, s, ds), V, 6, 6)
+    assert g["dev_error"] == sv.SV_DEV_NONFINITE | sv.SV_DEV_BAD_TOKEN | sv.SV_DEV_BAD_PARAM
+    assert (g["tokens"][1:6] == -1).all() and (g["accepted"][[0, 6, 7]] >= 0).all()
+    cu[7], cu[8] = 40, 41                     # too many rows, then past the end
+    g = check_verify((t, d, toks, cu, s, ds), V, 6, 6)
+    assert g["dev_error"] & sv.SV_DEV_BAD_CU_ROWS and (g["tokens"][6:] == -1).all()
+
+
+def test_verify_truncated_repeats_and_graph():
+    n, k, V = 9, 3, 9000
+    settings = [SETTINGS[i] for i in (0, 1, 3, 4, 5, 6, 7, 9, 10)]
+    case = verify_case(43, n, k, V, BF, settings)
+    want = run_verify(*case, V, 5, 2)
+    for stream in (torch.cuda.Stream(), None):
+        g = run_verify(*case, V, 5, 2, stream)
+        for key in want:
+            np.testing.assert_array_equal(g[key], want[key])
+    t, d, toks, cu = case[0].cuda(), case[1].cuda(), torch.from_numpy(case[2]).cuda(), \
+        torch.from_numpy(case[3]).cuda()
+    law = law_of(settings)
+    ws = torch.empty(sv.sv_verify_truncated_workspace_bytes(n, k), dtype=torch.uint8,
+                     device="cuda")
+    out = torch.zeros(n, k + 1, dtype=torch.int32, device="cuda")
+    acc = torch.zeros(n, dtype=torch.int32, device="cuda")
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side), torch.cuda.graph(graph, stream=side):
+        sv.sv_verify_truncated(t, d, toks, cu, law, law, 5, 2, out, acc, ws)
+    for i in range(3):
+        t.copy_(case[0].roll(i, 1))
+        d.copy_(case[1].roll(i, 1))
+        ws.fill_(0xFF)
+        graph.replay()
+        torch.cuda.synchronize()
+        g = run_verify(case[0].roll(i, 1), case[1].roll(i, 1), *case[2:], V, 5, 2)
+        np.testing.assert_array_equal(out.cpu().numpy(), g["tokens"])
+        np.testing.assert_array_equal(acc.cpu().numpy(), g["accepted"])
