@@ -13,13 +13,17 @@
 // fixed-point integers (two 64-bit words, 43 bits each below the point), so
 // their order does not change them.
 //
-// One workgroup of 1024 threads holds a row.  What takes part in the search
-// for the border is first cut down by a bound that costs one pass (the k-th
-// largest of the threads' own maxima, min-p's logit, or the logit below which
-// all ids together weigh less than top-p leaves out); what is left is kept in
-// LDS if it fits, and the search goes over that list instead of the row.  The
-// border is found digit by digit: 256 bins over 8 bits of the ordered key, the
-// bin that holds the border, then the next 8 bits within it.
+// One workgroup of 1024 threads takes a row.  Three ways to the border, by
+// what the settings ask for:
+//  - top-k up to 1024, or min-p: a bound that costs no pass (the k-th largest of
+//    the threads' own maxima, min-p's logit) leaves a few candidates, which are
+//    gathered in LDS, ranked by counting and summed there;
+//  - top-p alone: one pass sums the row and its histogram over 2048 steps of
+//    the weight (2^(1/32) each); the step that holds the border is gathered and
+//    ranked the same way while the ids above it are summed;
+//  - anything else, and what does not fit the lists (long runs of equal
+//    logits): the border is found digit by digit, 256 bins over 8 bits of the
+//    ordered key, then the next 8 bits within the bin that holds the border.
 #pragma once
 
 #include "sv_device.h"
@@ -31,6 +35,11 @@ namespace law {
 constexpr int kThreads = 1024;
 constexpr int kWaves = kThreads / kWave;
 constexpr int kList = 2048;  // candidates kept in LDS
+constexpr int kRank = 512;   // candidates ranked by counting
+constexpr int kSteps = 2048; // histogram of the weights, kPerOctave steps for a factor of 2
+constexpr float kPerOctave = 32.0f;
+constexpr int kMaxSteps = (SV_MAX_VOCAB + 8) / 8 / (kWaves * kWave) + 1;  // of a wave's segment
+constexpr double kLog2e64 = 1.4426950408889634074;
 constexpr float kInf = __builtin_inff();
 constexpr uint32_t kMinusInfKey = 0x007fffffu;
 
@@ -77,16 +86,38 @@ __device__ __forceinline__ Settings settings(const sv_sampling& a, int i, int vo
     return o;
 }
 
+// 2^t for t <= 0, to 4e-14: t = n + r with n an integer and |r| <= 1/2, 2^r = 1 +
+// r q(r) with q of degree 8 through the Chebyshev nodes of [-1/2, 1/2].  2^0 is
+// exactly 1, so equal logits have equal weights, and counts of them are exact.
+// Seventeen fp64 operations an id bound the passes that sum a row: 13 us for
+// 129,280 ids on one CU.
+__device__ __forceinline__ double pow2(double t) {
+    t = fmax(t, -1100.0);
+    const double shifted = t + 0x1.8p52;
+    const int n = (int)(uint32_t)(uint64_t)__double_as_longlong(shifted);
+    const double r = t - (shifted - 0x1.8p52);
+    double q = 0x1.b63880a30e9ffp-24;
+    q = fma(q, r, 0x1.63d136366db24p-20);
+    q = fma(q, r, 0x1.ffcb9515a8016p-17);
+    q = fma(q, r, 0x1.4308ac85aa947p-13);
+    q = fma(q, r, 0x1.5d87fe86fe88ep-10);
+    q = fma(q, r, 0x1.3b2ab7181b755p-7);
+    q = fma(q, r, 0x1.c6b08d7047e52p-5);
+    q = fma(q, r, 0x1.ebfbdff823cedp-3);
+    q = fma(q, r, 0x1.62e42fefa39efp-1);
+    return __builtin_amdgcn_ldexp(fma(q, r, 1.0), n);
+}
+
 // The ids of a law and their weights.
 struct Weigher {
-    double m, it;   // largest logit, 1 / T (0: T = 0, one id of weight 1)
+    double m, it;   // largest logit, log2(e) / T (0: T = 0, one id of weight 1)
     double s;       // min-p
     uint32_t ckey;  // the last logit's key and, among its ids, the last id
     int32_t cid;
     __device__ __forceinline__ bool above(uint32_t key, int id) const {
         return key > ckey || (key == ckey && id <= cid);
     }
-    __device__ __forceinline__ double raw(float z) const { return exp(((double)z - m) * it); }
+    __device__ __forceinline__ double raw(float z) const { return pow2(((double)z - m) * it); }
     __device__ __forceinline__ double operator()(float z, int id) const {
         if (!above(order_key(z), id)) return 0.0;
         const double w = raw(z);
@@ -95,19 +126,31 @@ struct Weigher {
 };
 
 struct Smem {
+    unsigned long long step[kSteps];   // histogram of the weights, in 2^-43
+    unsigned long long list[kList];    // candidates: key, then ~id: larger is earlier
+    unsigned long long sorted[kRank];  // ranked
+    double weight[kRank];
+    double prefix[kRank];
+    double seg[kMaxSteps];
     unsigned long long hi[256], lo[256];
     uint32_t cnt[256];
-    uint32_t list_key[kList];
-    int32_t list_id[kList];
     int list_n;
-    uint32_t red[kWaves];
+    uint32_t red[kWaves], red2[kWaves];
     int redi[kWaves];
     double redd[kWaves];
+    unsigned long long redu[kWaves];
+    int first, second;
     // what a scan of the bins found
     uint32_t digit, before_cnt, in_cnt;
     int found;
     Mass before;
 };
+
+__device__ __forceinline__ unsigned long long entry(uint32_t key, int id) {
+    return ((unsigned long long)key << 32) | (uint32_t)~id;
+}
+__device__ __forceinline__ uint32_t entry_key(unsigned long long e) { return (uint32_t)(e >> 32); }
+__device__ __forceinline__ int entry_id(unsigned long long e) { return (int)~(uint32_t)e; }
 
 // One row, as granules of 8 ids.  Granule i starts at a 16-byte boundary and
 // holds ids 8 i - shift .. + 7; the first and last may be partly outside.  Wave
@@ -129,48 +172,118 @@ struct Row {
     __device__ __forceinline__ int first_id(int wave, int step, int lane) const {
         return (wave * per + step * kWave + lane) * 8 - shift;
     }
-    // The 8 logits at ids id0 .. id0 + 7 (-inf outside the row).
-    __device__ __forceinline__ void load(int id0, float* z) const {
-        if (id0 >= 0 && id0 + 8 <= vocab) {
-            const char* at = base + (int64_t)(id0 + shift) * kBytes;
+    // 8 logits as they lie in memory
+    struct Raw {
+        uint32_t w[2 * kBytes];
+        __device__ __forceinline__ void unpack(float* z) const {
             if (DT == SV_BF16) {
-                const uint4 w = *reinterpret_cast<const uint4*>(at);
-                z[0] = bf16_lo(w.x), z[1] = bf16_hi(w.x), z[2] = bf16_lo(w.y);
-                z[3] = bf16_hi(w.y), z[4] = bf16_lo(w.z), z[5] = bf16_hi(w.z);
-                z[6] = bf16_lo(w.w), z[7] = bf16_hi(w.w);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    z[2 * i] = bf16_lo(w[i]);
+                    z[2 * i + 1] = bf16_hi(w[i]);
+                }
             } else {
-                const float4 a = reinterpret_cast<const float4*>(at)[0];
-                const float4 b = reinterpret_cast<const float4*>(at)[1];
-                z[0] = a.x, z[1] = a.y, z[2] = a.z, z[3] = a.w;
-                z[4] = b.x, z[5] = b.y, z[6] = b.z, z[7] = b.w;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) z[i] = __uint_as_float(w[i % (2 * kBytes)]);
             }
-            return;
         }
+    };
+    // The 8 logits at ids id0 .. id0 + 7 (-inf outside the row).
+    __device__ __forceinline__ Raw raw(int id0) const {
+        Raw out;
+        if (id0 >= 0 && id0 + 8 <= vocab) {
+            const uint4* at =
+                reinterpret_cast<const uint4*>(base + (int64_t)(id0 + shift) * kBytes);
+#pragma unroll
+            for (int i = 0; i < kBytes / 2; ++i) {
+                const uint4 v = at[i];
+                out.w[4 * i] = v.x, out.w[4 * i + 1] = v.y;
+                out.w[4 * i + 2] = v.z, out.w[4 * i + 3] = v.w;
+            }
+            return out;
+        }
+        uint32_t z[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             const int id = id0 + e;
-            z[e] = -kInf;
-            if (id >= 0 && id < vocab) z[e] = one(id);
+            z[e] = 0xff800000u;
+            if (id >= 0 && id < vocab) z[e] = __float_as_uint(one(id));
         }
+#pragma unroll
+        for (int i = 0; i < 2 * kBytes; ++i)
+            out.w[i] = DT == SV_BF16 ? (z[(2 * i) & 7] >> 16) | (z[(2 * i + 1) & 7] & 0xffff0000u)
+                                     : z[i & 7];
+        return out;
     }
+    __device__ __forceinline__ void load(int id0, float* z) const { raw(id0).unpack(z); }
     __device__ __forceinline__ float one(int id) const {
         const char* at = base + (int64_t)(id + shift) * kBytes;
         if (DT == SV_BF16)
             return __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t*>(at) << 16);
         return *reinterpret_cast<const float*>(at);
     }
-    // f(logit, id) over the calling thread's ids
+    // The wave that holds an id.
+    __device__ __forceinline__ int wave_of(int id) const { return ((id + shift) >> 3) / per; }
+    // f(logit, id) over the calling thread's ids, the next granule in flight
     template <class F>
     __device__ __forceinline__ void each(F f) const {
         const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-        for (int s = 0; s < steps; ++s) {
-            const int id0 = first_id(wave, s, lane);
-            if (id0 >= vocab) break;
+        int id0 = first_id(wave, 0, lane);
+        if (id0 >= vocab) return;
+        Raw next = raw(id0);
+        for (int s = 1;; ++s) {
+            const Raw now = next;
+            const int id1 = first_id(wave, s, lane);
+            const bool more = s < steps && id1 < vocab;
+            if (more) next = raw(id1);
             float z[8];
-            load(id0, z);
+            now.unpack(z);
 #pragma unroll
             for (int e = 0; e < 8; ++e) f(z[e], id0 + e);
+            if (!more) return;
+            id0 = id1;
         }
+    }
+};
+
+// Largest logit and faults of a thread's ids, on the raw words: positive floats
+// order as signed integers, negative ones backwards as unsigned.
+typedef short s16x2 __attribute__((ext_vector_type(2)));
+typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+template <sv_dtype DT>
+struct Extremes;
+template <>
+struct Extremes<SV_BF16> {
+    s16x2 smax{-32768, -32768};
+    u16x2 umax{0, 0}, umin{0xffff, 0xffff};
+    __device__ __forceinline__ void add(uint32_t w) {
+        smax = __builtin_elementwise_max(smax, __builtin_bit_cast(s16x2, w));
+        umax = __builtin_elementwise_max(umax, __builtin_bit_cast(u16x2, w));
+        umin = __builtin_elementwise_min(umin, __builtin_bit_cast(u16x2, w));
+    }
+    __device__ __forceinline__ uint32_t top() const {
+        const int s = max(smax.x, smax.y);
+        const uint32_t b = s >= 0 ? (uint32_t)s : (uint32_t)min(umin.x, umin.y);
+        return order_key(__uint_as_float(b << 16));
+    }
+    __device__ __forceinline__ bool bad() const {  // NaN or +inf
+        return max(smax.x, smax.y) >= 0x7f80 || max(umax.x, umax.y) > 0xff80;
+    }
+};
+template <>
+struct Extremes<SV_F32> {
+    int32_t smax = INT32_MIN;
+    uint32_t umax = 0, umin = 0xffffffffu;
+    __device__ __forceinline__ void add(uint32_t w) {
+        smax = max(smax, (int32_t)w);
+        umax = max(umax, w);
+        umin = min(umin, w);
+    }
+    __device__ __forceinline__ uint32_t top() const {
+        return order_key(__uint_as_float(smax >= 0 ? (uint32_t)smax : umin));
+    }
+    __device__ __forceinline__ bool bad() const {
+        return smax >= 0x7f800000 || umax > 0xff800000u;
     }
 };
 
@@ -246,9 +359,10 @@ __device__ __forceinline__ void scan_bins(Smem& sm, uint32_t want, double goal, 
             b.hi += wave_incl_sum_dpp(hs, lane) - hs;
             b.lo += wave_incl_sum_dpp(ls, lane) - ls;
         }
+        // of this lane's bins: the one found, and the last that holds any
         int at = -1, last = -1;
-        Mass ab{0, 0}, lb{0, 0};
-        uint32_t ac = 0, lc = 0;
+        unsigned long long at_hi = 0, at_lo = 0, last_hi = 0, last_lo = 0;
+        uint32_t at_cnt = 0, last_cnt = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             bool hit;
@@ -259,11 +373,24 @@ __device__ __forceinline__ void scan_bins(Smem& sm, uint32_t want, double goal, 
             } else {
                 hit = c[i] != 0 && cb + c[i] >= want;
             }
-            if (hit && at < 0) at = i, ab = b, ac = cb;
+            if (hit && at < 0) {
+                at = i;
+                at_hi = b.hi;
+                at_lo = b.lo;
+                at_cnt = cb;
+            }
             const bool any = MASS ? (h[i] | l[i]) != 0 : c[i] != 0;
-            if (any) last = i, lb = b, lc = cb;
+            if (any) {
+                last = i;
+                last_hi = b.hi;
+                last_lo = b.lo;
+                last_cnt = cb;
+            }
             cb += c[i];
-            if (MASS) b.hi += h[i], b.lo += l[i];
+            if (MASS) {
+                b.hi += h[i];
+                b.lo += l[i];
+            }
         }
         const unsigned long long hits = __ballot(at >= 0), lasts = __ballot(last >= 0);
         const bool found = hits != 0;
@@ -271,8 +398,9 @@ __device__ __forceinline__ void scan_bins(Smem& sm, uint32_t want, double goal, 
         if (lane == owner) {
             const int i = found ? at : last < 0 ? 0 : last;
             sm.digit = 4 * lane + i;
-            sm.before = found ? ab : lb;
-            sm.before_cnt = found ? ac : lc;
+            sm.before.hi = found ? at_hi : last_hi;
+            sm.before.lo = found ? at_lo : last_lo;
+            sm.before_cnt = found ? at_cnt : last_cnt;
             sm.in_cnt = sm.cnt[4 * lane + i];
             sm.found = found;
         }
@@ -325,11 +453,15 @@ __device__ Found descend(Smem& sm, Each each, int top, int low, uint32_t want, d
 
 // --------------------------------------------------------------- the law
 
+// Where a law's ids are found again: ranked in sm.sorted (the first n), among
+// sm.list, or in the row (with the waves' sums in sm.redd).
+enum Where { kRanked, kListed, kInRow };
+
 struct Result {
     Weigher w;
     int n;         // ids in the support
     double total;  // their weight
-    bool listed;   // the candidates are in sm.list_*
+    Where where;
     int fault;     // SV_DEV_* bits
 };
 
@@ -338,7 +470,7 @@ template <sv_dtype DT, class F>
 __device__ __forceinline__ void candidates(const Row<DT>& row, const Smem& sm, bool listed, F f) {
     if (listed) {
         for (int i = threadIdx.x; i < sm.list_n; i += kThreads)
-            f(key_logit(sm.list_key[i]), sm.list_id[i]);
+            f(key_logit(entry_key(sm.list[i])), entry_id(sm.list[i]));
     } else {
         row.each(f);
     }
@@ -357,18 +489,163 @@ __device__ __forceinline__ uint32_t ordinal_key(uint32_t ord) {
     return key;
 }
 
+// Ranks sm.list (n <= kRank entries) into sm.sorted, with weights and running
+// sums in that order.  The list's own order, which atomics made, does not show.
+__device__ __forceinline__ void rank_list(const Weigher& w, Smem& sm, int n) {
+    const int i = threadIdx.x, lane = i & 63, wave = i >> 6;
+    if (i < n) {
+        const unsigned long long mine = sm.list[i];
+        int rank = 0;
+        for (int j = 0; j < n; ++j) rank += sm.list[j] > mine;
+        sm.sorted[rank] = mine;
+    }
+    __syncthreads();
+    double x = 0.0;
+    if (i < n) x = w.raw(key_logit(entry_key(sm.sorted[i])));
+    double incl = 0.0;
+    if (wave < kRank / kWave) {
+        incl = wave_incl_sum_dpp(x, lane);
+        if (lane == 63) sm.redd[wave] = incl;
+    }
+    __syncthreads();
+    if (i < n) {
+        double before = 0.0;
+        for (int v = 0; v < wave; ++v) before += sm.redd[v];
+        sm.weight[i] = x;
+        sm.prefix[i] = before + incl;
+    }
+    __syncthreads();
+}
+
+// The smallest i < n for which test(i) holds, else n.
+template <class Test>
+__device__ __forceinline__ int first_of(Smem& sm, int n, Test test) {
+    __syncthreads();
+    if (threadIdx.x == 0) sm.first = n;
+    __syncthreads();
+    const int i = threadIdx.x;
+    if (i < n && test(i)) atomicMin(&sm.first, i);
+    __syncthreads();
+    return sm.first;
+}
+
+// Top-p alone: the histogram's way.  Returns false, with nothing decided, where
+// the ids next to the border do not fit the list.
+template <sv_dtype DT>
+__device__ bool find_nucleus(const Row<DT>& row, const Settings& set, Smem& sm, Result& r) {
+    Weigher& w = r.w;
+    const float m = (float)w.m, per_logit = fminf(kPerOctave * (float)w.it, 1e30f);
+    // monotone in z, whatever it rounds to
+    const auto step_of = [&](float z) {
+        return (int)fminf((m - z) * per_logit, (float)(kSteps - 1));
+    };
+    for (int i = threadIdx.x; i < kSteps; i += kThreads) sm.step[i] = 0;
+    __syncthreads();
+    double part = 0.0;
+    row.each([&](float z, int id) {
+        const double x = w.raw(z);  // -inf: 0
+        part += x;
+        // the weight in units of 2^-43: the low bits of 2^9 + x
+        const unsigned long long q =
+            (unsigned long long)__double_as_longlong(x + 512.0) & 0xfffffffffffffull;
+        if (q) atomicAdd(&sm.step[step_of(z)], q);
+    });
+    const double total = block_sum(part, sm);
+    const double goal = (double)set.p * total;
+    // the steps that can hold the border: each weight is off by at most half a unit
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const unsigned long long a = sm.step[2 * threadIdx.x], b = sm.step[2 * threadIdx.x + 1];
+    const unsigned long long incl = wave_incl_sum_dpp(a + b, lane);
+    if (lane == 63) sm.redu[wave] = incl;
+    if (threadIdx.x == 0) sm.first = sm.second = kSteps - 1, sm.list_n = 0;
+    __syncthreads();
+    unsigned long long before = incl - (a + b);
+    for (int v = 0; v < wave; ++v) before += sm.redu[v];
+    const double at = goal * 0x1p43, off = 2.0 * (double)row.vocab;
+    const double c0 = (double)(before + a), c1 = (double)(before + a + b);
+    if (c1 + off >= at) atomicMin(&sm.first, 2 * (int)threadIdx.x + (c0 + off >= at ? 0 : 1));
+    if (c1 - off >= at) atomicMin(&sm.second, 2 * (int)threadIdx.x + (c0 - off >= at ? 0 : 1));
+    __syncthreads();
+    const int b1 = sm.first, b2 = sm.second;
+    int n = 0;
+    part = 0.0;
+    row.each([&](float z, int id) {
+        const int s = step_of(z);
+        if (s < b1) {
+            part += w.raw(z);
+            ++n;
+        } else if (s <= b2 && z > -kInf) {
+            const int i = atomicAdd(&sm.list_n, 1);
+            if (i < kList) sm.list[i] = entry(order_key(z), id);
+        }
+    });
+    n = block_sum(n, sm);
+    const double above = block_sum(part, sm);
+    const int listed = sm.list_n;
+    if (listed > kRank || listed == 0 || above >= goal) return false;
+    // keep the waves' sums over the ranking
+    double mine = 0.0;
+    if (threadIdx.x < kWaves) mine = sm.redd[threadIdx.x];
+    __syncthreads();
+    rank_list(w, sm, listed);
+    const int last = first_of(sm, listed, [&](int i) { return above + sm.prefix[i] >= goal; });
+    if (last == listed) return false;
+    const unsigned long long cut = sm.sorted[last];
+    w.ckey = entry_key(cut);
+    w.cid = entry_id(cut);
+    w.s = (double)set.s;
+    if (sm.weight[last] < w.s) return true;  // min-p cuts further: summed by the caller
+    // the listed ids that stay, added to their waves' sums
+    if (threadIdx.x < kWaves) sm.hi[threadIdx.x] = sm.lo[threadIdx.x] = 0;
+    __syncthreads();
+    if ((int)threadIdx.x <= last) {
+        const int v = row.wave_of(entry_id(sm.sorted[threadIdx.x]));
+        const Mass q = to_mass(sm.weight[threadIdx.x]);
+        atomicAdd(&sm.hi[v], q.hi);
+        atomicAdd(&sm.lo[v], q.lo);
+    }
+    __syncthreads();
+    if (threadIdx.x < kWaves)
+        sm.redd[threadIdx.x] = mine + Mass{sm.hi[threadIdx.x], sm.lo[threadIdx.x]}.value();
+    __syncthreads();
+    r.n = n + last + 1;
+    r.total = 0.0;
+    for (int v = 0; v < kWaves; ++v) r.total += sm.redd[v];
+    r.where = kInRow;
+    return true;
+}
+
 template <sv_dtype DT>
 __device__ Result find_law(const Row<DT>& row, const Settings& set, Smem& sm) {
+    using Raw = typename Row<DT>::Raw;
+    // granules a thread keeps in registers from pass 1 to the gathering: 64
+    // registers, rows of up to 131,072 bf16 or 65,536 fp32 ids
+    constexpr int kHeld = 32 / Row<DT>::kBytes;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     Result r{};
     // pass 1: largest logit, faults
-    uint32_t mine = 0;
-    int bad = 0;
-    row.each([&](float z, int id) {
-        mine = max(mine, order_key(z));
-        bad |= !(z < kInf);  // NaN or +inf
-    });
+    Raw held[kHeld];
+    Extremes<DT> ex;
+#pragma unroll
+    for (int s = 0; s < kHeld; ++s) {
+        // granules outside the row read as -inf
+        if (s < row.steps) held[s] = row.raw(row.first_id(wave, s, lane));
+    }
+#pragma unroll
+    for (int s = 0; s < kHeld; ++s) {
+        if (s < row.steps) {
+#pragma unroll
+            for (int i = 0; i < 2 * Row<DT>::kBytes; ++i) ex.add(held[s].w[i]);
+        }
+    }
+    for (int s = kHeld; s < row.steps; ++s) {
+        const Raw g = row.raw(row.first_id(wave, s, lane));
+#pragma unroll
+        for (int i = 0; i < 2 * Row<DT>::kBytes; ++i) ex.add(g.w[i]);
+    }
+    const uint32_t mine = ex.top();
     const uint32_t top = block_max(mine, sm);
-    bad = __syncthreads_or(bad);
+    const int bad = __syncthreads_or(ex.bad());
     if (bad || top <= kMinusInfKey) r.fault |= SV_DEV_NONFINITE;
     if (set.bad) r.fault |= SV_DEV_BAD_PARAM;
     if (r.fault) return r;
@@ -379,67 +656,119 @@ __device__ Result find_law(const Row<DT>& row, const Settings& set, Smem& sm) {
     w.ckey = kMinusInfKey;
     w.cid = INT32_MIN;  // ids of -inf (and those before the row, read as -inf) never count
 
+    // f(logit, id) over the thread's ids of at least `least`
+    const auto gather = [&](float least, auto f) __attribute__((always_inline)) {
+        const auto look = [&](const Raw& g, int id0) __attribute__((always_inline)) {
+            float z[8];
+            g.unpack(z);
+            float big = z[0];
+#pragma unroll
+            for (int e = 1; e < 8; ++e) big = fmaxf(big, z[e]);
+            if (big >= least) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (z[e] >= least) f(z[e], id0 + e);
+            }
+        };
+#pragma unroll
+        for (int s = 0; s < kHeld; ++s)
+            if (s < row.steps) look(held[s], row.first_id(wave, s, lane));
+        for (int s = kHeld; s < row.steps; ++s) {
+            const int id0 = row.first_id(wave, s, lane);
+            look(row.raw(id0), id0);
+        }
+    };
+
     if (set.t == 0.0f) {
         // the lowest id of the largest logit
         uint32_t first = 0;
-        row.each([&](float z, int id) {
-            if (order_key(z) == top) first = max(first, ~(uint32_t)id);
-        });
+        gather(m, [&](float z, int id) { first = max(first, ~(uint32_t)id); });
         w.it = 0.0;
         w.ckey = top;
         w.cid = (int)~block_max(first, sm);
+        if (threadIdx.x == 0) {
+            sm.sorted[0] = entry(top, w.cid);
+            sm.weight[0] = 1.0;
+        }
+        __syncthreads();
         r.n = 1;
         r.total = 1.0;
+        r.where = kRanked;
         return r;
     }
-    w.it = 1.0 / (double)set.t;
+    w.it = kLog2e64 / (double)set.t;
 
     // lb: no id below this logit is in the support (nor, with top-k, among
     // the first k)
     const bool use_p = set.p < 1.0f;
     float lb = -kInf;
     if (set.k > 0 && set.k <= kThreads) {
-        // the k-th largest of the threads' maxima: k ids are at least that
+        // about the k-th largest of the threads' maxima, and no larger: k ids
+        // are at least that
+        const uint32_t low =
+            ~block_max(mine > kMinusInfKey ? ~mine : 0u, sm);  // the least of them
+        const float per = 255.0f / fmaxf((float)(top - low), 1.0f);
+        const uint32_t bin = mine > kMinusInfKey ? (uint32_t)((float)(top - mine) * per) : 0u;
         const Found f = descend<false>(
-            sm, [&](auto fn) { if (mine > kMinusInfKey) fn(~mine, [] { return 0.0; }); }, 24,
-            kLowDigit<DT>, (uint32_t)set.k, 0.0, false);
-        if (f.found) lb = key_logit(ordinal_key<DT>(f.ord));
+            sm, [&](auto fn) { if (mine > kMinusInfKey) fn(bin, [] { return 0.0; }); }, 0, 0,
+            (uint32_t)set.k, 0.0, false);
+        const uint32_t least =
+            ~block_max(mine > kMinusInfKey && bin <= f.ord ? ~mine : 0u, sm);
+        if (f.found) lb = key_logit(least);
     }
     if (set.s > 0.0f && !(use_p && set.k > 0)) {
         // a little below m + T ln s, for the roundings on the way (of the
         // logits' size, and of an exponent's: weights next to 1 round to 1)
-        const double z = w.m + log((double)set.s) / w.it;
+        const double z = w.m + log((double)set.s) * (double)set.t;
         const double slack = 1e-6 * (fabs(w.m) + fabs(z) + (double)set.t);
         lb = fmaxf(lb, (float)(z - slack));
     }
     double total = 0.0;
     if (use_p && set.k == 0) {
-        double part = 0.0;
-        row.each([&](float z, int id) { if (z > -kInf) part += w.raw(z); });
-        total = block_sum(part, sm);
-        // all ids below lb together weigh less than what top-p leaves out
-        const double left = (1.0 - (double)set.p) * total / (double)row.vocab;
-        const double z = w.m + log(left) / w.it;
-        const double slack = 1e-6 * (fabs(w.m) + fabs(z) + (double)set.t);
-        lb = fmaxf(lb, (float)(z - slack));
+        if (find_nucleus<DT>(row, set, sm, r)) {
+            if (r.n > 0) return r;
+        } else {
+            // all ids below lb together weigh less than what top-p leaves out
+            double part = 0.0;
+            row.each([&](float z, int id) { part += w.raw(z); });
+            total = block_sum(part, sm);
+            const double left = (1.0 - (double)set.p) * total / (double)row.vocab;
+            const double z = w.m + log(left) * (double)set.t;
+            const double slack = 1e-6 * (fabs(w.m) + fabs(z) + (double)set.t);
+            lb = fmaxf(lb, (float)(z - slack));
+        }
     }
     // keep what is left in LDS if it fits
-    r.listed = lb > -kInf;
-    if (r.listed) {
+    bool listed = lb > -kInf && w.ckey == kMinusInfKey;
+    if (listed) {
         if (threadIdx.x == 0) sm.list_n = 0;
         __syncthreads();
-        row.each([&](float z, int id) {
-            if (z >= lb) {
-                const int at = atomicAdd(&sm.list_n, 1);
-                if (at < kList) {
-                    sm.list_key[at] = order_key(z);
-                    sm.list_id[at] = id;
-                }
-            }
+        gather(lb, [&](float z, int id) {
+            const int at = atomicAdd(&sm.list_n, 1);
+            if (at < kList) sm.list[at] = entry(order_key(z), id);
         });
         __syncthreads();
-        r.listed = sm.list_n <= kList;
+        listed = sm.list_n <= kList;
     }
+    if (listed && sm.list_n <= kRank && !(use_p && set.k == 0)) {
+        const int all = sm.list_n;
+        rank_list(w, sm, all);
+        int n = set.k > 0 ? min(set.k, all) : all;
+        if (use_p) {
+            const double goal = (double)set.p * sm.prefix[n - 1];
+            n = min(n, first_of(sm, n, [&](int i) { return sm.prefix[i] >= goal; }) + 1);
+        }
+        if (set.s > 0.0f)
+            n = max(1, first_of(sm, n, [&](int i) { return sm.weight[i] < (double)set.s; }));
+        const unsigned long long cut = sm.sorted[n - 1];
+        w.ckey = entry_key(cut);
+        w.cid = entry_id(cut);
+        r.n = n;
+        r.total = sm.prefix[n - 1];
+        r.where = kRanked;
+        return r;
+    }
+    r.where = listed ? kListed : kInRow;
     const auto in = [&](float z) { return z >= lb && z > -kInf; };
 
     // a border after `want` of the ids at key ckey, of which in_cnt take part
@@ -450,7 +779,7 @@ __device__ Result find_law(const Row<DT>& row, const Settings& set, Smem& sm) {
             const Found f = descend<false>(
                 sm,
                 [&](auto fn) {
-                    candidates(row, sm, r.listed, [&](float z, int id) {
+                    candidates(row, sm, listed, [&](float z, int id) {
                         if (order_key(z) == key && was.above(key, id))
                             fn((uint32_t)id, [] { return 0.0; });
                     });
@@ -466,7 +795,7 @@ __device__ Result find_law(const Row<DT>& row, const Settings& set, Smem& sm) {
         const Found f = descend<false>(
             sm,
             [&](auto fn) {
-                candidates(row, sm, r.listed, [&](float z, int id) {
+                candidates(row, sm, listed, [&](float z, int id) {
                     if (in(z)) fn(~order_key(z), [] { return 0.0; });
                 });
             },
@@ -474,10 +803,10 @@ __device__ Result find_law(const Row<DT>& row, const Settings& set, Smem& sm) {
         if (f.found)
             cut_ties(ordinal_key<DT>(f.ord), (uint32_t)set.k - f.before_cnt, f.in_cnt);
     }
-    if (use_p) {
+    if (use_p && w.s == 0.0) {
         if (set.k > 0) {
             double part = 0.0;
-            if (r.listed) {
+            if (listed) {
                 // the list's order is not fixed: gathered in fixed point
                 __syncthreads();
                 if (threadIdx.x == 0) sm.hi[0] = sm.lo[0] = 0;
@@ -502,7 +831,7 @@ __device__ Result find_law(const Row<DT>& row, const Settings& set, Smem& sm) {
         const Found f = descend<true>(
             sm,
             [&](auto fn) {
-                candidates(row, sm, r.listed, [&](float z, int id) {
+                candidates(row, sm, listed, [&](float z, int id) {
                     if (in(z) && w.above(order_key(z), id))
                         fn(~order_key(z), [&] { return w.raw(z); });
                 });
@@ -520,7 +849,7 @@ __device__ Result find_law(const Row<DT>& row, const Settings& set, Smem& sm) {
 
     // how many, and their weight
     int n = 0;
-    if (r.listed) {
+    if (listed) {
         __syncthreads();
         if (threadIdx.x == 0) sm.hi[0] = sm.lo[0] = 0;
         __syncthreads();
@@ -551,12 +880,14 @@ __device__ Result find_law(const Row<DT>& row, const Settings& set, Smem& sm) {
     return r;
 }
 
-// The smallest id whose running sum, over a row in wave segments, passes goal:
-// the waves' sums are in sm.redd; the wave that holds the crossing walks its
-// segment again.  sum8(id0, x) gives the 8 weights at ids id0 .. id0 + 7.
-// If rounding leaves none, the last id of positive weight.
-template <class Sum8, class FirstId>
-__device__ int walk_row(Smem& sm, double goal, int steps, FirstId first_id, int vocab, Sum8 sum8) {
+// The smallest id whose running sum, over a row in wave segments, passes goal.
+// The waves' sums are in sm.redd; all waves together sum the steps of the
+// segment that holds the crossing, one wave walks the step that does.
+// weights(id0, x) gives the 8 weights at ids id0 .. id0 + 7.  If rounding leaves
+// no such id, the last one of positive weight.
+template <class Weights, class FirstId>
+__device__ int walk_row(Smem& sm, double goal, int steps, FirstId first_id, int vocab,
+                        Weights weights) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     double before = 0.0;
     int owner = -1;
@@ -573,37 +904,57 @@ __device__ int walk_row(Smem& sm, double goal, int steps, FirstId first_id, int 
         for (int w = 0; w < kWaves; ++w)
             if (sm.redd[w] > 0.0) owner = w;
     }
-    if (wave == owner) {
-        int tok = -1, last = -1;
-        for (int s = 0; s < steps && tok < 0; ++s) {
-            const int id0 = first_id(owner, s, lane);
-            double x[8], mine = 0.0;
-            if (id0 < vocab) {
-                sum8(id0, x);
-            } else {
+    const auto read = [&](int s, double* x) {
+        const int id0 = first_id(owner, s, lane);
+        double mine = 0.0;
+        if (id0 < vocab) {
+            weights(id0, x);
+        } else {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = 0.0;
-            }
-            int mylast = -1;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                mine += x[e];
-                if (x[e] > 0.0) mylast = id0 + e;
-            }
-            const double incl = wave_incl_sum_dpp(mine, lane);
-            double c = before + (incl - mine);
-            int hit = -1;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                c += x[e];
-                if (hit < 0 && x[e] > 0.0 && c > goal) hit = id0 + e;
-            }
-            const unsigned long long hits = __ballot(hit >= 0), some = __ballot(mylast >= 0);
-            if (hits) tok = __builtin_amdgcn_readlane(hit, __builtin_ctzll(hits));
-            if (some) last = __builtin_amdgcn_readlane(mylast, 63 - __builtin_clzll(some));
-            before += lane63(incl);
+            for (int e = 0; e < 8; ++e) x[e] = 0.0;
         }
-        if (lane == 0) sm.redi[0] = tok >= 0 ? tok : last;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) mine += x[e];
+        return mine;
+    };
+    for (int s = wave; s < steps; s += kWaves) {
+        double x[8];
+        const double sum = wave_sum(read(s, x));
+        if (lane == 0) sm.seg[s] = sum;
+    }
+    __syncthreads();
+    int step = -1, positive = 0;
+    double at = before;
+    for (int s = 0; s < steps; ++s) {
+        if (sm.seg[s] > 0.0) positive = s;
+        if (before + sm.seg[s] > goal) {
+            step = s;
+            at = before;
+            break;
+        }
+        before += sm.seg[s];
+    }
+    if (step < 0) {
+        step = positive;
+        goal = kInf;
+    }
+    if (wave == 0) {
+        double x[8];
+        const double mine = read(step, x);
+        const int id0 = first_id(owner, step, lane);
+        double c = at + (wave_incl_sum_dpp(mine, lane) - mine);
+        int hit = -1, last = -1;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            c += x[e];
+            if (x[e] > 0.0) last = id0 + e;
+            if (hit < 0 && x[e] > 0.0 && c > goal) hit = id0 + e;
+        }
+        const unsigned long long hits = __ballot(hit >= 0), some = __ballot(last >= 0);
+        int tok = 0;
+        if (hits) tok = __builtin_amdgcn_readlane(hit, __builtin_ctzll(hits));
+        else if (some) tok = __builtin_amdgcn_readlane(last, 63 - __builtin_clzll(some));
+        if (lane == 0) sm.redi[0] = tok;
     }
     __syncthreads();
     return sm.redi[0];
@@ -612,9 +963,26 @@ __device__ int walk_row(Smem& sm, double goal, int steps, FirstId first_id, int 
 // The id a uniform u in [0, 1) draws from a law find_law has just made.
 template <sv_dtype DT>
 __device__ int draw(const Row<DT>& row, const Result& r, float u, Smem& sm) {
-    if (r.w.it == 0.0) return r.w.cid;
     const double goal = (double)u * r.total;
-    if (!r.listed) {
+    if (r.where == kRanked) {
+        if (r.n == 1) return entry_id(sm.sorted[0]);
+        // running sums over ascending ids: each thread adds, in rank order,
+        // the weights of the ids up to its own
+        const int i = threadIdx.x;
+        if (i == 0) sm.first = INT32_MAX, sm.second = -1;
+        __syncthreads();
+        if (i < r.n && sm.weight[i] > 0.0) {
+            const uint32_t mine = (uint32_t)sm.sorted[i];  // ~id
+            double c = 0.0;
+            for (int j = 0; j < r.n; ++j)
+                c += (uint32_t)sm.sorted[j] >= mine ? sm.weight[j] : 0.0;
+            if (c > goal) atomicMin(&sm.first, (int)~mine);
+            atomicMax(&sm.second, (int)~mine);
+        }
+        __syncthreads();
+        return sm.first == INT32_MAX ? sm.second : sm.first;
+    }
+    if (r.where == kInRow) {
         return walk_row(
             sm, goal, row.steps,
             [&](int w, int s, int l) { return row.first_id(w, s, l); }, row.vocab,

@@ -70,7 +70,7 @@ __global__ __launch_bounds__(law::kThreads) void laws_kernel(VerifyTruncatedArgs
 __device__ law::Weigher weigher(const LawRecord& rec, const law::Settings& set) {
     law::Weigher w;
     w.m = (double)rec.top;
-    w.it = set.t == 0.0f ? 0.0 : 1.0 / (double)set.t;
+    w.it = set.t == 0.0f ? 0.0 : law::kLog2e64 / (double)set.t;
     w.s = set.t == 0.0f ? 0.0 : (double)set.s;
     w.ckey = rec.ckey;
     w.cid = rec.cid;
