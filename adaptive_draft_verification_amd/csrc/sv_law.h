@@ -19,8 +19,8 @@
 //    the threads' own maxima, min-p's logit) leaves a few candidates, which are
 //    gathered in LDS, ranked by counting and summed there;
 //  - top-p alone: one pass sums the row and its histogram over 2048 steps of
-//    the weight (2^(1/32) each); the step that holds the border is gathered and
-//    ranked the same way while the ids above it are summed;
+//    the weight (2^(1/32) each); the steps next to the border are gathered and
+//    searched the same way while the ids above them are summed;
 //  - anything else, and what does not fit the lists (long runs of equal
 //    logits): the border is found digit by digit, 256 bins over 8 bits of the
 //    ordered key, then the next 8 bits within the bin that holds the border.
@@ -35,7 +35,7 @@ namespace law {
 constexpr int kThreads = 1024;
 constexpr int kWaves = kThreads / kWave;
 constexpr int kList = 2048;  // candidates kept in LDS
-constexpr int kRank = 512;   // candidates ranked by counting
+constexpr int kRank = 256;   // candidates ranked by counting
 constexpr int kSteps = 2048; // histogram of the weights, kPerOctave steps for a factor of 2
 constexpr float kPerOctave = 32.0f;
 constexpr int kMaxSteps = (SV_MAX_VOCAB + 8) / 8 / (kWaves * kWave) + 1;  // of a wave's segment
@@ -108,25 +108,25 @@ __device__ __forceinline__ double pow2(double t) {
     return __builtin_amdgcn_ldexp(fma(q, r, 1.0), n);
 }
 
-// The ids of a law and their weights.
+// The ids of a law and their weights: logits above zc, and those equal to it
+// up to id cid, of weight at least s.
 struct Weigher {
-    double m, it;   // largest logit, log2(e) / T (0: T = 0, one id of weight 1)
-    double s;       // min-p
-    uint32_t ckey;  // the last logit's key and, among its ids, the last id
+    double m, it;  // largest logit, log2(e) / T (0: T = 0, one id of weight 1)
+    double s;      // min-p
+    float zc;
     int32_t cid;
-    __device__ __forceinline__ bool above(uint32_t key, int id) const {
-        return key > ckey || (key == ckey && id <= cid);
+    __device__ __forceinline__ bool above(float z, int id) const {
+        return z > zc || (z == zc && id <= cid);
     }
     __device__ __forceinline__ double raw(float z) const { return pow2(((double)z - m) * it); }
     __device__ __forceinline__ double operator()(float z, int id) const {
-        if (!above(order_key(z), id)) return 0.0;
         const double w = raw(z);
-        return w >= s ? w : 0.0;
+        return above(z, id) && w >= s ? w : 0.0;
     }
 };
 
 struct Smem {
-    unsigned long long step[kSteps];   // histogram of the weights, in 2^-43
+    uint32_t step[kSteps];             // histogram of the weights
     unsigned long long list[kList];    // candidates: key, then ~id: larger is earlier
     unsigned long long sorted[kRank];  // ranked
     double weight[kRank];
@@ -135,10 +135,9 @@ struct Smem {
     unsigned long long hi[256], lo[256];
     uint32_t cnt[256];
     int list_n;
-    uint32_t red[kWaves], red2[kWaves];
+    uint32_t red[kWaves];
     int redi[kWaves];
     double redd[kWaves];
-    unsigned long long redu[kWaves];
     int first, second;
     // what a scan of the bins found
     uint32_t digit, before_cnt, in_cnt;
@@ -224,23 +223,38 @@ struct Row {
     }
     // The wave that holds an id.
     __device__ __forceinline__ int wave_of(int id) const { return ((id + shift) >> 3) / per; }
-    // f(logit, id) over the calling thread's ids, the next granule in flight
+    // f(granule, first id) over the calling thread's granules, kAhead loads of
+    // them at a time.  Granules outside the row read as -inf.
+    template <int kAhead, class F>
+    __device__ __forceinline__ void granules(F f) const {
+        const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+        for (int s = 0; s < steps; s += kAhead) {
+            if (__builtin_amdgcn_readfirstlane(first_id(wave, s, 0)) >= vocab) break;
+            Raw g[kAhead];
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i)
+                if (s + i < steps) g[i] = raw(first_id(wave, s + i, lane));
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i)
+                if (s + i < steps) f(g[i], first_id(wave, s + i, lane));
+        }
+    }
+    // f(logit, id) over the calling thread's ids, the next granule in flight;
+    // lanes whose granule is outside the row take part with logits of -inf
     template <class F>
     __device__ __forceinline__ void each(F f) const {
         const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
         int id0 = first_id(wave, 0, lane);
-        if (id0 >= vocab) return;
         Raw next = raw(id0);
-        for (int s = 1;; ++s) {
+        for (int s = 1; s <= steps; ++s) {
+            if (first_id(wave, s - 1, 0) >= vocab) break;
             const Raw now = next;
             const int id1 = first_id(wave, s, lane);
-            const bool more = s < steps && id1 < vocab;
-            if (more) next = raw(id1);
+            if (s < steps) next = raw(id1);
             float z[8];
             now.unpack(z);
 #pragma unroll
             for (int e = 0; e < 8; ++e) f(z[e], id0 + e);
-            if (!more) return;
             id0 = id1;
         }
     }
@@ -496,6 +510,7 @@ __device__ __forceinline__ void rank_list(const Weigher& w, Smem& sm, int n) {
     if (i < n) {
         const unsigned long long mine = sm.list[i];
         int rank = 0;
+#pragma unroll 4
         for (int j = 0; j < n; ++j) rank += sm.list[j] > mine;
         sm.sorted[rank] = mine;
     }
@@ -517,7 +532,7 @@ __device__ __forceinline__ void rank_list(const Weigher& w, Smem& sm, int n) {
     __syncthreads();
 }
 
-// The smallest i < n for which test(i) holds, else n.
+// The smallest i < n for which test(i) holds, else n (n <= kThreads).
 template <class Test>
 __device__ __forceinline__ int first_of(Smem& sm, int n, Test test) {
     __syncthreads();
@@ -529,11 +544,123 @@ __device__ __forceinline__ int first_of(Smem& sm, int n, Test test) {
     return sm.first;
 }
 
-// Top-p alone: the histogram's way.  Returns false, with nothing decided, where
-// the ids next to the border do not fit the list.
+// Sums 64-bit weights of the listed ids that live(z, id) leaves, and counts
+// them, whatever the list's order.
+template <class Live>
+__device__ __forceinline__ double sum_list(Smem& sm, const Weigher& w, int& n, Live live) {
+    __syncthreads();
+    if (threadIdx.x == 0) sm.hi[0] = sm.lo[0] = 0, sm.second = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < sm.list_n; i += kThreads) {
+        const float z = key_logit(entry_key(sm.list[i]));
+        const double x = w.raw(z);
+        if (!live(z, entry_id(sm.list[i]), x)) continue;
+        const Mass q = to_mass(x);
+        atomicAdd(&sm.hi[0], q.hi);
+        atomicAdd(&sm.lo[0], q.lo);
+        atomicAdd(&sm.second, 1);
+    }
+    __syncthreads();
+    n = sm.second;
+    return Mass{sm.hi[0], sm.lo[0]}.value();
+}
+
+// Moves the border of w behind the first `want` of the ids (candidates that w
+// has now) whose logit has this key, of which in_cnt take part.
 template <sv_dtype DT>
-__device__ bool find_nucleus(const Row<DT>& row, const Settings& set, Smem& sm, Result& r) {
-    Weigher& w = r.w;
+__device__ __forceinline__ void cut_ties(const Row<DT>& row, Smem& sm, bool listed, Weigher& w,
+                                         uint32_t key, uint32_t want, uint32_t in_cnt) {
+    const float zk = key_logit(key);
+    int cid = INT32_MAX;
+    if (want < in_cnt) {
+        const Weigher was = w;
+        const Found f = descend<false>(
+            sm,
+            [&](auto fn) {
+                candidates(row, sm, listed, [&](float z, int id) {
+                    if (z == zk && was.above(z, id)) fn((uint32_t)id, [] { return 0.0; });
+                });
+            },
+            16, 0, want, 0.0, false);
+        cid = (int)f.ord;
+    }
+    w.zc = zk;
+    w.cid = cid;
+}
+
+// The border of top-p among the candidates: where their running weight reaches
+// goal.  False if it does not.
+template <sv_dtype DT, class In>
+__device__ __forceinline__ bool cut_mass(const Row<DT>& row, Smem& sm, bool listed, Weigher& w,
+                                         double goal, In in) {
+    const Found f = descend<true>(
+        sm,
+        [&](auto fn) {
+            candidates(row, sm, listed, [&](float z, int id) {
+                if (in(z) && w.above(z, id)) fn(~order_key(z), [&] { return w.raw(z); });
+            });
+        },
+        24, kLowDigit<DT>, 0, goal, false);
+    if (!f.found) return false;
+    const uint32_t key = ordinal_key<DT>(f.ord);
+    const double one = w.raw(key_logit(key));
+    double want = one > 0.0 ? ceil((goal - f.before.value()) / one) : 1.0;
+    want = fmin(fmax(want, 1.0), (double)f.in_cnt);
+    cut_ties(row, sm, listed, w, key, (uint32_t)want, f.in_cnt);
+    return true;
+}
+
+// The law by digits: any settings, any row.  lb: no id below it matters;
+// listed: the ids from lb up are in sm.list.  Not inlined: few rows need it,
+// and the others' code stays small.
+template <sv_dtype DT>
+__device__ __attribute__((noinline)) void find_by_digits(const Row<DT>& row, const Settings& set,
+                                                         Smem& sm, float lb, bool listed,
+                                                         Result& r) {
+    Weigher w = r.w;
+    const bool use_p = set.p < 1.0f;
+    const auto in = [&](float z) { return z >= lb && z > -kInf; };
+    if (set.k > 0) {
+        const Found f = descend<false>(
+            sm,
+            [&](auto fn) {
+                candidates(row, sm, listed, [&](float z, int id) {
+                    if (in(z)) fn(~order_key(z), [] { return 0.0; });
+                });
+            },
+            24, kLowDigit<DT>, (uint32_t)set.k, 0.0, false);
+        if (f.found)
+            cut_ties(row, sm, listed, w, ordinal_key<DT>(f.ord), (uint32_t)set.k - f.before_cnt,
+                     f.in_cnt);
+    }
+    if (use_p) {
+        double total;
+        int n;
+        if (listed) {
+            total = sum_list(sm, w, n, [&](float z, int id, double) { return w.above(z, id); });
+        } else {
+            double part = 0.0;
+            row.each([&](float z, int id) { part += w.above(z, id) ? w.raw(z) : 0.0; });
+            total = block_sum(part, sm);
+        }
+        cut_mass(row, sm, listed, w, (double)set.p * total, in);
+    }
+    w.s = (double)set.s;
+    r.w = w;
+    if (listed) {
+        r.total = sum_list(sm, w, r.n, [&](float z, int id, double x) {
+            return w.above(z, id) && x >= w.s;
+        });
+    }
+    r.where = listed ? kListed : kInRow;
+}
+
+// Top-p alone.  Returns false, with nothing decided, where the ids next to the
+// border do not fit the list.
+template <sv_dtype DT>
+__device__ __forceinline__ bool find_nucleus(const Row<DT>& row, const Settings& set, Smem& sm,
+                                             Result& r) {
+    Weigher w = r.w;
     const float m = (float)w.m, per_logit = fminf(kPerOctave * (float)w.it, 1e30f);
     // monotone in z, whatever it rounds to
     const auto step_of = [&](float z) {
@@ -541,168 +668,134 @@ __device__ bool find_nucleus(const Row<DT>& row, const Settings& set, Smem& sm, 
     };
     for (int i = threadIdx.x; i < kSteps; i += kThreads) sm.step[i] = 0;
     __syncthreads();
+    // The histogram only says where to look.  An id adds its weight over the
+    // step's largest (between 1 and 2^(-1/32), linear within 3e-5) in units of
+    // 1/1024: at most 2^30 a step.  (LDS adds in fp32 took 170 clocks a wave
+    // here, 64-bit integer ones 31.)
     double part = 0.0;
     row.each([&](float z, int id) {
-        const double x = w.raw(z);  // -inf: 0
-        part += x;
-        // the weight in units of 2^-43: the low bits of 2^9 + x
-        const unsigned long long q =
-            (unsigned long long)__double_as_longlong(x + 512.0) & 0xfffffffffffffull;
-        if (q) atomicAdd(&sm.step[step_of(z)], q);
+        part += w.raw(z);  // -inf: 0
+        const float v = fminf((m - z) * per_logit, (float)(kSteps - 1));
+        const float f = v - floorf(v);
+        atomicAdd(&sm.step[(int)v], (uint32_t)fmaf(f, -1024.0f * (1.0f - 0.978572f), 1024.5f));
     });
     const double total = block_sum(part, sm);
     const double goal = (double)set.p * total;
-    // the steps that can hold the border: each weight is off by at most half a unit
+    // The border is where the weight behind it falls to total - goal; taken
+    // from that side, a histogram off by 2^-11 of what it holds is off by
+    // little where top-p leaves little out.
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const unsigned long long a = sm.step[2 * threadIdx.x], b = sm.step[2 * threadIdx.x + 1];
-    const unsigned long long incl = wave_incl_sum_dpp(a + b, lane);
-    if (lane == 63) sm.redu[wave] = incl;
+    const double unit = pow2(-2.0 / (double)kPerOctave * (double)threadIdx.x) * 0x1p-10;
+    const double a = (double)sm.step[2 * threadIdx.x] * unit;
+    const double b = (double)sm.step[2 * threadIdx.x + 1] * unit * 0.97857206208770014;
+    const double incl = wave_incl_sum_dpp(a + b, lane);
+    __syncthreads();
+    if (lane == 63) sm.redd[wave] = incl;
     if (threadIdx.x == 0) sm.first = sm.second = kSteps - 1, sm.list_n = 0;
     __syncthreads();
-    unsigned long long before = incl - (a + b);
-    for (int v = 0; v < wave; ++v) before += sm.redu[v];
-    const double at = goal * 0x1p43, off = 2.0 * (double)row.vocab;
-    const double c0 = (double)(before + a), c1 = (double)(before + a + b);
-    if (c1 + off >= at) atomicMin(&sm.first, 2 * (int)threadIdx.x + (c0 + off >= at ? 0 : 1));
-    if (c1 - off >= at) atomicMin(&sm.second, 2 * (int)threadIdx.x + (c0 - off >= at ? 0 : 1));
+    double before = incl - (a + b), all = 0.0;
+    for (int v = 0; v < kWaves; ++v) {
+        if (v < wave) before += sm.redd[v];
+        all += sm.redd[v];
+    }
+    const double left = total - goal, off = 6e-4 * left + 1e-12 * total;
+    const double t0 = all - (before + a), t1 = all - (before + a + b);  // behind the two steps
+    if (t1 - off <= left) atomicMin(&sm.first, 2 * (int)threadIdx.x + (t0 - off <= left ? 0 : 1));
+    if (t1 + off <= left) atomicMin(&sm.second, 2 * (int)threadIdx.x + (t0 + off <= left ? 0 : 1));
     __syncthreads();
     const int b1 = sm.first, b2 = sm.second;
     int n = 0;
     part = 0.0;
     row.each([&](float z, int id) {
         const int s = step_of(z);
-        if (s < b1) {
-            part += w.raw(z);
-            ++n;
-        } else if (s <= b2 && z > -kInf) {
+        const bool higher = s < b1, near = !higher && s <= b2 && z > -kInf;
+        n += __popcll(__ballot(higher));
+        if (higher) part += w.raw(z);
+        if (near) {
             const int i = atomicAdd(&sm.list_n, 1);
             if (i < kList) sm.list[i] = entry(order_key(z), id);
         }
     });
-    n = block_sum(n, sm);
+    // every lane of a wave holds the wave's count
+    n = block_sum(lane == 0 ? n : 0, sm);
     const double above = block_sum(part, sm);
     const int listed = sm.list_n;
-    if (listed > kRank || listed == 0 || above >= goal) return false;
-    // keep the waves' sums over the ranking
+    if (listed > kList || listed == 0 || above >= goal) return false;
+    // the waves' sums, kept over the search
     double mine = 0.0;
     if (threadIdx.x < kWaves) mine = sm.redd[threadIdx.x];
     __syncthreads();
-    rank_list(w, sm, listed);
-    const int last = first_of(sm, listed, [&](int i) { return above + sm.prefix[i] >= goal; });
-    if (last == listed) return false;
-    const unsigned long long cut = sm.sorted[last];
-    w.ckey = entry_key(cut);
-    w.cid = entry_id(cut);
+    if (listed <= kRank) {
+        rank_list(w, sm, listed);
+        const int last = first_of(sm, listed, [&](int i) { return above + sm.prefix[i] >= goal; });
+        if (last == listed) return false;
+        w.zc = key_logit(entry_key(sm.sorted[last]));
+        w.cid = entry_id(sm.sorted[last]);
+    } else if (!cut_mass(row, sm, true, w, goal - above, [](float) { return true; })) {
+        return false;
+    }
     w.s = (double)set.s;
-    if (sm.weight[last] < w.s) return true;  // min-p cuts further: summed by the caller
+    r.w = w;
+    r.where = kInRow;
+    r.n = 0;
+    if (w.raw(w.zc) < w.s) return true;  // min-p cuts further: summed by the caller
     // the listed ids that stay, added to their waves' sums
-    if (threadIdx.x < kWaves) sm.hi[threadIdx.x] = sm.lo[threadIdx.x] = 0;
     __syncthreads();
-    if ((int)threadIdx.x <= last) {
-        const int v = row.wave_of(entry_id(sm.sorted[threadIdx.x]));
-        const Mass q = to_mass(sm.weight[threadIdx.x]);
+    if (threadIdx.x < kWaves) sm.hi[threadIdx.x] = sm.lo[threadIdx.x] = 0;
+    if (threadIdx.x == 0) sm.second = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < listed; i += kThreads) {
+        const float z = key_logit(entry_key(sm.list[i]));
+        const int id = entry_id(sm.list[i]);
+        if (!w.above(z, id)) continue;
+        const int v = row.wave_of(id);
+        const Mass q = to_mass(w.raw(z));
         atomicAdd(&sm.hi[v], q.hi);
         atomicAdd(&sm.lo[v], q.lo);
+        atomicAdd(&sm.second, 1);
     }
     __syncthreads();
     if (threadIdx.x < kWaves)
         sm.redd[threadIdx.x] = mine + Mass{sm.hi[threadIdx.x], sm.lo[threadIdx.x]}.value();
     __syncthreads();
-    r.n = n + last + 1;
+    r.n = n + sm.second;
     r.total = 0.0;
     for (int v = 0; v < kWaves; ++v) r.total += sm.redd[v];
-    r.where = kInRow;
     return true;
 }
 
 template <sv_dtype DT>
-__device__ Result find_law(const Row<DT>& row, const Settings& set, Smem& sm) {
+__device__ __forceinline__ Result find_law(const Row<DT>& row, const Settings& set, Smem& sm) {
     using Raw = typename Row<DT>::Raw;
-    // granules a thread keeps in registers from pass 1 to the gathering: 64
-    // registers, rows of up to 131,072 bf16 or 65,536 fp32 ids
-    constexpr int kHeld = 32 / Row<DT>::kBytes;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    constexpr int kAhead = 16 / Row<DT>::kBytes;  // 128 bytes a lane in flight
+    const int lane = threadIdx.x & 63;
     Result r{};
     // pass 1: largest logit, faults
-    Raw held[kHeld];
     Extremes<DT> ex;
-#pragma unroll
-    for (int s = 0; s < kHeld; ++s) {
-        // granules outside the row read as -inf
-        if (s < row.steps) held[s] = row.raw(row.first_id(wave, s, lane));
-    }
-#pragma unroll
-    for (int s = 0; s < kHeld; ++s) {
-        if (s < row.steps) {
-#pragma unroll
-            for (int i = 0; i < 2 * Row<DT>::kBytes; ++i) ex.add(held[s].w[i]);
-        }
-    }
-    for (int s = kHeld; s < row.steps; ++s) {
-        const Raw g = row.raw(row.first_id(wave, s, lane));
+    row.template granules<kAhead>([&](const Raw& g, int) {
 #pragma unroll
         for (int i = 0; i < 2 * Row<DT>::kBytes; ++i) ex.add(g.w[i]);
-    }
+    });
     const uint32_t mine = ex.top();
     const uint32_t top = block_max(mine, sm);
     const int bad = __syncthreads_or(ex.bad());
     if (bad || top <= kMinusInfKey) r.fault |= SV_DEV_NONFINITE;
     if (set.bad) r.fault |= SV_DEV_BAD_PARAM;
     if (r.fault) return r;
-    const float m = key_logit(top);
     Weigher& w = r.w;
-    w.m = (double)m;
+    w.m = (double)key_logit(top);
+    w.it = set.t == 0.0f ? 0.0 : kLog2e64 / (double)set.t;
     w.s = 0.0;
-    w.ckey = kMinusInfKey;
+    w.zc = -kInf;
     w.cid = INT32_MIN;  // ids of -inf (and those before the row, read as -inf) never count
-
-    // f(logit, id) over the thread's ids of at least `least`
-    const auto gather = [&](float least, auto f) __attribute__((always_inline)) {
-        const auto look = [&](const Raw& g, int id0) __attribute__((always_inline)) {
-            float z[8];
-            g.unpack(z);
-            float big = z[0];
-#pragma unroll
-            for (int e = 1; e < 8; ++e) big = fmaxf(big, z[e]);
-            if (big >= least) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (z[e] >= least) f(z[e], id0 + e);
-            }
-        };
-#pragma unroll
-        for (int s = 0; s < kHeld; ++s)
-            if (s < row.steps) look(held[s], row.first_id(wave, s, lane));
-        for (int s = kHeld; s < row.steps; ++s) {
-            const int id0 = row.first_id(wave, s, lane);
-            look(row.raw(id0), id0);
-        }
-    };
-
-    if (set.t == 0.0f) {
-        // the lowest id of the largest logit
-        uint32_t first = 0;
-        gather(m, [&](float z, int id) { first = max(first, ~(uint32_t)id); });
-        w.it = 0.0;
-        w.ckey = top;
-        w.cid = (int)~block_max(first, sm);
-        if (threadIdx.x == 0) {
-            sm.sorted[0] = entry(top, w.cid);
-            sm.weight[0] = 1.0;
-        }
-        __syncthreads();
-        r.n = 1;
-        r.total = 1.0;
-        r.where = kRanked;
-        return r;
-    }
-    w.it = kLog2e64 / (double)set.t;
 
     // lb: no id below this logit is in the support (nor, with top-k, among
     // the first k)
     const bool use_p = set.p < 1.0f;
     float lb = -kInf;
-    if (set.k > 0 && set.k <= kThreads) {
+    if (set.t == 0.0f) {
+        lb = key_logit(top);
+    } else if (set.k > 0 && set.k <= kThreads) {
         // about the k-th largest of the threads' maxima, and no larger: k ids
         // are at least that
         const uint32_t low =
@@ -716,41 +809,44 @@ __device__ Result find_law(const Row<DT>& row, const Settings& set, Smem& sm) {
             ~block_max(mine > kMinusInfKey && bin <= f.ord ? ~mine : 0u, sm);
         if (f.found) lb = key_logit(least);
     }
-    if (set.s > 0.0f && !(use_p && set.k > 0)) {
+    if (set.s > 0.0f && set.t > 0.0f && !(use_p && set.k > 0)) {
         // a little below m + T ln s, for the roundings on the way (of the
         // logits' size, and of an exponent's: weights next to 1 round to 1)
         const double z = w.m + log((double)set.s) * (double)set.t;
         const double slack = 1e-6 * (fabs(w.m) + fabs(z) + (double)set.t);
         lb = fmaxf(lb, (float)(z - slack));
     }
-    double total = 0.0;
-    if (use_p && set.k == 0) {
-        if (find_nucleus<DT>(row, set, sm, r)) {
-            if (r.n > 0) return r;
-        } else {
-            // all ids below lb together weigh less than what top-p leaves out
-            double part = 0.0;
-            row.each([&](float z, int id) { part += w.raw(z); });
-            total = block_sum(part, sm);
-            const double left = (1.0 - (double)set.p) * total / (double)row.vocab;
-            const double z = w.m + log(left) * (double)set.t;
-            const double slack = 1e-6 * (fabs(w.m) + fabs(z) + (double)set.t);
-            lb = fmaxf(lb, (float)(z - slack));
-        }
+    bool decided = false;
+    if (use_p && set.k == 0 && set.t > 0.0f) {
+        decided = find_nucleus<DT>(row, set, sm, r);
+        if (decided && r.n > 0) return r;
+        lb = -kInf;
     }
     // keep what is left in LDS if it fits
-    bool listed = lb > -kInf && w.ckey == kMinusInfKey;
+    bool listed = lb > -kInf;
     if (listed) {
         if (threadIdx.x == 0) sm.list_n = 0;
         __syncthreads();
-        gather(lb, [&](float z, int id) {
-            const int at = atomicAdd(&sm.list_n, 1);
-            if (at < kList) sm.list[at] = entry(order_key(z), id);
+        // a thread whose own maximum is below the bound has none
+        if (mine >= order_key(lb)) row.template granules<kAhead>([&](const Raw& g, int id0) {
+            float z[8];
+            g.unpack(z);
+            float big = z[0];
+#pragma unroll
+            for (int e = 1; e < 8; ++e) big = fmaxf(big, z[e]);
+            if (big < lb) return;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                if (z[e] >= lb) {
+                    const int at = atomicAdd(&sm.list_n, 1);
+                    if (at < kList) sm.list[at] = entry(order_key(z[e]), id0 + e);
+                }
+            }
         });
         __syncthreads();
         listed = sm.list_n <= kList;
     }
-    if (listed && sm.list_n <= kRank && !(use_p && set.k == 0)) {
+    if (listed && sm.list_n <= kRank) {
         const int all = sm.list_n;
         rank_list(w, sm, all);
         int n = set.k > 0 ? min(set.k, all) : all;
@@ -760,123 +856,51 @@ __device__ Result find_law(const Row<DT>& row, const Settings& set, Smem& sm) {
         }
         if (set.s > 0.0f)
             n = max(1, first_of(sm, n, [&](int i) { return sm.weight[i] < (double)set.s; }));
-        const unsigned long long cut = sm.sorted[n - 1];
-        w.ckey = entry_key(cut);
-        w.cid = entry_id(cut);
+        if (set.t == 0.0f) n = 1;
+        w.zc = key_logit(entry_key(sm.sorted[n - 1]));
+        w.cid = entry_id(sm.sorted[n - 1]);
         r.n = n;
         r.total = sm.prefix[n - 1];
         r.where = kRanked;
         return r;
     }
-    r.where = listed ? kListed : kInRow;
-    const auto in = [&](float z) { return z >= lb && z > -kInf; };
-
-    // a border after `want` of the ids at key ckey, of which in_cnt take part
-    const auto cut_ties = [&](uint32_t key, uint32_t want, uint32_t in_cnt) {
-        int cid = INT32_MAX;
-        if (want < in_cnt) {
-            const Weigher was = w;
-            const Found f = descend<false>(
-                sm,
-                [&](auto fn) {
-                    candidates(row, sm, listed, [&](float z, int id) {
-                        if (order_key(z) == key && was.above(key, id))
-                            fn((uint32_t)id, [] { return 0.0; });
-                    });
-                },
-                16, 0, want, 0.0, false);
-            cid = (int)f.ord;
-        }
-        w.ckey = key;
-        w.cid = cid;
-    };
-
-    if (set.k > 0) {
-        const Found f = descend<false>(
-            sm,
-            [&](auto fn) {
-                candidates(row, sm, listed, [&](float z, int id) {
-                    if (in(z)) fn(~order_key(z), [] { return 0.0; });
-                });
-            },
-            24, kLowDigit<DT>, (uint32_t)set.k, 0.0, false);
-        if (f.found)
-            cut_ties(ordinal_key<DT>(f.ord), (uint32_t)set.k - f.before_cnt, f.in_cnt);
+    if (set.t == 0.0f) {
+        // more than kRank ids of the largest logit: the lowest
+        uint32_t first = 0;
+        row.each([&](float z, int id) { if (z >= lb) first = max(first, ~(uint32_t)id); });
+        first = block_max(first, sm);
+        w.zc = lb;
+        w.cid = (int)~first;
+        if (threadIdx.x == 0) sm.sorted[0] = entry(top, w.cid);
+        __syncthreads();
+        r.n = 1;
+        r.total = 1.0;
+        r.where = kRanked;
+        return r;
     }
-    if (use_p && w.s == 0.0) {
-        if (set.k > 0) {
-            double part = 0.0;
-            if (listed) {
-                // the list's order is not fixed: gathered in fixed point
-                __syncthreads();
-                if (threadIdx.x == 0) sm.hi[0] = sm.lo[0] = 0;
-                __syncthreads();
-                candidates(row, sm, true, [&](float z, int id) {
-                    if (w.above(order_key(z), id)) {
-                        const Mass x = to_mass(w.raw(z));
-                        atomicAdd(&sm.hi[0], x.hi);
-                        atomicAdd(&sm.lo[0], x.lo);
-                    }
-                });
-                __syncthreads();
-                total = Mass{sm.hi[0], sm.lo[0]}.value();
-            } else {
-                row.each([&](float z, int id) {
-                    if (w.above(order_key(z), id)) part += w.raw(z);
-                });
-                total = block_sum(part, sm);
-            }
-        }
-        const double goal = (double)set.p * total;
-        const Found f = descend<true>(
-            sm,
-            [&](auto fn) {
-                candidates(row, sm, listed, [&](float z, int id) {
-                    if (in(z) && w.above(order_key(z), id))
-                        fn(~order_key(z), [&] { return w.raw(z); });
-                });
-            },
-            24, kLowDigit<DT>, 0, goal, false);
-        if (f.found) {
-            const uint32_t key = ordinal_key<DT>(f.ord);
-            const double one = w.raw(key_logit(key));
-            double want = one > 0.0 ? ceil((goal - f.before.value()) / one) : 1.0;
-            want = fmin(fmax(want, 1.0), (double)f.in_cnt);
-            cut_ties(key, (uint32_t)want, f.in_cnt);
-        }
+    r.where = kInRow;
+    if (!decided) {
+        if (use_p || set.k > 0 || listed) find_by_digits<DT>(row, set, sm, lb, listed, r);
+        if (r.where == kListed) return r;
     }
-    w.s = (double)set.s;
-
-    // how many, and their weight
+    r.w.s = (double)set.s;
+    // how many, and their weight; leaves the waves' sums in sm.redd
+    const Weigher law = r.w;
     int n = 0;
-    if (listed) {
-        __syncthreads();
-        if (threadIdx.x == 0) sm.hi[0] = sm.lo[0] = 0;
-        __syncthreads();
-        candidates(row, sm, true, [&](float z, int id) {
-            if (!w.above(order_key(z), id)) return;
-            const double x = w.raw(z);
-            if (x < w.s) return;
-            ++n;
-            const Mass q = to_mass(x);
-            atomicAdd(&sm.hi[0], q.hi);
-            atomicAdd(&sm.lo[0], q.lo);
-        });
-        r.n = block_sum(n, sm);
-        r.total = Mass{sm.hi[0], sm.lo[0]}.value();
-        __syncthreads();
-    } else {
-        double part = 0.0;
+    double part = 0.0;
+    if (law.zc == -kInf && law.s == 0.0) {
         row.each([&](float z, int id) {
-            if (!w.above(order_key(z), id)) return;
-            const double x = w.raw(z);
-            if (x < w.s) return;
-            ++n;
-            part += x;
+            n += __popcll(__ballot(z > -kInf));
+            part += law.raw(z);
         });
-        r.n = block_sum(n, sm);
-        r.total = block_sum(part, sm);  // leaves the waves' sums in sm.redd
-    }
+    } else row.each([&](float z, int id) {
+        const double x = law.raw(z);
+        const bool live = law.above(z, id) && x >= law.s;
+        n += __popcll(__ballot(live));
+        part += live ? x : 0.0;
+    });
+    r.n = block_sum(lane == 0 ? n : 0, sm);
+    r.total = block_sum(part, sm);
     return r;
 }
 

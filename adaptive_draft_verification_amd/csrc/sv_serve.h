@@ -100,7 +100,7 @@ hipError_t launch_sample(const SampleArgs& a, hipStream_t stream);
 struct LawRecord {
     double total;    // the support's weight
     float top;       // the largest logit
-    uint32_t ckey;   // the support's last logit (ordered key) and last id of it
+    float zc;        // the support's last logit and last id of it
     int32_t cid;
     int32_t fault;   // SV_DEV_* bits
     double drafted;  // the weight of the position's draft id (0: outside)

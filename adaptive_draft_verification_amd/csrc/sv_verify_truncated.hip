@@ -59,7 +59,7 @@ __global__ __launch_bounds__(law::kThreads) void laws_kernel(VerifyTruncatedArgs
     if (!res.fault) {
         rec.total = res.total;
         rec.top = (float)res.w.m;
-        rec.ckey = res.w.ckey;
+        rec.zc = res.w.zc;
         rec.cid = res.w.cid;
         const int d = j < s.b ? a.draft_tokens[(int64_t)r * a.k_max + j] : -1;
         if (d >= 0 && d < a.vocab) rec.drafted = res.w(row.one(d), d);
@@ -72,7 +72,7 @@ __device__ law::Weigher weigher(const LawRecord& rec, const law::Settings& set) 
     w.m = (double)rec.top;
     w.it = set.t == 0.0f ? 0.0 : law::kLog2e64 / (double)set.t;
     w.s = set.t == 0.0f ? 0.0 : (double)set.s;
-    w.ckey = rec.ckey;
+    w.zc = rec.zc;
     w.cid = rec.cid;
     return w;
 }
