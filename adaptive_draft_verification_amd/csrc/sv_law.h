@@ -40,6 +40,7 @@ constexpr int kSteps = 2048; // histogram of the weights, kPerOctave steps for a
 constexpr float kPerOctave = 32.0f;
 constexpr int kMaxSteps = (SV_MAX_VOCAB + 8) / 8 / (kWaves * kWave) + 1;  // of a wave's segment
 constexpr double kLog2e64 = 1.4426950408889634074;
+constexpr int kQueue = 640;  // ids a wave keeps for compact(): 64 left over and 512 of a step
 constexpr float kInf = __builtin_inff();
 constexpr uint32_t kMinusInfKey = 0x007fffffu;
 
@@ -132,6 +133,8 @@ struct Smem {
     double weight[kRank];
     double prefix[kRank];
     double seg[kMaxSteps];
+    float queue_z[kWaves][kQueue];
+    int queue_id[kWaves][kQueue];
     unsigned long long hi[256], lo[256];
     uint32_t cnt[256];
     int list_n;
@@ -239,11 +242,10 @@ struct Row {
                 if (s + i < steps) f(g[i], first_id(wave, s + i, lane));
         }
     }
-    // f(logit, id) over the calling thread's ids, the next granule in flight;
-    // lanes whose granule is outside the row take part with logits of -inf
+    // f(granule, first id), one granule at a time, the next one in flight; lanes
+    // whose granule is outside the row take part with logits of -inf
     template <class F>
-    __device__ __forceinline__ void each(F f) const {
-        const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    __device__ __forceinline__ void granules_of(int wave, int lane, F f) const {
         int id0 = first_id(wave, 0, lane);
         Raw next = raw(id0);
         for (int s = 1; s <= steps; ++s) {
@@ -251,14 +253,66 @@ struct Row {
             const Raw now = next;
             const int id1 = first_id(wave, s, lane);
             if (s < steps) next = raw(id1);
-            float z[8];
-            now.unpack(z);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) f(z[e], id0 + e);
+            f(now, id0);
             id0 = id1;
         }
     }
+    // f(logit, id) over the calling thread's ids
+    template <class F>
+    __device__ __forceinline__ void each(F f) const {
+        granules_of(threadIdx.x >> 6, threadIdx.x & 63, [&](const Raw& g, int id0) {
+            float z[8];
+            g.unpack(z);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f(z[e], id0 + e);
+        });
+    }
 };
+
+// Calls use(logit, id) for the ids that keep(logit) leaves, 64 of a wave at a
+// time and in id order within the wave, the last call with fewer lanes.  Where
+// a few per cent of the ids are kept, the work on them then costs a wave per 64
+// of them and not nearly a wave per 64 ids of the row (129,280 ids, 2 % kept:
+// 30 us against 9 for the sum of their weights).
+template <sv_dtype DT, class Keep, class Use>
+__device__ __forceinline__ void compact(const Row<DT>& row, Smem& sm, Keep keep, Use use) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    float* qz = sm.queue_z[wave];
+    int* qi = sm.queue_id[wave];
+    int n = 0;  // the same in every lane
+    row.granules_of(wave, lane, [&](const typename Row<DT>::Raw& g, int id0) {
+        float z[8];
+        g.unpack(z);
+        int c = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) c += keep(z[e]) ? 1 : 0;
+        if (__ballot(c != 0) == 0) return;
+        const int incl = wave_incl_sum_dpp(c, lane);
+        int at = n + incl - c;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            if (keep(z[e])) {
+                qz[at] = z[e];
+                qi[at] = id0 + e;
+                ++at;
+            }
+        }
+        n += lane63(incl);
+        __builtin_amdgcn_wave_barrier();
+        int head = 0;
+        for (; n - head >= kWave; head += kWave) use(qz[head + lane], qi[head + lane]);
+        if (head > 0) {
+            n -= head;
+            float mz = 0.0f;
+            int mi = 0;
+            if (lane < n) mz = qz[head + lane], mi = qi[head + lane];
+            __builtin_amdgcn_wave_barrier();
+            if (lane < n) qz[lane] = mz, qi[lane] = mi;
+            __builtin_amdgcn_wave_barrier();
+        }
+    });
+    if (lane < n) use(qz[lane], qi[lane]);
+}
 
 // Largest logit and faults of a thread's ids, on the raw words: positive floats
 // order as signed integers, negative ones backwards as unsigned.
@@ -510,7 +564,7 @@ __device__ __forceinline__ void rank_list(const Weigher& w, Smem& sm, int n) {
     if (i < n) {
         const unsigned long long mine = sm.list[i];
         int rank = 0;
-#pragma unroll 4
+#pragma unroll 8
         for (int j = 0; j < n; ++j) rank += sm.list[j] > mine;
         sm.sorted[rank] = mine;
     }
@@ -535,13 +589,15 @@ __device__ __forceinline__ void rank_list(const Weigher& w, Smem& sm, int n) {
 // The smallest i < n for which test(i) holds, else n (n <= kThreads).
 template <class Test>
 __device__ __forceinline__ int first_of(Smem& sm, int n, Test test) {
-    __syncthreads();
-    if (threadIdx.x == 0) sm.first = n;
-    __syncthreads();
     const int i = threadIdx.x;
-    if (i < n && test(i)) atomicMin(&sm.first, i);
+    const unsigned long long hits = __ballot(i < n && test(i));
     __syncthreads();
-    return sm.first;
+    if ((i & 63) == 0) sm.redi[i >> 6] = hits ? i + __builtin_ctzll(hits) : n;
+    __syncthreads();
+    int r = n;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) r = min(r, sm.redi[w]);
+    return r;
 }
 
 // Sums 64-bit weights of the listed ids that live(z, id) leaves, and counts
@@ -699,19 +755,24 @@ __device__ __forceinline__ bool find_nucleus(const Row<DT>& row, const Settings&
         all += sm.redd[v];
     }
     const double left = total - goal, off = 6e-4 * left + 1e-12 * total;
-    const double t0 = all - (before + a), t1 = all - (before + a + b);  // behind the two steps
-    if (t1 - off <= left) atomicMin(&sm.first, 2 * (int)threadIdx.x + (t0 - off <= left ? 0 : 1));
-    if (t1 + off <= left) atomicMin(&sm.second, 2 * (int)threadIdx.x + (t0 + off <= left ? 0 : 1));
+    // the weight behind what is ahead of the two steps, and behind each
+    const double tb = all - before, t0 = all - (before + a), t1 = all - (before + a + b);
+    if (t1 - off <= left && !(tb - off <= left && threadIdx.x > 0))
+        sm.first = 2 * (int)threadIdx.x + (t0 - off <= left ? 0 : 1);
+    if (t1 + off <= left && !(tb + off <= left && threadIdx.x > 0))
+        sm.second = 2 * (int)threadIdx.x + (t0 + off <= left ? 0 : 1);
     __syncthreads();
     const int b1 = sm.first, b2 = sm.second;
+    // logits of step b2 or less: at least this one, or a little below
+    const float edge = m - (float)(b2 + 1) / per_logit * 1.00001f - fabsf(m) * 1e-6f;
     int n = 0;
     part = 0.0;
-    row.each([&](float z, int id) {
+    compact(row, sm, [&](float z) { return z >= edge; }, [&](float z, int id) {
         const int s = step_of(z);
-        const bool higher = s < b1, near = !higher && s <= b2 && z > -kInf;
-        n += __popcll(__ballot(higher));
-        if (higher) part += w.raw(z);
-        if (near) {
+        n += __popcll(__ballot(s < b1));
+        if (s < b1) {
+            part += w.raw(z);
+        } else if (s <= b2 && z > -kInf) {
             const int i = atomicAdd(&sm.list_n, 1);
             if (i < kList) sm.list[i] = entry(order_key(z), id);
         }
@@ -893,12 +954,14 @@ __device__ __forceinline__ Result find_law(const Row<DT>& row, const Settings& s
             n += __popcll(__ballot(z > -kInf));
             part += law.raw(z);
         });
-    } else row.each([&](float z, int id) {
-        const double x = law.raw(z);
-        const bool live = law.above(z, id) && x >= law.s;
-        n += __popcll(__ballot(live));
-        part += live ? x : 0.0;
-    });
+    } else {
+        compact(row, sm, [&](float z) { return z >= law.zc && z >= lb; }, [&](float z, int id) {
+            const double x = law.raw(z);
+            const bool live = law.above(z, id) && x >= law.s;
+            n += __popcll(__ballot(live));
+            part += live ? x : 0.0;
+        });
+    }
     r.n = block_sum(lane == 0 ? n : 0, sm);
     r.total = block_sum(part, sm);
     return r;
@@ -941,32 +1004,37 @@ __device__ int walk_row(Smem& sm, double goal, int steps, FirstId first_id, int 
         for (int e = 0; e < 8; ++e) mine += x[e];
         return mine;
     };
+    // all waves sum the segment's steps; a wave keeps its last one's weights
+    double x[8], incl = 0.0;
+    int held = -1;
     for (int s = wave; s < steps; s += kWaves) {
-        double x[8];
-        const double sum = wave_sum(read(s, x));
-        if (lane == 0) sm.seg[s] = sum;
+        incl = wave_incl_sum_dpp(read(s, x), lane);
+        held = s;
+        if (lane == 63) sm.seg[s] = incl;
     }
     __syncthreads();
     int step = -1, positive = 0;
     double at = before;
     for (int s = 0; s < steps; ++s) {
-        if (sm.seg[s] > 0.0) positive = s;
-        if (before + sm.seg[s] > goal) {
+        const double sum = sm.seg[s];
+        if (sum > 0.0) positive = s;
+        if (step < 0 && before + sum > goal) {
             step = s;
             at = before;
-            break;
         }
-        before += sm.seg[s];
+        before += sum;
     }
     if (step < 0) {
         step = positive;
         goal = kInf;
     }
-    if (wave == 0) {
-        double x[8];
-        const double mine = read(step, x);
+    if (wave == step % kWaves) {
+        if (held != step) incl = wave_incl_sum_dpp(read(step, x), lane);
         const int id0 = first_id(owner, step, lane);
-        double c = at + (wave_incl_sum_dpp(mine, lane) - mine);
+        double mine = 0.0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) mine += x[e];
+        double c = at + (incl - mine);
         int hit = -1, last = -1;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -993,18 +1061,18 @@ __device__ int draw(const Row<DT>& row, const Result& r, float u, Smem& sm) {
         // running sums over ascending ids: each thread adds, in rank order,
         // the weights of the ids up to its own
         const int i = threadIdx.x;
-        if (i == 0) sm.first = INT32_MAX, sm.second = -1;
-        __syncthreads();
+        uint32_t past = 0, mine = 0;  // ~id of a thread's own id if it is drawn past
         if (i < r.n && sm.weight[i] > 0.0) {
-            const uint32_t mine = (uint32_t)sm.sorted[i];  // ~id
+            mine = (uint32_t)sm.sorted[i];
             double c = 0.0;
+#pragma unroll 8
             for (int j = 0; j < r.n; ++j)
                 c += (uint32_t)sm.sorted[j] >= mine ? sm.weight[j] : 0.0;
-            if (c > goal) atomicMin(&sm.first, (int)~mine);
-            atomicMax(&sm.second, (int)~mine);
+            if (c > goal) past = mine;
         }
-        __syncthreads();
-        return sm.first == INT32_MAX ? sm.second : sm.first;
+        past = block_max(past, sm);
+        if (past != 0) return (int)~past;
+        return (int)block_max(mine != 0 ? ~mine : 0u, sm);  // rounding left none: the last id
     }
     if (r.where == kInRow) {
         return walk_row(

@@ -185,16 +185,15 @@ __global__ __launch_bounds__(law::kThreads) void decide_kernel(VerifyTruncatedAr
             if (minus && x[e] > 0.0) x[e] = fmax(0.0, x[e] * ip - qw(y[e], id0 + e) * iq);
         }
     };
+    // only ids of p's support weigh anything, in the residual too
     const auto sum_row = [&]() {
         double part = 0.0;
-        for (int st = 0; st < prow.steps; ++st) {
-            const int id0 = prow.first_id(wave, st, lane);
-            if (id0 >= a.vocab) break;
-            double x[8];
-            weights(id0, x);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) part += x[e];
-        }
+        law::compact(prow, sm, [&](float z) { return z >= pw.zc && z > -law::kInf; },
+                     [&](float z, int id) {
+                         double x = pw(z, id);
+                         if (minus) x = fmax(0.0, x * ip - qw(qrow.one(id), id) * iq);
+                         part += x;
+                     });
         return law::block_sum(part, sm);
     };
     double total = sum_row();
