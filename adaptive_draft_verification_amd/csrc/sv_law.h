@@ -13,7 +13,7 @@
 // fixed-point integers (two 64-bit words, 43 bits each below the point), so
 // their order does not change them.
 //
-// One workgroup of 1024 threads takes a row.  Three ways to the border, by
+// One workgroup takes a row.  Three ways to the border, by
 // what the settings ask for:
 //  - top-k up to 1024, or min-p: a bound that costs no pass (the k-th largest of
 //    the threads' own maxima, min-p's logit) leaves a few candidates, which are
@@ -32,13 +32,11 @@
 namespace sv {
 namespace law {
 
-constexpr int kThreads = 1024;
-constexpr int kWaves = kThreads / kWave;
+constexpr int kCUs = 256;    // of an MI355X
 constexpr int kList = 2048;  // candidates kept in LDS
 constexpr int kRank = 256;   // candidates ranked by counting
 constexpr int kSteps = 2048; // histogram of the weights, kPerOctave steps for a factor of 2
 constexpr float kPerOctave = 32.0f;
-constexpr int kMaxSteps = (SV_MAX_VOCAB + 8) / 8 / (kWaves * kWave) + 1;  // of a wave's segment
 constexpr double kLog2e64 = 1.4426950408889634074;
 constexpr int kQueue = 640;  // ids a wave keeps for compact(): 64 left over and 512 of a step
 constexpr float kInf = __builtin_inff();
@@ -126,7 +124,10 @@ struct Weigher {
     }
 };
 
+template <int NT>
 struct Smem {
+    static constexpr int kWaves = NT / kWave;
+    static constexpr int kMaxSteps = (SV_MAX_VOCAB + 8) / 8 / NT + 1;  // of a wave's segment
     uint32_t step[kSteps];             // histogram of the weights
     unsigned long long list[kList];    // candidates: key, then ~id: larger is earlier
     unsigned long long sorted[kRank];  // ranked
@@ -138,9 +139,9 @@ struct Smem {
     unsigned long long hi[256], lo[256];
     uint32_t cnt[256];
     int list_n;
-    uint32_t red[kWaves];
-    int redi[kWaves];
-    double redd[kWaves];
+    uint32_t red[NT / kWave];
+    int redi[NT / kWave];
+    double redd[NT / kWave];
     int first, second;
     // what a scan of the bins found
     uint32_t digit, before_cnt, in_cnt;
@@ -154,25 +155,25 @@ __device__ __forceinline__ unsigned long long entry(uint32_t key, int id) {
 __device__ __forceinline__ uint32_t entry_key(unsigned long long e) { return (uint32_t)(e >> 32); }
 __device__ __forceinline__ int entry_id(unsigned long long e) { return (int)~(uint32_t)e; }
 
-// One row, as granules of 8 ids.  Granule i starts at a 16-byte boundary and
-// holds ids 8 i - shift .. + 7; the first and last may be partly outside.  Wave
-// w holds the granules w * per .. + per - 1, in id order over (wave, step,
-// lane).
-template <sv_dtype DT>
+// One row, as granules of 8 ids (8 i .. 8 i + 7).  Wave w holds the granules w *
+// per .. + per - 1, in id order over (wave, step, lane).  Loads are 16 bytes
+// wherever a row starts: the hardware takes them at any element.
+template <sv_dtype DT, int NT>
 struct Row {
-    const char* base;  // the row's start, rounded down to 16 bytes
-    int vocab, shift, per, steps;
+    static constexpr int kWaves = NT / kWave;
+    const char* base;
+    int vocab, per, steps;
     static constexpr int kBytes = DT == SV_BF16 ? 2 : 4;
+    static constexpr int kWords = 2 * kBytes;
+    static constexpr uint32_t kFill = DT == SV_BF16 ? 0xff80ff80u : 0xff800000u;  // -inf
 
-    __device__ __forceinline__ Row(const char* row, int v) : vocab(v) {
-        shift = (int)((reinterpret_cast<uintptr_t>(row) & 15) / kBytes);
-        base = row - shift * kBytes;
-        const int n = (v + shift + 7) / 8;
+    __device__ __forceinline__ Row(const char* row, int v) : base(row), vocab(v) {
+        const int n = (v + 7) / 8;
         per = ((n + kWaves - 1) / kWaves + kWave - 1) / kWave * kWave;
         steps = per / kWave;
     }
     __device__ __forceinline__ int first_id(int wave, int step, int lane) const {
-        return (wave * per + step * kWave + lane) * 8 - shift;
+        return (wave * per + step * kWave + lane) * 8;
     }
     // 8 logits as they lie in memory
     struct Raw {
@@ -190,56 +191,92 @@ struct Row {
             }
         }
     };
-    // The 8 logits at ids id0 .. id0 + 7 (-inf outside the row).
-    __device__ __forceinline__ Raw raw(int id0) const {
+    // 16-byte loads of the granule at id0; the row's last granule as its last 8
+    // ids, which settle() moves down.  A launch of one wave a row is for rows
+    // of fewer than 8 ids, read one by one.
+    __device__ __forceinline__ Raw fetch(int id0) const {
         Raw out;
-        if (id0 >= 0 && id0 + 8 <= vocab) {
-            const uint4* at =
-                reinterpret_cast<const uint4*>(base + (int64_t)(id0 + shift) * kBytes);
+        if constexpr (NT == kWave) {
 #pragma unroll
-            for (int i = 0; i < kBytes / 2; ++i) {
-                const uint4 v = at[i];
-                out.w[4 * i] = v.x, out.w[4 * i + 1] = v.y;
-                out.w[4 * i + 2] = v.z, out.w[4 * i + 3] = v.w;
+            for (int i = 0; i < kWords; ++i) out.w[i] = kFill;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                if (id0 != 0 || e >= vocab) break;
+                const uint32_t z = __float_as_uint(one(e));
+                if (DT == SV_F32) out.w[e % kWords] = z;
+                else if (e & 1) out.w[e / 2] = (out.w[e / 2] & 0xffffu) | z;
+                else out.w[e / 2] = (out.w[e / 2] & 0xffff0000u) | (z >> 16);
             }
-            return out;
+        } else {
+            __builtin_memcpy(out.w, base + (int64_t)min(id0, vocab - 8) * kBytes, sizeof(out.w));
         }
-        uint32_t z[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int id = id0 + e;
-            z[e] = 0xff800000u;
-            if (id >= 0 && id < vocab) z[e] = __float_as_uint(one(id));
-        }
-#pragma unroll
-        for (int i = 0; i < 2 * kBytes; ++i)
-            out.w[i] = DT == SV_BF16 ? (z[(2 * i) & 7] >> 16) | (z[(2 * i + 1) & 7] & 0xffff0000u)
-                                     : z[i & 7];
         return out;
+    }
+    // Ids past the row's end read as -inf.
+    __device__ __forceinline__ void settle(Raw& g, int id0) const {
+        if constexpr (NT == kWave) return;
+        const int over = id0 + 8 - vocab;
+        if (over <= 0) return;
+        int by_words = over;
+        if (DT == SV_BF16) {
+            if (over & 1) {
+#pragma unroll
+                for (int i = 0; i < kWords; ++i)
+                    g.w[i] = (g.w[i] >> 16) |
+                             (i + 1 < kWords ? g.w[(i + 1) % kWords] << 16 : 0xff800000u);
+            }
+            by_words = over >> 1;
+        }
+#pragma unroll
+        for (int by = 1; by < kWords; by *= 2) {
+            if (by_words & by) {
+#pragma unroll
+                for (int i = 0; i < kWords; ++i)
+                    g.w[i] = i + by < kWords ? g.w[(i + by) % kWords] : kFill;
+            }
+        }
+        if (over >= 8) {
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) g.w[i] = kFill;
+        }
+    }
+    __device__ __forceinline__ Raw raw(int id0) const {
+        Raw g = fetch(id0);
+        settle(g, id0);
+        return g;
+    }
+    // Whether a step of the wave holds ids past the row's end (the same in
+    // every lane).
+    __device__ __forceinline__ bool ends_in(int wave, int step) const {
+        return __builtin_amdgcn_readfirstlane(first_id(wave, step, kWave - 1)) + 8 > vocab;
     }
     __device__ __forceinline__ void load(int id0, float* z) const { raw(id0).unpack(z); }
     __device__ __forceinline__ float one(int id) const {
-        const char* at = base + (int64_t)(id + shift) * kBytes;
+        const char* at = base + (int64_t)id * kBytes;
         if (DT == SV_BF16)
             return __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t*>(at) << 16);
         return *reinterpret_cast<const float*>(at);
     }
     // The wave that holds an id.
-    __device__ __forceinline__ int wave_of(int id) const { return ((id + shift) >> 3) / per; }
+    __device__ __forceinline__ int wave_of(int id) const { return (id >> 3) / per; }
     // f(granule, first id) over the calling thread's granules, kAhead loads of
     // them at a time.  Granules outside the row read as -inf.
     template <int kAhead, class F>
     __device__ __forceinline__ void granules(F f) const {
         const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-        for (int s = 0; s < steps; s += kAhead) {
-            if (__builtin_amdgcn_readfirstlane(first_id(wave, s, 0)) >= vocab) break;
+        int s = 0;
+        for (; s + kAhead <= steps && !ends_in(wave, s + kAhead - 1); s += kAhead) {
             Raw g[kAhead];
 #pragma unroll
-            for (int i = 0; i < kAhead; ++i)
-                if (s + i < steps) g[i] = raw(first_id(wave, s + i, lane));
+            for (int i = 0; i < kAhead; ++i) g[i] = fetch(first_id(wave, s + i, lane));
 #pragma unroll
-            for (int i = 0; i < kAhead; ++i)
-                if (s + i < steps) f(g[i], first_id(wave, s + i, lane));
+            for (int i = 0; i < kAhead; ++i) f(g[i], first_id(wave, s + i, lane));
+        }
+#pragma unroll 1
+        for (; s < steps; ++s) {
+            const int id0 = first_id(wave, s, lane);
+            if (first_id(wave, s, 0) >= vocab) break;
+            f(raw(id0), id0);
         }
     }
     // f(granule, first id), one granule at a time, the next one in flight; lanes
@@ -247,12 +284,13 @@ struct Row {
     template <class F>
     __device__ __forceinline__ void granules_of(int wave, int lane, F f) const {
         int id0 = first_id(wave, 0, lane);
-        Raw next = raw(id0);
-        for (int s = 1; s <= steps; ++s) {
-            if (first_id(wave, s - 1, 0) >= vocab) break;
-            const Raw now = next;
-            const int id1 = first_id(wave, s, lane);
-            if (s < steps) next = raw(id1);
+        Raw next = fetch(id0);
+        for (int s = 0; s < steps; ++s) {
+            if (first_id(wave, s, 0) >= vocab) break;
+            Raw now = next;
+            const int id1 = first_id(wave, s + 1, lane);
+            if (s + 1 < steps) next = fetch(id1);
+            if (ends_in(wave, s)) settle(now, id0);
             f(now, id0);
             id0 = id1;
         }
@@ -274,13 +312,13 @@ struct Row {
 // a few per cent of the ids are kept, the work on them then costs a wave per 64
 // of them and not nearly a wave per 64 ids of the row (129,280 ids, 2 % kept:
 // 30 us against 9 for the sum of their weights).
-template <sv_dtype DT, class Keep, class Use>
-__device__ __forceinline__ void compact(const Row<DT>& row, Smem& sm, Keep keep, Use use) {
+template <sv_dtype DT, int NT, class Keep, class Use>
+__device__ __forceinline__ void compact(const Row<DT, NT>& row, Smem<NT>& sm, Keep keep, Use use) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     float* qz = sm.queue_z[wave];
     int* qi = sm.queue_id[wave];
     int n = 0;  // the same in every lane
-    row.granules_of(wave, lane, [&](const typename Row<DT>::Raw& g, int id0) {
+    row.granules_of(wave, lane, [&](const typename Row<DT, NT>::Raw& g, int id0) {
         float z[8];
         g.unpack(z);
         int c = 0;
@@ -357,7 +395,8 @@ struct Extremes<SV_F32> {
 
 // ------------------------------------------------------- workgroup reductions
 
-__device__ __forceinline__ uint32_t block_max(uint32_t v, Smem& sm) {
+template <int NT>
+__device__ __forceinline__ uint32_t block_max(uint32_t v, Smem<NT>& sm) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) v = max(v, (uint32_t)__shfl_xor((int)v, o));
@@ -366,11 +405,12 @@ __device__ __forceinline__ uint32_t block_max(uint32_t v, Smem& sm) {
     __syncthreads();
     uint32_t r = sm.red[0];
 #pragma unroll
-    for (int w = 1; w < kWaves; ++w) r = max(r, sm.red[w]);
+    for (int w = 1; w < NT / kWave; ++w) r = max(r, sm.red[w]);
     return r;
 }
 
-__device__ __forceinline__ int block_sum(int v, Smem& sm) {
+template <int NT>
+__device__ __forceinline__ int block_sum(int v, Smem<NT>& sm) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     v = wave_sum(v);
     __syncthreads();
@@ -378,12 +418,13 @@ __device__ __forceinline__ int block_sum(int v, Smem& sm) {
     __syncthreads();
     int r = 0;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) r += sm.redi[w];
+    for (int w = 0; w < NT / kWave; ++w) r += sm.redi[w];
     return r;
 }
 
 // Sums in a fixed order; also leaves each wave's own sum in sm.redd.
-__device__ __forceinline__ double block_sum(double v, Smem& sm) {
+template <int NT>
+__device__ __forceinline__ double block_sum(double v, Smem<NT>& sm) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     v = wave_sum(v);
     __syncthreads();
@@ -391,7 +432,7 @@ __device__ __forceinline__ double block_sum(double v, Smem& sm) {
     __syncthreads();
     double r = 0.0;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) r += sm.redd[w];
+    for (int w = 0; w < NT / kWave; ++w) r += sm.redd[w];
     return r;
 }
 
@@ -400,8 +441,8 @@ __device__ __forceinline__ double block_sum(double v, Smem& sm) {
 // Finds the first bin, in ascending order, whose running total reaches the
 // target (count: >= want; mass: >= goal, or > goal if strict).  If none does,
 // found = 0 and the bin is the last one that holds any mass.
-template <bool MASS>
-__device__ __forceinline__ void scan_bins(Smem& sm, uint32_t want, double goal, bool strict,
+template <bool MASS, int NT>
+__device__ __forceinline__ void scan_bins(Smem<NT>& sm, uint32_t want, double goal, bool strict,
                                           Mass before, uint32_t before_cnt) {
     __syncthreads();
     if (threadIdx.x < kWave) {
@@ -486,8 +527,8 @@ struct Found {
 
 // The border among the ordinals of what takes part: each(f) calls f(ord) or,
 // with masses, f(ord, w) for every part-taker of the calling thread.
-template <bool MASS, class Each>
-__device__ Found descend(Smem& sm, Each each, int top, int low, uint32_t want, double goal,
+template <bool MASS, int NT, class Each>
+__device__ Found descend(Smem<NT>& sm, Each each, int top, int low, uint32_t want, double goal,
                          bool strict) {
     Found r{0, 0, 0, {0, 0}, true};
     for (int sh = top; sh >= low; sh -= 8) {
@@ -509,7 +550,7 @@ __device__ Found descend(Smem& sm, Each each, int top, int low, uint32_t want, d
             }
         });
         // once a level found no border, the search goes for the last mass
-        scan_bins<MASS>(sm, want, r.found ? goal : (double)kInf, strict, r.before, r.before_cnt);
+        scan_bins<MASS, NT>(sm, want, r.found ? goal : (double)kInf, strict, r.before, r.before_cnt);
         r.ord |= sm.digit << sh;
         r.before_cnt = sm.before_cnt;
         r.in_cnt = sm.in_cnt;
@@ -534,10 +575,10 @@ struct Result {
 };
 
 // Calls f(logit, id) for the candidates of the calling thread.
-template <sv_dtype DT, class F>
-__device__ __forceinline__ void candidates(const Row<DT>& row, const Smem& sm, bool listed, F f) {
+template <sv_dtype DT, int NT, class F>
+__device__ __forceinline__ void candidates(const Row<DT, NT>& row, const Smem<NT>& sm, bool listed, F f) {
     if (listed) {
-        for (int i = threadIdx.x; i < sm.list_n; i += kThreads)
+        for (int i = threadIdx.x; i < sm.list_n; i += NT)
             f(key_logit(entry_key(sm.list[i])), entry_id(sm.list[i]));
     } else {
         row.each(f);
@@ -559,7 +600,8 @@ __device__ __forceinline__ uint32_t ordinal_key(uint32_t ord) {
 
 // Ranks sm.list (n <= kRank entries) into sm.sorted, with weights and running
 // sums in that order.  The list's own order, which atomics made, does not show.
-__device__ __forceinline__ void rank_list(const Weigher& w, Smem& sm, int n) {
+template <int NT>
+__device__ __forceinline__ void rank_list(const Weigher& w, Smem<NT>& sm, int n) {
     const int i = threadIdx.x, lane = i & 63, wave = i >> 6;
     if (i < n) {
         const unsigned long long mine = sm.list[i];
@@ -586,9 +628,9 @@ __device__ __forceinline__ void rank_list(const Weigher& w, Smem& sm, int n) {
     __syncthreads();
 }
 
-// The smallest i < n for which test(i) holds, else n (n <= kThreads).
-template <class Test>
-__device__ __forceinline__ int first_of(Smem& sm, int n, Test test) {
+// The smallest i < n for which test(i) holds, else n (n <= NT).
+template <int NT, class Test>
+__device__ __forceinline__ int first_of(Smem<NT>& sm, int n, Test test) {
     const int i = threadIdx.x;
     const unsigned long long hits = __ballot(i < n && test(i));
     __syncthreads();
@@ -596,18 +638,18 @@ __device__ __forceinline__ int first_of(Smem& sm, int n, Test test) {
     __syncthreads();
     int r = n;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) r = min(r, sm.redi[w]);
+    for (int w = 0; w < NT / kWave; ++w) r = min(r, sm.redi[w]);
     return r;
 }
 
 // Sums 64-bit weights of the listed ids that live(z, id) leaves, and counts
 // them, whatever the list's order.
-template <class Live>
-__device__ __forceinline__ double sum_list(Smem& sm, const Weigher& w, int& n, Live live) {
+template <int NT, class Live>
+__device__ __forceinline__ double sum_list(Smem<NT>& sm, const Weigher& w, int& n, Live live) {
     __syncthreads();
     if (threadIdx.x == 0) sm.hi[0] = sm.lo[0] = 0, sm.second = 0;
     __syncthreads();
-    for (int i = threadIdx.x; i < sm.list_n; i += kThreads) {
+    for (int i = threadIdx.x; i < sm.list_n; i += NT) {
         const float z = key_logit(entry_key(sm.list[i]));
         const double x = w.raw(z);
         if (!live(z, entry_id(sm.list[i]), x)) continue;
@@ -623,8 +665,8 @@ __device__ __forceinline__ double sum_list(Smem& sm, const Weigher& w, int& n, L
 
 // Moves the border of w behind the first `want` of the ids (candidates that w
 // has now) whose logit has this key, of which in_cnt take part.
-template <sv_dtype DT>
-__device__ __forceinline__ void cut_ties(const Row<DT>& row, Smem& sm, bool listed, Weigher& w,
+template <sv_dtype DT, int NT>
+__device__ __forceinline__ void cut_ties(const Row<DT, NT>& row, Smem<NT>& sm, bool listed, Weigher& w,
                                          uint32_t key, uint32_t want, uint32_t in_cnt) {
     const float zk = key_logit(key);
     int cid = INT32_MAX;
@@ -646,8 +688,8 @@ __device__ __forceinline__ void cut_ties(const Row<DT>& row, Smem& sm, bool list
 
 // The border of top-p among the candidates: where their running weight reaches
 // goal.  False if it does not.
-template <sv_dtype DT, class In>
-__device__ __forceinline__ bool cut_mass(const Row<DT>& row, Smem& sm, bool listed, Weigher& w,
+template <sv_dtype DT, int NT, class In>
+__device__ __forceinline__ bool cut_mass(const Row<DT, NT>& row, Smem<NT>& sm, bool listed, Weigher& w,
                                          double goal, In in) {
     const Found f = descend<true>(
         sm,
@@ -669,9 +711,9 @@ __device__ __forceinline__ bool cut_mass(const Row<DT>& row, Smem& sm, bool list
 // The law by digits: any settings, any row.  lb: no id below it matters;
 // listed: the ids from lb up are in sm.list.  Not inlined: few rows need it,
 // and the others' code stays small.
-template <sv_dtype DT>
-__device__ __attribute__((noinline)) void find_by_digits(const Row<DT>& row, const Settings& set,
-                                                         Smem& sm, float lb, bool listed,
+template <sv_dtype DT, int NT>
+__device__ __attribute__((noinline)) void find_by_digits(const Row<DT, NT>& row, const Settings& set,
+                                                         Smem<NT>& sm, float lb, bool listed,
                                                          Result& r) {
     Weigher w = r.w;
     const bool use_p = set.p < 1.0f;
@@ -713,8 +755,8 @@ __device__ __attribute__((noinline)) void find_by_digits(const Row<DT>& row, con
 
 // Top-p alone.  Returns false, with nothing decided, where the ids next to the
 // border do not fit the list.
-template <sv_dtype DT>
-__device__ __forceinline__ bool find_nucleus(const Row<DT>& row, const Settings& set, Smem& sm,
+template <sv_dtype DT, int NT>
+__device__ __forceinline__ bool find_nucleus(const Row<DT, NT>& row, const Settings& set, Smem<NT>& sm,
                                              Result& r) {
     Weigher w = r.w;
     const float m = (float)w.m, per_logit = fminf(kPerOctave * (float)w.it, 1e30f);
@@ -722,7 +764,7 @@ __device__ __forceinline__ bool find_nucleus(const Row<DT>& row, const Settings&
     const auto step_of = [&](float z) {
         return (int)fminf((m - z) * per_logit, (float)(kSteps - 1));
     };
-    for (int i = threadIdx.x; i < kSteps; i += kThreads) sm.step[i] = 0;
+    for (int i = threadIdx.x; i < kSteps; i += NT) sm.step[i] = 0;
     __syncthreads();
     // The histogram only says where to look.  An id adds its weight over the
     // step's largest (between 1 and 2^(-1/32), linear within 3e-5) in units of
@@ -741,26 +783,34 @@ __device__ __forceinline__ bool find_nucleus(const Row<DT>& row, const Settings&
     // from that side, a histogram off by 2^-11 of what it holds is off by
     // little where top-p leaves little out.
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const double unit = pow2(-2.0 / (double)kPerOctave * (double)threadIdx.x) * 0x1p-10;
-    const double a = (double)sm.step[2 * threadIdx.x] * unit;
-    const double b = (double)sm.step[2 * threadIdx.x + 1] * unit * 0.97857206208770014;
-    const double incl = wave_incl_sum_dpp(a + b, lane);
+    constexpr int kEach = kSteps / NT;  // steps a thread adds up
+    double mass[kEach], own = 0.0;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        const int s = kEach * threadIdx.x + i;
+        mass[i] = (double)sm.step[s] * (pow2((double)-s / (double)kPerOctave) * 0x1p-10);
+        own += mass[i];
+    }
+    const double incl = wave_incl_sum_dpp(own, lane);
     __syncthreads();
     if (lane == 63) sm.redd[wave] = incl;
     if (threadIdx.x == 0) sm.first = sm.second = kSteps - 1, sm.list_n = 0;
     __syncthreads();
-    double before = incl - (a + b), all = 0.0;
-    for (int v = 0; v < kWaves; ++v) {
+    double before = incl - own, all = 0.0;
+    for (int v = 0; v < NT / kWave; ++v) {
         if (v < wave) before += sm.redd[v];
         all += sm.redd[v];
     }
     const double left = total - goal, off = 6e-4 * left + 1e-12 * total;
-    // the weight behind what is ahead of the two steps, and behind each
-    const double tb = all - before, t0 = all - (before + a), t1 = all - (before + a + b);
-    if (t1 - off <= left && !(tb - off <= left && threadIdx.x > 0))
-        sm.first = 2 * (int)threadIdx.x + (t0 - off <= left ? 0 : 1);
-    if (t1 + off <= left && !(tb + off <= left && threadIdx.x > 0))
-        sm.second = 2 * (int)threadIdx.x + (t0 + off <= left ? 0 : 1);
+    double behind = all - before;  // the weight from a step on
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        const int s = kEach * threadIdx.x + i;
+        const double next = behind - mass[i];
+        if (next - off <= left && (s == 0 || behind - off > left)) sm.first = s;
+        if (next + off <= left && (s == 0 || behind + off > left)) sm.second = s;
+        behind = next;
+    }
     __syncthreads();
     const int b1 = sm.first, b2 = sm.second;
     // logits of step b2 or less: at least this one, or a little below
@@ -784,7 +834,7 @@ __device__ __forceinline__ bool find_nucleus(const Row<DT>& row, const Settings&
     if (listed > kList || listed == 0 || above >= goal) return false;
     // the waves' sums, kept over the search
     double mine = 0.0;
-    if (threadIdx.x < kWaves) mine = sm.redd[threadIdx.x];
+    if (threadIdx.x < NT / kWave) mine = sm.redd[threadIdx.x];
     __syncthreads();
     if (listed <= kRank) {
         rank_list(w, sm, listed);
@@ -802,10 +852,10 @@ __device__ __forceinline__ bool find_nucleus(const Row<DT>& row, const Settings&
     if (w.raw(w.zc) < w.s) return true;  // min-p cuts further: summed by the caller
     // the listed ids that stay, added to their waves' sums
     __syncthreads();
-    if (threadIdx.x < kWaves) sm.hi[threadIdx.x] = sm.lo[threadIdx.x] = 0;
+    if (threadIdx.x < NT / kWave) sm.hi[threadIdx.x] = sm.lo[threadIdx.x] = 0;
     if (threadIdx.x == 0) sm.second = 0;
     __syncthreads();
-    for (int i = threadIdx.x; i < listed; i += kThreads) {
+    for (int i = threadIdx.x; i < listed; i += NT) {
         const float z = key_logit(entry_key(sm.list[i]));
         const int id = entry_id(sm.list[i]);
         if (!w.above(z, id)) continue;
@@ -816,26 +866,27 @@ __device__ __forceinline__ bool find_nucleus(const Row<DT>& row, const Settings&
         atomicAdd(&sm.second, 1);
     }
     __syncthreads();
-    if (threadIdx.x < kWaves)
+    if (threadIdx.x < NT / kWave)
         sm.redd[threadIdx.x] = mine + Mass{sm.hi[threadIdx.x], sm.lo[threadIdx.x]}.value();
     __syncthreads();
     r.n = n + sm.second;
     r.total = 0.0;
-    for (int v = 0; v < kWaves; ++v) r.total += sm.redd[v];
+    for (int v = 0; v < NT / kWave; ++v) r.total += sm.redd[v];
     return true;
 }
 
-template <sv_dtype DT>
-__device__ __forceinline__ Result find_law(const Row<DT>& row, const Settings& set, Smem& sm) {
-    using Raw = typename Row<DT>::Raw;
-    constexpr int kAhead = 16 / Row<DT>::kBytes;  // 128 bytes a lane in flight
+template <sv_dtype DT, int NT>
+__device__ __forceinline__ Result find_law(const Row<DT, NT>& row, const Settings& set, Smem<NT>& sm) {
+    using Raw = typename Row<DT, NT>::Raw;
+    // granules of a batch of loads: 128 bytes a lane in flight
+    constexpr int kAhead = 16 / Row<DT, NT>::kBytes;
     const int lane = threadIdx.x & 63;
     Result r{};
     // pass 1: largest logit, faults
     Extremes<DT> ex;
     row.template granules<kAhead>([&](const Raw& g, int) {
 #pragma unroll
-        for (int i = 0; i < 2 * Row<DT>::kBytes; ++i) ex.add(g.w[i]);
+        for (int i = 0; i < 2 * Row<DT, NT>::kBytes; ++i) ex.add(g.w[i]);
     });
     const uint32_t mine = ex.top();
     const uint32_t top = block_max(mine, sm);
@@ -848,7 +899,7 @@ __device__ __forceinline__ Result find_law(const Row<DT>& row, const Settings& s
     w.it = set.t == 0.0f ? 0.0 : kLog2e64 / (double)set.t;
     w.s = 0.0;
     w.zc = -kInf;
-    w.cid = INT32_MIN;  // ids of -inf (and those before the row, read as -inf) never count
+    w.cid = -1;  // no id of -inf counts
 
     // lb: no id below this logit is in the support (nor, with top-k, among
     // the first k)
@@ -856,7 +907,7 @@ __device__ __forceinline__ Result find_law(const Row<DT>& row, const Settings& s
     float lb = -kInf;
     if (set.t == 0.0f) {
         lb = key_logit(top);
-    } else if (set.k > 0 && set.k <= kThreads) {
+    } else if (set.k > 0 && set.k <= NT) {
         // about the k-th largest of the threads' maxima, and no larger: k ids
         // are at least that
         const uint32_t low =
@@ -879,7 +930,7 @@ __device__ __forceinline__ Result find_law(const Row<DT>& row, const Settings& s
     }
     bool decided = false;
     if (use_p && set.k == 0 && set.t > 0.0f) {
-        decided = find_nucleus<DT>(row, set, sm, r);
+        decided = find_nucleus<DT, NT>(row, set, sm, r);
         if (decided && r.n > 0) return r;
         lb = -kInf;
     }
@@ -888,22 +939,47 @@ __device__ __forceinline__ Result find_law(const Row<DT>& row, const Settings& s
     if (listed) {
         if (threadIdx.x == 0) sm.list_n = 0;
         __syncthreads();
-        // a thread whose own maximum is below the bound has none
-        if (mine >= order_key(lb)) row.template granules<kAhead>([&](const Raw& g, int id0) {
-            float z[8];
-            g.unpack(z);
-            float big = z[0];
+        // A thread whose own maximum is below the bound has none; the others
+        // look which of their granules do, and read those again.  (Code that is
+        // run once is paid for in instruction fetches: none of it unrolled.)
+        if (mine >= order_key(lb)) {
+            const int wave = threadIdx.x >> 6;
+            for (int s0 = 0; s0 < row.steps; s0 += kAhead) {
+                unsigned hits = 0;
+                Raw g[kAhead];
 #pragma unroll
-            for (int e = 1; e < 8; ++e) big = fmaxf(big, z[e]);
-            if (big < lb) return;
+                for (int i = 0; i < kAhead; ++i)
+                    g[i] = row.fetch(min(row.first_id(wave, s0 + i, lane), row.vocab));
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                if (z[e] >= lb) {
-                    const int at = atomicAdd(&sm.list_n, 1);
-                    if (at < kList) sm.list[at] = entry(order_key(z[e]), id0 + e);
+                for (int i = 0; i < kAhead; ++i) {
+                    float z[8];
+                    g[i].unpack(z);
+                    float big = z[0];
+#pragma unroll
+                    for (int e = 1; e < 8; ++e) big = fmaxf(big, z[e]);
+                    // a granule past the row's end shows its last ids: looked
+                    // at again below
+                    if (big >= lb && s0 + i < row.steps) hits |= 1u << i;
+                }
+#pragma unroll 1
+                for (; hits != 0; hits &= hits - 1) {
+                    const int id0 = row.first_id(wave, s0 + __builtin_ctz(hits), lane);
+                    float z[8];
+                    row.raw(id0).unpack(z);
+                    int c = 0;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) c += z[e] >= lb ? 1 : 0;
+                    int at = atomicAdd(&sm.list_n, c);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        if (z[e] >= lb) {
+                            if (at < kList) sm.list[at] = entry(order_key(z[e]), id0 + e);
+                            ++at;
+                        }
+                    }
                 }
             }
-        });
+        }
         __syncthreads();
         listed = sm.list_n <= kList;
     }
@@ -941,7 +1017,7 @@ __device__ __forceinline__ Result find_law(const Row<DT>& row, const Settings& s
     }
     r.where = kInRow;
     if (!decided) {
-        if (use_p || set.k > 0 || listed) find_by_digits<DT>(row, set, sm, lb, listed, r);
+        if (use_p || set.k > 0 || listed) find_by_digits<DT, NT>(row, set, sm, lb, listed, r);
         if (r.where == kListed) return r;
     }
     r.w.s = (double)set.s;
@@ -972,13 +1048,13 @@ __device__ __forceinline__ Result find_law(const Row<DT>& row, const Settings& s
 // segment that holds the crossing, one wave walks the step that does.
 // weights(id0, x) gives the 8 weights at ids id0 .. id0 + 7.  If rounding leaves
 // no such id, the last one of positive weight.
-template <class Weights, class FirstId>
-__device__ int walk_row(Smem& sm, double goal, int steps, FirstId first_id, int vocab,
+template <int NT, class Weights, class FirstId>
+__device__ int walk_row(Smem<NT>& sm, double goal, int steps, FirstId first_id, int vocab,
                         Weights weights) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     double before = 0.0;
     int owner = -1;
-    for (int w = 0; w < kWaves; ++w) {
+    for (int w = 0; w < NT / kWave; ++w) {
         if (before + sm.redd[w] > goal) {
             owner = w;
             break;
@@ -988,7 +1064,7 @@ __device__ int walk_row(Smem& sm, double goal, int steps, FirstId first_id, int 
     if (owner < 0) {
         goal = kInf;
         before = 0.0;
-        for (int w = 0; w < kWaves; ++w)
+        for (int w = 0; w < NT / kWave; ++w)
             if (sm.redd[w] > 0.0) owner = w;
     }
     const auto read = [&](int s, double* x) {
@@ -1007,7 +1083,7 @@ __device__ int walk_row(Smem& sm, double goal, int steps, FirstId first_id, int 
     // all waves sum the segment's steps; a wave keeps its last one's weights
     double x[8], incl = 0.0;
     int held = -1;
-    for (int s = wave; s < steps; s += kWaves) {
+    for (int s = wave; s < steps; s += NT / kWave) {
         incl = wave_incl_sum_dpp(read(s, x), lane);
         held = s;
         if (lane == 63) sm.seg[s] = incl;
@@ -1028,7 +1104,7 @@ __device__ int walk_row(Smem& sm, double goal, int steps, FirstId first_id, int 
         step = positive;
         goal = kInf;
     }
-    if (wave == step % kWaves) {
+    if (wave == step % (NT / kWave)) {
         if (held != step) incl = wave_incl_sum_dpp(read(step, x), lane);
         const int id0 = first_id(owner, step, lane);
         double mine = 0.0;
@@ -1053,8 +1129,8 @@ __device__ int walk_row(Smem& sm, double goal, int steps, FirstId first_id, int 
 }
 
 // The id a uniform u in [0, 1) draws from a law find_law has just made.
-template <sv_dtype DT>
-__device__ int draw(const Row<DT>& row, const Result& r, float u, Smem& sm) {
+template <sv_dtype DT, int NT>
+__device__ int draw(const Row<DT, NT>& row, const Result& r, float u, Smem<NT>& sm) {
     const double goal = (double)u * r.total;
     if (r.where == kRanked) {
         if (r.n == 1) return entry_id(sm.sorted[0]);

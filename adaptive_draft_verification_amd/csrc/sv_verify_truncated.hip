@@ -3,7 +3,7 @@
 // sv_verify's (rejection sampling keeps the target's law), with p and q the
 // truncated laws.
 //
-// Launch 1, one 1024-thread workgroup per row slot: the law of each target row
+// Launch 1, one 512-thread workgroup per row slot: the law of each target row
 // 0 .. b and draft row 0 .. b - 1 of a request (LawRecord), and the weight it
 // gives the position's draft id.  Launch 2, one workgroup per request: wave 0
 // decides (lane j: position j), then the token at L is drawn over the one or
@@ -15,7 +15,8 @@
 namespace sv {
 namespace {
 
-using law::Row;
+template <sv_dtype DT>
+constexpr int kBytes = DT == SV_BF16 ? 2 : 4;
 
 struct Span {
     int lo, b;
@@ -31,28 +32,28 @@ __device__ __forceinline__ Span span(const VerifyTruncatedArgs& a, int r) {
 template <sv_dtype DT>
 __device__ __forceinline__ const char* target_row(const VerifyTruncatedArgs& a, int lo, int j) {
     return static_cast<const char*>(a.target) +
-           ((int64_t)lo + j) * a.target_ld * Row<DT>::kBytes;
+           ((int64_t)lo + j) * a.target_ld * kBytes<DT>;
 }
 template <sv_dtype DT>
 __device__ __forceinline__ const char* draft_row(const VerifyTruncatedArgs& a, int r, int j) {
     return static_cast<const char*>(a.draft) +
-           ((int64_t)r * a.k_max + j) * a.draft_ld * Row<DT>::kBytes;
+           ((int64_t)r * a.k_max + j) * a.draft_ld * kBytes<DT>;
 }
 
 // grid: position-major, so that the slots past a request's rows, which exit at
 // once, come last
-template <sv_dtype DT>
-__global__ __launch_bounds__(law::kThreads) void laws_kernel(VerifyTruncatedArgs a) {
-    __shared__ law::Smem sm;
+template <sv_dtype DT, int kLaws>
+__global__ __launch_bounds__(kLaws, kLaws == kWave ? 1 : 4) void laws_kernel(VerifyTruncatedArgs a) {
+    __shared__ law::Smem<kLaws> sm;
     const int r = blockIdx.x % a.n_req, slot = blockIdx.x / a.n_req;
     const bool is_draft = slot & 1;       // target 0, draft 0, target 1, ...
     const int j = slot >> 1;
     const Span s = span(a, r);
     if (!s.ok || j > s.b || (is_draft && j == s.b)) return;
-    const Row<DT> row(is_draft ? draft_row<DT>(a, r, j) : target_row<DT>(a, s.lo, j), a.vocab);
+    const law::Row<DT, kLaws> row(is_draft ? draft_row<DT>(a, r, j) : target_row<DT>(a, s.lo, j), a.vocab);
     const law::Settings set =
         law::settings(is_draft ? a.draft_law : a.target_law, r, a.vocab);
-    const law::Result res = law::find_law<DT>(row, set, sm);
+    const law::Result res = law::find_law(row, set, sm);
     if (threadIdx.x != 0) return;
     LawRecord rec{};
     rec.fault = res.fault;
@@ -80,12 +81,12 @@ __device__ law::Weigher weigher(const LawRecord& rec, const law::Settings& set) 
 struct DecideSmem {
     int L, fault;
     float v;
-    double redd[law::kWaves];
 };
 
-template <sv_dtype DT>
-__global__ __launch_bounds__(law::kThreads) void decide_kernel(VerifyTruncatedArgs a) {
-    __shared__ law::Smem sm;
+template <sv_dtype DT, int kDecide>
+__global__ __launch_bounds__(kDecide, kDecide == kWave ? 1 : 4) void decide_kernel(VerifyTruncatedArgs a) {
+    using Row = law::Row<DT, kDecide>;
+    __shared__ law::Smem<kDecide> sm;
     __shared__ DecideSmem ds;
     const int r = blockIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int k_max = a.k_max;
@@ -152,33 +153,22 @@ __global__ __launch_bounds__(law::kThreads) void decide_kernel(VerifyTruncatedAr
     const bool residual = L < s.b;
     const LawRecord pr = laws[L];
     const law::Weigher pw = weigher(pr, pset);
-    const Row<DT> prow(target_row<DT>(a, s.lo, L), a.vocab);
+    const Row prow(target_row<DT>(a, s.lo, L), a.vocab);
     const double ip = 1.0 / pr.total;
     law::Weigher qw = pw;
-    Row<DT> qrow = prow;
+    Row qrow = prow;
     double iq = 0.0;
     if (residual) {
         const LawRecord qr = laws[k_max + 1 + L];
         qw = weigher(qr, qset);
-        qrow = Row<DT>(draft_row<DT>(a, r, L), a.vocab);
+        qrow = Row(draft_row<DT>(a, r, L), a.vocab);
         iq = 1.0 / qr.total;
     }
-    const bool same = qrow.shift == prow.shift;
     bool minus = residual;
     const auto weights = [&](int id0, double* x) {
         float z[8], y[8];
         prow.load(id0, z);
-        if (minus) {
-            if (same) {
-                qrow.load(id0, y);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int id = id0 + e;
-                    y[e] = id >= 0 && id < a.vocab ? qrow.one(id) : -law::kInf;
-                }
-            }
-        }
+        if (minus) qrow.load(id0, y);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             x[e] = pw(z[e], id0 + e);
@@ -209,21 +199,24 @@ __global__ __launch_bounds__(law::kThreads) void decide_kernel(VerifyTruncatedAr
     if (threadIdx.x == 0) out[L] = tok;
 }
 
+template <sv_dtype DT>
+hipError_t run(const VerifyTruncatedArgs& a, hipStream_t stream) {
+    const unsigned slots = (unsigned)a.n_req * (2 * a.k_max + 1);
+    // two workgroups of 512 threads share a CU in the first launch, whose rows
+    // are many; rows of fewer than 8 ids take one wave
+    if (a.vocab < 8) laws_kernel<DT, kWave><<<slots, kWave, 0, stream>>>(a);
+    else laws_kernel<DT, 512><<<slots, 512, 0, stream>>>(a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    if (a.vocab < 8) decide_kernel<DT, kWave><<<a.n_req, kWave, 0, stream>>>(a);
+    else decide_kernel<DT, 1024><<<a.n_req, 1024, 0, stream>>>(a);
+    return hipGetLastError();
+}
+
 }  // namespace
 
 hipError_t launch_verify_truncated(const VerifyTruncatedArgs& a, hipStream_t stream) {
-    const unsigned slots = (unsigned)a.n_req * (2 * a.k_max + 1);
-    if (a.dtype == SV_BF16)
-        laws_kernel<SV_BF16><<<slots, law::kThreads, 0, stream>>>(a);
-    else
-        laws_kernel<SV_F32><<<slots, law::kThreads, 0, stream>>>(a);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    if (a.dtype == SV_BF16)
-        decide_kernel<SV_BF16><<<a.n_req, law::kThreads, 0, stream>>>(a);
-    else
-        decide_kernel<SV_F32><<<a.n_req, law::kThreads, 0, stream>>>(a);
-    return hipGetLastError();
+    return a.dtype == SV_BF16 ? run<SV_BF16>(a, stream) : run<SV_F32>(a, stream);
 }
 
 }  // namespace sv

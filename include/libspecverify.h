@@ -536,7 +536,8 @@ typedef struct {
  * A row with NaN, +inf or only -inf (SV_DEV_NONFINITE), bad settings or a
  * uniform outside [0, 1) (SV_DEV_BAD_PARAM) gives -1 in all of them.
  * Repeated calls agree bit for bit.
- * Launch: one kernel, one 1024-thread workgroup a row; no workspace.
+ * Launch: one kernel, one workgroup a row (1024 threads; 512 above 256 rows);
+ * no workspace.
  * Errors: SV_ERR_NULL; SV_ERR_DTYPE; SV_ERR_SHAPE.
  */
 sv_status sv_sample(const void* logits, int64_t ld, int32_t n_rows, sv_dtype dtype,
@@ -561,8 +562,8 @@ sv_status sv_sample(const void* logits, int64_t ld, int32_t n_rows, sv_dtype dty
  *          record for each of a request's 2 k_max + 1 row slots), 8-byte
  *          aligned, uninitialised.  Calls that overlap in time must not share
  *          it.
- * Launch: two kernels: one 1024-thread workgroup per row slot, then one per
- * request.
+ * Launch: two kernels: one 512-thread workgroup per row slot, then one of 1024
+ * threads per request.
  * Errors: SV_ERR_NULL; SV_ERR_DTYPE; SV_ERR_SHAPE; SV_ERR_WORKSPACE.
  */
 size_t sv_verify_truncated_workspace_bytes(int32_t n_req, int32_t k_max);
