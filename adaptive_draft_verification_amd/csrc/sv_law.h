@@ -753,6 +753,13 @@ __device__ __attribute__((noinline)) void find_by_digits(const Row<DT, NT>& row,
     r.where = listed ? kListed : kInRow;
 }
 
+// cut_mass over the list, not inlined (rarely needed).
+template <sv_dtype DT, int NT>
+__device__ __attribute__((noinline)) bool cut_listed(const Row<DT, NT>& row, Smem<NT>& sm,
+                                                     Weigher& w, double goal) {
+    return cut_mass(row, sm, true, w, goal, [](float) { return true; });
+}
+
 // Top-p alone.  Returns false, with nothing decided, where the ids next to the
 // border do not fit the list.
 template <sv_dtype DT, int NT>
@@ -842,8 +849,10 @@ __device__ __forceinline__ bool find_nucleus(const Row<DT, NT>& row, const Setti
         if (last == listed) return false;
         w.zc = key_logit(entry_key(sm.sorted[last]));
         w.cid = entry_id(sm.sorted[last]);
-    } else if (!cut_mass(row, sm, true, w, goal - above, [](float) { return true; })) {
-        return false;
+    } else {
+        Weigher cut = w;
+        if (!cut_listed(row, sm, cut, goal - above)) return false;
+        w = cut;
     }
     w.s = (double)set.s;
     r.w = w;
@@ -1128,6 +1137,22 @@ __device__ int walk_row(Smem<NT>& sm, double goal, int steps, FirstId first_id, 
     return sm.redi[0];
 }
 
+// A draw over the listed ids, digit by digit of the id; not inlined (rarely
+// needed).
+template <sv_dtype DT, int NT>
+__device__ __attribute__((noinline)) int draw_listed(const Row<DT, NT>& row, Smem<NT>& sm,
+                                                     const Weigher w, float u, double goal) {
+    const auto live = [&](auto fn) {
+        candidates(row, sm, true, [&](float z, int id) {
+            const double x = w(z, id);
+            if (x > 0.0) fn((uint32_t)id, [&] { return x; });
+        });
+    };
+    // u = 0: the lowest id of any weight, however small
+    if (u == 0.0f) return (int)descend<false>(sm, live, 16, 0, 1, 0.0, false).ord;
+    return (int)descend<true>(sm, live, 16, 0, 0, goal, true).ord;
+}
+
 // The id a uniform u in [0, 1) draws from a law find_law has just made.
 template <sv_dtype DT, int NT>
 __device__ int draw(const Row<DT, NT>& row, const Result& r, float u, Smem<NT>& sm) {
@@ -1161,15 +1186,7 @@ __device__ int draw(const Row<DT, NT>& row, const Result& r, float u, Smem<NT>& 
                 for (int e = 0; e < 8; ++e) x[e] = r.w(z[e], id0 + e);
             });
     }
-    const auto live = [&](auto fn) {
-        candidates(row, sm, true, [&](float z, int id) {
-            const double x = r.w(z, id);
-            if (x > 0.0) fn((uint32_t)id, [&] { return x; });
-        });
-    };
-    // u = 0: the lowest id of any weight, however small
-    if (u == 0.0f) return (int)descend<false>(sm, live, 16, 0, 1, 0.0, false).ord;
-    return (int)descend<true>(sm, live, 16, 0, 0, goal, true).ord;
+    return draw_listed(row, sm, r.w, u, goal);
 }
 
 }  // namespace law
