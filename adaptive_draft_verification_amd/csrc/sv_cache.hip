@@ -165,21 +165,29 @@ struct Attend {
     static constexpr int kVWords = F8 ? kDpl / 4 : kDpl / 2;
     static constexpr int kAcc = D / 4;      // accumulators a slot tile and lane
     static constexpr int kEsize = F8 ? 1 : 2;
+    // waves a SIMD has registers for; two sets of value registers where they fit
+    static constexpr int kOccupancy = D < 256 && MT * D <= 256 ? 2 : 1;
+    static constexpr bool kTwoV = D < 256 && MT < 4;
 
-    // Partial result of a slot tile in one lane: running maximum (in units of
-    // log2), sum and unnormalised output of slot lane % 16.
-    struct Smem {
-        float acc[2][MT][kAcc / 4][kWave][4];
-        float m[2][MT][kWave], l[2][MT][kWave];
+    union Smem {
+        uint4 q[MT][kSteps][kWave];  // the queries as operand B, lane by lane
+        // Partial results of slot tiles, lane by lane: running maximum (in
+        // units of log2), sum and unnormalised output of slot lane % 16.
+        struct {
+            float acc[2][MT][kAcc / 4][kWave][4];
+            float m[2][MT][kWave], l[2][MT][kWave];
+        } part;
     };
 };
 
 template <int D, bool F8, int MT, bool PG16>
-__global__ __launch_bounds__(256) void attend_kernel(AttendArgs a) {
+__global__ __launch_bounds__(256, (Attend<D, F8, MT, PG16>::kOccupancy))
+void attend_kernel(AttendArgs a) {
     using C = Attend<D, F8, MT, PG16>;
     __shared__ typename C::Smem sm;
     const sv_cache& c = a.cache;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int col = lane & 15, g = lane >> 4;
     // grid: kv heads fastest, then requests, slot blocks and parts
     int id = blockIdx.x;
@@ -208,40 +216,6 @@ __global__ __launch_bounds__(256) void attend_kernel(AttendArgs a) {
     const int begin = part * plen, end = min(len, begin + plen);
     if (begin >= len) return;
 
-    // queries of this lane's slot, as operand B
-    bf16x8 q[MT][C::kSteps];
-    int last[MT];  // the last position the slot sees
-    const uint16_t* qp = static_cast<const uint16_t*>(a.q);
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-        const int i = mt * 16 + col, slot = mb * 16 * MT + i;
-        const bool live = i < slots;
-        const int row = slot / G, head = h * G + slot % G;
-        last[mt] = live ? ctx + row : -1;
-#pragma unroll
-        for (int s = 0; s < C::kSteps; ++s) {
-            const int d = F8 ? (s / 2) * 64 + g * 16 + (s & 1) * 8 : s * 32 + g * 8;
-            uint4 w = make_uint4(0, 0, 0, 0);
-            if (live)
-                w = *reinterpret_cast<const uint4*>(qp + (int64_t)(lo + row) * a.q_ld +
-                                                    (int64_t)head * D + d);
-            q[mt][s] = as_bf16x8(w.x, w.y, w.z, w.w);
-        }
-    }
-    const float scale =
-        a.scale * kLog2e * (F8 && c.k_scale != nullptr ? c.k_scale[h] : 1.0f);
-
-    f32x4 acc[MT][C::kDpl];
-    float m[MT], mu[MT], l[MT];  // running max (-inf: none yet), the max used, sum
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-        for (int i = 0; i < C::kDpl; ++i) acc[mt][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        m[mt] = -kInf;
-        mu[mt] = 0.0f;
-        l[mt] = 0.0f;
-    }
-
     const char* kbase = static_cast<const char*>(c.k) + (int64_t)h * c.head_stride * C::kEsize;
     const char* vbase = static_cast<const char*>(c.v) + (int64_t)h * c.head_stride * C::kEsize;
     const int32_t* table = a.page_table + (int64_t)r * a.max_pages;
@@ -255,136 +229,215 @@ __global__ __launch_bounds__(256) void attend_kernel(AttendArgs a) {
         return ((int64_t)page * c.page_stride + (int64_t)(t % c.page_size) * c.token_stride) *
                C::kEsize;
     };
-
-    // The byte offsets of a tile's rows: pages of a multiple of 16 positions
-    // hold each half of a tile (16 positions) in one page.
-    struct Rows {
-        int64_t half[2];
-        bool ok[2];
+    // Pages of a multiple of 16 positions hold each half of a tile (16
+    // positions) in one page: two ids a tile, the same in every lane, fetched
+    // a tile ahead of the loads that need them.
+    const int last16 = (len - 1) & ~15;
+    auto page_index = [&](int t) {
+        return a.page_shift >= 0 ? t >> a.page_shift : (int)((unsigned)t / (unsigned)c.page_size);
     };
-    auto find = [&](int t0) {
-        Rows p;
+    struct Ids {
+        int page[2];
+    };
+    auto look_up = [&](int t0) {
+        Ids p;
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            const int t = min(t0 + 16 * s, (len - 1) & ~15);
-            int page = table[t / c.page_size];
-            p.ok[s] = page >= 0 && page < c.n_pages;
-            page = p.ok[s] ? page : 0;
-            p.half[s] = ((int64_t)page * c.page_stride +
-                         (int64_t)(t % c.page_size) * c.token_stride) * C::kEsize;
-        }
+        for (int u = 0; u < 2; ++u)
+            p.page[u] = table[page_index(min(t0 + 16 * u, last16))];
         return p;
     };
 
     Words<4> kr[2][C::kKLoads];
-    Words<C::kVWords> vr[8];
-    uint32_t vok = 0;  // bit j: the page of the lane's j-th position is good
     const int64_t tstride = c.token_stride * C::kEsize;
-    auto load_k = [&](int t0, const Rows& p) {
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            const char* at;
-            if (PG16) {
-                at = kbase + p.half[s] + col * tstride;
-            } else {
-                bool ok;
-                at = kbase + row_offset(t0 + 16 * s + col, ok);
-            }
-#pragma unroll
-            for (int i = 0; i < C::kKLoads; ++i) kr[s][i] = load_words<4>(at + (i * 64 + g * 16));
-        }
+    const uint32_t koff = (uint32_t)(col * tstride) + g * 16;
+    const uint32_t voff = (uint32_t)(g * 4 * tstride) + col * C::kDpl * C::kEsize;
+    struct Values {
+        Words<C::kVWords> r[8];
+        uint32_t ok;  // bit j: the page of the lane's j-th position is good
     };
-    auto load_v = [&](int t0, const Rows& p) {
-        vok = 0;
+    // Issues a tile's loads: keys first, then values.
+    auto load = [&](int t0, Ids ids, Values* v, bool keys) __attribute__((always_inline)) {
+        if (PG16) {
+            const char* at[2];
+            uint32_t ok = 0;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int s = j >> 2, o = g * 4 + (j & 3);
-            const char* at;
-            bool ok;
-            if (PG16) {
-                at = vbase + p.half[s] + o * tstride;
-                ok = p.ok[s];
-            } else {
-                at = vbase + row_offset(t0 + 16 * s + o, ok);
+            for (int u = 0; u < 2; ++u) {
+                const int t = min(t0 + 16 * u, last16);
+                int page = __builtin_amdgcn_readfirstlane(ids.page[u]);
+                const bool good = page >= 0 && page < c.n_pages;
+                ok |= good ? 0xfu << (4 * u) : 0u;
+                page = good ? page : 0;
+                const int slot = t - page_index(t) * c.page_size;
+                const int64_t off =
+                    ((int64_t)page * c.page_stride + (int64_t)slot * c.token_stride) * C::kEsize;
+                at[u] = (keys ? kbase : vbase) + off;
             }
-            vok |= ok ? 1u << j : 0u;
-            vr[j] = load_words<C::kVWords>(at + col * C::kDpl * C::kEsize);
+            if (keys) {
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int i = 0; i < C::kKLoads; ++i)
+                        kr[u][i] = load_words<4>(at[u] + (koff + i * 64));
+            } else {
+                v->ok = ok;
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    v->r[j] = load_words<C::kVWords>(at[j >> 2] +
+                                                     (voff + (uint32_t)((j & 3) * tstride)));
+            }
+        } else if (keys) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                bool ok;
+                const char* at = kbase + row_offset(t0 + 16 * u + col, ok);
+#pragma unroll
+                for (int i = 0; i < C::kKLoads; ++i)
+                    kr[u][i] = load_words<4>(at + (i * 64 + g * 16));
+            }
+        } else {
+            v->ok = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                bool ok;
+                const char* at = vbase + row_offset(t0 + 16 * (j >> 2) + g * 4 + (j & 3), ok);
+                v->ok |= ok ? 1u << j : 0u;
+                v->r[j] = load_words<C::kVWords>(at + col * C::kDpl * C::kEsize);
+            }
         }
     };
 
+    // the first tile's loads go out before anything else is done
     const int stride = C::kWaves * C::kTile;
     int t0 = begin + wave * C::kTile;
+    Values va, vb;
+    Ids ids{};
+    if (t0 < end) {
+        if (PG16) ids = look_up(t0);
+        load(t0, ids, nullptr, true);
+        load(t0, ids, &va, false);
+        if (PG16) ids = look_up(min(t0 + stride, len - 1));
+    }
+
+    // queries of the block's slots: wave w brings steps w, w + 4, ...
+    const uint16_t* qp = static_cast<const uint16_t*>(a.q);
+    int last[MT];  // the last position the lane's slot sees
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+        const int i = mt * 16 + col, slot = mb * 16 * MT + i;
+        const bool live = i < slots;
+        const int row = slot / G, head = h * G + slot % G;
+        last[mt] = live ? ctx + row : -1;
+        for (int st = wave; st < C::kSteps; st += C::kWaves) {
+            const int d = F8 ? (st / 2) * 64 + g * 16 + (st & 1) * 8 : st * 32 + g * 8;
+            uint4 w = make_uint4(0, 0, 0, 0);
+            if (live)
+                w = *reinterpret_cast<const uint4*>(qp + (int64_t)(lo + row) * a.q_ld +
+                                                    (int64_t)head * D + d);
+            sm.q[mt][st][lane] = w;
+        }
+    }
+    __syncthreads();
+    const float scale =
+        a.scale * kLog2e * (F8 && c.k_scale != nullptr ? c.k_scale[h] : 1.0f);
+
+    f32x4 acc[MT][C::kDpl];
+    float m[MT], mu[MT], l[MT];  // running max (-inf: none yet), the max used, sum
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+        for (int i = 0; i < C::kDpl; ++i) acc[mt][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        m[mt] = -kInf;
+        mu[mt] = 0.0f;
+        l[mt] = 0.0f;
+    }
     int bad = 0;
-    for (; t0 < end; t0 += stride) {
-        Rows rows_at{};
-        if (PG16) rows_at = find(t0);
-        load_k(t0, rows_at);
-        load_v(t0, rows_at);
-        // the values' rows of the 8 positions, as bf16 pairs of dims
-        uint32_t vw[8][C::kDpl / 2];
+
+    auto tile = [&](Values& now, Values& next) __attribute__((always_inline)) {
+        f32x4 s[MT][2];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-            for (int i = 0; i < C::kVWords; ++i) {
+            for (int u = 0; u < 2; ++u) s[mt][u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int st = 0; st < C::kSteps; ++st) {
+            bf16x8 k8[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
                 if (F8) {
-                    vw[j][2 * i] = e4m3_pair<false>(vr[j].w[i]);
-                    vw[j][2 * i + 1] = e4m3_pair<true>(vr[j].w[i]);
+                    const uint32_t w0 = kr[u][st / 2].w[(st & 1) * 2];
+                    const uint32_t w1 = kr[u][st / 2].w[(st & 1) * 2 + 1];
+                    k8[u] = as_bf16x8(e4m3_pair<false>(w0), e4m3_pair<true>(w0),
+                                      e4m3_pair<false>(w1), e4m3_pair<true>(w1));
                 } else {
-                    vw[j][i] = vr[j].w[i];
+                    const Words<4>& w = kr[u][F8 ? 0 : st];
+                    k8[u] = as_bf16x8(w.w[0], w.w[1], w.w[2], w.w[3]);
                 }
             }
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                const uint4 w = sm.q[mt][st][lane];
+                const bf16x8 q8 = as_bf16x8(w.x, w.y, w.z, w.w);
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+                    s[mt][u] =
+                        __builtin_amdgcn_mfma_f32_16x16x32_bf16(k8[u], q8, s[mt][u], 0, 0, 0);
+            }
         }
-        if (vok != 0xffu) bad = 1;
-        // positions past the context are not seen by every row; positions
-        // past the end, or on a bad page, by none: their values are zeroed,
-        // since 0 times what lies there may be NaN
-        const bool edge = t0 + C::kTile > ctx || __ballot(vok != 0xffu) != 0;
+        // the next tile's loads, in flight over the softmax and the product
+        // with the values (the scores are taken first: the keys' registers)
+        const int t1 = t0 + stride;
+        const bool more = t1 < end;
+        const Ids ids1 = ids;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) asm volatile("" : "+v"(s[mt][u]));
+        if (more) {
+            load(t1, ids1, nullptr, true);
+            if (C::kTwoV) load(t1, ids1, &next, false);
+            if (PG16) ids = look_up(min(t1 + stride, len - 1));
+        }
+        __builtin_amdgcn_sched_barrier(0);
+
+        // Positions past the context are not seen by every row; positions past
+        // the end, or on a bad page, by none: their values are zeroed, since 0
+        // times what lies there may be NaN.  A value that is not finite behind
+        // the context poisons the product for the rows that do not see it.
+        if (now.ok != 0xffu) bad = 1;
+        const bool edge = t0 + C::kTile > ctx || __ballot(now.ok != 0xffu) != 0;
         bool poison = false;
         if (edge) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const int t = t0 + 16 * (j >> 2) + g * 4 + (j & 3);
-                const bool in = t < len && ((vok >> j) & 1);
+                const bool in = t < len && ((now.ok >> j) & 1);
                 bool nf = false;
 #pragma unroll
-                for (int i = 0; i < C::kDpl / 2; ++i) {
-                    if (!in) vw[j][i] = 0;
-                    nf |= bf16_pair_nonfinite(vw[j][i]);
+                for (int i = 0; i < C::kVWords; ++i) {
+                    if (!in) now.r[j].w[i] = 0;
+                    if (F8) {
+                        nf |= bf16_pair_nonfinite(e4m3_pair<false>(now.r[j].w[i])) ||
+                              bf16_pair_nonfinite(e4m3_pair<true>(now.r[j].w[i]));
+                    } else {
+                        nf |= bf16_pair_nonfinite(now.r[j].w[i]);
+                    }
                 }
                 poison |= nf && t > ctx;
             }
             poison = __ballot(poison) != 0;
         }
+        bf16x8 pb[MT];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
             if (mt * 16 >= slots) break;
-            f32x4 s[2];
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                s[u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                for (int st = 0; st < C::kSteps; ++st) {
-                    bf16x8 k8;
-                    if (F8) {
-                        const uint32_t w0 = kr[u][st / 2].w[(st & 1) * 2];
-                        const uint32_t w1 = kr[u][st / 2].w[(st & 1) * 2 + 1];
-                        k8 = as_bf16x8(e4m3_pair<false>(w0), e4m3_pair<true>(w0),
-                                       e4m3_pair<false>(w1), e4m3_pair<true>(w1));
-                    } else {
-                        const Words<4>& w = kr[u][st];
-                        k8 = as_bf16x8(w.w[0], w.w[1], w.w[2], w.w[3]);
-                    }
-                    s[u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k8, q[mt][st], s[u], 0, 0, 0);
-                }
-            }
             float p[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) p[j] = s[j >> 2][j & 3] * scale;
+            for (int j = 0; j < 8; ++j) p[j] = s[mt][j >> 2][j & 3] * scale;
             if (edge) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     const int t = t0 + 16 * (j >> 2) + g * 4 + (j & 3);
-                    if (t > last[mt] || !((vok >> j) & 1)) p[j] = -kInf;
+                    if (t > last[mt] || !((now.ok >> j) & 1)) p[j] = -kInf;
                 }
             }
             float mx = p[0];
@@ -409,9 +462,12 @@ __global__ __launch_bounds__(256) void attend_kernel(AttendArgs a) {
                 p[j] = fast_exp2(p[j] - mu[mt]);
                 l[mt] += p[j];
             }
+            // weights rounded to bf16 for the matrix product: at most 2^-8 of
+            // each, as far as the output's own rounding
+            pb[mt] = as_bf16x8(pack_bf16(p[0], p[1]), pack_bf16(p[2], p[3]),
+                               pack_bf16(p[4], p[5]), pack_bf16(p[6], p[7]));
             if (poison) {
-                // a later row's value is not finite: no product over all 32
-                // positions (0 times it is NaN); position by position instead
+                // position by position, each row only what it sees
                 for (int gg = 0; gg < 4; ++gg) {
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
@@ -434,23 +490,49 @@ __global__ __launch_bounds__(256) void attend_kernel(AttendArgs a) {
                         }
                     }
                 }
-                continue;
-            }
-            // weights rounded to bf16 for the matrix product: at most 2^-9 of
-            // each, as far as the output's own rounding
-            const bf16x8 pb = as_bf16x8(pack_bf16(p[0], p[1]), pack_bf16(p[2], p[3]),
-                                        pack_bf16(p[4], p[5]), pack_bf16(p[6], p[7]));
-#pragma unroll
-            for (int i = 0; i < C::kDpl; ++i) {
-                const uint32_t sel = (i & 1) ? 0x07060302u : 0x05040100u;
-                const bf16x8 vt = as_bf16x8(
-                    __builtin_amdgcn_perm(vw[1][i / 2], vw[0][i / 2], sel),
-                    __builtin_amdgcn_perm(vw[3][i / 2], vw[2][i / 2], sel),
-                    __builtin_amdgcn_perm(vw[5][i / 2], vw[4][i / 2], sel),
-                    __builtin_amdgcn_perm(vw[7][i / 2], vw[6][i / 2], sel));
-                acc[mt][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vt, pb, acc[mt][i], 0, 0, 0);
             }
         }
+        if (!poison) {
+#pragma unroll
+            for (int i2 = 0; i2 < C::kDpl / 2; ++i2) {
+                uint32_t w[8];  // dims 2 i2 and 2 i2 + 1 of the 8 positions
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    if (F8)
+                        w[j] = (i2 & 1) ? e4m3_pair<true>(now.r[j].w[i2 / 2])
+                                        : e4m3_pair<false>(now.r[j].w[i2 / 2]);
+                    else
+                        w[j] = now.r[j].w[F8 ? 0 : i2];
+                }
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const uint32_t sel = half ? 0x07060302u : 0x05040100u;
+                    const bf16x8 vt = as_bf16x8(__builtin_amdgcn_perm(w[1], w[0], sel),
+                                                __builtin_amdgcn_perm(w[3], w[2], sel),
+                                                __builtin_amdgcn_perm(w[5], w[4], sel),
+                                                __builtin_amdgcn_perm(w[7], w[6], sel));
+                    const int i = 2 * i2 + half;
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) {
+                        if (mt * 16 >= slots) break;
+                        acc[mt][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vt, pb[mt],
+                                                                              acc[mt][i], 0, 0, 0);
+                    }
+                }
+            }
+        }
+        if (!C::kTwoV && more) load(t1, ids1, &next, false);
+        t0 = t1;
+    };
+
+    if (C::kTwoV) {
+        while (t0 < end) {
+            tile(va, vb);
+            if (t0 >= end) break;
+            tile(vb, va);
+        }
+    } else {
+        while (t0 < end) tile(va, va);
     }
     if (__ballot(bad) != 0 && lane == 0) raise_error(a.dev_error, SV_DEV_BAD_PAGE);
 
@@ -472,9 +554,9 @@ __global__ __launch_bounds__(256) void attend_kernel(AttendArgs a) {
                 if (mt * 16 >= slots) break;
 #pragma unroll
                 for (int i = 0; i < C::kDpl; ++i)
-                    *reinterpret_cast<f32x4*>(sm.acc[b][mt][i][lane]) = acc[mt][i];
-                sm.m[b][mt][lane] = m[mt];
-                sm.l[b][mt][lane] = l[mt];
+                    *reinterpret_cast<f32x4*>(sm.part.acc[b][mt][i][lane]) = acc[mt][i];
+                sm.part.m[b][mt][lane] = m[mt];
+                sm.part.l[b][mt][lane] = l[mt];
             }
         }
         __syncthreads();
@@ -482,7 +564,7 @@ __global__ __launch_bounds__(256) void attend_kernel(AttendArgs a) {
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
                 if (mt * 16 >= slots) break;
-                const float m2 = sm.m[wave][mt][lane], l2 = sm.l[wave][mt][lane];
+                const float m2 = sm.part.m[wave][mt][lane], l2 = sm.part.l[wave][mt][lane];
                 const float mx = fmaxf(m[mt], m2);
                 const float f1 = m[mt] == mx ? 1.0f : fast_exp2(m[mt] - mx);
                 const float f2 = m2 == mx ? 1.0f : fast_exp2(m2 - mx);
@@ -490,7 +572,7 @@ __global__ __launch_bounds__(256) void attend_kernel(AttendArgs a) {
                 m[mt] = mx;
 #pragma unroll
                 for (int i = 0; i < C::kDpl; ++i) {
-                    const f32x4 o = *reinterpret_cast<const f32x4*>(sm.acc[wave][mt][i][lane]);
+                    const f32x4 o = *reinterpret_cast<const f32x4*>(sm.part.acc[wave][mt][i][lane]);
                     acc[mt][i] = acc[mt][i] * f1 + o * f2;
                 }
             }
@@ -523,9 +605,15 @@ __global__ __launch_bounds__(256) void attend_kernel(AttendArgs a) {
         } else {
             const int64_t rec = (((int64_t)r * a.n_heads + head) * (a.k_max + 1) + row) * a.parts +
                                 part;
-            float* o = a.part_out + rec * D + g * C::kAcc;
+            f32x4* o = reinterpret_cast<f32x4*>(a.part_out + rec * D + g * C::kAcc);
 #pragma unroll
-            for (int e = 0; e < C::kAcc; ++e) o[e] = acc[mt][e % C::kDpl][e / C::kDpl] * vscale;
+            for (int e = 0; e < C::kAcc; e += 4) {
+                f32x4 x;
+#pragma unroll
+                for (int i4 = 0; i4 < 4; ++i4)
+                    x[i4] = acc[mt][(e + i4) % C::kDpl][(e + i4) / C::kDpl] * vscale;
+                o[e / 4] = x;
+            }
             if (g == 0) {
                 a.part_ml[rec * 2] = m[mt];
                 a.part_ml[rec * 2 + 1] = l[mt];
@@ -534,40 +622,68 @@ __global__ __launch_bounds__(256) void attend_kernel(AttendArgs a) {
     }
 }
 
-// Merges the parts of one (row, head): one wave, lanes over the dims.
+// Merges the parts of one (row, head): a workgroup of four waves, wave w the
+// parts w, w + 4, ... (eight loads in flight each), lanes over the dims; the
+// waves' sums meet in LDS, in a fixed order.
 template <int D>
 __global__ __launch_bounds__(256) void join_kernel(AttendArgs a) {
+    constexpr int E = D / 64;
+    __shared__ float sm_o[4][D], sm_f[128];
     const sv_cache& c = a.cache;
-    const int lane = threadIdx.x & 63;
-    const int64_t id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int per = (a.k_max + 1) * a.n_heads;
-    if (id >= (int64_t)a.n_req * per) return;
-    const int r = (int)(id / per), rest = (int)(id % per);
+    const int r = blockIdx.x / per, rest = blockIdx.x % per;
     const int head = rest / (a.k_max + 1), row = rest % (a.k_max + 1);
     const int lo = a.cu_rows[r], hi = a.cu_rows[r + 1], rows = hi - lo, ctx = a.ctx_len[r];
     if (lo < 0 || hi < lo || rows > a.k_max + 1 || hi > a.q_rows || row >= rows) return;
     if (ctx < 0 || (int64_t)ctx + rows > (int64_t)a.max_pages * c.page_size) return;
     const int len = ctx + rows, plen = part_len(len, a.parts);
-    const int n = (len + plen - 1) / plen;
+    const int n = (len + plen - 1) / plen;  // at most 128
     const int64_t rec = (((int64_t)r * a.n_heads + head) * (a.k_max + 1) + row) * a.parts;
-    float m = -kInf;
-    for (int p = 0; p < n; ++p) m = fmaxf(m, a.part_ml[(rec + p) * 2]);
-    float l = 0.0f, o[D / 64];
+    const float* ml = a.part_ml + rec * 2;
+    const float* po = a.part_out + rec * D + lane * E;
+    // every wave: the largest maximum and the parts' factors, two a lane
+    float m0 = -kInf, m1 = -kInf, l0 = 0.0f, l1 = 0.0f;
+    if (lane < n) m0 = ml[2 * lane], l0 = ml[2 * lane + 1];
+    if (lane + 64 < n) m1 = ml[2 * lane + 128], l1 = ml[2 * lane + 129];
+    const float m = wave_max(fmaxf(m0, m1));
+    const float f0 = m0 == m ? 1.0f : fast_exp2(m0 - m), f1 = m1 == m ? 1.0f : fast_exp2(m1 - m);
+    const float l = wave_sum((lane < n ? f0 * l0 : 0.0f) + (lane + 64 < n ? f1 * l1 : 0.0f));
+    float o[E];
 #pragma unroll
-    for (int e = 0; e < D / 64; ++e) o[e] = 0.0f;
-    for (int p = 0; p < n; ++p) {
-        const float mp = a.part_ml[(rec + p) * 2];
-        const float f = mp == m ? 1.0f : fast_exp2(mp - m);
-        l += f * a.part_ml[(rec + p) * 2 + 1];
-        const float* src = a.part_out + (rec + p) * D + lane * (D / 64);
-#pragma unroll
-        for (int e = 0; e < D / 64; ++e) o[e] += f * src[e];
+    for (int e = 0; e < E; ++e) o[e] = 0.0f;
+    if (wave == 0) {
+        sm_f[lane] = f0;
+        sm_f[lane + 64] = f1;
     }
+    __syncthreads();
+    for (int p0 = wave; p0 < n; p0 += 32) {
+        float x[8][E];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int e = 0; e < E; ++e) x[i][e] = po[(int64_t)min(p0 + 4 * i, n - 1) * D + e];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (p0 + 4 * i >= n) break;
+            const float f = sm_f[p0 + 4 * i];
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[e] += f * x[i][e];
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) sm_o[wave][lane * E + e] = o[e];
+    __syncthreads();
+    if (wave != 0) return;
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     uint16_t* out = static_cast<uint16_t*>(a.out) + (int64_t)(lo + row) * a.out_ld +
-                    (int64_t)head * D + lane * (D / 64);
+                    (int64_t)head * D + lane * E;
 #pragma unroll
-    for (int e = 0; e < D / 64; ++e) out[e] = (uint16_t)pack_bf16(o[e] * inv, 0.0f);
+    for (int e = 0; e < E; ++e) {
+        const int i = lane * E + e;
+        const float x = (sm_o[0][i] + sm_o[1][i]) + (sm_o[2][i] + sm_o[3][i]);
+        out[e] = (uint16_t)pack_bf16(x * inv, 0.0f);
+    }
     if (a.out_lse != nullptr && lane == 0)
         a.out_lse[(int64_t)(lo + row) * a.n_heads + head] =
             l == 0.0f ? -kInf : (m + log2f(l)) * kLn2;
@@ -575,7 +691,7 @@ __global__ __launch_bounds__(256) void join_kernel(AttendArgs a) {
 
 template <int D, bool F8, int MT>
 void run_attend(const AttendArgs& a, unsigned grid, hipStream_t stream) {
-    if (a.cache.page_size % 16 == 0)
+    if (a.cache.page_size % 16 == 0 && 16 * a.cache.token_stride <= (int64_t)1 << 28)
         attend_kernel<D, F8, MT, true><<<grid, 256, 0, stream>>>(a);
     else
         attend_kernel<D, F8, MT, false><<<grid, 256, 0, stream>>>(a);
@@ -586,13 +702,12 @@ hipError_t run_attend_mt(const AttendArgs& a, hipStream_t stream) {
     const unsigned grid =
         (unsigned)((int64_t)a.cache.n_kv_heads * a.n_req * a.slot_blocks * a.parts);
     if (a.slot_tiles == 1) run_attend<D, F8, 1>(a, grid, stream);
+    else if constexpr (D == 256) return hipErrorInvalidValue;  // AttendPlan takes one
     else if (a.slot_tiles == 2) run_attend<D, F8, 2>(a, grid, stream);
-    else if constexpr (D < 256) run_attend<D, F8, 4>(a, grid, stream);
-    else return hipErrorInvalidValue;
+    else run_attend<D, F8, 4>(a, grid, stream);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.parts == 1) return e;
-    const int64_t waves = (int64_t)a.n_req * (a.k_max + 1) * a.n_heads;
-    join_kernel<D><<<(unsigned)((waves + 3) / 4), 256, 0, stream>>>(a);
+    join_kernel<D><<<(unsigned)(a.n_req * (a.k_max + 1) * a.n_heads), 256, 0, stream>>>(a);
     return hipGetLastError();
 }
 

@@ -34,6 +34,12 @@ sv_status check_cache(const sv_cache* c, int32_t max_pages) {
     return SV_OK;
 }
 
+int log2_exact(int32_t n) {
+    for (int i = 0; i < 31; ++i)
+        if (n == (int32_t)1 << i) return i;
+    return -1;
+}
+
 // Heads of one row are contiguous; rows start on 16 bytes.
 bool row_layout_ok(const void* p, int64_t ld, int64_t width) {
     return ld >= width && ld % 8 == 0 && aligned16(p);
@@ -121,7 +127,7 @@ sv_status sv_cache_attend(const sv_cache* cache, const int32_t* page_table, int3
     const sv::AttendArgs a{*cache,  page_table, max_pages, q,       q_ld,
                            q_rows,  n_heads,    n_heads / cache->n_kv_heads,
                            cu_rows, ctx_len,    n_req,     k_max,   scale,
-                           out,     out_ld,     out_lse,   dev_error,
+                           out,     out_ld,     out_lse,   dev_error, log2_exact(cache->page_size),
                            p.slot_tiles, p.slot_blocks, p.parts, part_out, part_ml};
     const hipError_t e = sv::launch_cache_attend(a, as_stream(stream));
     return sv::finish_launch(e, as_stream(stream));

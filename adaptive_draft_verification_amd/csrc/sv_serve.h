@@ -45,6 +45,7 @@ struct AttendArgs {
     int64_t out_ld;
     float* out_lse;
     int32_t* dev_error;
+    int page_shift;                      // log2 of the page size, -1 if it is no power of two
     int slot_tiles, slot_blocks, parts;  // AttendPlan's
     float* part_out;                     // parts > 1: [n_req, n_heads, k_max + 1, parts, head_dim]
     float* part_ml;                      //            [..., parts, 2] maximum and sum
@@ -57,6 +58,9 @@ inline __host__ __device__ int part_len(int len, int parts) {
     return ((len + parts - 1) / parts + 127) / 128 * 128;
 }
 
+#ifndef SV_ATTEND_WANT
+#define SV_ATTEND_WANT 2048
+#endif
 // How an attend call is cut into workgroups: by host-known sizes alone.
 struct AttendPlan {
     int slot_tiles;   // 16-slot tiles a workgroup takes: 1, 2 or 4
@@ -64,10 +68,10 @@ struct AttendPlan {
     int parts;        // workgroups over the cached positions
     AttendPlan(int n_req, int k_max, int n_heads, int n_kv_heads, int head_dim, int64_t capacity) {
         const int slots = (k_max + 1) * (n_heads / n_kv_heads);
-        slot_tiles = slots <= 16 ? 1 : slots <= 32 || head_dim > 128 ? 2 : 4;
+        slot_tiles = slots <= 16 || head_dim > 128 ? 1 : slots <= 32 ? 2 : 4;
         slot_blocks = (slots + 16 * slot_tiles - 1) / (16 * slot_tiles);
         const int64_t groups = (int64_t)n_req * n_kv_heads * slot_blocks;
-        const int64_t want = groups > 0 ? (2048 + groups - 1) / groups : 1;
+        const int64_t want = groups > 0 ? (SV_ATTEND_WANT + groups - 1) / groups : 1;
         const int64_t most = (capacity + 127) / 128;
         const int64_t p = want < most ? want : most;
         parts = (int)(p < 1 ? 1 : p > 128 ? 128 : p);
