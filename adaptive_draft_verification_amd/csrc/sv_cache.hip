@@ -157,7 +157,11 @@ __device__ __forceinline__ bool bf16_pair_nonfinite(uint32_t w) {
 
 template <int D, bool F8, int MT, bool PG16>
 struct Attend {
-    static constexpr int kTile = 32;        // positions a wave takes at once
+    // blocks of 32 positions a wave takes at once: 16 KB of keys and values in
+    // flight a wave where the registers allow it
+    static constexpr int kBlocks = MT == 4 ? 1 : 1;
+    static constexpr int kTile = 32 * kBlocks;
+    static constexpr int kHalves = 2 * kBlocks;  // of 16 positions
     static constexpr int kWaves = 4;
     static constexpr int kSteps = D / 32;   // products a 16-position score needs
     static constexpr int kKLoads = F8 ? D / 64 : D / 32;  // 16-byte loads of a key row's share
@@ -167,9 +171,10 @@ struct Attend {
     static constexpr int kEsize = F8 ? 1 : 2;
     // waves a SIMD has registers for; two sets of value registers where they fit
     static constexpr int kOccupancy = D < 256 && MT * D <= 256 ? 2 : 1;
-    static constexpr bool kTwoV = D < 256 && MT < 4;
+    static constexpr bool kTwoV = false;
 
     union Smem {
+        int lens[256];
         uint4 q[MT][kSteps][kWave];  // the queries as operand B, lane by lane
         // Partial results of slot tiles, lane by lane: running maximum (in
         // units of log2), sum and unnormalised output of slot lane % 16.
@@ -180,6 +185,38 @@ struct Attend {
     };
 };
 
+// The request of rank `rank` by context length, longest first (ties to the
+// lower request), for up to 256 requests: where workgroups take turns on the
+// CUs, a long request that starts last would be waited for alone (256 requests
+// of 0 .. 4096 positions: 429 us in their own order, 398 this way).
+__device__ __forceinline__ int longest(int rank, const int32_t* ctx_len, int n, int* lens) {
+    __shared__ int found;
+    const int t = threadIdx.x;
+    // lengths from 2^22 on count as equal: any order is a right one
+    const int mine = t < n ? (min(max(ctx_len[t], 0), (1 << 22) - 1) << 8) | (255 - t) : -1;
+    lens[t] = mine;
+    __syncthreads();
+    int ahead = 0;
+#pragma unroll 4
+    for (int j = 0; j < n; j += 4) {
+        const int4 v = *reinterpret_cast<const int4*>(lens + j);
+        ahead += (v.x > mine) + (v.y > mine) + (v.z > mine) + (v.w > mine);
+    }
+    if (t < n && ahead == rank) found = t;
+    __syncthreads();
+    return found;
+}
+
+// Consecutive workgroups go to the eight XCDs in turn, each with an L2 of its
+// own; `run` neighbouring work items that read the same lines (slot blocks of
+// a head, heads narrower than a line) are given to one XCD, one behind the
+// other: 64 requests, 16 heads of 64 bytes: 42 us without, 31 with.
+__device__ __forceinline__ int spread(int b, int total, int run) {
+    const int group = 8 * run, g = b / group, rest = b - g * group;
+    if ((g + 1) * group > total) return b;
+    return g * group + (rest & 7) * run + (rest >> 3);
+}
+
 template <int D, bool F8, int MT, bool PG16>
 __global__ __launch_bounds__(256, (Attend<D, F8, MT, PG16>::kOccupancy))
 void attend_kernel(AttendArgs a) {
@@ -189,13 +226,15 @@ void attend_kernel(AttendArgs a) {
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int col = lane & 15, g = lane >> 4;
-    // grid: kv heads fastest, then requests, slot blocks and parts
-    int id = blockIdx.x;
+    // grid: slot blocks fastest, then kv heads, requests and parts
+    int id = spread(blockIdx.x, gridDim.x, a.xcd_run * a.slot_blocks);
+    const int mb = id % a.slot_blocks;
+    id /= a.slot_blocks;
     const int h = id % c.n_kv_heads;
     id /= c.n_kv_heads;
-    const int r = id % a.n_req;
-    id /= a.n_req;
-    const int mb = id % a.slot_blocks, part = id / a.slot_blocks;
+    int r = id % a.n_req;
+    const int part = id / a.n_req;
+    if (a.longest_first) r = longest(r, a.ctx_len, a.n_req, sm.lens);
 
     const int lo = a.cu_rows[r], hi = a.cu_rows[r + 1];
     const int rows = hi - lo;
@@ -212,9 +251,10 @@ void attend_kernel(AttendArgs a) {
     const int slots = rows * G - mb * 16 * MT;  // slots of this block
     if (slots <= 0) return;
     const int len = ctx + rows;
-    const int plen = part_len(len, a.parts);
+    const int plen = part_len(len, a.parts, a.part_min);
     const int begin = part * plen, end = min(len, begin + plen);
     if (begin >= len) return;
+    const bool whole = plen >= len;  // the request's only part
 
     const char* kbase = static_cast<const char*>(c.k) + (int64_t)h * c.head_stride * C::kEsize;
     const char* vbase = static_cast<const char*>(c.v) + (int64_t)h * c.head_stride * C::kEsize;
@@ -237,31 +277,31 @@ void attend_kernel(AttendArgs a) {
         return a.page_shift >= 0 ? t >> a.page_shift : (int)((unsigned)t / (unsigned)c.page_size);
     };
     struct Ids {
-        int page[2];
+        int page[C::kHalves];
     };
     auto look_up = [&](int t0) {
         Ids p;
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int u = 0; u < C::kHalves; ++u)
             p.page[u] = table[page_index(min(t0 + 16 * u, last16))];
         return p;
     };
 
-    Words<4> kr[2][C::kKLoads];
+    Words<4> kr[C::kHalves][C::kKLoads];
     const int64_t tstride = c.token_stride * C::kEsize;
     const uint32_t koff = (uint32_t)(col * tstride) + g * 16;
     const uint32_t voff = (uint32_t)(g * 4 * tstride) + col * C::kDpl * C::kEsize;
     struct Values {
-        Words<C::kVWords> r[8];
+        Words<C::kVWords> r[4 * C::kHalves];
         uint32_t ok;  // bit j: the page of the lane's j-th position is good
     };
     // Issues a tile's loads: keys first, then values.
     auto load = [&](int t0, Ids ids, Values* v, bool keys) __attribute__((always_inline)) {
         if (PG16) {
-            const char* at[2];
+            const char* at[C::kHalves];
             uint32_t ok = 0;
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
+            for (int u = 0; u < C::kHalves; ++u) {
                 const int t = min(t0 + 16 * u, last16);
                 int page = __builtin_amdgcn_readfirstlane(ids.page[u]);
                 const bool good = page >= 0 && page < c.n_pages;
@@ -274,20 +314,20 @@ void attend_kernel(AttendArgs a) {
             }
             if (keys) {
 #pragma unroll
-                for (int u = 0; u < 2; ++u)
+                for (int u = 0; u < C::kHalves; ++u)
 #pragma unroll
                     for (int i = 0; i < C::kKLoads; ++i)
                         kr[u][i] = load_words<4>(at[u] + (koff + i * 64));
             } else {
                 v->ok = ok;
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
+                for (int j = 0; j < 4 * C::kHalves; ++j)
                     v->r[j] = load_words<C::kVWords>(at[j >> 2] +
                                                      (voff + (uint32_t)((j & 3) * tstride)));
             }
         } else if (keys) {
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
+            for (int u = 0; u < C::kHalves; ++u) {
                 bool ok;
                 const char* at = kbase + row_offset(t0 + 16 * u + col, ok);
 #pragma unroll
@@ -297,7 +337,7 @@ void attend_kernel(AttendArgs a) {
         } else {
             v->ok = 0;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
+            for (int j = 0; j < 4 * C::kHalves; ++j) {
                 bool ok;
                 const char* at = vbase + row_offset(t0 + 16 * (j >> 2) + g * 4 + (j & 3), ok);
                 v->ok |= ok ? 1u << j : 0u;
@@ -353,16 +393,18 @@ void attend_kernel(AttendArgs a) {
     int bad = 0;
 
     auto tile = [&](Values& now, Values& next) __attribute__((always_inline)) {
-        f32x4 s[MT][2];
+        constexpr int U = C::kHalves, J = 4 * U;  // halves; positions a lane holds
+        constexpr uint32_t kAllOk = J == 32 ? ~0u : (1u << J) - 1;
+        f32x4 s[MT][U];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-            for (int u = 0; u < 2; ++u) s[mt][u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            for (int u = 0; u < U; ++u) s[mt][u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int st = 0; st < C::kSteps; ++st) {
-            bf16x8 k8[2];
+            bf16x8 k8[U];
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
+            for (int u = 0; u < U; ++u) {
                 if (F8) {
                     const uint32_t w0 = kr[u][st / 2].w[(st & 1) * 2];
                     const uint32_t w1 = kr[u][st / 2].w[(st & 1) * 2 + 1];
@@ -378,7 +420,7 @@ void attend_kernel(AttendArgs a) {
                 const uint4 w = sm.q[mt][st][lane];
                 const bf16x8 q8 = as_bf16x8(w.x, w.y, w.z, w.w);
 #pragma unroll
-                for (int u = 0; u < 2; ++u)
+                for (int u = 0; u < U; ++u)
                     s[mt][u] =
                         __builtin_amdgcn_mfma_f32_16x16x32_bf16(k8[u], q8, s[mt][u], 0, 0, 0);
             }
@@ -391,7 +433,7 @@ void attend_kernel(AttendArgs a) {
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-            for (int u = 0; u < 2; ++u) asm volatile("" : "+v"(s[mt][u]));
+            for (int u = 0; u < U; ++u) asm volatile("" : "+v"(s[mt][u]));
         if (more) {
             load(t1, ids1, nullptr, true);
             if (C::kTwoV) load(t1, ids1, &next, false);
@@ -403,12 +445,12 @@ void attend_kernel(AttendArgs a) {
         // the end, or on a bad page, by none: their values are zeroed, since 0
         // times what lies there may be NaN.  A value that is not finite behind
         // the context poisons the product for the rows that do not see it.
-        if (now.ok != 0xffu) bad = 1;
-        const bool edge = t0 + C::kTile > ctx || __ballot(now.ok != 0xffu) != 0;
+        if (now.ok != kAllOk) bad = 1;
+        const bool edge = t0 + C::kTile > ctx || __ballot(now.ok != kAllOk) != 0;
         bool poison = false;
         if (edge) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
+            for (int j = 0; j < J; ++j) {
                 const int t = t0 + 16 * (j >> 2) + g * 4 + (j & 3);
                 const bool in = t < len && ((now.ok >> j) & 1);
                 bool nf = false;
@@ -426,23 +468,23 @@ void attend_kernel(AttendArgs a) {
             }
             poison = __ballot(poison) != 0;
         }
-        bf16x8 pb[MT];
+        bf16x8 pb[MT][C::kBlocks];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
             if (mt * 16 >= slots) break;
-            float p[8];
+            float p[J];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) p[j] = s[mt][j >> 2][j & 3] * scale;
+            for (int j = 0; j < J; ++j) p[j] = s[mt][j >> 2][j & 3] * scale;
             if (edge) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
+                for (int j = 0; j < J; ++j) {
                     const int t = t0 + 16 * (j >> 2) + g * 4 + (j & 3);
                     if (t > last[mt] || !((now.ok >> j) & 1)) p[j] = -kInf;
                 }
             }
             float mx = p[0];
 #pragma unroll
-            for (int j = 1; j < 8; ++j) mx = fmaxf(mx, p[j]);
+            for (int j = 1; j < J; ++j) mx = fmaxf(mx, p[j]);
             // the maximum moves only when a score passes it by 2^8: sums and
             // outputs are relative to it either way, and stay far from
             // overflow; most tiles then rescale nothing
@@ -458,19 +500,22 @@ void attend_kernel(AttendArgs a) {
                 }
             }
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
+            for (int j = 0; j < J; ++j) {
                 p[j] = fast_exp2(p[j] - mu[mt]);
                 l[mt] += p[j];
             }
             // weights rounded to bf16 for the matrix product: at most 2^-8 of
             // each, as far as the output's own rounding
-            pb[mt] = as_bf16x8(pack_bf16(p[0], p[1]), pack_bf16(p[2], p[3]),
-                               pack_bf16(p[4], p[5]), pack_bf16(p[6], p[7]));
+#pragma unroll
+            for (int b = 0; b < C::kBlocks; ++b)
+                pb[mt][b] =
+                    as_bf16x8(pack_bf16(p[8 * b], p[8 * b + 1]), pack_bf16(p[8 * b + 2], p[8 * b + 3]),
+                              pack_bf16(p[8 * b + 4], p[8 * b + 5]), pack_bf16(p[8 * b + 6], p[8 * b + 7]));
             if (poison) {
                 // position by position, each row only what it sees
                 for (int gg = 0; gg < 4; ++gg) {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
+                    for (int j = 0; j < J; ++j) {
                         const float pj = __shfl(p[j], gg * 16 + col);
                         const int t = t0 + 16 * (j >> 2) + gg * 4 + (j & 3);
                         bool ok;
@@ -495,28 +540,32 @@ void attend_kernel(AttendArgs a) {
         if (!poison) {
 #pragma unroll
             for (int i2 = 0; i2 < C::kDpl / 2; ++i2) {
-                uint32_t w[8];  // dims 2 i2 and 2 i2 + 1 of the 8 positions
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    if (F8)
-                        w[j] = (i2 & 1) ? e4m3_pair<true>(now.r[j].w[i2 / 2])
-                                        : e4m3_pair<false>(now.r[j].w[i2 / 2]);
-                    else
-                        w[j] = now.r[j].w[F8 ? 0 : i2];
-                }
+                for (int b = 0; b < C::kBlocks; ++b) {
+                    uint32_t w[8];  // dims 2 i2 and 2 i2 + 1 of the block's 8 positions
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const uint32_t sel = half ? 0x07060302u : 0x05040100u;
-                    const bf16x8 vt = as_bf16x8(__builtin_amdgcn_perm(w[1], w[0], sel),
-                                                __builtin_amdgcn_perm(w[3], w[2], sel),
-                                                __builtin_amdgcn_perm(w[5], w[4], sel),
-                                                __builtin_amdgcn_perm(w[7], w[6], sel));
-                    const int i = 2 * i2 + half;
+                    for (int j = 0; j < 8; ++j) {
+                        const Words<C::kVWords>& v = now.r[8 * b + j];
+                        if (F8)
+                            w[j] = (i2 & 1) ? e4m3_pair<true>(v.w[i2 / 2])
+                                            : e4m3_pair<false>(v.w[i2 / 2]);
+                        else
+                            w[j] = v.w[F8 ? 0 : i2];
+                    }
 #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) {
-                        if (mt * 16 >= slots) break;
-                        acc[mt][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vt, pb[mt],
-                                                                              acc[mt][i], 0, 0, 0);
+                    for (int half = 0; half < 2; ++half) {
+                        const uint32_t sel = half ? 0x07060302u : 0x05040100u;
+                        const bf16x8 vt = as_bf16x8(__builtin_amdgcn_perm(w[1], w[0], sel),
+                                                    __builtin_amdgcn_perm(w[3], w[2], sel),
+                                                    __builtin_amdgcn_perm(w[5], w[4], sel),
+                                                    __builtin_amdgcn_perm(w[7], w[6], sel));
+                        const int i = 2 * i2 + half;
+#pragma unroll
+                        for (int mt = 0; mt < MT; ++mt) {
+                            if (mt * 16 >= slots) break;
+                            acc[mt][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                                vt, pb[mt][b], acc[mt][i], 0, 0, 0);
+                        }
                     }
                 }
             }
@@ -586,7 +635,7 @@ void attend_kernel(AttendArgs a) {
         const int i = mt * 16 + col, slot = mb * 16 * MT + i;
         if (i >= slots) continue;
         const int row = slot / G, head = h * G + slot % G;
-        if (a.parts == 1) {
+        if (whole) {
             const float inv = l[mt] == 0.0f ? 0.0f : vscale / l[mt];
             uint32_t w[C::kAcc / 2];
 #pragma unroll
@@ -622,71 +671,100 @@ void attend_kernel(AttendArgs a) {
     }
 }
 
-// Merges the parts of one (row, head): a workgroup of four waves, wave w the
-// parts w, w + 4, ... (eight loads in flight each), lanes over the dims; the
-// waves' sums meet in LDS, in a fixed order.
-template <int D>
+// Merges the parts of a (row, head): W waves, wave w the parts w, w + W, ...
+// (eight loads in flight each), lanes over the dims; the waves' sums meet in
+// LDS, in a fixed order.  A request of one part wrote its outputs itself.
+template <int D, int W>
 __global__ __launch_bounds__(256) void join_kernel(AttendArgs a) {
-    constexpr int E = D / 64;
-    __shared__ float sm_o[4][D], sm_f[128];
+    constexpr int E = D / 64, kEach = 4 / W;  // (row, head)s a workgroup takes at once
+    __shared__ float sm_o[4][D], sm_f[4][128];
     const sv_cache& c = a.cache;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int w = wave % W;
     const int per = (a.k_max + 1) * a.n_heads;
-    const int r = blockIdx.x / per, rest = blockIdx.x % per;
-    const int head = rest / (a.k_max + 1), row = rest % (a.k_max + 1);
-    const int lo = a.cu_rows[r], hi = a.cu_rows[r + 1], rows = hi - lo, ctx = a.ctx_len[r];
-    if (lo < 0 || hi < lo || rows > a.k_max + 1 || hi > a.q_rows || row >= rows) return;
-    if (ctx < 0 || (int64_t)ctx + rows > (int64_t)a.max_pages * c.page_size) return;
-    const int len = ctx + rows, plen = part_len(len, a.parts);
-    const int n = (len + plen - 1) / plen;  // at most 128
-    const int64_t rec = (((int64_t)r * a.n_heads + head) * (a.k_max + 1) + row) * a.parts;
-    const float* ml = a.part_ml + rec * 2;
-    const float* po = a.part_out + rec * D + lane * E;
-    // every wave: the largest maximum and the parts' factors, two a lane
-    float m0 = -kInf, m1 = -kInf, l0 = 0.0f, l1 = 0.0f;
-    if (lane < n) m0 = ml[2 * lane], l0 = ml[2 * lane + 1];
-    if (lane + 64 < n) m1 = ml[2 * lane + 128], l1 = ml[2 * lane + 129];
-    const float m = wave_max(fmaxf(m0, m1));
-    const float f0 = m0 == m ? 1.0f : fast_exp2(m0 - m), f1 = m1 == m ? 1.0f : fast_exp2(m1 - m);
-    const float l = wave_sum((lane < n ? f0 * l0 : 0.0f) + (lane + 64 < n ? f1 * l1 : 0.0f));
-    float o[E];
+    const int64_t total = (int64_t)a.n_req * per;
+    for (int64_t first = (int64_t)blockIdx.x * kEach; first < total;
+         first += (int64_t)gridDim.x * kEach) {
+        const int64_t id = first + wave / W;
+        const int r = (int)(min(id, total - 1) / per), rest = (int)(min(id, total - 1) % per);
+        const int row = rest / a.n_heads, head = rest % a.n_heads;
+        const int lo = a.cu_rows[r], hi = a.cu_rows[r + 1], rows = hi - lo, ctx = a.ctx_len[r];
+        bool live = id < total && lo >= 0 && hi >= lo && rows <= a.k_max + 1 && hi <= a.q_rows &&
+                    row < rows && ctx >= 0 &&
+                    (int64_t)ctx + rows <= (int64_t)a.max_pages * c.page_size;
+        const int len = ctx + rows, plen = live ? part_len(len, a.parts, a.part_min) : 1;
+        live = live && plen < len;
+        if (W == 4 && !live) continue;  // the same in every wave
+        const int n = live ? (len + plen - 1) / plen : 0;  // at most 128
+        const int64_t rec =
+            (((int64_t)r * a.n_heads + head) * (a.k_max + 1) + row) * a.parts;
+        const float* ml = a.part_ml + rec * 2;
+        const float* po = a.part_out + rec * D + lane * E;
+        float m = -kInf, l = 0.0f, o[E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = 0.0f;
-    if (wave == 0) {
-        sm_f[lane] = f0;
-        sm_f[lane + 64] = f1;
-    }
-    __syncthreads();
-    for (int p0 = wave; p0 < n; p0 += 32) {
-        float x[8][E];
+        for (int e = 0; e < E; ++e) o[e] = 0.0f;
+        if (live) {
+            // every wave: the largest maximum and the parts' factors, two a lane
+            float m0 = -kInf, m1 = -kInf, l0 = 0.0f, l1 = 0.0f;
+            if (lane < n) m0 = ml[2 * lane], l0 = ml[2 * lane + 1];
+            if (lane + 64 < n) m1 = ml[2 * lane + 128], l1 = ml[2 * lane + 129];
+            m = wave_max(fmaxf(m0, m1));
+            const float f0 = m0 == m ? 1.0f : fast_exp2(m0 - m);
+            const float f1 = m1 == m ? 1.0f : fast_exp2(m1 - m);
+            l = wave_sum((lane < n ? f0 * l0 : 0.0f) + (lane + 64 < n ? f1 * l1 : 0.0f));
+            float* factor = sm_f[wave];
+            factor[lane] = f0;
+            factor[lane + 64] = f1;
+            __builtin_amdgcn_wave_barrier();
+            for (int p0 = w; p0 < n; p0 += 8 * W) {
+                float x[8][E];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+                for (int i = 0; i < 8; ++i)
 #pragma unroll
-            for (int e = 0; e < E; ++e) x[i][e] = po[(int64_t)min(p0 + 4 * i, n - 1) * D + e];
+                    for (int e = 0; e < E; ++e)
+                        x[i][e] = po[(int64_t)min(p0 + W * i, n - 1) * D + e];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if (p0 + 4 * i >= n) break;
-            const float f = sm_f[p0 + 4 * i];
+                for (int i = 0; i < 8; ++i) {
+                    if (p0 + W * i >= n) break;
+                    const float f = factor[p0 + W * i];
 #pragma unroll
-            for (int e = 0; e < E; ++e) o[e] += f * x[i][e];
+                    for (int e = 0; e < E; ++e) o[e] += f * x[i][e];
+                }
+            }
         }
-    }
+        if (W > 1) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) sm_o[wave][lane * E + e] = o[e];
-    __syncthreads();
-    if (wave != 0) return;
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    uint16_t* out = static_cast<uint16_t*>(a.out) + (int64_t)(lo + row) * a.out_ld +
-                    (int64_t)head * D + lane * E;
+            for (int e = 0; e < E; ++e) sm_o[wave][lane * E + e] = o[e];
+            __syncthreads();
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-        const int i = lane * E + e;
-        const float x = (sm_o[0][i] + sm_o[1][i]) + (sm_o[2][i] + sm_o[3][i]);
-        out[e] = (uint16_t)pack_bf16(x * inv, 0.0f);
+            for (int e = 0; e < E; ++e) {
+                const int i = lane * E + e;
+                o[e] = (sm_o[0][i] + sm_o[1][i]) + (sm_o[2][i] + sm_o[3][i]);
+            }
+            __syncthreads();
+        }
+        if (!live || w != 0) continue;
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        uint16_t* out = static_cast<uint16_t*>(a.out) + (int64_t)(lo + row) * a.out_ld +
+                        (int64_t)head * D + lane * E;
+#pragma unroll
+        for (int e = 0; e < E; ++e) out[e] = (uint16_t)pack_bf16(o[e] * inv, 0.0f);
+        if (a.out_lse != nullptr && lane == 0)
+            a.out_lse[(int64_t)(lo + row) * a.n_heads + head] =
+                l == 0.0f ? -kInf : (m + log2f(l)) * kLn2;
     }
-    if (a.out_lse != nullptr && lane == 0)
-        a.out_lse[(int64_t)(lo + row) * a.n_heads + head] =
-            l == 0.0f ? -kInf : (m + log2f(l)) * kLn2;
+}
+
+template <int D>
+void run_join(const AttendArgs& a, hipStream_t stream) {
+    const int64_t total = (int64_t)a.n_req * (a.k_max + 1) * a.n_heads;
+    // up to 16 parts one wave keeps them all in flight in two goes
+    if (a.parts <= 16) {
+        const int64_t grid = (total + 3) / 4;
+        join_kernel<D, 1><<<(unsigned)(grid < 4096 ? grid : 4096), 256, 0, stream>>>(a);
+    } else {
+        join_kernel<D, 4><<<(unsigned)(total < 4096 ? total : 4096), 256, 0, stream>>>(a);
+    }
 }
 
 template <int D, bool F8, int MT>
@@ -707,7 +785,7 @@ hipError_t run_attend_mt(const AttendArgs& a, hipStream_t stream) {
     else run_attend<D, F8, 4>(a, grid, stream);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.parts == 1) return e;
-    join_kernel<D><<<(unsigned)(a.n_req * (a.k_max + 1) * a.n_heads), 256, 0, stream>>>(a);
+    run_join<D>(a, stream);
     return hipGetLastError();
 }
 

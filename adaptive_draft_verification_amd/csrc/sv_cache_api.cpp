@@ -2,6 +2,7 @@
 // the caller's stream.  Every check runs before any HIP call.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
@@ -40,6 +41,13 @@ int log2_exact(int32_t n) {
     return -1;
 }
 
+// How many neighbouring heads' rows of a position lie in a 128-byte line.
+int xcd_run(const sv_cache& c) {
+    const int64_t row = (int64_t)c.head_dim * (c.dtype == SV_E4M3 ? 1 : 2);
+    if (c.head_stride != c.head_dim || row >= 128) return 1;
+    return (int)std::min<int64_t>(128 / row, c.n_kv_heads);
+}
+
 // Heads of one row are contiguous; rows start on 16 bytes.
 bool row_layout_ok(const void* p, int64_t ld, int64_t width) {
     return ld >= width && ld % 8 == 0 && aligned16(p);
@@ -68,7 +76,8 @@ size_t sv_cache_attend_workspace_bytes(int32_t n_req, int32_t k_max, int32_t n_h
     const int64_t capacity = (int64_t)max_pages * page_size;
     if (check_attend_sizes(n_req, k_max, n_heads, n_kv_heads, head_dim, capacity) != SV_OK)
         return 0;
-    const sv::AttendPlan p(n_req, k_max, n_heads, n_kv_heads, head_dim, capacity);
+    // two-byte caches are cut into no fewer parts than one-byte ones
+    const sv::AttendPlan p(n_req, k_max, n_heads, n_kv_heads, head_dim, 2, capacity);
     return p.bytes(n_req, k_max, n_heads, head_dim);
 }
 
@@ -115,7 +124,8 @@ sv_status sv_cache_attend(const sv_cache* cache, const int32_t* page_table, int3
     if ((double)q_rows * (double)q_ld > 2.0e18 || (double)q_rows * (double)out_ld > 2.0e18)
         return SV_ERR_SHAPE;
     if (cache->n_pages == 0) return SV_ERR_SHAPE;  // a bad page id reads page 0 instead
-    const sv::AttendPlan p(n_req, k_max, n_heads, cache->n_kv_heads, cache->head_dim, capacity);
+    const sv::AttendPlan p(n_req, k_max, n_heads, cache->n_kv_heads, cache->head_dim,
+                           cache->dtype == SV_E4M3 ? 1 : 2, capacity);
     const size_t need = p.bytes(n_req, k_max, n_heads, cache->head_dim);
     if (need > 0 && (ws == nullptr || ws_bytes < need)) return SV_ERR_WORKSPACE;
     if (!aligned16(ws)) return SV_ERR_WORKSPACE;
@@ -127,8 +137,10 @@ sv_status sv_cache_attend(const sv_cache* cache, const int32_t* page_table, int3
     const sv::AttendArgs a{*cache,  page_table, max_pages, q,       q_ld,
                            q_rows,  n_heads,    n_heads / cache->n_kv_heads,
                            cu_rows, ctx_len,    n_req,     k_max,   scale,
-                           out,     out_ld,     out_lse,   dev_error, log2_exact(cache->page_size),
-                           p.slot_tiles, p.slot_blocks, p.parts, part_out, part_ml};
+                           out,     out_ld,     out_lse,   dev_error, xcd_run(*cache),
+                           n_req > 1 && n_req <= 256 && p.grid(n_req, cache->n_kv_heads) > 1024,
+                           log2_exact(cache->page_size),
+                           p.slot_tiles, p.slot_blocks, p.parts, p.part_min, part_out, part_ml};
     const hipError_t e = sv::launch_cache_attend(a, as_stream(stream));
     return sv::finish_launch(e, as_stream(stream));
 }

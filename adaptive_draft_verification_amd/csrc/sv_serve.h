@@ -45,34 +45,47 @@ struct AttendArgs {
     int64_t out_ld;
     float* out_lse;
     int32_t* dev_error;
+    int xcd_run;                         // neighbouring heads that share cache lines
+    bool longest_first;                  // requests by length (n_req <= 256)
     int page_shift;                      // log2 of the page size, -1 if it is no power of two
-    int slot_tiles, slot_blocks, parts;  // AttendPlan's
+    int slot_tiles, slot_blocks, parts, part_min;  // AttendPlan's
     float* part_out;                     // parts > 1: [n_req, n_heads, k_max + 1, parts, head_dim]
     float* part_ml;                      //            [..., parts, 2] maximum and sum
 };
 hipError_t launch_cache_attend(const AttendArgs& a, hipStream_t stream);
 
 // Positions in each part of a request's length: a multiple of 128 (four waves
-// of 32), so that short requests use fewer parts than the launch has.
-inline __host__ __device__ int part_len(int len, int parts) {
-    return ((len + parts - 1) / parts + 127) / 128 * 128;
+// of 32), no fewer than part_min.
+inline __host__ __device__ int part_len(int len, int parts, int part_min) {
+    const int even = ((len + parts - 1) / parts + 127) / 128 * 128;
+    return even > part_min ? even : part_min;
 }
 
 #ifndef SV_ATTEND_WANT
-#define SV_ATTEND_WANT 2048
+#define SV_ATTEND_WANT 1024
+#endif
+#ifndef SV_ATTEND_MIN
+#define SV_ATTEND_MIN 32
 #endif
 // How an attend call is cut into workgroups: by host-known sizes alone.
 struct AttendPlan {
     int slot_tiles;   // 16-slot tiles a workgroup takes: 1, 2 or 4
     int slot_blocks;  // workgroups over a (request, kv head)'s query slots
-    int parts;        // workgroups over the cached positions
-    AttendPlan(int n_req, int k_max, int n_heads, int n_kv_heads, int head_dim, int64_t capacity) {
+    int parts;        // workgroups over the cached positions, at most
+    int part_min;     // positions a part has at least
+    AttendPlan(int n_req, int k_max, int n_heads, int n_kv_heads, int head_dim, int esize,
+               int64_t capacity) {
         const int slots = (k_max + 1) * (n_heads / n_kv_heads);
         slot_tiles = slots <= 16 || head_dim > 128 ? 1 : slots <= 32 ? 2 : 4;
         slot_blocks = (slots + 16 * slot_tiles - 1) / (16 * slot_tiles);
+        // a part writes and the join reads 8 bytes a slot and dim, against
+        // 2 esize bytes a position and dim read: 32 positions a slot (64 for
+        // one-byte caches) keep that to an eighth of the reads
+        const int block = slots < 16 * slot_tiles ? slots : 16 * slot_tiles;
+        part_min = (SV_ATTEND_MIN * (esize == 1 ? 2 : 1) * block + 127) / 128 * 128;
         const int64_t groups = (int64_t)n_req * n_kv_heads * slot_blocks;
         const int64_t want = groups > 0 ? (SV_ATTEND_WANT + groups - 1) / groups : 1;
-        const int64_t most = (capacity + 127) / 128;
+        const int64_t most = (capacity + part_min - 1) / part_min;
         const int64_t p = want < most ? want : most;
         parts = (int)(p < 1 ? 1 : p > 128 ? 128 : p);
     }

@@ -373,3 +373,15 @@ def test_append_faults_leave_the_cache_alone():
         torch.cuda.synchronize()
         assert int(err) == bit
         assert torch.equal(b.kd, before[0]) and torch.equal(b.vd, before[1])
+
+
+@pytest.mark.parametrize("n,heads,kv,dim,dtype", [(200, 16, 8, 64, F8), (257, 8, 8, 64, BF),
+                                                  (40, 32, 32, 128, BF)])
+def test_attend_many_workgroups(n, heads, kv, dim, dtype):
+    """More workgroups than the CUs take at once: requests served longest first
+    (up to 256 of them), heads that share cache lines kept together."""
+    rng = np.random.default_rng(n)
+    rows = [int(x) for x in rng.integers(0, 3, n)]
+    ctx = [int(x) for x in rng.integers(0, 60, n)]
+    ctx[3], ctx[n // 2] = 700, 700
+    Batch(30 + n, rows, ctx, heads, kv, dim, 16, dtype, k_max=2).device().check()
