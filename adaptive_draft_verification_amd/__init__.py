@@ -133,36 +133,42 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
-def _same_device(first, *others):
-    for t in others:
-        if t is not None and t.device != first.device:
-            raise ValueError("every tensor must be on one device")
+# The serving calls below run every decode step, some of them many times: their
+# checks are written for few Python operations (addresses go to the library as
+# plain integers, devices are compared by index).
+
+def _on(t, dtype, name, device, shape):
+    """Address of a contiguous device tensor of this type, device and shape (None: no tensor)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.get_device() != device or not t.is_contiguous():
+        _dev(t, dtype, name)
+        raise ValueError(f"{name} must be on the call's device")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    return t.data_ptr()
 
 
-class _on_device:
-    """Makes a tensor's device current for a launch on one of its streams."""
-
-    def __init__(self, t, stream):
-        if stream is not None and stream.device != t.device:
-            raise ValueError("the stream must be on the tensors' device")
-        self.want, self.back = t.device.index, None
-
-    def __enter__(self):
-        cur = torch.cuda.current_device()
-        if cur != self.want:
-            self.back = cur
-            torch.cuda.set_device(self.want)
-
-    def __exit__(self, *exc):
-        if self.back is not None:
-            torch.cuda.set_device(self.back)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _stream_on(t, stream):
-    """The stream given, else the current one of the tensor's device."""
+def _launch(fn, name, device, stream, *args):
+    """fn(*args, stream) with `device` current; stream: the given one, else the device's current."""
     if stream is None:
-        stream = torch.cuda.current_stream(t.device)
-    return ctypes.c_void_p(stream.cuda_stream)
+        handle = (_raw_stream(device) if _raw_stream is not None
+                  else torch.cuda.current_stream(device).cuda_stream)
+    elif stream.device.index != device:
+        raise ValueError("the stream must be on the tensors' device")
+    else:
+        handle = stream.cuda_stream
+    current = torch.cuda.current_device()
+    if current == device:
+        status = fn(*args, handle)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, handle)
+    if status != SV_OK:
+        raise SvError(status, name)
 
 
 def _dev(t, dtype, name, ndim=None):
@@ -510,52 +516,46 @@ class Sampling(NamedTuple):
     min_p: Optional[torch.Tensor] = None
 
 
-def _law(law, n, like, name="law"):
+def _law(law, n, device, name="law"):
     if law is None:
         return None
-    for field, t, dtype in zip(law._fields, law, (torch.float32, torch.int32, torch.float32,
-                                                  torch.float32)):
-        _dev(t, dtype, f"{name}.{field}", 1)
-        if t is not None and t.numel() != n:
-            raise ValueError(f"{name}.{field} must have {n} entries")
-    _same_device(like, *law)
-    return ctypes.byref(_Law(*(None if t is None else t.data_ptr() for t in law)))
+    n = (n,)
+    return ctypes.byref(_Law(_on(law.temperature, torch.float32, f"{name}.temperature", device, n),
+                             _on(law.top_k, torch.int32, f"{name}.top_k", device, n),
+                             _on(law.top_p, torch.float32, f"{name}.top_p", device, n),
+                             _on(law.min_p, torch.float32, f"{name}.min_p", device, n)))
 
 
-def _logits(t, name):
-    """Row stride of a logit matrix: rows may lie further apart than they are long."""
+def _logits(t, name, vocab):
+    """(address, row stride, rows) of a logit matrix, whose rows may lie further apart than
+    they are long."""
     if not t.is_cuda or t.dtype not in _DTYPES or t.dim() != 2:
         raise ValueError(f"{name} must be a bfloat16 or float32 device matrix")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    rows, width = t.shape
+    if vocab is not None and vocab > width:
+        raise ValueError(f"vocab must not pass {name}'s width")
+    if t.is_contiguous():
+        return t.data_ptr(), width, rows
+    if width > 1 and t.stride(1) != 1:
         raise ValueError(f"{name} must have contiguous rows")
-    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+    if rows > 1 and t.stride(0) < width:
         raise ValueError(f"{name}'s rows must not overlap")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    return t.data_ptr(), t.stride(0) if rows > 1 else width, rows
 
 
 def sv_sample(logits, u, law, out_tokens, out_prob=None, out_support=None, dev_error=None,
               vocab=None, stream=None):
     """logits [rows, >=V] (bf16 or f32), u [rows] f32 in [0, 1) -> out_tokens [rows] i32 drawn
     under law (a Sampling or None), out_prob [rows] f32, out_support [rows] i32."""
-    ld = _logits(logits, "logits")
-    n = logits.shape[0]
-    _dev(u, torch.float32, "u", 1)
-    _dev(out_prob, torch.float32, "out_prob", 1)
-    for name, t in (("out_tokens", out_tokens), ("out_support", out_support),
-                    ("dev_error", dev_error)):
-        _dev(t, torch.int32, name, 1)
-    for t in (u, out_tokens, out_prob, out_support):
-        if t is not None and t.numel() != n:
-            raise ValueError("u, out_tokens, out_prob, out_support need one entry a row")
-    V = logits.shape[1] if vocab is None else int(vocab)
-    if V > logits.shape[1]:
-        raise ValueError("vocab must not pass the rows' width")
-    _same_device(logits, u, out_tokens, out_prob, out_support, dev_error)
-    with _on_device(logits, stream):
-        _check(_lib.sv_sample(_ptr(logits), ld, n, _DTYPES[logits.dtype], V,
-                              _law(law, n, logits), _ptr(u), _ptr(out_tokens), _ptr(out_prob),
-                              _ptr(out_support), _ptr(dev_error), _stream_on(logits, stream)),
-               "sv_sample")
+    at, ld, n = _logits(logits, "logits", vocab)
+    device, rows = logits.get_device(), (n,)
+    _launch(_lib.sv_sample, "sv_sample", device, stream, at, ld, n, _DTYPES[logits.dtype],
+            logits.shape[1] if vocab is None else int(vocab), _law(law, n, device),
+            _on(u, torch.float32, "u", device, rows),
+            _on(out_tokens, torch.int32, "out_tokens", device, rows),
+            _on(out_prob, torch.float32, "out_prob", device, rows),
+            _on(out_support, torch.int32, "out_support", device, rows),
+            _on(dev_error, torch.int32, "dev_error", device, None))
 
 
 def sv_verify_truncated_workspace_bytes(n_req, k_max):
@@ -568,42 +568,30 @@ def sv_verify_truncated(target, draft, draft_tokens, cu_rows, target_law, draft_
     """sv_verify with each request's truncated laws: target [rows, >=V], draft [n*k_max, >=V]
     (None if k_max is 0), target_law and draft_law a Sampling of [n] settings or None;
     ws: uint8 device buffer of sv_verify_truncated_workspace_bytes(n, k_max) bytes."""
-    _dev(draft_tokens, torch.int32, "draft_tokens", 2)
-    _dev(out_tokens, torch.int32, "out_tokens", 2)
-    for name, t in (("cu_rows", cu_rows), ("out_accepted", out_accepted),
-                    ("dev_error", dev_error)):
-        _dev(t, torch.int32, name, 1)
-    _dev(ws, torch.uint8, "ws", 1)
-    _dev(out_residual_mass, torch.float32, "out_residual_mass", 1)
+    at, ld, rows = _logits(target, "target", vocab)
+    device = target.get_device()
+    V = target.shape[1] if vocab is None else int(vocab)
+    if draft_tokens.dim() != 2:
+        raise ValueError("draft_tokens must have 2 dimensions")
     n, k_max = draft_tokens.shape
-    ld, V = _logits(target, "target"), target.shape[1] if vocab is None else int(vocab)
-    draft_ld = V
+    draft_at, draft_ld = None, V
     if draft is not None:
-        draft_ld = _logits(draft, "draft")
-        if draft.dtype != target.dtype or draft.shape[0] < n * k_max or V > draft.shape[1]:
-            raise ValueError("draft must hold n*k_max rows of the target's type and width")
-    if V > target.shape[1]:
-        raise ValueError("vocab must not pass the rows' width")
-    if cu_rows.numel() != n + 1 or tuple(out_tokens.shape) != (n, k_max + 1) \
-            or out_accepted.numel() != n:
-        raise ValueError("cu_rows [n+1], out_tokens [n, k_max+1], out_accepted [n]")
-    for name, t in (("out_p_draft", out_p_draft), ("out_q_draft", out_q_draft)):
-        _dev(t, torch.float32, name, 2)
-        if t is not None and tuple(t.shape) != (n, k_max):
-            raise ValueError(f"{name} must be [n, k_max]")
-    if out_residual_mass is not None and out_residual_mass.numel() != n:
-        raise ValueError("out_residual_mass must have n entries")
-    _same_device(target, draft, draft_tokens, cu_rows, out_tokens, out_accepted, ws, out_p_draft,
-                 out_q_draft, out_residual_mass, dev_error)
-    with _on_device(target, stream):
-        _check(_lib.sv_verify_truncated(
-            _ptr(target), ld, target.shape[0], _ptr(draft), draft_ld, _DTYPES[target.dtype], V,
-            _ptr(draft_tokens), _ptr(cu_rows), n, k_max, _law(target_law, n, target, "target_law"),
-            _law(draft_law, n, target, "draft_law"), int(seed), int(step), _ptr(out_tokens),
-            _ptr(out_accepted), _ptr(out_p_draft), _ptr(out_q_draft), _ptr(out_residual_mass),
-            _ptr(dev_error), _ptr(ws), 0 if ws is None else ws.numel(),
-            _stream_on(target, stream)),
-            "sv_verify_truncated")
+        draft_at, draft_ld, draft_rows = _logits(draft, "draft", V)
+        if draft.dtype is not target.dtype or draft_rows < n * k_max \
+                or draft.get_device() != device:
+            raise ValueError("draft must hold n*k_max rows of the target's type, on its device")
+    _launch(_lib.sv_verify_truncated, "sv_verify_truncated", device, stream, at, ld, rows,
+            draft_at, draft_ld, _DTYPES[target.dtype], V,
+            _on(draft_tokens, torch.int32, "draft_tokens", device, None),
+            _on(cu_rows, torch.int32, "cu_rows", device, (n + 1,)), n, k_max,
+            _law(target_law, n, device, "target_law"), _law(draft_law, n, device, "draft_law"),
+            int(seed), int(step), _on(out_tokens, torch.int32, "out_tokens", device, (n, k_max + 1)),
+            _on(out_accepted, torch.int32, "out_accepted", device, (n,)),
+            _on(out_p_draft, torch.float32, "out_p_draft", device, (n, k_max)),
+            _on(out_q_draft, torch.float32, "out_q_draft", device, (n, k_max)),
+            _on(out_residual_mass, torch.float32, "out_residual_mass", device, (n,)),
+            _on(dev_error, torch.int32, "dev_error", device, None),
+            _on(ws, torch.uint8, "ws", device, None), 0 if ws is None else ws.numel())
 
 
 class PagedCache:
@@ -611,42 +599,52 @@ class PagedCache:
     float8_e4m3fn), any strides over pages, positions and heads that both share, the last
     dimension contiguous; k_scale, v_scale [n_kv_heads] f32 (float8 caches)."""
 
+    __slots__ = ("k", "v", "k_scale", "v_scale", "device", "n_kv_heads", "head_dim", "page_size",
+                 "_c", "_at")
+
     def __init__(self, k, v, k_scale=None, v_scale=None):
-        if not (k.is_cuda and v.is_cuda) or k.device != v.device:
+        dtype = _CACHE_DTYPES.get(k.dtype)
+        if not k.is_cuda or v.get_device() != k.get_device():
             raise ValueError("k and v must be device tensors on one device")
-        if k.dtype not in _CACHE_DTYPES or v.dtype != k.dtype:
+        if dtype is None or v.dtype is not k.dtype:
             raise ValueError("k and v must both be bfloat16 or float8_e4m3fn")
-        if k.dim() != 4 or v.shape != k.shape or v.stride() != k.stride() or k.stride(3) != 1:
+        strides = k.stride()
+        if k.dim() != 4 or v.shape != k.shape or v.stride() != strides or strides[3] != 1:
             raise ValueError("k and v must be [n_pages, page_size, n_kv_heads, head_dim] with "
                              "the same strides, the last dimension contiguous")
-        for name, s in (("k_scale", k_scale), ("v_scale", v_scale)):
-            if s is None:
-                continue
-            if k.dtype == torch.bfloat16:
-                raise ValueError("scales belong to float8 caches")
-            _dev(s, torch.float32, name, 1)
-            if s.numel() != k.shape[2] or s.device != k.device:
-                raise ValueError(f"{name} must be [n_kv_heads] on the cache's device")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self.n_kv_heads, self.head_dim = k.shape[2], k.shape[3]
-        self.page_size = k.shape[1]
-        addr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
-        self._c = _Cache(k.data_ptr(), v.data_ptr(), _CACHE_DTYPES[k.dtype], *k.shape,
-                         *k.stride()[:3], addr(k_scale), addr(v_scale))
+        self.device = k.get_device()
+        n_pages, self.page_size, self.n_kv_heads, self.head_dim = k.shape
+        if dtype == SV_BF16 and (k_scale is not None or v_scale is not None):
+            raise ValueError("scales belong to float8 caches")
+        heads = (self.n_kv_heads,)
+        self._c = _Cache(k.data_ptr(), v.data_ptr(), dtype, n_pages, self.page_size,
+                         self.n_kv_heads, self.head_dim, strides[0], strides[1], strides[2],
+                         _on(k_scale, torch.float32, "k_scale", self.device, heads),
+                         _on(v_scale, torch.float32, "v_scale", self.device, heads))
+        self._at = ctypes.addressof(self._c)
 
 
 _CACHE_DTYPES = {torch.bfloat16: SV_BF16, torch.float8_e4m3fn: SV_E4M3}
 
 
-def _rows(t, name, heads, dim):
-    """Row stride of a [rows, heads, dim] bfloat16 tensor whose rows are contiguous."""
-    if not t.is_cuda or t.dtype != torch.bfloat16 or t.dim() != 3 \
-            or (heads is not None and t.shape[1] != heads) or t.shape[2] != dim:
-        raise ValueError(f"{name} must be a bfloat16 device tensor "
-                         f"[rows, {heads or 'heads'}, {dim}]")
-    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != dim):
+def _rows(t, name, device, heads, dim):
+    """(address, row stride) of a [rows, heads, dim] bfloat16 tensor whose rows are contiguous."""
+    if t.dtype is not torch.bfloat16 or t.get_device() != device or t.dim() != 3 \
+            or t.shape[1] != heads or t.shape[2] != dim:
+        raise ValueError(f"{name} must be bfloat16 [rows, {heads}, {dim}] on the cache's device")
+    if t.is_contiguous():
+        return t.data_ptr(), heads * dim
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim):
         raise ValueError(f"{name} must have contiguous heads within a row")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * dim
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else heads * dim
+
+
+def _table(page_table, device):
+    at = _on(page_table, torch.int32, "page_table", device, None)
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [n, max_pages]")
+    return at, page_table.shape[0], page_table.shape[1]
 
 
 def sv_cache_append(cache, page_table, k, v, row_req, row_pos, ctx_len, dev_error=None,
@@ -654,23 +652,18 @@ def sv_cache_append(cache, page_table, k, v, row_req, row_pos, ctx_len, dev_erro
     """Rows k, v [rows, n_kv_heads, head_dim] bf16 into the cache, row i at position
     ctx_len[row_req[i]] + row_pos[i] (the maps pack_varlen writes; -1: skipped);
     page_table [n, max_pages] i32, ctx_len [n] i32."""
-    _dev(page_table, torch.int32, "page_table", 2)
-    for name, t in (("row_req", row_req), ("row_pos", row_pos), ("ctx_len", ctx_len),
-                    ("dev_error", dev_error)):
-        _dev(t, torch.int32, name, 1)
-    ld = _rows(k, "k", cache.n_kv_heads, cache.head_dim)
-    if _rows(v, "v", cache.n_kv_heads, cache.head_dim) != ld or v.shape[0] != k.shape[0]:
+    device = cache.device
+    table, n, max_pages = _table(page_table, device)
+    k_at, ld = _rows(k, "k", device, cache.n_kv_heads, cache.head_dim)
+    v_at, v_ld = _rows(v, "v", device, cache.n_kv_heads, cache.head_dim)
+    rows = k.shape[0]
+    if v_ld != ld or v.shape[0] != rows:
         raise ValueError("k and v must have the same rows and row stride")
-    n, max_pages = page_table.shape
-    if row_req.numel() != k.shape[0] or row_pos.numel() != k.shape[0] or ctx_len.numel() != n:
-        raise ValueError("row_req, row_pos need one entry a row, ctx_len one a request")
-    _same_device(cache.k, page_table, k, v, row_req, row_pos, ctx_len, dev_error)
-    with _on_device(cache.k, stream):
-        _check(_lib.sv_cache_append(ctypes.byref(cache._c), _ptr(page_table), max_pages, _ptr(k),
-                                    _ptr(v), ld, _ptr(row_req), _ptr(row_pos), k.shape[0],
-                                    _ptr(ctx_len), n, _ptr(dev_error),
-                                    _stream_on(cache.k, stream)),
-               "sv_cache_append")
+    _launch(_lib.sv_cache_append, "sv_cache_append", device, stream, cache._at, table, max_pages,
+            k_at, v_at, ld, _on(row_req, torch.int32, "row_req", device, (rows,)),
+            _on(row_pos, torch.int32, "row_pos", device, (rows,)), rows,
+            _on(ctx_len, torch.int32, "ctx_len", device, (n,)), n,
+            _on(dev_error, torch.int32, "dev_error", device, None))
 
 
 def sv_cache_attend_workspace_bytes(n_req, k_max, n_heads, n_kv_heads, head_dim, max_pages,
@@ -685,27 +678,19 @@ def sv_cache_attend(cache, page_table, q, cu_rows, ctx_len, k_max, scale, out, w
     (packed row cu_rows[r] + j) sees the cache's positions 0 .. ctx_len[r] + j.
     ws: uint8 device buffer of sv_cache_attend_workspace_bytes(...) bytes (None if 0);
     out_lse [rows, n_heads] f32."""
-    _dev(page_table, torch.int32, "page_table", 2)
-    for name, t in (("cu_rows", cu_rows), ("ctx_len", ctx_len), ("dev_error", dev_error)):
-        _dev(t, torch.int32, name, 1)
-    _dev(out_lse, torch.float32, "out_lse", 2)
-    _dev(ws, torch.uint8, "ws", 1)
-    q_ld = _rows(q, "q", None, cache.head_dim)
-    heads = q.shape[1]
-    out_ld = _rows(out, "out", heads, cache.head_dim)
-    n, max_pages = page_table.shape
-    if out.shape != q.shape or cu_rows.numel() != n + 1 or ctx_len.numel() != n:
-        raise ValueError("out must have q's shape; cu_rows [n+1], ctx_len [n]")
-    if out_lse is not None and tuple(out_lse.shape) != (q.shape[0], heads):
-        raise ValueError("out_lse must be [rows, n_heads]")
-    _same_device(cache.k, page_table, q, cu_rows, ctx_len, out, ws, out_lse, dev_error)
-    with _on_device(cache.k, stream):
-        _check(_lib.sv_cache_attend(ctypes.byref(cache._c), _ptr(page_table), max_pages, _ptr(q),
-                                    q_ld, q.shape[0], heads, _ptr(cu_rows), _ptr(ctx_len), n,
-                                    int(k_max), float(scale), _ptr(out), out_ld, _ptr(out_lse),
-                                    _ptr(dev_error), _ptr(ws), 0 if ws is None else ws.numel(),
-                                    _stream_on(cache.k, stream)),
-               "sv_cache_attend")
+    device = cache.device
+    table, n, max_pages = _table(page_table, device)
+    if q.dim() != 3 or out.shape != q.shape:
+        raise ValueError("q must be [rows, n_heads, head_dim] and out of its shape")
+    rows, heads, _ = q.shape
+    q_at, q_ld = _rows(q, "q", device, heads, cache.head_dim)
+    out_at, out_ld = _rows(out, "out", device, heads, cache.head_dim)
+    _launch(_lib.sv_cache_attend, "sv_cache_attend", device, stream, cache._at, table, max_pages,
+            q_at, q_ld, rows, heads, _on(cu_rows, torch.int32, "cu_rows", device, (n + 1,)),
+            _on(ctx_len, torch.int32, "ctx_len", device, (n,)), n, int(k_max), float(scale),
+            out_at, out_ld, _on(out_lse, torch.float32, "out_lse", device, (rows, heads)),
+            _on(dev_error, torch.int32, "dev_error", device, None),
+            _on(ws, torch.uint8, "ws", device, None), 0 if ws is None else ws.numel())
 
 
 # ----------------------------------------------------------------------------
