@@ -167,9 +167,11 @@ struct Row {
     static constexpr int kWords = 2 * kBytes;
     static constexpr uint32_t kFill = DT == SV_BF16 ? 0xff80ff80u : 0xff800000u;  // -inf
 
-    __device__ __forceinline__ Row(const char* row, int v) : base(row), vocab(v) {
+    // segments: one for each of the workgroup's waves, or more
+    __device__ __forceinline__ Row(const char* row, int v, int segments = kWaves)
+        : base(row), vocab(v) {
         const int n = (v + 7) / 8;
-        per = ((n + kWaves - 1) / kWaves + kWave - 1) / kWave * kWave;
+        per = ((n + segments - 1) / segments + kWave - 1) / kWave * kWave;
         steps = per / kWave;
     }
     __device__ __forceinline__ int first_id(int wave, int step, int lane) const {
@@ -313,12 +315,13 @@ struct Row {
 // of them and not nearly a wave per 64 ids of the row (129,280 ids, 2 % kept:
 // 30 us against 9 for the sum of their weights).
 template <sv_dtype DT, int NT, class Keep, class Use>
-__device__ __forceinline__ void compact(const Row<DT, NT>& row, Smem<NT>& sm, Keep keep, Use use) {
+__device__ __forceinline__ void compact(const Row<DT, NT>& row, Smem<NT>& sm, int segment, Keep keep,
+                                        Use use) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     float* qz = sm.queue_z[wave];
     int* qi = sm.queue_id[wave];
     int n = 0;  // the same in every lane
-    row.granules_of(wave, lane, [&](const typename Row<DT, NT>::Raw& g, int id0) {
+    row.granules_of(segment, lane, [&](const typename Row<DT, NT>::Raw& g, int id0) {
         float z[8];
         g.unpack(z);
         int c = 0;
@@ -824,7 +827,7 @@ __device__ __forceinline__ bool find_nucleus(const Row<DT, NT>& row, const Setti
     const float edge = m - (float)(b2 + 1) / per_logit * 1.00001f - fabsf(m) * 1e-6f;
     int n = 0;
     part = 0.0;
-    compact(row, sm, [&](float z) { return z >= edge; }, [&](float z, int id) {
+    compact(row, sm, wave, [&](float z) { return z >= edge; }, [&](float z, int id) {
         const int s = step_of(z);
         n += __popcll(__ballot(s < b1));
         if (s < b1) {
@@ -917,18 +920,15 @@ __device__ __forceinline__ Result find_law(const Row<DT, NT>& row, const Setting
     if (set.t == 0.0f) {
         lb = key_logit(top);
     } else if (set.k > 0 && set.k <= NT) {
-        // about the k-th largest of the threads' maxima, and no larger: k ids
-        // are at least that
-        const uint32_t low =
-            ~block_max(mine > kMinusInfKey ? ~mine : 0u, sm);  // the least of them
-        const float per = 255.0f / fmaxf((float)(top - low), 1.0f);
-        const uint32_t bin = mine > kMinusInfKey ? (uint32_t)((float)(top - mine) * per) : 0u;
+        // Just below the k-th largest of the threads' maxima: k ids are at
+        // least that.  Bins of 2^16 key steps (a bf16 step) below the largest
+        // logit; where fewer than k maxima are in the first 255, no bound.
+        const uint32_t bin = min((top - mine) >> 16, 255u);
         const Found f = descend<false>(
             sm, [&](auto fn) { if (mine > kMinusInfKey) fn(bin, [] { return 0.0; }); }, 0, 0,
             (uint32_t)set.k, 0.0, false);
-        const uint32_t least =
-            ~block_max(mine > kMinusInfKey && bin <= f.ord ? ~mine : 0u, sm);
-        if (f.found) lb = key_logit(least);
+        const uint32_t below = (f.ord + 1) << 16;
+        if (f.found && f.ord < 255 && top - kMinusInfKey > below) lb = key_logit(top - below + 1);
     }
     if (set.s > 0.0f && set.t > 0.0f && !(use_p && set.k > 0)) {
         // a little below m + T ln s, for the roundings on the way (of the
@@ -1040,7 +1040,7 @@ __device__ __forceinline__ Result find_law(const Row<DT, NT>& row, const Setting
             part += law.raw(z);
         });
     } else {
-        compact(row, sm, [&](float z) { return z >= law.zc && z >= lb; }, [&](float z, int id) {
+        compact(row, sm, threadIdx.x >> 6, [&](float z) { return z >= law.zc && z >= lb; }, [&](float z, int id) {
             const double x = law.raw(z);
             const bool live = law.above(z, id) && x >= law.s;
             n += __popcll(__ballot(live));
@@ -1052,29 +1052,30 @@ __device__ __forceinline__ Result find_law(const Row<DT, NT>& row, const Setting
     return r;
 }
 
-// The smallest id whose running sum, over a row in wave segments, passes goal.
-// The waves' sums are in sm.redd; all waves together sum the steps of the
-// segment that holds the crossing, one wave walks the step that does.
-// weights(id0, x) gives the 8 weights at ids id0 .. id0 + 7.  If rounding leaves
-// no such id, the last one of positive weight.
+// The smallest id whose running sum, over a row in segments, passes goal.  sums
+// holds the sum of each of the `segments`; all waves together sum the steps of
+// the segment that holds the crossing, one wave walks the step that does.
+// first_id(segment, step, lane) is a lane's first id, weights(id0, x) gives the
+// 8 weights at ids id0 .. id0 + 7.  If rounding leaves no such id, the last one
+// of positive weight.
 template <int NT, class Weights, class FirstId>
-__device__ int walk_row(Smem<NT>& sm, double goal, int steps, FirstId first_id, int vocab,
-                        Weights weights) {
+__device__ int walk_row(Smem<NT>& sm, const double* sums, int segments, double goal, int steps,
+                        FirstId first_id, int vocab, Weights weights) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     double before = 0.0;
     int owner = -1;
-    for (int w = 0; w < NT / kWave; ++w) {
-        if (before + sm.redd[w] > goal) {
+    for (int w = 0; w < segments; ++w) {
+        if (before + sums[w] > goal) {
             owner = w;
             break;
         }
-        before += sm.redd[w];
+        before += sums[w];
     }
     if (owner < 0) {
         goal = kInf;
         before = 0.0;
-        for (int w = 0; w < NT / kWave; ++w)
-            if (sm.redd[w] > 0.0) owner = w;
+        for (int w = 0; w < segments; ++w)
+            if (sums[w] > 0.0) owner = w;
     }
     const auto read = [&](int s, double* x) {
         const int id0 = first_id(owner, s, lane);
@@ -1177,7 +1178,7 @@ __device__ int draw(const Row<DT, NT>& row, const Result& r, float u, Smem<NT>& 
     }
     if (r.where == kInRow) {
         return walk_row(
-            sm, goal, row.steps,
+            sm, sm.redd, NT / kWave, goal, row.steps,
             [&](int w, int s, int l) { return row.first_id(w, s, l); }, row.vocab,
             [&](int id0, double* x) {
                 float z[8];

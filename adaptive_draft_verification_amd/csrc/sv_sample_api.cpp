@@ -43,7 +43,8 @@ size_t sv_verify_truncated_workspace_bytes(int32_t n_req, int32_t k_max) {
     if (n_req < 0 || k_max < 0 || k_max > SV_MAX_DRAFT ||
         (int64_t)n_req * (2 * k_max + 1) > SV_MAX_VERIFY_SLOTS)
         return 0;
-    return (size_t)n_req * (2 * k_max + 1) * sizeof(sv::LawRecord);
+    return (size_t)n_req * ((2 * k_max + 1) * sizeof(sv::LawRecord) +
+                            sv::kVerifyParts * sizeof(double));
 }
 
 sv_status sv_verify_truncated(const void* target_logits, int64_t target_ld, int64_t target_rows,
@@ -79,7 +80,10 @@ sv_status sv_verify_truncated(const void* target_logits, int64_t target_ld, int6
                                     law_of(target_law), law_of(draft_law), seed, step,
                                     out_tokens, out_accepted, out_p_draft, out_q_draft,
                                     out_residual_mass, dev_error,
-                                    static_cast<sv::LawRecord*>(ws)};
+                                    static_cast<sv::LawRecord*>(ws),
+                                    reinterpret_cast<double*>(
+                                        static_cast<sv::LawRecord*>(ws) +
+                                        (size_t)n_req * (2 * k_max + 1))};
     const hipError_t e = sv::launch_verify_truncated(a, as_stream(stream));
     return sv::finish_launch(e, as_stream(stream));
 }

@@ -146,7 +146,9 @@ struct VerifyTruncatedArgs {
     float* out_residual_mass;
     int32_t* dev_error;
     LawRecord* laws;  // [n_req, 2 k_max + 1]: target rows 0 .. k_max, draft rows
+    double* sums;     // [n_req, kVerifyParts]: of the row the token at L is drawn from
 };
+constexpr int kVerifyParts = 8;
 hipError_t launch_verify_truncated(const VerifyTruncatedArgs& a, hipStream_t stream);
 
 }  // namespace sv

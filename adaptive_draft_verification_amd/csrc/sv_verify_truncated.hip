@@ -5,10 +5,10 @@
 //
 // Launch 1, one 512-thread workgroup per row slot: the law of each target row
 // 0 .. b and draft row 0 .. b - 1 of a request (LawRecord), and the weight it
-// gives the position's draft id.  Launch 2, one workgroup per request: wave 0
-// decides (lane j: position j), then the token at L is drawn over the one or
-// two rows that decide it, in 64 bits: each wave sums a contiguous segment of
-// ids, the wave that holds the crossing walks its segment again.
+// gives the position's draft id.  From these a wave decides (lane j: position
+// j).  Launch 2: the row or two rows that decide the token at L are summed in
+// eight parts, in 64 bits.  Launch 3: the outputs, and the draw: the part that
+// holds the crossing is summed again by segments and steps, one step is walked.
 #include "sv_law.h"
 #include "sv_launch.h"
 
@@ -78,94 +78,81 @@ __device__ law::Weigher weigher(const LawRecord& rec, const law::Settings& set) 
     return w;
 }
 
-struct DecideSmem {
-    int L, fault;
-    float v;
+// A request's decisions, as one wave takes them (lane j: position j).
+struct Decision {
+    int L, fault;  // the same in every lane; SV_DEV_* bits
+    float v;       // the draw's uniform
+    bool acc;
+    double p, q;   // of the lane's draft id (-1: none)
+    int d;
 };
 
-template <sv_dtype DT, int kDecide>
-__global__ __launch_bounds__(kDecide, kDecide == kWave ? 1 : 4) void decide_kernel(VerifyTruncatedArgs a) {
-    using Row = law::Row<DT, kDecide>;
-    __shared__ law::Smem<kDecide> sm;
-    __shared__ DecideSmem ds;
-    const int r = blockIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int k_max = a.k_max;
-    const Span s = span(a, r);
+__device__ __forceinline__ Decision decide(const VerifyTruncatedArgs& a, int r, const Span& s) {
+    const int j = threadIdx.x & 63, k_max = a.k_max;
     const LawRecord* laws = a.laws + (int64_t)r * (2 * k_max + 1);
-    const law::Settings pset = law::settings(a.target_law, r, a.vocab);
-    const law::Settings qset = law::settings(a.draft_law, r, a.vocab);
-    int32_t* out = a.out_tokens + (int64_t)r * (k_max + 1);
-    if (wave == 0) {
-        const int j = lane;
-        int fault = s.ok ? 0 : SV_DEV_BAD_CU_ROWS;
-        // settings of the draft's law matter only where a draft row is read
-        if (pset.bad || (qset.bad && s.ok && s.b > 0)) fault |= SV_DEV_BAD_PARAM;
-        float u = 0.0f, v = 0.0f;
-        draw_uniforms(a.seed, a.step, (uint32_t)r, (uint32_t)j, &u, &v);
-        bool acc = true;
-        double p = -1.0, q = -1.0;
-        int d = -1;
-        if (s.ok) {
-            if (j < s.b) {
-                d = a.draft_tokens[(int64_t)r * k_max + j];
-                if (d < 0 || d >= a.vocab) fault |= SV_DEV_BAD_TOKEN;
-                const LawRecord t = laws[j], w = laws[k_max + 1 + j];
-                fault |= t.fault | w.fault;
-                if (!(t.fault | w.fault)) {
-                    p = t.drafted / t.total;
-                    q = w.drafted / w.total;
-                    acc = q > 0.0 ? (double)u < p / q : p > 0.0;
-                }
+    Decision o{0, s.ok ? 0 : SV_DEV_BAD_CU_ROWS, 0.0f, true, -1.0, -1.0, -1};
+    // settings of the draft's law matter only where a draft row is read
+    if (law::settings(a.target_law, r, a.vocab).bad ||
+        (s.ok && s.b > 0 && law::settings(a.draft_law, r, a.vocab).bad))
+        o.fault |= SV_DEV_BAD_PARAM;
+    float u = 0.0f, v = 0.0f;
+    draw_uniforms(a.seed, a.step, (uint32_t)r, (uint32_t)j, &u, &v);
+    if (s.ok) {
+        if (j < s.b) {
+            o.d = a.draft_tokens[(int64_t)r * k_max + j];
+            if (o.d < 0 || o.d >= a.vocab) o.fault |= SV_DEV_BAD_TOKEN;
+            const LawRecord t = laws[j], w = laws[k_max + 1 + j];
+            o.fault |= t.fault | w.fault;
+            if (!(t.fault | w.fault)) {
+                o.p = t.drafted / t.total;
+                o.q = w.drafted / w.total;
+                o.acc = o.q > 0.0 ? (double)u < o.p / o.q : o.p > 0.0;
             }
-            if (j == 0) fault |= laws[s.b].fault;
         }
-        fault = wave_or_int(fault);
-        const uint64_t rej = __ballot(!acc);
-        const int L = rej ? __builtin_ctzll(rej) : s.b;
-        if (lane == 0) {
-            ds.L = L;
-            ds.fault = fault;
-        }
-        if (j == L) ds.v = v;
-        if (L == kWave && lane == 0) {
-            float u2;
-            draw_uniforms(a.seed, a.step, (uint32_t)r, (uint32_t)L, &u2, &v);
-            ds.v = v;
-        }
-        if (fault && lane == 0) raise_error(a.dev_error, fault);
-        for (int i = j; i <= k_max; i += kWave) {
-            if (fault) out[i] = -1;
-            else if (i != L) out[i] = i < L ? d : -1;
-        }
-        if (j < k_max) {
-            const int64_t o = (int64_t)r * k_max + j;
-            if (a.out_p_draft) a.out_p_draft[o] = fault || j >= s.b ? -1.0f : (float)p;
-            if (a.out_q_draft) a.out_q_draft[o] = fault || j >= s.b ? -1.0f : (float)q;
-        }
-        if (j == 0) {
-            a.out_accepted[r] = fault ? -1 : L;
-            if (a.out_residual_mass && (fault || L == s.b)) a.out_residual_mass[r] = -1.0f;
+        if (j == 0) o.fault |= laws[s.b].fault;
+    }
+    o.fault = wave_or_int(o.fault);
+    const uint64_t rej = __ballot(!o.acc);
+    o.L = rej ? __builtin_ctzll(rej) : s.b;
+    o.v = __shfl(v, o.L & 63);
+    if (o.L == kWave) {
+        float u2;
+        draw_uniforms(a.seed, a.step, (uint32_t)r, (uint32_t)o.L, &u2, &v);
+        o.v = v;
+    }
+    return o;
+}
+
+// The weights the token at L is drawn from: p's, or the residual's.
+template <sv_dtype DT, int NT>
+struct Drawn {
+    law::Weigher pw, qw;
+    law::Row<DT, NT> prow, qrow;
+    double ip, iq;
+    bool minus;  // the residual p - q, not p
+
+    __device__ __forceinline__ Drawn(const VerifyTruncatedArgs& a, int r, const Span& s, int L,
+                                     int segments)
+        : prow(target_row<DT>(a, s.lo, L), a.vocab, segments),
+          qrow(prow), ip(0.0), iq(0.0), minus(L < s.b) {
+        const LawRecord* laws = a.laws + (int64_t)r * (2 * a.k_max + 1);
+        const LawRecord pr = laws[L];
+        pw = weigher(pr, law::settings(a.target_law, r, a.vocab));
+        qw = pw;
+        if (minus) {
+            const LawRecord qr = laws[a.k_max + 1 + L];
+            qw = weigher(qr, law::settings(a.draft_law, r, a.vocab));
+            qrow = law::Row<DT, NT>(draft_row<DT>(a, r, L), a.vocab, segments);
+            ip = 1.0 / pr.total;
+            iq = 1.0 / qr.total;
         }
     }
-    __syncthreads();
-    if (ds.fault) return;
-    const int L = ds.L;
-    const bool residual = L < s.b;
-    const LawRecord pr = laws[L];
-    const law::Weigher pw = weigher(pr, pset);
-    const Row prow(target_row<DT>(a, s.lo, L), a.vocab);
-    const double ip = 1.0 / pr.total;
-    law::Weigher qw = pw;
-    Row qrow = prow;
-    double iq = 0.0;
-    if (residual) {
-        const LawRecord qr = laws[k_max + 1 + L];
-        qw = weigher(qr, qset);
-        qrow = Row(draft_row<DT>(a, r, L), a.vocab);
-        iq = 1.0 / qr.total;
+    // z: p's logit at id
+    __device__ __forceinline__ double of(float z, int id) const {
+        const double x = pw(z, id);
+        return minus && x > 0.0 ? fmax(0.0, x * ip - qw(qrow.one(id), id) * iq) : x;
     }
-    bool minus = residual;
-    const auto weights = [&](int id0, double* x) {
+    __device__ __forceinline__ void of8(int id0, double* x) const {
         float z[8], y[8];
         prow.load(id0, z);
         if (minus) qrow.load(id0, y);
@@ -174,29 +161,123 @@ __global__ __launch_bounds__(kDecide, kDecide == kWave ? 1 : 4) void decide_kern
             x[e] = pw(z[e], id0 + e);
             if (minus && x[e] > 0.0) x[e] = fmax(0.0, x[e] * ip - qw(y[e], id0 + e) * iq);
         }
-    };
-    // only ids of p's support weigh anything, in the residual too
-    const auto sum_row = [&]() {
-        double part = 0.0;
-        law::compact(prow, sm, [&](float z) { return z >= pw.zc && z > -law::kInf; },
-                     [&](float z, int id) {
-                         double x = pw(z, id);
-                         if (minus) x = fmax(0.0, x * ip - qw(qrow.one(id), id) * iq);
-                         part += x;
-                     });
-        return law::block_sum(part, sm);
-    };
-    double total = sum_row();
-    if (residual && threadIdx.x == 0 && a.out_residual_mass)
-        a.out_residual_mass[r] = (float)total;
-    if (total == 0.0) {  // no residual mass: p itself
-        minus = false;
-        total = sum_row();
     }
+    // The calling wave's sum over a segment of the row, in every lane.
+    __device__ __forceinline__ double sum(law::Smem<NT>& sm, int segment) const {
+        double part = 0.0;
+        if (pw.zc == -law::kInf) {  // nothing cut: every id weighs
+            const int lane = threadIdx.x & 63;
+            for (int st = 0; st < prow.steps; ++st) {
+                const int id0 = prow.first_id(segment, st, lane);
+                if (prow.first_id(segment, st, 0) >= prow.vocab) break;
+                double x[8];
+                of8(id0, x);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) part += x[e];
+            }
+        } else {
+            law::compact(prow, sm, segment, [&](float z) { return z >= pw.zc; },
+                         [&](float z, int id) { part += of(z, id); });
+        }
+        return wave_sum(part);
+    }
+};
+
+// The calling workgroup's segments of a part of the row, summed by its waves
+// into sm.redd, and their total, the same whenever it is taken.
+template <sv_dtype DT, int NT>
+__device__ double sum_part(const Drawn<DT, NT>& drawn, law::Smem<NT>& sm, int part) {
+    constexpr int kWaves = NT / kWave;
+    const int wave = threadIdx.x >> 6;
+    const double x = drawn.sum(sm, part * kWaves + wave);
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) sm.redd[wave] = x;
+    __syncthreads();
+    double total = 0.0;
+    for (int w = 0; w < kWaves; ++w) total += sm.redd[w];
+    return total;
+}
+
+// Launch 2: the sums of the row (or two) that decide the token at L, kParts
+// workgroups a request: requests whose settings cut nothing take a hundred times
+// the work of greedy ones, and would leave most CUs waiting if each had one
+// workgroup (256 x 7, mixed: 129 us).
+template <sv_dtype DT, int NT, int kParts>
+__global__ __launch_bounds__(NT, NT == kWave ? 1 : 4) void sums_kernel(VerifyTruncatedArgs a) {
+    __shared__ law::Smem<NT> sm;
+    const int r = blockIdx.x / kParts, part = blockIdx.x % kParts;
+    const Span s = span(a, r);
+    const Decision o = decide(a, r, s);  // every wave for itself
+    if (o.fault) return;
+    const Drawn<DT, NT> drawn(a, r, s, o.L, kParts * NT / kWave);
+    const double total = sum_part(drawn, sm, part);
+    if (threadIdx.x == 0) a.sums[(int64_t)r * kVerifyParts + part] = total;
+}
+
+// Launch 3: outputs and the token at L, a workgroup per request.
+template <sv_dtype DT, int NT, int kParts>
+__global__ __launch_bounds__(NT, NT == kWave ? 1 : 4) void decide_kernel(VerifyTruncatedArgs a) {
+    __shared__ law::Smem<NT> sm;
+    const int r = blockIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int k_max = a.k_max;
+    const Span s = span(a, r);
+    const Decision o = decide(a, r, s);
+    int32_t* out = a.out_tokens + (int64_t)r * (k_max + 1);
+    if (wave == 0) {
+        const int j = lane;
+        if (o.fault && lane == 0) raise_error(a.dev_error, o.fault);
+        for (int i = j; i <= k_max; i += kWave) {
+            if (o.fault) out[i] = -1;
+            else if (i != o.L) out[i] = i < o.L ? o.d : -1;
+        }
+        if (j < k_max) {
+            const int64_t at = (int64_t)r * k_max + j;
+            if (a.out_p_draft) a.out_p_draft[at] = o.fault || j >= s.b ? -1.0f : (float)o.p;
+            if (a.out_q_draft) a.out_q_draft[at] = o.fault || j >= s.b ? -1.0f : (float)o.q;
+        }
+        if (j == 0) {
+            a.out_accepted[r] = o.fault ? -1 : o.L;
+            if (a.out_residual_mass && (o.fault || o.L == s.b)) a.out_residual_mass[r] = -1.0f;
+        }
+    }
+    if (o.fault) return;
+    Drawn<DT, NT> drawn(a, r, s, o.L, kParts * NT / kWave);
+    double sums[kParts], total = 0.0;
+#pragma unroll
+    for (int i = 0; i < kParts; ++i) sums[i] = a.sums[(int64_t)r * kVerifyParts + i];
+#pragma unroll
+    for (int i = 0; i < kParts; ++i) total += sums[i];
+    if (drawn.minus && threadIdx.x == 0 && a.out_residual_mass)
+        a.out_residual_mass[r] = (float)total;
+    if (total == 0.0) {  // no residual mass: p itself (rare: summed here)
+        drawn.minus = false;
+#pragma unroll 1
+        for (int i = 0; i < kParts; ++i) {
+            const double x = sum_part(drawn, sm, i);
+#pragma unroll
+            for (int e = 0; e < kParts; ++e) sums[e] = e == i ? x : sums[e];
+            total += x;
+        }
+    }
+    // the part that holds the crossing; if rounding leaves none, the last of
+    // any weight, and in it the last id of any
+    double goal = (double)o.v * total, before = 0.0, at = 0.0;
+    int part = -1, positive = 0;
+#pragma unroll
+    for (int i = 0; i < kParts; ++i) {
+        if (part < 0 && before + sums[i] > goal) part = i, at = before;
+        if (sums[i] > 0.0) positive = i;
+        before += sums[i];
+    }
+    goal = part < 0 ? (double)law::kInf : goal - at;
+    if (part < 0) part = positive;
+    sum_part(drawn, sm, part);
+    const int base = part * (NT / kWave);
     const int tok = law::walk_row(
-        sm, (double)ds.v * total, prow.steps,
-        [&](int w, int st, int l) { return prow.first_id(w, st, l); }, a.vocab, weights);
-    if (threadIdx.x == 0) out[L] = tok;
+        sm, sm.redd, NT / kWave, goal, drawn.prow.steps,
+        [&](int g, int st, int l) { return drawn.prow.first_id(base + g, st, l); }, a.vocab,
+        [&](int id0, double* x) { drawn.of8(id0, x); });
+    if (threadIdx.x == 0) out[o.L] = tok;
 }
 
 template <sv_dtype DT>
@@ -208,8 +289,14 @@ hipError_t run(const VerifyTruncatedArgs& a, hipStream_t stream) {
     else laws_kernel<DT, 512><<<slots, 512, 0, stream>>>(a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    if (a.vocab < 8) decide_kernel<DT, kWave><<<a.n_req, kWave, 0, stream>>>(a);
-    else decide_kernel<DT, 1024><<<a.n_req, 1024, 0, stream>>>(a);
+    if (a.vocab < 8) {
+        sums_kernel<DT, kWave, 1><<<a.n_req, kWave, 0, stream>>>(a);
+        decide_kernel<DT, kWave, 1><<<a.n_req, kWave, 0, stream>>>(a);
+    } else {
+        constexpr int P = kVerifyParts;
+        sums_kernel<DT, 512, P><<<a.n_req * P, 512, 0, stream>>>(a);
+        decide_kernel<DT, 512, P><<<a.n_req, 512, 0, stream>>>(a);
+    }
     return hipGetLastError();
 }
 

@@ -559,11 +559,11 @@ sv_status sv_sample(const void* logits, int64_t ld, int32_t n_rows, sv_dtype dty
  *          those of sv_verify; a faulty request writes -1 to all its outputs.
  * Numerics: 64 bits up to the outputs; repeated calls agree bit for bit.
  * ws:      sv_verify_truncated_workspace_bytes(n_req, k_max) bytes (a 32-byte
- *          record for each of a request's 2 k_max + 1 row slots), 8-byte
- *          aligned, uninitialised.  Calls that overlap in time must not share
+ *          record for each of a request's 2 k_max + 1 row slots and eight
+ *          sums), 8-byte aligned, uninitialised.  Calls that overlap in time must not share
  *          it.
- * Launch: two kernels: one 512-thread workgroup per row slot, then one of 1024
- * threads per request.
+ * Launch: three kernels of 512-thread workgroups: one per row slot, eight per
+ * request, one per request.
  * Errors: SV_ERR_NULL; SV_ERR_DTYPE; SV_ERR_SHAPE; SV_ERR_WORKSPACE.
  */
 size_t sv_verify_truncated_workspace_bytes(int32_t n_req, int32_t k_max);

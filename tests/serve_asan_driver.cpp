@@ -76,7 +76,7 @@ int main() {
     EXPECT(g_launches == before + 2);
 
     const size_t need = sv_verify_truncated_workspace_bytes(4, 3);
-    EXPECT(need == 4 * 7 * sizeof(sv::LawRecord) && sizeof(sv::LawRecord) == 32);
+    EXPECT(need == 4 * (7 * sizeof(sv::LawRecord) + 64) && sizeof(sv::LawRecord) == 32);
     before = g_launches;
     EXPECT(sv_verify_truncated(F, 10, 8, F, 10, SV_F32, 10, ci, ci, 4, 3, &law, nullptr, 1, 2, mi, mi,
                                mf, mf, mf, mi, F, need - 1, nullptr) == SV_ERR_WORKSPACE);

@@ -52,7 +52,7 @@ def verify(**kw):
 
 
 def test_verify_truncated_refusals():
-    assert sv.sv_verify_truncated_workspace_bytes(4, 3) == 4 * 7 * 32
+    assert sv.sv_verify_truncated_workspace_bytes(4, 3) == 4 * (7 * 32 + 8 * 8)
     for n, k in ((-1, 3), (1, 65), (1, -1), (sv.SV_MAX_VERIFY_SLOTS // 15 + 1, 7)):
         assert sv.sv_verify_truncated_workspace_bytes(n, k) == 0
         assert verify(n_req=n, k_max=k) == sv.SV_ERR_SHAPE
