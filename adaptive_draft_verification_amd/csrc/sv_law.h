@@ -38,6 +38,7 @@ constexpr int kRank = 256;   // candidates ranked by counting
 constexpr int kSteps = 2048; // histogram of the weights, kPerOctave steps for a factor of 2
 constexpr float kPerOctave = 32.0f;
 constexpr double kLog2e64 = 1.4426950408889634074;
+constexpr int kValues = 2048;  // bf16 values of either sign counted by value: 16 octaves
 constexpr int kQueue = 640;  // ids a wave keeps for compact(): 64 left over and 512 of a step
 constexpr float kInf = __builtin_inff();
 constexpr uint32_t kMinusInfKey = 0x007fffffu;
@@ -134,8 +135,13 @@ struct Smem {
     double weight[kRank];
     double prefix[kRank];
     double seg[kMaxSteps];
-    float queue_z[kWaves][kQueue];
-    int queue_id[kWaves][kQueue];
+    union {
+        struct {  // compact()
+            float queue_z[kWaves][kQueue];
+            int queue_id[kWaves][kQueue];
+        };
+        uint32_t value[2 * kValues];  // by_value(): how many ids have each logit
+    };
     unsigned long long hi[256], lo[256];
     uint32_t cnt[256];
     int list_n;
@@ -763,6 +769,166 @@ __device__ __attribute__((noinline)) bool cut_listed(const Row<DT, NT>& row, Sme
     return cut_mass(row, sm, true, w, goal, [](float) { return true; });
 }
 
+// The sum of a bf16 row's weights, and top-p's border, from how many ids have
+// each value: one LDS add an id (8 clocks a wave) where a weight takes 21 fp64
+// operations, then one weight a value (129,280 ids: 24 us for the pass that sums
+// them by id, 7 us this way).  The values counted are the 16 octaves up to the
+// largest magnitude that matters, of either sign; the few ids of smaller ones
+// are listed and ranked; larger negative ones weigh less than 2^-64 and add
+// nothing.  Sets r.total, and for top-p the border and r.n.  False, with nothing
+// decided, where the list does not hold the small ones or the border's ties.
+template <int NT>
+__device__ __forceinline__ bool by_value(const Row<SV_BF16, NT>& row, const Settings& set,
+                                         Smem<NT>& sm, Result& r) {
+    Weigher w = r.w;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    // 2^(-65) of the largest weight lies 45 T below it
+    const float m = (float)w.m, most = fmaxf(fabsf(m), fabsf(m - 45.0f * set.t));
+    if (!(most < 1e38f)) return false;
+    const uint32_t base = (uint32_t)max((int)(__float_as_uint(most) >> 16) + 1 - (kValues - 1), 0);
+    for (int i = threadIdx.x; i < 2 * kValues; i += NT) sm.value[i] = 0;
+    if (threadIdx.x == 0) sm.list_n = 0;
+    __syncthreads();
+    // Bins in descending order of the logit: positive values from the largest
+    // down, then negative ones from the smallest magnitude up.
+    row.granules_of(wave, lane, [&](const typename Row<SV_BF16, NT>::Raw& g, int id0) {
+        bool small = false;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t h = (i & 1) ? g.w[i / 2] >> 16 : g.w[i / 2] & 0xffffu;
+            const uint32_t mag = h & 0x7fffu, at = mag - base;
+            if (at < (uint32_t)kValues)
+                atomicAdd(&sm.value[h >> 15 ? kValues + at : kValues - 1 - at], 1u);
+            small |= mag < base;
+        }
+        if (small) {
+            float z[8];
+            g.unpack(z);
+            const float below = __uint_as_float(base << 16);
+            int c = 0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) c += fabsf(z[e]) < below ? 1 : 0;
+            int at = atomicAdd(&sm.list_n, c);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                if (fabsf(z[e]) < below) {
+                    if (at < kRank) sm.list[at] = entry(order_key(z[e]), id0 + e);
+                    ++at;
+                }
+            }
+        }
+    });
+    __syncthreads();
+    const int small = sm.list_n;
+    if (small > kRank) return false;
+    rank_list(w, sm, small);
+    const double small_mass = small > 0 ? sm.prefix[small - 1] : 0.0;
+    // each thread's share of the bins, and what is ahead of it
+    constexpr int kEach = 2 * kValues / NT;
+    double mass[kEach], own = 0.0;
+    uint32_t cnt[kEach], own_cnt = 0;
+    const auto logit = [&](int o) {
+        const uint32_t mag = base + (uint32_t)(o < kValues ? kValues - 1 - o : o - kValues);
+        return __uint_as_float((mag << 16) | (o < kValues ? 0u : 0x80000000u));
+    };
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        const int o = kEach * (int)threadIdx.x + i;
+        cnt[i] = sm.value[o];
+        mass[i] = cnt[i] ? (double)cnt[i] * w.raw(logit(o)) : 0.0;
+        own += mass[i];
+        own_cnt += cnt[i];
+    }
+    const double incl = wave_incl_sum_dpp(own, lane);
+    const uint32_t incl_cnt = wave_incl_sum_dpp(own_cnt, lane);
+    if (lane == 63) {
+        sm.redd[wave] = incl;
+        sm.red[wave] = incl_cnt;
+    }
+    if (threadIdx.x == 0) sm.first = -1;
+    __syncthreads();
+    double before = incl - own, total = small_mass;
+    uint32_t before_cnt = incl_cnt - own_cnt;
+    for (int v = 0; v < NT / kWave; ++v) {
+        if (v < wave) before += sm.redd[v], before_cnt += sm.red[v];
+        total += sm.redd[v];
+    }
+    r.total = total;
+    if (set.p >= 1.0f) return true;
+    // the border: a value, or one of the small ids
+    const double goal = (double)set.p * total;
+    const bool negative = kEach * (int)threadIdx.x >= kValues;
+    if (negative) before += small_mass, before_cnt += small;
+    double at_mass = 0.0;
+    uint32_t at_cnt = 0;
+    int found = -1;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        if (found < 0 && cnt[i] != 0 && before + mass[i] >= goal) {
+            found = i;
+            at_mass = before;
+            at_cnt = before_cnt;
+        }
+        before += mass[i];
+        before_cnt += cnt[i];
+    }
+    // positive bins end where the small ids begin
+    if (threadIdx.x == kValues / kEach - 1) sm.before.hi = __double_as_longlong(before), sm.cnt[0] = before_cnt;
+    const int thread = first_of(sm, NT, [&](int) { return found >= 0; });
+    const double positive = __longlong_as_double((long long)sm.before.hi);
+    const int in_small = first_of(sm, small, [&](int i) { return positive + sm.prefix[i] >= goal; });
+    if (in_small < small && thread >= kValues / kEach) {
+        w.zc = key_logit(entry_key(sm.sorted[in_small]));
+        w.cid = entry_id(sm.sorted[in_small]);
+        r.n = (int)sm.cnt[0] + in_small + 1;
+        r.total = positive + sm.prefix[in_small];
+    } else {
+        if (thread >= NT) return false;
+        if ((int)threadIdx.x == thread) {
+            uint32_t n = 0;
+            double x = 0.0;
+#pragma unroll
+            for (int i = 0; i < kEach; ++i)
+                if (i == found) n = cnt[i], x = mass[i];
+            const float z = logit(kEach * thread + found);
+            const double one = w.raw(z);
+            double want = one > 0.0 ? ceil((goal - at_mass) / one) : 1.0;
+            want = fmin(fmax(want, 1.0), (double)n);
+            sm.digit = order_key(z);
+            sm.before_cnt = (uint32_t)want;
+            sm.in_cnt = n;
+            sm.first = (int)at_cnt;
+            sm.before.lo = __double_as_longlong(want == (double)n ? at_mass + x : at_mass + want * one);
+        }
+        __syncthreads();
+        const uint32_t want = sm.before_cnt, n = sm.in_cnt;
+        w.zc = key_logit(sm.digit);
+        r.n = sm.first + (int)want;
+        r.total = __longlong_as_double((long long)sm.before.lo);
+        __syncthreads();
+        if (want == n) {
+            w.cid = INT32_MAX;
+        } else {
+            // the want-th lowest id of the border's value
+            if (n > (uint32_t)kRank) return false;
+            if (threadIdx.x == 0) sm.list_n = 0;
+            __syncthreads();
+            compact(row, sm, wave, [&](float z) { return z == w.zc; }, [&](float z, int id) {
+                const int i = atomicAdd(&sm.list_n, 1);
+                if (i < kRank) sm.list[i] = entry(order_key(z), id);
+            });
+            __syncthreads();
+            rank_list(w, sm, (int)n);
+            w.cid = entry_id(sm.sorted[want - 1]);
+        }
+    }
+    w.s = (double)set.s;
+    if (w.raw(w.zc) < w.s) r.n = 0;  // min-p cuts further: summed by the caller
+    r.w = w;
+    r.where = kInRow;
+    return true;
+}
+
 // Top-p alone.  Returns false, with nothing decided, where the ids next to the
 // border do not fit the list.
 template <sv_dtype DT, int NT>
@@ -887,7 +1053,9 @@ __device__ __forceinline__ bool find_nucleus(const Row<DT, NT>& row, const Setti
     return true;
 }
 
-template <sv_dtype DT, int NT>
+// DRAWS: a draw follows, which needs the waves' sums (sm.redd) where the law is
+// found again in the row; without it r.n of a row that nothing cuts is not set.
+template <bool DRAWS, sv_dtype DT, int NT>
 __device__ __forceinline__ Result find_law(const Row<DT, NT>& row, const Settings& set, Smem<NT>& sm) {
     using Raw = typename Row<DT, NT>::Raw;
     // granules of a batch of loads: 128 bytes a lane in flight
@@ -938,10 +1106,17 @@ __device__ __forceinline__ Result find_law(const Row<DT, NT>& row, const Setting
         lb = fmaxf(lb, (float)(z - slack));
     }
     bool decided = false;
-    if (use_p && set.k == 0 && set.t > 0.0f) {
-        decided = find_nucleus<DT, NT>(row, set, sm, r);
-        if (decided && r.n > 0) return r;
-        lb = -kInf;
+    if (set.k == 0 && set.t > 0.0f) {
+        if constexpr (DT == SV_BF16) {
+            // the border, and without a draw everything, by the row's values
+            if (use_p || (!DRAWS && set.s == 0.0f)) decided = by_value(row, set, sm, r);
+            if (decided && !DRAWS && (r.n > 0 || !use_p)) return r;
+        }
+        if (!decided && use_p) {
+            decided = find_nucleus(row, set, sm, r);
+            if (decided && r.n > 0) return r;
+        }
+        if (use_p) lb = -kInf;
     }
     // keep what is left in LDS if it fits
     bool listed = lb > -kInf;

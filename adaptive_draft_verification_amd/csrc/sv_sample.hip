@@ -15,7 +15,7 @@ __global__ __launch_bounds__(NT, NT == kWave ? 1 : 4) void sample_kernel(SampleA
     law::Settings set = law::settings(a.law, i, a.vocab);
     const float u = a.u[i];
     set.bad |= !(u >= 0.0f && u < 1.0f);
-    const law::Result r = law::find_law(row, set, sm);
+    const law::Result r = law::find_law<true>(row, set, sm);
     int tok = -1;
     if (!r.fault) tok = law::draw(row, r, u, sm);
     if (threadIdx.x == 0) {

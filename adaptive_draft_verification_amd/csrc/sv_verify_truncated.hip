@@ -53,7 +53,7 @@ __global__ __launch_bounds__(kLaws, kLaws == kWave ? 1 : 4) void laws_kernel(Ver
     const law::Row<DT, kLaws> row(is_draft ? draft_row<DT>(a, r, j) : target_row<DT>(a, s.lo, j), a.vocab);
     const law::Settings set =
         law::settings(is_draft ? a.draft_law : a.target_law, r, a.vocab);
-    const law::Result res = law::find_law(row, set, sm);
+    const law::Result res = law::find_law<false>(row, set, sm);
     if (threadIdx.x != 0) return;
     LawRecord rec{};
     rec.fault = res.fault;
