@@ -769,15 +769,92 @@ __device__ __attribute__((noinline)) bool cut_listed(const Row<DT, NT>& row, Sme
     return cut_mass(row, sm, true, w, goal, [](float) { return true; });
 }
 
+// Top-p's border among the ids near it, once it is known where to look: side(z)
+// is 0 for logits ahead of it, 1 for those next to it, 2 behind; none of side 0
+// or 1 lies below edge.  Sums the ids ahead by wave, in id order, and gathers,
+// ranks and adds those near.  False, with nothing decided, where these do not
+// fit the list or the border is not among them.
+template <sv_dtype DT, int NT, class Side>
+__device__ __forceinline__ bool finish_nucleus(const Row<DT, NT>& row, const Settings& set,
+                                               Smem<NT>& sm, Result& r, double goal, float edge,
+                                               Side side) {
+    Weigher w = r.w;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    __syncthreads();
+    if (threadIdx.x == 0) sm.list_n = 0;
+    __syncthreads();
+    int n = 0;
+    double part = 0.0;
+    compact(row, sm, wave, [&](float z) { return z >= edge; }, [&](float z, int id) {
+        const int s = side(z);
+        n += __popcll(__ballot(s == 0));
+        if (s == 0) {
+            part += w.raw(z);
+        } else if (s == 1 && z > -kInf) {
+            const int i = atomicAdd(&sm.list_n, 1);
+            if (i < kList) sm.list[i] = entry(order_key(z), id);
+        }
+    });
+    // every lane of a wave holds the wave's count
+    n = block_sum(lane == 0 ? n : 0, sm);
+    const double above = block_sum(part, sm);
+    const int listed = sm.list_n;
+    if (listed > kList || listed == 0 || above >= goal) return false;
+    // the waves' sums, kept over the search
+    double mine = 0.0;
+    if (threadIdx.x < NT / kWave) mine = sm.redd[threadIdx.x];
+    __syncthreads();
+    if (listed <= kRank) {
+        rank_list(w, sm, listed);
+        const int last = first_of(sm, listed, [&](int i) { return above + sm.prefix[i] >= goal; });
+        if (last == listed) return false;
+        w.zc = key_logit(entry_key(sm.sorted[last]));
+        w.cid = entry_id(sm.sorted[last]);
+    } else {
+        Weigher cut = w;
+        if (!cut_listed(row, sm, cut, goal - above)) return false;
+        w = cut;
+    }
+    w.s = (double)set.s;
+    r.w = w;
+    r.where = kInRow;
+    r.n = 0;
+    if (w.raw(w.zc) < w.s) return true;  // min-p cuts further: summed by the caller
+    // the listed ids that stay, added to their waves' sums
+    __syncthreads();
+    if (threadIdx.x < NT / kWave) sm.hi[threadIdx.x] = sm.lo[threadIdx.x] = 0;
+    if (threadIdx.x == 0) sm.second = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < listed; i += NT) {
+        const float z = key_logit(entry_key(sm.list[i]));
+        const int id = entry_id(sm.list[i]);
+        if (!w.above(z, id)) continue;
+        const int v = row.wave_of(id);
+        const Mass q = to_mass(w.raw(z));
+        atomicAdd(&sm.hi[v], q.hi);
+        atomicAdd(&sm.lo[v], q.lo);
+        atomicAdd(&sm.second, 1);
+    }
+    __syncthreads();
+    if (threadIdx.x < NT / kWave)
+        sm.redd[threadIdx.x] = mine + Mass{sm.hi[threadIdx.x], sm.lo[threadIdx.x]}.value();
+    __syncthreads();
+    r.n = n + sm.second;
+    r.total = 0.0;
+    for (int v = 0; v < NT / kWave; ++v) r.total += sm.redd[v];
+    return true;
+}
+
 // The sum of a bf16 row's weights, and top-p's border, from how many ids have
 // each value: one LDS add an id (8 clocks a wave) where a weight takes 21 fp64
 // operations, then one weight a value (129,280 ids: 24 us for the pass that sums
 // them by id, 7 us this way).  The values counted are the 16 octaves up to the
 // largest magnitude that matters, of either sign; the few ids of smaller ones
 // are listed and ranked; larger negative ones weigh less than 2^-64 and add
-// nothing.  Sets r.total, and for top-p the border and r.n.  False, with nothing
-// decided, where the list does not hold the small ones or the border's ties.
-template <int NT>
+// nothing.  Sets r.total, and for top-p the border and r.n; where a draw follows,
+// the waves' sums too (finish_nucleus).  False, with nothing decided, where the
+// list does not hold the small ones or the border's ties.
+template <bool DRAWS, int NT>
 __device__ __forceinline__ bool by_value(const Row<SV_BF16, NT>& row, const Settings& set,
                                          Smem<NT>& sm, Result& r) {
     Weigher w = r.w;
@@ -903,6 +980,11 @@ __device__ __forceinline__ bool by_value(const Row<SV_BF16, NT>& row, const Sett
         __syncthreads();
         const uint32_t want = sm.before_cnt, n = sm.in_cnt;
         w.zc = key_logit(sm.digit);
+        if constexpr (DRAWS) {
+            const float zc = w.zc;
+            return finish_nucleus(row, set, sm, r, goal, zc,
+                                  [zc](float z) { return z > zc ? 0 : 1; });
+        }
         r.n = sm.first + (int)want;
         r.total = __longlong_as_double((long long)sm.before.lo);
         __syncthreads();
@@ -923,7 +1005,8 @@ __device__ __forceinline__ bool by_value(const Row<SV_BF16, NT>& row, const Sett
         }
     }
     w.s = (double)set.s;
-    if (w.raw(w.zc) < w.s) r.n = 0;  // min-p cuts further: summed by the caller
+    // min-p cuts further, or the waves' sums are wanted: summed by the caller
+    if (DRAWS || w.raw(w.zc) < w.s) r.n = 0;
     r.w = w;
     r.where = kInRow;
     return true;
@@ -991,66 +1074,10 @@ __device__ __forceinline__ bool find_nucleus(const Row<DT, NT>& row, const Setti
     const int b1 = sm.first, b2 = sm.second;
     // logits of step b2 or less: at least this one, or a little below
     const float edge = m - (float)(b2 + 1) / per_logit * 1.00001f - fabsf(m) * 1e-6f;
-    int n = 0;
-    part = 0.0;
-    compact(row, sm, wave, [&](float z) { return z >= edge; }, [&](float z, int id) {
+    return finish_nucleus(row, set, sm, r, goal, edge, [&](float z) {
         const int s = step_of(z);
-        n += __popcll(__ballot(s < b1));
-        if (s < b1) {
-            part += w.raw(z);
-        } else if (s <= b2 && z > -kInf) {
-            const int i = atomicAdd(&sm.list_n, 1);
-            if (i < kList) sm.list[i] = entry(order_key(z), id);
-        }
+        return s < b1 ? 0 : s <= b2 ? 1 : 2;
     });
-    // every lane of a wave holds the wave's count
-    n = block_sum(lane == 0 ? n : 0, sm);
-    const double above = block_sum(part, sm);
-    const int listed = sm.list_n;
-    if (listed > kList || listed == 0 || above >= goal) return false;
-    // the waves' sums, kept over the search
-    double mine = 0.0;
-    if (threadIdx.x < NT / kWave) mine = sm.redd[threadIdx.x];
-    __syncthreads();
-    if (listed <= kRank) {
-        rank_list(w, sm, listed);
-        const int last = first_of(sm, listed, [&](int i) { return above + sm.prefix[i] >= goal; });
-        if (last == listed) return false;
-        w.zc = key_logit(entry_key(sm.sorted[last]));
-        w.cid = entry_id(sm.sorted[last]);
-    } else {
-        Weigher cut = w;
-        if (!cut_listed(row, sm, cut, goal - above)) return false;
-        w = cut;
-    }
-    w.s = (double)set.s;
-    r.w = w;
-    r.where = kInRow;
-    r.n = 0;
-    if (w.raw(w.zc) < w.s) return true;  // min-p cuts further: summed by the caller
-    // the listed ids that stay, added to their waves' sums
-    __syncthreads();
-    if (threadIdx.x < NT / kWave) sm.hi[threadIdx.x] = sm.lo[threadIdx.x] = 0;
-    if (threadIdx.x == 0) sm.second = 0;
-    __syncthreads();
-    for (int i = threadIdx.x; i < listed; i += NT) {
-        const float z = key_logit(entry_key(sm.list[i]));
-        const int id = entry_id(sm.list[i]);
-        if (!w.above(z, id)) continue;
-        const int v = row.wave_of(id);
-        const Mass q = to_mass(w.raw(z));
-        atomicAdd(&sm.hi[v], q.hi);
-        atomicAdd(&sm.lo[v], q.lo);
-        atomicAdd(&sm.second, 1);
-    }
-    __syncthreads();
-    if (threadIdx.x < NT / kWave)
-        sm.redd[threadIdx.x] = mine + Mass{sm.hi[threadIdx.x], sm.lo[threadIdx.x]}.value();
-    __syncthreads();
-    r.n = n + sm.second;
-    r.total = 0.0;
-    for (int v = 0; v < NT / kWave; ++v) r.total += sm.redd[v];
-    return true;
 }
 
 // DRAWS: a draw follows, which needs the waves' sums (sm.redd) where the law is
@@ -1109,8 +1136,8 @@ __device__ __forceinline__ Result find_law(const Row<DT, NT>& row, const Setting
     if (set.k == 0 && set.t > 0.0f) {
         if constexpr (DT == SV_BF16) {
             // the border, and without a draw everything, by the row's values
-            if (use_p || (!DRAWS && set.s == 0.0f)) decided = by_value(row, set, sm, r);
-            if (decided && !DRAWS && (r.n > 0 || !use_p)) return r;
+            if (use_p || (!DRAWS && set.s == 0.0f)) decided = by_value<DRAWS>(row, set, sm, r);
+            if (decided && (r.n > 0 || !use_p)) return r;
         }
         if (!decided && use_p) {
             decided = find_nucleus(row, set, sm, r);
