@@ -128,6 +128,7 @@ struct Weigher {
 template <int NT>
 struct Smem {
     static constexpr int kWaves = NT / kWave;
+    static constexpr int kBatches = 8192 / NT;
     static constexpr int kMaxSteps = (SV_MAX_VOCAB + 8) / 8 / NT + 1;  // of a wave's segment
     uint32_t step[kSteps];             // histogram of the weights
     unsigned long long list[kList];    // candidates: key, then ~id: larger is earlier
@@ -141,6 +142,7 @@ struct Smem {
             int queue_id[kWaves][kQueue];
         };
         uint32_t value[2 * kValues];  // by_value(): how many ids have each logit
+        uint16_t batch_top[kBatches][NT];  // pass 1: key of each batch's largest logit
     };
     unsigned long long hi[256], lo[256];
     uint32_t cnt[256];
@@ -268,9 +270,10 @@ struct Row {
     // The wave that holds an id.
     __device__ __forceinline__ int wave_of(int id) const { return (id >> 3) / per; }
     // f(granule, first id) over the calling thread's granules, kAhead loads of
-    // them at a time.  Granules outside the row read as -inf.
-    template <int kAhead, class F>
-    __device__ __forceinline__ void granules(F f) const {
+    // them at a time, done(batch) after each.  Granules outside the row read as
+    // -inf.
+    template <int kAhead, class F, class Done>
+    __device__ __forceinline__ void granules(F f, Done done) const {
         const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
         int s = 0;
         for (; s + kAhead <= steps && !ends_in(wave, s + kAhead - 1); s += kAhead) {
@@ -279,12 +282,13 @@ struct Row {
             for (int i = 0; i < kAhead; ++i) g[i] = fetch(first_id(wave, s + i, lane));
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) f(g[i], first_id(wave, s + i, lane));
+            done(s / kAhead);
         }
 #pragma unroll 1
         for (; s < steps; ++s) {
             const int id0 = first_id(wave, s, lane);
-            if (first_id(wave, s, 0) >= vocab) break;
-            f(raw(id0), id0);
+            if (first_id(wave, s, 0) < vocab) f(raw(id0), id0);
+            if ((s + 1) % kAhead == 0 || s + 1 == steps) done(s / kAhead);
         }
     }
     // f(granule, first id), one granule at a time, the next one in flight; lanes
@@ -376,6 +380,11 @@ struct Extremes<SV_BF16> {
         umax = __builtin_elementwise_max(umax, __builtin_bit_cast(u16x2, w));
         umin = __builtin_elementwise_min(umin, __builtin_bit_cast(u16x2, w));
     }
+    __device__ __forceinline__ void add(const Extremes& o) {
+        smax = __builtin_elementwise_max(smax, o.smax);
+        umax = __builtin_elementwise_max(umax, o.umax);
+        umin = __builtin_elementwise_min(umin, o.umin);
+    }
     __device__ __forceinline__ uint32_t top() const {
         const int s = max(smax.x, smax.y);
         const uint32_t b = s >= 0 ? (uint32_t)s : (uint32_t)min(umin.x, umin.y);
@@ -393,6 +402,11 @@ struct Extremes<SV_F32> {
         smax = max(smax, (int32_t)w);
         umax = max(umax, w);
         umin = min(umin, w);
+    }
+    __device__ __forceinline__ void add(const Extremes& o) {
+        smax = max(smax, o.smax);
+        umax = max(umax, o.umax);
+        umin = min(umin, o.umin);
     }
     __device__ __forceinline__ uint32_t top() const {
         return order_key(__uint_as_float(smax >= 0 ? (uint32_t)smax : umin));
@@ -1090,11 +1104,18 @@ __device__ __forceinline__ Result find_law(const Row<DT, NT>& row, const Setting
     const int lane = threadIdx.x & 63;
     Result r{};
     // pass 1: largest logit, faults
-    Extremes<DT> ex;
-    row.template granules<kAhead>([&](const Raw& g, int) {
+    Extremes<DT> ex, batch;
+    row.template granules<kAhead>(
+        [&](const Raw& g, int) {
 #pragma unroll
-        for (int i = 0; i < 2 * Row<DT, NT>::kBytes; ++i) ex.add(g.w[i]);
-    });
+            for (int i = 0; i < 2 * Row<DT, NT>::kBytes; ++i) batch.add(g.w[i]);
+        },
+        [&](int b) {
+            if (b < Smem<NT>::kBatches)
+                sm.batch_top[b][threadIdx.x] = (uint16_t)(batch.top() >> 16);
+            ex.add(batch);
+            batch = Extremes<DT>{};
+        });
     const uint32_t mine = ex.top();
     const uint32_t top = block_max(mine, sm);
     const int bad = __syncthreads_or(ex.bad());
@@ -1151,11 +1172,15 @@ __device__ __forceinline__ Result find_law(const Row<DT, NT>& row, const Setting
         if (threadIdx.x == 0) sm.list_n = 0;
         __syncthreads();
         // A thread whose own maximum is below the bound has none; the others
-        // look which of their granules do, and read those again.  (Code that is
-        // run once is paid for in instruction fetches: none of it unrolled.)
+        // look at their batches whose maximum is not, which of the granules
+        // hold one, and read those again.  (Code that is run once is paid for
+        // in instruction fetches: none of it unrolled.)
         if (mine >= order_key(lb)) {
             const int wave = threadIdx.x >> 6;
+            const uint32_t least = order_key(lb) >> 16;
             for (int s0 = 0; s0 < row.steps; s0 += kAhead) {
+                const int b = s0 / kAhead;
+                if (b < Smem<NT>::kBatches && sm.batch_top[b][threadIdx.x] < least) continue;
                 unsigned hits = 0;
                 Raw g[kAhead];
 #pragma unroll
