@@ -30,7 +30,8 @@ SV_DEV_BAD_PAGE, SV_DEV_BAD_CTX, SV_DEV_BAD_PARAM = 64, 128, 256
 SV_MAX_BUDGET_SLOTS, SV_MAX_DRAFT, SV_MAX_VOCAB = 8192, 64, 1048576
 SV_MAX_VERIFY_SLOTS = 524288
 SV_NOALLOC_WS_BYTES = 8388608
-SV_MAX_ATTEND_SLOTS, SV_MAX_APPEND_VALUES = 16777216, 1073741824
+SV_MAX_ATTEND_SLOTS, SV_MAX_CONTEXT = 16777215, 2147418112
+SV_MAX_APPEND_VALUES = 1073741824
 SV_MAX_SAMPLE_ROWS = 4194303
 
 EXPORTED = ["sv_status_str", "sv_budget_workspace_bytes", "sv_verify_workspace_bytes",

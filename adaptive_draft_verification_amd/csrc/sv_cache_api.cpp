@@ -23,7 +23,7 @@ sv_status check_cache(const sv_cache* c, int32_t max_pages) {
     if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return SV_ERR_SHAPE;
     if (c->n_pages < 0 || c->page_size < 1 || c->n_kv_heads < 1 || max_pages < 0)
         return SV_ERR_SHAPE;
-    if ((int64_t)max_pages * c->page_size > INT32_MAX) return SV_ERR_SHAPE;
+    if ((int64_t)max_pages * c->page_size > SV_MAX_CONTEXT) return SV_ERR_SHAPE;
     const int64_t per16 = c->dtype == SV_E4M3 ? 16 : 8;
     for (const int64_t s : {c->page_stride, c->token_stride, c->head_stride})
         if (s < 0 || s % per16 != 0) return SV_ERR_SHAPE;
@@ -59,9 +59,10 @@ sv_status check_attend_sizes(int32_t n_req, int32_t k_max, int32_t n_heads, int3
     if (n_req < 0 || k_max < 0 || k_max > SV_MAX_DRAFT) return SV_ERR_SHAPE;
     if (n_kv_heads < 1 || n_heads < n_kv_heads || n_heads % n_kv_heads != 0) return SV_ERR_SHAPE;
     if (head_dim != 64 && head_dim != 128 && head_dim != 256) return SV_ERR_SHAPE;
-    if (capacity < 0 || capacity > INT32_MAX) return SV_ERR_SHAPE;
-    // every grid stays below 2^32 work-items
-    if ((int64_t)n_req * n_heads * (k_max + 1) > SV_MAX_ATTEND_SLOTS) return SV_ERR_SHAPE;
+    if (capacity < 0 || capacity > SV_MAX_CONTEXT) return SV_ERR_SHAPE;
+    // every grid stays below 2^32 work-items, every count of slots in 32 bits
+    if (std::max<int64_t>(n_req, 1) * n_heads * (k_max + 1) > SV_MAX_ATTEND_SLOTS)
+        return SV_ERR_SHAPE;
     return SV_OK;
 }
 

@@ -41,7 +41,9 @@
  *    and return SV_ERR_DATA, launching nothing, where the kernels would set a
  *    dev_error bit for them.  Both make calls synchronous and slow; neither
  *    changes any result.  sv_verify_noalloc honours SV_FORCE_SYNC only (its
- *    contract is to allocate nothing, host memory included).
+ *    contract is to allocate nothing, host memory included), and so do the
+ *    calls of truncated laws and of the paged cache (their kernels check
+ *    every index themselves).
  */
 #ifndef LIBSPECVERIFY_H
 #define LIBSPECVERIFY_H
@@ -596,7 +598,8 @@ sv_status sv_verify_truncated(const void* target_logits, int64_t target_ld, int6
  *               multiple of 16 positions faster).
  * Alignment: k, v and every stride to 16 bytes.
  * page_table:   [n_req, max_pages] int32; entries past a request's positions
- *               are not read.
+ *               are not read.  Requests may share pages (a common prefix) as long
+ *               as none appends to a shared one.
  */
 typedef struct {
     void* k;
@@ -608,7 +611,9 @@ typedef struct {
     const float* v_scale;
 } sv_cache;
 
-#define SV_MAX_ATTEND_SLOTS  16777216   /* n_req * n_heads * (k_max + 1) for sv_cache_attend */
+#define SV_MAX_ATTEND_SLOTS  16777215   /* n_req * n_heads * (k_max + 1) for sv_cache_attend: its grid
+                                           stays below 2^32 work-items */
+#define SV_MAX_CONTEXT       2147418112 /* max_pages * page_size: positions count in 32 bits, a tile past the end included */
 #define SV_MAX_APPEND_VALUES 1073741824 /* n_rows * n_kv_heads * head_dim for sv_cache_append */
 
 /*
@@ -623,7 +628,7 @@ typedef struct {
  * (ties to even), held at +-448; NaN stays NaN.
  * Rows of an unknown request (SV_DEV_BAD_CU_ROWS), past the page table
  * (SV_DEV_BAD_CTX) or with a page id outside [0, n_pages) (SV_DEV_BAD_PAGE)
- * are not written.
+ * are not written.  Of two rows at one place either may be stored.
  * Launch: one kernel, 16 bytes of input a thread.
  * Errors: SV_ERR_NULL; SV_ERR_DTYPE; SV_ERR_SHAPE.
  */
@@ -660,7 +665,7 @@ sv_status sv_cache_append(const sv_cache* cache, const int32_t* page_table, int3
  *          NULL will do), uninitialised.  Calls that overlap in time must not
  *          share it.
  * Launch: one kernel, four waves for each request, kv head, block of up to 64
- * query slots and part of the length; a second one merges the parts if there
+ * query slots (16 at head_dim 256) and part of the length; a second one merges the parts if there
  * are several (few requests, long tables).
  * Errors: SV_ERR_NULL; SV_ERR_DTYPE; SV_ERR_SHAPE; SV_ERR_VALUE (scale not
  * finite); SV_ERR_WORKSPACE.

@@ -188,3 +188,23 @@ def test_serving_host_side_under_sanitizers(tmp_path):
     run = subprocess.run([str(exe)], capture_output=True, text=True, env=env, timeout=120)
     assert run.returncode == 0, run.stdout[-2000:] + run.stderr[-4000:]
     assert "serving checks passed" in run.stdout
+
+
+def test_cache_sizes_at_the_limits():
+    f = sv.sv_cache_attend_workspace_bytes
+    heads = sv.SV_MAX_ATTEND_SLOTS + 1
+    assert heads * 256 == 2 ** 32   # one workgroup a slot would pass a grid's limit
+    for kw in (dict(n_req=heads, k_max=0, n_heads=2), dict(n_req=heads // 4, k_max=0),
+               dict(n_req=1, k_max=0, n_heads=heads, q_ld=64 * heads, out_ld=64 * heads)):
+        assert attend(**kw) == sv.SV_ERR_SHAPE, kw
+    # no request, but sizes whose product passes 32 bits
+    assert f(0, 64, 2 ** 31 - 1, 1, 64, 4, 16) == 0
+    assert attend(cache(n_kv_heads=1), n_req=0, k_max=64, n_heads=2 ** 31 - 1) == sv.SV_ERR_SHAPE
+    # positions and a tile past the last one count in 32 bits
+    assert sv.SV_MAX_CONTEXT + 65536 == 2 ** 31
+    pages = sv.SV_MAX_CONTEXT // 16
+    assert f(1, 0, 1, 1, 64, pages, 16) > 0
+    assert f(1, 0, 1, 1, 64, pages + 1, 16) == 0
+    assert attend(max_pages=pages) == sv.SV_ERR_WORKSPACE
+    assert attend(max_pages=pages + 1) == sv.SV_ERR_SHAPE
+    assert append(max_pages=pages + 1) == sv.SV_ERR_SHAPE
