@@ -157,11 +157,11 @@ __device__ __forceinline__ bool bf16_pair_nonfinite(uint32_t w) {
 
 template <int D, bool F8, int MT, bool PG16>
 struct Attend {
-    // blocks of 32 positions a wave takes at once: 16 KB of keys and values in
-    // flight a wave where the registers allow it
-    static constexpr int kBlocks = MT == 4 ? 1 : 1;
-    static constexpr int kTile = 32 * kBlocks;
-    static constexpr int kHalves = 2 * kBlocks;  // of 16 positions
+    // Positions a wave takes at once: 16 KB of keys and values in flight a wave
+    // at 128 two-byte dims.  64 positions spill (MT = 4) or lose the second
+    // wave of a SIMD: no faster anywhere.
+    static constexpr int kTile = 32;
+    static constexpr int kHalves = 2;  // of 16 positions
     static constexpr int kWaves = 4;
     static constexpr int kSteps = D / 32;   // products a 16-position score needs
     static constexpr int kKLoads = F8 ? D / 64 : D / 32;  // 16-byte loads of a key row's share
@@ -169,9 +169,8 @@ struct Attend {
     static constexpr int kVWords = F8 ? kDpl / 4 : kDpl / 2;
     static constexpr int kAcc = D / 4;      // accumulators a slot tile and lane
     static constexpr int kEsize = F8 ? 1 : 2;
-    // waves a SIMD has registers for; two sets of value registers where they fit
+    // waves a SIMD has registers for without spilling
     static constexpr int kOccupancy = D < 256 && MT * D <= 256 ? 2 : 1;
-    static constexpr bool kTwoV = false;
 
     union Smem {
         int lens[256];
@@ -188,7 +187,7 @@ struct Attend {
 // The request of rank `rank` by context length, longest first (ties to the
 // lower request), for up to 256 requests: where workgroups take turns on the
 // CUs, a long request that starts last would be waited for alone (256 requests
-// of 0 .. 4096 positions: 429 us in their own order, 398 this way).
+// of 0 .. 4096 positions: 429 us in their own order, 394 this way).
 __device__ __forceinline__ int longest(int rank, const int32_t* ctx_len, int n, int* lens) {
     __shared__ int found;
     const int t = threadIdx.x;
@@ -295,8 +294,9 @@ void attend_kernel(AttendArgs a) {
         Words<C::kVWords> r[4 * C::kHalves];
         uint32_t ok;  // bit j: the page of the lane's j-th position is good
     };
-    // Issues a tile's loads: keys first, then values.
-    auto load = [&](int t0, Ids ids, Values* v, bool keys) __attribute__((always_inline)) {
+    Values vals;
+    // Issues a tile's loads of keys or of values.
+    auto load = [&](int t0, Ids ids, bool keys) __attribute__((always_inline)) {
         if (PG16) {
             const char* at[C::kHalves];
             uint32_t ok = 0;
@@ -319,10 +319,10 @@ void attend_kernel(AttendArgs a) {
                     for (int i = 0; i < C::kKLoads; ++i)
                         kr[u][i] = load_words<4>(at[u] + (koff + i * 64));
             } else {
-                v->ok = ok;
+                vals.ok = ok;
 #pragma unroll
                 for (int j = 0; j < 4 * C::kHalves; ++j)
-                    v->r[j] = load_words<C::kVWords>(at[j >> 2] +
+                    vals.r[j] = load_words<C::kVWords>(at[j >> 2] +
                                                      (voff + (uint32_t)((j & 3) * tstride)));
             }
         } else if (keys) {
@@ -335,13 +335,13 @@ void attend_kernel(AttendArgs a) {
                     kr[u][i] = load_words<4>(at + (i * 64 + g * 16));
             }
         } else {
-            v->ok = 0;
+            vals.ok = 0;
 #pragma unroll
             for (int j = 0; j < 4 * C::kHalves; ++j) {
                 bool ok;
                 const char* at = vbase + row_offset(t0 + 16 * (j >> 2) + g * 4 + (j & 3), ok);
-                v->ok |= ok ? 1u << j : 0u;
-                v->r[j] = load_words<C::kVWords>(at + col * C::kDpl * C::kEsize);
+                vals.ok |= ok ? 1u << j : 0u;
+                vals.r[j] = load_words<C::kVWords>(at + col * C::kDpl * C::kEsize);
             }
         }
     };
@@ -349,12 +349,11 @@ void attend_kernel(AttendArgs a) {
     // the first tile's loads go out before anything else is done
     const int stride = C::kWaves * C::kTile;
     int t0 = begin + wave * C::kTile;
-    Values va, vb;
     Ids ids{};
     if (t0 < end) {
         if (PG16) ids = look_up(t0);
-        load(t0, ids, nullptr, true);
-        load(t0, ids, &va, false);
+        load(t0, ids, true);
+        load(t0, ids, false);
         if (PG16) ids = look_up(min(t0 + stride, len - 1));
     }
 
@@ -392,9 +391,9 @@ void attend_kernel(AttendArgs a) {
     }
     int bad = 0;
 
-    auto tile = [&](Values& now, Values& next) __attribute__((always_inline)) {
+    while (t0 < end) {
         constexpr int U = C::kHalves, J = 4 * U;  // halves; positions a lane holds
-        constexpr uint32_t kAllOk = J == 32 ? ~0u : (1u << J) - 1;
+        constexpr uint32_t kAllOk = (1u << J) - 1;
         f32x4 s[MT][U];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
@@ -425,8 +424,10 @@ void attend_kernel(AttendArgs a) {
                         __builtin_amdgcn_mfma_f32_16x16x32_bf16(k8[u], q8, s[mt][u], 0, 0, 0);
             }
         }
-        // the next tile's loads, in flight over the softmax and the product
-        // with the values (the scores are taken first: the keys' registers)
+        // the next tile's keys, in flight over the softmax and the product with
+        // the values (the scores are taken first: the keys' registers); its
+        // values follow the product, into the same registers.  A second set of
+        // value registers spills: 445 us of 256 requests against 394.
         const int t1 = t0 + stride;
         const bool more = t1 < end;
         const Ids ids1 = ids;
@@ -435,8 +436,7 @@ void attend_kernel(AttendArgs a) {
 #pragma unroll
             for (int u = 0; u < U; ++u) asm volatile("" : "+v"(s[mt][u]));
         if (more) {
-            load(t1, ids1, nullptr, true);
-            if (C::kTwoV) load(t1, ids1, &next, false);
+            load(t1, ids1, true);
             if (PG16) ids = look_up(min(t1 + stride, len - 1));
         }
         __builtin_amdgcn_sched_barrier(0);
@@ -445,30 +445,30 @@ void attend_kernel(AttendArgs a) {
         // the end, or on a bad page, by none: their values are zeroed, since 0
         // times what lies there may be NaN.  A value that is not finite behind
         // the context poisons the product for the rows that do not see it.
-        if (now.ok != kAllOk) bad = 1;
-        const bool edge = t0 + C::kTile > ctx || __ballot(now.ok != kAllOk) != 0;
+        if (vals.ok != kAllOk) bad = 1;
+        const bool edge = t0 + C::kTile > ctx || __ballot(vals.ok != kAllOk) != 0;
         bool poison = false;
         if (edge) {
 #pragma unroll
             for (int j = 0; j < J; ++j) {
                 const int t = t0 + 16 * (j >> 2) + g * 4 + (j & 3);
-                const bool in = t < len && ((now.ok >> j) & 1);
+                const bool in = t < len && ((vals.ok >> j) & 1);
                 bool nf = false;
 #pragma unroll
                 for (int i = 0; i < C::kVWords; ++i) {
-                    if (!in) now.r[j].w[i] = 0;
+                    if (!in) vals.r[j].w[i] = 0;
                     if (F8) {
-                        nf |= bf16_pair_nonfinite(e4m3_pair<false>(now.r[j].w[i])) ||
-                              bf16_pair_nonfinite(e4m3_pair<true>(now.r[j].w[i]));
+                        nf |= bf16_pair_nonfinite(e4m3_pair<false>(vals.r[j].w[i])) ||
+                              bf16_pair_nonfinite(e4m3_pair<true>(vals.r[j].w[i]));
                     } else {
-                        nf |= bf16_pair_nonfinite(now.r[j].w[i]);
+                        nf |= bf16_pair_nonfinite(vals.r[j].w[i]);
                     }
                 }
                 poison |= nf && t > ctx;
             }
             poison = __ballot(poison) != 0;
         }
-        bf16x8 pb[MT][C::kBlocks];
+        bf16x8 pb[MT];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
             if (mt * 16 >= slots) break;
@@ -479,7 +479,7 @@ void attend_kernel(AttendArgs a) {
 #pragma unroll
                 for (int j = 0; j < J; ++j) {
                     const int t = t0 + 16 * (j >> 2) + g * 4 + (j & 3);
-                    if (t > last[mt] || !((now.ok >> j) & 1)) p[j] = -kInf;
+                    if (t > last[mt] || !((vals.ok >> j) & 1)) p[j] = -kInf;
                 }
             }
             float mx = p[0];
@@ -506,11 +506,8 @@ void attend_kernel(AttendArgs a) {
             }
             // weights rounded to bf16 for the matrix product: at most 2^-8 of
             // each, as far as the output's own rounding
-#pragma unroll
-            for (int b = 0; b < C::kBlocks; ++b)
-                pb[mt][b] =
-                    as_bf16x8(pack_bf16(p[8 * b], p[8 * b + 1]), pack_bf16(p[8 * b + 2], p[8 * b + 3]),
-                              pack_bf16(p[8 * b + 4], p[8 * b + 5]), pack_bf16(p[8 * b + 6], p[8 * b + 7]));
+            pb[mt] = as_bf16x8(pack_bf16(p[0], p[1]), pack_bf16(p[2], p[3]),
+                               pack_bf16(p[4], p[5]), pack_bf16(p[6], p[7]));
             if (poison) {
                 // position by position, each row only what it sees
                 for (int gg = 0; gg < 4; ++gg) {
@@ -540,48 +537,35 @@ void attend_kernel(AttendArgs a) {
         if (!poison) {
 #pragma unroll
             for (int i2 = 0; i2 < C::kDpl / 2; ++i2) {
+                uint32_t w[8];  // dims 2 i2 and 2 i2 + 1 of the lane's 8 positions
 #pragma unroll
-                for (int b = 0; b < C::kBlocks; ++b) {
-                    uint32_t w[8];  // dims 2 i2 and 2 i2 + 1 of the block's 8 positions
+                for (int j = 0; j < 8; ++j) {
+                    const Words<C::kVWords>& v = vals.r[j];
+                    if (F8)
+                        w[j] = (i2 & 1) ? e4m3_pair<true>(v.w[i2 / 2])
+                                        : e4m3_pair<false>(v.w[i2 / 2]);
+                    else
+                        w[j] = v.w[F8 ? 0 : i2];
+                }
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const Words<C::kVWords>& v = now.r[8 * b + j];
-                        if (F8)
-                            w[j] = (i2 & 1) ? e4m3_pair<true>(v.w[i2 / 2])
-                                            : e4m3_pair<false>(v.w[i2 / 2]);
-                        else
-                            w[j] = v.w[F8 ? 0 : i2];
-                    }
+                for (int half = 0; half < 2; ++half) {
+                    const uint32_t sel = half ? 0x07060302u : 0x05040100u;
+                    const bf16x8 vt = as_bf16x8(__builtin_amdgcn_perm(w[1], w[0], sel),
+                                                __builtin_amdgcn_perm(w[3], w[2], sel),
+                                                __builtin_amdgcn_perm(w[5], w[4], sel),
+                                                __builtin_amdgcn_perm(w[7], w[6], sel));
+                    const int i = 2 * i2 + half;
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        const uint32_t sel = half ? 0x07060302u : 0x05040100u;
-                        const bf16x8 vt = as_bf16x8(__builtin_amdgcn_perm(w[1], w[0], sel),
-                                                    __builtin_amdgcn_perm(w[3], w[2], sel),
-                                                    __builtin_amdgcn_perm(w[5], w[4], sel),
-                                                    __builtin_amdgcn_perm(w[7], w[6], sel));
-                        const int i = 2 * i2 + half;
-#pragma unroll
-                        for (int mt = 0; mt < MT; ++mt) {
-                            if (mt * 16 >= slots) break;
-                            acc[mt][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                                vt, pb[mt][b], acc[mt][i], 0, 0, 0);
-                        }
+                    for (int mt = 0; mt < MT; ++mt) {
+                        if (mt * 16 >= slots) break;
+                        acc[mt][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vt, pb[mt],
+                                                                             acc[mt][i], 0, 0, 0);
                     }
                 }
             }
         }
-        if (!C::kTwoV && more) load(t1, ids1, &next, false);
+        if (more) load(t1, ids1, false);
         t0 = t1;
-    };
-
-    if (C::kTwoV) {
-        while (t0 < end) {
-            tile(va, vb);
-            if (t0 >= end) break;
-            tile(vb, va);
-        }
-    } else {
-        while (t0 < end) tile(va, va);
     }
     if (__ballot(bad) != 0 && lane == 0) raise_error(a.dev_error, SV_DEV_BAD_PAGE);
 

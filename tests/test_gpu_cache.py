@@ -385,3 +385,38 @@ def test_attend_many_workgroups(n, heads, kv, dim, dtype):
     ctx = [int(x) for x in rng.integers(0, 60, n)]
     ctx[3], ctx[n // 2] = 700, 700
     Batch(30 + n, rows, ctx, heads, kv, dim, 16, dtype, k_max=2).device().check()
+
+
+@pytest.mark.parametrize("dtype", [BF, F8])
+def test_attend_requests_that_share_pages(dtype):
+    """A common prefix: the requests' tables hold the same pages, and one page twice."""
+    b = Batch(41, [2, 1, 3], [40, 63, 20], 8, 2, 128, 16, dtype)
+    b.table[1, :2] = b.table[0, :2]
+    b.table[2, :2] = b.table[0, :2]
+    b.table[2, 0] = b.table[2, 1]
+    b.device().check()
+
+
+def test_attend_two_calls_at_once():
+    """Two streams, each with a workspace of its own, their launches interleaved."""
+    b = Batch(42, [2, 1], [9000, 4000], 8, 2, 128, 16).device()
+    q, table, cu, ctx = b.q.cuda(), b.table.cuda(), b.cu.cuda(), b.ctx.cuda()
+    want, want_lse, _ = b.attend()
+    streams, outs = [torch.cuda.Stream() for _ in range(2)], []
+    torch.cuda.synchronize()
+    for i in range(8):
+        outs.append((torch.zeros_like(q), torch.zeros(q.shape[:2], device="cuda"), b.ws()))
+    torch.cuda.synchronize()
+    for i, (out, lse, ws) in enumerate(outs):
+        sv.sv_cache_attend(b.cache, table, q, cu, ctx, b.k_max, b.scale, out, ws, lse,
+                           stream=streams[i % 2])
+    torch.cuda.synchronize()
+    rows = int(b.cu[-1])
+    for out, lse, _ in outs:
+        assert torch.equal(out[:rows], want[:rows]) and torch.equal(lse[:rows], want_lse[:rows])
+
+
+def test_attend_head_groups_wider_than_a_block():
+    """More query slots than one workgroup takes, at 256 dims and at 64."""
+    Batch(43, [5, 1], [70, 3], 24, 1, 256, 16).device().check()
+    Batch(44, [9, 2], [70, 3], 24, 1, 64, 16, F8).device().check()

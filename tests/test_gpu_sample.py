@@ -357,3 +357,53 @@ def test_verify_truncated_repeats_and_graph():
         g = run_verify(case[0].roll(i, 1), case[1].roll(i, 1), *case[2:], V, 5, 2)
         np.testing.assert_array_equal(out.cpu().numpy(), g["tokens"])
         np.testing.assert_array_equal(acc.cpu().numpy(), g["accepted"])
+
+
+def odd_rows(V, seed):
+    """Logit rows of many shapes, every border of top-p and min-p among them somewhere odd."""
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(V, generator=g)
+    ninf = float("-inf")
+    at = torch.arange(V)
+    tiny = torch.full((V,), -8.0)
+    tiny[:50] = 4.0
+    tiny[1000:1100] = x[1000:1100] * 1e-6      # 100 ids next to 0, ...
+    many = tiny.clone()
+    many[1000:1600] = x[1000:1600] * 1e-6      # ... and more than a list of 256 holds
+    return torch.stack([
+        x.sort().values * 4, x.sort(descending=True).values * 4, x * 1e-3, x * 300, x - 5000,
+        x * 1e-30, torch.zeros(V), torch.full((V,), -77.0), x * 1e30, -x.abs() * 1e-3 - 1e3,
+        torch.where(at == V - 1, 80.0, x), torch.where(at % 2 == 0, ninf, 1.0) + 0.0 * x,
+        torch.where(at == 17, 3.0, ninf), (x * 2).round(), (x * 2).round() * 0.5 - 3, tiny, many,
+        torch.where(at % 3 == 0, -0.0, 0.0), torch.where(at < 700, 5.0, x)])
+
+
+ODD_SETTINGS = [(1.0, 0, 1.0, 0.0), (0.7, 0, 0.9, 0.0), (1.0, 0, 0.8233, 0.0), (1.5, 0, 0.3, 0.01),
+                (1e-3, 0, 0.999, 0.0), (40.0, 0, 0.6, 0.0), (1.0, 0, 1.0, 0.2),
+                (0.9, 300, 0.95, 0.0)]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_sample_odd_rows(dtype):
+    z = odd_rows(9001, 51).to(dtype).cuda()
+    g = torch.Generator().manual_seed(52)
+    for s in ODD_SETTINGS:
+        check_sample(z, torch.rand(len(z), generator=g).tolist(), [s] * len(z))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("s", ODD_SETTINGS)
+def test_verify_truncated_odd_rows(dtype, s):
+    """Each row as a target against another as its draft, one draft a request."""
+    V = 9001
+    z = odd_rows(V, 53).to(dtype)
+    n = len(z)
+    target = z.repeat_interleave(2, 0).clone()
+    target[1::2] = z.roll(1, 0)                 # the bonus rows
+    draft = z.roll(3, 0).clone()
+    draft[::2] = z[::2]                         # every other draft's law is the target's
+    u = torch.rand(n, generator=torch.Generator().manual_seed(54))
+    toks = np.array([[sample_row(draft[r].float().numpy(), float(u[r]), *s)[0]]
+                     for r in range(n)], np.int32)
+    cu = np.arange(0, 2 * n + 1, 2, dtype=np.int32)
+    check_verify((target, draft, toks, cu, [s] * n, [s] * n), V, 55, 6)
