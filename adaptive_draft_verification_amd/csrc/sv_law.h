@@ -876,7 +876,8 @@ __device__ __forceinline__ bool by_value(const Row<SV_BF16, NT>& row, const Sett
     // 2^(-65) of the largest weight lies 45 T below it
     const float m = (float)w.m, most = fmaxf(fabsf(m), fabsf(m - 45.0f * set.t));
     if (!(most < 1e38f)) return false;
-    const uint32_t base = (uint32_t)max((int)(__float_as_uint(most) >> 16) + 1 - (kValues - 1), 0);
+    // at least 1: 0 and -0 are one logit, and in the list they are
+    const uint32_t base = (uint32_t)max((int)(__float_as_uint(most) >> 16) + 1 - (kValues - 1), 1);
     for (int i = threadIdx.x; i < 2 * kValues; i += NT) sm.value[i] = 0;
     if (threadIdx.x == 0) sm.list_n = 0;
     __syncthreads();

@@ -407,3 +407,17 @@ def test_verify_truncated_odd_rows(dtype, s):
                      for r in range(n)], np.int32)
     cu = np.arange(0, 2 * n + 1, 2, dtype=np.int32)
     check_verify((target, draft, toks, cu, [s] * n, [s] * n), V, 55, 6)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_zeros_of_both_signs_at_a_tiny_temperature(dtype):
+    """0 and -0 are one logit: ties between them go by id, whatever the temperature."""
+    V, n = 200, 3
+    z = torch.zeros(n, V)
+    z[:, ::2] = -0.0
+    z = z.to(dtype)
+    s = [(2e-38, 0, 0.25, 0.0), (2e-38, 0, 0.5, 0.0), (1.0, 0, 0.5, 0.0)]
+    check_sample(z.cuda(), [0.0, TOP_U, 0.5], s)
+    toks = np.array([[10], [99], [60]], np.int32)
+    cu = np.arange(0, 2 * n + 1, 2, dtype=np.int32)
+    check_verify((z.repeat_interleave(2, 0), z.clone(), toks, cu, s, s), V, 57, 1)
