@@ -141,7 +141,7 @@ struct Smem {
             float queue_z[kWaves][kQueue];
             int queue_id[kWaves][kQueue];
         };
-        uint32_t value[2 * kValues];  // by_value(): how many ids have each logit
+        uint32_t value[2 * kValues + kWave];  // by_value(): how many ids have each logit
         uint16_t batch_top[kBatches][NT];  // pass 1: key of each batch's largest logit
     };
     unsigned long long hi[256], lo[256];
@@ -269,27 +269,42 @@ struct Row {
     }
     // The wave that holds an id.
     __device__ __forceinline__ int wave_of(int id) const { return (id >> 3) / per; }
-    // f(granule, first id) over the calling thread's granules, kAhead loads of
-    // them at a time, done(batch) after each.  Granules outside the row read as
-    // -inf.
+    // The same granules dealt to the threads in turn, for passes whose order
+    // does not matter.
+    __device__ __forceinline__ int turn_id(int s) const {
+        return (s * NT + (int)threadIdx.x) * 8;
+    }
+    __device__ __forceinline__ int turns() const { return (vocab + 8 * NT - 1) / (8 * NT); }
+    // f(granule, first id) over the granules dealt to the calling thread, kAhead
+    // loads of them at a time, done(batch) after each.  Granules outside the row
+    // read as -inf.
     template <int kAhead, class F, class Done>
     __device__ __forceinline__ void granules(F f, Done done) const {
-        const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+        const int n = turns();
         int s = 0;
-        for (; s + kAhead <= steps && !ends_in(wave, s + kAhead - 1); s += kAhead) {
+        for (; (s + kAhead) * NT * 8 <= vocab; s += kAhead) {
             Raw g[kAhead];
 #pragma unroll
-            for (int i = 0; i < kAhead; ++i) g[i] = fetch(first_id(wave, s + i, lane));
+            for (int i = 0; i < kAhead; ++i) g[i] = fetch(turn_id(s + i));
 #pragma unroll
-            for (int i = 0; i < kAhead; ++i) f(g[i], first_id(wave, s + i, lane));
+            for (int i = 0; i < kAhead; ++i) f(g[i], turn_id(s + i));
             done(s / kAhead);
         }
-#pragma unroll 1
-        for (; s < steps; ++s) {
-            const int id0 = first_id(wave, s, lane);
-            if (first_id(wave, s, 0) < vocab) f(raw(id0), id0);
-            if ((s + 1) % kAhead == 0 || s + 1 == steps) done(s / kAhead);
+        if (s >= n) return;
+        // the last batch, its loads in flight together too (taken one by one
+        // they cost a pass over 129,280 ids a third of its time)
+        const int end = vocab & ~7;
+        Raw g[kAhead], part = fetch(end);
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) g[i] = fetch(turn_id(s + i));
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            if (turn_id(s + i) < end) f(g[i], turn_id(s + i));
+        if (end < vocab && (int)threadIdx.x == end / 8 % NT) {
+            settle(part, end);
+            f(part, end);
         }
+        done(s / kAhead);
     }
     // f(granule, first id), one granule at a time, the next one in flight; lanes
     // whose granule is outside the row take part with logits of -inf
@@ -307,10 +322,14 @@ struct Row {
             id0 = id1;
         }
     }
+    template <class F>
+    __device__ __forceinline__ void each_granule(F f) const {
+        granules_of(threadIdx.x >> 6, threadIdx.x & 63, f);
+    }
     // f(logit, id) over the calling thread's ids
     template <class F>
     __device__ __forceinline__ void each(F f) const {
-        granules_of(threadIdx.x >> 6, threadIdx.x & 63, [&](const Raw& g, int id0) {
+        each_granule([&](const Raw& g, int id0) {
             float z[8];
             g.unpack(z);
 #pragma unroll
@@ -859,63 +878,108 @@ __device__ __forceinline__ bool finish_nucleus(const Row<DT, NT>& row, const Set
     return true;
 }
 
+// by_value() counts the 16 octaves of magnitude up to `most`, of either sign,
+// from this bf16 magnitude on.  At least 1: 0 and -0 are one logit, and in the
+// list of smaller ones they are.
+__device__ __forceinline__ uint32_t value_base(float most) {
+    return (uint32_t)max((int)(__float_as_uint(most) >> 16) + 1 - (kValues - 1), 1);
+}
+// The largest magnitude that matters: 2^(-65) of the largest weight lies 45 T
+// below it.
+__device__ __forceinline__ float value_reach(float m, float t) {
+    return fmaxf(fabsf(m), fabsf(m - 45.0f * t));
+}
+
+template <int NT>
+__device__ __forceinline__ void clear_values(Smem<NT>& sm) {
+    for (int i = threadIdx.x; i < 2 * kValues; i += NT) sm.value[i] = 0;
+    if (threadIdx.x == 0) sm.list_n = 0;
+    __syncthreads();
+}
+
+// Counts a granule's values, positive ones by magnitude and behind them negative
+// ones (values out of range behind both, a place for each lane), and lists the
+// ids of magnitudes below the range.
+template <int NT>
+__device__ __forceinline__ void count_values(const typename Row<SV_BF16, NT>::Raw& g, int id0,
+                                             Smem<NT>& sm, uint32_t base) {
+    const uint32_t out = 2 * kValues + (threadIdx.x & 63);
+    u16x2 least{0xffff, 0xffff};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t mags = g.w[i] & 0x7fff7fffu;
+        least = __builtin_elementwise_min(least, __builtin_bit_cast(u16x2, mags));
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const uint32_t at = (half ? mags >> 16 : mags & 0xffffu) - base;
+            const uint32_t negative = (g.w[i] >> (half ? 31 : 15)) & 1u;
+            atomicAdd(&sm.value[at < (uint32_t)kValues ? at + negative * kValues : out], 1u);
+        }
+    }
+    if (min(least.x, least.y) >= base) return;
+    float z[8];
+    g.unpack(z);
+    const float below = __uint_as_float(base << 16);
+    int c = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) c += fabsf(z[e]) < below ? 1 : 0;
+    int at = atomicAdd(&sm.list_n, c);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        if (fabsf(z[e]) < below) {
+            if (at < kRank) sm.list[at] = entry(order_key(z[e]), id0 + e);
+            ++at;
+        }
+    }
+}
+
+// The want-th lowest of the listed ids; not inlined (rarely needed).
+template <int NT>
+__device__ __attribute__((noinline)) int nth_id(Smem<NT>& sm, uint32_t want) {
+    return (int)descend<false>(
+               sm,
+               [&](auto fn) {
+                   for (int i = threadIdx.x; i < sm.list_n; i += NT)
+                       fn((uint32_t)entry_id(sm.list[i]), [] { return 0.0; });
+               },
+               16, 0, want, 0.0, false).ord;
+}
+
 // The sum of a bf16 row's weights, and top-p's border, from how many ids have
 // each value: one LDS add an id (8 clocks a wave) where a weight takes 21 fp64
 // operations, then one weight a value (129,280 ids: 24 us for the pass that sums
 // them by id, 7 us this way).  The values counted are the 16 octaves up to the
 // largest magnitude that matters, of either sign; the few ids of smaller ones
 // are listed and ranked; larger negative ones weigh less than 2^-64 and add
-// nothing.  Sets r.total, and for top-p the border and r.n; where a draw follows,
-// the waves' sums too (finish_nucleus).  False, with nothing decided, where the
-// list does not hold the small ones or the border's ties.
+// nothing.  base: where the values that pass 1 counted begin, 0 if it counted
+// none; they are counted again if they do not reach far enough.  Sets r.total,
+// and for top-p the border and r.n; where a draw follows, the waves' sums too
+// (finish_nucleus).  False, with nothing decided, where the list does not hold
+// the small ones or the border's ties.
 template <bool DRAWS, int NT>
 __device__ __forceinline__ bool by_value(const Row<SV_BF16, NT>& row, const Settings& set,
-                                         Smem<NT>& sm, Result& r) {
+                                         Smem<NT>& sm, Result& r, uint32_t base) {
     Weigher w = r.w;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    // 2^(-65) of the largest weight lies 45 T below it
-    const float m = (float)w.m, most = fmaxf(fabsf(m), fabsf(m - 45.0f * set.t));
+    const float most = value_reach((float)w.m, set.t);
     if (!(most < 1e38f)) return false;
-    // at least 1: 0 and -0 are one logit, and in the list they are
-    const uint32_t base = (uint32_t)max((int)(__float_as_uint(most) >> 16) + 1 - (kValues - 1), 1);
-    for (int i = threadIdx.x; i < 2 * kValues; i += NT) sm.value[i] = 0;
-    if (threadIdx.x == 0) sm.list_n = 0;
-    __syncthreads();
-    // Bins in descending order of the logit: positive values from the largest
-    // down, then negative ones from the smallest magnitude up.
-    row.granules_of(wave, lane, [&](const typename Row<SV_BF16, NT>::Raw& g, int id0) {
-        bool small = false;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t h = (i & 1) ? g.w[i / 2] >> 16 : g.w[i / 2] & 0xffffu;
-            const uint32_t mag = h & 0x7fffu, at = mag - base;
-            if (at < (uint32_t)kValues)
-                atomicAdd(&sm.value[h >> 15 ? kValues + at : kValues - 1 - at], 1u);
-            small |= mag < base;
-        }
-        if (small) {
-            float z[8];
-            g.unpack(z);
-            const float below = __uint_as_float(base << 16);
-            int c = 0;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) c += fabsf(z[e]) < below ? 1 : 0;
-            int at = atomicAdd(&sm.list_n, c);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                if (fabsf(z[e]) < below) {
-                    if (at < kRank) sm.list[at] = entry(order_key(z[e]), id0 + e);
-                    ++at;
-                }
-            }
-        }
-    });
-    __syncthreads();
+    const uint32_t exact = value_base(most);
+    if (base < exact || (base > exact && sm.list_n > kRank)) {
+        base = exact;
+        __syncthreads();
+        clear_values(sm);
+        row.each_granule([&](const typename Row<SV_BF16, NT>::Raw& g, int id0) {
+            count_values(g, id0, sm, base);
+        });
+        __syncthreads();
+    }
     const int small = sm.list_n;
     if (small > kRank) return false;
     rank_list(w, sm, small);
     const double small_mass = small > 0 ? sm.prefix[small - 1] : 0.0;
-    // each thread's share of the bins, and what is ahead of it
+    // each thread's share of the values, in descending order (positive ones from
+    // the largest down, then negative ones from the smallest magnitude up), and
+    // what is ahead of it
     constexpr int kEach = 2 * kValues / NT;
     double mass[kEach], own = 0.0;
     uint32_t cnt[kEach], own_cnt = 0;
@@ -926,7 +990,7 @@ __device__ __forceinline__ bool by_value(const Row<SV_BF16, NT>& row, const Sett
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
         const int o = kEach * (int)threadIdx.x + i;
-        cnt[i] = sm.value[o];
+        cnt[i] = sm.value[o < kValues ? kValues - 1 - o : o];
         mass[i] = cnt[i] ? (double)cnt[i] * w.raw(logit(o)) : 0.0;
         own += mass[i];
         own_cnt += cnt[i];
@@ -1007,16 +1071,37 @@ __device__ __forceinline__ bool by_value(const Row<SV_BF16, NT>& row, const Sett
             w.cid = INT32_MAX;
         } else {
             // the want-th lowest id of the border's value
-            if (n > (uint32_t)kRank) return false;
+            if (n > (uint32_t)kList) return false;
             if (threadIdx.x == 0) sm.list_n = 0;
             __syncthreads();
-            compact(row, sm, wave, [&](float z) { return z == w.zc; }, [&](float z, int id) {
-                const int i = atomicAdd(&sm.list_n, 1);
-                if (i < kRank) sm.list[i] = entry(order_key(z), id);
-            });
+            const uint32_t at = __float_as_uint(w.zc), both = at | at >> 16;
+            row.template granules<8>(
+                [&](const typename Row<SV_BF16, NT>::Raw& g, int id0) {
+                    // whether some half word equals zc's (or may)
+                    uint32_t some = 0;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t x = g.w[i] ^ both;
+                        some |= (x - 0x00010001u) & ~x;
+                    }
+                    if ((some & 0x80008000u) == 0) return;
+                    float z[8];
+                    g.unpack(z);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (z[e] == w.zc) {
+                            const int i = atomicAdd(&sm.list_n, 1);
+                            if (i < kList) sm.list[i] = entry(sm.digit, id0 + e);
+                        }
+                },
+                [](int) {});
             __syncthreads();
-            rank_list(w, sm, (int)n);
-            w.cid = entry_id(sm.sorted[want - 1]);
+            if (n <= (uint32_t)kRank) {
+                rank_list(w, sm, (int)n);
+                w.cid = entry_id(sm.sorted[want - 1]);
+            } else {
+                w.cid = nth_id(sm, want);
+            }
         }
     }
     w.s = (double)set.s;
@@ -1104,19 +1189,47 @@ __device__ __forceinline__ Result find_law(const Row<DT, NT>& row, const Setting
     constexpr int kAhead = 16 / Row<DT, NT>::kBytes;
     const int lane = threadIdx.x & 63;
     Result r{};
-    // pass 1: largest logit, faults
+    // pass 1: largest logit, faults; for a bf16 row that by_value() decides, its
+    // values too, in a range guessed from the largest of the first ids and twice
+    // as far (256 x 7 laws of top-p, 129,280 ids: 338 us against 384 with a pass
+    // of its own)
+    const bool use_p = set.p < 1.0f;
     Extremes<DT> ex, batch;
-    row.template granules<kAhead>(
-        [&](const Raw& g, int) {
+    uint32_t base = 0;
+    if constexpr (DT == SV_BF16) {
+        if (!set.bad && set.k == 0 && set.t > 0.0f && (use_p || (!DRAWS && set.s == 0.0f))) {
+            Extremes<DT> first;
+            const Raw g = row.raw(row.turn_id(0));
 #pragma unroll
-            for (int i = 0; i < 2 * Row<DT, NT>::kBytes; ++i) batch.add(g.w[i]);
-        },
-        [&](int b) {
-            if (b < Smem<NT>::kBatches)
-                sm.batch_top[b][threadIdx.x] = (uint16_t)(batch.top() >> 16);
-            ex.add(batch);
-            batch = Extremes<DT>{};
-        });
+            for (int i = 0; i < 4; ++i) first.add(g.w[i]);
+            const float m = key_logit(block_max(first.top(), sm));
+            const float most = 2.0f * value_reach(m, set.t);
+            if (most < 1e38f) base = value_base(most);
+        }
+        if (base != 0) {
+            clear_values(sm);
+            row.template granules<DRAWS ? 2 : 8>(
+                [&](const Raw& g, int id0) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) ex.add(g.w[i]);
+                    count_values(g, id0, sm, base);
+                },
+                [](int) {});
+        }
+    }
+    if (base == 0) {
+        row.template granules<kAhead>(
+            [&](const Raw& g, int) {
+#pragma unroll
+                for (int i = 0; i < 2 * Row<DT, NT>::kBytes; ++i) batch.add(g.w[i]);
+            },
+            [&](int b) {
+                if (b < Smem<NT>::kBatches)
+                    sm.batch_top[b][threadIdx.x] = (uint16_t)(batch.top() >> 16);
+                ex.add(batch);
+                batch = Extremes<DT>{};
+            });
+    }
     const uint32_t mine = ex.top();
     const uint32_t top = block_max(mine, sm);
     const int bad = __syncthreads_or(ex.bad());
@@ -1132,7 +1245,6 @@ __device__ __forceinline__ Result find_law(const Row<DT, NT>& row, const Setting
 
     // lb: no id below this logit is in the support (nor, with top-k, among
     // the first k)
-    const bool use_p = set.p < 1.0f;
     float lb = -kInf;
     if (set.t == 0.0f) {
         lb = key_logit(top);
@@ -1158,7 +1270,7 @@ __device__ __forceinline__ Result find_law(const Row<DT, NT>& row, const Setting
     if (set.k == 0 && set.t > 0.0f) {
         if constexpr (DT == SV_BF16) {
             // the border, and without a draw everything, by the row's values
-            if (use_p || (!DRAWS && set.s == 0.0f)) decided = by_value<DRAWS>(row, set, sm, r);
+            if (use_p || (!DRAWS && set.s == 0.0f)) decided = by_value<DRAWS>(row, set, sm, r, base);
             if (decided && (r.n > 0 || !use_p)) return r;
         }
         if (!decided && use_p) {
@@ -1177,16 +1289,15 @@ __device__ __forceinline__ Result find_law(const Row<DT, NT>& row, const Setting
         // hold one, and read those again.  (Code that is run once is paid for
         // in instruction fetches: none of it unrolled.)
         if (mine >= order_key(lb)) {
-            const int wave = threadIdx.x >> 6;
             const uint32_t least = order_key(lb) >> 16;
-            for (int s0 = 0; s0 < row.steps; s0 += kAhead) {
+            for (int s0 = 0; s0 < row.turns(); s0 += kAhead) {
                 const int b = s0 / kAhead;
                 if (b < Smem<NT>::kBatches && sm.batch_top[b][threadIdx.x] < least) continue;
                 unsigned hits = 0;
                 Raw g[kAhead];
 #pragma unroll
                 for (int i = 0; i < kAhead; ++i)
-                    g[i] = row.fetch(min(row.first_id(wave, s0 + i, lane), row.vocab));
+                    g[i] = row.fetch(min(row.turn_id(s0 + i), row.vocab));
 #pragma unroll
                 for (int i = 0; i < kAhead; ++i) {
                     float z[8];
@@ -1196,11 +1307,11 @@ __device__ __forceinline__ Result find_law(const Row<DT, NT>& row, const Setting
                     for (int e = 1; e < 8; ++e) big = fmaxf(big, z[e]);
                     // a granule past the row's end shows its last ids: looked
                     // at again below
-                    if (big >= lb && s0 + i < row.steps) hits |= 1u << i;
+                    if (big >= lb && row.turn_id(s0 + i) < row.vocab) hits |= 1u << i;
                 }
 #pragma unroll 1
                 for (; hits != 0; hits &= hits - 1) {
-                    const int id0 = row.first_id(wave, s0 + __builtin_ctz(hits), lane);
+                    const int id0 = row.turn_id(s0 + __builtin_ctz(hits));
                     float z[8];
                     row.raw(id0).unpack(z);
                     int c = 0;
