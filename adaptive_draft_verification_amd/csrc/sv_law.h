@@ -37,6 +37,7 @@ constexpr int kList = 2048;  // candidates kept in LDS
 constexpr int kRank = 256;   // candidates ranked by counting
 constexpr int kSteps = 2048; // histogram of the weights, kPerOctave steps for a factor of 2
 constexpr float kPerOctave = 32.0f;
+constexpr int kAbove = 640;  // of them above the logit they start from
 constexpr double kLog2e64 = 1.4426950408889634074;
 constexpr int kValues = 2048;  // bf16 values of either sign counted by value: 16 octaves
 constexpr int kQueue = 640;  // ids a wave keeps for compact(): 64 left over and 512 of a step
@@ -320,6 +321,24 @@ struct Row {
             if (ends_in(wave, s)) settle(now, id0);
             f(now, id0);
             id0 = id1;
+        }
+    }
+    // f(granule, first id) over the calling wave's granules in id order, kAhead
+    // loads of them at a time
+    template <int kAhead, class F>
+    __device__ __forceinline__ void in_order(F f) const {
+        const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+        for (int s = 0; s < steps && first_id(wave, s, 0) < vocab; s += kAhead) {
+            Raw g[kAhead];
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) g[i] = fetch(first_id(wave, s + i, lane));
+            if (ends_in(wave, s + kAhead - 1)) {
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i) settle(g[i], first_id(wave, s + i, lane));
+            }
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i)
+                if (s + i < steps) f(g[i], first_id(wave, s + i, lane));
         }
     }
     template <class F>
@@ -1112,31 +1131,54 @@ __device__ __forceinline__ bool by_value(const Row<SV_BF16, NT>& row, const Sett
     return true;
 }
 
-// Top-p alone.  Returns false, with nothing decided, where the ids next to the
-// border do not fit the list.
-template <sv_dtype DT, int NT>
-__device__ __forceinline__ bool find_nucleus(const Row<DT, NT>& row, const Settings& set, Smem<NT>& sm,
-                                             Result& r) {
-    Weigher w = r.w;
-    const float m = (float)w.m, per_logit = fminf(kPerOctave * (float)w.it, 1e30f);
-    // monotone in z, whatever it rounds to
-    const auto step_of = [&](float z) {
-        return (int)fminf((m - z) * per_logit, (float)(kSteps - 1));
-    };
+// Steps of the weight, from a logit that is about the row's largest: kPerOctave
+// for each factor of 2, the first kAbove of them above it.
+struct Steps {
+    float ref, per_logit;
+    // the step's number, with the place within it; monotone in z, whatever it
+    // rounds to
+    __device__ __forceinline__ float at(float z) const {
+        const float v = (ref - z) * per_logit + (float)kAbove;
+        return fminf(fmaxf(v, 0.0f), (float)(kSteps - 1));
+    }
+    __device__ __forceinline__ int of(float z) const { return (int)at(z); }
+};
+
+template <int NT>
+__device__ __forceinline__ void clear_steps(Smem<NT>& sm) {
     for (int i = threadIdx.x; i < kSteps; i += NT) sm.step[i] = 0;
     __syncthreads();
-    // The histogram only says where to look.  An id adds its weight over the
-    // step's largest (between 1 and 2^(-1/32), linear within 3e-5) in units of
-    // 1/1024: at most 2^30 a step.  (LDS adds in fp32 took 170 clocks a wave
-    // here, 64-bit integer ones 31.)
-    double part = 0.0;
-    row.each([&](float z, int id) {
-        part += w.raw(z);  // -inf: 0
-        const float v = fminf((m - z) * per_logit, (float)(kSteps - 1));
-        const float f = v - floorf(v);
+}
+
+// The histogram only says where to look.  An id adds its weight over the step's
+// largest (between 1 and 2^(-1/32), linear within 3e-5) in units of 1/1024: at
+// most 2^30 a step; the last step's, of next to no weight, are left out.  (LDS
+// adds in fp32 took 170 clocks a wave here, 64-bit integer ones 31.)
+template <int NT>
+__device__ __forceinline__ void count_step(Smem<NT>& sm, const Steps& steps, float z) {
+    const float v = steps.at(z), f = v - floorf(v);
+    if (v < (float)(kSteps - 1))
         atomicAdd(&sm.step[(int)v], (uint32_t)fmaf(f, -1024.0f * (1.0f - 0.978572f), 1024.5f));
-    });
-    const double total = block_sum(part, sm);
+}
+
+// Top-p alone.  steps: of the histogram that pass 1 made, total: the sum it took
+// of the row's weights (not made: both are made here).  Returns false, with
+// nothing decided, where the ids next to the border do not fit the list.
+template <sv_dtype DT, int NT>
+__device__ __forceinline__ bool find_nucleus(const Row<DT, NT>& row, const Settings& set, Smem<NT>& sm,
+                                             Result& r, Steps steps, double total, bool made) {
+    Weigher w = r.w;
+    if (!made) {
+        steps.ref = (float)w.m;
+        clear_steps(sm);
+        double part = 0.0;
+        row.each([&](float z, int id) {
+            part += w.raw(z);  // -inf: 0
+            count_step(sm, steps, z);
+        });
+        total = block_sum(part, sm);
+    }
+    const double above = w.raw(steps.ref);  // of the largest weight
     const double goal = (double)set.p * total;
     // The border is where the weight behind it falls to total - goal; taken
     // from that side, a histogram off by 2^-11 of what it holds is off by
@@ -1147,7 +1189,8 @@ __device__ __forceinline__ bool find_nucleus(const Row<DT, NT>& row, const Setti
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
         const int s = kEach * threadIdx.x + i;
-        mass[i] = (double)sm.step[s] * (pow2((double)-s / (double)kPerOctave) * 0x1p-10);
+        mass[i] = (double)sm.step[s] * above *
+                  (pow2((double)(kAbove - s) / (double)kPerOctave) * 0x1p-10);
         own += mass[i];
     }
     const double incl = wave_incl_sum_dpp(own, lane);
@@ -1173,9 +1216,11 @@ __device__ __forceinline__ bool find_nucleus(const Row<DT, NT>& row, const Setti
     __syncthreads();
     const int b1 = sm.first, b2 = sm.second;
     // logits of step b2 or less: at least this one, or a little below
-    const float edge = m - (float)(b2 + 1) / per_logit * 1.00001f - fabsf(m) * 1e-6f;
+    const float down = (float)(b2 + 1 - kAbove) / steps.per_logit;
+    const float edge = steps.ref - down - (fabsf(down) * 1e-5f + 1e-3f / steps.per_logit) -
+                       fabsf(steps.ref) * 1e-6f;
     return finish_nucleus(row, set, sm, r, goal, edge, [&](float z) {
-        const int s = step_of(z);
+        const int s = steps.of(z);
         return s < b1 ? 0 : s <= b2 ? 1 : 2;
     });
 }
@@ -1189,35 +1234,63 @@ __device__ __forceinline__ Result find_law(const Row<DT, NT>& row, const Setting
     constexpr int kAhead = 16 / Row<DT, NT>::kBytes;
     const int lane = threadIdx.x & 63;
     Result r{};
-    // pass 1: largest logit, faults; for a bf16 row that by_value() decides, its
-    // values too, in a range guessed from the largest of the first ids and twice
-    // as far (256 x 7 laws of top-p, 129,280 ids: 338 us against 384 with a pass
-    // of its own)
+    // Pass 1: largest logit, faults; and where nothing but top-p may cut, what
+    // needs every id, taken relative to the largest of the first ids: the values
+    // of a bf16 row that by_value() decides, in a range twice as far as that one
+    // asks for (256 x 7 laws of top-p, 129,280 ids: 338 us against 384 with a
+    // pass of its own); else the sum of the weights, by wave, and top-p's
+    // histogram.
     const bool use_p = set.p < 1.0f;
     Extremes<DT> ex, batch;
     uint32_t base = 0;
-    if constexpr (DT == SV_BF16) {
-        if (!set.bad && set.k == 0 && set.t > 0.0f && (use_p || (!DRAWS && set.s == 0.0f))) {
-            Extremes<DT> first;
-            const Raw g = row.raw(row.turn_id(0));
+    bool made = false;
+    float ref = 0.0f;
+    double part = 0.0;
+    int n_part = 0;
+    Weigher& w = r.w;
+    w.it = set.t == 0.0f ? 0.0 : kLog2e64 / (double)set.t;
+    Steps steps{0.0f, fminf(kPerOctave * (float)w.it, 1e30f)};
+    if (!set.bad && set.k == 0 && set.t > 0.0f && (use_p || set.s == 0.0f)) {
+        Extremes<DT> first;
+        const Raw g = row.raw(row.turn_id(0));
 #pragma unroll
-            for (int i = 0; i < 4; ++i) first.add(g.w[i]);
-            const float m = key_logit(block_max(first.top(), sm));
-            const float most = 2.0f * value_reach(m, set.t);
-            if (most < 1e38f) base = value_base(most);
+        for (int i = 0; i < Row<DT, NT>::kWords; ++i) first.add(g.w[i]);
+        ref = key_logit(block_max(first.top(), sm));
+        if constexpr (DT == SV_BF16) {
+            const float most = 2.0f * value_reach(ref, set.t);
+            if ((use_p || !DRAWS) && most < 1e38f) {
+                base = value_base(most);
+                clear_values(sm);
+                row.template granules<DRAWS ? 2 : 8>(
+                    [&](const Raw& g, int id0) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) ex.add(g.w[i]);
+                        count_values(g, id0, sm, base);
+                    },
+                    [](int) {});
+            }
         }
-        if (base != 0) {
-            clear_values(sm);
-            row.template granules<DRAWS ? 2 : 8>(
-                [&](const Raw& g, int id0) {
+        if (base == 0 && is_finite_bits(ref)) {
+            made = true;
+            steps.ref = ref;
+            w.m = (double)ref;
+            const Weigher law = w;
+            if (use_p) clear_steps(sm);
+            row.template in_order<kAhead / (DT == SV_BF16 ? 4 : 1)>([&](const Raw& g, int) {
+                float z[8];
+                g.unpack(z);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) ex.add(g.w[i]);
-                    count_values(g, id0, sm, base);
-                },
-                [](int) {});
+                for (int i = 0; i < Row<DT, NT>::kWords; ++i) ex.add(g.w[i]);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    part += law.raw(z[e]);
+                    if (use_p) count_step(sm, steps, z[e]);
+                    else n_part += __popcll(__ballot(z[e] > -kInf));
+                }
+            });
         }
     }
-    if (base == 0) {
+    if (base == 0 && !made) {
         row.template granules<kAhead>(
             [&](const Raw& g, int) {
 #pragma unroll
@@ -1236,9 +1309,7 @@ __device__ __forceinline__ Result find_law(const Row<DT, NT>& row, const Setting
     if (bad || top <= kMinusInfKey) r.fault |= SV_DEV_NONFINITE;
     if (set.bad) r.fault |= SV_DEV_BAD_PARAM;
     if (r.fault) return r;
-    Weigher& w = r.w;
     w.m = (double)key_logit(top);
-    w.it = set.t == 0.0f ? 0.0 : kLog2e64 / (double)set.t;
     w.s = 0.0;
     w.zc = -kInf;
     w.cid = -1;  // no id of -inf counts
@@ -1266,6 +1337,22 @@ __device__ __forceinline__ Result find_law(const Row<DT, NT>& row, const Setting
         const double slack = 1e-6 * (fabs(w.m) + fabs(z) + (double)set.t);
         lb = fmaxf(lb, (float)(z - slack));
     }
+    // Sums relative to a logit so far below the largest that the histogram, or
+    // the exponents, do not reach it are taken again.  (Of 256 rows some lie 8
+    // octaves off, and the slowest counts.)
+    if (made && (w.m - (double)ref) * w.it > (use_p ? (double)kAbove / (double)kPerOctave : 500.0))
+        made = false;
+    double total = 0.0;
+    if (made) {
+        part *= w.raw(ref);
+        total = block_sum(part, sm);
+        if (!use_p) {  // nothing is cut
+            r.n = block_sum(lane == 0 ? n_part : 0, sm);
+            r.total = total;
+            r.where = kInRow;
+            return r;
+        }
+    }
     bool decided = false;
     if (set.k == 0 && set.t > 0.0f) {
         if constexpr (DT == SV_BF16) {
@@ -1274,7 +1361,7 @@ __device__ __forceinline__ Result find_law(const Row<DT, NT>& row, const Setting
             if (decided && (r.n > 0 || !use_p)) return r;
         }
         if (!decided && use_p) {
-            decided = find_nucleus(row, set, sm, r);
+            decided = find_nucleus(row, set, sm, r, steps, total, made);
             if (decided && r.n > 0) return r;
         }
         if (use_p) lb = -kInf;
@@ -1372,22 +1459,22 @@ __device__ __forceinline__ Result find_law(const Row<DT, NT>& row, const Setting
     // how many, and their weight; leaves the waves' sums in sm.redd
     const Weigher law = r.w;
     int n = 0;
-    double part = 0.0;
+    double mass = 0.0;
     if (law.zc == -kInf && law.s == 0.0) {
         row.each([&](float z, int id) {
             n += __popcll(__ballot(z > -kInf));
-            part += law.raw(z);
+            mass += law.raw(z);
         });
     } else {
         compact(row, sm, threadIdx.x >> 6, [&](float z) { return z >= law.zc && z >= lb; }, [&](float z, int id) {
             const double x = law.raw(z);
             const bool live = law.above(z, id) && x >= law.s;
             n += __popcll(__ballot(live));
-            part += live ? x : 0.0;
+            mass += live ? x : 0.0;
         });
     }
     r.n = block_sum(lane == 0 ? n : 0, sm);
-    r.total = block_sum(part, sm);
+    r.total = block_sum(mass, sm);
     return r;
 }
 
