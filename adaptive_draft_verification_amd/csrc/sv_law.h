@@ -13,17 +13,25 @@
 // fixed-point integers (two 64-bit words, 43 bits each below the point), so
 // their order does not change them.
 //
-// One workgroup takes a row.  Three ways to the border, by
-// what the settings ask for:
-//  - top-k up to 1024, or min-p: a bound that costs no pass (the k-th largest of
-//    the threads' own maxima, min-p's logit) leaves a few candidates, which are
-//    gathered in LDS, ranked by counting and summed there;
-//  - top-p alone: one pass sums the row and its histogram over 2048 steps of
-//    the weight (2^(1/32) each); the steps next to the border are gathered and
-//    searched the same way while the ids above them are summed;
-//  - anything else, and what does not fit the lists (long runs of equal
-//    logits): the border is found digit by digit, 256 bins over 8 bits of the
-//    ordered key, then the next 8 bits within the bin that holds the border.
+// One workgroup takes a row.  Four ways to the border, by what the settings ask
+// for (times: 256 rows, one a workgroup; the pass over memory that finds the
+// largest logit and the faults is part of each):
+//  - T = 0, top-k up to the workgroup's threads, or min-p: a bound that costs no
+//    pass (the largest logit, the k-th largest of the threads' own maxima,
+//    min-p's logit) leaves a few candidates, which are gathered in LDS, ranked by
+//    counting and summed there (129,280 bf16: 25, 32, 41 us; 256,000 fp32: 52,
+//    61, 75);
+//  - bf16, top-p alone, and no cut where no draw follows: how many ids have each
+//    value, counted in the first pass, gives the sum and the border (by_value();
+//    57 us with a draw);
+//  - fp32, top-p alone, and no cut: the first pass takes the sum, and top-p's
+//    histogram over 2048 steps of the weight (2^(1/32) each); the steps next to
+//    the border are gathered and searched like candidates while the ids above
+//    them are summed (find_nucleus(); 140 us, 83 without top-p);
+//  - anything else, and what does not fit the lists (long runs of equal logits):
+//    the border is found digit by digit, 256 bins over 8 bits of the ordered key,
+//    then the next 8 bits within the bin that holds the border (top-k of 2000 of
+//    129,280 bf16: 165 us).
 #pragma once
 
 #include "sv_device.h"
@@ -90,8 +98,8 @@ __device__ __forceinline__ Settings settings(const sv_sampling& a, int i, int vo
 // 2^t for t <= 0, to 4e-14: t = n + r with n an integer and |r| <= 1/2, 2^r = 1 +
 // r q(r) with q of degree 8 through the Chebyshev nodes of [-1/2, 1/2].  2^0 is
 // exactly 1, so equal logits have equal weights, and counts of them are exact.
-// Seventeen fp64 operations an id bound the passes that sum a row: 13 us for
-// 129,280 ids on one CU.
+// Some eighteen fp64 operations an id (4.1 clocks a wave each) bound the passes
+// that sum a row: 18 us for 129,280 ids on one CU.
 __device__ __forceinline__ double pow2(double t) {
     t = fmax(t, -1100.0);
     const double shifted = t + 0x1.8p52;
@@ -361,7 +369,7 @@ struct Row {
 // time and in id order within the wave, the last call with fewer lanes.  Where
 // a few per cent of the ids are kept, the work on them then costs a wave per 64
 // of them and not nearly a wave per 64 ids of the row (129,280 ids, 2 % kept:
-// 30 us against 9 for the sum of their weights).
+// 30 us for the sum of their weights id by id, 9 this way).
 template <sv_dtype DT, int NT, class Keep, class Use>
 __device__ __forceinline__ void compact(const Row<DT, NT>& row, Smem<NT>& sm, int segment, Keep keep,
                                         Use use) {

@@ -40,8 +40,9 @@ void run(const SampleArgs& a, hipStream_t stream) {
 hipError_t launch_sample(const SampleArgs& a, hipStream_t stream) {
     // Up to a workgroup for each CU, a row's own time counts: 1024 threads.
     // More rows share a CU: two workgroups of 512 threads, one summing while
-    // the other waits for memory (2048 rows of 129,280 bf16, top-p: 551 us
-    // against 659; 256 rows: 92 against 85).
+    // the other waits for memory (129,280 bf16 ids under top-p, 512 threads
+    // against 1024 as first measured: 2048 rows 551 us against 659, 256 rows 92
+    // against 85).
     // Rows of fewer than 8 ids: one wave each.
     if (a.vocab < 8) run<kWave>(a, stream);
     else if (a.n_rows > law::kCUs) run<512>(a, stream);
