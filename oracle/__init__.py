@@ -59,6 +59,12 @@ Parity pin status (what the oracle is checked against, in tests/):
   32-token vocabulary (the law must equal the target distribution), by
   chi-square over seeded trials, by the closed form E[L] = sum_j prod_i alpha_i,
   and by the identity residual mass = 1 - sum min(p, q) = 0.5 * |p - q|_1.
+* truncated laws (truncate.py: sample_row, verify_truncated) — pinned by laws
+  derived by hand, by every prefix length tried against the definition, by the
+  plain verify where nothing is cut, and by exact enumeration of the output law.
+* the paged cache (cache.py: e4m3_round, cache_append, cache_attend) — pinned
+  by every e4m3 value and torch's rounding between neighbours, by torch's dense
+  softmax on scattered pages, and by edges derived by hand.
 """
 
 from .philox import philox4x32_10, uniforms, PHILOX_ROUNDS
