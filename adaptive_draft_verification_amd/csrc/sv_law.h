@@ -778,13 +778,16 @@ __device__ __forceinline__ bool cut_mass(const Row<DT, NT>& row, Smem<NT>& sm, b
 }
 
 // The law by digits: any settings, any row.  lb: no id below it matters;
-// listed: the ids from lb up are in sm.list.  Not inlined: few rows need it,
-// and the others' code stays small.
+// listed: the ids from lb up are in sm.list; m, it: the weigher's.  Not inlined:
+// few rows need it, and the others' code stays small.  It and its like take and
+// return their structures by value, in registers: by reference they would live
+// in memory on every row's path.
 template <sv_dtype DT, int NT>
-__device__ __attribute__((noinline)) void find_by_digits(const Row<DT, NT>& row, const Settings& set,
-                                                         Smem<NT>& sm, float lb, bool listed,
-                                                         Result& r) {
-    Weigher w = r.w;
+__device__ __attribute__((noinline)) Result find_by_digits(const Row<DT, NT> row, const Settings set,
+                                                           Smem<NT>& sm, float lb, bool listed,
+                                                           double m, double it) {
+    Result r{};
+    Weigher w{m, it, 0.0, -kInf, -1};
     const bool use_p = set.p < 1.0f;
     const auto in = [&](float z) { return z >= lb && z > -kInf; };
     if (set.k > 0) {
@@ -820,13 +823,20 @@ __device__ __attribute__((noinline)) void find_by_digits(const Row<DT, NT>& row,
         });
     }
     r.where = listed ? kListed : kInRow;
+    return r;
 }
 
 // cut_mass over the list, not inlined (rarely needed).
+struct Cut {
+    Weigher w;
+    int found;
+};
 template <sv_dtype DT, int NT>
-__device__ __attribute__((noinline)) bool cut_listed(const Row<DT, NT>& row, Smem<NT>& sm,
-                                                     Weigher& w, double goal) {
-    return cut_mass(row, sm, true, w, goal, [](float) { return true; });
+__device__ __attribute__((noinline)) Cut cut_listed(const Row<DT, NT> row, Smem<NT>& sm,
+                                                    const Weigher w, double goal) {
+    Cut c{w, 0};
+    c.found = cut_mass(row, sm, true, c.w, goal, [](float) { return true; });
+    return c;
 }
 
 // Top-p's border among the ids near it, once it is known where to look: side(z)
@@ -871,9 +881,9 @@ __device__ __forceinline__ bool finish_nucleus(const Row<DT, NT>& row, const Set
         w.zc = key_logit(entry_key(sm.sorted[last]));
         w.cid = entry_id(sm.sorted[last]);
     } else {
-        Weigher cut = w;
-        if (!cut_listed(row, sm, cut, goal - above)) return false;
-        w = cut;
+        const Cut cut = cut_listed(row, sm, w, goal - above);
+        if (!cut.found) return false;
+        w = cut.w;
     }
     w.s = (double)set.s;
     r.w = w;
@@ -1460,7 +1470,8 @@ __device__ __forceinline__ Result find_law(const Row<DT, NT>& row, const Setting
     }
     r.where = kInRow;
     if (!decided) {
-        if (use_p || set.k > 0 || listed) find_by_digits<DT, NT>(row, set, sm, lb, listed, r);
+        if (use_p || set.k > 0 || listed)
+            r = find_by_digits<DT, NT>(row, set, sm, lb, listed, w.m, w.it);
         if (r.where == kListed) return r;
     }
     r.w.s = (double)set.s;
@@ -1575,7 +1586,7 @@ __device__ int walk_row(Smem<NT>& sm, const double* sums, int segments, double g
 // A draw over the listed ids, digit by digit of the id; not inlined (rarely
 // needed).
 template <sv_dtype DT, int NT>
-__device__ __attribute__((noinline)) int draw_listed(const Row<DT, NT>& row, Smem<NT>& sm,
+__device__ __attribute__((noinline)) int draw_listed(const Row<DT, NT> row, Smem<NT>& sm,
                                                      const Weigher w, float u, double goal) {
     const auto live = [&](auto fn) {
         candidates(row, sm, true, [&](float z, int id) {
