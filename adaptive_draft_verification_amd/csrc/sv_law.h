@@ -335,7 +335,11 @@ struct Row {
     // loads of them at a time
     template <int kAhead, class F>
     __device__ __forceinline__ void in_order(F f) const {
-        const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+        in_order<kAhead>(threadIdx.x >> 6, f);
+    }
+    template <int kAhead, class F>
+    __device__ __forceinline__ void in_order(int wave, F f) const {
+        const int lane = threadIdx.x & 63;
         for (int s = 0; s < steps && first_id(wave, s, 0) < vocab; s += kAhead) {
             Raw g[kAhead];
 #pragma unroll
@@ -369,15 +373,16 @@ struct Row {
 // time and in id order within the wave, the last call with fewer lanes.  Where
 // a few per cent of the ids are kept, the work on them then costs a wave per 64
 // of them and not nearly a wave per 64 ids of the row (129,280 ids, 2 % kept:
-// 30 us for the sum of their weights id by id, 9 this way).
-template <sv_dtype DT, int NT, class Keep, class Use>
+// 30 us for the sum of their weights id by id, 9 this way).  kAhead: loads in
+// flight together, 1: the next one while one is worked on.
+template <int kAhead = 1, sv_dtype DT, int NT, class Keep, class Use>
 __device__ __forceinline__ void compact(const Row<DT, NT>& row, Smem<NT>& sm, int segment, Keep keep,
                                         Use use) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     float* qz = sm.queue_z[wave];
     int* qi = sm.queue_id[wave];
     int n = 0;  // the same in every lane
-    row.granules_of(segment, lane, [&](const typename Row<DT, NT>::Raw& g, int id0) {
+    const auto take = [&](const typename Row<DT, NT>::Raw& g, int id0) {
         float z[8];
         g.unpack(z);
         int c = 0;
@@ -407,7 +412,9 @@ __device__ __forceinline__ void compact(const Row<DT, NT>& row, Smem<NT>& sm, in
             if (lane < n) qz[lane] = mz, qi[lane] = mi;
             __builtin_amdgcn_wave_barrier();
         }
-    });
+    };
+    if constexpr (kAhead > 1) row.template in_order<kAhead>(segment, take);
+    else row.granules_of(segment, lane, take);
     if (lane < n) use(qz[lane], qi[lane]);
 }
 
@@ -1504,7 +1511,7 @@ __device__ __forceinline__ Result find_law(const Row<DT, NT>& row, const Setting
 // 8 weights at ids id0 .. id0 + 7.  If rounding leaves no such id, the last one
 // of positive weight.
 template <int NT, class Weights, class FirstId>
-__device__ int walk_row(Smem<NT>& sm, const double* sums, int segments, double goal, int steps,
+__device__ __forceinline__ int walk_row(Smem<NT>& sm, const double* sums, int segments, double goal, int steps,
                         FirstId first_id, int vocab, Weights weights) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     double before = 0.0;
@@ -1601,7 +1608,7 @@ __device__ __attribute__((noinline)) int draw_listed(const Row<DT, NT> row, Smem
 
 // The id a uniform u in [0, 1) draws from a law find_law has just made.
 template <sv_dtype DT, int NT>
-__device__ int draw(const Row<DT, NT>& row, const Result& r, float u, Smem<NT>& sm) {
+__device__ __forceinline__ int draw(const Row<DT, NT>& row, const Result& r, float u, Smem<NT>& sm) {
     const double goal = (double)u * r.total;
     if (r.where == kRanked) {
         if (r.n == 1) return entry_id(sm.sorted[0]);

@@ -165,7 +165,10 @@ struct Drawn {
     // The calling wave's sum over a segment of the row, in every lane.
     __device__ __forceinline__ double sum(law::Smem<NT>& sm, int segment) const {
         double part = 0.0;
-        if (pw.zc == -law::kInf) {  // nothing cut: every id weighs
+        if (pw.it == 0.0) {  // greedy: one id
+            if ((pw.cid >> 3) / prow.per == segment && (threadIdx.x & 63) == 0)
+                part = of(prow.one(pw.cid), pw.cid);
+        } else if (pw.zc == -law::kInf) {  // nothing cut: every id weighs
             const int lane = threadIdx.x & 63;
             for (int st = 0; st < prow.steps; ++st) {
                 const int id0 = prow.first_id(segment, st, lane);
@@ -176,7 +179,7 @@ struct Drawn {
                 for (int e = 0; e < 8; ++e) part += x[e];
             }
         } else {
-            law::compact(prow, sm, segment, [&](float z) { return z >= pw.zc; },
+            law::compact<4>(prow, sm, segment, [&](float z) { return z >= pw.zc; },
                          [&](float z, int id) { part += of(z, id); });
         }
         return wave_sum(part);
