@@ -19,19 +19,19 @@
 //  - T = 0, top-k up to the workgroup's threads, or min-p: a bound that costs no
 //    pass (the largest logit, the k-th largest of the threads' own maxima,
 //    min-p's logit) leaves a few candidates, which are gathered in LDS, ranked by
-//    counting and summed there (129,280 bf16: 25, 32, 41 us; 256,000 fp32: 52,
-//    61, 75);
+//    counting and summed there (129,280 bf16: 17, 24, 36 us; 256,000 fp32: 44,
+//    54, 65);
 //  - bf16, top-p alone, and no cut where no draw follows: how many ids have each
 //    value, counted in the first pass, gives the sum and the border (by_value();
-//    57 us with a draw);
+//    47 us with a draw);
 //  - fp32, top-p alone, and no cut: the first pass takes the sum, and top-p's
 //    histogram over 2048 steps of the weight (2^(1/32) each); the steps next to
 //    the border are gathered and searched like candidates while the ids above
-//    them are summed (find_nucleus(); 140 us, 83 without top-p);
+//    them are summed (find_nucleus(); 130 us, 71 without top-p);
 //  - anything else, and what does not fit the lists (long runs of equal logits):
 //    the border is found digit by digit, 256 bins over 8 bits of the ordered key,
 //    then the next 8 bits within the bin that holds the border (top-k of 2000 of
-//    129,280 bf16: 165 us).
+//    129,280 bf16: 131 us).
 #pragma once
 
 #include "sv_device.h"
@@ -1262,7 +1262,7 @@ __device__ __forceinline__ Result find_law(const Row<DT, NT>& row, const Setting
     // Pass 1: largest logit, faults; and where nothing but top-p may cut, what
     // needs every id, taken relative to the largest of the first ids: the values
     // of a bf16 row that by_value() decides, in a range twice as far as that one
-    // asks for (256 x 7 laws of top-p, 129,280 ids: 338 us against 384 with a
+    // asks for (256 x 7 laws of top-p, 129,280 ids, as first measured: 338 us against 384 with a
     // pass of its own); else the sum of the weights, by wave, and top-p's
     // histogram.
     const bool use_p = set.p < 1.0f;
