@@ -78,7 +78,7 @@ struct AttendPlan {
         const int block = slots < 16 * slot_tiles ? slots : 16 * slot_tiles;
         part_min = (32 * (esize == 1 ? 2 : 1) * block + 127) / 128 * 128;
         // Parts until there are about 1024 workgroups, four for a CU (3 requests
-        // of 100,004 positions, 8 kv heads, e4m3: 168-176 us for 512, 141 for
+        // of 100,005 positions, 8 kv heads, e4m3: 168-176 us for 512, 141 for
         // 1024, 159 for 2048, 157 for 8192).
         const int64_t groups = (int64_t)n_req * n_kv_heads * slot_blocks;
         const int64_t want = groups > 0 ? (1024 + groups - 1) / groups : 1;

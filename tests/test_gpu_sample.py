@@ -421,3 +421,27 @@ def test_zeros_of_both_signs_at_a_tiny_temperature(dtype):
     toks = np.array([[10], [99], [60]], np.int32)
     cu = np.arange(0, 2 * n + 1, 2, dtype=np.int32)
     check_verify((z.repeat_interleave(2, 0), z.clone(), toks, cu, s, s), V, 57, 1)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("s", [(1.0, 0, 1.0, 0.0), (1e-3, 0, 1.0, 0.0), (1.0, 0, 0.9, 0.0),
+                               (0.05, 0, 0.99, 0.0), (30.0, 0, 0.5, 0.0), (1.0, 0, 0.9, 0.05)])
+def test_rows_whose_first_ids_do_not_tell(dtype, s):
+    """The first ids bound nothing: all -inf, far below the largest logit, far above in
+    size, or the only ones of their sign."""
+    V = 20000
+    g = torch.Generator().manual_seed(61)
+    x, at = torch.randn(V, generator=g), torch.arange(V)
+    ninf = float("-inf")
+    z = torch.stack([
+        torch.where(at < 17000, ninf, x), torch.where(at < 17000, -300.0, x + 200),
+        torch.where(at < 17000, x * 2, x * 2 + 12), torch.where(at < 17000, x - 1e6, x),
+        torch.where(at < 17000, -x.abs() * 1e-3, x.abs() * 50), torch.where(at == V - 1, 1e30, x),
+        torch.where(at < 9000, -3e38, x * 1e-20)]).to(dtype)
+    n = len(z)
+    u = torch.rand(n, generator=g).tolist()
+    check_sample(z.cuda(), u, [s] * n)
+    toks = np.array([[sample_row(z[r].float().numpy(), u[r], *s)[0]] for r in range(n)], np.int32)
+    cu = np.arange(0, 2 * n + 1, 2, dtype=np.int32)
+    check_verify((z.repeat_interleave(2, 0), (z.float() * 0.5).to(dtype), toks, cu, [s] * n,
+                  [s] * n), V, 63, 2)
