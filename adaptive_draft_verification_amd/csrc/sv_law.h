@@ -745,7 +745,8 @@ template <sv_dtype DT, int NT>
 __device__ __forceinline__ void cut_ties(const Row<DT, NT>& row, Smem<NT>& sm, bool listed, Weigher& w,
                                          uint32_t key, uint32_t want, uint32_t in_cnt) {
     const float zk = key_logit(key);
-    int cid = INT32_MAX;
+    // all that take part: up to the border there was, if it lies at this logit
+    int cid = zk == w.zc ? w.cid : INT32_MAX;
     if (want < in_cnt) {
         const Weigher was = w;
         const Found f = descend<false>(

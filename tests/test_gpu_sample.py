@@ -445,3 +445,25 @@ def test_rows_whose_first_ids_do_not_tell(dtype, s):
     cu = np.arange(0, 2 * n + 1, 2, dtype=np.int32)
     check_verify((z.repeat_interleave(2, 0), (z.float() * 0.5).to(dtype), toks, cu, [s] * n,
                   [s] * n), V, 63, 2)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("V", [7, 300, 5000, 30000])
+def test_top_p_that_keeps_all_of_a_top_k_among_ties(dtype, V):
+    """top-k ends inside a run of equal logits, and top-p (or min-p) cuts nothing more."""
+    s = [(0.7, 1, 0.9999, 0.0), (0.7, 3, 0.9, 0.0), (1.0, 5, 0.9999, 0.3), (2.0, 1, 0.3, 0.9),
+         (1.0, V // 2, 0.99999, 0.0), (1.0, V - 1, 0.99999, 0.05), (1.0, 4, 0.6, 0.0)]
+    n = len(s)
+    g = torch.Generator().manual_seed(V)
+    flat = torch.full((n, V), 500.0)
+    steps = (torch.randn(n, V, generator=g) * 0.6).round()
+    gaps = torch.where(torch.rand(n, V, generator=g) < 0.4, float("-inf"), 2.0)
+    gaps[:, 0] = 2.0
+    u = torch.rand(n, generator=g).tolist()
+    for z in (flat, steps, gaps):
+        z = z.to(dtype)
+        check_sample(z.cuda(), u, s)
+        toks = np.array([[sample_row(z[r].float().numpy(), u[r], *s[r])[0]] for r in range(n)],
+                        np.int32)
+        cu = np.arange(0, 2 * n + 1, 2, dtype=np.int32)
+        check_verify((z.repeat_interleave(2, 0), z.clone(), toks, cu, s, s), V, 65, 2)
