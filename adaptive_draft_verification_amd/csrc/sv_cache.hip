@@ -168,6 +168,16 @@ struct Attend {
     static constexpr int kDpl = D / 16;     // dims a lane loads of a value row
     static constexpr int kVWords = F8 ? kDpl / 4 : kDpl / 2;
     static constexpr int kAcc = D / 4;      // accumulators a slot tile and lane
+    // Weights are 2^(score - m) with m the running maximum plus kHold, so at most
+    // 2^(8 - kHold), and m is raised by kRaise where a lane's sum has passed kFull.
+    // A lane's 8 weights of a tile then add up to 2^-7, its sum stays below 2^-6 +
+    // 2^-7, those of a slot's four lanes in four waves below 3/8 together: sums of
+    // bf16 values stay in fp32's range however large the values are.  (Products
+    // with values below 2^-108 are denormal, and weights below 2^-108 of the
+    // largest are lost, below 2^-92 once m was raised, which takes a sum of 2^16
+    // largest weights in a wave.)  e4m3 values, at most 448, need none of it.
+    static constexpr float kHold = F8 ? 0.0f : 18.0f;
+    static constexpr float kFull = 0x1p-6f, kRaise = 16.0f;
     static constexpr int kEsize = F8 ? 1 : 2;
     // waves a SIMD has registers for without spilling
     static constexpr int kOccupancy = D < 256 && MT * D <= 256 ? 2 : 1;
@@ -380,7 +390,7 @@ void attend_kernel(AttendArgs a) {
         a.scale * kLog2e * (F8 && c.k_scale != nullptr ? c.k_scale[h] : 1.0f);
 
     f32x4 acc[MT][C::kDpl];
-    float m[MT], mu[MT], l[MT];  // running max (-inf: none yet), the max used, sum
+    float m[MT], mu[MT], l[MT];  // running m (-inf: no score yet), the m used, sum
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
@@ -485,18 +495,24 @@ void attend_kernel(AttendArgs a) {
             float mx = p[0];
 #pragma unroll
             for (int j = 1; j < J; ++j) mx = fmaxf(mx, p[j]);
-            // the maximum moves only when a score passes it by 2^8: sums and
-            // outputs are relative to it either way, and stay far from
-            // overflow; most tiles then rescale nothing
-            if (__ballot(mx > m[mt] + 8.0f) != 0) {
+            // m moves only when a score passes the maximum it came from by 2^8,
+            // or the sum is full: sums and outputs are relative to it either
+            // way; most tiles then rescale nothing
+            if (__ballot(mx > m[mt] + (8.0f - C::kHold) || (!F8 && l[mt] > C::kFull)) != 0) {
                 mx = fmaxf(mx, __shfl_xor(mx, 16));
                 mx = fmaxf(mx, __shfl_xor(mx, 32));
-                if (mx > m[mt]) {
-                    const float f = fast_exp2(m[mt] - mx);  // m = -inf: 0
+                float to = fmaxf(m[mt], mx + C::kHold);
+                if (!F8) {
+                    float most = fmaxf(l[mt], __shfl_xor(l[mt], 16));
+                    most = fmaxf(most, __shfl_xor(most, 32));
+                    if (most > C::kFull) to += C::kRaise;
+                }
+                if (to > m[mt]) {
+                    const float f = fast_exp2(m[mt] - to);  // m = -inf: 0
 #pragma unroll
                     for (int i = 0; i < C::kDpl; ++i) acc[mt][i] *= f;
                     l[mt] *= f;
-                    m[mt] = mu[mt] = mx;
+                    m[mt] = mu[mt] = to;
                 }
             }
 #pragma unroll
@@ -634,7 +650,9 @@ void attend_kernel(AttendArgs a) {
                 o[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
             if (a.out_lse != nullptr && g == 0)
                 a.out_lse[(int64_t)(lo + row) * a.n_heads + head] =
-                    l[mt] == 0.0f ? -kInf : (m[mt] + log2f(l[mt])) * kLn2;
+                    l[mt] == 0.0f
+                        ? -kInf
+                        : ((m[mt] - C::kHold) + log2f(l[mt] * exp2f(C::kHold))) * kLn2;
         } else {
             const int64_t rec = (((int64_t)r * a.n_heads + head) * (a.k_max + 1) + row) * a.parts +
                                 part;
@@ -658,9 +676,10 @@ void attend_kernel(AttendArgs a) {
 // Merges the parts of a (row, head): W waves, wave w the parts w, w + W, ...
 // (eight loads in flight each), lanes over the dims; the waves' sums meet in
 // LDS, in a fixed order.  A request of one part wrote its outputs itself.
-template <int D, int W>
+template <int D, bool F8, int W>
 __global__ __launch_bounds__(256) void join_kernel(AttendArgs a) {
     constexpr int E = D / 64, kEach = 4 / W;  // (row, head)s a workgroup takes at once
+    constexpr float kHold = Attend<D, F8, 1, true>::kHold;
     __shared__ float sm_o[4][D], sm_f[4][128];
     const sv_cache& c = a.cache;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -696,9 +715,12 @@ __global__ __launch_bounds__(256) void join_kernel(AttendArgs a) {
             const float f0 = m0 == m ? 1.0f : fast_exp2(m0 - m);
             const float f1 = m1 == m ? 1.0f : fast_exp2(m1 - m);
             l = wave_sum((lane < n ? f0 * l0 : 0.0f) + (lane + 64 < n ? f1 * l1 : 0.0f));
+            // over the whole sum before the outputs are added up: they are then
+            // shares of the mean, and stay in range
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
             float* factor = sm_f[wave];
-            factor[lane] = f0;
-            factor[lane + 64] = f1;
+            factor[lane] = f0 * inv;
+            factor[lane + 64] = f1 * inv;
             __builtin_amdgcn_wave_barrier();
             for (int p0 = w; p0 < n; p0 += 8 * W) {
                 float x[8][E];
@@ -728,26 +750,25 @@ __global__ __launch_bounds__(256) void join_kernel(AttendArgs a) {
             __syncthreads();
         }
         if (!live || w != 0) continue;
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
         uint16_t* out = static_cast<uint16_t*>(a.out) + (int64_t)(lo + row) * a.out_ld +
                         (int64_t)head * D + lane * E;
 #pragma unroll
-        for (int e = 0; e < E; ++e) out[e] = (uint16_t)pack_bf16(o[e] * inv, 0.0f);
+        for (int e = 0; e < E; ++e) out[e] = (uint16_t)pack_bf16(o[e], 0.0f);
         if (a.out_lse != nullptr && lane == 0)
             a.out_lse[(int64_t)(lo + row) * a.n_heads + head] =
-                l == 0.0f ? -kInf : (m + log2f(l)) * kLn2;
+                l == 0.0f ? -kInf : ((m - kHold) + log2f(l * exp2f(kHold))) * kLn2;
     }
 }
 
-template <int D>
+template <int D, bool F8>
 void run_join(const AttendArgs& a, hipStream_t stream) {
     const int64_t total = (int64_t)a.n_req * (a.k_max + 1) * a.n_heads;
     // up to 16 parts one wave keeps them all in flight in two goes
     if (a.parts <= 16) {
         const int64_t grid = (total + 3) / 4;
-        join_kernel<D, 1><<<(unsigned)(grid < 4096 ? grid : 4096), 256, 0, stream>>>(a);
+        join_kernel<D, F8, 1><<<(unsigned)(grid < 4096 ? grid : 4096), 256, 0, stream>>>(a);
     } else {
-        join_kernel<D, 4><<<(unsigned)(total < 4096 ? total : 4096), 256, 0, stream>>>(a);
+        join_kernel<D, F8, 4><<<(unsigned)(total < 4096 ? total : 4096), 256, 0, stream>>>(a);
     }
 }
 
@@ -769,7 +790,7 @@ hipError_t run_attend_mt(const AttendArgs& a, hipStream_t stream) {
     else run_attend<D, F8, 4>(a, grid, stream);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.parts == 1) return e;
-    run_join<D>(a, stream);
+    run_join<D, F8>(a, stream);
     return hipGetLastError();
 }
 

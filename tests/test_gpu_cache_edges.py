@@ -1,0 +1,105 @@
+"""sv_cache_attend at the sizes, parts, pages and values that the oracle's
+comparisons of random batches do not reach or cannot tell apart."""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from test_gpu_cache import BF, Batch, values
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True, scope="module")
+def _need_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("ctx", [3, 40, 1000, 9000])
+def test_values_at_the_largest(dim, ctx):
+    """Equal scores over values of the bf16 maximum: their mean is that maximum, while
+    their sum is far past fp32."""
+    for n in (1, 300):          # the length split, and not
+        if n * ctx * dim > 3e7:
+            continue
+        b = Batch(57, [2] * n, [ctx] * n, 4, 2, dim, 16)
+        b.q.zero_()
+        most = torch.finfo(BF).max
+        b.v.fill_(most)
+        b.v[..., 1::2] = -most
+        out, lse, _ = b.device().attend()
+        got = values(out)[:2 * n]
+        assert (got[..., ::2] == most).all() and (got[..., 1::2] == -most).all()
+        assert torch.isfinite(lse[:2 * n]).all()
+
+
+@pytest.mark.parametrize("ctx", [3, 1000, 9000])
+def test_values_at_the_smallest(ctx):
+    """Equal scores over values of 2^-104: their mean, with nothing lost on the way."""
+    b = Batch(62, [2], [ctx], 4, 2, 128, 16)
+    b.q.zero_()
+    b.v.fill_(2.0 ** -104)
+    out, _, _ = b.device().attend()
+    assert (values(out)[:2] == 2.0 ** -104).all()
+
+
+def test_sums_that_fill_up():
+    """One part of 300,000 positions a request, of equal scores, then of rising ones: m is
+    raised on the way."""
+    b = Batch(63, [1] * 2, [300000, 299990], 1, 1, 64, 64, extra=0)
+    b.table = b.table.repeat(1024, 1)[:2048].contiguous()      # so many that no length is split
+    b.n, b.rows, b.k_max = 2048, [1] * 2048, 0
+    b.ctx = torch.full((b.n,), 20, dtype=torch.int32)
+    b.ctx[:2] = torch.tensor([300000, 299990])
+    b.cu = torch.arange(b.n + 1, dtype=torch.int32)
+    b.q = torch.zeros(b.n, 1, 64, dtype=BF)
+    assert b.ws() is None
+    b.v.zero_()
+    most = torch.finfo(BF).max
+    b.v[:, :, 0, 0] = 1.0
+    b.v[:, :, 0, 1] = most
+    out, lse, _ = b.device().attend()
+    got = values(out)
+    assert (got[:, 0, 0] == 1.0).all() and (got[:, 0, 1] == most).all()
+    for r, n in ((0, 300001), (1, 299991), (2, 21)):
+        assert abs(float(lse[r]) - math.log(n)) <= 2.0 ** -21 * math.log(n)
+    # position t scores t / 2^14 (18 nats over the length), in steps of 1 / 16
+    b.q[:, 0, 0] = 1.0 / b.scale / 16
+    t = torch.arange(300032)
+    for r in range(2):
+        page = b.table[r, :300032 // 64].long().repeat_interleave(64)
+        b.k[page, t % 64, 0, 0] = (t // 1024).to(BF)
+    b.k[..., 1:] = 0
+    out, lse, _ = b.device().attend()
+    s = (t // 1024).to(BF).double() / 16
+    # a lane adds a sixteenth of the weights one by one: n / 16 roundings of 2^-24
+    added = 300001 / 16 * 2.0 ** -24
+    for r in range(2):
+        want = torch.logsumexp(s[:int(b.ctx[r]) + 1], 0)
+        assert abs(float(lse[r]) - float(want)) <= added + 2.0 ** -21 * float(want)
+    got = values(out)
+    # the weights' rounding and the output's, 2^-8 each
+    assert (np.abs(got[:2, 0, 0] - 1) <= 2 * 2.0 ** -8 + added).all() and np.isfinite(got).all()
+
+
+@pytest.mark.parametrize("heads,kv,rows", [(4, 4, 1), (8, 1, 4), (8, 1, 7)])
+@pytest.mark.parametrize("ctx", [20, 900, 9000])
+def test_large_values_and_uneven_scores(heads, kv, rows, ctx):
+    """Values of 2^124: a few weights more than one and their sum passes fp32."""
+    b = Batch(58, [rows, 1], [ctx, 5], heads, kv, 128, 16)
+    b.v = (b.v.float().clamp(-7, 7) * 2.0 ** 124).to(BF)
+    out, _ = b.device().check()
+    assert torch.isfinite(out).all()
+
+
+def test_large_values_beside_faulty_ones():
+    """Values near the maximum while a later row's value, NaN, is not seen by all rows."""
+    b = Batch(59, [4, 1], [60, 900], 4, 2, 64, 16)
+    b.v = (b.v.float().clamp(-7, 7) * 2.0 ** 124).to(BF)
+    b.v[int(b.table[0, 3]), 62 % 16, :, 5] = float("nan")
+    out, _ = b.device().check()
+    assert torch.isfinite(out[:2]).all() and torch.isnan(out[2:4, :, 5]).all()
