@@ -636,12 +636,14 @@ void attend_kernel(AttendArgs a) {
         if (i >= slots) continue;
         const int row = slot / G, head = h * G + slot % G;
         if (whole) {
-            const float inv = l[mt] == 0.0f ? 0.0f : vscale / l[mt];
+            // the mean first, then its scale: only their product has to be in range
+            const float inv = l[mt] == 0.0f ? 0.0f : 1.0f / l[mt];
             uint32_t w[C::kAcc / 2];
 #pragma unroll
             for (int e = 0; e < C::kAcc; e += 2)
-                w[e / 2] = pack_bf16(acc[mt][e % C::kDpl][e / C::kDpl] * inv,
-                                     acc[mt][(e + 1) % C::kDpl][(e + 1) / C::kDpl] * inv);
+                w[e / 2] =
+                    pack_bf16(acc[mt][e % C::kDpl][e / C::kDpl] * inv * vscale,
+                              acc[mt][(e + 1) % C::kDpl][(e + 1) / C::kDpl] * inv * vscale);
             uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) +
                                                 (int64_t)(lo + row) * a.out_ld +
                                                 (int64_t)head * D + g * C::kAcc);
@@ -662,7 +664,7 @@ void attend_kernel(AttendArgs a) {
                 f32x4 x;
 #pragma unroll
                 for (int i4 = 0; i4 < 4; ++i4)
-                    x[i4] = acc[mt][(e + i4) % C::kDpl][(e + i4) / C::kDpl] * vscale;
+                    x[i4] = acc[mt][(e + i4) % C::kDpl][(e + i4) / C::kDpl];
                 o[e / 4] = x;
             }
             if (g == 0) {
@@ -750,10 +752,11 @@ __global__ __launch_bounds__(256) void join_kernel(AttendArgs a) {
             __syncthreads();
         }
         if (!live || w != 0) continue;
+        const float vscale = F8 && c.v_scale != nullptr ? c.v_scale[head / a.group] : 1.0f;
         uint16_t* out = static_cast<uint16_t*>(a.out) + (int64_t)(lo + row) * a.out_ld +
                         (int64_t)head * D + lane * E;
 #pragma unroll
-        for (int e = 0; e < E; ++e) out[e] = (uint16_t)pack_bf16(o[e], 0.0f);
+        for (int e = 0; e < E; ++e) out[e] = (uint16_t)pack_bf16(o[e] * vscale, 0.0f);
         if (a.out_lse != nullptr && lane == 0)
             a.out_lse[(int64_t)(lo + row) * a.n_heads + head] =
                 l == 0.0f ? -kInf : ((m - kHold) + log2f(l * exp2f(kHold))) * kLn2;

@@ -7,7 +7,7 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_cache import BF, Batch, values
+from test_gpu_cache import BF, F8, Batch, values
 
 pytestmark = pytest.mark.gpu
 
@@ -103,3 +103,14 @@ def test_large_values_beside_faulty_ones():
     b.v[int(b.table[0, 3]), 62 % 16, :, 5] = float("nan")
     out, _ = b.device().check()
     assert torch.isfinite(out[:2]).all() and torch.isnan(out[2:4, :, 5]).all()
+
+
+@pytest.mark.parametrize("ctx", [50, 9000])
+def test_large_value_scale(ctx):
+    """An 8-bit cache whose value scale is 2^115: only the mean has to be in range."""
+    b = Batch(60, [2, 1], [ctx, 20], 4, 2, 128, 16, F8)
+    b.scales[1].fill_(2.0 ** 115)
+    b.q.zero_()
+    b.v.copy_(torch.full(b.v.shape, 448.0))
+    out, _, _ = b.device().attend()
+    assert (values(out)[:3] == 448.0 * 2.0 ** 115).all()
