@@ -636,6 +636,11 @@ void attend_kernel(AttendArgs a) {
         if (i >= slots) continue;
         const int row = slot / G, head = h * G + slot % G;
         if (whole) {
+            // no weight at all: 0, also where 0 times a value was NaN
+            if (l[mt] == 0.0f) {
+#pragma unroll
+                for (int e = 0; e < C::kDpl; ++e) acc[mt][e] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            }
             // the mean first, then its scale: only their product has to be in range
             const float inv = l[mt] == 0.0f ? 0.0f : 1.0f / l[mt];
             uint32_t w[C::kAcc / 2];
@@ -756,7 +761,8 @@ __global__ __launch_bounds__(256) void join_kernel(AttendArgs a) {
         uint16_t* out = static_cast<uint16_t*>(a.out) + (int64_t)(lo + row) * a.out_ld +
                         (int64_t)head * D + lane * E;
 #pragma unroll
-        for (int e = 0; e < E; ++e) out[e] = (uint16_t)pack_bf16(o[e] * vscale, 0.0f);
+        for (int e = 0; e < E; ++e)
+            out[e] = (uint16_t)pack_bf16(l == 0.0f ? 0.0f : o[e] * vscale, 0.0f);
         if (a.out_lse != nullptr && lane == 0)
             a.out_lse[(int64_t)(lo + row) * a.n_heads + head] =
                 l == 0.0f ? -kInf : ((m - kHold) + log2f(l * exp2f(kHold))) * kLn2;

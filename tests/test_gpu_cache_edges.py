@@ -114,3 +114,17 @@ def test_large_value_scale(ctx):
     b.v.copy_(torch.full(b.v.shape, 448.0))
     out, _, _ = b.device().attend()
     assert (values(out)[:3] == 448.0 * 2.0 ** 115).all()
+
+
+@pytest.mark.parametrize("ctx", [0, 40, 3000])
+def test_rows_of_minus_infinity_over_faulty_values(ctx):
+    """All of a row's scores are -inf: it gives 0 and lse -inf whatever the values hold."""
+    b = Batch(61, [1, 1], [ctx, 20], 2, 1, 64, 16)
+    b.q = b.q.abs() + 1
+    for t in range(ctx + 1):
+        b.k[int(b.table[0, t // 16]), t % 16] = -float("inf")
+    b.v[int(b.table[0, 0]), 0, 0, :3] = torch.tensor([float("nan"), float("inf"), -float("inf")])
+    out, lse, err = b.device().attend()
+    assert err == 0
+    assert (out[0] == 0).all() and torch.isneginf(lse[0]).all()
+    assert torch.isfinite(out[1]).all() and torch.isfinite(lse[1]).all()
