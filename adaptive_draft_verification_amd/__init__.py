@@ -598,10 +598,21 @@ def sv_verify_truncated(target, draft, draft_tokens, cu_rows, target_law, draft_
 class PagedCache:
     """A paged key-value cache: k and v [n_pages, page_size, n_kv_heads, head_dim] (bfloat16 or
     float8_e4m3fn), any strides over pages, positions and heads that both share, the last
-    dimension contiguous; k_scale, v_scale [n_kv_heads] f32 (float8 caches)."""
+    dimension contiguous; k_scale, v_scale [n_kv_heads] f32 (float8 caches).
 
-    __slots__ = ("k", "v", "k_scale", "v_scale", "device", "n_kv_heads", "head_dim", "page_size",
-                 "_c", "_at")
+    The tensors' addresses and layout are taken once: they are held and cannot be exchanged
+    (another cache is another PagedCache), and their storage must not be (set_, resize_)."""
+
+    __slots__ = ("_k", "_v", "_k_scale", "_v_scale", "_device", "_n_kv_heads", "_head_dim",
+                 "_page_size", "_c", "_at")
+    k = property(lambda self: self._k)
+    v = property(lambda self: self._v)
+    k_scale = property(lambda self: self._k_scale)
+    v_scale = property(lambda self: self._v_scale)
+    device = property(lambda self: self._device)
+    n_kv_heads = property(lambda self: self._n_kv_heads)
+    head_dim = property(lambda self: self._head_dim)
+    page_size = property(lambda self: self._page_size)
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
         dtype = _CACHE_DTYPES.get(k.dtype)
@@ -613,16 +624,16 @@ class PagedCache:
         if k.dim() != 4 or v.shape != k.shape or v.stride() != strides or strides[3] != 1:
             raise ValueError("k and v must be [n_pages, page_size, n_kv_heads, head_dim] with "
                              "the same strides, the last dimension contiguous")
-        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self.device = k.get_device()
-        n_pages, self.page_size, self.n_kv_heads, self.head_dim = k.shape
+        self._k, self._v, self._k_scale, self._v_scale = k, v, k_scale, v_scale
+        self._device = k.get_device()
+        n_pages, self._page_size, self._n_kv_heads, self._head_dim = k.shape
         if dtype == SV_BF16 and (k_scale is not None or v_scale is not None):
             raise ValueError("scales belong to float8 caches")
-        heads = (self.n_kv_heads,)
-        self._c = _Cache(k.data_ptr(), v.data_ptr(), dtype, n_pages, self.page_size,
-                         self.n_kv_heads, self.head_dim, strides[0], strides[1], strides[2],
-                         _on(k_scale, torch.float32, "k_scale", self.device, heads),
-                         _on(v_scale, torch.float32, "v_scale", self.device, heads))
+        heads = (self._n_kv_heads,)
+        self._c = _Cache(k.data_ptr(), v.data_ptr(), dtype, n_pages, self._page_size,
+                         self._n_kv_heads, self._head_dim, strides[0], strides[1], strides[2],
+                         _on(k_scale, torch.float32, "k_scale", self._device, heads),
+                         _on(v_scale, torch.float32, "v_scale", self._device, heads))
         self._at = ctypes.addressof(self._c)
 
 
@@ -653,10 +664,10 @@ def sv_cache_append(cache, page_table, k, v, row_req, row_pos, ctx_len, dev_erro
     """Rows k, v [rows, n_kv_heads, head_dim] bf16 into the cache, row i at position
     ctx_len[row_req[i]] + row_pos[i] (the maps pack_varlen writes; -1: skipped);
     page_table [n, max_pages] i32, ctx_len [n] i32."""
-    device = cache.device
+    device = cache._device
     table, n, max_pages = _table(page_table, device)
-    k_at, ld = _rows(k, "k", device, cache.n_kv_heads, cache.head_dim)
-    v_at, v_ld = _rows(v, "v", device, cache.n_kv_heads, cache.head_dim)
+    k_at, ld = _rows(k, "k", device, cache._n_kv_heads, cache._head_dim)
+    v_at, v_ld = _rows(v, "v", device, cache._n_kv_heads, cache._head_dim)
     rows = k.shape[0]
     if v_ld != ld or v.shape[0] != rows:
         raise ValueError("k and v must have the same rows and row stride")
@@ -679,13 +690,13 @@ def sv_cache_attend(cache, page_table, q, cu_rows, ctx_len, k_max, scale, out, w
     (packed row cu_rows[r] + j) sees the cache's positions 0 .. ctx_len[r] + j.
     ws: uint8 device buffer of sv_cache_attend_workspace_bytes(...) bytes (None if 0);
     out_lse [rows, n_heads] f32."""
-    device = cache.device
+    device = cache._device
     table, n, max_pages = _table(page_table, device)
     if q.dim() != 3 or out.shape != q.shape:
         raise ValueError("q must be [rows, n_heads, head_dim] and out of its shape")
     rows, heads, _ = q.shape
-    q_at, q_ld = _rows(q, "q", device, heads, cache.head_dim)
-    out_at, out_ld = _rows(out, "out", device, heads, cache.head_dim)
+    q_at, q_ld = _rows(q, "q", device, heads, cache._head_dim)
+    out_at, out_ld = _rows(out, "out", device, heads, cache._head_dim)
     _launch(_lib.sv_cache_attend, "sv_cache_attend", device, stream, cache._at, table, max_pages,
             q_at, q_ld, rows, heads, _on(cu_rows, torch.int32, "cu_rows", device, (n + 1,)),
             _on(ctx_len, torch.int32, "ctx_len", device, (n,)), n, int(k_max), float(scale),
