@@ -128,3 +128,36 @@ def test_rows_of_minus_infinity_over_faulty_values(ctx):
     assert err == 0
     assert (out[0] == 0).all() and torch.isneginf(lse[0]).all()
     assert torch.isfinite(out[1]).all() and torch.isfinite(lse[1]).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F8])
+@pytest.mark.parametrize("dim,heads,rows", [(64, 1, 1), (128, 8, 4), (128, 8, 7), (256, 4, 2)])
+@pytest.mark.parametrize("gap", [0.3, 1.1, 2.7])
+def test_weights_keep_sixteen_bits(dtype, dim, heads, rows, gap):
+    """Two scores `gap` apart over values of +1 and -1 that nearly cancel: every weight of the
+    smaller score is rounded the same way, so their rounding shows in the output (2^-16 of the
+    weighted mean of |v| for two bf16 terms; the scores' own rounding is below 2^-20 of it)."""
+    ctx = 900
+    b = Batch(64, [rows], [ctx], heads, 1, dim, 16, dtype)
+    if b.scales:
+        for s in b.scales:
+            s.fill_(1.0)
+    b.q.zero_()
+    b.q[:, :, 0] = 1.0
+    b.scale = float(np.float32(gap / 16))
+    bits = lambda t: t.view(torch.uint8 if dtype == F8 else torch.int16)  # noqa: E731
+    bits(b.k).zero_()
+    one = torch.tensor([1.0, -1.0, -16.0]).to(dtype)
+    low = round(math.exp(gap) / (1 + math.exp(gap)) * ctx)      # so many of the smaller weight
+    for t in range(ctx + rows):
+        p, s = int(b.table[0, t // 16]), t % 16
+        bits(b.v)[p, s] = bits(one)[1 if t < low else 0]
+        if t < low:
+            bits(b.k)[p, s, 0, 0] = bits(one)[2]
+    out, _, _ = b.device().attend()
+    (o, _, spread), _ = b.expect()
+    got = values(out)[:rows]
+    # of the inputs alone: nearly balanced, and each later row adds one more value of +1
+    assert (np.abs(o[:rows]) < 0.02 * rows).all()
+    tol = 2.0 ** -8 * np.abs(o[:rows]) + (2.0 ** -16 + 2.0 ** -20) * spread[:rows]
+    assert (np.abs(got - o[:rows]) <= tol).all(), np.max(np.abs(got - o[:rows]) / tol)
