@@ -1,5 +1,4 @@
-"""sv_cache_attend at the sizes, parts, pages and values that the oracle's
-comparisons of random batches do not reach or cannot tell apart."""
+"""sv_cache_attend at values near the types' limits, and the bits its weights keep."""
 
 import math
 
