@@ -547,7 +547,8 @@ def _logits(t, name, vocab):
 def sv_sample(logits, u, law, out_tokens, out_prob=None, out_support=None, dev_error=None,
               vocab=None, stream=None):
     """logits [rows, >=V] (bf16 or f32), u [rows] f32 in [0, 1) -> out_tokens [rows] i32 drawn
-    under law (a Sampling or None), out_prob [rows] f32, out_support [rows] i32."""
+    under law (a Sampling or None), out_prob [rows] f32, out_support [rows] i32.
+    u of drafts: not the uniforms of the (seed, step) that verifies them."""
     at, ld, n = _logits(logits, "logits", vocab)
     device, rows = logits.get_device(), (n,)
     _launch(_lib.sv_sample, "sv_sample", device, stream, at, ld, n, _DTYPES[logits.dtype],

@@ -511,7 +511,8 @@ sv_status sv_calibrate_predict(const float* theta, const float* q_draft, const f
  * (sv_verify_truncated); NULL: 1, off, 1 and 0.  A row or request whose
  * temperature is negative or not finite, top_p negative or NaN, or min_p
  * outside [0, 1] is faulty (SV_DEV_BAD_PARAM).
- * Numerics: weights, sums and borders in 64 bits, whatever the logits' type.
+ * Numerics: weights, sums and borders in 64 bits, whatever the logits' type; a
+ * weight is within 4e-14 of its value (relative).
  */
 typedef struct {
     const float* temperature;
@@ -531,7 +532,10 @@ typedef struct {
  * total, as sv_verify draws.
  * logits:  [n_rows] rows of vocab values, ld apart; rows need no alignment.
  * law:     host pointer to the settings, or NULL (softmax at temperature 1).
- * u:       [n_rows] fp32 in [0, 1) (sv_philox_uniforms draws such).
+ * u:       [n_rows] fp32 in [0, 1), as sv_philox_uniforms draws them.  For a
+ *          draft not with the (seed, step) that will verify it: that call tests
+ *          draft j with the same u_j it was drawn from, and what it emits no
+ *          longer follows the target's law.  Another seed for drafts will do.
  * out_tokens: [n_rows] int32.   out_prob: [n_rows] fp32, the token's
  *          probability under the law, or NULL.   out_support: [n_rows] int32,
  *          how many ids the law leaves, or NULL.
@@ -539,7 +543,9 @@ typedef struct {
  * uniform outside [0, 1) (SV_DEV_BAD_PARAM) gives -1 in all of them.
  * Repeated calls agree bit for bit.
  * Launch: one kernel, one workgroup a row (1024 threads; 512 above 256 rows);
- * no workspace.
+ * no workspace.  Settings that leave much of a row take several passes over it:
+ * top_k of more than half the threads, and fp32 rows under top_p whose border
+ * lies among thousands of near-equal weights (temperatures of 2 and more).
  * Errors: SV_ERR_NULL; SV_ERR_DTYPE; SV_ERR_SHAPE.
  */
 sv_status sv_sample(const void* logits, int64_t ld, int32_t n_rows, sv_dtype dtype,
