@@ -195,9 +195,10 @@ struct Attend {
 };
 
 // The request of rank `rank` by context length, longest first (ties to the
-// lower request), for up to 256 requests: where workgroups take turns on the
-// CUs, a long request that starts last would be waited for alone (256 requests
-// of 0 .. 4096 positions: 429 us in their own order, 394 this way).
+// lower request): where workgroups take turns on the CUs, a long request that
+// starts last would be waited for alone (256 requests of 0 .. 4096 positions: 429
+// us in their own order, 394 this way).  For up to 256 requests, a thread each;
+// more keep their own order (256 requests 410 us, 257 441).
 __device__ __forceinline__ int longest(int rank, const int32_t* ctx_len, int n, int* lens) {
     __shared__ int found;
     const int t = threadIdx.x;
@@ -219,7 +220,7 @@ __device__ __forceinline__ int longest(int rank, const int32_t* ctx_len, int n, 
 // Consecutive workgroups go to the eight XCDs in turn, each with an L2 of its
 // own; `run` neighbouring work items that read the same lines (slot blocks of
 // a head, heads narrower than a line) are given to one XCD, one behind the
-// other: 64 requests, 16 heads of 64 bytes: 42 us without, 31 with.
+// other: 64 requests, 16 heads of 64 bytes: 42 us without, 29 with.
 __device__ __forceinline__ int spread(int b, int total, int run) {
     const int group = 8 * run, g = b / group, rest = b - g * group;
     if ((g + 1) * group > total) return b;

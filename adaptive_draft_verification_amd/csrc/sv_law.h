@@ -14,24 +14,28 @@
 // their order does not change them.
 //
 // One workgroup takes a row.  Four ways to the border, by what the settings ask
-// for (times: 256 rows, one a workgroup; the pass over memory that finds the
-// largest logit and the faults is part of each):
+// for (times: calls of 256 rows, one a workgroup, normal logits of spread 3, T =
+// 1; the pass over memory that finds the largest logit and the faults is part of
+// each):
 //  - T = 0, top-k up to the workgroup's threads, or min-p: a bound that costs no
 //    pass (the largest logit, the k-th largest of the threads' own maxima,
 //    min-p's logit) leaves a few candidates, which are gathered in LDS, ranked by
-//    counting and summed there (129,280 bf16: 17, 24, 36 us; 256,000 fp32: 44,
-//    54, 65);
+//    counting and summed there (T = 0, top-k of 50, min-p of 0.05: 129,280 bf16
+//    17, 24, 34 us; 256,000 fp32 44, 54, 67).  Near the thread count top-k leaves
+//    more of them than the list holds (of 1024 threads: 50 us at 512, 131 at 1024);
 //  - bf16, top-p alone, and no cut where no draw follows: how many ids have each
 //    value, counted in the first pass, gives the sum and the border (by_value();
-//    47 us with a draw);
+//    53 us with a draw; 67 at T = 2, 98 at T = 5, where more than 256 ids lie below
+//    the 16 octaves of values and are counted over);
 //  - fp32, top-p alone, and no cut: the first pass takes the sum, and top-p's
 //    histogram over 2048 steps of the weight (2^(1/32) each); the steps next to
 //    the border are gathered and searched like candidates while the ids above
-//    them are summed (find_nucleus(); 130 us, 71 without top-p);
-//  - anything else, and what does not fit the lists (long runs of equal logits):
+//    them are summed (find_nucleus(); 134 us, 69 without top-p);
+//  - anything else, and what does not fit the lists (long runs of equal logits,
+//    fp32 top-p with thousands of ids in the border's step, 807 us at T = 2):
 //    the border is found digit by digit, 256 bins over 8 bits of the ordered key,
 //    then the next 8 bits within the bin that holds the border (top-k of 2000 of
-//    129,280 bf16: 131 us).
+//    129,280 bf16: 128 us).
 #pragma once
 
 #include "sv_device.h"
@@ -1263,9 +1267,13 @@ __device__ __forceinline__ Result find_law(const Row<DT, NT>& row, const Setting
     // Pass 1: largest logit, faults; and where nothing but top-p may cut, what
     // needs every id, taken relative to the largest of the first ids: the values
     // of a bf16 row that by_value() decides, in a range twice as far as that one
-    // asks for (256 x 7 laws of top-p, 129,280 ids, as first measured: 338 us against 384 with a
-    // pass of its own); else the sum of the weights, by wave, and top-p's
-    // histogram.
+    // asks for; else the sum of the weights, by wave, and top-p's histogram.
+    // Loads in flight while values are counted: eight without a draw (verification
+    // of 256 x 7 rows under top-p: 308 us, 313 with four, 331 with two); two with
+    // one, where more make the kernel's other ways slower (2048 rows, greedy: 94
+    // us, 104 with four or eight; top-k: 127, 144 and 143) than top-p gains (341,
+    // 327 and 327).  Two of bf16 and four of fp32 while weights are summed: twice
+    // or four times as many measured the same within 3 %.
     const bool use_p = set.p < 1.0f;
     Extremes<DT> ex, batch;
     uint32_t base = 0;

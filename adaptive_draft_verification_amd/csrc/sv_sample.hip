@@ -40,9 +40,12 @@ void run(const SampleArgs& a, hipStream_t stream) {
 hipError_t launch_sample(const SampleArgs& a, hipStream_t stream) {
     // Up to a workgroup for each CU, a row's own time counts: 1024 threads.
     // More rows share a CU: two workgroups of 512 threads, one summing while
-    // the other waits for memory (129,280 bf16 ids under top-p, 512 threads
-    // against 1024 as first measured: 2048 rows 551 us against 659, 256 rows 92
-    // against 85).
+    // the other waits for memory.  129,280 bf16 ids, 512 threads against 1024: 256
+    // rows under top-p 74.7 us against 58.4, top-k 27.7 against 26.6, at a
+    // temperature alone 44 against 39; 257 rows 76 against 77, 29 against 34, 66
+    // against 70; 2048 rows 341 against 417, 125 against 167, 254 against 297;
+    // 1024 rows of 256,000 fp32 ids under top-p 496 against 560.  (The exception
+    // found: 257 .. 512 rows of settings mixed in turn, 74 against 57 us at 257.)
     // Rows of fewer than 8 ids: one wave each.
     if (a.vocab < 8) run<kWave>(a, stream);
     else if (a.n_rows > law::kCUs) run<512>(a, stream);

@@ -50,7 +50,7 @@ struct AttendArgs {
     int page_shift;                      // log2 of the page size, -1 if it is no power of two
     int slot_tiles, slot_blocks, parts, part_min;  // AttendPlan's
     float* part_out;                     // parts > 1: [n_req, n_heads, k_max + 1, parts, head_dim]
-    float* part_ml;                      //            [..., parts, 2] maximum and sum
+    float* part_ml;                      //            [..., parts, 2] m and sum
 };
 hipError_t launch_cache_attend(const AttendArgs& a, hipStream_t stream);
 
@@ -77,9 +77,16 @@ struct AttendPlan {
         // caches) keep that to a sixteenth of the reads
         const int block = slots < 16 * slot_tiles ? slots : 16 * slot_tiles;
         part_min = (32 * (esize == 1 ? 2 : 1) * block + 127) / 128 * 128;
-        // Parts until there are about 1024 workgroups, four for a CU (3 requests
-        // of 100,005 positions, 8 kv heads, e4m3: 168-176 us for 512, 141 for
-        // 1024, 159 for 2048, 157 for 8192).
+        // Parts until there are about 1024 workgroups, four for a CU, at most 128
+        // (two factors a lane of the join).  Measured with 256, 512, 1024 and 2048:
+        // e4m3, whose conversions want waves, 3 requests of 100,005 positions 198,
+        // 182, 154, 165 us, 16 of 4001 42, 30, 36, 39; bf16, 1 request of 16,001
+        // 20, 22, 29, 29, 16 of 4001 47, 50, 49, 55, 64 of 2001 102, 102, 107, 112,
+        // 1 of 131,001 108, 110, 117, 116.  The cap leaves CUs idle at one kv head
+        // (131,001 positions: 31 us, 2.2 TB/s; two heads 37, 3.6; eight 118, 4.6).
+        // Lengths are not known here: a batch that fills the chip is not split,
+        // and waits for a request much longer than the rest (255 of up to 2000
+        // positions 204 us, with one of 32,000 588, of 100,000 1553).
         const int64_t groups = (int64_t)n_req * n_kv_heads * slot_blocks;
         const int64_t want = groups > 0 ? (1024 + groups - 1) / groups : 1;
         const int64_t most = (capacity + part_min - 1) / part_min;
