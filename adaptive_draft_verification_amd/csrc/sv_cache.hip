@@ -479,7 +479,7 @@ void attend_kernel(AttendArgs a) {
             }
             poison = __ballot(poison) != 0;
         }
-        bf16x8 pb[MT], pr[MT];  // the weights, and what their rounding left
+        bf16x8 pb[MT], pr[MT];  // the weights' upper halves and rests
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
             if (mt * 16 >= slots) break;
@@ -521,16 +521,22 @@ void attend_kernel(AttendArgs a) {
                 p[j] = fast_exp2(p[j] - mu[mt]);
                 l[mt] += p[j];
             }
-            // Weights go into the matrix product as two bf16 terms, off by at
-            // most 2^-16 of each.  One term (2^-8) let the error against 64 bits
-            // grow by up to a quarter; the second costs 0 .. 2 % where reading
-            // bounds the call (256 requests, ctx 4096: 392.0 and 393.7 us; 3 x
-            // 100,005 e4m3: 141.4 and 144.8), 8 % at four slot tiles.
+            // Weights go into the matrix product as two bf16 terms, the upper
+            // half of the fp32 weight and the rest, off by at most 2^-15 of each.
+            // Both are positive where the weight is (the rest of 1 + 2^-23 times
+            // it is taken): an infinite value times 0 or a negative rest would
+            // make NaN.  One term (2^-8) let the error against 64 bits grow by up
+            // to a quarter; the second costs 0 .. 2 % where reading bounds the
+            // call (256 requests, ctx 4096: 392.0 and 393.7 us; 3 x 100,005 e4m3:
+            // 141.4 and 144.8), 8 % at four slot tiles.
+            constexpr float kOneUp = 1.0f + 0x1p-23f;
             uint32_t hw[4], rw[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                hw[i] = pack_bf16(p[2 * i], p[2 * i + 1]);
-                rw[i] = pack_bf16(p[2 * i] - bf16_lo(hw[i]), p[2 * i + 1] - bf16_hi(hw[i]));
+                const uint32_t a = __float_as_uint(p[2 * i]), b = __float_as_uint(p[2 * i + 1]);
+                hw[i] = __builtin_amdgcn_perm(b, a, 0x07060302u);
+                rw[i] = pack_bf16(fmaf(p[2 * i], kOneUp, -bf16_hi(a)),
+                                  fmaf(p[2 * i + 1], kOneUp, -bf16_hi(b)));
             }
             pb[mt] = as_bf16x8(hw[0], hw[1], hw[2], hw[3]);
             pr[mt] = as_bf16x8(rw[0], rw[1], rw[2], rw[3]);

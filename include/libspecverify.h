@@ -665,9 +665,10 @@ sv_status sv_cache_append(const sv_cache* cache, const int32_t* page_table, int3
  * written.
  * Numerics: products of bf16 values (an 8-bit cache's values are exact in
  * bf16) summed in fp32; maxima, sums and merges in fp32; the weights e^(s_i -
- * max) as two bf16 terms (2^-16 of each at most) for the product with v.  Sums of v stay in fp32's range
- * however large its finite values are; bf16 values below 2^-92 may lose bits, and
- * weights below 2^-92 of the largest may count as 0.  Repeated calls agree bit for
+ * max) as two bf16 terms (2^-15 of each at most) for the product with v.  Sums
+ * of v stay in fp32's range however large its finite values are; bf16 values
+ * below 2^-92 may lose bits, and weights below 2^-92 of the largest (beside
+ * infinite values, below 2^-69) may count as 0.  Repeated calls agree bit for
  * bit.
  * ws:      sv_cache_attend_workspace_bytes(...) bytes, 16-byte aligned (0:
  *          NULL will do), uninitialised.  Calls that overlap in time must not

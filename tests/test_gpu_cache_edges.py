@@ -134,8 +134,9 @@ def test_rows_of_minus_infinity_over_faulty_values(ctx):
 @pytest.mark.parametrize("gap", [0.3, 1.1, 2.7])
 def test_weights_keep_sixteen_bits(dtype, dim, heads, rows, gap):
     """Two scores `gap` apart over values of +1 and -1 that nearly cancel: every weight of the
-    smaller score is rounded the same way, so their rounding shows in the output (2^-16 of the
-    weighted mean of |v| for two bf16 terms; the scores' own rounding is below 2^-20 of it)."""
+    smaller score is rounded the same way, so their rounding shows in the output (2^-15 of each
+    for two bf16 terms, and they are half of the weighted mean of |v|; the scores' own rounding
+    is below 2^-20 of it)."""
     ctx = 900
     b = Batch(64, [rows], [ctx], heads, 1, dim, 16, dtype)
     if b.scales:
@@ -160,3 +161,21 @@ def test_weights_keep_sixteen_bits(dtype, dim, heads, rows, gap):
     assert (np.abs(o[:rows]) < 0.02 * rows).all()
     tol = 2.0 ** -8 * np.abs(o[:rows]) + (2.0 ** -16 + 2.0 ** -20) * spread[:rows]
     assert (np.abs(got - o[:rows]) <= tol).all(), np.max(np.abs(got - o[:rows]) / tol)
+
+
+@pytest.mark.parametrize("scores", ["equal", "random"])
+@pytest.mark.parametrize("dim,heads,rows", [(64, 1, 1), (128, 8, 4), (128, 8, 7), (256, 4, 2)])
+@pytest.mark.parametrize("ctx", [100, 5000])
+def test_infinite_values_that_every_row_sees(scores, dim, heads, rows, ctx):
+    """A value of inf or -inf far inside the context goes into every row's output as itself,
+    one of each sign in one dim as NaN."""
+    b = Batch(65, [rows, 1], [ctx, 40], heads, 1, dim, 16, qscale=0.3)
+    if scores == "equal":
+        b.q.zero_()
+    inf = float("inf")
+    for t, d, x in ((3, 0, inf), (37, 1, -inf), (38, 2, inf), (39, 2, -inf), (ctx - 40, 3, inf)):
+        b.v[int(b.table[0, t // 16]), t % 16, 0, d] = x
+    got = values(b.device().attend()[0])
+    assert (got[:rows, :, [0, 3]] == inf).all() and (got[:rows, :, 1] == -inf).all()
+    assert np.isnan(got[:rows, :, 2]).all()
+    assert np.isfinite(got[:rows, :, 4:]).all() and np.isfinite(got[rows]).all()
