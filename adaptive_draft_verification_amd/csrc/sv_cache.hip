@@ -198,7 +198,7 @@ struct Attend {
 // lower request): where workgroups take turns on the CUs, a long request that
 // starts last would be waited for alone (256 requests of 0 .. 4096 positions: 429
 // us in their own order, 394 this way).  For up to 256 requests, a thread each;
-// more keep their own order (256 requests 410 us, 257 441).
+// more keep their own order (256 requests 393 us, 257 424).
 __device__ __forceinline__ int longest(int rank, const int32_t* ctx_len, int n, int* lens) {
     __shared__ int found;
     const int t = threadIdx.x;

@@ -83,10 +83,10 @@ struct AttendPlan {
         // 182, 154, 165 us, 16 of 4001 42, 30, 36, 39; bf16, 1 request of 16,001
         // 20, 22, 29, 29, 16 of 4001 47, 50, 49, 55, 64 of 2001 102, 102, 107, 112,
         // 1 of 131,001 108, 110, 117, 116.  The cap leaves CUs idle at one kv head
-        // (131,001 positions: 31 us, 2.2 TB/s; two heads 37, 3.6; eight 118, 4.6).
+        // (131,001 positions: 31 us, 2.2 TB/s; two heads 37, 3.6; eight 117, 4.6).
         // Lengths are not known here: a batch that fills the chip is not split,
         // and waits for a request much longer than the rest (255 of up to 2000
-        // positions 204 us, with one of 32,000 588, of 100,000 1553).
+        // positions 200 us, with one of 32,000 585, of 100,000 1550).
         const int64_t groups = (int64_t)n_req * n_kv_heads * slot_blocks;
         const int64_t want = groups > 0 ? (1024 + groups - 1) / groups : 1;
         const int64_t most = (capacity + part_min - 1) / part_min;
