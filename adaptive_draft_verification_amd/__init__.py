@@ -26,13 +26,14 @@ SV_F32, SV_BF16, SV_E4M3 = 0, 1, 2
 SV_STOCHASTIC, SV_GREEDY = 0, 1
 SV_DEV_BAD_CU_ROWS, SV_DEV_BAD_TOKEN, SV_DEV_NONFINITE = 1, 2, 4
 SV_DEV_BAD_DRAFT_LEN, SV_DEV_BAD_COST, SV_DEV_BAD_KEPT = 8, 16, 32
-SV_DEV_BAD_PAGE, SV_DEV_BAD_CTX, SV_DEV_BAD_PARAM = 64, 128, 256
+SV_DEV_BAD_PAGE, SV_DEV_BAD_CTX, SV_DEV_BAD_PARAM, SV_DEV_BAD_SLOT = 64, 128, 256, 512
 SV_MAX_BUDGET_SLOTS, SV_MAX_DRAFT, SV_MAX_VOCAB = 8192, 64, 1048576
 SV_MAX_VERIFY_SLOTS = 524288
 SV_NOALLOC_WS_BYTES = 8388608
 SV_MAX_ATTEND_SLOTS, SV_MAX_CONTEXT = 16777215, 2147418112
 SV_MAX_APPEND_VALUES = 1073741824
 SV_MAX_SAMPLE_ROWS = 4194303
+SV_MAX_HISTORY_TOKENS = 1073741824
 
 EXPORTED = ["sv_status_str", "sv_budget_workspace_bytes", "sv_verify_workspace_bytes",
             "sv_cost_table_prepare", "sv_budget_select", "sv_budget_allocate",
@@ -42,7 +43,8 @@ EXPORTED = ["sv_status_str", "sv_budget_workspace_bytes", "sv_verify_workspace_b
             "sv_verify_stages", "sv_verify_noalloc", "sv_accept_stats", "sv_calibrate_update", "sv_calibrate_predict",
             "sv_philox_uniforms",
             "sv_cache_append", "sv_cache_attend", "sv_cache_attend_workspace_bytes",
-            "sv_sample", "sv_verify_truncated", "sv_verify_truncated_workspace_bytes"]
+            "sv_sample", "sv_verify_truncated", "sv_verify_truncated_workspace_bytes",
+            "sv_history_clear", "sv_history_add", "sv_adjust_logits"]
 
 
 class _Cache(ctypes.Structure):
@@ -59,6 +61,31 @@ class _Law(ctypes.Structure):
     """sv_sampling of the C header."""
     _fields_ = [("temperature", ctypes.c_void_p), ("top_k", ctypes.c_void_p),
                 ("top_p", ctypes.c_void_p), ("min_p", ctypes.c_void_p)]
+
+
+class _History(ctypes.Structure):
+    """sv_history of the C header."""
+    _fields_ = [("counts", ctypes.c_void_p), ("seen", ctypes.c_void_p),
+                ("n_seen", ctypes.c_void_p), ("n_slots", ctypes.c_int32),
+                ("vocab", ctypes.c_int32), ("cap", ctypes.c_int32)]
+
+
+class _Penalties(ctypes.Structure):
+    """sv_penalties of the C header."""
+    _fields_ = [("repetition", ctypes.c_void_p), ("frequency", ctypes.c_void_p),
+                ("presence", ctypes.c_void_p)]
+
+
+class _Bias(ctypes.Structure):
+    """sv_bias of the C header."""
+    _fields_ = [("start", ctypes.c_void_p), ("ids", ctypes.c_void_p),
+                ("values", ctypes.c_void_p), ("n_entries", ctypes.c_int32)]
+
+
+class _TokenMask(ctypes.Structure):
+    """sv_token_mask of the C header."""
+    _fields_ = [("bits", ctypes.c_void_p), ("ld", ctypes.c_int64), ("n_masks", ctypes.c_int32),
+                ("row_mask", ctypes.c_void_p)]
 
 
 class SvError(RuntimeError):
@@ -113,6 +140,10 @@ def _load():
         "sv_verify_truncated": (ctypes.c_int, [vp, i64, i64, vp, i64, ctypes.c_int, i32, vp, vp,
                                                i32, i32, vp, vp, u64, u64, vp, vp, vp, vp, vp, vp,
                                                vp, sz, vp]),
+        "sv_history_clear": (ctypes.c_int, [vp, vp, i32, vp, vp]),
+        "sv_history_add": (ctypes.c_int, [vp, vp, vp, i64, i32, i32, i32, vp, vp]),
+        "sv_adjust_logits": (ctypes.c_int, [vp, i64, vp, i64, i32, ctypes.c_int, i32, vp, vp, i32,
+                                            i32, vp, vp, vp, vp, vp, vp, vp, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -594,6 +625,153 @@ def sv_verify_truncated(target, draft, draft_tokens, cu_rows, target_law, draft_
             _on(out_residual_mass, torch.float32, "out_residual_mass", device, (n,)),
             _on(dev_error, torch.int32, "dev_error", device, None),
             _on(ws, torch.uint8, "ws", device, None), 0 if ws is None else ws.numel())
+
+
+class TokenHistory:
+    """What requests have said: counts [n_slots, vocab] i32, seen [n_slots, cap] i32, n_seen
+    [n_slots] i32, as sv_history describes them (start with zeroed counts and n_seen).
+
+    The tensors' addresses are taken once: they cannot be exchanged, and their storage must not
+    be (set_, resize_)."""
+
+    __slots__ = ("_counts", "_seen", "_n_seen", "_device", "_vocab", "_c", "_at")
+    counts = property(lambda self: self._counts)
+    seen = property(lambda self: self._seen)
+    n_seen = property(lambda self: self._n_seen)
+    device = property(lambda self: self._device)
+    vocab = property(lambda self: self._vocab)
+
+    def __init__(self, counts, seen, n_seen):
+        if not counts.is_cuda or counts.dim() != 2 or seen.dim() != 2:
+            raise ValueError("counts must be [n_slots, vocab] and seen [n_slots, cap] device tensors")
+        self._counts, self._seen, self._n_seen = counts, seen, n_seen
+        self._device = counts.get_device()
+        n_slots, self._vocab = counts.shape
+        cap = seen.shape[1]
+        self._c = _History(_on(counts, torch.int32, "counts", self._device, None),
+                           _on(seen, torch.int32, "seen", self._device, (n_slots, cap)),
+                           _on(n_seen, torch.int32, "n_seen", self._device, (n_slots,)), n_slots,
+                           self._vocab, cap)
+        self._at = ctypes.addressof(self._c)
+
+    @classmethod
+    def empty(cls, n_slots, vocab, cap=None, device="cuda"):
+        """A history of empty slots; cap: ids a slot lists (None: every id fits)."""
+        return cls(torch.zeros(n_slots, vocab, dtype=torch.int32, device=device),
+                   torch.zeros(n_slots, vocab if cap is None else cap, dtype=torch.int32,
+                               device=device),
+                   torch.zeros(n_slots, dtype=torch.int32, device=device))
+
+
+def sv_history_clear(history, slots, dev_error=None, stream=None):
+    """Empties the slots named by slots [n] i32."""
+    device = history._device
+    at = _on(slots, torch.int32, "slots", device, (slots.numel(),))
+    _launch(_lib.sv_history_clear, "sv_history_clear", device, stream, history._at, at,
+            slots.shape[0], _on(dev_error, torch.int32, "dev_error", device, None))
+
+
+def sv_history_add(history, slots, tokens, in_prompt=False, dev_error=None, stream=None):
+    """tokens [n, width] i32 (-1: skipped) added to slots [n] i32 (None: row r to slot r), as
+    the prompt's ids or as emitted ones."""
+    device = history._device
+    if tokens.dim() != 2:
+        raise ValueError("tokens must have 2 dimensions")
+    n, width = tokens.shape
+    ld = width
+    if not tokens.is_contiguous():
+        if tokens.dtype is not torch.int32 or tokens.get_device() != device \
+                or (width > 1 and tokens.stride(1) != 1) or (n > 1 and tokens.stride(0) < width):
+            raise ValueError("tokens must be int32 rows on the history's device")
+        ld, at = (tokens.stride(0) if n > 1 else width), tokens.data_ptr()
+    else:
+        at = _on(tokens, torch.int32, "tokens", device, None)
+    _launch(_lib.sv_history_add, "sv_history_add", device, stream, history._at,
+            _on(slots, torch.int32, "slots", device, (n,)), at, ld, n, width, int(bool(in_prompt)),
+            _on(dev_error, torch.int32, "dev_error", device, None))
+
+
+class Penalties(NamedTuple):
+    """Per-request penalties [n] f32, each a device tensor or None: repetition (None: 1),
+    frequency (None: 0), presence (None: 0)."""
+    repetition: Optional[torch.Tensor] = None
+    frequency: Optional[torch.Tensor] = None
+    presence: Optional[torch.Tensor] = None
+
+
+class Bias(NamedTuple):
+    """Per-request biases: request r's are entries start[r] .. start[r + 1] - 1 of ids (i32,
+    ascending, each once) and values (f32, finite or -inf); start [n + 1] i32."""
+    start: torch.Tensor
+    ids: torch.Tensor
+    values: torch.Tensor
+
+
+class TokenMask(NamedTuple):
+    """Allowed ids: bits [masks, >= ceil(vocab / 32)] i32 (id x: bit x % 32 of word x // 32),
+    row_mask [rows] i32: each row's mask, -1: none (None: row i has mask i)."""
+    bits: torch.Tensor
+    row_mask: Optional[torch.Tensor] = None
+
+
+def sv_adjust_logits(logits, out, row_req, row_pos, history=None, slots=None, penalties=None,
+                     draft_tokens=None, bias=None, mask=None, dev_error=None, n_req=None,
+                     stream=None):
+    """logits [rows, V] (bf16 or f32) -> out (the same shape and type; out = logits: in place)
+    under the requests' penalties, biases and grammar masks.  Row i is position row_pos[i] of
+    request row_req[i] (-1: skipped; both None: row i is request i); the drafts before a row's
+    position (draft_tokens [n, k_max] i32) count as said.  history, slots [n] i32: what was said
+    before.  n_req: needed where no other argument tells it."""
+    at, ld, rows = _logits(logits, "logits", None)
+    out_at, out_ld, _ = _logits(out, "out", None)
+    device, V = logits.get_device(), logits.shape[1]
+    if out.shape != logits.shape or out.dtype is not logits.dtype or out.get_device() != device:
+        raise ValueError("out must be of the logits' shape and type, on their device")
+    k_max, drafts = 0, None
+    if draft_tokens is not None:
+        if draft_tokens.dim() != 2:
+            raise ValueError("draft_tokens must have 2 dimensions")
+        drafts = _on(draft_tokens, torch.int32, "draft_tokens", device, None)
+        n, k_max = draft_tokens.shape
+    elif n_req is not None:
+        n = int(n_req)
+    elif slots is not None:
+        n = slots.shape[0]
+    elif row_req is None:
+        n = rows
+    elif bias is not None:
+        n = bias.start.shape[0] - 1
+    else:
+        raise ValueError("n_req is needed without draft_tokens, slots and bias")
+    if n_req is not None and n != n_req:
+        raise ValueError("draft_tokens must have n_req rows")
+    if history is not None and history._device != device:
+        raise ValueError("the history must be on the logits' device")
+    pen = b = m = None
+    if penalties is not None:
+        pen = _Penalties(*(_on(x, torch.float32, f"penalties.{name}", device, (n,))
+                           for name, x in zip(Penalties._fields, penalties)))
+    if bias is not None:
+        entries = bias.ids.numel()
+        b = _Bias(_on(bias.start, torch.int32, "bias.start", device, (n + 1,)),
+                  _on(bias.ids, torch.int32, "bias.ids", device, (entries,)),
+                  _on(bias.values, torch.float32, "bias.values", device, (entries,)), entries)
+    if mask is not None:
+        bits = _on(mask.bits, torch.int32, "mask.bits", device, None)
+        if mask.bits.dim() != 2:
+            raise ValueError("mask.bits must have 2 dimensions")
+        m = _TokenMask(bits, mask.bits.shape[1], mask.bits.shape[0],
+                       _on(mask.row_mask, torch.int32, "mask.row_mask", device, (rows,)))
+    _launch(_lib.sv_adjust_logits, "sv_adjust_logits", device, stream, at, ld, out_at, out_ld,
+            rows, _DTYPES[logits.dtype], V, _on(row_req, torch.int32, "row_req", device, (rows,)),
+            _on(row_pos, torch.int32, "row_pos", device, (rows,)), n, k_max, drafts,
+            None if history is None else history._at,
+            _on(slots, torch.int32, "slots", device, (n,)), _ref(pen), _ref(b), _ref(m),
+            _on(dev_error, torch.int32, "dev_error", device, None))
+
+
+def _ref(struct):
+    return None if struct is None else ctypes.addressof(struct)
 
 
 class PagedCache:

@@ -96,8 +96,9 @@ typedef enum {
 #define SV_DEV_BAD_COST      16 /* a consulted cost entry is not finite and > 0 (never chosen)   */
 #define SV_DEV_BAD_KEPT      32 /* a kept count is outside [0, k_max] (clamped)                  */
 #define SV_DEV_BAD_PAGE      64 /* a page id is outside [0, n_pages)                             */
-#define SV_DEV_BAD_PARAM    256 /* a temperature, top_p, min_p or uniform is out of range        */
+#define SV_DEV_BAD_PARAM    256 /* a setting or uniform is out of range                          */
 #define SV_DEV_BAD_CTX      128 /* a context length is negative or its rows pass the page table  */
+#define SV_DEV_BAD_SLOT     512 /* a history slot is outside [0, n_slots)                        */
 
 /* Limits checked on the host. */
 #define SV_MAX_BUDGET_SLOTS 8192   /* n_req and n_req * k_max for sv_budget_select (LDS-resident) */
@@ -583,6 +584,129 @@ sv_status sv_verify_truncated(const void* target_logits, int64_t target_ld, int6
                               int32_t* out_tokens, int32_t* out_accepted, float* out_p_draft,
                               float* out_q_draft, float* out_residual_mass, int32_t* dev_error,
                               void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * What requests have said, and the logits adjusted for it.
+ *
+ * FOS page, section "속도, 메모리, 정확도에 주는 영향", row 정확도: the output law
+ * is the target's.  A request that is served with penalties for repeated
+ * tokens, biases or a grammar has the adjusted law as its target, and the row
+ * behind draft j is conditioned on drafts 0 .. j - 1 (section "추측 디코딩이란"),
+ * which count as said there.  The adjusted rows go into sv_verify,
+ * sv_verify_truncated or sv_sample.
+ *
+ * A request sits in a slot of the history for as long as it lives.
+ * counts:  [n_slots, vocab] int32: 2 * (times the id was emitted) + 1 if it
+ *          stands in the prompt; all 0 in an empty slot.
+ * n_seen:  [n_slots] int32: ids whose count is not 0.
+ * seen:    [n_slots, cap] int32: those ids, each once, in no order.  Where there
+ *          are more than cap of them, calls read the slot's whole row of counts
+ *          instead: right at any cap, fast while the ids fit.
+ * Start with zeroed counts and n_seen.  Counts hold 2^30 - 1 emissions.
+ */
+typedef struct {
+    int32_t* counts;
+    int32_t* seen;
+    int32_t* n_seen;
+    int32_t n_slots, vocab, cap;
+} sv_history;
+
+#define SV_MAX_HISTORY_TOKENS 1073741824 /* n * width for sv_history_add, n * 1024 for sv_history_clear */
+
+/*
+ * sv_history_clear — empty slots (a request left, another takes its place).
+ *
+ * slots: [n] int32, or NULL: 0 .. n - 1.  A slot outside [0, n_slots) is
+ * skipped (SV_DEV_BAD_SLOT).
+ * Launch: one kernel, one workgroup a slot.
+ * Errors: SV_ERR_NULL; SV_ERR_SHAPE.
+ */
+sv_status sv_history_clear(const sv_history* history, const int32_t* slots, int32_t n,
+                           int32_t* dev_error, void* stream);
+
+/*
+ * sv_history_add — ids added to slots: prompts, or what a step emitted.
+ *
+ * tokens:  [n] rows of width int32 ids, tokens_ld apart; -1 is skipped, so
+ *          sv_verify's and sv_pack_varlen's outputs go in as they are.  Another
+ *          id outside [0, vocab) is skipped (SV_DEV_BAD_TOKEN), a slot outside
+ *          [0, n_slots) too (SV_DEV_BAD_SLOT).
+ * slots:   as above; rows of one slot in one call add up.
+ * in_prompt: 0: emitted (each occurrence counts), else: the prompt's.
+ * Launch: one kernel, one thread an id.
+ * Errors: SV_ERR_NULL; SV_ERR_SHAPE.
+ */
+sv_status sv_history_add(const sv_history* history, const int32_t* slots, const int32_t* tokens,
+                         int64_t tokens_ld, int32_t n, int32_t width, int32_t in_prompt,
+                         int32_t* dev_error, void* stream);
+
+/* [n_req] fp32 each, NULL: 1, 0 and 0. */
+typedef struct {
+    const float* repetition;
+    const float* frequency;
+    const float* presence;
+} sv_penalties;
+
+/* Request r's biases are entries start[r] .. start[r + 1] - 1: ids ascending,
+ * each once, values finite or -inf.  start: [n_req + 1] int32; ids, values:
+ * [n_entries]. */
+typedef struct {
+    const int32_t* start;
+    const int32_t* ids;
+    const float* values;
+    int32_t n_entries;
+} sv_bias;
+
+/* Allowed ids: id x of mask m is bit x % 32 of word bits[m * ld + x / 32].
+ * row_mask: [n_rows] int32, the mask of each row, -1: none; NULL: row i has mask
+ * i. */
+typedef struct {
+    const int32_t* bits;
+    int64_t ld;
+    int32_t n_masks;
+    const int32_t* row_mask;
+} sv_token_mask;
+
+/*
+ * sv_adjust_logits — penalties, biases and grammar masks on packed rows.
+ *
+ * Row i is position j = row_pos[i] of request r = row_req[i] (as sv_pack_varlen
+ * writes them; -1: the row is skipped, neither read nor written).  With c(x)
+ * the times x was emitted, drafts 0 .. j - 1 of this step counted too, and z
+ * its logit:
+ *   z1 = z / repetition if z > 0, else z * repetition   (c(x) > 0, or x in the prompt)
+ *   z2 = z1 - frequency * c(x) - presence               (c(x) > 0)
+ *   z3 = z2 + the id's bias                             (ids that have one)
+ *   out = z3, or -inf where the row's mask does not allow x.
+ * In fp32, rounded once to the rows' type.
+ *
+ * logits, out: [n_rows] rows of vocab values, ld and out_ld apart; rows need no
+ *          alignment.  out = logits with out_ld = ld adjusts in place, which
+ *          touches the said, biased and masked ids only; other overlaps are
+ *          refused.
+ * row_req, row_pos: [n_rows] int32; NULL: row i is request i, position 0.
+ * draft_tokens: [n_req, k_max] int32, NULL if k_max is 0 or there are no
+ *          penalties (positions then are not looked at beyond their sign).
+ * history: with slots [n_req] (NULL: request r is in slot r); NULL: nothing was
+ *          said before this step.
+ * penalties, bias, mask: host pointers, or NULL: none.
+ * A row with an unknown request or position (SV_DEV_BAD_CU_ROWS), slot
+ * (SV_DEV_BAD_SLOT), draft or bias id (SV_DEV_BAD_TOKEN; also ids that do not
+ * ascend), or with a repetition that is not positive and finite, another
+ * penalty or a bias that is not finite (-inf biases are), a bias range or a
+ * mask that is not there (SV_DEV_BAD_PARAM) is filled with NaN, so that a draw
+ * from it is refused.
+ * Launch: one kernel; few rows are cut into parts.
+ * Errors: SV_ERR_NULL; SV_ERR_DTYPE; SV_ERR_SHAPE (also a history of another
+ * vocab).
+ */
+sv_status sv_adjust_logits(const void* logits, int64_t ld, void* out, int64_t out_ld,
+                           int32_t n_rows, sv_dtype dtype, int32_t vocab, const int32_t* row_req,
+                           const int32_t* row_pos, int32_t n_req, int32_t k_max,
+                           const int32_t* draft_tokens, const sv_history* history,
+                           const int32_t* slots, const sv_penalties* penalties,
+                           const sv_bias* bias, const sv_token_mask* mask, int32_t* dev_error,
+                           void* stream);
 
 /*
  * The paged key-value cache of the packed batch.
