@@ -33,7 +33,7 @@ SV_NOALLOC_WS_BYTES = 8388608
 SV_MAX_ATTEND_SLOTS, SV_MAX_CONTEXT = 16777215, 2147418112
 SV_MAX_APPEND_VALUES = 1073741824
 SV_MAX_SAMPLE_ROWS = 4194303
-SV_MAX_HISTORY_TOKENS = 1073741824
+SV_MAX_HISTORY_TOKENS, SV_MAX_ADJUST_PARTS = 1073741824, 16777215
 
 EXPORTED = ["sv_status_str", "sv_budget_workspace_bytes", "sv_verify_workspace_bytes",
             "sv_cost_table_prepare", "sv_budget_select", "sv_budget_allocate",

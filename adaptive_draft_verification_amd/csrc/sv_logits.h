@@ -45,17 +45,21 @@ struct AdjustArgs {
     bool masked;
     sv_token_mask mask;
     int32_t* dev_error;
-    int parts;     // workgroups a row
-    int part_len;  // ids of each, a multiple of 32
+    int parts;  // workgroups a row, a power of two
 };
 hipError_t launch_adjust(const AdjustArgs& a, hipStream_t stream);
 
-// Ids a workgroup takes: rows are cut until there are some 2048 workgroups, not
-// below 4096 ids.
-inline int adjust_part_len(int n_rows, int vocab) {
-    const int64_t want = n_rows > 0 ? (2048 + n_rows - 1) / n_rows : 1;
-    const int64_t even = ((vocab + want - 1) / want + 31) / 32 * 32;
-    return (int)(even < 4096 ? 4096 : even);
+constexpr int kAdjustTile = 512;         // ids
+constexpr int kAdjustPartBytes = 32768;  // of a row, at most
+
+// Workgroups a row: the power of two that makes some 8192 of them, with 4096 ids
+// each at least, and no more ids than LDS holds.
+inline int adjust_parts(int n_rows, int vocab, int esize) {
+    const int tiles = (vocab + kAdjustTile - 1) / kAdjustTile;
+    int p = 1;
+    while ((int64_t)n_rows * p < 8192 && vocab > 2 * p * 2048) p *= 2;
+    while ((tiles + p - 1) / p * kAdjustTile * esize > kAdjustPartBytes) p *= 2;
+    return p;
 }
 
 }  // namespace sv

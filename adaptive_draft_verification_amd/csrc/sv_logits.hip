@@ -65,12 +65,14 @@ __global__ __launch_bounds__(256) void add_kernel(HistoryAddArgs a, int blocks_a
 
 // ------------------------------------------------------------------- adjust
 //
-// One workgroup takes part of a row.  First every id of the part is copied with
-// the mask applied, 16 bytes a thread (in place only the masked vectors are
-// written); then the few ids that the request has said, drafted or biased are
-// computed from the row's own logits and written over.  Each of those ids is
-// one thread's: listed ids by their place in the list, drafted ones that are
-// not listed by their first occurrence, biased ones if they are neither.
+// Bound by the rows, read and written once.  One workgroup takes a part of a row.
+// Out of place (kStaged) the part goes through LDS: the few ids that the request
+// has said, drafted or biased are adjusted there, and the part leaves with the mask
+// applied.  In place only the masked vectors and those few ids are touched.  Each of
+// the ids is one thread's, which finds its count and its bias itself.
+// A part is every parts-th tile of kAdjustTile ids: the ids that texts repeat most
+// are neighbours (the lowest ones, as tokenisers number them), and would be one
+// workgroup's otherwise.
 
 template <typename T>
 struct Row;
@@ -110,29 +112,62 @@ struct Row<uint16_t> {
 };
 
 constexpr int kAdjustThreads = 256;
+constexpr int kPlaces = 6;  // places a thread looks at, their loads in flight together
 
-template <typename T>
-__global__ __launch_bounds__(kAdjustThreads) void adjust_kernel(AdjustArgs a) {
+template <typename T, bool kStaged>
+__global__ __launch_bounds__(kAdjustThreads, kStaged ? 4 : 8) void adjust_kernel(AdjustArgs a) {
     constexpr int kVec = Row<T>::kVec;
+    constexpr int kVecs = kAdjustPartBytes / 16 / kAdjustThreads;  // a thread's, staged
+    __shared__ uint4 staged[kStaged ? kAdjustPartBytes / 16 : 1];
     __shared__ int drafts[SV_MAX_DRAFT];
+    // bit x % kSieve: x may be drafted or biased (a bias is found by halving the
+    // list, some steps of memory latency: not for every id that was said)
+    constexpr int kSieve = 8192;
+    __shared__ uint32_t sieve[kSieve / 32];
+    __shared__ int found[kPlaces * kAdjustThreads], n_found;
     const int tid = threadIdx.x;
     const int row = blockIdx.x / a.parts, part = blockIdx.x - row * a.parts;
-    const int begin = part * a.part_len, end = min(a.vocab, begin + a.part_len);
     const char* in = static_cast<const char*>(a.logits) + (int64_t)row * a.ld * sizeof(T);
     char* out = static_cast<char*>(a.out) + (int64_t)row * a.out_ld * sizeof(T);
-    const bool in_place = a.logits == a.out;
+    // ids of the part: whole tiles, and what the last one lacks; parts is a power of
+    // two
+    const int tiles = (a.vocab + kAdjustTile - 1) / kAdjustTile;
+    const int my_tiles = part < tiles ? (tiles - part + a.parts - 1) / a.parts : 0;
+    const bool has_last = my_tiles > 0 && ((tiles - 1) & (a.parts - 1)) == part;
+    const int my_ids = my_tiles * kAdjustTile - (has_last ? tiles * kAdjustTile - a.vocab : 0);
+    const int vecs = my_ids / kVec;
+    auto id_at = [&](int i) {
+        return ((i / kAdjustTile) * a.parts + part) * kAdjustTile + i % kAdjustTile;
+    };
+    auto mine = [&](int x) {
+        return x >= 0 && x < a.vocab && ((x / kAdjustTile) & (a.parts - 1)) == part;
+    };
 
     const int r = a.row_req != nullptr ? a.row_req[row] : row;
     if (r == -1) return;
+    // the steps from here to the counts wait for memory five times, one for the
+    // other: the part is on its way meanwhile
+    uint32_t w[kVecs][4];
+    if constexpr (kStaged) {
+#pragma unroll
+        for (int u = 0; u < kVecs; ++u) {
+            const int v = u * kAdjustThreads + tid;
+            if (v < vecs) __builtin_memcpy(w[u], in + (int64_t)id_at(v * kVec) * sizeof(T), 16);
+        }
+    }
+    for (int i = tid; i < kSieve / 32; i += kAdjustThreads) sieve[i] = 0;
+    if (tid == 0) n_found = 0;
+    __syncthreads();
+    auto sift = [&](int x) { atomicOr(&sieve[(x % kSieve) / 32], 1u << (x % 32)); };
     const int j = a.row_pos != nullptr ? a.row_pos[row] : 0;
     int fault =
         r < 0 || r >= a.n_req || j < 0 || (a.penalised && j > a.k_max) ? SV_DEV_BAD_CU_ROWS : 0;
     float rho = 1.0f, phi = 0.0f, pi = 0.0f;
     int slot = 0, n_seen = 0, b0 = 0, b1 = 0;
     const uint32_t* mask = nullptr;
-    const bool known = fault == 0;
     const bool said = a.penalised && a.history.counts != nullptr;
-    if (known) {
+    const int n_drafts = a.penalised && fault == 0 ? j : 0;
+    if (fault == 0) {
         if (said) {
             slot = a.slots != nullptr ? a.slots[r] : r;
             if (slot < 0 || slot >= a.history.n_slots) {
@@ -150,10 +185,11 @@ __global__ __launch_bounds__(kAdjustThreads) void adjust_kernel(AdjustArgs a) {
             if (!is_finite_bits(rho) || !(rho > 0.0f) || !is_finite_bits(phi) ||
                 !is_finite_bits(pi))
                 fault |= SV_DEV_BAD_PARAM;
-            if (tid < j) {
+            if (tid < n_drafts) {
                 const int d = a.draft_tokens[(int64_t)r * a.k_max + tid];
                 drafts[tid] = d;
                 if (d < 0 || d >= a.vocab) fault |= SV_DEV_BAD_TOKEN;
+                else sift(d);
             }
         }
         if (a.bias.n_entries > 0) {
@@ -167,6 +203,7 @@ __global__ __launch_bounds__(kAdjustThreads) void adjust_kernel(AdjustArgs a) {
                 const int x = a.bias.ids[i];
                 if (x < 0 || x >= a.vocab || (i > b0 && a.bias.ids[i - 1] >= x))
                     fault |= SV_DEV_BAD_TOKEN;
+                else sift(x);
                 const float v = a.bias.values[i];
                 if (!is_finite_bits(v) && __float_as_uint(v) != 0xff800000u)
                     fault |= SV_DEV_BAD_PARAM;
@@ -179,88 +216,130 @@ __global__ __launch_bounds__(kAdjustThreads) void adjust_kernel(AdjustArgs a) {
                 mask = reinterpret_cast<const uint32_t*>(a.mask.bits) + (int64_t)m * a.mask.ld;
         }
     }
+    if constexpr (kStaged) {
+#pragma unroll
+        for (int u = 0; u < kVecs; ++u) {
+            const int v = u * kAdjustThreads + tid;
+            if (v < vecs) staged[v] = make_uint4(w[u][0], w[u][1], w[u][2], w[u][3]);
+        }
+        const int i = vecs * kVec + tid;
+        if (i < my_ids) Row<T>::put(staged, i, Row<T>::get(in, id_at(i)));
+    }
     if (__syncthreads_or(fault)) {
         raise_error(a.dev_error, fault);
-        for (int x = begin + tid; x < end; x += kAdjustThreads)
-            Row<T>::put(out, x, __builtin_nanf(""));
+        for (int i = tid; i < my_ids; i += kAdjustThreads)
+            Row<T>::put(out, id_at(i), __builtin_nanf(""));
         return;
     }
+    auto allowed = [&](int x) { return mask == nullptr || ((mask[x >> 5] >> (x & 31)) & 1); };
 
-    // every id of the part; vectors start at multiples of kVec ids, so that a
-    // vector's bits lie in one word
-    if (!in_place || mask != nullptr) {
-        const int full = begin + (end - begin) / kVec * kVec;
-        for (int x = begin + tid * kVec; x < full; x += kAdjustThreads * kVec) {
-            uint32_t allowed = ~0u;
-            if (mask != nullptr) allowed = mask[x >> 5] >> (x & 31);
-            constexpr uint32_t kAll = (1u << kVec) - 1;
-            if (in_place && (allowed & kAll) == kAll) continue;
-            uint32_t w[4] = {};
-            if ((allowed & kAll) != 0) __builtin_memcpy(w, in + (int64_t)x * sizeof(T), 16);
-            if (mask != nullptr) Row<T>::mask(w, allowed);
-            __builtin_memcpy(out + (int64_t)x * sizeof(T), w, 16);
+    // in place: vectors with an id that the mask does not allow; vectors start at
+    // multiples of kVec ids, so that a vector's bits lie in one word
+    constexpr uint32_t kAll = (1u << kVec) - 1;
+    if (!kStaged && mask != nullptr) {
+        for (int v = tid; v < vecs; v += kAdjustThreads) {
+            const int x = id_at(v * kVec);
+            const uint32_t bits = (mask[x >> 5] >> (x & 31)) & kAll;
+            if (bits == kAll) continue;
+            uint32_t t[4] = {};
+            if (bits != 0) __builtin_memcpy(t, in + (int64_t)x * sizeof(T), 16);
+            Row<T>::mask(t, bits);
+            __builtin_memcpy(out + (int64_t)x * sizeof(T), t, 16);
         }
-        const int x = full + tid;
-        if (x < end) {
-            const bool ok = mask == nullptr || ((mask[x >> 5] >> (x & 31)) & 1);
-            Row<T>::put(out, x, ok ? Row<T>::get(in, x) : -kInf);
-        }
+        const int i = vecs * kVec + tid;
+        if (i < my_ids && !allowed(id_at(i))) Row<T>::put(out, id_at(i), -kInf);
+        __syncthreads();
     }
-    if (!a.penalised && b0 == b1) return;
-    __syncthreads();
 
+    // Ids stand in the history's list (or among its counts of the part, where the
+    // list did not hold every id); biases and drafts are looked at where they are
+    // not in the history, equal drafts at the first.
     const int32_t* counts =
         said ? a.history.counts + (int64_t)slot * a.history.vocab : nullptr;
-    const int n_drafts = a.penalised ? j : 0;
-    // ids of this part that the mask allows
-    auto mine = [&](int x) {
-        return x >= begin && x < end && (mask == nullptr || ((mask[x >> 5] >> (x & 31)) & 1));
-    };
-    auto drafted = [&](int x, int before) {
-        int n = 0;
-        for (int i = 0; i < before; ++i) n += drafts[i] == x;
-        return n;
-    };
-    // z3 of an id that history holds (twice the times it was emitted, + 1) and the
-    // drafts repeat
-    auto adjust = [&](int x, int held, int again) {
-        float z = Row<T>::get(in, x);
-        z = z > 0.0f ? __fdiv_rn(z, rho) : z * rho;
-        const int c = (held >> 1) + again;
-        if (c > 0) z = z - phi * (float)c - pi;
-        int lo = b0, hi = b1;  // the first entry not below x
+    const bool list = n_seen <= a.history.cap;
+    const int n_said = !said ? 0 : list ? n_seen : my_ids;
+    const int n_bias = b1 - b0;
+    auto bias_of = [&](int x) {  // x's entry, or -1
+        int lo = b0, hi = b1;
         while (lo < hi) {
             const int mid = (lo + hi) >> 1;
             if (a.bias.ids[mid] < x) lo = mid + 1;
             else hi = mid;
         }
-        if (lo < b1 && a.bias.ids[lo] == x) z += a.bias.values[lo];
-        Row<T>::put(out, x, z);
+        return lo < b1 && a.bias.ids[lo] == x ? lo : -1;
     };
-    if (said) {
-        if (n_seen <= a.history.cap) {
-            const int32_t* seen = a.history.seen + (int64_t)slot * a.history.cap;
-            for (int i = tid; i < n_seen; i += kAdjustThreads) {
-                const int x = seen[i];
-                if (mine(x)) adjust(x, counts[x], drafted(x, n_drafts));
-            }
-        } else {
-            for (int x = begin + tid; x < end; x += kAdjustThreads) {
-                const int held = counts[x];
-                if (held != 0 && mine(x)) adjust(x, held, drafted(x, n_drafts));
-            }
+    auto sifted = [&](int x) { return (sieve[(x % kSieve) / 32] >> (x % 32)) & 1; };
+    // z3 of x, with its entry (-1: it has none, -2: to be looked for)
+    auto adjust = [&](int x, int held, int entry) {
+        if (sifted(x)) {
+            for (int e = 0; e < n_drafts; ++e) held += drafts[e] == x ? 2 : 0;
+            if (entry == -2) entry = bias_of(x);
+        }
+        void* row_at = kStaged ? static_cast<void*>(staged) : out;
+        const int i = kStaged ? x / (kAdjustTile * a.parts) * kAdjustTile + x % kAdjustTile : x;
+        float z = Row<T>::get(row_at, i);
+        if (held > 0) z = z > 0.0f ? __fdiv_rn(z, rho) : z * rho;
+        if (held > 1) z = z - phi * (float)(held >> 1) - pi;
+        if (entry >= 0) z += a.bias.values[entry];
+        Row<T>::put(row_at, i, z);
+    };
+    for (int from = 0; from < n_said; from += kPlaces * kAdjustThreads) {
+        // the part's ids among the next places, packed: one in parts of a list's
+        if (from > 0) {
+            __syncthreads();
+            if (tid == 0) n_found = 0;
+            __syncthreads();
+        }
+        int x[kPlaces];
+#pragma unroll
+        for (int u = 0; u < kPlaces; ++u) {
+            const int i = from + u * kAdjustThreads + tid;
+            x[u] = -1;
+            if (i < n_said)
+                x[u] = list ? a.history.seen[(int64_t)slot * a.history.cap + i] : id_at(i);
+        }
+#pragma unroll
+        for (int u = 0; u < kPlaces; ++u)
+            if (mine(x[u])) found[atomicAdd(&n_found, 1)] = x[u];
+        __syncthreads();
+        for (int i = tid; i < n_found; i += kAdjustThreads) {
+            const int y = found[i], held = counts[y];
+            // staged parts are masked as they leave
+            if (held != 0 && (kStaged || allowed(y))) adjust(y, held, -2);
         }
     }
-    if (tid < n_drafts) {
-        const int x = drafts[tid];
-        if (mine(x) && drafted(x, tid) == 0 && (!said || counts[x] == 0))
-            adjust(x, 0, drafted(x, n_drafts));
+    for (int i = tid; i < n_bias + n_drafts; i += kAdjustThreads) {
+        const int d = i - n_bias;  // below 0: a bias
+        const int x = d < 0 ? a.bias.ids[b0 + i] : drafts[d];
+        if (!mine(x) || !(kStaged || allowed(x)) || (said && counts[x] != 0)) continue;
+        bool again = d >= 0 && bias_of(x) >= 0;
+        for (int e = 0; e < d; ++e) again |= drafts[e] == x;
+        if (!again) adjust(x, 0, d < 0 ? b0 + i : -1);
     }
-    for (int i = b0 + tid; i < b1; i += kAdjustThreads) {
-        const int x = a.bias.ids[i];
-        if (mine(x) && (!said || counts[x] == 0) && drafted(x, n_drafts) == 0)
-            Row<T>::put(out, x, Row<T>::get(in, x) + a.bias.values[i]);
+    if constexpr (kStaged) {
+        __syncthreads();
+        for (int v = tid; v < vecs; v += kAdjustThreads) {
+            const int x = id_at(v * kVec);
+            const uint4 s = staged[v];
+            uint32_t t[4] = {s.x, s.y, s.z, s.w};
+            if (mask != nullptr) Row<T>::mask(t, mask[x >> 5] >> (x & 31));
+            __builtin_memcpy(out + (int64_t)x * sizeof(T), t, 16);
+        }
+        const int i = vecs * kVec + tid;
+        if (i < my_ids) {
+            const int x = id_at(i);
+            Row<T>::put(out, x, allowed(x) ? Row<T>::get(staged, i) : -kInf);
+        }
     }
+}
+
+template <typename T>
+void run_adjust(const AdjustArgs& a, hipStream_t stream) {
+    const unsigned grid = (unsigned)((int64_t)a.n_rows * a.parts);
+    if (a.logits == a.out)
+        adjust_kernel<T, false><<<grid, kAdjustThreads, 0, stream>>>(a);
+    else
+        adjust_kernel<T, true><<<grid, kAdjustThreads, 0, stream>>>(a);
 }
 
 }  // namespace
@@ -278,11 +357,8 @@ hipError_t launch_history_add(const HistoryAddArgs& a, hipStream_t stream) {
 }
 
 hipError_t launch_adjust(const AdjustArgs& a, hipStream_t stream) {
-    const unsigned grid = (unsigned)((int64_t)a.n_rows * a.parts);
-    if (a.dtype == SV_BF16)
-        adjust_kernel<uint16_t><<<grid, kAdjustThreads, 0, stream>>>(a);
-    else
-        adjust_kernel<float><<<grid, kAdjustThreads, 0, stream>>>(a);
+    if (a.dtype == SV_BF16) run_adjust<uint16_t>(a, stream);
+    else run_adjust<float>(a, stream);
     return hipGetLastError();
 }
 

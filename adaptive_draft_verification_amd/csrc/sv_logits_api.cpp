@@ -105,7 +105,8 @@ sv_status sv_adjust_logits(const void* logits, int64_t ld, void* out, int64_t ou
     if ((double)n_rows * (double)ld > 2.0e18 || (double)n_rows * (double)out_ld > 2.0e18)
         return SV_ERR_SHAPE;
     if (!overlap_ok(logits, ld, out, out_ld, n_rows, vocab, (int64_t)esize)) return SV_ERR_SHAPE;
-    const int len = sv::adjust_part_len(n_rows, vocab);
+    const int parts = sv::adjust_parts(n_rows, vocab, (int)esize);
+    if ((int64_t)n_rows * parts > SV_MAX_ADJUST_PARTS) return SV_ERR_SHAPE;
     const sv::AdjustArgs a{logits, ld, out, out_ld, n_rows, dtype, vocab, row_req, row_pos, n_req,
                            k_max, draft_tokens,
                            history != nullptr && penalties != nullptr ? *history : sv_history{},
@@ -113,7 +114,7 @@ sv_status sv_adjust_logits(const void* logits, int64_t ld, void* out, int64_t ou
                            penalties != nullptr ? *penalties : sv_penalties{},
                            bias != nullptr ? *bias : sv_bias{}, mask != nullptr,
                            mask != nullptr ? *mask : sv_token_mask{}, dev_error,
-                           (vocab + len - 1) / len, len};
+                           parts};
     const hipError_t e = sv::launch_adjust(a, as_stream(stream));
     return sv::finish_launch(e, as_stream(stream));
 }

@@ -640,6 +640,9 @@ sv_status sv_history_add(const sv_history* history, const int32_t* slots, const 
                          int64_t tokens_ld, int32_t n, int32_t width, int32_t in_prompt,
                          int32_t* dev_error, void* stream);
 
+#define SV_MAX_ADJUST_PARTS 16777215 /* workgroups of sv_adjust_logits, 32 KB of a row each (half of
+                                        that at least where vocab is no power of two) */
+
 /* [n_req] fp32 each, NULL: 1, 0 and 0. */
 typedef struct {
     const float* repetition;
@@ -696,7 +699,7 @@ typedef struct {
  * penalty or a bias that is not finite (-inf biases are), a bias range or a
  * mask that is not there (SV_DEV_BAD_PARAM) is filled with NaN, so that a draw
  * from it is refused.
- * Launch: one kernel; few rows are cut into parts.
+ * Launch: one kernel, a workgroup for each 4096 ids or more of a row (up to 32 KB).
  * Errors: SV_ERR_NULL; SV_ERR_DTYPE; SV_ERR_SHAPE (also a history of another
  * vocab).
  */
