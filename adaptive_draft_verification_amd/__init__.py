@@ -33,6 +33,7 @@ SV_NOALLOC_WS_BYTES = 8388608
 SV_MAX_ATTEND_SLOTS, SV_MAX_CONTEXT = 16777215, 2147418112
 SV_MAX_APPEND_VALUES = 1073741824
 SV_MAX_SAMPLE_ROWS = 4194303
+SV_LATENT_ROPE = 64
 SV_MAX_HISTORY_TOKENS, SV_MAX_ADJUST_PARTS = 1073741824, 16777215
 
 EXPORTED = ["sv_status_str", "sv_budget_workspace_bytes", "sv_verify_workspace_bytes",
@@ -44,7 +45,8 @@ EXPORTED = ["sv_status_str", "sv_budget_workspace_bytes", "sv_verify_workspace_b
             "sv_philox_uniforms",
             "sv_cache_append", "sv_cache_attend", "sv_cache_attend_workspace_bytes",
             "sv_sample", "sv_verify_truncated", "sv_verify_truncated_workspace_bytes",
-            "sv_history_clear", "sv_history_add", "sv_adjust_logits"]
+            "sv_history_clear", "sv_history_add", "sv_adjust_logits",
+            "sv_latent_append", "sv_latent_attend", "sv_latent_attend_workspace_bytes"]
 
 
 class _Cache(ctypes.Structure):
@@ -61,6 +63,14 @@ class _Law(ctypes.Structure):
     """sv_sampling of the C header."""
     _fields_ = [("temperature", ctypes.c_void_p), ("top_k", ctypes.c_void_p),
                 ("top_p", ctypes.c_void_p), ("min_p", ctypes.c_void_p)]
+
+
+class _LatentCache(ctypes.Structure):
+    """sv_latent_cache of the C header."""
+    _fields_ = [("kv", ctypes.c_void_p), ("dtype", ctypes.c_int), ("n_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("latent_dim", ctypes.c_int32),
+                ("page_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+                ("scale", ctypes.c_void_p)]
 
 
 class _History(ctypes.Structure):
@@ -140,6 +150,11 @@ def _load():
         "sv_verify_truncated": (ctypes.c_int, [vp, i64, i64, vp, i64, ctypes.c_int, i32, vp, vp,
                                                i32, i32, vp, vp, u64, u64, vp, vp, vp, vp, vp, vp,
                                                vp, sz, vp]),
+        "sv_latent_append": (ctypes.c_int, [vp, vp, i32, vp, i64, vp, i64, vp, vp, i32, vp, i32, vp,
+                                            vp]),
+        "sv_latent_attend_workspace_bytes": (sz, [i32, i32, i32, i32, i32, i32]),
+        "sv_latent_attend": (ctypes.c_int, [vp, vp, i32, vp, i64, i64, i32, vp, vp, i32, i32, f32,
+                                            vp, i64, vp, vp, vp, sz, vp]),
         "sv_history_clear": (ctypes.c_int, [vp, vp, i32, vp, vp]),
         "sv_history_add": (ctypes.c_int, [vp, vp, vp, i64, i32, i32, i32, vp, vp]),
         "sv_adjust_logits": (ctypes.c_int, [vp, i64, vp, i64, i32, ctypes.c_int, i32, vp, vp, i32,
@@ -877,6 +892,97 @@ def sv_cache_attend(cache, page_table, q, cu_rows, ctx_len, k_max, scale, out, w
     q_at, q_ld = _rows(q, "q", device, heads, cache._head_dim)
     out_at, out_ld = _rows(out, "out", device, heads, cache._head_dim)
     _launch(_lib.sv_cache_attend, "sv_cache_attend", device, stream, cache._at, table, max_pages,
+            q_at, q_ld, rows, heads, _on(cu_rows, torch.int32, "cu_rows", device, (n + 1,)),
+            _on(ctx_len, torch.int32, "ctx_len", device, (n,)), n, int(k_max), float(scale),
+            out_at, out_ld, _on(out_lse, torch.float32, "out_lse", device, (rows, heads)),
+            _on(dev_error, torch.int32, "dev_error", device, None),
+            _on(ws, torch.uint8, "ws", device, None), 0 if ws is None else ws.numel())
+
+
+class LatentCache:
+    """A paged cache of latent vectors: kv [n_pages, page_size, latent_dim + 64] (bfloat16 or
+    float8_e4m3fn), any strides over pages and positions, the last dimension contiguous;
+    latent_dim 256 or 512; scale [1] f32 (float8 caches).
+
+    The tensor's address and layout are taken once: it is held and cannot be exchanged, and its
+    storage must not be (set_, resize_)."""
+
+    __slots__ = ("_kv", "_scale", "_device", "_latent_dim", "_page_size", "_c", "_at")
+    kv = property(lambda self: self._kv)
+    scale = property(lambda self: self._scale)
+    device = property(lambda self: self._device)
+    latent_dim = property(lambda self: self._latent_dim)
+    page_size = property(lambda self: self._page_size)
+
+    def __init__(self, kv, latent_dim, scale=None):
+        dtype = _CACHE_DTYPES.get(kv.dtype)
+        if not kv.is_cuda or dtype is None:
+            raise ValueError("kv must be a bfloat16 or float8_e4m3fn device tensor")
+        if kv.dim() != 3 or kv.stride(2) != 1 or kv.shape[2] != latent_dim + SV_LATENT_ROPE:
+            raise ValueError("kv must be [n_pages, page_size, latent_dim + 64], the last dimension "
+                             "contiguous")
+        if dtype == SV_BF16 and scale is not None:
+            raise ValueError("scales belong to float8 caches")
+        self._kv, self._scale, self._device = kv, scale, kv.get_device()
+        n_pages, self._page_size, _ = kv.shape
+        self._latent_dim = int(latent_dim)
+        self._c = _LatentCache(kv.data_ptr(), dtype, n_pages, self._page_size, self._latent_dim,
+                               kv.stride(0), kv.stride(1),
+                               _on(scale, torch.float32, "scale", self._device, (1,)))
+        self._at = ctypes.addressof(self._c)
+
+
+def _matrix(t, name, device, width):
+    """(address, row stride) of a [rows, width] bfloat16 tensor whose rows are contiguous."""
+    if t.dtype is not torch.bfloat16 or t.get_device() != device or t.dim() != 2 \
+            or t.shape[1] != width:
+        raise ValueError(f"{name} must be bfloat16 [rows, {width}] on the cache's device")
+    if t.is_contiguous():
+        return t.data_ptr(), width
+    if t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else width
+
+
+def sv_latent_append(cache, page_table, latent, rope, row_req, row_pos, ctx_len, dev_error=None,
+                     stream=None):
+    """Rows latent [rows, latent_dim] and rope [rows, 64] bf16 into the cache, row i at position
+    ctx_len[row_req[i]] + row_pos[i] (the maps pack_varlen writes; -1: skipped);
+    page_table [n, max_pages] i32, ctx_len [n] i32."""
+    device = cache._device
+    table, n, max_pages = _table(page_table, device)
+    at, ld = _matrix(latent, "latent", device, cache._latent_dim)
+    rope_at, rope_ld = _matrix(rope, "rope", device, SV_LATENT_ROPE)
+    rows = latent.shape[0]
+    if rope.shape[0] != rows:
+        raise ValueError("latent and rope must have the same rows")
+    _launch(_lib.sv_latent_append, "sv_latent_append", device, stream, cache._at, table, max_pages,
+            at, ld, rope_at, rope_ld, _on(row_req, torch.int32, "row_req", device, (rows,)),
+            _on(row_pos, torch.int32, "row_pos", device, (rows,)), rows,
+            _on(ctx_len, torch.int32, "ctx_len", device, (n,)), n,
+            _on(dev_error, torch.int32, "dev_error", device, None))
+
+
+def sv_latent_attend_workspace_bytes(n_req, k_max, n_heads, latent_dim, max_pages, page_size):
+    return int(_lib.sv_latent_attend_workspace_bytes(n_req, k_max, n_heads, latent_dim, max_pages,
+                                                     page_size))
+
+
+def sv_latent_attend(cache, page_table, q, cu_rows, ctx_len, k_max, scale, out, ws=None,
+                     out_lse=None, dev_error=None, stream=None):
+    """Packed rows q [rows, n_heads, latent_dim + 64] bf16 -> out [rows, n_heads, latent_dim]: row
+    j of request r (packed row cu_rows[r] + j) sees the cache's positions 0 .. ctx_len[r] + j.
+    ws: uint8 device buffer of sv_latent_attend_workspace_bytes(...) bytes (None if 0);
+    out_lse [rows, n_heads] f32."""
+    device, dim = cache._device, cache._latent_dim
+    table, n, max_pages = _table(page_table, device)
+    if q.dim() != 3 or out.dim() != 3 or out.shape[:2] != q.shape[:2]:
+        raise ValueError("q must be [rows, n_heads, latent_dim + 64] and out [rows, n_heads, "
+                         "latent_dim]")
+    rows, heads, _ = q.shape
+    q_at, q_ld = _rows(q, "q", device, heads, dim + SV_LATENT_ROPE)
+    out_at, out_ld = _rows(out, "out", device, heads, dim)
+    _launch(_lib.sv_latent_attend, "sv_latent_attend", device, stream, cache._at, table, max_pages,
             q_at, q_ld, rows, heads, _on(cu_rows, torch.int32, "cu_rows", device, (n + 1,)),
             _on(ctx_len, torch.int32, "ctx_len", device, (n,)), n, int(k_max), float(scale),
             out_at, out_ld, _on(out_lse, torch.float32, "out_lse", device, (rows, heads)),

@@ -1,21 +1,13 @@
 // The paged key-value cache of the packed verify batch (gfx950, wave64):
 // sv_cache_append writes a step's new keys and values behind each request's
 // context, sv_cache_attend lets the packed rows attend to it.
+#include "sv_attend.h"
 #include "sv_device.h"
 #include "sv_launch.h"
 #include "sv_serve.h"
 
 namespace sv {
 namespace {
-
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef float f32x2 __attribute__((ext_vector_type(2)));
-
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kInf = __builtin_inff();
 
 // ------------------------------------------------------------------- append
 
@@ -59,23 +51,9 @@ __global__ void append_kernel(AppendArgs a) {
         *reinterpret_cast<uint4*>(static_cast<uint16_t*>(is_v ? c.v : c.k) + at) = w;
         return;
     }
-    // x / scale rounded to fp32, then to e4m3 (nearest, ties to even), held
-    // at the type's largest value; NaN stays NaN
     const float* scales = is_v ? c.v_scale : c.k_scale;
     const float s = scales != nullptr ? scales[h] : 1.0f;
-    float x[8] = {bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y),
-                  bf16_lo(w.z), bf16_hi(w.z), bf16_lo(w.w), bf16_hi(w.w)};
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        x[e] = __fdiv_rn(x[e], s);
-        x[e] = x[e] > 448.0f ? 448.0f : x[e] < -448.0f ? -448.0f : x[e];
-    }
-    int lo = 0, hi = 0;
-    lo = __builtin_amdgcn_cvt_pk_fp8_f32(x[0], x[1], lo, false);
-    lo = __builtin_amdgcn_cvt_pk_fp8_f32(x[2], x[3], lo, true);
-    hi = __builtin_amdgcn_cvt_pk_fp8_f32(x[4], x[5], hi, false);
-    hi = __builtin_amdgcn_cvt_pk_fp8_f32(x[6], x[7], hi, true);
-    *reinterpret_cast<int2*>(static_cast<uint8_t*>(is_v ? c.v : c.k) + at) = make_int2(lo, hi);
+    *reinterpret_cast<int2*>(static_cast<uint8_t*>(is_v ? c.v : c.k) + at) = e4m3_of(w, s);
 }
 
 // ------------------------------------------------------------------- attend
@@ -127,34 +105,6 @@ __device__ __forceinline__ Words<N> load_words(const void* p) {
     return out;
 }
 
-__device__ __forceinline__ bf16x8 as_bf16x8(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-    const uint32_t w[4] = {a, b, c, d};
-    bf16x8 r;
-    __builtin_memcpy(&r, w, 16);
-    return r;
-}
-
-// Two e4m3 values (low or high half of w) as two bf16: exact.
-template <bool HI>
-__device__ __forceinline__ uint32_t e4m3_pair(uint32_t w) {
-    const bf16x2 v = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, HI);
-    uint32_t r;
-    __builtin_memcpy(&r, &v, 4);
-    return r;
-}
-
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-    const f32x2 f = {a, b};
-    const bf16x2 v = __builtin_convertvector(f, bf16x2);
-    uint32_t r;
-    __builtin_memcpy(&r, &v, 4);
-    return r;
-}
-
-__device__ __forceinline__ bool bf16_pair_nonfinite(uint32_t w) {
-    return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
-}
-
 template <int D, bool F8, int MT, bool PG16>
 struct Attend {
     // Positions a wave takes at once: 16 KB of keys and values in flight a wave
@@ -193,39 +143,6 @@ struct Attend {
         } part;
     };
 };
-
-// The request of rank `rank` by context length, longest first (ties to the
-// lower request): where workgroups take turns on the CUs, a long request that
-// starts last would be waited for alone (256 requests of 0 .. 4096 positions: 429
-// us in their own order, 394 this way).  For up to 256 requests, a thread each;
-// more keep their own order (256 requests 393 us, 257 424).
-__device__ __forceinline__ int longest(int rank, const int32_t* ctx_len, int n, int* lens) {
-    __shared__ int found;
-    const int t = threadIdx.x;
-    // lengths from 2^22 on count as equal: any order is a right one
-    const int mine = t < n ? (min(max(ctx_len[t], 0), (1 << 22) - 1) << 8) | (255 - t) : -1;
-    lens[t] = mine;
-    __syncthreads();
-    int ahead = 0;
-#pragma unroll 4
-    for (int j = 0; j < n; j += 4) {
-        const int4 v = *reinterpret_cast<const int4*>(lens + j);
-        ahead += (v.x > mine) + (v.y > mine) + (v.z > mine) + (v.w > mine);
-    }
-    if (t < n && ahead == rank) found = t;
-    __syncthreads();
-    return found;
-}
-
-// Consecutive workgroups go to the eight XCDs in turn, each with an L2 of its
-// own; `run` neighbouring work items that read the same lines (slot blocks of
-// a head, heads narrower than a line) are given to one XCD, one behind the
-// other: 64 requests, 16 heads of 64 bytes: 42 us without, 29 with.
-__device__ __forceinline__ int spread(int b, int total, int run) {
-    const int group = 8 * run, g = b / group, rest = b - g * group;
-    if ((g + 1) * group > total) return b;
-    return g * group + (rest & 7) * run + (rest >> 3);
-}
 
 template <int D, bool F8, int MT, bool PG16>
 __global__ __launch_bounds__(256, (Attend<D, F8, MT, PG16>::kOccupancy))

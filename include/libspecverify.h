@@ -816,6 +816,86 @@ sv_status sv_cache_attend(const sv_cache* cache, const int32_t* page_table, int3
                           int32_t* dev_error, void* ws, size_t ws_bytes, void* stream);
 
 /*
+ * The paged cache of shared latent vectors.
+ *
+ * agentlens page, section "기술적 구현 및 CUDA Graphs", item Graph Capture: the
+ * varlen decode shape holds 1 .. k+1 query tokens per request; the models it
+ * is written for keep one latent vector a token, shared by all heads, from
+ * which keys and values are up-projected.  The projections are absorbed: the
+ * keys' into the queries before the call, the values' into what follows it, so
+ * that every head attends to the latent vectors themselves.  (Expanding keys
+ * and values instead pays from some 170 rows a request on; a verify step has
+ * SV_MAX_DRAFT + 1 at most.)
+ *
+ * kv: position t of request r is the latent_dim + SV_LATENT_ROPE consecutive
+ *     values at page_table[r, t / page_size] * page_stride + (t % page_size) *
+ *     token_stride (strides in values): the latent vector, then the part of the
+ *     key that carries the position.
+ * dtype: SV_BF16, or SV_E4M3: a stored value times *scale (fp32, device; NULL =
+ *     1) is the value.   latent_dim: 256 or 512.   page_size: any.
+ * Alignment: kv and both strides to 16 bytes.   page_table: as for sv_cache.
+ */
+#define SV_LATENT_ROPE 64
+typedef struct {
+    void* kv;
+    sv_dtype dtype;
+    int32_t n_pages, page_size, latent_dim;
+    int64_t page_stride, token_stride;
+    const float* scale;
+} sv_latent_cache;
+
+/*
+ * sv_latent_append — write a step's latent vectors behind the contexts.
+ *
+ * latent:  [n_rows, latent_dim], rope: [n_rows, SV_LATENT_ROPE] bf16, rows
+ *          latent_ld and rope_ld values apart (multiples of 8, 16-byte aligned).
+ * The other arguments, the rounding to 8 bits, rows that are skipped, faults
+ * and errors are sv_cache_append's.
+ * Launch: one kernel, 16 bytes of input a thread.
+ */
+sv_status sv_latent_append(const sv_latent_cache* cache, const int32_t* page_table,
+                           int32_t max_pages, const void* latent, int64_t latent_ld,
+                           const void* rope, int64_t rope_ld, const int32_t* row_req,
+                           const int32_t* row_pos, int32_t n_rows, const int32_t* ctx_len,
+                           int32_t n_req, int32_t* dev_error, void* stream);
+
+/*
+ * sv_latent_attend — the packed rows attend to the latent cache.
+ *
+ * For row j of request r (position t = ctx_len[r] + j), every head and the
+ * positions i = 0 .. t, c_i the latent vector and e_i = (c_i, rope_i):
+ *   s_i = scale * <q, e_i>;  out = sum_i e^(s_i) c_i / sum_i e^(s_i);
+ *   lse = ln sum_i e^(s_i).
+ * q:       [q_rows, n_heads, latent_dim + SV_LATENT_ROPE] bf16, rows q_ld values
+ *          apart; out: [q_rows, n_heads, latent_dim] bf16, rows out_ld apart
+ *          (multiples of 8, 16-byte aligned).  Rows outside every request are
+ *          neither read nor written.
+ * cu_rows, ctx_len, k_max, out_lse, bad pages and offsets, rows that see nothing:
+ * as for sv_cache_attend.  A position behind the context (one of the step's own)
+ * whose vector holds NaN or infinity makes NaN of the rows that see it and does
+ * not touch the others.
+ * Numerics: as for sv_cache_attend, except that values below 2^-86 may lose bits
+ * and weights below 2^-86 of the largest may count as 0.  Repeated calls agree
+ * bit for bit.
+ * ws:      sv_latent_attend_workspace_bytes(...) bytes, 16-byte aligned (0: NULL
+ *          will do), uninitialised.  Calls that overlap in time must not share it.
+ * Launch: one kernel of four waves for each request, block of up to 128 query
+ * slots (rows times heads; 64 where there are few) and part of the length; a
+ * second one merges the parts if there are several.
+ * Errors: SV_ERR_NULL; SV_ERR_DTYPE; SV_ERR_SHAPE (SV_MAX_ATTEND_SLOTS holds
+ * here too); SV_ERR_VALUE (scale not finite); SV_ERR_WORKSPACE.
+ */
+size_t sv_latent_attend_workspace_bytes(int32_t n_req, int32_t k_max, int32_t n_heads,
+                                        int32_t latent_dim, int32_t max_pages,
+                                        int32_t page_size);
+sv_status sv_latent_attend(const sv_latent_cache* cache, const int32_t* page_table,
+                           int32_t max_pages, const void* q, int64_t q_ld, int64_t q_rows,
+                           int32_t n_heads, const int32_t* cu_rows, const int32_t* ctx_len,
+                           int32_t n_req, int32_t k_max, float scale, void* out, int64_t out_ld,
+                           float* out_lse, int32_t* dev_error, void* ws, size_t ws_bytes,
+                           void* stream);
+
+/*
  * sv_philox_uniforms — the (u, v) pairs sv_verify draws, for inspection.
  * u, v: [n_req, n_pos] fp32 out for counters (r, j, step) with r < n_req,
  * j < n_pos.  Errors: SV_ERR_NULL; SV_ERR_SHAPE if a size is negative.

@@ -1,0 +1,336 @@
+"""The latent cache on the GPU: sv_latent_append and sv_latent_attend against the fp64
+oracle.
+
+Tolerances, from the arithmetic (bf16 rounding is off by at most 2^-8, fp32 by 2^-24
+relative):
+* scores: fp32 sums of dim products (an error of at most (dim + 8) 2^-24 times the sum of
+  |q k| scale, the products of bf16 values being exact), and the exponent's own rounding and
+  exp2's ulp (2^-21 of a score's size at most): together `delta`, absolute in the score,
+  relative in each weight;
+* out: 2^-15 of each weight (two bf16 terms), the sums' roundings (n 2^-24 at most) and 2
+  delta, all in units of the weighted mean of |v|, then 2^-8 of the output;
+* lse: delta, the sum's own rounding (n 2^-24 of it at most) and 2^-22 of the result.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import adaptive_draft_verification_amd as sv
+from oracle.latent import latent_append, latent_attend
+
+pytestmark = pytest.mark.gpu
+
+BF, F8 = torch.bfloat16, torch.float8_e4m3fn
+
+
+@pytest.fixture(autouse=True, scope="module")
+def _need_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+def values(t):
+    return t.cpu().float().double().numpy()
+
+
+class Batch:
+    """A batch of requests: pages in random order, a table wider than needed."""
+
+    def __init__(self, seed, rows, ctx, heads, rank, page, dtype=BF, k_max=None, extra=2, qscale=1.0,
+                 pad=0):
+        g = torch.Generator().manual_seed(seed)
+        self.n, self.heads, self.rank, self.page = len(rows), heads, rank, page
+        self.dim = rank + 64
+        self.k_max = max(max(rows) - 1, 0) if k_max is None else k_max
+        self.ctx = torch.tensor(ctx, dtype=torch.int32)
+        self.cu = torch.zeros(self.n + 1, dtype=torch.int32)
+        self.cu[1:] = torch.cumsum(torch.tensor(rows), 0)
+        width = max(-(-(c + r) // page) for c, r in zip(ctx, rows)) + extra
+        pages = self.n * width + 1
+        self.table = torch.randperm(pages, generator=g)[:self.n * width].int().view(self.n, width)
+        self.kv = torch.randn(pages, page, self.dim + pad, generator=g).to(dtype)[..., :self.dim]
+        self.kv_scale = None if dtype == BF else 0.5 + torch.rand(1, generator=g)
+        total = int(self.cu[-1])
+        self.q = (torch.randn(total + 3, heads, self.dim, generator=g) * qscale).to(BF)
+        self.scale = 192 ** -0.5
+
+    def device(self):
+        self.kvd = torch.empty_strided(self.kv.shape, self.kv.stride(), dtype=self.kv.dtype,
+                                       device="cuda")
+        self.kvd.copy_(self.kv)
+        self.cache = sv.LatentCache(self.kvd, self.rank,
+                                    None if self.kv_scale is None else self.kv_scale.cuda())
+        return self
+
+    def ws(self):
+        b = sv.sv_latent_attend_workspace_bytes(self.n, self.k_max, self.heads, self.rank,
+                                                self.table.shape[1], self.page)
+        return torch.full((b,), 0xFF, dtype=torch.uint8, device="cuda") if b else None
+
+    def attend(self, q=None, stream=None):
+        q = self.q.cuda() if q is None else q
+        out = torch.full((*q.shape[:2], self.rank), -7.0, dtype=BF, device="cuda")
+        lse = torch.full(q.shape[:2], -7.0, device="cuda")
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        sv.sv_latent_attend(self.cache, self.table.cuda(), q, self.cu.cuda(), self.ctx.cuda(),
+                            self.k_max, self.scale, out, self.ws(), lse, err, stream)
+        torch.cuda.synchronize()
+        return out, lse, int(err)
+
+    def expect(self):
+        kv = values(self.kv)
+        if self.kv_scale is not None:
+            kv = kv * self.kv_scale.double().numpy()
+        return latent_attend(values(self.q), kv, self.rank, self.table.numpy(), self.cu.numpy(),
+                             self.ctx.numpy(), self.scale), kv
+
+    def check(self, want_err=0):
+        out, lse, err = self.attend()
+        assert err == want_err
+        (o, e, spread), k = self.expect()
+        got, got_lse = values(out), values(lse)
+        tail = np.arange(len(e)) >= int(self.cu[-1])
+        assert (got[tail] == -7).all() and (got_lse[tail] == -7).all()
+        head = ~tail
+        kmax = np.abs(k[np.isfinite(k)]).max()
+        qsum = np.abs(values(self.q)).sum(-1)[head]
+        delta = qsum * kmax * abs(self.scale) * ((self.dim + 8) * 2.0 ** -24 + 2.0 ** -21)
+        o, e, spread, got, got_lse = o[head], e[head], spread[head], got[head], got_lse[head]
+        np.testing.assert_array_equal(np.isnan(got), np.isnan(o))
+        np.testing.assert_array_equal(np.isneginf(got_lse), np.isneginf(e))
+        fine = np.isfinite(o)
+        n = int(self.ctx.max()) + self.k_max + 1
+        tol = 2.0 ** -8 * np.abs(o) + 1e-30
+        tol += (2.0 ** -15 + n * 2.0 ** -24 + 2 * delta[..., None]) * spread
+        assert (np.abs(got - o) <= tol)[fine].all(), np.max((np.abs(got - o) / tol)[fine])
+        f = np.isfinite(e)
+        etol = delta + n * 2.0 ** -24 + 2.0 ** -22 * np.abs(e)
+        assert (np.abs(got_lse - e) <= etol)[f].all(), np.max((np.abs(got_lse - e) / etol)[f])
+        return out, lse
+
+
+@pytest.mark.parametrize("dtype", [BF, F8])
+@pytest.mark.parametrize("rank", [256, 512])
+@pytest.mark.parametrize("heads", [1, 5, 16, 33, 64, 128])
+def test_attend_heads_and_types(dtype, rank, heads):
+    Batch(1, [1, 3, 4], [0, 37, 130], heads, rank, 16, dtype).device().check()
+
+
+@pytest.mark.parametrize("dtype", [BF, F8])
+@pytest.mark.parametrize("page", [1, 3, 16, 17, 64])
+def test_attend_pages(dtype, page):
+    Batch(2, [2, 1, 4], [70, 31, 128], 16, 512, page, dtype).device().check()
+
+
+@pytest.mark.parametrize("rank", [256, 512])
+@pytest.mark.parametrize("ctx", [0, 1, 30, 31, 32, 33, 62, 63, 64, 65, 95, 127, 128, 129, 255])
+def test_attend_lengths_around_tiles(ctx, rank):
+    Batch(ctx, [1, 5], [ctx, max(0, ctx - 3)], 20, rank, 32).device().check()
+
+
+@pytest.mark.parametrize("dtype", [BF, F8])
+def test_attend_every_row_count(dtype):
+    """0 .. 65 rows a request; requests without rows leave everything alone."""
+    Batch(3, [0, 65, 1, 0, 17, 8], [9, 40, 0, 7, 100, 3], 3, 256, 16, dtype).device().check()
+
+
+@pytest.mark.parametrize("dtype", [BF, F8])
+@pytest.mark.parametrize("rank", [256, 512])
+def test_attend_a_length_in_parts(dtype, rank):
+    b = Batch(4, [2, 1], [3001, 700], 16, rank, 16, dtype).device()
+    assert b.ws() is not None
+    b.check()
+
+
+@pytest.mark.parametrize("dtype", [BF, F8])
+@pytest.mark.parametrize("rank", [256, 512])
+def test_attend_blocks_of_128_slots(dtype, rank):
+    """Enough requests for the wide workgroups, some of their waves without slots."""
+    rows = [1 + i % 3 for i in range(130)]
+    b = Batch(5, rows, [(37 * i) % 150 for i in range(130)], 70, rank, 16, dtype, qscale=1.5)
+    b.device()
+    assert (b.k_max + 1) * b.heads > 128 and b.ws() is None
+    b.check()
+
+
+@pytest.mark.parametrize("n", [257, 300])
+def test_attend_more_requests_than_are_ordered(n):
+    Batch(6, [1] * n, [i % 50 for i in range(n)], 8, 256, 16).device().check()
+
+
+def test_attend_scores_that_rise():
+    """Later scores far above the first ones: sums are taken relative to new maxima."""
+    for rise in (3.0, 30.0, 300.0):
+        b = Batch(7, [2, 1], [500, 450], 4, 512, 16)
+        # positions in order: keys along q of row 0 head 0, growing
+        q0 = b.q[0, 0].float()
+        for r in range(2):
+            for t in range(0, int(b.ctx[r]), 7):
+                v = q0 * (rise * t / 500 / q0.norm())
+                b.kv[int(b.table[r, t // 16]), t % 16] = v.to(BF)
+        b.device().check()
+
+
+def test_attend_large_and_small_values():
+    for size in (2.0 ** 60, 2.0 ** -60):
+        b = Batch(8, [2, 3], [100, 64], 6, 256, 16)
+        b.kv = (b.kv.float() * size).to(BF)
+        b.q = (b.q.float() / size).to(BF)
+        b.device().check()
+
+
+def test_attend_scores_of_minus_infinity():
+    b = Batch(9, [2, 1], [20, 0], 2, 256, 16)
+    b.q[1, 0] = 0
+    b.q[1, 0, 300] = 1
+    r, t = 0, 5  # one position of -inf for that row; one row with nothing else
+    b.kv[int(b.table[r, t // 16]), t % 16, 300] = -torch.inf
+    b.q[0] = 0
+    b.q[0, :, 300] = 1
+    b.q[1, 1, 300] = 1
+    b.device().check()
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("dim", [0, 255, 256, 319])
+def test_attend_rows_do_not_touch_each_other(value, dim):
+    """A vector of the step's own that is not finite reaches the rows that see it alone."""
+    b = Batch(10, [4, 3], [61, 30], 3, 256, 16)
+    for r, j in ((0, 2), (1, 1)):
+        t = int(b.ctx[r]) + j
+        b.kv[int(b.table[r, t // 16]), t % 16, dim] = value
+    out, _ = b.device().check()
+    nan = torch.isnan(out).any(-1).any(-1).tolist()
+    assert nan[:7] == [False, False, True, True, False, True, True]
+
+
+def test_attend_positions_that_are_not_seen():
+    """What lies behind the rows, in pages of others and in the table's rest does not matter."""
+    b = Batch(11, [2, 3], [30, 45], 5, 512, 16).device()
+    want, want_lse, _ = b.attend()
+    seen = torch.zeros(b.kv.shape[:2], dtype=torch.bool)
+    for r in range(2):
+        for t in range(int(b.ctx[r] + b.cu[r + 1] - b.cu[r])):
+            seen[b.table[r, t // 16].long(), t % 16] = True
+    b.kvd[~seen.cuda()] = float("nan")
+    b.table[:, -2:] = 10 ** 6
+    out, lse, err = b.attend()
+    assert err == 0 and torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
+@pytest.mark.parametrize("rank", [256, 512])
+def test_attend_bad_pages_are_absent(rank):
+    b = Batch(12, [2, 1, 1], [100, 40, 10], 4, rank, 16)
+    pages = b.kv.shape[0]
+    b.table[0, 2], b.table[1, 0], b.table[2, 0] = pages, -1, -5
+    b.kv[0] = float("nan")  # the page a careless kernel would read instead
+    b.table[b.table == 0] = 1
+    b.device().check(want_err=sv.SV_DEV_BAD_PAGE)
+
+
+def test_attend_bad_requests_are_not_written():
+    b = Batch(13, [2, 2, 2, 2], [10, 20, 30, 40], 4, 256, 16, k_max=2).device()
+    good, _, _ = b.attend()
+    for what, bit in ((("ctx", 1, -1), sv.SV_DEV_BAD_CTX), (("ctx", 1, 10 ** 6), sv.SV_DEV_BAD_CTX)):
+        keep = b.ctx.clone()
+        b.ctx[what[1]] = what[2]
+        out, _, err = b.attend()
+        b.ctx = keep
+        assert err == bit and bool((out[2:4] == -7).all())
+        assert torch.equal(out[:2], good[:2]) and torch.equal(out[4:8], good[4:8])
+    keep = b.cu.clone()
+    for cu in ([0, 2, 8, 6, 8], [0, 2, 1, 6, 8], [0, 2, 4, 6, 100]):
+        b.cu = torch.tensor(cu, dtype=torch.int32)
+        out, _, err = b.attend()
+        assert err == sv.SV_DEV_BAD_CU_ROWS and torch.equal(out[:2], good[:2])
+    b.cu = keep
+
+
+def test_attend_strides():
+    b = Batch(14, [2, 3], [40, 17], 6, 512, 16, pad=32).device()
+    wide = torch.full((b.q.shape[0], 8, b.dim), 3.0, dtype=BF, device="cuda")
+    q = wide[:, :6]
+    q.copy_(b.q.cuda())
+    big = torch.full((b.q.shape[0], 9, b.rank), -7.0, dtype=BF, device="cuda")
+    sv.sv_latent_attend(b.cache, b.table.cuda(), q, b.cu.cuda(), b.ctx.cuda(), b.k_max, b.scale,
+                        big[:, :6], b.ws())
+    want, _ = b.check()
+    assert torch.equal(big[:, :6], want) and bool((big[:, 6:] == -7).all())
+
+
+@pytest.mark.parametrize("dtype", [BF, F8])
+def test_append(dtype):
+    rng = np.random.default_rng(1)
+    for rank, page, n, k in ((256, 1, 3, 2), (512, 16, 40, 7), (512, 17, 2, 0)):
+        rows = rng.integers(1, k + 2, n)
+        cap = n * (k + 1)
+        req, pos = np.full(cap, -1, np.int32), np.full(cap, -1, np.int32)
+        req[:rows.sum()] = np.repeat(np.arange(n), rows)
+        pos[:rows.sum()] = np.concatenate([np.arange(x) for x in rows])
+        ctx = rng.integers(0, 50, n).astype(np.int32)
+        width = -(-(50 + k + 1) // page)
+        table = rng.permutation(n * width).astype(np.int32).reshape(n, width)
+        g = torch.Generator().manual_seed(n)
+        kv = torch.randn(n * width, page, rank + 64, generator=g).to(dtype)
+        scale = None if dtype == BF else torch.tensor([0.37])
+        new = (100 * torch.randn(cap, rank + 8, generator=g)).to(BF)[:, :rank]
+        rope = torch.randn(cap, 64, generator=g).to(BF)
+        new[0, 0], rope[0, 1] = float("nan"), 1e30
+        d = kv.cuda()
+        wide = torch.empty(cap, rank + 8, dtype=BF, device="cuda")
+        wide[:, :rank] = new.cuda()
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        cache = sv.LatentCache(d, rank, None if scale is None else scale.cuda())
+        sv.sv_latent_append(cache, torch.from_numpy(table).cuda(), wide[:, :rank], rope.cuda(),
+                            torch.from_numpy(req).cuda(), torch.from_numpy(pos).cuda(),
+                            torch.from_numpy(ctx).cuda(), err)
+        want = latent_append(values(kv), table, values(new), values(rope), req, pos, ctx,
+                             None if scale is None else scale.item())
+        assert int(err) == 0
+        np.testing.assert_array_equal(values(d), want)
+
+
+def test_append_faults():
+    kv = torch.zeros(4, 16, 320, dtype=BF, device="cuda")
+    cache = sv.LatentCache(kv, 256)
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    one = torch.ones(1, 256, dtype=BF, device="cuda"), torch.ones(1, 64, dtype=BF, device="cuda")
+    for req, pos, ctx, table, bit in (
+            (2, 0, 0, (0, 1), sv.SV_DEV_BAD_CU_ROWS), (-2, 0, 0, (0, 1), sv.SV_DEV_BAD_CU_ROWS),
+            (0, -1, 0, (0, 1), sv.SV_DEV_BAD_CU_ROWS), (0, 0, -1, (0, 1), sv.SV_DEV_BAD_CTX),
+            (0, 0, 32, (0, 1), sv.SV_DEV_BAD_CTX), (0, 1, 15, (0, 4), sv.SV_DEV_BAD_PAGE),
+            (0, 0, 0, (-1, 1), sv.SV_DEV_BAD_PAGE), (-1, 5, 10 ** 6, (9, 9), 0)):
+        err = i32(0)
+        sv.sv_latent_append(cache, i32(table, table), *one, i32(req), i32(pos), i32(ctx, ctx), err)
+        assert int(err) == bit and float(kv.abs().sum()) == 0
+
+
+def test_two_calls_at_once_and_graphs():
+    b = Batch(15, [2, 1, 3], [900, 33, 410], 16, 512, 16).device()
+    want, want_lse, _ = b.attend()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    args = b.table.cuda(), b.q.cuda(), b.cu.cuda(), b.ctx.cuda()
+    outs = [torch.full_like(want, -7.0) for _ in streams]
+    wss = [b.ws() for _ in streams]
+    torch.cuda.synchronize()
+    for s, o, ws in zip(streams, outs, wss):
+        sv.sv_latent_attend(b.cache, args[0], args[1], args[2], args[3], b.k_max, b.scale, o, ws,
+                            stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs)
+    out, lse, ws = torch.zeros_like(want), torch.zeros_like(want_lse), b.ws()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        sv.sv_latent_attend(b.cache, args[0], args[1], args[2], args[3], b.k_max, b.scale, out, ws,
+                            lse)
+    for i in range(4):
+        args[1].copy_(torch.randn_like(args[1]))
+        args[3].copy_(torch.tensor([900 - 10 * i, 33 + i, 7 * i], dtype=torch.int32))
+        graph.replay()
+        torch.cuda.synchronize()
+        b.q, b.ctx = args[1].cpu(), args[3].cpu()
+        eager, eager_lse, _ = b.attend()
+        n = int(b.cu[-1])
+        assert torch.equal(out[:n], eager[:n]) and torch.equal(lse[:n], eager_lse[:n])
