@@ -64,6 +64,25 @@ __device__ __forceinline__ int2 e4m3_of(const uint4& w, float s) {
     return make_int2(lo, hi);
 }
 
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+    return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char*)p;
+}
+
+// 16 bytes a lane from `from` + i STEP (each lane's own) to LDS at `to` + 16 lane (the
+// same `to` in every lane), without registers.  Done when vmcnt says so: the
+// caller waits, then meets the other waves at a barrier.  In assembly because
+// the compiler waits for such a load before any later read of LDS, whichever
+// part of it that reads.  The instruction's offset counts in both addresses.
+template <int STEP>
+__device__ __forceinline__ void load_to_lds(const char* from, uint32_t to, int i) {
+    uint32_t keep;  // m0 is the compiler's
+    asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 1\n\t"
+                 "global_load_lds_dwordx4 %2, off offset:%3\n\ts_mov_b32 m0, %0"
+                 : "=&s"(keep)
+                 : "s"(to - i * STEP), "v"(from), "i"(i * STEP)
+                 : "memory");
+}
+
 // The request of rank `rank` by context length, longest first (ties to the
 // lower request): where workgroups take turns on the CUs, a long request that
 // starts last would be waited for alone (256 requests of 0 .. 4096 positions: 429

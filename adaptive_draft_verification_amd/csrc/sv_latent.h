@@ -47,7 +47,7 @@ struct LatentAttendArgs {
     int32_t* dev_error;
     bool longest_first;  // requests by length (n_req <= 256)
     int page_shift;      // log2 of the page size, -1 if it is no power of two
-    int slot_waves, slot_blocks, parts, part_min;  // LatentPlan's
+    int slot_blocks, parts, part_min;  // LatentPlan's
     float* part_out;     // parts > 1: [n_req, k_max + 1, n_heads, parts, latent_dim]
     float* part_ml;      //            [..., parts, 2] m and sum
 };
@@ -55,15 +55,12 @@ hipError_t launch_latent_attend(const LatentAttendArgs& a, hipStream_t stream);
 
 // How a call is cut into workgroups: by host-known sizes alone.
 struct LatentPlan {
-    int slot_waves;   // waves over a workgroup's query slots, 32 each: 4 or 2 (the
-                      // other two then take half of the positions)
-    int slot_blocks;  // workgroups over a request's query slots
+    int slot_blocks;  // workgroups over a request's query slots, 64 each
     int parts;        // workgroups over the cached positions, at most
     int part_min;     // positions a part has at least
     LatentPlan(int n_req, int k_max, int n_heads, int64_t capacity) {
         const int64_t slots = (int64_t)(k_max + 1) * n_heads;
-        slot_waves = slots > 64 && (slots + 127) / 128 * n_req >= 256 ? 4 : 2;
-        const int block = 32 * slot_waves;
+        constexpr int block = 64;
         slot_blocks = (int)((slots + block - 1) / block);
         // A part writes, and the join reads, four bytes a slot and latent dim, as much
         // as two positions' keys: four positions a slot keep that below the products'

@@ -9,9 +9,7 @@
 namespace sv {
 namespace {
 
-typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 // ------------------------------------------------------------------- append
 
@@ -57,20 +55,23 @@ __global__ void latent_append_kernel(LatentAppendArgs a) {
 // ------------------------------------------------------------------- attend
 //
 // A request's query slots are its rows times the heads (slot i: row i / H, head
-// i % H): all of them read the same vectors.  A workgroup of four waves takes 32 WS
-// slots over one part of the cached positions, N = 32 * 4 / WS of them at a time,
-// in LDS as bf16; wave (ws, wp) takes 32 slots and 32 positions, with everything
-// else in registers, in the operand layouts of v_mfma_f32_32x32x16_bf16:
-//   S^T = K Q^T: operand A holds 32 positions (lane % 32) by 16 dims, B 32 slots by
-//   the same dims, kept in registers over the whole length, so a lane ends with
-//   scores of ONE slot (lane % 32) at positions 8 (i / 4) + 4 h + i % 4 (h = lane /
-//   32, i = 0 .. 15);
-//   O^T = C^T P^T: B's lane holds 8 positions of one slot, in the order in which
-//   the lane has them from S; A needs the same 8 positions of one dim a lane:
-//   two transposing LDS reads of 4 positions by 16 dims for each 16 lanes.
-// With 32 slots a wave each KB read from LDS feeds 32 clocks of products: the
-// 128 bytes a clock that LDS gives are two thirds used at full rate.  512 registers
-// a lane: queries 4 (R + 64) / 16, accumulators R / 2.
+// i % H): all of them read the same vectors.  A workgroup of four waves takes 64
+// slots over one part of the cached positions, 32 of them at a time, which lie in
+// LDS as bf16.  A pair of waves takes 32 slots.  Each of the two takes the scores
+// of 16 positions over all dims and half of the output's dims over all 32 positions,
+// so that the accumulators are R / 4 registers a lane beside R / 4 + 16 of queries;
+// the weights of the other 16 positions come from the other wave through LDS.
+// Operands of v_mfma_f32_16x16x32_bf16:
+//   S^T = K Q^T: A holds 16 positions (lane % 16) by 32 dims (8 for each g = lane /
+//   16), B 16 slots by the same dims, so a lane ends with the scores of ONE slot
+//   (lane % 16) at positions 4 g .. 4 g + 3;
+//   O^T = C^T P^T: B's lane holds 8 positions of one slot, 4 g .. of either wave's
+//   16, just as the two have them; A needs the same positions of one dim a lane: two
+//   transposing LDS reads of 4 positions by 16 dims for each 16 lanes.
+// A KB read from LDS feeds 32 clocks of products with keys and 64 with values: 95
+// of the 128 bytes a clock that LDS gives at full rate.  The weights of a tile are
+// taken between the products of the tile before with its values: one wave a SIMD
+// has the registers, so nothing else would fill that time.
 // In LDS 8 positions by 8 chunks of 16 bytes are a KB, the chunk c of position x at
 // (c ^ swizzle(x)) of its 128 bytes: 8 neighbouring positions' chunk c, and 4
 // positions' chunks c and c ^ 1, lie in different banks.  A load brings one such KB,
@@ -78,45 +79,47 @@ __global__ void latent_append_kernel(LatentAppendArgs a) {
 
 __device__ __forceinline__ int swizzle(int pos) { return ((pos & 3) << 1) | ((pos >> 2) & 1); }
 
-template <int R, bool F8, int WS>
+template <int R, bool F8>
 struct Latent {
-    static constexpr int kWaves = 4, kWP = kWaves / WS, kTile = 32 * kWP;
+    static constexpr int kTile = 32, kSlots = 64;
     static constexpr int kDim = R + SV_LATENT_ROPE, kChunks = kDim / 8;
-    static constexpr int kRow = kDim * 2;           // bytes
-    static constexpr int kTileBytes = kTile * kRow;
-    static constexpr int kGroups = kTile / 8 / kWaves;  // 8-position groups a wave brings
-    static constexpr int kLoads = kChunks / 8;          // of each
-    static constexpr int kGroup = kRow * 8;             // bytes
-    static constexpr int kSteps = kDim / 16;        // products of a score
-    static constexpr int kDims = R / 32;            // 32-dim tiles of the output
+    static constexpr int kGroup = kDim * 2 * 8;    // bytes of 8 positions
+    static constexpr int kTileBytes = 4 * kGroup;  // a group a wave
+    static constexpr int kLoads = kChunks / 8;     // of a group
+    static constexpr int kSteps = kDim / 32;       // products of a score
+    static constexpr int kDims = R / 32;           // 16-dim tiles of a wave's output
     static constexpr int kEsize = F8 ? 1 : 2;
-    // Weights are 2^(score - m), m kHold above the first scores' maximum and raised
-    // where a score passes that by 2^kSlack: weights are 2^-32 at most, so that sums
-    // over 2^31 positions stay below 1 and sums of weighted values in fp32's range,
-    // however large the values are.  Raising is rare: it takes the accumulators out
-    // of the registers that products alone can use.
+    static constexpr int kIds = 2048;              // page ids in LDS, of as many positions
+    // Weights are 2^(score - m), m kHold above the maximum of the slot's first tile.
+    // They are 2^-32 at most while no score passes that maximum by 2^kSlack, so that
+    // sums over 2^31 positions stay below 1 and sums of weighted values in fp32's
+    // range, however large the values are.  Where one does, which is rare, the
+    // workgroup starts again from the true maxima.
     static constexpr float kHold = 64.0f, kSlack = 32.0f;
 };
 
-template <int R, bool F8, int WS>
+template <int R, bool F8>
 __global__ __launch_bounds__(256, 1) void latent_kernel(LatentAttendArgs a) {
-    using C = Latent<R, F8, WS>;
-    __shared__ __attribute__((aligned(16))) char tiles[2][C::kTileBytes];
-    __shared__ int lens[256];
-    __shared__ uint32_t absent[2][C::kWaves];  // bit i: position i of the wave's is none
-    __shared__ uint32_t tainted[2][C::kWaves];
+    using C = Latent<R, F8>;
+    __shared__ __attribute__((aligned(16))) char tiles[3][C::kTileBytes];
+    __shared__ uint4 weights[2][4][2][kWave];  // of even and odd tiles: a wave's, for the other
+    __shared__ float tops[4][32];              // maxima of a wave's slots
+    __shared__ int ids[C::kIds];               // page of position begin + i at i % kIds
+    // bit i: position i of the tile is none, or not finite
+    __shared__ uint32_t absent[3], tainted[3];
+    __shared__ int risen[2];  // a score passed its slot's m by too much, in an even or odd tile
     const sv_latent_cache& c = a.cache;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int col = lane & 31, h = lane >> 5;
-    const int ws = wave % WS, wp = wave / WS;
+    const int col = lane & 15, g = lane >> 4;
+    const int pair = wave >> 1, half = wave & 1;
     // grid: slot blocks fastest, then requests and parts
     int id = spread(blockIdx.x, gridDim.x, a.slot_blocks);
     const int mb = id % a.slot_blocks;
     id /= a.slot_blocks;
     int r = id % a.n_req;
     const int part = id / a.n_req;
-    if (a.longest_first) r = longest(r, a.ctx_len, a.n_req, lens);
+    if (a.longest_first) r = longest(r, a.ctx_len, a.n_req, reinterpret_cast<int*>(tiles));
 
     const int lo = a.cu_rows[r], hi = a.cu_rows[r + 1];
     const int rows = hi - lo;
@@ -129,7 +132,7 @@ __global__ __launch_bounds__(256, 1) void latent_kernel(LatentAttendArgs a) {
         if (threadIdx.x == 0) raise_error(a.dev_error, SV_DEV_BAD_CTX);
         return;
     }
-    const int slots = rows * a.n_heads - mb * 32 * WS;  // slots of this block
+    const int slots = rows * a.n_heads - mb * C::kSlots;  // slots of this block
     if (slots <= 0) return;
     const int len = ctx + rows;
     const int plen = part_len(len, a.parts, a.part_min);
@@ -137,248 +140,319 @@ __global__ __launch_bounds__(256, 1) void latent_kernel(LatentAttendArgs a) {
     if (begin >= len) return;
     const bool whole = plen >= len;  // the request's only part
 
-    // ---- the vectors' way into LDS: wave w brings the 8-position groups w kGroups ..
+    // ---- the vectors' way into LDS: wave w brings positions 8 w .. 8 w + 7 of a tile
     const char* kv = static_cast<const char*>(c.kv);
     const int32_t* table = a.page_table + (int64_t)r * a.max_pages;
-    const int mine = wave * C::kGroups * 8 + (lane >> 3);  // in the first group
+    const int mine = wave * 8 + (lane >> 3);
     const int chunk_of = (lane & 7) ^ swizzle(lane >> 3);
-    struct Pages {
-        int id[C::kGroups];
+    auto page_of = [&](int t) {
+        return a.page_shift >= 0 ? t >> a.page_shift : (int)((unsigned)t / (unsigned)c.page_size);
     };
-    auto pages_of = [&](int t0) {
-        Pages p;
-#pragma unroll
-        for (int g = 0; g < C::kGroups; ++g) {
-            const int t = min(t0 + mine + 8 * g, len - 1);
-            p.id[g] = table[a.page_shift >= 0 ? t >> a.page_shift : t / c.page_size];
-        }
-        return p;
+    // Page ids go through LDS too, kIds / 2 at a time: a wait for one of them in
+    // registers would be a wait for the tile that is on its way.
+    auto fetch_ids = [&](int from, int n) __attribute__((always_inline)) {
+        n = min(n, end - from);
+        for (int i = threadIdx.x; i < n; i += 256)
+            ids[(from + i - begin) & (C::kIds - 1)] = table[page_of(from + i)];
     };
-    uint2 raw[F8 ? C::kGroups : 1][F8 ? C::kLoads : 1];
+    // of position t0 + mine; past the end any one
+    auto look_up = [&](int t0) { return ids[(t0 + mine - begin) & (C::kIds - 1)]; };
+    uint2 raw[F8 ? C::kLoads : 1];
     bool bad = false;
-    // issues the loads of the tile at t0, whose pages these are
-    auto issue = [&](int t0, int buf, const Pages& pages) __attribute__((always_inline)) {
+    // issues the loads of the tile at t0
+    auto issue = [&](int t0, int buf, int page) __attribute__((always_inline)) {
+        const int t = t0 + mine;
+        const bool there = t < end, good = page >= 0 && page < c.n_pages;
+        bad |= there && !good;
+        const char* from =
+            kv + ((int64_t)(good ? page : 0) * c.page_stride +
+                  (int64_t)(t - page_of(t) * c.page_size) * c.token_stride + chunk_of * 8) *
+                     C::kEsize;
+        char* to = tiles[buf] + wave * C::kGroup;
+        const uint32_t to_lds = __builtin_amdgcn_readfirstlane(lds_address(to));
+        const uint64_t none = __ballot(!there || !good);
         uint32_t gone = 0;
 #pragma unroll
-        for (int g = 0; g < C::kGroups; ++g) {
-            const int t = t0 + mine + 8 * g, page = pages.id[g];
-            const int slot =
-                t - (a.page_shift >= 0 ? t >> a.page_shift : t / c.page_size) * c.page_size;
-            const bool there = t < end, good = page >= 0 && page < c.n_pages;
-            bad |= there && !good;
-            const char* from = kv + ((int64_t)page * c.page_stride + (int64_t)slot * c.token_stride +
-                                     chunk_of * 8) *
-                                        C::kEsize;
-            char* to = tiles[buf] + (wave * C::kGroups + g) * C::kGroup;
-            // bit i of a byte: the group's position i is none
-            const uint64_t none = __ballot(!there || !good);
+        for (int i = 0; i < 8; ++i) gone |= (uint32_t)((none >> (8 * i)) & 1) << i;
+        if (lane == 0) reinterpret_cast<uint8_t*>(&absent[buf])[wave] = (uint8_t)gone;
+        if (there && good) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) gone |= (uint32_t)((none >> (8 * i)) & 1) << (8 * g + i);
-            if (there && good) {
+            for (int i = 0; i < C::kLoads; ++i) {
+                if constexpr (F8) raw[i] = *reinterpret_cast<const uint2*>(from + i * 64);
+                else load_to_lds<128>(from, to_lds + i * 1024, i);
+            }
+        } else {
 #pragma unroll
-                for (int i = 0; i < C::kLoads; ++i) {
-                    if constexpr (F8) {
-                        raw[g][i] = *reinterpret_cast<const uint2*>(from + i * 64);
-                    } else {
-                        __builtin_amdgcn_global_load_lds(
-                            (const __attribute__((address_space(1))) void*)(from + i * 128),
-                            (__attribute__((address_space(3))) void*)(to + i * 1024), 16, 0, 0);
-                    }
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < C::kLoads; ++i) {
-                    if constexpr (F8) raw[g][i] = make_uint2(0, 0);
-                    else *reinterpret_cast<uint4*>(to + i * 1024 + lane * 16) = make_uint4(0, 0, 0, 0);
-                }
+            for (int i = 0; i < C::kLoads; ++i) {
+                if constexpr (F8) raw[i] = make_uint2(0, 0);
+                else *reinterpret_cast<uint4*>(to + i * 1024 + lane * 16) = make_uint4(0, 0, 0, 0);
             }
         }
-        if (lane == 0) absent[buf][wave] = gone;
     };
     // an 8-bit tile goes into LDS as bf16 when it has arrived
     auto settle = [&](int buf) __attribute__((always_inline)) {
         if constexpr (F8) {
 #pragma unroll
-            for (int g = 0; g < C::kGroups; ++g)
-#pragma unroll
-                for (int i = 0; i < C::kLoads; ++i) {
-                    const uint2 v = raw[g][i];
-                    char* to = tiles[buf] + (wave * C::kGroups + g) * C::kGroup + i * 1024 + lane * 16;
-                    *reinterpret_cast<uint4*>(to) =
-                        make_uint4(e4m3_pair<false>(v.x), e4m3_pair<true>(v.x),
-                                   e4m3_pair<false>(v.y), e4m3_pair<true>(v.y));
-                }
+            for (int i = 0; i < C::kLoads; ++i)
+                *reinterpret_cast<uint4*>(tiles[buf] + wave * C::kGroup + i * 1024 + lane * 16) =
+                    make_uint4(e4m3_pair<false>(raw[i].x), e4m3_pair<true>(raw[i].x),
+                               e4m3_pair<false>(raw[i].y), e4m3_pair<true>(raw[i].y));
         }
+        __builtin_amdgcn_s_waitcnt(0);
     };
 
-    int t0 = begin, buf = 0;
-    issue(t0, 0, pages_of(t0));
-    Pages pages = pages_of(t0 + C::kTile);
+    if (threadIdx.x < 2) risen[threadIdx.x] = 0;
+    fetch_ids(begin, C::kIds);
+    __syncthreads();  // and the order of requests was read from where the tiles go
+    issue(begin, 0, look_up(begin));
 
-    // ---- queries of the wave's slots, operand B of every step
-    const int slot = mb * 32 * WS + ws * 32 + col;
-    const bool live = ws * 32 + col < slots;
-    const int q_row = slot / a.n_heads, head = slot - q_row * a.n_heads;
-    const int last = live ? ctx + q_row : -1;  // the last position the slot sees
-    bf16x8 q[C::kSteps];
-    {
+    // ---- queries of the pair's slots, operand B of every step
+    int q_row[2], head[2], last[2];  // last: the position a slot sees last
+    bool live[2];
+    bf16x8 q[C::kSteps][2];
+#pragma unroll
+    for (int sh = 0; sh < 2; ++sh) {
+        const int i = pair * 32 + sh * 16 + col, slot = mb * C::kSlots + i;
+        live[sh] = i < slots;
+        q_row[sh] = slot / a.n_heads;
+        head[sh] = slot - q_row[sh] * a.n_heads;
+        last[sh] = live[sh] ? ctx + q_row[sh] : -1;
         // a slot that is not there takes the first one's: it sees nothing
         const uint16_t* qp = static_cast<const uint16_t*>(a.q) +
-                             (int64_t)(live ? lo + q_row : lo) * a.q_ld +
-                             (int64_t)(live ? head : 0) * C::kDim + h * 8;
+                             (int64_t)(live[sh] ? lo + q_row[sh] : lo) * a.q_ld +
+                             (int64_t)(live[sh] ? head[sh] : 0) * C::kDim + g * 8;
 #pragma unroll
         for (int st = 0; st < C::kSteps; ++st) {
-            const uint4 w = *reinterpret_cast<const uint4*>(qp + st * 16);
-            q[st] = as_bf16x8(w.x, w.y, w.z, w.w);
+            const uint4 w = *reinterpret_cast<const uint4*>(qp + st * 32);
+            q[st][sh] = as_bf16x8(w.x, w.y, w.z, w.w);
         }
     }
+    // waited for here, not among the loads of a tile
+#pragma unroll
+    for (int st = 0; st < C::kSteps; ++st)
+        asm volatile("" : "+v"(q[st][0]), "+v"(q[st][1]));
     const float kv_scale = F8 && c.scale != nullptr ? *c.scale : 1.0f;
     const float scale = a.scale * kLog2e * kv_scale;
 
-    f32x16 acc[C::kDims];
-#pragma unroll
-    for (int i = 0; i < C::kDims; ++i)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) acc[i][e] = 0.0f;
-    float m = -kInf, mu = 0.0f, l = 0.0f;  // running m (-inf: no score yet), the m used, sum
+    f32x4 acc[C::kDims][2];
+    float m[2] = {-kInf, -kInf}, mu[2] = {0.0f, 0.0f};  // m (-inf: no score yet), the m used
+    float l[2];                                         // sum
 
-    // where a lane reads keys: chunks 2 st + h of its position
-    const int k_pos = wp * 32 + col;
-    const int k_at = (k_pos >> 3) * C::kGroup + (k_pos & 7) * 128;
-    const int k_sw = swizzle(k_pos);
-    // and values: 4 positions by 16 dims for 16 lanes
-    const int v_pos = wp * 32 + 4 * h + ((lane & 15) >> 2);
-    const int v_at = (v_pos >> 3) * C::kGroup + (v_pos & 7) * 128 + (lane & 1) * 8;
-    const int v_sw = swizzle(v_pos);
-    const int v_chunk = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+    // where a lane reads keys: chunks 4 st + g of its position, st = 0, 1 of 128 bytes
+    int k_at[2], v_at[4];
+    {
+        const int pos = half * 16 + col, at = (pos >> 3) * C::kGroup + (pos & 7) * 128;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) k_at[j] = at + ((4 * j + g) ^ swizzle(pos)) * 16;
+    }
+    // and values: 4 positions by 16 dims for 16 lanes, tiles 0 .. 3 of 128 bytes, from
+    // the wave's half of the dims on
+    {
+        const int pos = 4 * g + (col >> 2);
+        const int at = (pos >> 3) * C::kGroup + (pos & 7) * 128 + (lane & 1) * 8 +
+                       half * (R / 128) * 1024;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            v_at[j] = at + ((2 * j + ((lane >> 1) & 1)) ^ swizzle(pos)) * 16;
+    }
+    constexpr int kAhead = 4;  // LDS reads stay that many steps ahead of their products
 
-    bool again = false;  // the tile at t0 is taken a second time, m having been raised
-    for (;;) {
-        float to = 0.0f;
-        for (; t0 < end; t0 += C::kTile, buf ^= 1) {
-            const bool edge = t0 + C::kTile > ctx;
-            if (!again) {
-                settle(buf);
-                __builtin_amdgcn_s_waitcnt(0);
-                __syncthreads();
-                if (t0 + C::kTile < end) {
-                    issue(t0 + C::kTile, buf ^ 1, pages);
-                    pages = pages_of(t0 + 2 * C::kTile);
+    // The tile at t0 has arrived: sends for the next one, and cleans this one where it
+    // holds the step's own rows.
+    auto enter = [&](int t0, int buf, int& page) __attribute__((always_inline)) {
+        if (t0 + C::kTile < end) {
+            issue(t0 + C::kTile, buf == 2 ? 0 : buf + 1, page);
+            page = look_up(t0 + 2 * C::kTile);
+        }
+        if (t0 > begin && ((t0 - begin) & (C::kIds / 2 - 1)) == 0)
+            fetch_ids(t0 + C::kIds / 2, C::kIds / 2);
+        if (t0 + C::kTile > ctx) {
+            // These rows do not all see each other: a vector that is not finite may
+            // touch only those that see it.  It is zeroed, and its score is NaN.
+            uint32_t taint = 0;
+#pragma unroll 1
+            for (int i = 0; i < 8; ++i) {
+                if (t0 + wave * 8 + i <= ctx) continue;
+                uint4* at = reinterpret_cast<uint4*>(tiles[buf] + wave * C::kGroup + i * 128 +
+                                                     (lane >> 3) * 1024 + (lane & 7) * 16);
+                bool nf = false;
+                for (int ch = 0; ch < C::kChunks; ch += kWave) {
+                    if (ch + lane >= C::kChunks) break;
+                    const uint4 w = at[ch * 8];
+                    nf |= bf16_pair_nonfinite(w.x) || bf16_pair_nonfinite(w.y) ||
+                          bf16_pair_nonfinite(w.z) || bf16_pair_nonfinite(w.w);
                 }
-                if (edge) {
-                    // The step's own rows do not all see each other: a vector that is not
-                    // finite may touch only those that see it.  It is zeroed, and its
-                    // score is NaN.
-                    uint32_t taint = 0;
-                    for (int i = 0; i < C::kGroups * 8; ++i) {
-                        const int pos = wave * C::kGroups * 8 + i;
-                        if (t0 + pos <= ctx) continue;
-                        uint4* at = reinterpret_cast<uint4*>(
-                            tiles[buf] + (pos >> 3) * C::kGroup + (pos & 7) * 128 +
-                            (lane >> 3) * 1024 + (lane & 7) * 16);
-                        bool nf = false;
-                        for (int ch = 0; ch < C::kChunks; ch += kWave) {
-                            if (ch + lane >= C::kChunks) break;
-                            const uint4 w = at[ch * 8];
-                            nf |= bf16_pair_nonfinite(w.x) || bf16_pair_nonfinite(w.y) ||
-                                  bf16_pair_nonfinite(w.z) || bf16_pair_nonfinite(w.w);
-                        }
-                        if (__ballot(nf) == 0) continue;
-                        taint |= 1u << i;
-                        for (int ch = 0; ch < C::kChunks; ch += kWave)
-                            if (ch + lane < C::kChunks) at[ch * 8] = make_uint4(0, 0, 0, 0);
-                    }
-                    if (lane == 0) tainted[buf][wave] = taint;
-                    __syncthreads();
-                }
+                if (__ballot(nf) == 0) continue;
+                taint |= 1u << i;
+                for (int ch = 0; ch < C::kChunks; ch += kWave)
+                    if (ch + lane < C::kChunks) at[ch * 8] = make_uint4(0, 0, 0, 0);
             }
-            const char* tile = tiles[buf];
-            uint64_t none = 0, nan = 0;  // positions of the tile
+            if (lane == 0) reinterpret_cast<uint8_t*>(&tainted[buf])[wave] = (uint8_t)taint;
+            __syncthreads();
+        }
+    };
+    // The scores of the lane's four positions and two slots, in units of log2.
+    auto score = [&](int t0, int buf, float (&p)[2][4]) __attribute__((always_inline)) {
+        const char* tile = tiles[buf];
+        auto key = [&](int st) __attribute__((always_inline)) {
+            const uint4 w = *reinterpret_cast<const uint4*>(tile + k_at[st & 1] + (st >> 1) * 1024);
+            return as_bf16x8(w.x, w.y, w.z, w.w);
+        };
+        f32x4 s[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
+        bf16x8 k8[kAhead];
 #pragma unroll
-            for (int w = 0; w < C::kWaves; ++w) {
-                none |= (uint64_t)absent[buf][w] << (w * C::kGroups * 8);
-                if (edge) nan |= (uint64_t)tainted[buf][w] << (w * C::kGroups * 8);
-            }
-            const uint32_t no = (uint32_t)(none >> (wp * 32)), nn = (uint32_t)(nan >> (wp * 32));
-
-            // LDS reads stay kAhead products ahead of their own, in this order
-            constexpr int kAhead = 4;
-            auto key = [&](int st) __attribute__((always_inline)) {
-                const int chunk = 2 * st + h;
-                const uint4 w = *reinterpret_cast<const uint4*>(
-                    tile + k_at + (st >> 2) * 1024 + ((chunk & 7) ^ k_sw) * 16);
-                return as_bf16x8(w.x, w.y, w.z, w.w);
-            };
-            f32x16 s;
+        for (int st = 0; st < kAhead; ++st) k8[st] = key(st);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) s[e] = 0.0f;
-            bf16x8 k8[kAhead];
+        for (int st = 0; st < C::kSteps; ++st) {
 #pragma unroll
-            for (int st = 0; st < kAhead; ++st) k8[st] = key(st);
+            for (int sh = 0; sh < 2; ++sh)
+                s[sh] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k8[st % kAhead], q[st][sh], s[sh], 0,
+                                                                0, 0);
+            if (st + kAhead < C::kSteps) k8[st % kAhead] = key(st + kAhead);
             __builtin_amdgcn_sched_barrier(0);
+        }
+        const bool edge = t0 + C::kTile > ctx;
+        const uint32_t none = __builtin_amdgcn_readfirstlane(absent[buf]);
 #pragma unroll
-            for (int st = 0; st < C::kSteps; ++st) {
-                s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k8[st % kAhead], q[st], s, 0, 0, 0);
-                if (st + kAhead < C::kSteps) k8[st % kAhead] = key(st + kAhead);
-                __builtin_amdgcn_sched_barrier(0);
-            }
-
-            float p[16];
+        for (int sh = 0; sh < 2; ++sh)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) p[e] = s[e] * scale;
-            if (edge || (no | nn) != 0) {
+            for (int e = 0; e < 4; ++e) p[sh][e] = s[sh][e] * scale;
+        if (edge || none != 0) {
+            const int first = half * 16 + 4 * g;
+            const uint32_t no = none >> first, nan = edge ? tainted[buf] >> first : 0;
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const int pos = 8 * (e >> 2) + 4 * h + (e & 3);
-                    if ((nn >> pos) & 1) p[e] = __builtin_nanf("");
-                    if (((no >> pos) & 1) || t0 + wp * 32 + pos > last) p[e] = -kInf;
+            for (int sh = 0; sh < 2; ++sh) {
+                const int sees = last[sh] - (t0 + first);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if ((nan >> e) & 1) p[sh][e] = __builtin_nanf("");
+                    if (((no >> e) & 1) || e > sees) p[sh][e] = -kInf;
                 }
             }
-            float mx = p[0];
+        }
+    };
+    // Over the lanes of a slot.
+    auto top_of = [&](float x) {
+        x = fmaxf(x, __shfl_xor(x, 16));
+        return fmaxf(x, __shfl_xor(x, 32));
+    };
+    // The pair's maximum of both slots, from each lane's own.
+    auto exchange = [&](float (&x)[2]) __attribute__((always_inline)) {
 #pragma unroll
-            for (int e = 1; e < 16; ++e) mx = fmaxf(mx, p[e]);
-            if (__ballot(mx > m + (C::kSlack - C::kHold)) != 0) {
-                mx = fmaxf(mx, __shfl_xor(mx, 32));
-                to = fmaxf(m, mx + C::kHold);
-                // the slot's first scores: nothing to rescale yet
-                if (m == -kInf && to > m) m = mu = to;
-                if (__ballot(to > m + C::kSlack) != 0) break;
+        for (int sh = 0; sh < 2; ++sh) {
+            x[sh] = top_of(x[sh]);
+            if (g == 0) tops[wave][sh * 16 + col] = x[sh];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int sh = 0; sh < 2; ++sh) x[sh] = fmaxf(x[sh], tops[wave ^ 1][sh * 16 + col]);
+    };
+
+    auto refer = [&](const float (&top)[2]) {
+#pragma unroll
+        for (int sh = 0; sh < 2; ++sh) {
+            m[sh] = top[sh] + C::kHold;
+            mu[sh] = m[sh] == -kInf ? 0.0f : m[sh];
+        }
+    };
+    // Weights go into the product as two bf16 terms, the upper half of the fp32 weight
+    // and the rest, off by at most 2^-15 of each: one term's 2^-8 would show in the
+    // result beside its own rounding.  Both are positive where the weight is (the rest
+    // of 1 + 2^-23 times it is taken): an infinite value times 0 or a negative rest
+    // would make NaN.
+    auto weigh = [&](float& x, int sh) __attribute__((always_inline)) {
+        x = fast_exp2(x - mu[sh]);
+        l[sh] += x;
+    };
+    auto split = [&](const float (&p)[4]) __attribute__((always_inline)) {
+        constexpr float kOneUp = 1.0f + 0x1p-23f;
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float x = p[2 * i], y = p[2 * i + 1];
+            const uint32_t xb = __float_as_uint(x), yb = __float_as_uint(y);
+            w[i] = __builtin_amdgcn_perm(yb, xb, 0x07060302u);
+            w[2 + i] = pack_bf16(fmaf(x, kOneUp, -bf16_hi(xb)), fmaf(y, kOneUp, -bf16_hi(yb)));
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    };
+
+    // a second time from the true maxima, if a score rose too far above the first ones
+    for (bool again = false;; again = true) {
+#pragma unroll
+        for (int i = 0; i < C::kDims; ++i)
+#pragma unroll
+            for (int sh = 0; sh < 2; ++sh) acc[i][sh] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        l[0] = l[1] = 0.0f;
+        if (again) {
+            fetch_ids(begin, C::kIds);
+            __syncthreads();
+            issue(begin, 0, look_up(begin));
+        }
+        int page = look_up(begin + C::kTile);
+        uint4 own[2];  // weights of the tile before: slots 0 .. 15, 16 .. 31; two terms each
+        {
+            settle(0);
+            __syncthreads();
+            enter(begin, 0, page);
+            float p[2][4];
+            score(begin, 0, p);
+            if (!again) {
+                float mx[2];
+#pragma unroll
+                for (int sh = 0; sh < 2; ++sh)
+                    mx[sh] = fmaxf(fmaxf(p[sh][0], p[sh][1]), fmaxf(p[sh][2], p[sh][3]));
+                exchange(mx);
+                refer(mx);
             }
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                p[e] = fast_exp2(p[e] - mu);
-                l += p[e];
+            for (int sh = 0; sh < 2; ++sh) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) weigh(p[sh][e], sh);
+                own[sh] = split(p[sh]);
+                weights[0][wave][sh][lane] = own[sh];
             }
-            // Weights go into the product as two bf16 terms, the upper half of the fp32
-            // weight and the rest, off by at most 2^-15 of each: one term's 2^-8 would
-            // show in the result beside its own rounding.  Both are positive where the
-            // weight is (the rest of 1 + 2^-23 times it is taken): an infinite value
-            // times 0 or a negative rest would make NaN.
-            constexpr float kOneUp = 1.0f + 0x1p-23f;
+        }
+        // a turn takes the scores of its tile (there is none in the last turn) and the
+        // values of the one before
+        bool rose = false, more = true;
+        int buf = 1, odd = 1;
+        for (int t0 = begin + C::kTile; more; t0 += C::kTile) {
+            settle(buf);
+            __syncthreads();
+            // in the tile before: no wave is a tile further before this one has read it
+            rose = !again && __builtin_amdgcn_readfirstlane(risen[odd ^ 1]) != 0;
+            more = t0 < end && !rose;
+            float p[2][4] = {};
+            if (more) {
+                enter(t0, buf, page);
+                score(t0, buf, p);
+                if (!again) {
+                    bool far = false;
+#pragma unroll
+                    for (int sh = 0; sh < 2; ++sh)
+                        far |= fmaxf(fmaxf(p[sh][0], p[sh][1]), fmaxf(p[sh][2], p[sh][3])) >
+                               m[sh] + (C::kSlack - C::kHold);
+                    if (__ballot(far) != 0 && lane == 0) risen[odd] = 1;
+                }
+            }
+            // positions 4 g .. of either wave's 16, in their order
+            const char* tile = tiles[buf == 0 ? 2 : buf - 1];
             bf16x8 pb[2], pr[2];
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                uint32_t hw[4], rw[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float x = p[8 * t + 2 * i], y = p[8 * t + 2 * i + 1];
-                    const uint32_t xb = __float_as_uint(x), yb = __float_as_uint(y);
-                    hw[i] = __builtin_amdgcn_perm(yb, xb, 0x07060302u);
-                    rw[i] = pack_bf16(fmaf(x, kOneUp, -bf16_hi(xb)), fmaf(y, kOneUp, -bf16_hi(yb)));
-                }
-                pb[t] = as_bf16x8(hw[0], hw[1], hw[2], hw[3]);
-                pr[t] = as_bf16x8(rw[0], rw[1], rw[2], rw[3]);
+            for (int sh = 0; sh < 2; ++sh) {
+                const uint4 o = weights[odd ^ 1][wave ^ 1][sh][lane];
+                const uint4 x = half == 0 ? own[sh] : o, y = half == 0 ? o : own[sh];
+                pb[sh] = as_bf16x8(x.x, x.y, y.x, y.y);
+                pr[sh] = as_bf16x8(x.z, x.w, y.z, y.w);
             }
-            // 16 positions (half t of the wave's) of 32 dims
-            auto value = [&](int it) __attribute__((always_inline)) {
-                const int i = it >> 1, t = it & 1;
-                const int chunk = 4 * i + v_chunk;
-                const char* at = tile + v_at + t * 2 * C::kGroup + (i >> 1) * 1024 +
-                                 ((chunk & 7) ^ v_sw) * 16;
+            auto value = [&](int i) __attribute__((always_inline)) {
+                const char* at = tile + v_at[i & 3] + (i >> 2) * 1024;
                 const s16x4 x0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
                     (__attribute__((address_space(3))) s16x4*)at);
                 const s16x4 x1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                    (__attribute__((address_space(3))) s16x4*)(at + C::kGroup));
+                    (__attribute__((address_space(3))) s16x4*)(at + 2 * C::kGroup));
                 uint2 w0, w1;
                 __builtin_memcpy(&w0, &x0, 8);
                 __builtin_memcpy(&w1, &x1, 8);
@@ -386,118 +460,126 @@ __global__ __launch_bounds__(256, 1) void latent_kernel(LatentAttendArgs a) {
             };
             bf16x8 v8[kAhead];
 #pragma unroll
-            for (int it = 0; it < kAhead; ++it) v8[it] = value(it);
+            for (int i = 0; i < kAhead; ++i) v8[i] = value(i);
             __builtin_amdgcn_sched_barrier(0);
+            const float keep[2] = {l[0], l[1]};
 #pragma unroll
-            for (int it = 0; it < 2 * C::kDims; ++it) {
-                const int i = it >> 1, t = it & 1;
-                acc[i] =
-                    __builtin_amdgcn_mfma_f32_32x32x16_bf16(v8[it % kAhead], pb[t], acc[i], 0, 0, 0);
-                acc[i] =
-                    __builtin_amdgcn_mfma_f32_32x32x16_bf16(v8[it % kAhead], pr[t], acc[i], 0, 0, 0);
-                if (it + kAhead < 2 * C::kDims) v8[it % kAhead] = value(it + kAhead);
+            for (int i = 0; i < C::kDims; ++i) {
+#pragma unroll
+                for (int sh = 0; sh < 2; ++sh)
+                    acc[i][sh] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v8[i % kAhead], pb[sh],
+                                                                         acc[i][sh], 0, 0, 0);
+#pragma unroll
+                for (int sh = 0; sh < 2; ++sh)
+                    acc[i][sh] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v8[i % kAhead], pr[sh],
+                                                                         acc[i][sh], 0, 0, 0);
+                if (i + kAhead < C::kDims) v8[i % kAhead] = value(i + kAhead);
+                // a weight of this turn's tile between the products
+                if (i < 8) weigh(p[i >> 2][i & 3], i >> 2);
                 __builtin_amdgcn_sched_barrier(0);
             }
-            again = false;
-        }
-        if (t0 >= end) break;
-        const float f = to > m ? fast_exp2(m - to) : 1.0f;
-        if (to > m) {
-            l *= f;
-            m = mu = to;
-        }
+            if (!more) {
+                l[0] = keep[0];
+                l[1] = keep[1];
+            }
 #pragma unroll
-        for (int i = 0; i < C::kDims; ++i)
+            for (int sh = 0; sh < 2; ++sh) {
+                own[sh] = split(p[sh]);
+                weights[odd][wave][sh][lane] = own[sh];
+            }
+            buf = buf == 2 ? 0 : buf + 1;
+            odd ^= 1;
+        }
+        if (!rose) break;
+        __syncthreads();  // every wave has left the tiles
+        fetch_ids(begin, C::kIds);
+        __syncthreads();
+        issue(begin, 0, look_up(begin));
+        page = look_up(begin + C::kTile);
+        float mx[2] = {-kInf, -kInf};
+        buf = 0;
+        for (int t0 = begin; t0 < end; t0 += C::kTile, buf = buf == 2 ? 0 : buf + 1) {
+            settle(buf);
+            __syncthreads();
+            enter(t0, buf, page);
+            float p[2][4];
+            score(t0, buf, p);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) acc[i][e] *= f;
-        again = true;
+            for (int sh = 0; sh < 2; ++sh)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) mx[sh] = fmaxf(mx[sh], p[sh][e]);
+        }
+        exchange(mx);
+        refer(mx);
+        __syncthreads();
     }
     if (__ballot(bad) != 0 && lane == 0) raise_error(a.dev_error, SV_DEV_BAD_PAGE);
 
-    // the other half's positions of the slot
-    l += __shfl_xor(l, 32);
-    if constexpr (C::kWP == 2) {
-        // and the other wave's: its accumulators, lane by lane, through LDS
-        __syncthreads();
-        f32x4* give = reinterpret_cast<f32x4*>(tiles[0]) + ws * (C::kDims * 4 + 1) * kWave + lane;
-        static_assert(WS * (C::kDims * 4 + 1) * kWave * 16 <= 2 * C::kTileBytes, "fits in the tiles");
-        if (wp == 1) {
+    // sums over the positions of a slot's lanes, and of the other wave
 #pragma unroll
-            for (int i = 0; i < C::kDims; ++i)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    give[(i * 4 + e) * kWave] = f32x4{acc[i][4 * e], acc[i][4 * e + 1],
-                                                      acc[i][4 * e + 2], acc[i][4 * e + 3]};
-            give[C::kDims * 4 * kWave] = f32x4{m, l, 0.0f, 0.0f};
-        }
-        __syncthreads();
-        if (wp == 1) return;
-        const f32x4 ml = give[C::kDims * 4 * kWave];
-        const float mx = fmaxf(m, ml[0]);
-        const float f1 = m == mx ? 1.0f : fast_exp2(m - mx);
-        const float f2 = ml[0] == mx ? 1.0f : fast_exp2(ml[0] - mx);
-        l = l * f1 + ml[1] * f2;
-        m = mx;
-#pragma unroll
-        for (int i = 0; i < C::kDims; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const f32x4 o = give[(i * 4 + e) * kWave];
-#pragma unroll
-                for (int x = 0; x < 4; ++x) acc[i][4 * e + x] = acc[i][4 * e + x] * f1 + o[x] * f2;
-            }
+    for (int sh = 0; sh < 2; ++sh) {
+        l[sh] += __shfl_xor(l[sh], 16);
+        l[sh] += __shfl_xor(l[sh], 32);
+        if (g == 0) tops[wave][sh * 16 + col] = l[sh];
     }
+    __syncthreads();
+#pragma unroll
+    for (int sh = 0; sh < 2; ++sh) {
+        const float o = tops[wave ^ 1][sh * 16 + col];
+        l[sh] = half == 0 ? l[sh] + o : o + l[sh];
+    }
+    const int dim0 = half * (R / 2);
     if (!whole) {
-        if (!live) return;
-        const int64_t rec =
-            (((int64_t)r * (a.k_max + 1) + q_row) * a.n_heads + head) * a.parts + part;
-        float* o = a.part_out + rec * R + 4 * h;
 #pragma unroll
-        for (int i = 0; i < C::kDims; ++i)
+        for (int sh = 0; sh < 2; ++sh) {
+            if (!live[sh]) continue;
+            const int64_t rec =
+                (((int64_t)r * (a.k_max + 1) + q_row[sh]) * a.n_heads + head[sh]) * a.parts + part;
+            float* o = a.part_out + rec * R + dim0 + 4 * g;
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                *reinterpret_cast<f32x4*>(o + i * 32 + e * 8) = f32x4{
-                    acc[i][4 * e], acc[i][4 * e + 1], acc[i][4 * e + 2], acc[i][4 * e + 3]};
-        if (h == 0) {
-            a.part_ml[rec * 2] = m;
-            a.part_ml[rec * 2 + 1] = l;
+            for (int i = 0; i < C::kDims; ++i) *reinterpret_cast<f32x4*>(o + i * 16) = acc[i][sh];
+            if (g == 0 && half == 0) {
+                a.part_ml[rec * 2] = m[sh];
+                a.part_ml[rec * 2 + 1] = l[sh];
+            }
         }
         return;
     }
-    // no weight at all: 0, also where 0 times a value was NaN
-    const bool nothing = l == 0.0f;
-    const float inv = nothing ? 0.0f : 1.0f / l;
-    uint16_t* o = static_cast<uint16_t*>(a.out) + (int64_t)(lo + q_row) * a.out_ld +
-                  (int64_t)head * R + 8 * h;
 #pragma unroll
-    for (int i = 0; i < C::kDims; ++i)
+    for (int sh = 0; sh < 2; ++sh) {
+        // no weight at all: 0, also where 0 times a value was NaN
+        const bool nothing = l[sh] == 0.0f;
+        const float inv = nothing ? 0.0f : 1.0f / l[sh];
+        // dims 8 (g / 2) .. of tile i + g % 2 after the exchange of quarters
+        uint16_t* o = static_cast<uint16_t*>(a.out) + (int64_t)(lo + q_row[sh]) * a.out_ld +
+                      (int64_t)head[sh] * R + dim0 + (g & 1) * 16 + (g >> 1) * 8;
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-            // dims 16 g .. 16 g + 7 and + 8 .. + 15 of the tile: halves of both in either
-            // half of the wave, exchanged so that a lane stores 8 in a row
-            uint32_t w[4];
+        for (int i = 0; i < C::kDims; i += 2) {
+            uint32_t w[2][2];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float x = acc[i][8 * g + 2 * e], y = acc[i][8 * g + 2 * e + 1];
-                // the mean first, then its scale: only their product has to be in range
-                w[e] = nothing ? 0u : pack_bf16(x * inv * kv_scale, y * inv * kv_scale);
-            }
-            const auto s0 = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
-            const auto s1 = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
-            if (live)
-                *reinterpret_cast<uint4*>(o + i * 32 + g * 16) =
-                    make_uint4(s0[0], s1[0], s0[1], s1[1]);
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float x = acc[i + j][sh][2 * e], y = acc[i + j][sh][2 * e + 1];
+                    // the mean first, then its scale: only their product has to be in range
+                    w[j][e] = nothing ? 0u : pack_bf16(x * inv * kv_scale, y * inv * kv_scale);
+                }
+            const auto s0 = __builtin_amdgcn_permlane16_swap(w[0][0], w[1][0], false, false);
+            const auto s1 = __builtin_amdgcn_permlane16_swap(w[0][1], w[1][1], false, false);
+            if (live[sh])
+                *reinterpret_cast<uint4*>(o + i * 16) = make_uint4(s0[0], s1[0], s0[1], s1[1]);
         }
-    if (live && a.out_lse != nullptr && h == 0)
-        a.out_lse[(int64_t)(lo + q_row) * a.n_heads + head] =
-            nothing ? -kInf : ((m - C::kHold) + log2f(l * exp2f(C::kHold))) * kLn2;
+        if (live[sh] && a.out_lse != nullptr && g == 0 && half == 0)
+            a.out_lse[(int64_t)(lo + q_row[sh]) * a.n_heads + head[sh]] =
+                nothing ? -kInf : ((m[sh] - C::kHold) + log2f(l[sh] * exp2f(C::kHold))) * kLn2;
+    }
 }
 
 // Merges the parts of a (row, head), a wave each: lanes over the dims.
 template <int R, bool F8>
 __global__ __launch_bounds__(256) void latent_join_kernel(LatentAttendArgs a) {
     constexpr int E = R / kWave;
-    constexpr float kHold = Latent<R, F8, 2>::kHold;
+    constexpr float kHold = Latent<R, F8>::kHold;
     __shared__ float factors[4][128];
     const sv_latent_cache& c = a.cache;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -564,8 +646,7 @@ __global__ __launch_bounds__(256) void latent_join_kernel(LatentAttendArgs a) {
 template <int R, bool F8>
 hipError_t run_latent(const LatentAttendArgs& a, hipStream_t stream) {
     const unsigned grid = (unsigned)((int64_t)a.n_req * a.slot_blocks * a.parts);
-    if (a.slot_waves == 4) latent_kernel<R, F8, 4><<<grid, 256, 0, stream>>>(a);
-    else latent_kernel<R, F8, 2><<<grid, 256, 0, stream>>>(a);
+    latent_kernel<R, F8><<<grid, 256, 0, stream>>>(a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.parts == 1) return e;
     const int64_t total = (int64_t)a.n_req * (a.k_max + 1) * a.n_heads;

@@ -129,7 +129,7 @@ sv_status sv_latent_attend(const sv_latent_cache* cache, const int32_t* page_tab
     const sv::LatentAttendArgs a{*cache, page_table, max_pages, q, q_ld, q_rows, n_heads, cu_rows,
                                  ctx_len, n_req, k_max, scale, out, out_ld, out_lse, dev_error,
                                  n_req > 1 && n_req <= 256 && p.grid(n_req) > 256,
-                                 log2_exact(cache->page_size), p.slot_waves, p.slot_blocks, p.parts,
+                                 log2_exact(cache->page_size), p.slot_blocks, p.parts,
                                  p.part_min, part_out, part_ml};
     const hipError_t e = sv::launch_latent_attend(a, as_stream(stream));
     return sv::finish_launch(e, as_stream(stream));
