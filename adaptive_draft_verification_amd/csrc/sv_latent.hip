@@ -73,11 +73,14 @@ __global__ void latent_append_kernel(LatentAppendArgs a) {
 // taken between the products of the tile before with its values: one wave a SIMD
 // has the registers, so nothing else would fill that time.
 // In LDS 8 positions by 8 chunks of 16 bytes are a KB, the chunk c of position x at
-// (c ^ swizzle(x)) of its 128 bytes: 8 neighbouring positions' chunk c, and 4
-// positions' chunks c and c ^ 1, lie in different banks.  A load brings one such KB,
-// 8 lanes a position.
+// (c ^ swizzle(x)) of its 128 bytes.  LDS has 64 banks of 4 bytes: the chunk c of 16
+// neighbouring positions, and the chunks c and c ^ 1 of 8, lie in different ones.
+// A load brings one such KB, 8 lanes a position.
 
-__device__ __forceinline__ int swizzle(int pos) { return ((pos & 3) << 1) | ((pos >> 2) & 1); }
+__device__ __forceinline__ int swizzle(int pos) { return (pos & 6) | ((pos >> 3) & 1); }
+
+// What a position without a page is loaded from.
+__device__ const uint4 kZeros[(512 + SV_LATENT_ROPE) / 8] = {};
 
 template <int R, bool F8>
 struct Latent {
@@ -87,9 +90,10 @@ struct Latent {
     static constexpr int kTileBytes = 4 * kGroup;  // a group a wave
     static constexpr int kLoads = kChunks / 8;     // of a group
     static constexpr int kSteps = kDim / 32;       // products of a score
+    static constexpr int kEarly = kSteps / 4;      // loads issued between them
     static constexpr int kDims = R / 32;           // 16-dim tiles of a wave's output
     static constexpr int kEsize = F8 ? 1 : 2;
-    static constexpr int kIds = 2048;              // page ids in LDS, of as many positions
+    static constexpr int kPlaces = 1024;           // positions whose places are in LDS
     // Weights are 2^(score - m), m kHold above the maximum of the slot's first tile.
     // They are 2^-32 at most while no score passes that maximum by 2^kSlack, so that
     // sums over 2^31 positions stay below 1 and sums of weighted values in fp32's
@@ -104,9 +108,10 @@ __global__ __launch_bounds__(256, 1) void latent_kernel(LatentAttendArgs a) {
     __shared__ __attribute__((aligned(16))) char tiles[3][C::kTileBytes];
     __shared__ uint4 weights[2][4][2][kWave];  // of even and odd tiles: a wave's, for the other
     __shared__ float tops[4][32];              // maxima of a wave's slots
-    __shared__ int ids[C::kIds];               // page of position begin + i at i % kIds
-    // bit i: position i of the tile is none, or not finite
-    __shared__ uint32_t absent[3], tainted[3];
+    __shared__ int64_t places[C::kPlaces];     // bytes to position begin + i at i % kPlaces
+    // a byte a position of the tile: it is none, or not finite
+    __shared__ __attribute__((aligned(4))) uint8_t absent[3][C::kTile], tainted[3][C::kTile];
+    __shared__ int holes;     // a position before the end is none
     __shared__ int risen[2];  // a score passed its slot's m by too much, in an even or odd tile
     const sv_latent_cache& c = a.cache;
     const int lane = threadIdx.x & 63;
@@ -144,50 +149,53 @@ __global__ __launch_bounds__(256, 1) void latent_kernel(LatentAttendArgs a) {
     const char* kv = static_cast<const char*>(c.kv);
     const int32_t* table = a.page_table + (int64_t)r * a.max_pages;
     const int mine = wave * 8 + (lane >> 3);
-    const int chunk_of = (lane & 7) ^ swizzle(lane >> 3);
-    auto page_of = [&](int t) {
-        return a.page_shift >= 0 ? t >> a.page_shift : (int)((unsigned)t / (unsigned)c.page_size);
-    };
-    // Page ids go through LDS too, kIds / 2 at a time: a wait for one of them in
-    // registers would be a wait for the tile that is on its way.
-    auto fetch_ids = [&](int from, int n) __attribute__((always_inline)) {
-        n = min(n, end - from);
-        for (int i = threadIdx.x; i < n; i += 256)
-            ids[(from + i - begin) & (C::kIds - 1)] = table[page_of(from + i)];
-    };
-    // of position t0 + mine; past the end any one
-    auto look_up = [&](int t0) { return ids[(t0 + mine - begin) & (C::kIds - 1)]; };
-    uint2 raw[F8 ? C::kLoads : 1];
+    const int chunk_of = ((lane & 7) ^ swizzle(mine)) * 8 * C::kEsize;
+    // The places of `n` positions from `from` on, into LDS: kPlaces at first, then half
+    // as many at a time (a wait for a page id in registers would be a wait for the tile
+    // that is on its way).  -1: after the end, or on a page that is not there.
     bool bad = false;
-    // issues the loads of the tile at t0
-    auto issue = [&](int t0, int buf, int page) __attribute__((always_inline)) {
-        const int t = t0 + mine;
-        const bool there = t < end, good = page >= 0 && page < c.n_pages;
-        bad |= there && !good;
-        const char* from =
-            kv + ((int64_t)(good ? page : 0) * c.page_stride +
-                  (int64_t)(t - page_of(t) * c.page_size) * c.token_stride + chunk_of * 8) *
-                     C::kEsize;
-        char* to = tiles[buf] + wave * C::kGroup;
-        const uint32_t to_lds = __builtin_amdgcn_readfirstlane(lds_address(to));
-        const uint64_t none = __ballot(!there || !good);
-        uint32_t gone = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) gone |= (uint32_t)((none >> (8 * i)) & 1) << i;
-        if (lane == 0) reinterpret_cast<uint8_t*>(&absent[buf])[wave] = (uint8_t)gone;
-        if (there && good) {
-#pragma unroll
-            for (int i = 0; i < C::kLoads; ++i) {
-                if constexpr (F8) raw[i] = *reinterpret_cast<const uint2*>(from + i * 64);
-                else load_to_lds<128>(from, to_lds + i * 1024, i);
+    auto fetch_places = [&](int from, int n) __attribute__((always_inline)) {
+        for (int i = threadIdx.x; i < n && from + i < end + 3 * C::kTile; i += 256) {
+            const int t = from + i;
+            int64_t place = -1;
+            if (t < end) {
+                const int in = a.page_shift >= 0 ? t >> a.page_shift
+                                                 : (int)((unsigned)t / (unsigned)c.page_size);
+                const int page = table[in];
+                if (page >= 0 && page < c.n_pages) {
+                    place = ((int64_t)page * c.page_stride +
+                             (int64_t)(t - in * c.page_size) * c.token_stride) *
+                            C::kEsize;
+                } else {
+                    bad = true;
+                    holes = 1;
+                }
             }
-        } else {
-#pragma unroll
-            for (int i = 0; i < C::kLoads; ++i) {
-                if constexpr (F8) raw[i] = make_uint2(0, 0);
-                else *reinterpret_cast<uint4*>(to + i * 1024 + lane * 16) = make_uint4(0, 0, 0, 0);
-            }
+            places[(t - begin) & (C::kPlaces - 1)] = place;
         }
+    };
+    auto look_up = [&](int t0) { return places[(t0 + mine - begin) & (C::kPlaces - 1)]; };
+    uint2 raw[F8 ? C::kLoads : 1];
+    const char* from;
+    uint32_t to_lds;
+    // the loads of a tile are made ready, and then issued one by one
+    auto prepare = [&](int buf, int64_t place) __attribute__((always_inline)) {
+        from = (place >= 0 ? kv + place : reinterpret_cast<const char*>(kZeros)) + chunk_of;
+        absent[buf][mine] = place < 0;
+        to_lds = __builtin_amdgcn_readfirstlane(lds_address(tiles[buf] + wave * C::kGroup));
+    };
+    auto issue = [&](int i) __attribute__((always_inline)) {
+        if constexpr (F8) raw[i] = *reinterpret_cast<const uint2*>(from + i * 64);
+        else load_to_lds<128>(from, to_lds + i * 1024, i);
+    };
+    // the first tile's
+    auto start = [&]() __attribute__((always_inline)) {
+        fetch_places(begin, C::kPlaces);
+        __syncthreads();
+        prepare(0, look_up(begin));
+#pragma unroll
+        for (int i = 0; i < C::kLoads; ++i) issue(i);
+        return look_up(begin + C::kTile);
     };
     // an 8-bit tile goes into LDS as bf16 when it has arrived
     auto settle = [&](int buf) __attribute__((always_inline)) {
@@ -201,12 +209,20 @@ __global__ __launch_bounds__(256, 1) void latent_kernel(LatentAttendArgs a) {
         __builtin_amdgcn_s_waitcnt(0);
     };
 
-    if (threadIdx.x < 2) risen[threadIdx.x] = 0;
-    fetch_ids(begin, C::kIds);
-    __syncthreads();  // and the order of requests was read from where the tiles go
-    issue(begin, 0, look_up(begin));
+    // the order of requests was read from where the tiles go
+    if (threadIdx.x == 0) risen[0] = risen[1] = holes = 0;
+    __syncthreads();
+    int64_t place = start();
 
     // ---- queries of the pair's slots, operand B of every step
+    // The scale is taken as positive (queries change their sign with it), so that the
+    // largest product is the largest score and a masked -inf stays one; 0 as 1 of
+    // queries that are 0.
+    const float kv_scale = F8 && c.scale != nullptr ? *c.scale : 1.0f;
+    const float signed_scale = a.scale * kLog2e * kv_scale;
+    const float scale = signed_scale == 0.0f ? 1.0f : fabsf(signed_scale);
+    const uint32_t q_sign = signed_scale < 0.0f ? 0x80008000u : 0u;
+    const uint32_t q_keep = signed_scale == 0.0f ? 0u : ~0u;
     int q_row[2], head[2], last[2];  // last: the position a slot sees last
     bool live[2];
     bf16x8 q[C::kSteps][2];
@@ -224,54 +240,56 @@ __global__ __launch_bounds__(256, 1) void latent_kernel(LatentAttendArgs a) {
 #pragma unroll
         for (int st = 0; st < C::kSteps; ++st) {
             const uint4 w = *reinterpret_cast<const uint4*>(qp + st * 32);
-            q[st][sh] = as_bf16x8(w.x, w.y, w.z, w.w);
+            q[st][sh] = as_bf16x8((w.x ^ q_sign) & q_keep, (w.y ^ q_sign) & q_keep,
+                                  (w.z ^ q_sign) & q_keep, (w.w ^ q_sign) & q_keep);
         }
     }
-    // waited for here, not among the loads of a tile
+    // Waited for here, not among the loads of a tile.  512 registers a lane are 256 for
+    // any use and 256 for products alone: half of the queries go among the latter.
 #pragma unroll
     for (int st = 0; st < C::kSteps; ++st)
-        asm volatile("" : "+v"(q[st][0]), "+v"(q[st][1]));
-    const float kv_scale = F8 && c.scale != nullptr ? *c.scale : 1.0f;
-    const float scale = a.scale * kLog2e * kv_scale;
+        if (2 * st < C::kSteps) asm volatile("" : "+v"(q[st][0]), "+v"(q[st][1]));
+        else asm volatile("" : "+a"(q[st][0]), "+a"(q[st][1]));
 
     f32x4 acc[C::kDims][2];
-    float m[2] = {-kInf, -kInf}, mu[2] = {0.0f, 0.0f};  // m (-inf: no score yet), the m used
-    float l[2];                                         // sum
+    float m[2], mu[2];  // m (-inf: no score in the first tile), the m used
+    float far[2];       // the product whose score is kSlack above the first ones
+    float l[2];         // sum
 
     // where a lane reads keys: chunks 4 st + g of its position, st = 0, 1 of 128 bytes
-    int k_at[2], v_at[4];
+    int k_at[2], v_own[4], v_other[4];
     {
         const int pos = half * 16 + col, at = (pos >> 3) * C::kGroup + (pos & 7) * 128;
 #pragma unroll
         for (int j = 0; j < 2; ++j) k_at[j] = at + ((4 * j + g) ^ swizzle(pos)) * 16;
     }
     // and values: 4 positions by 16 dims for 16 lanes, tiles 0 .. 3 of 128 bytes, from
-    // the wave's half of the dims on
+    // the wave's half of the dims on; of its own positions and of the other wave's
     {
         const int pos = 4 * g + (col >> 2);
         const int at = (pos >> 3) * C::kGroup + (pos & 7) * 128 + (lane & 1) * 8 +
                        half * (R / 128) * 1024;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            v_at[j] = at + ((2 * j + ((lane >> 1) & 1)) ^ swizzle(pos)) * 16;
-    }
-    constexpr int kAhead = 4;  // LDS reads stay that many steps ahead of their products
-
-    // The tile at t0 has arrived: sends for the next one, and cleans this one where it
-    // holds the step's own rows.
-    auto enter = [&](int t0, int buf, int& page) __attribute__((always_inline)) {
-        if (t0 + C::kTile < end) {
-            issue(t0 + C::kTile, buf == 2 ? 0 : buf + 1, page);
-            page = look_up(t0 + 2 * C::kTile);
+        for (int j = 0; j < 4; ++j) {
+            const int x = at + ((2 * j + ((lane >> 1) & 1)) ^ swizzle(pos)) * 16;
+            v_own[j] = x + half * 2 * C::kGroup;
+            v_other[j] = x + (half ^ 1) * 2 * C::kGroup;
         }
-        if (t0 > begin && ((t0 - begin) & (C::kIds / 2 - 1)) == 0)
-            fetch_ids(t0 + C::kIds / 2, C::kIds / 2);
+    }
+
+    // The tile at t0 has arrived: makes the next one's loads ready (after the end they
+    // bring zeros), and cleans this one where it holds the step's own rows.
+    auto enter = [&](int t0, int buf) __attribute__((always_inline)) {
+        prepare(buf == 2 ? 0 : buf + 1, place);
+        place = look_up(t0 + 2 * C::kTile);
+        if (t0 > begin && ((t0 - begin) & (C::kPlaces / 2 - 1)) == 0)
+            fetch_places(t0 + C::kPlaces / 2, C::kPlaces / 2);
         if (t0 + C::kTile > ctx) {
             // These rows do not all see each other: a vector that is not finite may
             // touch only those that see it.  It is zeroed, and its score is NaN.
-            uint32_t taint = 0;
 #pragma unroll 1
             for (int i = 0; i < 8; ++i) {
+                if (lane == 0) tainted[buf][wave * 8 + i] = 0;
                 if (t0 + wave * 8 + i <= ctx) continue;
                 uint4* at = reinterpret_cast<uint4*>(tiles[buf] + wave * C::kGroup + i * 128 +
                                                      (lane >> 3) * 1024 + (lane & 7) * 16);
@@ -283,51 +301,60 @@ __global__ __launch_bounds__(256, 1) void latent_kernel(LatentAttendArgs a) {
                           bf16_pair_nonfinite(w.z) || bf16_pair_nonfinite(w.w);
                 }
                 if (__ballot(nf) == 0) continue;
-                taint |= 1u << i;
+                if (lane == 0) tainted[buf][wave * 8 + i] = 1;
                 for (int ch = 0; ch < C::kChunks; ch += kWave)
                     if (ch + lane < C::kChunks) at[ch * 8] = make_uint4(0, 0, 0, 0);
             }
-            if (lane == 0) reinterpret_cast<uint8_t*>(&tainted[buf])[wave] = (uint8_t)taint;
             __syncthreads();
         }
     };
-    // The scores of the lane's four positions and two slots, in units of log2.
+    // The products of the lane's four positions and two slots.  Between two matrix
+    // instructions there is time for three others: the keys' reads, kAhead steps before
+    // their products, and the first of the next tile's loads.
     auto score = [&](int t0, int buf, float (&p)[2][4]) __attribute__((always_inline)) {
         const char* tile = tiles[buf];
+        const int any_hole = holes;
         auto key = [&](int st) __attribute__((always_inline)) {
             const uint4 w = *reinterpret_cast<const uint4*>(tile + k_at[st & 1] + (st >> 1) * 1024);
             return as_bf16x8(w.x, w.y, w.z, w.w);
         };
-        f32x4 s[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
+        // two sums a slot: a product waits for the one before it on the same sum
+        constexpr int kAhead = 5;
+        f32x4 s[2][2];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[i >> 1][i & 1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         bf16x8 k8[kAhead];
 #pragma unroll
         for (int st = 0; st < kAhead; ++st) k8[st] = key(st);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int st = 0; st < C::kSteps; ++st) {
-#pragma unroll
-            for (int sh = 0; sh < 2; ++sh)
-                s[sh] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k8[st % kAhead], q[st][sh], s[sh], 0,
-                                                                0, 0);
+            s[0][st & 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k8[st % kAhead], q[st][0],
+                                                                   s[0][st & 1], 0, 0, 0);
+            if (st % 4 == 1 && st / 4 < C::kEarly) issue(st / 4);
+            __builtin_amdgcn_sched_barrier(0);
+            s[1][st & 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k8[st % kAhead], q[st][1],
+                                                                   s[1][st & 1], 0, 0, 0);
             if (st + kAhead < C::kSteps) k8[st % kAhead] = key(st + kAhead);
             __builtin_amdgcn_sched_barrier(0);
         }
-        const bool edge = t0 + C::kTile > ctx;
-        const uint32_t none = __builtin_amdgcn_readfirstlane(absent[buf]);
 #pragma unroll
         for (int sh = 0; sh < 2; ++sh)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) p[sh][e] = s[sh][e] * scale;
-        if (edge || none != 0) {
+            for (int e = 0; e < 4; ++e) p[sh][e] = s[sh][0][e] + s[sh][1][e];
+        const bool edge = t0 + C::kTile > ctx;
+        if (edge || __builtin_amdgcn_readfirstlane(any_hole) != 0) {
             const int first = half * 16 + 4 * g;
-            const uint32_t no = none >> first, nan = edge ? tainted[buf] >> first : 0;
+            const uint32_t no = *reinterpret_cast<const uint32_t*>(&absent[buf][first]);
+            const uint32_t nan =
+                edge ? *reinterpret_cast<const uint32_t*>(&tainted[buf][first]) : 0;
 #pragma unroll
             for (int sh = 0; sh < 2; ++sh) {
                 const int sees = last[sh] - (t0 + first);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    if ((nan >> e) & 1) p[sh][e] = __builtin_nanf("");
-                    if (((no >> e) & 1) || e > sees) p[sh][e] = -kInf;
+                    if ((nan >> (8 * e)) & 1) p[sh][e] = __builtin_nanf("");
+                    if (((no >> (8 * e)) & 1) || e > sees) p[sh][e] = -kInf;
                 }
             }
         }
@@ -352,8 +379,9 @@ __global__ __launch_bounds__(256, 1) void latent_kernel(LatentAttendArgs a) {
     auto refer = [&](const float (&top)[2]) {
 #pragma unroll
         for (int sh = 0; sh < 2; ++sh) {
-            m[sh] = top[sh] + C::kHold;
+            m[sh] = top[sh] * scale + C::kHold;
             mu[sh] = m[sh] == -kInf ? 0.0f : m[sh];
+            far[sh] = top[sh] + C::kSlack / scale;
         }
     };
     // Weights go into the product as two bf16 terms, the upper half of the fp32 weight
@@ -362,8 +390,9 @@ __global__ __launch_bounds__(256, 1) void latent_kernel(LatentAttendArgs a) {
     // of 1 + 2^-23 times it is taken): an infinite value times 0 or a negative rest
     // would make NaN.
     auto weigh = [&](float& x, int sh) __attribute__((always_inline)) {
-        x = fast_exp2(x - mu[sh]);
+        x = fast_exp2(fmaf(x, scale, -mu[sh]));
         l[sh] += x;
+        asm volatile("" : "+v"(x));  // here, not where it is used
     };
     auto split = [&](const float (&p)[4]) __attribute__((always_inline)) {
         constexpr float kOneUp = 1.0f + 0x1p-23f;
@@ -385,19 +414,16 @@ __global__ __launch_bounds__(256, 1) void latent_kernel(LatentAttendArgs a) {
 #pragma unroll
             for (int sh = 0; sh < 2; ++sh) acc[i][sh] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         l[0] = l[1] = 0.0f;
-        if (again) {
-            fetch_ids(begin, C::kIds);
-            __syncthreads();
-            issue(begin, 0, look_up(begin));
-        }
-        int page = look_up(begin + C::kTile);
+        if (again) place = start();
         uint4 own[2];  // weights of the tile before: slots 0 .. 15, 16 .. 31; two terms each
         {
             settle(0);
             __syncthreads();
-            enter(begin, 0, page);
+            enter(begin, 0);
             float p[2][4];
             score(begin, 0, p);
+#pragma unroll
+            for (int i = C::kEarly; i < C::kLoads; ++i) issue(i);
             if (!again) {
                 float mx[2];
 #pragma unroll
@@ -421,99 +447,115 @@ __global__ __launch_bounds__(256, 1) void latent_kernel(LatentAttendArgs a) {
         for (int t0 = begin + C::kTile; more; t0 += C::kTile) {
             settle(buf);
             __syncthreads();
-            // in the tile before: no wave is a tile further before this one has read it
-            rose = !again && __builtin_amdgcn_readfirstlane(risen[odd ^ 1]) != 0;
-            more = t0 < end && !rose;
-            float p[2][4] = {};
+            // of the tile before: no wave is a tile further before this one has read it
+            const int rose_before = risen[odd ^ 1];
+            const uint4 other[2] = {weights[odd ^ 1][wave ^ 1][0][lane],
+                                    weights[odd ^ 1][wave ^ 1][1][lane]};
+            more = t0 < end;
+            float p[2][4];
             if (more) {
-                enter(t0, buf, page);
+                enter(t0, buf);
                 score(t0, buf, p);
-                if (!again) {
-                    bool far = false;
+                bool above = false;
 #pragma unroll
-                    for (int sh = 0; sh < 2; ++sh)
-                        far |= fmaxf(fmaxf(p[sh][0], p[sh][1]), fmaxf(p[sh][2], p[sh][3])) >
-                               m[sh] + (C::kSlack - C::kHold);
-                    if (__ballot(far) != 0 && lane == 0) risen[odd] = 1;
-                }
+                for (int sh = 0; sh < 2; ++sh)
+                    above |= fmaxf(fmaxf(p[sh][0], p[sh][1]), fmaxf(p[sh][2], p[sh][3])) > far[sh];
+                if (__ballot(above) != 0) risen[odd] = 1;
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) p[e >> 2][e & 3] = -kInf;
             }
-            // positions 4 g .. of either wave's 16, in their order
+            rose = !again && __builtin_amdgcn_readfirstlane(rose_before) != 0;
+            more = more && !rose;
+            // positions 4 g .. of the wave's own 16, then of the other's
             const char* tile = tiles[buf == 0 ? 2 : buf - 1];
             bf16x8 pb[2], pr[2];
+            uint4 next[2];
 #pragma unroll
             for (int sh = 0; sh < 2; ++sh) {
-                const uint4 o = weights[odd ^ 1][wave ^ 1][sh][lane];
-                const uint4 x = half == 0 ? own[sh] : o, y = half == 0 ? o : own[sh];
+                const uint4 x = own[sh], y = other[sh];
                 pb[sh] = as_bf16x8(x.x, x.y, y.x, y.y);
                 pr[sh] = as_bf16x8(x.z, x.w, y.z, y.w);
             }
             auto value = [&](int i) __attribute__((always_inline)) {
-                const char* at = tile + v_at[i & 3] + (i >> 2) * 1024;
                 const s16x4 x0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                    (__attribute__((address_space(3))) s16x4*)at);
+                    (__attribute__((address_space(3)))
+                     s16x4*)(tile + v_own[i & 3] + (i >> 2) * 1024));
                 const s16x4 x1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                    (__attribute__((address_space(3))) s16x4*)(at + 2 * C::kGroup));
+                    (__attribute__((address_space(3)))
+                     s16x4*)(tile + v_other[i & 3] + (i >> 2) * 1024));
                 uint2 w0, w1;
                 __builtin_memcpy(&w0, &x0, 8);
                 __builtin_memcpy(&w1, &x1, 8);
                 return as_bf16x8(w0.x, w0.y, w1.x, w1.y);
             };
+            // Two tiles at a time: a product waits for the one before it on the same sum.
+            // Between them the values' reads, kAhead tiles ahead, this turn's weights and
+            // the rest of the next tile's loads (in the last turn weights of 0, and loads to
+            // where nothing is read any more).
+            constexpr int kAhead = 4;
             bf16x8 v8[kAhead];
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) v8[i] = value(i);
             __builtin_amdgcn_sched_barrier(0);
-            const float keep[2] = {l[0], l[1]};
 #pragma unroll
-            for (int i = 0; i < C::kDims; ++i) {
+            for (int i0 = 0; i0 < C::kDims; i0 += 2) {
 #pragma unroll
-                for (int sh = 0; sh < 2; ++sh)
-                    acc[i][sh] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v8[i % kAhead], pb[sh],
-                                                                         acc[i][sh], 0, 0, 0);
+                for (int x = 0; x < 8; ++x) {
+                    const int i = i0 + ((x >> 1) & 1), sh = x & 1;
+                    acc[i][sh] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                        v8[i % kAhead], x < 4 ? pb[sh] : pr[sh], acc[i][sh], 0, 0, 0);
+                    constexpr int kEach = C::kDims >= 16 ? 1 : 2;  // weights at a time
+                    if (x == 0 || x == 2) {
 #pragma unroll
-                for (int sh = 0; sh < 2; ++sh)
-                    acc[i][sh] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v8[i % kAhead], pr[sh],
-                                                                         acc[i][sh], 0, 0, 0);
-                if (i + kAhead < C::kDims) v8[i % kAhead] = value(i + kAhead);
-                // a weight of this turn's tile between the products
-                if (i < 8) weigh(p[i >> 2][i & 3], i >> 2);
-                __builtin_amdgcn_sched_barrier(0);
-            }
-            if (!more) {
-                l[0] = keep[0];
-                l[1] = keep[1];
+                        for (int e = 0; e < kEach; ++e) {
+                            const int n = (i0 + x / 2) * kEach + e;
+                            if (n < 8) weigh(p[n >> 2][n & 3], n >> 2);
+                        }
+                    }
+                    if (x == 3) {
+                        const int n = (i0 / 2 - (C::kDims / 2 - 2)) ;
+                        if (n >= 0) next[n] = split(p[n]);
+                    }
+                    if (x == 4 && C::kEarly + i0 / 2 < C::kLoads) issue(C::kEarly + i0 / 2);
+                    if (x >= 6 && i0 + kAhead + (x - 6) < C::kDims)
+                        v8[(i0 + x - 6) % kAhead] = value(i0 + kAhead + (x - 6));
+                    __builtin_amdgcn_sched_barrier(0);
+                }
             }
 #pragma unroll
             for (int sh = 0; sh < 2; ++sh) {
-                own[sh] = split(p[sh]);
+                own[sh] = next[sh];
                 weights[odd][wave][sh][lane] = own[sh];
             }
             buf = buf == 2 ? 0 : buf + 1;
             odd ^= 1;
         }
+        __builtin_amdgcn_s_waitcnt(0);  // nothing is on its way to LDS
         if (!rose) break;
         __syncthreads();  // every wave has left the tiles
-        fetch_ids(begin, C::kIds);
-        __syncthreads();
-        issue(begin, 0, look_up(begin));
-        page = look_up(begin + C::kTile);
+        place = start();
         float mx[2] = {-kInf, -kInf};
         buf = 0;
         for (int t0 = begin; t0 < end; t0 += C::kTile, buf = buf == 2 ? 0 : buf + 1) {
             settle(buf);
             __syncthreads();
-            enter(t0, buf, page);
+            enter(t0, buf);
             float p[2][4];
             score(t0, buf, p);
+#pragma unroll
+            for (int i = C::kEarly; i < C::kLoads; ++i) issue(i);
 #pragma unroll
             for (int sh = 0; sh < 2; ++sh)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) mx[sh] = fmaxf(mx[sh], p[sh][e]);
         }
+        __builtin_amdgcn_s_waitcnt(0);
         exchange(mx);
         refer(mx);
         __syncthreads();
     }
-    if (__ballot(bad) != 0 && lane == 0) raise_error(a.dev_error, SV_DEV_BAD_PAGE);
+    if (bad && lane == 0) raise_error(a.dev_error, SV_DEV_BAD_PAGE);
 
     // sums over the positions of a slot's lanes, and of the other wave
 #pragma unroll
