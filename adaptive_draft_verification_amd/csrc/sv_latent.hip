@@ -215,41 +215,45 @@ __global__ __launch_bounds__(256, 1) void latent_kernel(LatentAttendArgs a) {
     int64_t place = start();
 
     // ---- queries of the pair's slots, operand B of every step
-    // The scale is taken as positive (queries change their sign with it), so that the
-    // largest product is the largest score and a masked -inf stays one; 0 as 1 of
-    // queries that are 0.
-    const float kv_scale = F8 && c.scale != nullptr ? *c.scale : 1.0f;
-    const float signed_scale = a.scale * kLog2e * kv_scale;
-    const float scale = signed_scale == 0.0f ? 1.0f : fabsf(signed_scale);
-    const uint32_t q_sign = signed_scale < 0.0f ? 0x80008000u : 0u;
-    const uint32_t q_keep = signed_scale == 0.0f ? 0u : ~0u;
     int q_row[2], head[2], last[2];  // last: the position a slot sees last
     bool live[2];
-    bf16x8 q[C::kSteps][2];
+    const uint16_t* q_at[2];
 #pragma unroll
     for (int sh = 0; sh < 2; ++sh) {
         const int i = pair * 32 + sh * 16 + col, slot = mb * C::kSlots + i;
         live[sh] = i < slots;
-        q_row[sh] = slot / a.n_heads;
+        q_row[sh] = (int)((unsigned)slot / (unsigned)a.n_heads);
         head[sh] = slot - q_row[sh] * a.n_heads;
         last[sh] = live[sh] ? ctx + q_row[sh] : -1;
         // a slot that is not there takes the first one's: it sees nothing
-        const uint16_t* qp = static_cast<const uint16_t*>(a.q) +
-                             (int64_t)(live[sh] ? lo + q_row[sh] : lo) * a.q_ld +
-                             (int64_t)(live[sh] ? head[sh] : 0) * C::kDim + g * 8;
-#pragma unroll
-        for (int st = 0; st < C::kSteps; ++st) {
-            const uint4 w = *reinterpret_cast<const uint4*>(qp + st * 32);
-            q[st][sh] = as_bf16x8((w.x ^ q_sign) & q_keep, (w.y ^ q_sign) & q_keep,
-                                  (w.z ^ q_sign) & q_keep, (w.w ^ q_sign) & q_keep);
-        }
+        q_at[sh] = static_cast<const uint16_t*>(a.q) +
+                   (int64_t)(live[sh] ? lo + q_row[sh] : lo) * a.q_ld +
+                   (int64_t)(live[sh] ? head[sh] : 0) * C::kDim + g * 8;
     }
+    bf16x8 q[C::kSteps][2];
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int st = 0; st < C::kSteps; ++st)
+#pragma unroll
+        for (int sh = 0; sh < 2; ++sh) {
+            const uint4 w = *reinterpret_cast<const uint4*>(q_at[sh] + st * 32);
+            q[st][sh] = as_bf16x8(w.x, w.y, w.z, w.w);
+        }
+    __builtin_amdgcn_sched_barrier(0);
     // Waited for here, not among the loads of a tile.  512 registers a lane are 256 for
     // any use and 256 for products alone: half of the queries go among the latter.
 #pragma unroll
     for (int st = 0; st < C::kSteps; ++st)
         if (2 * st < C::kSteps) asm volatile("" : "+v"(q[st][0]), "+v"(q[st][1]));
         else asm volatile("" : "+a"(q[st][0]), "+a"(q[st][1]));
+
+    // The scale is taken as positive (products change their sign with it), so that the
+    // largest product is the largest score and a masked -inf stays one; 0 as 1 of
+    // products that are 0.
+    const float kv_scale = F8 && c.scale != nullptr ? *c.scale : 1.0f;
+    const float signed_scale = a.scale * kLog2e * kv_scale;
+    const float scale = signed_scale == 0.0f ? 1.0f : fabsf(signed_scale);
+    const float sign = signed_scale == 0.0f ? 0.0f : signed_scale < 0.0f ? -1.0f : 1.0f;
 
     f32x4 acc[C::kDims][2];
     float m[2], mu[2];  // m (-inf: no score in the first tile), the m used
@@ -341,7 +345,7 @@ __global__ __launch_bounds__(256, 1) void latent_kernel(LatentAttendArgs a) {
 #pragma unroll
         for (int sh = 0; sh < 2; ++sh)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) p[sh][e] = s[sh][0][e] + s[sh][1][e];
+            for (int e = 0; e < 4; ++e) p[sh][e] = (s[sh][0][e] + s[sh][1][e]) * sign;
         const bool edge = t0 + C::kTile > ctx;
         if (edge || __builtin_amdgcn_readfirstlane(any_hole) != 0) {
             const int first = half * 16 + 4 * g;

@@ -334,3 +334,11 @@ def test_two_calls_at_once_and_graphs():
         eager, eager_lse, _ = b.attend()
         n = int(b.cu[-1])
         assert torch.equal(out[:n], eager[:n]) and torch.equal(lse[:n], eager_lse[:n])
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.07, 1e-3, 0.9])
+def test_attend_scales(scale):
+    """Negative scales order the scores the other way round; 0 makes every weight the same."""
+    b = Batch(16, [2, 3], [70, 33], 5, 512, 16)
+    b.scale = scale
+    b.device().check()
