@@ -46,7 +46,8 @@ EXPORTED = ["sv_status_str", "sv_budget_workspace_bytes", "sv_verify_workspace_b
             "sv_cache_append", "sv_cache_attend", "sv_cache_attend_workspace_bytes",
             "sv_sample", "sv_verify_truncated", "sv_verify_truncated_workspace_bytes",
             "sv_history_clear", "sv_history_add", "sv_adjust_logits",
-            "sv_latent_append", "sv_latent_attend", "sv_latent_attend_workspace_bytes"]
+            "sv_latent_append", "sv_latent_attend", "sv_latent_attend_workspace_bytes",
+            "sv_cache_attend_shared", "sv_cache_attend_shared_workspace_bytes"]
 
 
 class _Cache(ctypes.Structure):
@@ -150,6 +151,9 @@ def _load():
         "sv_verify_truncated": (ctypes.c_int, [vp, i64, i64, vp, i64, ctypes.c_int, i32, vp, vp,
                                                i32, i32, vp, vp, u64, u64, vp, vp, vp, vp, vp, vp,
                                                vp, sz, vp]),
+        "sv_cache_attend_shared_workspace_bytes": (sz, [i32, i32, i32, i32, i32, i32, i32, i32]),
+        "sv_cache_attend_shared": (ctypes.c_int, [vp, vp, i32, vp, i64, i64, i32, vp, vp, i32, i32,
+                                                  vp, vp, i32, f32, vp, i64, vp, vp, vp, sz, vp]),
         "sv_latent_append": (ctypes.c_int, [vp, vp, i32, vp, i64, vp, i64, vp, vp, i32, vp, i32, vp,
                                             vp]),
         "sv_latent_attend_workspace_bytes": (sz, [i32, i32, i32, i32, i32, i32]),
@@ -894,6 +898,37 @@ def sv_cache_attend(cache, page_table, q, cu_rows, ctx_len, k_max, scale, out, w
     _launch(_lib.sv_cache_attend, "sv_cache_attend", device, stream, cache._at, table, max_pages,
             q_at, q_ld, rows, heads, _on(cu_rows, torch.int32, "cu_rows", device, (n + 1,)),
             _on(ctx_len, torch.int32, "ctx_len", device, (n,)), n, int(k_max), float(scale),
+            out_at, out_ld, _on(out_lse, torch.float32, "out_lse", device, (rows, heads)),
+            _on(dev_error, torch.int32, "dev_error", device, None),
+            _on(ws, torch.uint8, "ws", device, None), 0 if ws is None else ws.numel())
+
+
+def sv_cache_attend_shared_workspace_bytes(n_req, n_groups, k_max, n_heads, n_kv_heads, head_dim,
+                                           max_pages, page_size):
+    return int(_lib.sv_cache_attend_shared_workspace_bytes(n_req, n_groups, k_max, n_heads,
+                                                           n_kv_heads, head_dim, max_pages,
+                                                           page_size))
+
+
+def sv_cache_attend_shared(cache, page_table, q, cu_rows, ctx_len, group_start, prefix_len, k_max,
+                           scale, out, ws, out_lse=None, dev_error=None, stream=None):
+    """sv_cache_attend of a batch in groups of neighbours that share a prefix: requests
+    group_start[g] .. group_start[g + 1] - 1 (group_start [groups + 1] i32) have their first
+    prefix_len[g] positions ([groups] i32) in common, which are read once.
+    ws: uint8 device buffer of sv_cache_attend_shared_workspace_bytes(...) bytes."""
+    device = cache._device
+    table, n, max_pages = _table(page_table, device)
+    if q.dim() != 3 or out.shape != q.shape:
+        raise ValueError("q must be [rows, n_heads, head_dim] and out of its shape")
+    rows, heads, _ = q.shape
+    groups = prefix_len.numel()
+    q_at, q_ld = _rows(q, "q", device, heads, cache._head_dim)
+    out_at, out_ld = _rows(out, "out", device, heads, cache._head_dim)
+    _launch(_lib.sv_cache_attend_shared, "sv_cache_attend_shared", device, stream, cache._at, table,
+            max_pages, q_at, q_ld, rows, heads, _on(cu_rows, torch.int32, "cu_rows", device, (n + 1,)),
+            _on(ctx_len, torch.int32, "ctx_len", device, (n,)), n, int(k_max),
+            _on(group_start, torch.int32, "group_start", device, (groups + 1,)),
+            _on(prefix_len, torch.int32, "prefix_len", device, (groups,)), groups, float(scale),
             out_at, out_ld, _on(out_lse, torch.float32, "out_lse", device, (rows, heads)),
             _on(dev_error, torch.int32, "dev_error", device, None),
             _on(ws, torch.uint8, "ws", device, None), 0 if ws is None else ws.numel())

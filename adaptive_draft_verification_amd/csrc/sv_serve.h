@@ -51,6 +51,8 @@ struct AttendArgs {
     int slot_tiles, slot_blocks, parts, part_min;  // AttendPlan's
     float* part_out;                     // parts > 1: [n_req, n_heads, k_max + 1, parts, head_dim]
     float* part_ml;                      //            [..., parts, 2] m and sum
+    const int32_t* first;                // [n_req] the first position of the request's own, where a
+                                         // prefix is shared
 };
 hipError_t launch_cache_attend(const AttendArgs& a, hipStream_t stream);
 

@@ -816,6 +816,54 @@ sv_status sv_cache_attend(const sv_cache* cache, const int32_t* page_table, int3
                           int32_t* dev_error, void* ws, size_t ws_bytes, void* stream);
 
 /*
+ * sv_cache_attend_shared — the packed rows attend to the cache; prefixes that
+ * requests share are read once for all of them.
+ *
+ * agentlens page, section "기술적 구현 및 CUDA Graphs", item Graph Capture: the
+ * decode shape's rows of all requests lie behind each other.  Requests with a
+ * common beginning (a system prompt, a document) are neighbours in the batch:
+ * group g is requests group_start[g] .. group_start[g + 1] - 1, which share
+ * their first prefix_len[g] positions.  The rows of a group attend to the prefix
+ * as one long block of queries, each request's to its own positions as in
+ * sv_cache_attend, and the results are merged: what a row gets is what
+ * sv_cache_attend would give it.
+ *
+ * group_start: [n_groups + 1] int32, ascending from 0 or more to n_req or less.
+ *          Requests before the first and behind the last group share nothing.
+ * prefix_len: [n_groups] int32; any length, 0 too; no longer than the context of
+ *          any of its requests.  The prefix is read through the first request's
+ *          row of page_table; another request's entries of whole pages of it are
+ *          not read.
+ * The other arguments are sv_cache_attend's.
+ * Faults, besides those of sv_cache_attend (whose requests are not written):
+ * group_start that does not ascend within 0 .. n_req (SV_DEV_BAD_CU_ROWS): no
+ * row is written; a group with a request of bad offsets (SV_DEV_BAD_CU_ROWS) or a
+ * prefix that is negative or passes the page table (SV_DEV_BAD_CTX): its
+ * requests are not written; a context shorter than the prefix (SV_DEV_BAD_CTX):
+ * the request is not.
+ * Numerics: as for sv_cache_attend, which sums in another order; repeated calls
+ * agree bit for bit.
+ * ws:      sv_cache_attend_shared_workspace_bytes(...) bytes, 16-byte aligned,
+ *          uninitialised.  Calls that overlap in time must not share it.
+ * Launch: four kernels: one workgroup that lays out the groups; the prefixes, four
+ * waves for each kv head, 128 query slots and part of the length; the requests' own
+ * positions; the join.
+ * Errors: SV_ERR_NULL; SV_ERR_DTYPE; SV_ERR_SHAPE (also n_groups outside 0 ..
+ * n_req); SV_ERR_VALUE (scale not finite); SV_ERR_WORKSPACE.
+ */
+size_t sv_cache_attend_shared_workspace_bytes(int32_t n_req, int32_t n_groups, int32_t k_max,
+                                              int32_t n_heads, int32_t n_kv_heads,
+                                              int32_t head_dim, int32_t max_pages,
+                                              int32_t page_size);
+sv_status sv_cache_attend_shared(const sv_cache* cache, const int32_t* page_table,
+                                 int32_t max_pages, const void* q, int64_t q_ld, int64_t q_rows,
+                                 int32_t n_heads, const int32_t* cu_rows, const int32_t* ctx_len,
+                                 int32_t n_req, int32_t k_max, const int32_t* group_start,
+                                 const int32_t* prefix_len, int32_t n_groups, float scale,
+                                 void* out, int64_t out_ld, float* out_lse, int32_t* dev_error,
+                                 void* ws, size_t ws_bytes, void* stream);
+
+/*
  * The paged cache of shared latent vectors.
  *
  * agentlens page, section "기술적 구현 및 CUDA Graphs", item Graph Capture: the
