@@ -11,16 +11,33 @@
 
 namespace sv {
 
-// A block of a group's query slots, found by the first launch.
-struct SharedBlock {
-    int32_t group;  // -1: none
-    int32_t index;
+// Work on the prefixes is counted in tiles: 32 positions for a block of 128 query slots
+// of one kv head.  Tiles lie in the order of kv heads, groups, the group's blocks and
+// positions, and every workgroup takes an equal run of them, whatever blocks it falls
+// into: one partial result for each, a segment.
+
+// A group as the first launch finds it; one more behind the last has the totals.
+struct SharedGroup {
+    int64_t tile;   // tiles of a kv head before the group
+    int32_t block;  // blocks before the group
+    int32_t broken; // error bits: its requests are left alone
 };
 
-// What the first launch finds out about a request.
+struct SharedTotals {
+    int64_t run;     // tiles a workgroup takes
+    int32_t chunks;  // workgroups with something to do
+    int32_t pad;
+};
+
 struct SharedRequest {
-    int32_t group;   // -1: of no group
-    int32_t record;  // where the records of its first row over the prefix are
+    int32_t group;  // -1: of no group
+    int32_t row;    // its first row among the group's
+};
+
+// The workgroups that share a block: the block's segment of workgroup c is number
+// (block of all heads) + c.
+struct SharedSpan {
+    int32_t first, last;
 };
 
 struct SharedArgs {
@@ -28,53 +45,48 @@ struct SharedArgs {
     const int32_t* group_start;
     const int32_t* prefix_len;
     int n_groups;
-    int prefix_blocks, prefix_parts, prefix_min;  // SharedPlan's
+    int chunks;              // SharedPlan's
     int32_t* first;          // [n_req] the first position of the request's own, -1: left alone
     SharedRequest* request;  // [n_req]
-    int32_t* broken;         // [n_groups] error bits
-    SharedBlock* block;      // [prefix_blocks]
-    float* prefix_out;       // [n_req, k_max + 1, n_heads, prefix_parts, head_dim]
-    float* prefix_ml;        // [..., prefix_parts, 2] m and sum
+    SharedGroup* group;      // [n_groups + 1]
+    SharedTotals* totals;
+    SharedSpan* span;        // [kv heads, blocks]
+    float* prefix_out;       // [segments, 128, head_dim]
+    float* prefix_ml;        // [segments, 128, 2] m and sum
 };
 hipError_t launch_cache_attend_shared(const SharedArgs& a, hipStream_t stream);
 
 // How the prefixes' launch is cut into workgroups: by host-known sizes alone.
 struct SharedPlan {
-    static constexpr int kSlots = 128;  // of a workgroup
-    int prefix_blocks;  // blocks of query slots over all groups, at most
-    int prefix_parts;   // workgroups over a prefix's positions, at most
-    int prefix_min;     // positions a part has at least
+    static constexpr int kSlots = 128, kTile = 32;
+    // A run is four tiles at least (a segment's start costs about as much), and long
+    // enough that a block has 64 segments at most.
+    static constexpr int kRunMin = 4, kSegments = 64;
+    int64_t blocks;  // blocks of query slots over all groups and kv heads, at most
+    int chunks;      // workgroups
     AttendPlan own;
     SharedPlan(int n_req, int n_groups, int k_max, int n_heads, int n_kv_heads, int head_dim,
                int esize, int64_t capacity)
         : own(n_req, k_max, n_heads, n_kv_heads, head_dim, esize, capacity) {
         if (own.parts > 64) own.parts = 64;  // the join takes 128 of both kinds
         const int64_t slots = (int64_t)n_req * (k_max + 1) * (n_heads / n_kv_heads);
-        prefix_blocks = (int)(slots / kSlots + n_groups);
-        // Parts until there are some 1024 workgroups.  A part writes, and the join reads,
-        // four bytes a slot and dim: 256 positions are eight tiles, a tenth of whose
-        // products' time that takes.
-        prefix_min = 256;
-        const int64_t groups = (int64_t)prefix_blocks * n_kv_heads;
-        const int64_t want = groups > 0 ? (1024 + groups - 1) / groups : 1;
-        const int64_t most = (capacity + prefix_min - 1) / prefix_min;
-        const int64_t p = want < most ? want : most;
-        prefix_parts = (int)(p < 1 ? 1 : p > 64 ? 64 : p);
+        blocks = n_groups == 0 ? 0 : (slots / kSlots + n_groups) * n_kv_heads;
+        // as many as are on the chip at once, or as there are runs
+        chunks = head_dim < 256 ? 512 : 256;
+        const double runs = (double)blocks * ((capacity + kTile - 1) / kTile) / kRunMin + 8;
+        if (runs < chunks) chunks = (int)runs & ~7;
     }
-    int64_t prefix_grid(int n_kv_heads) const {
-        return (int64_t)prefix_blocks * n_kv_heads * prefix_parts;
-    }
-    // The workspace: records of both launches, then what the first launch finds.
-    static size_t records(int n_req, int k_max, int n_heads) {
-        return (size_t)n_req * (k_max + 1) * n_heads;
-    }
-    size_t float_count(int n_req, int k_max, int n_heads, int head_dim) const {
-        return records(n_req, k_max, n_heads) * (size_t)(prefix_parts + own.parts) * (head_dim + 2);
+    int64_t segments() const { return blocks + chunks; }
+    // The workspace: partial results of both launches, then what the first launch finds.
+    size_t own_records(int n_req, int k_max, int n_heads) const {
+        return (size_t)n_req * (k_max + 1) * n_heads * own.parts;
     }
     size_t bytes(int n_req, int n_groups, int k_max, int n_heads, int head_dim) const {
-        return float_count(n_req, k_max, n_heads, head_dim) * sizeof(float) +
-               (size_t)n_req * (sizeof(int32_t) + sizeof(SharedRequest)) +
-               (size_t)n_groups * sizeof(int32_t) + (size_t)prefix_blocks * sizeof(SharedBlock);
+        return ((size_t)segments() * kSlots + own_records(n_req, k_max, n_heads)) *
+                   (head_dim + 2) * sizeof(float) +
+               (size_t)blocks * sizeof(SharedSpan) + sizeof(SharedTotals) +
+               (size_t)(n_groups + 1) * sizeof(SharedGroup) +
+               (size_t)n_req * (sizeof(SharedRequest) + sizeof(int32_t));
     }
 };
 

@@ -16,13 +16,24 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kLayoutThreads = 1024;
 
-// Checks the groups and their requests, and lists the prefixes' blocks of query slots:
-// one workgroup, so that the launches behind it only read.
+__device__ __forceinline__ int64_t wave_incl_sum64(int64_t v, int lane) {
+#pragma unroll
+    for (int off = 1; off < kWave; off <<= 1) {
+        const int64_t x = __shfl_up((long long)v, off);
+        if (lane >= off) v += x;
+    }
+    return v;
+}
+
+// Checks the groups and their requests, and counts the tiles: one workgroup, so that
+// the launches behind it only read.
 __global__ __launch_bounds__(kLayoutThreads) void layout_kernel(SharedArgs s) {
     const AttendArgs& a = s.own;
-    __shared__ int sums[kLayoutThreads / kWave];
+    __shared__ int block_sums[kLayoutThreads / kWave], longest_prefix;
+    __shared__ int64_t tile_sums[kLayoutThreads / kWave];
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
     int err = 0;
+    if (t == 0) longest_prefix = 0;
     for (int g = t; g <= s.n_groups && s.n_groups > 0; g += kLayoutThreads) {
         const int at = s.group_start[g];
         if (at < 0 || at > a.n_req || (g > 0 && s.group_start[g - 1] > at))
@@ -32,10 +43,9 @@ __global__ __launch_bounds__(kLayoutThreads) void layout_kernel(SharedArgs s) {
     for (int g = t; g < s.n_groups; g += kLayoutThreads) {
         const int P = s.prefix_len[g];
         const bool fits = P >= 0 && P <= (int64_t)a.max_pages * a.cache.page_size;
-        __hip_atomic_store(s.broken + g, none || fits ? 0 : SV_DEV_BAD_CTX, __ATOMIC_RELAXED,
-                           __HIP_MEMORY_SCOPE_AGENT);
+        __hip_atomic_store(&s.group[g].broken, none || fits ? 0 : SV_DEV_BAD_CTX,
+                           __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
-    for (int b = t; b < s.prefix_blocks; b += kLayoutThreads) s.block[b].group = -1;
     __syncthreads();
     // every request's group, and whether its rows are where they have to be
     for (int r = t; r < a.n_req; r += kLayoutThreads) {
@@ -50,48 +60,76 @@ __global__ __launch_bounds__(kLayoutThreads) void layout_kernel(SharedArgs s) {
             group = lo;
             const int from = a.cu_rows[r], to = a.cu_rows[r + 1];
             if (from < 0 || to < from || to - from > a.k_max + 1 || to > a.q_rows)
-                atomicOr(s.broken + group, SV_DEV_BAD_CU_ROWS);
+                atomicOr(&s.group[group].broken, SV_DEV_BAD_CU_ROWS);
         }
         s.request[r].group = group;
     }
     __syncthreads();
-    int before = 0;  // blocks of earlier groups
+    int blocks = 0;  // of earlier groups
+    int64_t tiles = 0;
     for (int g0 = 0; g0 < s.n_groups; g0 += kLayoutThreads) {
         const int g = g0 + t;
-        int n = 0;
+        int n = 0, each = 0;
         if (g < s.n_groups && !none) {
-            const int bits =
-                __hip_atomic_load(s.broken + g, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            const int bits = __hip_atomic_load(&s.group[g].broken, __ATOMIC_RELAXED,
+                                               __HIP_MEMORY_SCOPE_AGENT);
             err |= bits;
             const int from = s.group_start[g], to = s.group_start[g + 1];
-            if (bits == 0 && s.prefix_len[g] > 0 && to > from)
+            const int P = s.prefix_len[g];
+            if (bits == 0 && P > 0 && to > from)
                 n = ((a.cu_rows[to] - a.cu_rows[from]) * a.group + SharedPlan::kSlots - 1) /
                     SharedPlan::kSlots;
+            if (n > 0) {
+                each = (int)(((int64_t)P + SharedPlan::kTile - 1) / SharedPlan::kTile);
+                atomicMax(&longest_prefix, each);
+            }
         }
-        const int upto = wave_incl_sum_dpp(n, lane);
-        if (lane == 63) sums[wave] = upto;
+        const int blocks_to = wave_incl_sum_dpp(n, lane);
+        const int64_t tiles_to = wave_incl_sum64((int64_t)n * each, lane);
+        if (lane == 63) {
+            block_sums[wave] = blocks_to;
+            tile_sums[wave] = tiles_to;
+        }
         __syncthreads();
-        int at = before + upto - n, all = 0;
+        int block = blocks + blocks_to - n;
+        int64_t tile = tiles + tiles_to - (int64_t)n * each;
         for (int w = 0; w < kLayoutThreads / kWave; ++w) {
-            if (w < wave) at += sums[w];
-            all += sums[w];
+            if (w < wave) {
+                block += block_sums[w];
+                tile += tile_sums[w];
+            }
+            blocks += block_sums[w];
+            tiles += tile_sums[w];
         }
-        for (int i = 0; i < n && at + i < s.prefix_blocks; ++i) s.block[at + i] = SharedBlock{g, i};
-        before += all;
+        if (g < s.n_groups) {
+            s.group[g].tile = tile;
+            s.group[g].block = block;
+        }
         __syncthreads();
+    }
+    if (t == 0) {
+        s.group[s.n_groups].tile = tiles;
+        s.group[s.n_groups].block = blocks;
+        // equal runs; a block of n tiles lies in n / run + 2 of them at most
+        const int64_t all = tiles * a.cache.n_kv_heads;
+        const int64_t few = (longest_prefix + SharedPlan::kSegments - 3) / (SharedPlan::kSegments - 2);
+        int64_t run = s.chunks > 0 ? (all + s.chunks - 1) / s.chunks : 0;
+        run = run < few ? few : run;
+        run = run < SharedPlan::kRunMin ? SharedPlan::kRunMin : run;
+        s.totals->run = run;
+        s.totals->chunks = (int)((all + run - 1) / run);
     }
     for (int r = t; r < a.n_req; r += kLayoutThreads) {
         const int g = s.request[r].group;
-        int first = none ? -1 : 0, record = 0;
+        int first = none ? -1 : 0, row = 0;
         if (g >= 0) {
-            const int bits =
-                __hip_atomic_load(s.broken + g, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            const int from = s.group_start[g];
+            const int bits = __hip_atomic_load(&s.group[g].broken, __ATOMIC_RELAXED,
+                                               __HIP_MEMORY_SCOPE_AGENT);
             first = bits != 0 ? -1 : s.prefix_len[g];
-            record = from * (a.k_max + 1) + (a.cu_rows[r] - a.cu_rows[from]);
+            row = a.cu_rows[r] - a.cu_rows[s.group_start[g]];
         }
         s.first[r] = first;
-        s.request[r].record = record;
+        s.request[r].row = row;
     }
     if (err != 0) raise_error(a.dev_error, err);
 }
@@ -154,20 +192,55 @@ __global__ __launch_bounds__(256, (Prefix<D, F8>::kOccupancy)) void prefix_kerne
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int col = lane & 15, g = lane >> 4;
-    // grid: kv heads fastest (an XCD each), then slot blocks and parts
-    int id = blockIdx.x;
-    const int h = id % c.n_kv_heads;
-    id /= c.n_kv_heads;
-    const SharedBlock block = s.block[id % s.prefix_blocks];
-    const int part = id / s.prefix_blocks;
-    if (block.group < 0) return;
-    const int from_req = s.group_start[block.group], to_req = s.group_start[block.group + 1];
-    const int P = s.prefix_len[block.group];
+    // consecutive runs of tiles (they read the same keys and values) to one XCD: every
+    // eighth workgroup
+    const SharedTotals totals = *s.totals;
+    const int each = (totals.chunks + 7) / 8;
+    const int chunk = (blockIdx.x % 8) * each + blockIdx.x / 8;
+    if ((int)blockIdx.x / 8 >= each || chunk >= totals.chunks) return;
+    const int64_t head_tiles = s.group[s.n_groups].tile;
+    const int head_blocks = s.group[s.n_groups].block;
+    int64_t tile = chunk * totals.run;
+    const int64_t to_tile = min(tile + totals.run, head_tiles * c.n_kv_heads);
+    int h = (int)(tile / head_tiles);
+    int64_t in_head = tile - h * head_tiles;
+    // the group the run starts in: the last one whose tiles begin there or before
+    int group = 0;
+    for (int n = s.n_groups; n > 1;) {
+        const int step = (n + kWave - 1) / kWave, at = group + lane * step;
+        const bool before = lane * step < n && s.group[at].tile <= in_head;
+        const int skip = (__popcll(__ballot(before)) - 1) * step;  // lane 0's is
+        group += skip;
+        n = min(step, n - skip);
+    }
+    bool bad = false;
+    if (threadIdx.x == 0) holes = 0;
+    // ---- the run's segments
+    while (tile < to_tile) {
+    if (in_head == head_tiles) {
+        in_head = 0;
+        group = 0;
+        ++h;
+    }
+    while (s.group[group + 1].tile <= in_head) ++group;
+    const int from_req = s.group_start[group], to_req = s.group_start[group + 1];
+    const int P = s.prefix_len[group];
     const int lo = a.cu_rows[from_req];
-    const int slots = (a.cu_rows[to_req] - lo) * a.group - block.index * SharedPlan::kSlots;
-    const int plen = part_len(P, s.prefix_parts, s.prefix_min);
-    const int begin = part * plen, end = min(P, begin + plen);
-    if (begin >= P || slots <= 0) return;
+    const int block_tiles = (int)(((int64_t)P + C::kTile - 1) / C::kTile);
+    const int64_t in_group = in_head - s.group[group].tile;
+    const int index = (int)((uint64_t)in_group / (uint32_t)block_tiles);  // the block's
+    const int first_tile = (int)(in_group - (int64_t)index * block_tiles);
+    const int n_tiles = (int)min((int64_t)(block_tiles - first_tile), to_tile - tile);
+    const int64_t block_id = (int64_t)h * head_blocks + s.group[group].block + index;
+    const int slots = (a.cu_rows[to_req] - lo) * a.group - index * SharedPlan::kSlots;
+    const int begin = first_tile * C::kTile;
+    const int end = min(P, begin + n_tiles * C::kTile);
+    if (threadIdx.x == 0) {
+        if (first_tile == 0) s.span[block_id].first = chunk;
+        if (first_tile + n_tiles == block_tiles) s.span[block_id].last = chunk;
+    }
+    tile += n_tiles;
+    in_head += n_tiles;
 
     // ---- keys' and values' way into LDS: wave w brings positions 8 w .. of a tile
     const int32_t* table = a.page_table + (int64_t)from_req * a.max_pages;
@@ -178,7 +251,6 @@ __global__ __launch_bounds__(256, (Prefix<D, F8>::kOccupancy)) void prefix_kerne
     // The places of `n` positions from `from` on, into LDS: kPlaces at first, then half
     // as many at a time (a wait for a page id in registers would be a wait for the tiles
     // that are on their way).  -1: after the end, or on a page that is not there.
-    bool bad = false;
     auto fetch_places = [&](int from, int n) __attribute__((always_inline)) {
         for (int i = threadIdx.x; i < n && from + i < end + 4 * C::kTile; i += 256) {
             const int t = from + i;
@@ -240,8 +312,7 @@ __global__ __launch_bounds__(256, (Prefix<D, F8>::kOccupancy)) void prefix_kerne
         }
     };
 
-    if (threadIdx.x == 0) holes = 0;
-    __syncthreads();
+    __syncthreads();  // the segment before has been read
     fetch_places(begin, C::kPlaces);
     __syncthreads();
     issue(0, look_up(begin));
@@ -254,12 +325,12 @@ __global__ __launch_bounds__(256, (Prefix<D, F8>::kOccupancy)) void prefix_kerne
     bf16x8 q[C::kSteps][2];
 #pragma unroll
     for (int sh = 0; sh < 2; ++sh) {
-        const int i = wave * 32 + sh * 16 + col, slot = block.index * SharedPlan::kSlots + i;
+        const int i = wave * 32 + sh * 16 + col, slot = index * SharedPlan::kSlots + i;
         live[sh] = i < slots;
         row[sh] = (int)((unsigned)slot / (unsigned)a.group);
         head[sh] = h * a.group + slot - row[sh] * a.group;
         // a slot that is not there takes the block's first one's
-        const int first = block.index * SharedPlan::kSlots;
+        const int first = index * SharedPlan::kSlots;
         const int q_row = live[sh] ? row[sh] : first / a.group;
         const int q_head = live[sh] ? head[sh] : h * a.group + first % a.group;
         const uint16_t* qp = static_cast<const uint16_t*>(a.q) + (int64_t)(lo + q_row) * a.q_ld +
@@ -349,7 +420,13 @@ __global__ __launch_bounds__(256, (Prefix<D, F8>::kOccupancy)) void prefix_kerne
 #pragma unroll
         for (int sh = 0; sh < 2; ++sh)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) p[sh][e] = sc[e >> 2][sh][e & 3] * sign;
+            for (int e = 0; e < 8; ++e) p[sh][e] = sc[e >> 2][sh][e & 3];
+        if (sign != 1.0f) {
+#pragma unroll
+            for (int sh = 0; sh < 2; ++sh)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) p[sh][e] *= sign;
+        }
         if (t0 + C::kTile > end || __builtin_amdgcn_readfirstlane(holes) != 0) {
 #pragma unroll
             for (int ph = 0; ph < 2; ++ph) {
@@ -440,8 +517,7 @@ __global__ __launch_bounds__(256, (Prefix<D, F8>::kOccupancy)) void prefix_kerne
         }
         buf = buf == 2 ? 0 : buf + 1;
     }
-    __builtin_amdgcn_s_waitcnt(0);  // nothing is on its way to LDS when the wave ends
-    if (__ballot(bad) != 0 && lane == 0) raise_error(a.dev_error, SV_DEV_BAD_PAGE);
+    __builtin_amdgcn_s_waitcnt(0);  // nothing is on its way to LDS when it is used anew
 
 #pragma unroll
     for (int sh = 0; sh < 2; ++sh) {
@@ -449,8 +525,7 @@ __global__ __launch_bounds__(256, (Prefix<D, F8>::kOccupancy)) void prefix_kerne
         l[sh] += __shfl_xor(l[sh], 32);
         if (!live[sh]) continue;
         const int64_t rec =
-            (((int64_t)from_req * (a.k_max + 1) + row[sh]) * a.n_heads + head[sh]) *
-                s.prefix_parts + part;
+            (block_id + chunk) * SharedPlan::kSlots + wave * 32 + sh * 16 + col;
         float* o = s.prefix_out + rec * D + 4 * g;
 #pragma unroll
         for (int i = 0; i < C::kDims; ++i) *reinterpret_cast<f32x4*>(o + i * 16) = acc[i][sh];
@@ -459,6 +534,8 @@ __global__ __launch_bounds__(256, (Prefix<D, F8>::kOccupancy)) void prefix_kerne
             s.prefix_ml[rec * 2 + 1] = l[sh];
         }
     }
+    }
+    if (__ballot(bad) != 0 && lane == 0) raise_error(a.dev_error, SV_DEV_BAD_PAGE);
 }
 
 // --------------------------------------------------------------------- join
@@ -484,14 +561,19 @@ __global__ __launch_bounds__(256) void shared_join_kernel(SharedArgs s) {
         return;
     // the parts as the two launches made them
     int n1 = 0;
+    int64_t rec1 = 0;  // parts are kSlots records apart
     if (first > 0) {
-        const int plen = part_len(first, s.prefix_parts, s.prefix_min);
-        n1 = (first + plen - 1) / plen;
+        const SharedRequest at = s.request[r];
+        const int h = head / a.group;
+        const int slot = (at.row + row) * a.group + head - h * a.group;
+        const int64_t block_id = (int64_t)h * s.group[s.n_groups].block +
+                                 s.group[at.group].block + slot / SharedPlan::kSlots;
+        const SharedSpan span = s.span[block_id];
+        n1 = span.last - span.first + 1;
+        rec1 = (block_id + span.first) * SharedPlan::kSlots + slot % SharedPlan::kSlots;
     }
     const int len = ctx + rows - (first & ~15), plen = part_len(len, a.parts, a.part_min);
     const int n = n1 + (len + plen - 1) / plen;  // at most 128
-    const int64_t rec1 =
-        ((int64_t)(s.request[r].record + row) * a.n_heads + head) * s.prefix_parts;
     // attend_kernel's records: request, head, row
     const int64_t rec2 = (((int64_t)r * a.n_heads + head) * (a.k_max + 1) + row) * a.parts;
     // the largest maximum and the parts' factors, two a lane
@@ -500,7 +582,7 @@ __global__ __launch_bounds__(256) void shared_join_kernel(SharedArgs s) {
     for (int i = 0; i < 2; ++i) {
         const int p = lane + 64 * i;
         if (p >= n) continue;
-        const float* ml = p < n1 ? s.prefix_ml + (rec1 + p) * 2 : a.part_ml + (rec2 + p - n1) * 2;
+        const float* ml = p < n1 ? s.prefix_ml + (rec1 + p * SharedPlan::kSlots) * 2 : a.part_ml + (rec2 + p - n1) * 2;
         mm[i] = ml[0];
         ll[i] = ml[1];
     }
@@ -525,7 +607,8 @@ __global__ __launch_bounds__(256) void shared_join_kernel(SharedArgs s) {
         for (int i = 0; i < 4; ++i) {
             const int p = min(p0 + i, n - 1);
             const float* from =
-                (p < n1 ? s.prefix_out + (rec1 + p) * D : a.part_out + (rec2 + p - n1) * D) + lane * E;
+                (p < n1 ? s.prefix_out + (rec1 + p * SharedPlan::kSlots) * D
+                       : a.part_out + (rec2 + p - n1) * D) + lane * E;
 #pragma unroll
             for (int e = 0; e < E; ++e) x[i][e] = from[e];
         }
@@ -566,10 +649,8 @@ hipError_t run_shared(const SharedArgs& s, hipStream_t stream) {
     layout_kernel<<<1, kLayoutThreads, 0, stream>>>(s);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    if (s.n_groups > 0) {
-        const unsigned grid =
-            (unsigned)((int64_t)s.prefix_blocks * a.cache.n_kv_heads * s.prefix_parts);
-        prefix_kernel<D, F8><<<grid, 256, 0, stream>>>(s);
+    if (s.chunks > 0) {
+        prefix_kernel<D, F8><<<(unsigned)s.chunks, 256, 0, stream>>>(s);
         e = hipGetLastError();
         if (e != hipSuccess) return e;
     }

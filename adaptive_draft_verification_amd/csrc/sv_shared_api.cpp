@@ -20,10 +20,7 @@ sv_status check_sizes(int32_t n_req, int32_t n_groups, int32_t k_max, int32_t n_
     const sv_status s =
         sv::check_attend_sizes(n_req, k_max, n_heads, n_kv_heads, head_dim, capacity);
     if (s != SV_OK) return s;
-    if (n_groups < 0 || n_groups > n_req) return SV_ERR_SHAPE;
-    // the prefixes' grid too stays below 2^32 work-items
-    const sv::SharedPlan p(n_req, n_groups, k_max, n_heads, n_kv_heads, head_dim, 2, capacity);
-    return p.prefix_grid(n_kv_heads) > SV_MAX_ATTEND_SLOTS ? SV_ERR_SHAPE : SV_OK;
+    return n_groups < 0 || n_groups > n_req ? SV_ERR_SHAPE : SV_OK;
 }
 
 }  // namespace
@@ -73,16 +70,18 @@ sv_status sv_cache_attend_shared(const sv_cache* cache, const int32_t* page_tabl
                            cache->dtype == SV_E4M3 ? 1 : 2, capacity);
     const size_t need = p.bytes(n_req, n_groups, k_max, n_heads, cache->head_dim);
     if (ws == nullptr || ws_bytes < need || !sv::aligned16(ws)) return SV_ERR_WORKSPACE;
-    // whole rows of values first: they are stored 16 bytes at a time
-    const size_t records = sv::SharedPlan::records(n_req, k_max, n_heads);
+    // what is stored 16 bytes at a time first, then what has 8-byte members
+    const size_t segment = (size_t)p.segments() * sv::SharedPlan::kSlots;
+    const size_t own = p.own_records(n_req, k_max, n_heads);
     float* prefix_out = static_cast<float*>(ws);
-    float* own_out = prefix_out + records * p.prefix_parts * cache->head_dim;
-    float* prefix_ml = own_out + records * p.own.parts * cache->head_dim;
-    float* own_ml = prefix_ml + records * p.prefix_parts * 2;
-    int32_t* first = reinterpret_cast<int32_t*>(own_ml + records * p.own.parts * 2);
-    sv::SharedRequest* request = reinterpret_cast<sv::SharedRequest*>(first + n_req);
-    sv::SharedBlock* block = reinterpret_cast<sv::SharedBlock*>(request + n_req);
-    int32_t* broken = reinterpret_cast<int32_t*>(block + p.prefix_blocks);
+    float* own_out = prefix_out + segment * cache->head_dim;
+    float* prefix_ml = own_out + own * cache->head_dim;
+    float* own_ml = prefix_ml + segment * 2;
+    sv::SharedGroup* group = reinterpret_cast<sv::SharedGroup*>(own_ml + own * 2);
+    sv::SharedTotals* totals = reinterpret_cast<sv::SharedTotals*>(group + n_groups + 1);
+    sv::SharedSpan* span = reinterpret_cast<sv::SharedSpan*>(totals + 1);
+    sv::SharedRequest* request = reinterpret_cast<sv::SharedRequest*>(span + p.blocks);
+    int32_t* first = reinterpret_cast<int32_t*>(request + n_req);
     const sv::SharedArgs a{
         {*cache, page_table, max_pages, q, q_ld, q_rows, n_heads, n_heads / cache->n_kv_heads,
          cu_rows, ctx_len, n_req, k_max, scale, out, out_ld, out_lse, dev_error,
@@ -90,8 +89,8 @@ sv_status sv_cache_attend_shared(const sv_cache* cache, const int32_t* page_tabl
          n_req > 1 && n_req <= 256 && p.own.grid(n_req, cache->n_kv_heads) > 1024,
          sv::log2_exact(cache->page_size), p.own.slot_tiles, p.own.slot_blocks, p.own.parts,
          p.own.part_min, own_out, own_ml, first},
-        group_start, prefix_len, n_groups, p.prefix_blocks, p.prefix_parts, p.prefix_min, first,
-        request, broken, block, prefix_out, prefix_ml};
+        group_start, prefix_len, n_groups, p.chunks, first, request, group, totals, span,
+        prefix_out, prefix_ml};
     const hipError_t e = sv::launch_cache_attend_shared(a, as_stream(stream));
     return sv::finish_launch(e, as_stream(stream));
 }
