@@ -2,6 +2,8 @@
 // sv_cache_attend_shared.  Four launches: the groups laid out; every group's rows over
 // its prefix, as one long block of queries; every request's rows over its own
 // positions (sv_cache_attend's kernel, from the prefix's end on); the join.
+#include <type_traits>
+
 #include "sv_attend_kernel.h"
 #include "sv_device.h"
 #include "sv_launch.h"
@@ -182,10 +184,10 @@ struct Prefix {
 template <int D, bool F8>
 __global__ __launch_bounds__(256, (Prefix<D, F8>::kOccupancy)) void prefix_kernel(SharedArgs s) {
     using C = Prefix<D, F8>;
-    __shared__ __attribute__((aligned(16))) char tiles[3][C::kTileBytes];
+    __shared__ __attribute__((aligned(16))) char tiles[4][C::kTileBytes];
     __shared__ int64_t places[C::kPlaces];  // bytes to position begin + i at i % kPlaces
     // a byte a position of the tile: it is none
-    __shared__ __attribute__((aligned(4))) uint8_t absent[3][C::kTile];
+    __shared__ __attribute__((aligned(4))) uint8_t absent[4][C::kTile];
     __shared__ int holes;  // a position before the end is none
     const AttendArgs& a = s.own;
     const sv_cache& c = a.cache;
@@ -380,22 +382,41 @@ __global__ __launch_bounds__(256, (Prefix<D, F8>::kOccupancy)) void prefix_kerne
                       ((2 * j + ((lane >> 1) & 1)) ^ swizzle(pos)) * 16;
     }
 
-    int buf = 0;
-    for (int t0 = begin; t0 < end; t0 += C::kTile) {
+    // The weights that are not yet multiplied with their values, as two bf16 terms (see
+    // attend_kernel): word i of slot sh is positions 4 g + 2 (i % 2) .. of 16 (i / 2).
+    uint32_t hi_w[2][4] = {}, rest_w[2][4] = {};
+    auto value = [&](const char* tile, int i) __attribute__((always_inline)) {
+        const char* at = tile + v_at[i & 3] + (i >> 2) * 1024;
+        const s16x4 x0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (__attribute__((address_space(3))) s16x4*)at);
+        const s16x4 x1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (__attribute__((address_space(3))) s16x4*)(at + 2 * C::kGroup));
+        uint2 w0, w1;
+        __builtin_memcpy(&w0, &x0, 8);
+        __builtin_memcpy(&w1, &x1, 8);
+        return as_bf16x8(w0.x, w0.y, w1.x, w1.y);
+    };
+    constexpr int kValuesAhead = 4;
+    // One turn: the scores of tile t, then its weights between the products of tile
+    // t - 1's with their values (BEHIND: there is one).
+    auto turn = [&](auto behind, int t0) __attribute__((always_inline)) {
+        constexpr bool kBehind = decltype(behind)::value;
+        const int buf = ((t0 - begin) / C::kTile) & 3;
         settle(buf);
         __syncthreads();
-        issue(F8 ? (buf == 2 ? 0 : buf + 1) : (buf == 0 ? 2 : buf - 1), place);
+        issue((buf + (F8 ? 1 : 2)) & 3, place);
         place = look_up(t0 + (F8 ? 2 : 3) * C::kTile);
-        if (t0 > begin && ((t0 - begin) & (C::kPlaces / 2 - 1)) == 0)
+        if (kBehind && ((t0 - begin) & (C::kPlaces / 2 - 1)) == 0)
             fetch_places(t0 + C::kPlaces / 2, C::kPlaces / 2);
         const char* tile = tiles[buf];
+        const char* tile_behind = tiles[(buf + 3) & 3];
 
         // scores: both 16 positions of a step, two slots' products each
         f32x4 sc[2][2];
 #pragma unroll
         for (int i = 0; i < 4; ++i) sc[i >> 1][i & 1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         constexpr int kAhead = C::kSteps < 3 ? C::kSteps : 3;
-        bf16x8 k8[kAhead][2];
+        bf16x8 k8[kAhead][2], v8[kValuesAhead];
         auto key = [&](int st, int ph) __attribute__((always_inline)) {
             const uint4 w = *reinterpret_cast<const uint4*>(tile + k_at[st & 1] + (st >> 1) * 1024 +
                                                             ph * 2 * C::kGroup);
@@ -416,6 +437,9 @@ __global__ __launch_bounds__(256, (Prefix<D, F8>::kOccupancy)) void prefix_kerne
                 if (st + kAhead < C::kSteps) k8[st % kAhead][ph] = key(st + kAhead, ph);
             __builtin_amdgcn_sched_barrier(0);
         }
+        if (kBehind)
+#pragma unroll
+            for (int i = 0; i < kValuesAhead; ++i) v8[i] = value(tile_behind, i);
         float p[2][8];  // of a slot: positions 4 g .. of the first 16, of the second
 #pragma unroll
         for (int sh = 0; sh < 2; ++sh)
@@ -454,68 +478,116 @@ __global__ __launch_bounds__(256, (Prefix<D, F8>::kOccupancy)) void prefix_kerne
             for (int sh = 0; sh < 2; ++sh) {
                 float top = fmaxf(mx[sh], __shfl_xor(mx[sh], 16));
                 top = fmaxf(top, __shfl_xor(top, 32));
-                float to = fmaxf(m[sh], top * scale + C::kHold);
+                float to = fmaxf(m[sh], ceilf(top * scale) + C::kHold);
                 if (!F8) {
                     float most = fmaxf(l[sh], __shfl_xor(l[sh], 16));
                     most = fmaxf(most, __shfl_xor(most, 32));
                     if (most > C::kFull) to += C::kRaise;
                 }
                 if (to > m[sh]) {
-                    const float f = fast_exp2(m[sh] - to);  // m = -inf: 0
+                    // m = -inf: 0; else a power of two, as m is an integer
+                    const float f = fast_exp2(m[sh] - to);
+                    if (kBehind) {
 #pragma unroll
-                    for (int i = 0; i < C::kDims; ++i) acc[i][sh] *= f;
+                        for (int i = 0; i < C::kDims; ++i) acc[i][sh] *= f;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            hi_w[sh][i] = pack_bf16(bf16_lo(hi_w[sh][i]) * f,
+                                                    bf16_hi(hi_w[sh][i]) * f);
+                            rest_w[sh][i] = pack_bf16(bf16_lo(rest_w[sh][i]) * f,
+                                                      bf16_hi(rest_w[sh][i]) * f);
+                        }
+                    }
                     l[sh] *= f;
                     m[sh] = mu[sh] = to;
                     far[sh] = (to - C::kHold + C::kSlack) / scale;
                 }
             }
         }
-        // weights as two bf16 terms (see attend_kernel)
-        bf16x8 pb[2], pr[2];
+        uint32_t new_hi[2][4], new_rest[2][4];
         constexpr float kOneUp = 1.0f + 0x1p-23f;
-#pragma unroll
-        for (int sh = 0; sh < 2; ++sh) {
-            uint32_t hw[4], rw[4];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                p[sh][e] = fast_exp2(fmaf(p[sh][e], scale, -mu[sh]));
-                l[sh] += p[sh][e];
+        // word w of the eight: a quarter of its work at a time
+        auto weigh = [&](int w, int part) __attribute__((always_inline)) {
+            const int sh = w >> 2, i = w & 3;
+            float &x = p[sh][2 * i], &y = p[sh][2 * i + 1];
+            if (part == 0) {
+                x = fast_exp2(fmaf(x, scale, -mu[sh]));
+                y = fast_exp2(fmaf(y, scale, -mu[sh]));
+            } else if (part == 1) {
+                l[sh] += x;
+                new_hi[sh][i] =
+                    __builtin_amdgcn_perm(__float_as_uint(y), __float_as_uint(x), 0x07060302u);
+            } else if (part == 2) {
+                l[sh] += y;
+                x = fmaf(x, kOneUp, -bf16_hi(__float_as_uint(x)));
+            } else {
+                y = fmaf(y, kOneUp, -bf16_hi(__float_as_uint(y)));
+                new_rest[sh][i] = pack_bf16(x, y);
             }
+        };
+        if (kBehind) {
+            const bf16x8 pb[2] = {as_bf16x8(hi_w[0][0], hi_w[0][1], hi_w[0][2], hi_w[0][3]),
+                                  as_bf16x8(hi_w[1][0], hi_w[1][1], hi_w[1][2], hi_w[1][3])};
+            const bf16x8 pr[2] = {
+                as_bf16x8(rest_w[0][0], rest_w[0][1], rest_w[0][2], rest_w[0][3]),
+                as_bf16x8(rest_w[1][0], rest_w[1][1], rest_w[1][2], rest_w[1][3])};
+#pragma unroll
+            for (int i = 0; i < C::kDims; ++i) {
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    acc[i][x & 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                        v8[i % kValuesAhead], x < 2 ? pb[x & 1] : pr[x & 1], acc[i][x & 1], 0, 0,
+                        0);
+                    // quarters i 32 / kDims + ... of the words' 32
+#pragma unroll
+                    for (int k = (i * 4 + x) * 8 / C::kDims; k < (i * 4 + x + 1) * 8 / C::kDims; ++k)
+                        weigh(k >> 2, k & 3);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                if (i + kValuesAhead < C::kDims)
+                    v8[i % kValuesAhead] = value(tile_behind, i + kValuesAhead);
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) weigh(k >> 2, k & 3);
+        }
+#pragma unroll
+        for (int sh = 0; sh < 2; ++sh)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float x = p[sh][2 * i], y = p[sh][2 * i + 1];
-                const uint32_t xb = __float_as_uint(x), yb = __float_as_uint(y);
-                hw[i] = __builtin_amdgcn_perm(yb, xb, 0x07060302u);
-                rw[i] = pack_bf16(fmaf(x, kOneUp, -bf16_hi(xb)), fmaf(y, kOneUp, -bf16_hi(yb)));
+                hi_w[sh][i] = new_hi[sh][i];
+                rest_w[sh][i] = new_rest[sh][i];
+                // made here, not where it is used
+                asm volatile("" : "+v"(hi_w[sh][i]), "+v"(rest_w[sh][i]));
             }
-            pb[sh] = as_bf16x8(hw[0], hw[1], hw[2], hw[3]);
-            pr[sh] = as_bf16x8(rw[0], rw[1], rw[2], rw[3]);
-        }
-        auto value = [&](int i) __attribute__((always_inline)) {
-            const char* at = tile + v_at[i & 3] + (i >> 2) * 1024;
-            const s16x4 x0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                (__attribute__((address_space(3))) s16x4*)at);
-            const s16x4 x1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                (__attribute__((address_space(3))) s16x4*)(at + 2 * C::kGroup));
-            uint2 w0, w1;
-            __builtin_memcpy(&w0, &x0, 8);
-            __builtin_memcpy(&w1, &x1, 8);
-            return as_bf16x8(w0.x, w0.y, w1.x, w1.y);
-        };
-        constexpr int kValuesAhead = 4;
+    };
+    turn(std::false_type{}, begin);
+    int t0 = begin + C::kTile;
+    if (t0 < end) {
+        do {
+            turn(std::true_type{}, t0);
+            t0 += C::kTile;
+        } while (t0 < end);
+    }
+    // the last tile's weights
+    {
+        const char* tile = tiles[((end - 1 - begin) / C::kTile) & 3];
+        const bf16x8 pb[2] = {as_bf16x8(hi_w[0][0], hi_w[0][1], hi_w[0][2], hi_w[0][3]),
+                              as_bf16x8(hi_w[1][0], hi_w[1][1], hi_w[1][2], hi_w[1][3])};
+        const bf16x8 pr[2] = {as_bf16x8(rest_w[0][0], rest_w[0][1], rest_w[0][2], rest_w[0][3]),
+                              as_bf16x8(rest_w[1][0], rest_w[1][1], rest_w[1][2], rest_w[1][3])};
         bf16x8 v8[kValuesAhead];
 #pragma unroll
-        for (int i = 0; i < kValuesAhead; ++i) v8[i] = value(i);
+        for (int i = 0; i < kValuesAhead; ++i) v8[i] = value(tile, i);
 #pragma unroll
         for (int i = 0; i < C::kDims; ++i) {
 #pragma unroll
             for (int x = 0; x < 4; ++x)
                 acc[i][x & 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
                     v8[i % kValuesAhead], x < 2 ? pb[x & 1] : pr[x & 1], acc[i][x & 1], 0, 0, 0);
-            if (i + kValuesAhead < C::kDims) v8[i % kValuesAhead] = value(i + kValuesAhead);
+            if (i + kValuesAhead < C::kDims) v8[i % kValuesAhead] = value(tile, i + kValuesAhead);
             __builtin_amdgcn_sched_barrier(0);
         }
-        buf = buf == 2 ? 0 : buf + 1;
     }
     __builtin_amdgcn_s_waitcnt(0);  // nothing is on its way to LDS when it is used anew
 
