@@ -95,19 +95,18 @@ struct Attend {
     };
 };
 
-// OWN: of request r only the positions from a.first[r] on (below 0: the request is
+// One of `blocks` workgroups.  OWN: of request r only the positions from a.first[r] on (below 0: the request is
 // left alone), always into partial results.
-template <int D, bool F8, int MT, bool PG16, bool OWN = false>
-__global__ __launch_bounds__(256, (Attend<D, F8, MT, PG16>::kOccupancy))
-void attend_kernel(AttendArgs a) {
+template <int D, bool F8, int MT, bool PG16, bool OWN>
+__device__ __forceinline__ void attend(const AttendArgs& a, unsigned block, unsigned blocks,
+                                       typename Attend<D, F8, MT, PG16>::Smem& sm) {
     using C = Attend<D, F8, MT, PG16>;
-    __shared__ typename C::Smem sm;
     const sv_cache& c = a.cache;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int col = lane & 15, g = lane >> 4;
     // grid: slot blocks fastest, then kv heads, requests and parts
-    int id = spread(blockIdx.x, gridDim.x, a.xcd_run * a.slot_blocks);
+    int id = spread(block, blocks, a.xcd_run * a.slot_blocks);
     const int mb = id % a.slot_blocks;
     id /= a.slot_blocks;
     const int h = id % c.n_kv_heads;

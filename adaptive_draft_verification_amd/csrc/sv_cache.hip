@@ -159,6 +159,13 @@ void run_join(const AttendArgs& a, hipStream_t stream) {
     }
 }
 
+template <int D, bool F8, int MT, bool PG16>
+__global__ __launch_bounds__(256, (Attend<D, F8, MT, PG16>::kOccupancy))
+void attend_kernel(AttendArgs a) {
+    __shared__ typename Attend<D, F8, MT, PG16>::Smem sm;
+    attend<D, F8, MT, PG16, false>(a, blockIdx.x, gridDim.x, sm);
+}
+
 template <int D, bool F8, int MT>
 void run_attend(const AttendArgs& a, unsigned grid, hipStream_t stream) {
     if (a.cache.page_size % 16 == 0 && 16 * a.cache.token_stride <= (int64_t)1 << 28)

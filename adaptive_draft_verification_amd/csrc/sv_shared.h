@@ -69,10 +69,17 @@ struct SharedPlan {
                int esize, int64_t capacity)
         : own(n_req, k_max, n_heads, n_kv_heads, head_dim, esize, capacity) {
         if (own.parts > 64) own.parts = 64;  // the join takes 128 of both kinds
+        // both kinds of workgroups are of one launch, with registers for two waves a SIMD
+        if (own.slot_tiles * head_dim > 256) {
+            own.slot_blocks *= own.slot_tiles * head_dim / 256;
+            own.slot_tiles = 256 / head_dim;
+        }
         const int64_t slots = (int64_t)n_req * (k_max + 1) * (n_heads / n_kv_heads);
         blocks = n_groups == 0 ? 0 : (slots / kSlots + n_groups) * n_kv_heads;
-        // as many as are on the chip at once, or as there are runs
-        chunks = head_dim < 256 ? 512 : 256;
+        // As many as are on the chip at once, or half of that beside a lot of workgroups
+        // over own positions; no more than there are runs.
+        const bool many = own.grid(n_req, n_kv_heads) >= 512;
+        chunks = head_dim < 256 && !many ? 512 : 256;
         const double runs = (double)blocks * ((capacity + kTile - 1) / kTile) / kRunMin + 8;
         if (runs < chunks) chunks = (int)runs & ~7;
     }

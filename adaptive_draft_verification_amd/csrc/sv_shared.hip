@@ -179,16 +179,25 @@ struct Prefix {
     // sum kFull.
     static constexpr float kHold = F8 ? 0.0f : 18.0f, kSlack = 8.0f;
     static constexpr float kFull = 0x1p-6f, kRaise = 16.0f;
+
+    struct Smem {
+        __attribute__((aligned(16))) char tiles[4][kTileBytes];
+        int64_t places[kPlaces];  // bytes to position begin + i at i % kPlaces
+        // a byte a position of the tile: it is none
+        __attribute__((aligned(4))) uint8_t absent[4][kTile];
+        int holes;  // a position before the end is none
+    };
 };
 
+// Workgroup `id` of s.chunks.
 template <int D, bool F8>
-__global__ __launch_bounds__(256, (Prefix<D, F8>::kOccupancy)) void prefix_kernel(SharedArgs s) {
+__device__ __forceinline__ void prefix(const SharedArgs& s, int id,
+                                       typename Prefix<D, F8>::Smem& sm) {
     using C = Prefix<D, F8>;
-    __shared__ __attribute__((aligned(16))) char tiles[4][C::kTileBytes];
-    __shared__ int64_t places[C::kPlaces];  // bytes to position begin + i at i % kPlaces
-    // a byte a position of the tile: it is none
-    __shared__ __attribute__((aligned(4))) uint8_t absent[4][C::kTile];
-    __shared__ int holes;  // a position before the end is none
+    auto& tiles = sm.tiles;
+    auto& places = sm.places;
+    auto& absent = sm.absent;
+    auto& holes = sm.holes;
     const AttendArgs& a = s.own;
     const sv_cache& c = a.cache;
     const int lane = threadIdx.x & 63;
@@ -198,8 +207,8 @@ __global__ __launch_bounds__(256, (Prefix<D, F8>::kOccupancy)) void prefix_kerne
     // eighth workgroup
     const SharedTotals totals = *s.totals;
     const int each = (totals.chunks + 7) / 8;
-    const int chunk = (blockIdx.x % 8) * each + blockIdx.x / 8;
-    if ((int)blockIdx.x / 8 >= each || chunk >= totals.chunks) return;
+    const int chunk = (id % 8) * each + id / 8;
+    if (id / 8 >= each || chunk >= totals.chunks) return;
     const int64_t head_tiles = s.group[s.n_groups].tile;
     const int head_blocks = s.group[s.n_groups].block;
     int64_t tile = chunk * totals.run;
@@ -610,6 +619,24 @@ __global__ __launch_bounds__(256, (Prefix<D, F8>::kOccupancy)) void prefix_kerne
     if (__ballot(bad) != 0 && lane == 0) raise_error(a.dev_error, SV_DEV_BAD_PAGE);
 }
 
+// Both kinds of workgroups: products keep those over the prefixes busy, loads of keys
+// and values those over the requests' own positions, so that they share the CUs well.
+// 256 x 1..8 rows (32 heads over 8, dim 128) behind 8192 shared positions and up to 500
+// of their own: XX us, one launch after the other XX.
+template <int D, bool F8, int MT, bool PG16>
+__global__ __launch_bounds__(256, (Prefix<D, F8>::kOccupancy)) void shared_kernel(SharedArgs s) {
+    using Own = Attend<D, F8, MT, PG16>;
+    static_assert(Own::kOccupancy >= Prefix<D, F8>::kOccupancy, "registers for both");
+    __shared__ union {
+        typename Prefix<D, F8>::Smem prefix;
+        typename Own::Smem own;
+    } sm;
+    if ((int)blockIdx.x < s.chunks)
+        prefix<D, F8>(s, blockIdx.x, sm.prefix);
+    else
+        attend<D, F8, MT, PG16, true>(s.own, blockIdx.x - s.chunks, gridDim.x - s.chunks, sm.own);
+}
+
 // --------------------------------------------------------------------- join
 
 // Merges the parts of a (row, head), those over the prefix first: a wave each, lanes
@@ -708,11 +735,14 @@ __global__ __launch_bounds__(256) void shared_join_kernel(SharedArgs s) {
 }
 
 template <int D, bool F8, int MT>
-void run_own(const AttendArgs& a, unsigned grid, hipStream_t stream) {
+void run_both(const SharedArgs& s, hipStream_t stream) {
+    const AttendArgs& a = s.own;
+    const unsigned grid = (unsigned)(s.chunks + (int64_t)a.cache.n_kv_heads * a.n_req *
+                                                    a.slot_blocks * a.parts);
     if (a.cache.page_size % 16 == 0 && 16 * a.cache.token_stride <= (int64_t)1 << 28)
-        attend_kernel<D, F8, MT, true, true><<<grid, 256, 0, stream>>>(a);
+        shared_kernel<D, F8, MT, true><<<grid, 256, 0, stream>>>(s);
     else
-        attend_kernel<D, F8, MT, false, true><<<grid, 256, 0, stream>>>(a);
+        shared_kernel<D, F8, MT, false><<<grid, 256, 0, stream>>>(s);
 }
 
 template <int D, bool F8>
@@ -721,17 +751,12 @@ hipError_t run_shared(const SharedArgs& s, hipStream_t stream) {
     layout_kernel<<<1, kLayoutThreads, 0, stream>>>(s);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    if (s.chunks > 0) {
-        prefix_kernel<D, F8><<<(unsigned)s.chunks, 256, 0, stream>>>(s);
-        e = hipGetLastError();
-        if (e != hipSuccess) return e;
-    }
-    const unsigned grid =
-        (unsigned)((int64_t)a.cache.n_kv_heads * a.n_req * a.slot_blocks * a.parts);
-    if (a.slot_tiles == 1) run_own<D, F8, 1>(a, grid, stream);
-    else if constexpr (D == 256) return hipErrorInvalidValue;  // AttendPlan takes one
-    else if (a.slot_tiles == 2) run_own<D, F8, 2>(a, grid, stream);
-    else run_own<D, F8, 4>(a, grid, stream);
+    // the plan takes slot_tiles * D <= 256
+    if (a.slot_tiles == 1) run_both<D, F8, 1>(s, stream);
+    else if constexpr (D == 256) return hipErrorInvalidValue;
+    else if (a.slot_tiles == 2) run_both<D, F8, 2>(s, stream);
+    else if constexpr (D == 128) return hipErrorInvalidValue;
+    else run_both<D, F8, 4>(s, stream);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
     const int64_t total = (int64_t)a.n_req * (a.k_max + 1) * a.n_heads;

@@ -20,7 +20,10 @@ sv_status check_sizes(int32_t n_req, int32_t n_groups, int32_t k_max, int32_t n_
     const sv_status s =
         sv::check_attend_sizes(n_req, k_max, n_heads, n_kv_heads, head_dim, capacity);
     if (s != SV_OK) return s;
-    return n_groups < 0 || n_groups > n_req ? SV_ERR_SHAPE : SV_OK;
+    if (n_groups < 0 || n_groups > n_req) return SV_ERR_SHAPE;
+    // the launch stays below 2^32 work-items
+    const sv::SharedPlan p(n_req, n_groups, k_max, n_heads, n_kv_heads, head_dim, 2, capacity);
+    return p.chunks + p.own.grid(n_req, n_kv_heads) > SV_MAX_ATTEND_SLOTS ? SV_ERR_SHAPE : SV_OK;
 }
 
 }  // namespace

@@ -1,0 +1,750 @@
+// Attention of a batch whose requests share prefixes (gfx950, wave64):
+// sv_cache_attend_shared.  Four launches: the groups laid out; every group's rows over
+// its prefix, as one long block of queries; every request's rows over its own
+// positions (sv_cache_attend's kernel, from the prefix's end on); the join.
+#include <type_traits>
+
+#include "sv_attend_kernel.h"
+#include "sv_device.h"
+#include "sv_launch.h"
+#include "sv_shared.h"
+
+namespace sv {
+namespace {
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+// ------------------------------------------------------------------- layout
+
+constexpr int kLayoutThreads = 1024;
+
+__device__ __forceinline__ int64_t wave_incl_sum64(int64_t v, int lane) {
+#pragma unroll
+    for (int off = 1; off < kWave; off <<= 1) {
+        const int64_t x = __shfl_up((long long)v, off);
+        if (lane >= off) v += x;
+    }
+    return v;
+}
+
+// Checks the groups and their requests, and counts the tiles: one workgroup, so that
+// the launches behind it only read.
+__global__ __launch_bounds__(kLayoutThreads) void layout_kernel(SharedArgs s) {
+    const AttendArgs& a = s.own;
+    __shared__ int block_sums[kLayoutThreads / kWave], longest_prefix;
+    __shared__ int64_t tile_sums[kLayoutThreads / kWave];
+    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+    int err = 0;
+    if (t == 0) longest_prefix = 0;
+    for (int g = t; g <= s.n_groups && s.n_groups > 0; g += kLayoutThreads) {
+        const int at = s.group_start[g];
+        if (at < 0 || at > a.n_req || (g > 0 && s.group_start[g - 1] > at))
+            err = SV_DEV_BAD_CU_ROWS;
+    }
+    const bool none = __syncthreads_or(err) != 0;
+    for (int g = t; g < s.n_groups; g += kLayoutThreads) {
+        const int P = s.prefix_len[g];
+        const bool fits = P >= 0 && P <= (int64_t)a.max_pages * a.cache.page_size;
+        __hip_atomic_store(&s.group[g].broken, none || fits ? 0 : SV_DEV_BAD_CTX,
+                           __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    __syncthreads();
+    // every request's group, and whether its rows are where they have to be
+    for (int r = t; r < a.n_req; r += kLayoutThreads) {
+        int group = -1;
+        if (!none && s.n_groups > 0 && r >= s.group_start[0] && r < s.group_start[s.n_groups]) {
+            int lo = 0, hi = s.n_groups;  // the last group that starts at r or before
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (s.group_start[mid] <= r) lo = mid;
+                else hi = mid;
+            }
+            group = lo;
+            const int from = a.cu_rows[r], to = a.cu_rows[r + 1];
+            if (from < 0 || to < from || to - from > a.k_max + 1 || to > a.q_rows)
+                atomicOr(&s.group[group].broken, SV_DEV_BAD_CU_ROWS);
+        }
+        s.request[r].group = group;
+    }
+    __syncthreads();
+    int blocks = 0;  // of earlier groups
+    int64_t tiles = 0;
+    for (int g0 = 0; g0 < s.n_groups; g0 += kLayoutThreads) {
+        const int g = g0 + t;
+        int n = 0, each = 0;
+        if (g < s.n_groups && !none) {
+            const int bits = __hip_atomic_load(&s.group[g].broken, __ATOMIC_RELAXED,
+                                               __HIP_MEMORY_SCOPE_AGENT);
+            err |= bits;
+            const int from = s.group_start[g], to = s.group_start[g + 1];
+            const int P = s.prefix_len[g];
+            if (bits == 0 && P > 0 && to > from)
+                n = ((a.cu_rows[to] - a.cu_rows[from]) * a.group + SharedPlan::kSlots - 1) /
+                    SharedPlan::kSlots;
+            if (n > 0) {
+                each = (int)(((int64_t)P + SharedPlan::kTile - 1) / SharedPlan::kTile);
+                atomicMax(&longest_prefix, each);
+            }
+        }
+        const int blocks_to = wave_incl_sum_dpp(n, lane);
+        const int64_t tiles_to = wave_incl_sum64((int64_t)n * each, lane);
+        if (lane == 63) {
+            block_sums[wave] = blocks_to;
+            tile_sums[wave] = tiles_to;
+        }
+        __syncthreads();
+        int block = blocks + blocks_to - n;
+        int64_t tile = tiles + tiles_to - (int64_t)n * each;
+        for (int w = 0; w < kLayoutThreads / kWave; ++w) {
+            if (w < wave) {
+                block += block_sums[w];
+                tile += tile_sums[w];
+            }
+            blocks += block_sums[w];
+            tiles += tile_sums[w];
+        }
+        if (g < s.n_groups) {
+            s.group[g].tile = tile;
+            s.group[g].block = block;
+        }
+        __syncthreads();
+    }
+    if (t == 0) {
+        s.group[s.n_groups].tile = tiles;
+        s.group[s.n_groups].block = blocks;
+        // equal runs; a block of n tiles lies in n / run + 2 of them at most
+        const int64_t all = tiles * a.cache.n_kv_heads;
+        const int64_t few = (longest_prefix + SharedPlan::kSegments - 3) / (SharedPlan::kSegments - 2);
+        int64_t run = s.chunks > 0 ? (all + s.chunks - 1) / s.chunks : 0;
+        run = run < few ? few : run;
+        run = run < SharedPlan::kRunMin ? SharedPlan::kRunMin : run;
+        s.totals->run = run;
+        s.totals->chunks = (int)((all + run - 1) / run);
+    }
+    for (int r = t; r < a.n_req; r += kLayoutThreads) {
+        const int g = s.request[r].group;
+        int first = none ? -1 : 0, row = 0;
+        if (g >= 0) {
+            const int bits = __hip_atomic_load(&s.group[g].broken, __ATOMIC_RELAXED,
+                                               __HIP_MEMORY_SCOPE_AGENT);
+            first = bits != 0 ? -1 : s.prefix_len[g];
+            row = a.cu_rows[r] - a.cu_rows[s.group_start[g]];
+        }
+        s.first[r] = first;
+        s.request[r].row = row;
+    }
+    if (err != 0) raise_error(a.dev_error, err);
+}
+
+// ------------------------------------------------------------------- prefix
+//
+// A group's query slots of one kv head are its rows times the G query heads that
+// share it (slot i: row i / G, head h G + i % G): all of them see the whole prefix.
+// A workgroup of four waves takes 128 slots over one part of it, 32 positions at a
+// time, whose keys and values lie in LDS as bf16; a wave takes 32 slots.  Operands of
+// v_mfma_f32_16x16x32_bf16:
+//   S^T = K Q^T: A holds 16 positions (lane % 16) by 32 dims (8 for each g = lane /
+//   16), B 16 slots by the same dims, so a lane ends with the scores of ONE slot
+//   (lane % 16) at positions 4 g .. 4 g + 3 of each 16;
+//   O^T = V^T P^T: B's lane holds 8 positions of one slot, 4 g .. of either 16, just as
+//   the scores are; A needs the same positions of one dim a lane: two transposing LDS
+//   reads of 4 positions by 16 dims for each 16 lanes.
+// Bound by products and the softmax beside them: at 128 dims 48 products (768 clocks)
+// and some 130 other instructions a wave and tile, two waves a SIMD (one at 256 dims).
+// Tiles come two turns ahead (8-bit ones, which pass registers, one), into one of
+// three places, so that one barrier a tile is enough.
+// In LDS 8 positions by 8 chunks of 16 bytes are a KB, the chunk c of position x at
+// (c ^ swizzle(x)) of its 128 bytes.  LDS has 64 banks of 4 bytes: the chunk c of 16
+// neighbouring positions, and the chunks c and c ^ 1 of 8, lie in different ones.
+
+__device__ __forceinline__ int swizzle(int pos) { return (pos & 6) | ((pos >> 3) & 1); }
+
+// What a position without a page is loaded from.
+__device__ const uint4 kZeros[256 / 8] = {};
+
+template <int D, bool F8>
+struct Prefix {
+    static constexpr int kTile = 32;
+    static constexpr int kLoads = D / 64;           // KB of 8 positions' keys, or values
+    static constexpr int kGroup = kLoads * 1024;    // bytes
+    static constexpr int kKeys = 4 * kGroup;        // of a tile: a group a wave
+    static constexpr int kTileBytes = 2 * kKeys;
+    static constexpr int kSteps = D / 32;           // products of a score
+    static constexpr int kDims = D / 16;            // 16-dim tiles of the output
+    static constexpr int kEsize = F8 ? 1 : 2;
+    static constexpr int kPlaces = 1024;            // positions whose places are in LDS
+    static constexpr int kOccupancy = D < 256 ? 2 : 1;
+    // Weights are held as attend_kernel holds them: 2^(score - m), m kHold above the
+    // maximum that it was set from, raised where a score passes that by 2^8 or a lane's
+    // sum kFull.
+    static constexpr float kHold = F8 ? 0.0f : 18.0f, kSlack = 8.0f;
+    static constexpr float kFull = 0x1p-6f, kRaise = 16.0f;
+};
+
+template <int D, bool F8>
+__global__ __launch_bounds__(256, (Prefix<D, F8>::kOccupancy)) void prefix_kernel(SharedArgs s) {
+    using C = Prefix<D, F8>;
+    __shared__ __attribute__((aligned(16))) char tiles[4][C::kTileBytes];
+    __shared__ int64_t places[C::kPlaces];  // bytes to position begin + i at i % kPlaces
+    // a byte a position of the tile: it is none
+    __shared__ __attribute__((aligned(4))) uint8_t absent[4][C::kTile];
+    __shared__ int holes;  // a position before the end is none
+    const AttendArgs& a = s.own;
+    const sv_cache& c = a.cache;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int col = lane & 15, g = lane >> 4;
+    // consecutive runs of tiles (they read the same keys and values) to one XCD: every
+    // eighth workgroup
+    const SharedTotals totals = *s.totals;
+    const int each = (totals.chunks + 7) / 8;
+    const int chunk = (blockIdx.x % 8) * each + blockIdx.x / 8;
+    if ((int)blockIdx.x / 8 >= each || chunk >= totals.chunks) return;
+    const int64_t head_tiles = s.group[s.n_groups].tile;
+    const int head_blocks = s.group[s.n_groups].block;
+    int64_t tile = chunk * totals.run;
+    const int64_t to_tile = min(tile + totals.run, head_tiles * c.n_kv_heads);
+    int h = (int)(tile / head_tiles);
+    int64_t in_head = tile - h * head_tiles;
+    // the group the run starts in: the last one whose tiles begin there or before
+    int group = 0;
+    for (int n = s.n_groups; n > 1;) {
+        const int step = (n + kWave - 1) / kWave, at = group + lane * step;
+        const bool before = lane * step < n && s.group[at].tile <= in_head;
+        const int skip = (__popcll(__ballot(before)) - 1) * step;  // lane 0's is
+        group += skip;
+        n = min(step, n - skip);
+    }
+    bool bad = false;
+    if (threadIdx.x == 0) holes = 0;
+    // ---- the run's segments
+    while (tile < to_tile) {
+    if (in_head == head_tiles) {
+        in_head = 0;
+        group = 0;
+        ++h;
+    }
+    while (s.group[group + 1].tile <= in_head) ++group;
+    const int from_req = s.group_start[group], to_req = s.group_start[group + 1];
+    const int P = s.prefix_len[group];
+    const int lo = a.cu_rows[from_req];
+    const int block_tiles = (int)(((int64_t)P + C::kTile - 1) / C::kTile);
+    const int64_t in_group = in_head - s.group[group].tile;
+    const int index = (int)((uint64_t)in_group / (uint32_t)block_tiles);  // the block's
+    const int first_tile = (int)(in_group - (int64_t)index * block_tiles);
+    const int n_tiles = (int)min((int64_t)(block_tiles - first_tile), to_tile - tile);
+    const int64_t block_id = (int64_t)h * head_blocks + s.group[group].block + index;
+    const int slots = (a.cu_rows[to_req] - lo) * a.group - index * SharedPlan::kSlots;
+    const int begin = first_tile * C::kTile;
+    const int end = min(P, begin + n_tiles * C::kTile);
+    if (threadIdx.x == 0) {
+        if (first_tile == 0) s.span[block_id].first = chunk;
+        if (first_tile + n_tiles == block_tiles) s.span[block_id].last = chunk;
+    }
+    tile += n_tiles;
+    in_head += n_tiles;
+
+    // ---- keys' and values' way into LDS: wave w brings positions 8 w .. of a tile
+    const int32_t* table = a.page_table + (int64_t)from_req * a.max_pages;
+    const int mine = wave * 8 + (lane >> 3);
+    const int chunk_of = ((lane & 7) ^ swizzle(mine)) * 8 * C::kEsize;
+    const char* k_base = static_cast<const char*>(c.k) + (int64_t)h * c.head_stride * C::kEsize;
+    const int64_t v_from_k = static_cast<const char*>(c.v) - static_cast<const char*>(c.k);
+    // The places of `n` positions from `from` on, into LDS: kPlaces at first, then half
+    // as many at a time (a wait for a page id in registers would be a wait for the tiles
+    // that are on their way).  -1: after the end, or on a page that is not there.
+    auto fetch_places = [&](int from, int n) __attribute__((always_inline)) {
+        for (int i = threadIdx.x; i < n && from + i < end + 4 * C::kTile; i += 256) {
+            const int t = from + i;
+            int64_t place = -1;
+            if (t < end) {
+                const int in = a.page_shift >= 0 ? t >> a.page_shift
+                                                 : (int)((unsigned)t / (unsigned)c.page_size);
+                const int page = table[in];
+                if (page >= 0 && page < c.n_pages) {
+                    place = ((int64_t)page * c.page_stride +
+                             (int64_t)(t - in * c.page_size) * c.token_stride) *
+                            C::kEsize;
+                } else {
+                    bad = true;
+                    holes = 1;
+                }
+            }
+            places[(t - begin) & (C::kPlaces - 1)] = place;
+        }
+    };
+    auto look_up = [&](int t0) { return places[(t0 + mine - begin) & (C::kPlaces - 1)]; };
+    uint2 raw[F8 ? 2 * C::kLoads : 1];
+    // issues the loads of a tile
+    auto issue = [&](int buf, int64_t place) __attribute__((always_inline)) {
+        const bool there = place >= 0;
+        const char* k_from = (there ? k_base + place : reinterpret_cast<const char*>(kZeros)) + chunk_of;
+        const char* v_from = there ? k_from + v_from_k : k_from;
+        absent[buf][mine] = !there;
+        if constexpr (F8) {
+#pragma unroll
+            for (int i = 0; i < C::kLoads; ++i) {
+                raw[i] = *reinterpret_cast<const uint2*>(k_from + i * 64);
+                raw[C::kLoads + i] = *reinterpret_cast<const uint2*>(v_from + i * 64);
+            }
+        } else {
+            const uint32_t to =
+                __builtin_amdgcn_readfirstlane(lds_address(tiles[buf] + wave * C::kGroup));
+#pragma unroll
+            for (int i = 0; i < C::kLoads; ++i) {
+                load_to_lds<128>(k_from, to + i * 1024, i);
+                load_to_lds<128>(v_from, to + C::kKeys + i * 1024, i);
+            }
+        }
+    };
+    // the tile of this turn has arrived: an 8-bit one goes into LDS as bf16
+    auto settle = [&](int buf) __attribute__((always_inline)) {
+        if constexpr (F8) {
+#pragma unroll
+            for (int i = 0; i < 2 * C::kLoads; ++i) {
+                char* to = tiles[buf] + (i < C::kLoads ? 0 : C::kKeys) + wave * C::kGroup +
+                           (i % C::kLoads) * 1024 + lane * 16;
+                *reinterpret_cast<uint4*>(to) =
+                    make_uint4(e4m3_pair<false>(raw[i].x), e4m3_pair<true>(raw[i].x),
+                               e4m3_pair<false>(raw[i].y), e4m3_pair<true>(raw[i].y));
+            }
+        } else {
+            // all but the tile behind it
+            asm volatile("s_waitcnt vmcnt(%0)" : : "n"(2 * C::kLoads) : "memory");
+        }
+    };
+
+    __syncthreads();  // the segment before has been read
+    fetch_places(begin, C::kPlaces);
+    __syncthreads();
+    issue(0, look_up(begin));
+    if (!F8) issue(1, look_up(begin + C::kTile));
+    int64_t place = look_up(begin + (F8 ? 1 : 2) * C::kTile);
+
+    // ---- queries of the wave's slots, operand B of every step
+    int row[2], head[2];
+    bool live[2];
+    bf16x8 q[C::kSteps][2];
+#pragma unroll
+    for (int sh = 0; sh < 2; ++sh) {
+        const int i = wave * 32 + sh * 16 + col, slot = index * SharedPlan::kSlots + i;
+        live[sh] = i < slots;
+        row[sh] = (int)((unsigned)slot / (unsigned)a.group);
+        head[sh] = h * a.group + slot - row[sh] * a.group;
+        // a slot that is not there takes the block's first one's
+        const int first = index * SharedPlan::kSlots;
+        const int q_row = live[sh] ? row[sh] : first / a.group;
+        const int q_head = live[sh] ? head[sh] : h * a.group + first % a.group;
+        const uint16_t* qp = static_cast<const uint16_t*>(a.q) + (int64_t)(lo + q_row) * a.q_ld +
+                             (int64_t)q_head * D + g * 8;
+#pragma unroll
+        for (int st = 0; st < C::kSteps; ++st) {
+            const uint4 w = *reinterpret_cast<const uint4*>(qp + st * 32);
+            q[st][sh] = as_bf16x8(w.x, w.y, w.z, w.w);
+        }
+    }
+    // waited for here, not among the loads of a tile
+#pragma unroll
+    for (int st = 0; st < C::kSteps; ++st)
+        asm volatile("" : "+v"(q[st][0]), "+v"(q[st][1]));
+    // The scale is taken as positive (products change their sign with it), so that the
+    // largest product is the largest score and a masked -inf stays one; 0 as 1 of
+    // products that are 0.
+    const float signed_scale =
+        a.scale * kLog2e * (F8 && c.k_scale != nullptr ? c.k_scale[h] : 1.0f);
+    const float scale = signed_scale == 0.0f ? 1.0f : fabsf(signed_scale);
+    const float sign = signed_scale == 0.0f ? 0.0f : signed_scale < 0.0f ? -1.0f : 1.0f;
+
+    f32x4 acc[C::kDims][2];
+#pragma unroll
+    for (int i = 0; i < C::kDims; ++i)
+#pragma unroll
+        for (int sh = 0; sh < 2; ++sh) acc[i][sh] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    // m (-inf: no score yet), the m used, the product from which m is raised, a lane's sum
+    float m[2], mu[2], far[2], l[2];
+#pragma unroll
+    for (int sh = 0; sh < 2; ++sh) {
+        m[sh] = far[sh] = -kInf;
+        mu[sh] = l[sh] = 0.0f;
+    }
+
+    // where a lane reads keys: chunks 4 st + g of its position of either 16, st = 0, 1 of
+    // 128 bytes; and values: 4 positions by 16 dims for 16 lanes, tiles 0 .. 3 of them
+    int k_at[2], v_at[4];
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+        k_at[j] = (col >> 3) * C::kGroup + (col & 7) * 128 + ((4 * j + g) ^ swizzle(col)) * 16;
+    {
+        const int pos = 4 * g + (col >> 2);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            v_at[j] = C::kKeys + (pos >> 3) * C::kGroup + (pos & 7) * 128 + (lane & 1) * 8 +
+                      ((2 * j + ((lane >> 1) & 1)) ^ swizzle(pos)) * 16;
+    }
+
+    // The weights that are not yet multiplied with their values, as two bf16 terms (see
+    // attend_kernel): word i of slot sh is positions 4 g + 2 (i % 2) .. of 16 (i / 2).
+    uint32_t hi_w[2][4] = {}, rest_w[2][4] = {};
+    auto value = [&](const char* tile, int i) __attribute__((always_inline)) {
+        const char* at = tile + v_at[i & 3] + (i >> 2) * 1024;
+        const s16x4 x0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (__attribute__((address_space(3))) s16x4*)at);
+        const s16x4 x1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (__attribute__((address_space(3))) s16x4*)(at + 2 * C::kGroup));
+        uint2 w0, w1;
+        __builtin_memcpy(&w0, &x0, 8);
+        __builtin_memcpy(&w1, &x1, 8);
+        return as_bf16x8(w0.x, w0.y, w1.x, w1.y);
+    };
+    constexpr int kValuesAhead = 4;
+    // One turn: the scores of tile t, then its weights between the products of tile
+    // t - 1's with their values (BEHIND: there is one).
+    auto turn = [&](auto behind, int t0) __attribute__((always_inline)) {
+        constexpr bool kBehind = decltype(behind)::value;
+        const int buf = ((t0 - begin) / C::kTile) & 3;
+        settle(buf);
+        __syncthreads();
+        issue((buf + (F8 ? 1 : 2)) & 3, place);
+        place = look_up(t0 + (F8 ? 2 : 3) * C::kTile);
+        if (kBehind && ((t0 - begin) & (C::kPlaces / 2 - 1)) == 0)
+            fetch_places(t0 + C::kPlaces / 2, C::kPlaces / 2);
+        const char* tile = tiles[buf];
+        const char* tile_behind = tiles[(buf + 3) & 3];
+
+        // scores: both 16 positions of a step, two slots' products each
+        f32x4 sc[2][2];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sc[i >> 1][i & 1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        constexpr int kAhead = 2;
+        bf16x8 k8[kAhead][2], v8[kValuesAhead];
+        auto key = [&](int st, int ph) __attribute__((always_inline)) {
+            const uint4 w = *reinterpret_cast<const uint4*>(tile + k_at[st & 1] + (st >> 1) * 1024 +
+                                                            ph * 2 * C::kGroup);
+            return as_bf16x8(w.x, w.y, w.z, w.w);
+        };
+#pragma unroll
+        for (int st = 0; st < kAhead; ++st)
+#pragma unroll
+            for (int ph = 0; ph < 2; ++ph) k8[st][ph] = key(st, ph);
+#pragma unroll
+        for (int st = 0; st < C::kSteps; ++st) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                sc[i >> 1][i & 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                    k8[st % kAhead][i >> 1], q[st][i & 1], sc[i >> 1][i & 1], 0, 0, 0);
+#pragma unroll
+            for (int ph = 0; ph < 2; ++ph)
+                if (st + kAhead < C::kSteps) k8[st % kAhead][ph] = key(st + kAhead, ph);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        if (kBehind)
+#pragma unroll
+            for (int i = 0; i < kValuesAhead; ++i) v8[i] = value(tile_behind, i);
+        float p[2][8];  // of a slot: positions 4 g .. of the first 16, of the second
+#pragma unroll
+        for (int sh = 0; sh < 2; ++sh)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) p[sh][e] = sc[e >> 2][sh][e & 3];
+        if (sign != 1.0f) {
+#pragma unroll
+            for (int sh = 0; sh < 2; ++sh)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) p[sh][e] *= sign;
+        }
+        if (t0 + C::kTile > end || __builtin_amdgcn_readfirstlane(holes) != 0) {
+#pragma unroll
+            for (int ph = 0; ph < 2; ++ph) {
+                const uint32_t no =
+                    *reinterpret_cast<const uint32_t*>(&absent[buf][ph * 16 + 4 * g]);
+#pragma unroll
+                for (int sh = 0; sh < 2; ++sh)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if ((no >> (8 * e)) & 1) p[sh][ph * 4 + e] = -kInf;
+            }
+        }
+        float mx[2];
+#pragma unroll
+        for (int sh = 0; sh < 2; ++sh) {
+            mx[sh] = p[sh][0];
+#pragma unroll
+            for (int e = 1; e < 8; ++e) mx[sh] = fmaxf(mx[sh], p[sh][e]);
+        }
+        // in the first tile, and hardly ever later
+        bool raise = mx[0] > far[0] || mx[1] > far[1];
+        if (!F8) raise = raise || fmaxf(l[0], l[1]) > C::kFull;
+        if (__ballot(raise) != 0) {
+#pragma unroll
+            for (int sh = 0; sh < 2; ++sh) {
+                float top = fmaxf(mx[sh], __shfl_xor(mx[sh], 16));
+                top = fmaxf(top, __shfl_xor(top, 32));
+                float to = fmaxf(m[sh], ceilf(top * scale) + C::kHold);
+                if (!F8) {
+                    float most = fmaxf(l[sh], __shfl_xor(l[sh], 16));
+                    most = fmaxf(most, __shfl_xor(most, 32));
+                    if (most > C::kFull) to += C::kRaise;
+                }
+                if (to > m[sh]) {
+                    // m = -inf: 0; else a power of two, as m is an integer
+                    const float f = fast_exp2(m[sh] - to);
+                    if (kBehind) {
+#pragma unroll
+                        for (int i = 0; i < C::kDims; ++i) acc[i][sh] *= f;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            hi_w[sh][i] = pack_bf16(bf16_lo(hi_w[sh][i]) * f,
+                                                    bf16_hi(hi_w[sh][i]) * f);
+                            rest_w[sh][i] = pack_bf16(bf16_lo(rest_w[sh][i]) * f,
+                                                      bf16_hi(rest_w[sh][i]) * f);
+                        }
+                    }
+                    l[sh] *= f;
+                    m[sh] = mu[sh] = to;
+                    far[sh] = (to - C::kHold + C::kSlack) / scale;
+                }
+            }
+        }
+        uint32_t new_hi[2][4], new_rest[2][4];
+        constexpr float kOneUp = 1.0f + 0x1p-23f;
+        // word w of the eight: a quarter of its work at a time
+        auto weigh = [&](int w, int part) __attribute__((always_inline)) {
+            const int sh = w >> 2, i = w & 3;
+            float &x = p[sh][2 * i], &y = p[sh][2 * i + 1];
+            if (part == 0) {
+                x = fast_exp2(fmaf(x, scale, -mu[sh]));
+                y = fast_exp2(fmaf(y, scale, -mu[sh]));
+            } else if (part == 1) {
+                l[sh] += x;
+                new_hi[sh][i] =
+                    __builtin_amdgcn_perm(__float_as_uint(y), __float_as_uint(x), 0x07060302u);
+            } else if (part == 2) {
+                l[sh] += y;
+                x = fmaf(x, kOneUp, -bf16_hi(__float_as_uint(x)));
+            } else {
+                y = fmaf(y, kOneUp, -bf16_hi(__float_as_uint(y)));
+                new_rest[sh][i] = pack_bf16(x, y);
+            }
+        };
+        if (kBehind) {
+            const bf16x8 pb[2] = {as_bf16x8(hi_w[0][0], hi_w[0][1], hi_w[0][2], hi_w[0][3]),
+                                  as_bf16x8(hi_w[1][0], hi_w[1][1], hi_w[1][2], hi_w[1][3])};
+            const bf16x8 pr[2] = {
+                as_bf16x8(rest_w[0][0], rest_w[0][1], rest_w[0][2], rest_w[0][3]),
+                as_bf16x8(rest_w[1][0], rest_w[1][1], rest_w[1][2], rest_w[1][3])};
+#pragma unroll
+            for (int i = 0; i < C::kDims; ++i) {
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    acc[i][x & 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                        v8[i % kValuesAhead], x < 2 ? pb[x & 1] : pr[x & 1], acc[i][x & 1], 0, 0,
+                        0);
+                    // quarters i 32 / kDims + ... of the words' 32
+#pragma unroll
+                    for (int k = (i * 4 + x) * 8 / C::kDims; k < (i * 4 + x + 1) * 8 / C::kDims; ++k)
+                        weigh(k >> 2, k & 3);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                if (i + kValuesAhead < C::kDims)
+                    v8[i % kValuesAhead] = value(tile_behind, i + kValuesAhead);
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) weigh(k >> 2, k & 3);
+        }
+#pragma unroll
+        for (int sh = 0; sh < 2; ++sh)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                hi_w[sh][i] = new_hi[sh][i];
+                rest_w[sh][i] = new_rest[sh][i];
+            }
+    };
+    turn(std::false_type{}, begin);
+    for (int t0 = begin + C::kTile; t0 < end; t0 += C::kTile) turn(std::true_type{}, t0);
+    // the last tile's weights
+    {
+        const char* tile = tiles[((end - 1 - begin) / C::kTile) & 3];
+        const bf16x8 pb[2] = {as_bf16x8(hi_w[0][0], hi_w[0][1], hi_w[0][2], hi_w[0][3]),
+                              as_bf16x8(hi_w[1][0], hi_w[1][1], hi_w[1][2], hi_w[1][3])};
+        const bf16x8 pr[2] = {as_bf16x8(rest_w[0][0], rest_w[0][1], rest_w[0][2], rest_w[0][3]),
+                              as_bf16x8(rest_w[1][0], rest_w[1][1], rest_w[1][2], rest_w[1][3])};
+        bf16x8 v8[kValuesAhead];
+#pragma unroll
+        for (int i = 0; i < kValuesAhead; ++i) v8[i] = value(tile, i);
+#pragma unroll
+        for (int i = 0; i < C::kDims; ++i) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+                acc[i][x & 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                    v8[i % kValuesAhead], x < 2 ? pb[x & 1] : pr[x & 1], acc[i][x & 1], 0, 0, 0);
+            if (i + kValuesAhead < C::kDims) v8[i % kValuesAhead] = value(tile, i + kValuesAhead);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+    __builtin_amdgcn_s_waitcnt(0);  // nothing is on its way to LDS when it is used anew
+
+#pragma unroll
+    for (int sh = 0; sh < 2; ++sh) {
+        l[sh] += __shfl_xor(l[sh], 16);
+        l[sh] += __shfl_xor(l[sh], 32);
+        if (!live[sh]) continue;
+        const int64_t rec =
+            (block_id + chunk) * SharedPlan::kSlots + wave * 32 + sh * 16 + col;
+        float* o = s.prefix_out + rec * D + 4 * g;
+#pragma unroll
+        for (int i = 0; i < C::kDims; ++i) *reinterpret_cast<f32x4*>(o + i * 16) = acc[i][sh];
+        if (g == 0) {
+            s.prefix_ml[rec * 2] = m[sh];
+            s.prefix_ml[rec * 2 + 1] = l[sh];
+        }
+    }
+    }
+    if (__ballot(bad) != 0 && lane == 0) raise_error(a.dev_error, SV_DEV_BAD_PAGE);
+}
+
+// --------------------------------------------------------------------- join
+
+// Merges the parts of a (row, head), those over the prefix first: a wave each, lanes
+// over the dims, in a fixed order.
+template <int D, bool F8>
+__global__ __launch_bounds__(256) void shared_join_kernel(SharedArgs s) {
+    constexpr int E = D / kWave;
+    __shared__ float factors[4][128];
+    const AttendArgs& a = s.own;
+    const sv_cache& c = a.cache;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int per = (a.k_max + 1) * a.n_heads;
+    const int64_t id = (int64_t)blockIdx.x * 4 + wave;
+    if (id >= (int64_t)a.n_req * per) return;
+    const int r = (int)(id / per), rest = (int)(id % per);
+    const int row = rest / a.n_heads, head = rest % a.n_heads;
+    const int first = s.first[r];
+    const int lo = a.cu_rows[r], hi = a.cu_rows[r + 1], rows = hi - lo, ctx = a.ctx_len[r];
+    if (first < 0 || lo < 0 || hi < lo || rows > a.k_max + 1 || hi > a.q_rows || row >= rows ||
+        ctx < first || (int64_t)ctx + rows > (int64_t)a.max_pages * c.page_size)
+        return;
+    // the parts as the two launches made them
+    int n1 = 0;
+    int64_t rec1 = 0;  // parts are kSlots records apart
+    if (first > 0) {
+        const SharedRequest at = s.request[r];
+        const int h = head / a.group;
+        const int slot = (at.row + row) * a.group + head - h * a.group;
+        const int64_t block_id = (int64_t)h * s.group[s.n_groups].block +
+                                 s.group[at.group].block + slot / SharedPlan::kSlots;
+        const SharedSpan span = s.span[block_id];
+        n1 = span.last - span.first + 1;
+        rec1 = (block_id + span.first) * SharedPlan::kSlots + slot % SharedPlan::kSlots;
+    }
+    const int len = ctx + rows - (first & ~15), plen = part_len(len, a.parts, a.part_min);
+    const int n = n1 + (len + plen - 1) / plen;  // at most 128
+    // attend_kernel's records: request, head, row
+    const int64_t rec2 = (((int64_t)r * a.n_heads + head) * (a.k_max + 1) + row) * a.parts;
+    // the largest maximum and the parts' factors, two a lane
+    float mm[2] = {-kInf, -kInf}, ll[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int p = lane + 64 * i;
+        if (p >= n) continue;
+        const float* ml = p < n1 ? s.prefix_ml + (rec1 + p * SharedPlan::kSlots) * 2 : a.part_ml + (rec2 + p - n1) * 2;
+        mm[i] = ml[0];
+        ll[i] = ml[1];
+    }
+    const float m = wave_max(fmaxf(mm[0], mm[1]));
+    const float f0 = mm[0] == m ? 1.0f : fast_exp2(mm[0] - m);
+    const float f1 = mm[1] == m ? 1.0f : fast_exp2(mm[1] - m);
+    const float l =
+        wave_sum((lane < n ? f0 * ll[0] : 0.0f) + (lane + 64 < n ? f1 * ll[1] : 0.0f));
+    // over the whole sum before the outputs are added up: they are then shares of the
+    // mean, and stay in range
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    float* factor = factors[wave];
+    factor[lane] = f0 * inv;
+    factor[lane + 64] = f1 * inv;
+    __builtin_amdgcn_wave_barrier();
+    float o[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = 0.0f;
+    for (int p0 = 0; p0 < n; p0 += 4) {
+        float x[4][E];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int p = min(p0 + i, n - 1);
+            const float* from =
+                (p < n1 ? s.prefix_out + (rec1 + p * SharedPlan::kSlots) * D
+                       : a.part_out + (rec2 + p - n1) * D) + lane * E;
+#pragma unroll
+            for (int e = 0; e < E; ++e) x[i][e] = from[e];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (p0 + i >= n) break;
+            const float f = factor[p0 + i];
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[e] += f * x[i][e];
+        }
+    }
+    const float vscale = F8 && c.v_scale != nullptr ? c.v_scale[head / a.group] : 1.0f;
+    uint16_t* out = static_cast<uint16_t*>(a.out) + (int64_t)(lo + row) * a.out_ld +
+                    (int64_t)head * D + lane * E;
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+        out[e] = (uint16_t)pack_bf16(l == 0.0f ? 0.0f : o[e] * vscale, 0.0f);
+    if (a.out_lse != nullptr && lane == 0) {
+        // the sum's exponent first: both terms are then of the result's size
+        int e;
+        const float f = frexpf(l, &e);
+        a.out_lse[(int64_t)(lo + row) * a.n_heads + head] =
+            l == 0.0f ? -kInf : ((m + (float)e) + log2f(f)) * kLn2;
+    }
+}
+
+template <int D, bool F8, int MT>
+void run_own(const AttendArgs& a, unsigned grid, hipStream_t stream) {
+    if (a.cache.page_size % 16 == 0 && 16 * a.cache.token_stride <= (int64_t)1 << 28)
+        attend_kernel<D, F8, MT, true, true><<<grid, 256, 0, stream>>>(a);
+    else
+        attend_kernel<D, F8, MT, false, true><<<grid, 256, 0, stream>>>(a);
+}
+
+template <int D, bool F8>
+hipError_t run_shared(const SharedArgs& s, hipStream_t stream) {
+    const AttendArgs& a = s.own;
+    layout_kernel<<<1, kLayoutThreads, 0, stream>>>(s);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    if (s.chunks > 0) {
+        prefix_kernel<D, F8><<<(unsigned)s.chunks, 256, 0, stream>>>(s);
+        e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    const unsigned grid =
+        (unsigned)((int64_t)a.cache.n_kv_heads * a.n_req * a.slot_blocks * a.parts);
+    if (a.slot_tiles == 1) run_own<D, F8, 1>(a, grid, stream);
+    else if constexpr (D == 256) return hipErrorInvalidValue;  // AttendPlan takes one
+    else if (a.slot_tiles == 2) run_own<D, F8, 2>(a, grid, stream);
+    else run_own<D, F8, 4>(a, grid, stream);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    const int64_t total = (int64_t)a.n_req * (a.k_max + 1) * a.n_heads;
+    shared_join_kernel<D, F8><<<(unsigned)((total + 3) / 4), 256, 0, stream>>>(s);
+    return hipGetLastError();
+}
+
+template <int D>
+hipError_t run_shared_d(const SharedArgs& s, hipStream_t stream) {
+    return s.own.cache.dtype == SV_E4M3 ? run_shared<D, true>(s, stream)
+                                        : run_shared<D, false>(s, stream);
+}
+
+}  // namespace
+
+hipError_t launch_cache_attend_shared(const SharedArgs& a, hipStream_t stream) {
+    switch (a.own.cache.head_dim) {
+        case 64: return run_shared_d<64>(a, stream);
+        case 128: return run_shared_d<128>(a, stream);
+        default: return run_shared_d<256>(a, stream);
+    }
+}
+
+}  // namespace sv
