@@ -167,8 +167,7 @@ struct Prefix {
     static constexpr int kTile = 32;
     static constexpr int kLoads = D / 64;           // KB of 8 positions' keys, or values
     static constexpr int kGroup = kLoads * 1024;    // bytes
-    static constexpr int kKeys = 4 * kGroup;        // of a tile: a group a wave
-    static constexpr int kTileBytes = 2 * kKeys;
+    static constexpr int kKeys = 4 * kGroup;        // of a tile, or its values: a group a wave
     static constexpr int kSteps = D / 32;           // products of a score
     static constexpr int kDims = D / 16;            // 16-dim tiles of the output
     static constexpr int kEsize = F8 ? 1 : 2;
@@ -181,7 +180,8 @@ struct Prefix {
     static constexpr float kFull = 0x1p-6f, kRaise = 16.0f;
 
     struct Smem {
-        __attribute__((aligned(16))) char tiles[4][kTileBytes];
+        __attribute__((aligned(16))) char keys[3][kKeys];
+        __attribute__((aligned(16))) char values[4][kKeys];
         int64_t places[kPlaces];  // bytes to position begin + i at i % kPlaces
         // a byte a position of the tile: it is none
         __attribute__((aligned(4))) uint8_t absent[4][kTile];
@@ -194,7 +194,6 @@ template <int D, bool F8>
 __device__ __forceinline__ void prefix(const SharedArgs& s, int id,
                                        typename Prefix<D, F8>::Smem& sm) {
     using C = Prefix<D, F8>;
-    auto& tiles = sm.tiles;
     auto& places = sm.places;
     auto& absent = sm.absent;
     auto& holes = sm.holes;
@@ -263,7 +262,7 @@ __device__ __forceinline__ void prefix(const SharedArgs& s, int id,
     // as many at a time (a wait for a page id in registers would be a wait for the tiles
     // that are on their way).  -1: after the end, or on a page that is not there.
     auto fetch_places = [&](int from, int n) __attribute__((always_inline)) {
-        for (int i = threadIdx.x; i < n && from + i < end + 4 * C::kTile; i += 256) {
+        for (int i = threadIdx.x; i < n && from + i < end + 5 * C::kTile; i += 256) {
             const int t = from + i;
             int64_t place = -1;
             if (t < end) {
@@ -284,51 +283,54 @@ __device__ __forceinline__ void prefix(const SharedArgs& s, int id,
     };
     auto look_up = [&](int t0) { return places[(t0 + mine - begin) & (C::kPlaces - 1)]; };
     uint2 raw[F8 ? 2 * C::kLoads : 1];
-    // issues the loads of a tile
-    auto issue = [&](int buf, int64_t place) __attribute__((always_inline)) {
-        const bool there = place >= 0;
-        const char* k_from = (there ? k_base + place : reinterpret_cast<const char*>(kZeros)) + chunk_of;
-        const char* v_from = there ? k_from + v_from_k : k_from;
-        absent[buf][mine] = !there;
+    auto source = [&](int64_t place) __attribute__((always_inline)) {
+        return (place >= 0 ? k_base + place : reinterpret_cast<const char*>(kZeros)) + chunk_of;
+    };
+    // issues the loads of a tile's keys, or of its values
+    auto bring = [&](int64_t place, char* into, int keys) __attribute__((always_inline)) {
+        const char* from = source(place) + (keys || place < 0 ? 0 : v_from_k);
         if constexpr (F8) {
 #pragma unroll
-            for (int i = 0; i < C::kLoads; ++i) {
-                raw[i] = *reinterpret_cast<const uint2*>(k_from + i * 64);
-                raw[C::kLoads + i] = *reinterpret_cast<const uint2*>(v_from + i * 64);
-            }
+            for (int i = 0; i < C::kLoads; ++i)
+                raw[(keys ? 0 : C::kLoads) + i] = *reinterpret_cast<const uint2*>(from + i * 64);
         } else {
             const uint32_t to =
-                __builtin_amdgcn_readfirstlane(lds_address(tiles[buf] + wave * C::kGroup));
+                __builtin_amdgcn_readfirstlane(lds_address(into + wave * C::kGroup));
 #pragma unroll
-            for (int i = 0; i < C::kLoads; ++i) {
-                load_to_lds<128>(k_from, to + i * 1024, i);
-                load_to_lds<128>(v_from, to + C::kKeys + i * 1024, i);
-            }
+            for (int i = 0; i < C::kLoads; ++i) load_to_lds<128>(from, to + i * 1024, i);
         }
     };
-    // the tile of this turn has arrived: an 8-bit one goes into LDS as bf16
-    auto settle = [&](int buf) __attribute__((always_inline)) {
+    // 8-bit ones pass registers and go into LDS as bf16
+    auto widen = [&](char* into, int keys) __attribute__((always_inline)) {
         if constexpr (F8) {
 #pragma unroll
-            for (int i = 0; i < 2 * C::kLoads; ++i) {
-                char* to = tiles[buf] + (i < C::kLoads ? 0 : C::kKeys) + wave * C::kGroup +
-                           (i % C::kLoads) * 1024 + lane * 16;
-                *reinterpret_cast<uint4*>(to) =
-                    make_uint4(e4m3_pair<false>(raw[i].x), e4m3_pair<true>(raw[i].x),
-                               e4m3_pair<false>(raw[i].y), e4m3_pair<true>(raw[i].y));
+            for (int i = 0; i < C::kLoads; ++i) {
+                const uint2 w = raw[(keys ? 0 : C::kLoads) + i];
+                *reinterpret_cast<uint4*>(into + wave * C::kGroup + i * 1024 + lane * 16) =
+                    make_uint4(e4m3_pair<false>(w.x), e4m3_pair<true>(w.x),
+                               e4m3_pair<false>(w.y), e4m3_pair<true>(w.y));
             }
-        } else {
-            // all but the tile behind it
-            asm volatile("s_waitcnt vmcnt(%0)" : : "n"(2 * C::kLoads) : "memory");
         }
     };
 
     __syncthreads();  // the segment before has been read
     fetch_places(begin, C::kPlaces);
     __syncthreads();
-    issue(0, look_up(begin));
-    if (!F8) issue(1, look_up(begin + C::kTile));
-    int64_t place = look_up(begin + (F8 ? 1 : 2) * C::kTile);
+    // places of tile t's keys and of its values; bf16: the keys of tiles 0 .. 2 and the
+    // values of 0 and 1, 8 bits: the keys of 0
+    int64_t place_k = look_up(begin), place_v;
+    bring(place_k, sm.keys[0], 1);
+    absent[0][mine] = place_k < 0;
+    if (!F8) {
+#pragma unroll
+        for (int t = 1; t < 3; ++t) {
+            place_v = place_k;
+            place_k = look_up(begin + t * C::kTile);
+            absent[t][mine] = place_k < 0;
+            bring(place_k, sm.keys[t], 1);
+            bring(place_v, sm.values[t - 1], 0);
+        }
+    }
 
     // ---- queries of the wave's slots, operand B of every step
     int row[2], head[2];
@@ -387,7 +389,7 @@ __device__ __forceinline__ void prefix(const SharedArgs& s, int id,
         const int pos = 4 * g + (col >> 2);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            v_at[j] = C::kKeys + (pos >> 3) * C::kGroup + (pos & 7) * 128 + (lane & 1) * 8 +
+            v_at[j] = (pos >> 3) * C::kGroup + (pos & 7) * 128 + (lane & 1) * 8 +
                       ((2 * j + ((lane >> 1) & 1)) ^ swizzle(pos)) * 16;
     }
 
@@ -406,49 +408,50 @@ __device__ __forceinline__ void prefix(const SharedArgs& s, int id,
         return as_bf16x8(w0.x, w0.y, w1.x, w1.y);
     };
     constexpr int kValuesAhead = 4;
-    // One turn: the scores of tile t, then its weights between the products of tile
-    // t - 1's with their values (BEHIND: there is one).
+    // the keys of a tile, operand A of every step
+    bf16x8 k8[C::kSteps][2];
+    auto key = [&](const char* tile, int i) __attribute__((always_inline)) {
+        const int st = i >> 1, ph = i & 1;
+        const uint4 w = *reinterpret_cast<const uint4*>(tile + k_at[st & 1] + (st >> 1) * 1024 +
+                                                        ph * 2 * C::kGroup);
+        k8[st][ph] = as_bf16x8(w.x, w.y, w.z, w.w);
+    };
+    if constexpr (F8) {
+        widen(sm.keys[0], 1);
+        place_v = place_k;
+        place_k = look_up(begin + C::kTile);
+        absent[1][mine] = place_k < 0;
+        bring(place_k, nullptr, 1);
+        bring(place_v, nullptr, 0);
+    } else {
+        asm volatile("s_waitcnt vmcnt(%0)" : : "n"(4 * C::kLoads) : "memory");
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 2 * C::kSteps; ++i) key(sm.keys[0], i);
+    place_v = place_k;
+    place_k = look_up(begin + (F8 ? 2 : 3) * C::kTile);
+    int in_keys = 1;  // of three: where the keys of tile t + 1 are
+    // One turn: the scores of tile t, whose keys are in registers, then its weights between
+    // the products of tile t - 1's with their values (BEHIND: there is one) and the loads
+    // of the next tile's keys.  Behind the turn's only barrier the keys of t + 1 and the
+    // values of t - 1 are in LDS, and the room of the keys of t and the values of t - 2 is
+    // free.
     auto turn = [&](auto behind, int t0) __attribute__((always_inline)) {
         constexpr bool kBehind = decltype(behind)::value;
         const int buf = ((t0 - begin) / C::kTile) & 3;
-        settle(buf);
-        __syncthreads();
-        issue((buf + (F8 ? 1 : 2)) & 3, place);
-        place = look_up(t0 + (F8 ? 2 : 3) * C::kTile);
-        if (kBehind && ((t0 - begin) & (C::kPlaces / 2 - 1)) == 0)
-            fetch_places(t0 + C::kPlaces / 2, C::kPlaces / 2);
-        const char* tile = tiles[buf];
-        const char* tile_behind = tiles[(buf + 3) & 3];
-
         // scores: both 16 positions of a step, two slots' products each
         f32x4 sc[2][2];
 #pragma unroll
         for (int i = 0; i < 4; ++i) sc[i >> 1][i & 1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        constexpr int kAhead = C::kSteps < 3 ? C::kSteps : 3;
-        bf16x8 k8[kAhead][2], v8[kValuesAhead];
-        auto key = [&](int st, int ph) __attribute__((always_inline)) {
-            const uint4 w = *reinterpret_cast<const uint4*>(tile + k_at[st & 1] + (st >> 1) * 1024 +
-                                                            ph * 2 * C::kGroup);
-            return as_bf16x8(w.x, w.y, w.z, w.w);
-        };
 #pragma unroll
-        for (int st = 0; st < kAhead; ++st)
-#pragma unroll
-            for (int ph = 0; ph < 2; ++ph) k8[st][ph] = key(st, ph);
-#pragma unroll
-        for (int st = 0; st < C::kSteps; ++st) {
+        for (int st = 0; st < C::kSteps; ++st)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 sc[i >> 1][i & 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                    k8[st % kAhead][i >> 1], q[st][i & 1], sc[i >> 1][i & 1], 0, 0, 0);
-#pragma unroll
-            for (int ph = 0; ph < 2; ++ph)
-                if (st + kAhead < C::kSteps) k8[st % kAhead][ph] = key(st + kAhead, ph);
-            __builtin_amdgcn_sched_barrier(0);
-        }
-        if (kBehind)
-#pragma unroll
-            for (int i = 0; i < kValuesAhead; ++i) v8[i] = value(tile_behind, i);
+                    k8[st][i >> 1], q[st][i & 1], sc[i >> 1][i & 1], 0, 0, 0);
+        const bool masked =
+            t0 + C::kTile > end || __builtin_amdgcn_readfirstlane(holes) != 0;
         float p[2][8];  // of a slot: positions 4 g .. of the first 16, of the second
 #pragma unroll
         for (int sh = 0; sh < 2; ++sh)
@@ -460,7 +463,7 @@ __device__ __forceinline__ void prefix(const SharedArgs& s, int id,
 #pragma unroll
                 for (int e = 0; e < 8; ++e) p[sh][e] *= sign;
         }
-        if (t0 + C::kTile > end || __builtin_amdgcn_readfirstlane(holes) != 0) {
+        if (masked) {
 #pragma unroll
             for (int ph = 0; ph < 2; ++ph) {
                 const uint32_t no =
@@ -513,6 +516,34 @@ __device__ __forceinline__ void prefix(const SharedArgs& s, int id,
                 }
             }
         }
+        const char* values_behind = sm.values[(buf + 3) & 3];
+        const char* next_keys = sm.keys[in_keys];
+        if constexpr (F8) {
+            widen(sm.keys[in_keys], 1);
+            widen(sm.values[buf], 0);
+        } else {
+            // all but the values of t, the keys of t + 2 and the values of t + 1
+            asm volatile("s_waitcnt vmcnt(%0)" : : "n"(3 * C::kLoads) : "memory");
+        }
+        __syncthreads();
+        bf16x8 v8[kValuesAhead];
+        if (kBehind)
+#pragma unroll
+            for (int i = 0; i < kValuesAhead; ++i) v8[i] = value(values_behind, i);
+        in_keys = in_keys == 2 ? 0 : in_keys + 1;
+        if constexpr (F8) {
+            bring(place_k, nullptr, 1);
+            bring(place_v, nullptr, 0);
+            absent[(buf + 2) & 3][mine] = place_k < 0;
+        } else {
+            bring(place_k, sm.keys[in_keys == 2 ? 0 : in_keys + 1], 1);
+            bring(place_v, sm.values[(buf + 2) & 3], 0);
+            absent[(buf + 3) & 3][mine] = place_k < 0;
+        }
+        place_v = place_k;
+        place_k = look_up(t0 + (F8 ? 3 : 4) * C::kTile);
+        if (kBehind && ((t0 - begin) & (C::kPlaces / 2 - 1)) == 0)
+            fetch_places(t0 + C::kPlaces / 2, C::kPlaces / 2);
         uint32_t new_hi[2][4], new_rest[2][4];
         constexpr float kOneUp = 1.0f + 0x1p-23f;
         // word w of the eight: a quarter of its work at a time
@@ -554,11 +585,14 @@ __device__ __forceinline__ void prefix(const SharedArgs& s, int id,
                     __builtin_amdgcn_sched_barrier(0);
                 }
                 if (i + kValuesAhead < C::kDims)
-                    v8[i % kValuesAhead] = value(tile_behind, i + kValuesAhead);
+                    v8[i % kValuesAhead] = value(values_behind, i + kValuesAhead);
+                key(next_keys, i);  // kDims = 2 kSteps of them
             }
         } else {
 #pragma unroll
             for (int k = 0; k < 32; ++k) weigh(k >> 2, k & 3);
+#pragma unroll
+            for (int i = 0; i < 2 * C::kSteps; ++i) key(next_keys, i);
         }
 #pragma unroll
         for (int sh = 0; sh < 2; ++sh)
@@ -580,7 +614,11 @@ __device__ __forceinline__ void prefix(const SharedArgs& s, int id,
     }
     // the last tile's weights
     {
-        const char* tile = tiles[((end - 1 - begin) / C::kTile) & 3];
+        if constexpr (!F8) {
+            __builtin_amdgcn_s_waitcnt(0);  // its values, the last that were on their way
+            __syncthreads();
+        }
+        const char* tile = sm.values[((end - 1 - begin) / C::kTile) & 3];
         const bf16x8 pb[2] = {as_bf16x8(hi_w[0][0], hi_w[0][1], hi_w[0][2], hi_w[0][3]),
                               as_bf16x8(hi_w[1][0], hi_w[1][1], hi_w[1][2], hi_w[1][3])};
         const bf16x8 pr[2] = {as_bf16x8(rest_w[0][0], rest_w[0][1], rest_w[0][2], rest_w[0][3]),
@@ -598,8 +636,6 @@ __device__ __forceinline__ void prefix(const SharedArgs& s, int id,
             __builtin_amdgcn_sched_barrier(0);
         }
     }
-    __builtin_amdgcn_s_waitcnt(0);  // nothing is on its way to LDS when it is used anew
-
 #pragma unroll
     for (int sh = 0; sh < 2; ++sh) {
         l[sh] += __shfl_xor(l[sh], 16);
