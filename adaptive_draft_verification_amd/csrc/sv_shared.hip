@@ -13,6 +13,7 @@ namespace sv {
 namespace {
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 // ------------------------------------------------------------------- layout
 
@@ -140,19 +141,18 @@ __global__ __launch_bounds__(kLayoutThreads) void layout_kernel(SharedArgs s) {
 //
 // A group's query slots of one kv head are its rows times the G query heads that
 // share it (slot i: row i / G, head h G + i % G): all of them see the whole prefix.
-// A workgroup of four waves takes 128 slots over one part of it, 32 positions at a
-// time, whose keys and values lie in LDS as bf16; a wave takes 32 slots.  Operands of
-// v_mfma_f32_16x16x32_bf16:
-//   S^T = K Q^T: A holds 16 positions (lane % 16) by 32 dims (8 for each g = lane /
-//   16), B 16 slots by the same dims, so a lane ends with the scores of ONE slot
-//   (lane % 16) at positions 4 g .. 4 g + 3 of each 16;
-//   O^T = V^T P^T: B's lane holds 8 positions of one slot, 4 g .. of either 16, just as
-//   the scores are; A needs the same positions of one dim a lane: two transposing LDS
-//   reads of 4 positions by 16 dims for each 16 lanes.
-// Bound by products and the softmax beside them: at 128 dims 48 products (768 clocks)
-// and some 130 other instructions a wave and tile, two waves a SIMD (one at 256 dims).
-// Tiles come two turns ahead (8-bit ones, which pass registers, one), into one of
-// three places, so that one barrier a tile is enough.
+// A workgroup of four waves takes 128 slots over a run of tiles of 32 positions, whose
+// keys and values lie in LDS as bf16; a wave takes 32 slots.  Operands of
+// v_mfma_f32_32x32x16_bf16:
+//   S^T = K Q^T: A holds 32 positions (lane % 32) by 16 dims (8 for each g = lane / 32),
+//   B 32 slots by the same dims, so a lane ends with 16 scores of ONE slot (lane % 32),
+//   at positions 4 g .. 4 g + 3 of each 8;
+//   O^T = V^T P^T: B's lane holds 8 positions of its slot, 4 g .. of two eights, just as
+//   the scores are; A needs the same positions of one dim (lane % 32): two transposing
+//   LDS reads of 4 positions by 16 dims for each 16 lanes.
+// What bounds it: at 128 dims 24 products of 32 clocks a wave and tile, and on the same
+// issue port some 105 other instructions of 4 clocks (exp2 8), beside which a product
+// takes 8 (measured; one of 16 x 16 x 32, of half the work, as many).
 // In LDS 8 positions by 8 chunks of 16 bytes are a KB, the chunk c of position x at
 // (c ^ swizzle(x)) of its 128 bytes.  LDS has 64 banks of 4 bytes: the chunk c of 16
 // neighbouring positions, and the chunks c and c ^ 1 of 8, lie in different ones.
@@ -164,14 +164,14 @@ __device__ const uint4 kZeros[256 / 8] = {};
 
 template <int D, bool F8>
 struct Prefix {
-    static constexpr int kTile = 32;
+    static constexpr int kTile = SharedPlan::kTile;
     static constexpr int kLoads = D / 64;           // KB of 8 positions' keys, or values
     static constexpr int kGroup = kLoads * 1024;    // bytes
-    static constexpr int kKeys = 4 * kGroup;        // of a tile, or its values: a group a wave
-    static constexpr int kSteps = D / 32;           // products of a score
-    static constexpr int kDims = D / 16;            // 16-dim tiles of the output
+    static constexpr int kBytes = 4 * kGroup;       // of a tile's keys, or values: a group a wave
+    static constexpr int kSteps = D / 16;           // products of a score
+    static constexpr int kDims = D / 32;            // 32-dim tiles of the output
     static constexpr int kEsize = F8 ? 1 : 2;
-    static constexpr int kPlaces = 1024;            // positions whose places are in LDS
+    static constexpr int kPlaces = 512;             // positions whose places are in LDS
     static constexpr int kOccupancy = D < 256 ? 2 : 1;
     // Weights are held as attend_kernel holds them: 2^(score - m), m kHold above the
     // maximum that it was set from, raised where a score passes that by 2^8 or a lane's
@@ -180,11 +180,13 @@ struct Prefix {
     static constexpr float kFull = 0x1p-6f, kRaise = 16.0f;
 
     struct Smem {
-        __attribute__((aligned(16))) char keys[3][kKeys];
-        __attribute__((aligned(16))) char values[4][kKeys];
-        int64_t places[kPlaces];  // bytes to position begin + i at i % kPlaces
-        // a byte a position of the tile: it is none
-        __attribute__((aligned(4))) uint8_t absent[4][kTile];
+        __attribute__((aligned(16))) char keys[3][kBytes];
+        __attribute__((aligned(16))) char values[4][kBytes];
+        // of position begin + i at i % kPlaces: where its key and its value are, and
+        // whether there is none
+        const char* key_at[kPlaces];
+        const char* value_at[kPlaces];
+        __attribute__((aligned(4))) uint8_t absent[kPlaces];
         int holes;  // a position before the end is none
     };
 };
@@ -194,14 +196,11 @@ template <int D, bool F8>
 __device__ __forceinline__ void prefix(const SharedArgs& s, int id,
                                        typename Prefix<D, F8>::Smem& sm) {
     using C = Prefix<D, F8>;
-    auto& places = sm.places;
-    auto& absent = sm.absent;
-    auto& holes = sm.holes;
     const AttendArgs& a = s.own;
     const sv_cache& c = a.cache;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int col = lane & 15, g = lane >> 4;
+    const int col = lane & 31, g = lane >> 5;
     // consecutive runs of tiles (they read the same keys and values) to one XCD: every
     // eighth workgroup
     const SharedTotals totals = *s.totals;
@@ -223,434 +222,403 @@ __device__ __forceinline__ void prefix(const SharedArgs& s, int id,
         group += skip;
         n = min(step, n - skip);
     }
-    bool bad = false;
-    if (threadIdx.x == 0) holes = 0;
-    // ---- the run's segments
-    while (tile < to_tile) {
-    if (in_head == head_tiles) {
-        in_head = 0;
-        group = 0;
-        ++h;
-    }
-    while (s.group[group + 1].tile <= in_head) ++group;
-    const int from_req = s.group_start[group], to_req = s.group_start[group + 1];
-    const int P = s.prefix_len[group];
-    const int lo = a.cu_rows[from_req];
-    const int block_tiles = (int)(((int64_t)P + C::kTile - 1) / C::kTile);
-    const int64_t in_group = in_head - s.group[group].tile;
-    const int index = (int)((uint64_t)in_group / (uint32_t)block_tiles);  // the block's
-    const int first_tile = (int)(in_group - (int64_t)index * block_tiles);
-    const int n_tiles = (int)min((int64_t)(block_tiles - first_tile), to_tile - tile);
-    const int64_t block_id = (int64_t)h * head_blocks + s.group[group].block + index;
-    const int slots = (a.cu_rows[to_req] - lo) * a.group - index * SharedPlan::kSlots;
-    const int begin = first_tile * C::kTile;
-    const int end = min(P, begin + n_tiles * C::kTile);
-    if (threadIdx.x == 0) {
-        if (first_tile == 0) s.span[block_id].first = chunk;
-        if (first_tile + n_tiles == block_tiles) s.span[block_id].last = chunk;
-    }
-    tile += n_tiles;
-    in_head += n_tiles;
-
-    // ---- keys' and values' way into LDS: wave w brings positions 8 w .. of a tile
-    const int32_t* table = a.page_table + (int64_t)from_req * a.max_pages;
+    // where a lane reads keys: chunk 2 st + g of its position, st = 0 .. 3 of 128 bytes;
+    // and values: 4 positions by 16 dims for 16 lanes, in the first or second 8 positions,
+    // of either 32 dims
+    int k_at[4], v_at[2][2];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        k_at[j] = (col >> 3) * C::kGroup + (col & 7) * 128 + ((2 * j + g) ^ swizzle(col)) * 16;
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int pos = 8 * r + 4 * g + ((lane & 15) >> 2);
+            const int ch = 4 * j + 2 * ((lane >> 4) & 1) + ((lane >> 1) & 1);
+            v_at[r][j] = (pos >> 3) * C::kGroup + (pos & 7) * 128 + (lane & 1) * 8 +
+                         (ch ^ swizzle(pos)) * 16;
+        }
+    // keys' and values' way into LDS: wave w brings positions 8 w .. of a tile
     const int mine = wave * 8 + (lane >> 3);
     const int chunk_of = ((lane & 7) ^ swizzle(mine)) * 8 * C::kEsize;
-    const char* k_base = static_cast<const char*>(c.k) + (int64_t)h * c.head_stride * C::kEsize;
-    const int64_t v_from_k = static_cast<const char*>(c.v) - static_cast<const char*>(c.k);
-    // The places of `n` positions from `from` on, into LDS: kPlaces at first, then half
-    // as many at a time (a wait for a page id in registers would be a wait for the tiles
-    // that are on their way).  -1: after the end, or on a page that is not there.
-    auto fetch_places = [&](int from, int n) __attribute__((always_inline)) {
-        for (int i = threadIdx.x; i < n && from + i < end + 5 * C::kTile; i += 256) {
-            const int t = from + i;
-            int64_t place = -1;
-            if (t < end) {
-                const int in = a.page_shift >= 0 ? t >> a.page_shift
-                                                 : (int)((unsigned)t / (unsigned)c.page_size);
-                const int page = table[in];
-                if (page >= 0 && page < c.n_pages) {
-                    place = ((int64_t)page * c.page_stride +
-                             (int64_t)(t - in * c.page_size) * c.token_stride) *
+    bool bad = false;
+    if (threadIdx.x == 0) sm.holes = 0;
+
+    // ---- the run's segments
+    while (tile < to_tile) {
+        if (in_head == head_tiles) {
+            in_head = 0;
+            group = 0;
+            ++h;
+        }
+        while (s.group[group + 1].tile <= in_head) ++group;
+        const int from_req = s.group_start[group], to_req = s.group_start[group + 1];
+        const int P = s.prefix_len[group];
+        const int lo = a.cu_rows[from_req];
+        const int block_tiles = (int)(((int64_t)P + C::kTile - 1) / C::kTile);
+        const int64_t in_group = in_head - s.group[group].tile;
+        const int index = (int)((uint64_t)in_group / (uint32_t)block_tiles);  // the block's
+        const int first_tile = (int)(in_group - (int64_t)index * block_tiles);
+        const int n_tiles = (int)min((int64_t)(block_tiles - first_tile), to_tile - tile);
+        const int64_t block_id = (int64_t)h * head_blocks + s.group[group].block + index;
+        const int slots = (a.cu_rows[to_req] - lo) * a.group - index * SharedPlan::kSlots;
+        const int begin = first_tile * C::kTile;
+        const int end = min(P, begin + n_tiles * C::kTile);
+        if (threadIdx.x == 0) {
+            if (first_tile == 0) s.span[block_id].first = chunk;
+            if (first_tile + n_tiles == block_tiles) s.span[block_id].last = chunk;
+        }
+        tile += n_tiles;
+        in_head += n_tiles;
+
+        // The places of `n` positions from `from` on, into LDS: kPlaces at first, then
+        // half as many at a time (a wait for a page id in registers would be a wait for
+        // the tiles that are on their way).  None: after the end, or on a page that is
+        // not there.
+        const int32_t* table = a.page_table + (int64_t)from_req * a.max_pages;
+        const int64_t of_head = (int64_t)h * c.head_stride * C::kEsize;
+        const char* k_base = static_cast<const char*>(c.k) + of_head;
+        const char* v_base = static_cast<const char*>(c.v) + of_head;
+        auto fetch_places = [&](int from, int n) __attribute__((always_inline)) {
+            for (int i = threadIdx.x; i < n; i += 256) {
+                // (positions past the last ones looked up are not reached: no overflow)
+                const int64_t t = (int64_t)from + i;
+                const char *k = reinterpret_cast<const char*>(kZeros), *v = k;
+                bool none = true;
+                if (t < end) {
+                    const int in = a.page_shift >= 0
+                                       ? (int)t >> a.page_shift
+                                       : (int)((unsigned)t / (unsigned)c.page_size);
+                    const int page = table[in];
+                    if (page >= 0 && page < c.n_pages) {
+                        const int64_t place =
+                            ((int64_t)page * c.page_stride +
+                             (int64_t)((int)t - in * c.page_size) * c.token_stride) *
                             C::kEsize;
-                } else {
-                    bad = true;
-                    holes = 1;
-                }
-            }
-            places[(t - begin) & (C::kPlaces - 1)] = place;
-        }
-    };
-    auto look_up = [&](int t0) { return places[(t0 + mine - begin) & (C::kPlaces - 1)]; };
-    uint2 raw[F8 ? 2 * C::kLoads : 1];
-    auto source = [&](int64_t place) __attribute__((always_inline)) {
-        return (place >= 0 ? k_base + place : reinterpret_cast<const char*>(kZeros)) + chunk_of;
-    };
-    // issues the loads of a tile's keys, or of its values
-    auto bring = [&](int64_t place, char* into, int keys) __attribute__((always_inline)) {
-        const char* from = source(place) + (keys || place < 0 ? 0 : v_from_k);
-        if constexpr (F8) {
-#pragma unroll
-            for (int i = 0; i < C::kLoads; ++i)
-                raw[(keys ? 0 : C::kLoads) + i] = *reinterpret_cast<const uint2*>(from + i * 64);
-        } else {
-            const uint32_t to =
-                __builtin_amdgcn_readfirstlane(lds_address(into + wave * C::kGroup));
-#pragma unroll
-            for (int i = 0; i < C::kLoads; ++i) load_to_lds<128>(from, to + i * 1024, i);
-        }
-    };
-    // 8-bit ones pass registers and go into LDS as bf16
-    auto widen = [&](char* into, int keys) __attribute__((always_inline)) {
-        if constexpr (F8) {
-#pragma unroll
-            for (int i = 0; i < C::kLoads; ++i) {
-                const uint2 w = raw[(keys ? 0 : C::kLoads) + i];
-                *reinterpret_cast<uint4*>(into + wave * C::kGroup + i * 1024 + lane * 16) =
-                    make_uint4(e4m3_pair<false>(w.x), e4m3_pair<true>(w.x),
-                               e4m3_pair<false>(w.y), e4m3_pair<true>(w.y));
-            }
-        }
-    };
-
-    __syncthreads();  // the segment before has been read
-    fetch_places(begin, C::kPlaces);
-    __syncthreads();
-    // places of tile t's keys and of its values; bf16: the keys of tiles 0 .. 2 and the
-    // values of 0 and 1, 8 bits: the keys of 0
-    int64_t place_k = look_up(begin), place_v;
-    bring(place_k, sm.keys[0], 1);
-    absent[0][mine] = place_k < 0;
-    if (!F8) {
-#pragma unroll
-        for (int t = 1; t < 3; ++t) {
-            place_v = place_k;
-            place_k = look_up(begin + t * C::kTile);
-            absent[t][mine] = place_k < 0;
-            bring(place_k, sm.keys[t], 1);
-            bring(place_v, sm.values[t - 1], 0);
-        }
-    }
-
-    // ---- queries of the wave's slots, operand B of every step
-    int row[2], head[2];
-    bool live[2];
-    bf16x8 q[C::kSteps][2];
-#pragma unroll
-    for (int sh = 0; sh < 2; ++sh) {
-        const int i = wave * 32 + sh * 16 + col, slot = index * SharedPlan::kSlots + i;
-        live[sh] = i < slots;
-        row[sh] = (int)((unsigned)slot / (unsigned)a.group);
-        head[sh] = h * a.group + slot - row[sh] * a.group;
-        // a slot that is not there takes the block's first one's
-        const int first = index * SharedPlan::kSlots;
-        const int q_row = live[sh] ? row[sh] : first / a.group;
-        const int q_head = live[sh] ? head[sh] : h * a.group + first % a.group;
-        const uint16_t* qp = static_cast<const uint16_t*>(a.q) + (int64_t)(lo + q_row) * a.q_ld +
-                             (int64_t)q_head * D + g * 8;
-#pragma unroll
-        for (int st = 0; st < C::kSteps; ++st) {
-            const uint4 w = *reinterpret_cast<const uint4*>(qp + st * 32);
-            q[st][sh] = as_bf16x8(w.x, w.y, w.z, w.w);
-        }
-    }
-    // waited for here, not among the loads of a tile
-#pragma unroll
-    for (int st = 0; st < C::kSteps; ++st)
-        asm volatile("" : "+v"(q[st][0]), "+v"(q[st][1]));
-    // The scale is taken as positive (products change their sign with it), so that the
-    // largest product is the largest score and a masked -inf stays one; 0 as 1 of
-    // products that are 0.
-    const float signed_scale =
-        a.scale * kLog2e * (F8 && c.k_scale != nullptr ? c.k_scale[h] : 1.0f);
-    const float scale = signed_scale == 0.0f ? 1.0f : fabsf(signed_scale);
-    const float sign = signed_scale == 0.0f ? 0.0f : signed_scale < 0.0f ? -1.0f : 1.0f;
-
-    f32x4 acc[C::kDims][2];
-#pragma unroll
-    for (int i = 0; i < C::kDims; ++i)
-#pragma unroll
-        for (int sh = 0; sh < 2; ++sh) acc[i][sh] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    // m (-inf: no score yet), the m used, the product from which m is raised, a lane's sum
-    float m[2], mu[2], far[2], l[2];
-#pragma unroll
-    for (int sh = 0; sh < 2; ++sh) {
-        m[sh] = far[sh] = -kInf;
-        mu[sh] = l[sh] = 0.0f;
-    }
-
-    // where a lane reads keys: chunks 4 st + g of its position of either 16, st = 0, 1 of
-    // 128 bytes; and values: 4 positions by 16 dims for 16 lanes, tiles 0 .. 3 of them
-    int k_at[2], v_at[4];
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-        k_at[j] = (col >> 3) * C::kGroup + (col & 7) * 128 + ((4 * j + g) ^ swizzle(col)) * 16;
-    {
-        const int pos = 4 * g + (col >> 2);
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            v_at[j] = (pos >> 3) * C::kGroup + (pos & 7) * 128 + (lane & 1) * 8 +
-                      ((2 * j + ((lane >> 1) & 1)) ^ swizzle(pos)) * 16;
-    }
-
-    // The weights that are not yet multiplied with their values, as two bf16 terms (see
-    // attend_kernel): word i of slot sh is positions 4 g + 2 (i % 2) .. of 16 (i / 2).
-    uint32_t hi_w[2][4] = {}, rest_w[2][4] = {};
-    auto value = [&](const char* tile, int i) __attribute__((always_inline)) {
-        const char* at = tile + v_at[i & 3] + (i >> 2) * 1024;
-        const s16x4 x0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-            (__attribute__((address_space(3))) s16x4*)at);
-        const s16x4 x1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-            (__attribute__((address_space(3))) s16x4*)(at + 2 * C::kGroup));
-        uint2 w0, w1;
-        __builtin_memcpy(&w0, &x0, 8);
-        __builtin_memcpy(&w1, &x1, 8);
-        return as_bf16x8(w0.x, w0.y, w1.x, w1.y);
-    };
-    constexpr int kValuesAhead = 4;
-    // the keys of a tile, operand A of every step
-    bf16x8 k8[C::kSteps][2];
-    auto key = [&](const char* tile, int i) __attribute__((always_inline)) {
-        const int st = i >> 1, ph = i & 1;
-        const uint4 w = *reinterpret_cast<const uint4*>(tile + k_at[st & 1] + (st >> 1) * 1024 +
-                                                        ph * 2 * C::kGroup);
-        k8[st][ph] = as_bf16x8(w.x, w.y, w.z, w.w);
-    };
-    if constexpr (F8) {
-        widen(sm.keys[0], 1);
-        place_v = place_k;
-        place_k = look_up(begin + C::kTile);
-        absent[1][mine] = place_k < 0;
-        bring(place_k, nullptr, 1);
-        bring(place_v, nullptr, 0);
-    } else {
-        asm volatile("s_waitcnt vmcnt(%0)" : : "n"(4 * C::kLoads) : "memory");
-    }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 2 * C::kSteps; ++i) key(sm.keys[0], i);
-    place_v = place_k;
-    place_k = look_up(begin + (F8 ? 2 : 3) * C::kTile);
-    int in_keys = 1;  // of three: where the keys of tile t + 1 are
-    // One turn: the scores of tile t, whose keys are in registers, then its weights between
-    // the products of tile t - 1's with their values (BEHIND: there is one) and the loads
-    // of the next tile's keys.  Behind the turn's only barrier the keys of t + 1 and the
-    // values of t - 1 are in LDS, and the room of the keys of t and the values of t - 2 is
-    // free.
-    auto turn = [&](auto behind, int t0) __attribute__((always_inline)) {
-        constexpr bool kBehind = decltype(behind)::value;
-        const int buf = ((t0 - begin) / C::kTile) & 3;
-        // scores: both 16 positions of a step, two slots' products each
-        f32x4 sc[2][2];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) sc[i >> 1][i & 1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int st = 0; st < C::kSteps; ++st)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                sc[i >> 1][i & 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                    k8[st][i >> 1], q[st][i & 1], sc[i >> 1][i & 1], 0, 0, 0);
-        const bool masked =
-            t0 + C::kTile > end || __builtin_amdgcn_readfirstlane(holes) != 0;
-        float p[2][8];  // of a slot: positions 4 g .. of the first 16, of the second
-#pragma unroll
-        for (int sh = 0; sh < 2; ++sh)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) p[sh][e] = sc[e >> 2][sh][e & 3];
-        if (sign != 1.0f) {
-#pragma unroll
-            for (int sh = 0; sh < 2; ++sh)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) p[sh][e] *= sign;
-        }
-        if (masked) {
-#pragma unroll
-            for (int ph = 0; ph < 2; ++ph) {
-                const uint32_t no =
-                    *reinterpret_cast<const uint32_t*>(&absent[buf][ph * 16 + 4 * g]);
-#pragma unroll
-                for (int sh = 0; sh < 2; ++sh)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if ((no >> (8 * e)) & 1) p[sh][ph * 4 + e] = -kInf;
-            }
-        }
-        float mx[2];
-#pragma unroll
-        for (int sh = 0; sh < 2; ++sh) {
-            mx[sh] = p[sh][0];
-#pragma unroll
-            for (int e = 1; e < 8; ++e) mx[sh] = fmaxf(mx[sh], p[sh][e]);
-        }
-        // in the first tile, and hardly ever later
-        bool raise = mx[0] > far[0] || mx[1] > far[1];
-        if (!F8) raise = raise || fmaxf(l[0], l[1]) > C::kFull;
-        if (__ballot(raise) != 0) {
-#pragma unroll
-            for (int sh = 0; sh < 2; ++sh) {
-                float top = fmaxf(mx[sh], __shfl_xor(mx[sh], 16));
-                top = fmaxf(top, __shfl_xor(top, 32));
-                float to = fmaxf(m[sh], ceilf(top * scale) + C::kHold);
-                if (!F8) {
-                    float most = fmaxf(l[sh], __shfl_xor(l[sh], 16));
-                    most = fmaxf(most, __shfl_xor(most, 32));
-                    if (most > C::kFull) to += C::kRaise;
-                }
-                if (to > m[sh]) {
-                    // m = -inf: 0; else a power of two, as m is an integer
-                    const float f = fast_exp2(m[sh] - to);
-                    if (kBehind) {
-#pragma unroll
-                        for (int i = 0; i < C::kDims; ++i) acc[i][sh] *= f;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            hi_w[sh][i] = pack_bf16(bf16_lo(hi_w[sh][i]) * f,
-                                                    bf16_hi(hi_w[sh][i]) * f);
-                            rest_w[sh][i] = pack_bf16(bf16_lo(rest_w[sh][i]) * f,
-                                                      bf16_hi(rest_w[sh][i]) * f);
-                        }
+                        k = k_base + place;
+                        v = v_base + place;
+                        none = false;
+                    } else {
+                        bad = true;
+                        sm.holes = 1;
                     }
-                    l[sh] *= f;
-                    m[sh] = mu[sh] = to;
-                    far[sh] = (to - C::kHold + C::kSlack) / scale;
                 }
-            }
-        }
-        const char* values_behind = sm.values[(buf + 3) & 3];
-        const char* next_keys = sm.keys[in_keys];
-        if constexpr (F8) {
-            widen(sm.keys[in_keys], 1);
-            widen(sm.values[buf], 0);
-        } else {
-            // all but the values of t, the keys of t + 2 and the values of t + 1
-            asm volatile("s_waitcnt vmcnt(%0)" : : "n"(3 * C::kLoads) : "memory");
-        }
-        __syncthreads();
-        bf16x8 v8[kValuesAhead];
-        if (kBehind)
-#pragma unroll
-            for (int i = 0; i < kValuesAhead; ++i) v8[i] = value(values_behind, i);
-        in_keys = in_keys == 2 ? 0 : in_keys + 1;
-        if constexpr (F8) {
-            bring(place_k, nullptr, 1);
-            bring(place_v, nullptr, 0);
-            absent[(buf + 2) & 3][mine] = place_k < 0;
-        } else {
-            bring(place_k, sm.keys[in_keys == 2 ? 0 : in_keys + 1], 1);
-            bring(place_v, sm.values[(buf + 2) & 3], 0);
-            absent[(buf + 3) & 3][mine] = place_k < 0;
-        }
-        place_v = place_k;
-        place_k = look_up(t0 + (F8 ? 3 : 4) * C::kTile);
-        if (kBehind && ((t0 - begin) & (C::kPlaces / 2 - 1)) == 0)
-            fetch_places(t0 + C::kPlaces / 2, C::kPlaces / 2);
-        uint32_t new_hi[2][4], new_rest[2][4];
-        constexpr float kOneUp = 1.0f + 0x1p-23f;
-        // word w of the eight: a quarter of its work at a time
-        auto weigh = [&](int w, int part) __attribute__((always_inline)) {
-            const int sh = w >> 2, i = w & 3;
-            float &x = p[sh][2 * i], &y = p[sh][2 * i + 1];
-            if (part == 0) {
-                x = fast_exp2(fmaf(x, scale, -mu[sh]));
-                y = fast_exp2(fmaf(y, scale, -mu[sh]));
-            } else if (part == 1) {
-                l[sh] += x;
-                new_hi[sh][i] =
-                    __builtin_amdgcn_perm(__float_as_uint(y), __float_as_uint(x), 0x07060302u);
-            } else if (part == 2) {
-                l[sh] += y;
-                x = fmaf(x, kOneUp, -bf16_hi(__float_as_uint(x)));
-            } else {
-                y = fmaf(y, kOneUp, -bf16_hi(__float_as_uint(y)));
-                new_rest[sh][i] = pack_bf16(x, y);
+                const int at = (int)(t - begin) & (C::kPlaces - 1);
+                sm.key_at[at] = k;
+                sm.value_at[at] = v;
+                sm.absent[at] = none;
             }
         };
-        if (kBehind) {
-            const bf16x8 pb[2] = {as_bf16x8(hi_w[0][0], hi_w[0][1], hi_w[0][2], hi_w[0][3]),
-                                  as_bf16x8(hi_w[1][0], hi_w[1][1], hi_w[1][2], hi_w[1][3])};
-            const bf16x8 pr[2] = {
-                as_bf16x8(rest_w[0][0], rest_w[0][1], rest_w[0][2], rest_w[0][3]),
-                as_bf16x8(rest_w[1][0], rest_w[1][1], rest_w[1][2], rest_w[1][3])};
+        auto place = [&](int t) __attribute__((always_inline)) {  // of the lane's in tile t
+            return (t * C::kTile + mine) & (C::kPlaces - 1);
+        };
+        uint2 raw[F8 ? 2 * C::kLoads : 1];
+        // issues load i of a tile's keys, or of its values
+        auto bring = [&](const char* from, char* into, int keys, int i)
+                         __attribute__((always_inline)) {
+            from += chunk_of;
+            if constexpr (F8) {
+                raw[(keys ? 0 : C::kLoads) + i] = *reinterpret_cast<const uint2*>(from + i * 64);
+            } else {
+                const uint32_t to =
+                    __builtin_amdgcn_readfirstlane(lds_address(into + wave * C::kGroup));
+                load_to_lds<128>(from, to + i * 1024, i);
+            }
+        };
+        auto bring_all = [&](const char* from, char* into, int keys)
+                             __attribute__((always_inline)) {
 #pragma unroll
-            for (int i = 0; i < C::kDims; ++i) {
+            for (int i = 0; i < C::kLoads; ++i) bring(from, into, keys, i);
+        };
+        // 8-bit ones pass registers and go into LDS as bf16
+        auto widen = [&](char* into, int keys) __attribute__((always_inline)) {
+            if constexpr (F8) {
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    acc[i][x & 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                        v8[i % kValuesAhead], x < 2 ? pb[x & 1] : pr[x & 1], acc[i][x & 1], 0, 0,
-                        0);
-                    // quarters i 32 / kDims + ... of the words' 32
+                for (int i = 0; i < C::kLoads; ++i) {
+                    const uint2 w = raw[(keys ? 0 : C::kLoads) + i];
+                    *reinterpret_cast<uint4*>(into + wave * C::kGroup + i * 1024 + lane * 16) =
+                        make_uint4(e4m3_pair<false>(w.x), e4m3_pair<true>(w.x),
+                                   e4m3_pair<false>(w.y), e4m3_pair<true>(w.y));
+                }
+            }
+        };
+
+        __syncthreads();  // the segment before has been read
+        fetch_places(begin, C::kPlaces);
+        __syncthreads();
+        // bf16: the keys of tiles 0 .. 2 and the values of 0 and 1; 8 bits: the keys of 0
+        bring_all(sm.key_at[place(0)], sm.keys[0], 1);
+        if (!F8) {
 #pragma unroll
-                    for (int k = (i * 4 + x) * 8 / C::kDims; k < (i * 4 + x + 1) * 8 / C::kDims; ++k)
+            for (int t = 1; t < 3; ++t) {
+                bring_all(sm.key_at[place(t)], sm.keys[t], 1);
+                bring_all(sm.value_at[place(t - 1)], sm.values[t - 1], 0);
+            }
+        }
+
+        // ---- queries of the wave's slots, operand B of every step
+        const int slot = index * SharedPlan::kSlots + wave * 32 + col;
+        const bool live = wave * 32 + col < slots;
+        bf16x8 q[C::kSteps];
+        {
+            // a slot that is not there takes the block's first one's
+            const int of = live ? slot : index * SharedPlan::kSlots;
+            const int row = (int)((unsigned)of / (unsigned)a.group);
+            const int head = h * a.group + of - row * a.group;
+            const uint16_t* qp = static_cast<const uint16_t*>(a.q) +
+                                 (int64_t)(lo + row) * a.q_ld + (int64_t)head * D + g * 8;
+#pragma unroll
+            for (int st = 0; st < C::kSteps; ++st) {
+                const uint4 w = *reinterpret_cast<const uint4*>(qp + st * 16);
+                q[st] = as_bf16x8(w.x, w.y, w.z, w.w);
+            }
+        }
+        // waited for here, not among the loads of a tile
+#pragma unroll
+        for (int st = 0; st < C::kSteps; ++st) asm volatile("" : "+v"(q[st]));
+        // The scale is taken as positive (products change their sign with it), so that
+        // the largest product is the largest score and a masked -inf stays one; 0 as 1 of
+        // products that are 0.
+        const float signed_scale =
+            a.scale * kLog2e * (F8 && c.k_scale != nullptr ? c.k_scale[h] : 1.0f);
+        const float scale = signed_scale == 0.0f ? 1.0f : fabsf(signed_scale);
+        const float sign = signed_scale == 0.0f ? 0.0f : signed_scale < 0.0f ? -1.0f : 1.0f;
+
+        f32x16 acc[C::kDims];
+#pragma unroll
+        for (int i = 0; i < C::kDims; ++i)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[i][e] = 0.0f;
+        // m (-inf: no score yet; else an integer), the m used, the product from which m is
+        // raised, the lane's sum
+        float m = -kInf, mu = 0.0f, far = -kInf, l = 0.0f;
+        // The weights that are not yet multiplied with their values, as two bf16 terms (see
+        // attend_kernel): a word two positions, 4 words an operand.
+        uint32_t hi_w[8] = {}, rest_w[8] = {};
+        auto value = [&](const char* values, int i) __attribute__((always_inline)) {
+            // i: 32 dims i / 2, 16 positions i % 2
+            const char* at = values + (i & 1) * 2 * C::kGroup + (i >> 2) * 1024;
+            const s16x4 x0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                (__attribute__((address_space(3))) s16x4*)(at + v_at[0][(i >> 1) & 1]));
+            const s16x4 x1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                (__attribute__((address_space(3))) s16x4*)(at + v_at[1][(i >> 1) & 1]));
+            uint2 w0, w1;
+            __builtin_memcpy(&w0, &x0, 8);
+            __builtin_memcpy(&w1, &x1, 8);
+            return as_bf16x8(w0.x, w0.y, w1.x, w1.y);
+        };
+        constexpr int kOperands = 2 * C::kDims, kAhead = 4;
+        static_assert(kOperands == C::kSteps && kOperands >= kAhead, "");
+        // the keys of a tile, operand A of every step
+        bf16x8 k8[C::kSteps];
+        auto key = [&](const char* keys, int st) __attribute__((always_inline)) {
+            const uint4 w =
+                *reinterpret_cast<const uint4*>(keys + k_at[st & 3] + (st >> 2) * 1024);
+            k8[st] = as_bf16x8(w.x, w.y, w.z, w.w);
+        };
+        if constexpr (F8) {
+            widen(sm.keys[0], 1);
+            bring_all(sm.key_at[place(1)], nullptr, 1);
+            bring_all(sm.value_at[place(0)], nullptr, 0);
+        } else {
+            asm volatile("s_waitcnt vmcnt(%0)" : : "n"(4 * C::kLoads) : "memory");
+        }
+        __syncthreads();
+#pragma unroll
+        for (int st = 0; st < C::kSteps; ++st) key(sm.keys[0], st);
+        const char* next_k = sm.key_at[place(F8 ? 2 : 3)];
+        const char* next_v = sm.value_at[place(F8 ? 1 : 2)];
+        int in_keys = 1;  // of three: where the keys of tile t + 1 are
+        // One turn: the scores of tile t, whose keys are in registers, then its weights
+        // between the products of tile t - 1's with their values (BEHIND: there is one) and
+        // the loads of the next tile's keys.  Behind the turn's only barrier the keys of
+        // t + 1 and the values of t are in LDS, and the room of the keys of t and the
+        // values of t - 2 is free.
+        auto turn = [&](auto behind, int t) __attribute__((always_inline)) {
+            constexpr bool kBehind = decltype(behind)::value;
+            const int t0 = begin + t * C::kTile;
+            f32x16 sc;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) sc[e] = 0.0f;
+#pragma unroll
+            for (int st = 0; st < C::kSteps; ++st)
+                sc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k8[st], q[st], sc, 0, 0, 0);
+            bf16x8 v8[kAhead];
+            const char* values_behind = sm.values[(t + 3) & 3];
+            if (kBehind)
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i) v8[i] = value(values_behind, i);
+            const bool masked =
+                t0 + C::kTile > end || __builtin_amdgcn_readfirstlane(sm.holes) != 0;
+            float p[16];  // position 8 (e / 4) + 4 g + e % 4
+#pragma unroll
+            for (int e = 0; e < 16; ++e) p[e] = sc[e];
+            if (sign != 1.0f) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) p[e] *= sign;
+            }
+            if (masked) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t no = *reinterpret_cast<const uint32_t*>(
+                        &sm.absent[(t * C::kTile + 8 * i + 4 * g) & (C::kPlaces - 1)]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if ((no >> (8 * e)) & 1) p[4 * i + e] = -kInf;
+                }
+            }
+            float mx = p[0];
+#pragma unroll
+            for (int e = 1; e < 16; ++e) mx = fmaxf(mx, p[e]);
+            // in the first tile, and hardly ever later
+            if (__ballot(mx > far || (!F8 && l > C::kFull)) != 0) {
+                const float top = fmaxf(mx, __shfl_xor(mx, 32));
+                float to = fmaxf(m, ceilf(top * scale) + C::kHold);
+                if (!F8 && fmaxf(l, __shfl_xor(l, 32)) > C::kFull) to += C::kRaise;
+                if (to > m) {
+                    // m = -inf: 0; else a power of two, as m is an integer
+                    const float f = fast_exp2(m - to);
+                    if (kBehind) {
+#pragma unroll
+                        for (int i = 0; i < C::kDims; ++i) acc[i] *= f;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            hi_w[i] = pack_bf16(bf16_lo(hi_w[i]) * f, bf16_hi(hi_w[i]) * f);
+                            rest_w[i] = pack_bf16(bf16_lo(rest_w[i]) * f, bf16_hi(rest_w[i]) * f);
+                        }
+                    }
+                    l *= f;
+                    m = mu = to;
+                    far = (to - C::kHold + C::kSlack) / scale;
+                }
+            }
+            const char* next_keys = sm.keys[in_keys];
+            if constexpr (F8) {
+                widen(sm.keys[in_keys], 1);
+                widen(sm.values[t & 3], 0);
+            } else {
+                // all but the keys of t + 2 and the values of t + 1
+                asm volatile("s_waitcnt vmcnt(%0)" : : "n"(2 * C::kLoads) : "memory");
+            }
+            __syncthreads();
+            in_keys = in_keys == 2 ? 0 : in_keys + 1;
+            char* into_keys = F8 ? nullptr : sm.keys[in_keys == 2 ? 0 : in_keys + 1];
+            char* into_values = F8 ? nullptr : sm.values[(t + 2) & 3];
+            if (kBehind && (t * C::kTile & (C::kPlaces / 2 - 1)) == 0)
+                fetch_places(t0 + C::kPlaces / 2, C::kPlaces / 2);
+            uint32_t new_hi[8], new_rest[8];
+            constexpr float kOneUp = 1.0f + 0x1p-23f;
+            // word i of the eight: a quarter of its work at a time
+            auto weigh = [&](int i, int part) __attribute__((always_inline)) {
+                float &x = p[2 * i], &y = p[2 * i + 1];
+                if (part == 0) {
+                    x = fast_exp2(fmaf(x, scale, -mu));
+                    y = fast_exp2(fmaf(y, scale, -mu));
+                } else if (part == 1) {
+                    l += x;
+                    new_hi[i] = __builtin_amdgcn_perm(__float_as_uint(y), __float_as_uint(x),
+                                                      0x07060302u);
+                } else if (part == 2) {
+                    l += y;
+                    x = fmaf(x, kOneUp, -bf16_hi(__float_as_uint(x)));
+                } else {
+                    y = fmaf(y, kOneUp, -bf16_hi(__float_as_uint(y)));
+                    new_rest[i] = pack_bf16(x, y);
+                }
+            };
+            if (kBehind) {
+                // the words' 32 quarters spread over the 2 kOperands products
+                constexpr int kEach = 16 / kOperands;
+#pragma unroll
+                for (int i = 0; i < kOperands; ++i) {
+                    const uint32_t *w = hi_w + 4 * (i & 1), *u = rest_w + 4 * (i & 1);
+                    f32x16& to = acc[i >> 1];
+                    to = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                        v8[i % kAhead], as_bf16x8(w[0], w[1], w[2], w[3]), to, 0, 0, 0);
+#pragma unroll
+                    for (int k = 2 * i * kEach; k < (2 * i + 1) * kEach; ++k)
                         weigh(k >> 2, k & 3);
                     __builtin_amdgcn_sched_barrier(0);
+                    to = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                        v8[i % kAhead], as_bf16x8(u[0], u[1], u[2], u[3]), to, 0, 0, 0);
+#pragma unroll
+                    for (int k = (2 * i + 1) * kEach; k < (2 * i + 2) * kEach; ++k)
+                        weigh(k >> 2, k & 3);
+                    if (i + kAhead < kOperands) v8[i % kAhead] = value(values_behind, i + kAhead);
+                    key(next_keys, i);
+                    // (all waves' loads at once would wait for each other)
+                    if (i % 2 == 0) {
+                        const int n = i / 2 % C::kLoads;
+                        if (i / 2 < C::kLoads) bring(next_k, into_keys, 1, n);
+                        else bring(next_v, into_values, 0, n);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
                 }
-                if (i + kValuesAhead < C::kDims)
-                    v8[i % kValuesAhead] = value(values_behind, i + kValuesAhead);
-                key(next_keys, i);  // kDims = 2 kSteps of them
+            } else {
+                bring_all(next_k, into_keys, 1);
+                bring_all(next_v, into_values, 0);
+#pragma unroll
+                for (int k = 0; k < 32; ++k) weigh(k >> 2, k & 3);
+#pragma unroll
+                for (int st = 0; st < C::kSteps; ++st) key(next_keys, st);
             }
-        } else {
 #pragma unroll
-            for (int k = 0; k < 32; ++k) weigh(k >> 2, k & 3);
-#pragma unroll
-            for (int i = 0; i < 2 * C::kSteps; ++i) key(next_keys, i);
-        }
-#pragma unroll
-        for (int sh = 0; sh < 2; ++sh)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                hi_w[sh][i] = new_hi[sh][i];
-                rest_w[sh][i] = new_rest[sh][i];
+            for (int i = 0; i < 8; ++i) {
+                hi_w[i] = new_hi[i];
+                rest_w[i] = new_rest[i];
                 // made here, not where it is used
-                asm volatile("" : "+v"(hi_w[sh][i]), "+v"(rest_w[sh][i]));
+                asm volatile("" : "+v"(hi_w[i]), "+v"(rest_w[i]));
             }
-    };
-    turn(std::false_type{}, begin);
-    int t0 = begin + C::kTile;
-    if (t0 < end) {
-        do {
-            turn(std::true_type{}, t0);
-            t0 += C::kTile;
-        } while (t0 < end);
-    }
-    // the last tile's weights
-    {
+            next_k = sm.key_at[place(t + (F8 ? 3 : 4))];
+            next_v = sm.value_at[place(t + (F8 ? 2 : 3))];
+        };
+        turn(std::false_type{}, 0);
+        int t = 1;
+        if (t < n_tiles) {
+            do {
+                turn(std::true_type{}, t);
+                ++t;
+            } while (t < n_tiles);
+        }
+        // the last tile's weights
         if constexpr (!F8) {
             __builtin_amdgcn_s_waitcnt(0);  // its values, the last that were on their way
             __syncthreads();
         }
-        const char* tile = sm.values[((end - 1 - begin) / C::kTile) & 3];
-        const bf16x8 pb[2] = {as_bf16x8(hi_w[0][0], hi_w[0][1], hi_w[0][2], hi_w[0][3]),
-                              as_bf16x8(hi_w[1][0], hi_w[1][1], hi_w[1][2], hi_w[1][3])};
-        const bf16x8 pr[2] = {as_bf16x8(rest_w[0][0], rest_w[0][1], rest_w[0][2], rest_w[0][3]),
-                              as_bf16x8(rest_w[1][0], rest_w[1][1], rest_w[1][2], rest_w[1][3])};
-        bf16x8 v8[kValuesAhead];
+        {
+            const char* values = sm.values[(n_tiles - 1) & 3];
+            bf16x8 v8[kAhead];
 #pragma unroll
-        for (int i = 0; i < kValuesAhead; ++i) v8[i] = value(tile, i);
+            for (int i = 0; i < kAhead; ++i) v8[i] = value(values, i);
 #pragma unroll
-        for (int i = 0; i < C::kDims; ++i) {
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-                acc[i][x & 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                    v8[i % kValuesAhead], x < 2 ? pb[x & 1] : pr[x & 1], acc[i][x & 1], 0, 0, 0);
-            if (i + kValuesAhead < C::kDims) v8[i % kValuesAhead] = value(tile, i + kValuesAhead);
-            __builtin_amdgcn_sched_barrier(0);
+            for (int i = 0; i < kOperands; ++i) {
+                const uint32_t *w = hi_w + 4 * (i & 1), *u = rest_w + 4 * (i & 1);
+                f32x16& to = acc[i >> 1];
+                to = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                    v8[i % kAhead], as_bf16x8(w[0], w[1], w[2], w[3]), to, 0, 0, 0);
+                to = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                    v8[i % kAhead], as_bf16x8(u[0], u[1], u[2], u[3]), to, 0, 0, 0);
+                if (i + kAhead < kOperands) v8[i % kAhead] = value(values, i + kAhead);
+                __builtin_amdgcn_sched_barrier(0);
+            }
         }
-    }
+
+        l += __shfl_xor(l, 32);
+        if (live) {
+            const int64_t rec = (block_id + chunk) * SharedPlan::kSlots + wave * 32 + col;
+            float* o = s.prefix_out + rec * D + 4 * g;
 #pragma unroll
-    for (int sh = 0; sh < 2; ++sh) {
-        l[sh] += __shfl_xor(l[sh], 16);
-        l[sh] += __shfl_xor(l[sh], 32);
-        if (!live[sh]) continue;
-        const int64_t rec =
-            (block_id + chunk) * SharedPlan::kSlots + wave * 32 + sh * 16 + col;
-        float* o = s.prefix_out + rec * D + 4 * g;
+            for (int i = 0; i < C::kDims; ++i)
 #pragma unroll
-        for (int i = 0; i < C::kDims; ++i) *reinterpret_cast<f32x4*>(o + i * 16) = acc[i][sh];
-        if (g == 0) {
-            s.prefix_ml[rec * 2] = m[sh];
-            s.prefix_ml[rec * 2 + 1] = l[sh];
+                for (int e = 0; e < 4; ++e)
+                    *reinterpret_cast<f32x4*>(o + i * 32 + e * 8) =
+                        f32x4{acc[i][4 * e], acc[i][4 * e + 1], acc[i][4 * e + 2],
+                              acc[i][4 * e + 3]};
+            if (g == 0) {
+                s.prefix_ml[rec * 2] = m;
+                s.prefix_ml[rec * 2 + 1] = l;
+            }
         }
-    }
     }
     if (__ballot(bad) != 0 && lane == 0) raise_error(a.dev_error, SV_DEV_BAD_PAGE);
 }
