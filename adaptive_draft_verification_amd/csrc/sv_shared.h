@@ -76,10 +76,10 @@ struct SharedPlan {
         }
         const int64_t slots = (int64_t)n_req * (k_max + 1) * (n_heads / n_kv_heads);
         blocks = n_groups == 0 ? 0 : (slots / kSlots + n_groups) * n_kv_heads;
-        // As many as are on the chip at once, or half of that beside a lot of workgroups
-        // over own positions; no more than there are runs.
+        // As many as are on the chip at once, fewer beside a lot of workgroups over own
+        // positions; no more than there are runs.
         const bool many = own.grid(n_req, n_kv_heads) >= 512;
-        chunks = head_dim < 256 && !many ? 512 : 256;
+        chunks = head_dim == 256 ? 256 : many ? 384 : 512;
         const double runs = (double)blocks * ((capacity + kTile - 1) / kTile) / kRunMin + 8;
         if (runs < chunks) chunks = (int)runs & ~7;
     }

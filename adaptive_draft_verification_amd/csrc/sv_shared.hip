@@ -17,8 +17,6 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 // ------------------------------------------------------------------- layout
 
-constexpr int kLayoutThreads = 1024;
-
 __device__ __forceinline__ int64_t wave_incl_sum64(int64_t v, int lane) {
 #pragma unroll
     for (int off = 1; off < kWave; off <<= 1) {
@@ -29,59 +27,80 @@ __device__ __forceinline__ int64_t wave_incl_sum64(int64_t v, int lane) {
 }
 
 // Checks the groups and their requests, and counts the tiles: one workgroup, so that
-// the launches behind it only read.
-__global__ __launch_bounds__(kLayoutThreads) void layout_kernel(SharedArgs s) {
+// the launches behind it only read.  KEEP: at most T requests; what is read more than
+// once is kept in LDS then, and one round trip to memory is left of six (2 requests
+// 5.2 -> XX us).
+template <int T, bool KEEP>
+__global__ __launch_bounds__(T) void layout_kernel(SharedArgs s) {
     const AttendArgs& a = s.own;
-    __shared__ int block_sums[kLayoutThreads / kWave], longest_prefix;
-    __shared__ int64_t tile_sums[kLayoutThreads / kWave];
+    constexpr int kKeep = KEEP ? T : 1;
+    __shared__ int kept_start[kKeep + 1], kept_prefix[kKeep], kept_cu[kKeep + 1];
+    __shared__ int kept_broken[kKeep];
+    __shared__ int block_sums[T / kWave], longest_prefix;
+    __shared__ int64_t tile_sums[T / kWave];
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
-    int err = 0;
     if (t == 0) longest_prefix = 0;
-    for (int g = t; g <= s.n_groups && s.n_groups > 0; g += kLayoutThreads) {
-        const int at = s.group_start[g];
-        if (at < 0 || at > a.n_req || (g > 0 && s.group_start[g - 1] > at))
-            err = SV_DEV_BAD_CU_ROWS;
+    if (KEEP) {
+        for (int i = t; i <= a.n_req; i += T) kept_cu[i] = a.cu_rows[i];
+        if (s.n_groups > 0)
+            for (int i = t; i <= s.n_groups; i += T) kept_start[i] = s.group_start[i];
+        if (t < s.n_groups) kept_prefix[t] = s.prefix_len[t];
+        __syncthreads();
+    }
+    auto start = [&](int g) { return KEEP ? kept_start[g] : s.group_start[g]; };
+    auto prefix_of = [&](int g) { return KEEP ? kept_prefix[g] : s.prefix_len[g]; };
+    auto cu = [&](int r) { return KEEP ? kept_cu[r] : a.cu_rows[r]; };
+    auto broken = [&](int g) -> int* { return KEEP ? kept_broken + g : &s.group[g].broken; };
+    auto bits_of = [&](int g) {
+        return KEEP ? kept_broken[g]
+                    : __hip_atomic_load(&s.group[g].broken, __ATOMIC_RELAXED,
+                                        __HIP_MEMORY_SCOPE_AGENT);
+    };
+    int err = 0;
+    for (int g = t; g <= s.n_groups && s.n_groups > 0; g += T) {
+        const int at = start(g);
+        if (at < 0 || at > a.n_req || (g > 0 && start(g - 1) > at)) err = SV_DEV_BAD_CU_ROWS;
+    }
+    for (int g = t; g < s.n_groups; g += T) {
+        const int P = prefix_of(g);
+        const bool fits = P >= 0 && P <= (int64_t)a.max_pages * a.cache.page_size;
+        if (KEEP)
+            kept_broken[g] = fits ? 0 : SV_DEV_BAD_CTX;
+        else
+            __hip_atomic_store(&s.group[g].broken, fits ? 0 : SV_DEV_BAD_CTX, __ATOMIC_RELAXED,
+                               __HIP_MEMORY_SCOPE_AGENT);
     }
     const bool none = __syncthreads_or(err) != 0;
-    for (int g = t; g < s.n_groups; g += kLayoutThreads) {
-        const int P = s.prefix_len[g];
-        const bool fits = P >= 0 && P <= (int64_t)a.max_pages * a.cache.page_size;
-        __hip_atomic_store(&s.group[g].broken, none || fits ? 0 : SV_DEV_BAD_CTX,
-                           __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    }
-    __syncthreads();
     // every request's group, and whether its rows are where they have to be
-    for (int r = t; r < a.n_req; r += kLayoutThreads) {
-        int group = -1;
-        if (!none && s.n_groups > 0 && r >= s.group_start[0] && r < s.group_start[s.n_groups]) {
+    int group = -1;  // of the thread's request (KEEP)
+    for (int r = t; r < a.n_req; r += T) {
+        group = -1;
+        if (!none && s.n_groups > 0 && r >= start(0) && r < start(s.n_groups)) {
             int lo = 0, hi = s.n_groups;  // the last group that starts at r or before
             while (hi - lo > 1) {
                 const int mid = (lo + hi) >> 1;
-                if (s.group_start[mid] <= r) lo = mid;
+                if (start(mid) <= r) lo = mid;
                 else hi = mid;
             }
             group = lo;
-            const int from = a.cu_rows[r], to = a.cu_rows[r + 1];
+            const int from = cu(r), to = cu(r + 1);
             if (from < 0 || to < from || to - from > a.k_max + 1 || to > a.q_rows)
-                atomicOr(&s.group[group].broken, SV_DEV_BAD_CU_ROWS);
+                atomicOr(broken(group), SV_DEV_BAD_CU_ROWS);
         }
-        s.request[r].group = group;
+        if (!KEEP) s.request[r].group = group;
     }
     __syncthreads();
     int blocks = 0;  // of earlier groups
     int64_t tiles = 0;
-    for (int g0 = 0; g0 < s.n_groups; g0 += kLayoutThreads) {
+    for (int g0 = 0; g0 < s.n_groups; g0 += T) {
         const int g = g0 + t;
         int n = 0, each = 0;
         if (g < s.n_groups && !none) {
-            const int bits = __hip_atomic_load(&s.group[g].broken, __ATOMIC_RELAXED,
-                                               __HIP_MEMORY_SCOPE_AGENT);
+            const int bits = bits_of(g);
             err |= bits;
-            const int from = s.group_start[g], to = s.group_start[g + 1];
-            const int P = s.prefix_len[g];
+            const int from = start(g), to = start(g + 1), P = prefix_of(g);
             if (bits == 0 && P > 0 && to > from)
-                n = ((a.cu_rows[to] - a.cu_rows[from]) * a.group + SharedPlan::kSlots - 1) /
-                    SharedPlan::kSlots;
+                n = ((cu(to) - cu(from)) * a.group + SharedPlan::kSlots - 1) / SharedPlan::kSlots;
             if (n > 0) {
                 each = (int)(((int64_t)P + SharedPlan::kTile - 1) / SharedPlan::kTile);
                 atomicMax(&longest_prefix, each);
@@ -96,7 +115,7 @@ __global__ __launch_bounds__(kLayoutThreads) void layout_kernel(SharedArgs s) {
         __syncthreads();
         int block = blocks + blocks_to - n;
         int64_t tile = tiles + tiles_to - (int64_t)n * each;
-        for (int w = 0; w < kLayoutThreads / kWave; ++w) {
+        for (int w = 0; w < T / kWave; ++w) {
             if (w < wave) {
                 block += block_sums[w];
                 tile += tile_sums[w];
@@ -115,24 +134,23 @@ __global__ __launch_bounds__(kLayoutThreads) void layout_kernel(SharedArgs s) {
         s.group[s.n_groups].block = blocks;
         // equal runs; a block of n tiles lies in n / run + 2 of them at most
         const int64_t all = tiles * a.cache.n_kv_heads;
-        const int64_t few = (longest_prefix + SharedPlan::kSegments - 3) / (SharedPlan::kSegments - 2);
+        const int64_t few =
+            (longest_prefix + SharedPlan::kSegments - 3) / (SharedPlan::kSegments - 2);
         int64_t run = s.chunks > 0 ? (all + s.chunks - 1) / s.chunks : 0;
         run = run < few ? few : run;
         run = run < SharedPlan::kRunMin ? SharedPlan::kRunMin : run;
         s.totals->run = run;
         s.totals->chunks = (int)((all + run - 1) / run);
     }
-    for (int r = t; r < a.n_req; r += kLayoutThreads) {
-        const int g = s.request[r].group;
+    for (int r = t; r < a.n_req; r += T) {
+        const int g = KEEP ? group : s.request[r].group;
         int first = none ? -1 : 0, row = 0;
         if (g >= 0) {
-            const int bits = __hip_atomic_load(&s.group[g].broken, __ATOMIC_RELAXED,
-                                               __HIP_MEMORY_SCOPE_AGENT);
-            first = bits != 0 ? -1 : s.prefix_len[g];
-            row = a.cu_rows[r] - a.cu_rows[s.group_start[g]];
+            first = bits_of(g) != 0 ? -1 : prefix_of(g);
+            row = cu(r) - cu(start(g));
         }
         s.first[r] = first;
-        s.request[r].row = row;
+        s.request[r] = SharedRequest{g, row};
     }
     if (err != 0) raise_error(a.dev_error, err);
 }
@@ -643,98 +661,162 @@ __global__ __launch_bounds__(256, (Prefix<D, F8>::kOccupancy)) void shared_kerne
 
 // --------------------------------------------------------------------- join
 
-// Merges the parts of a (row, head), those over the prefix first: a wave each, lanes
-// over the dims, in a fixed order.
-template <int D, bool F8>
+// Merges the parts of a row's heads, those over the prefix first, in a fixed order.  W
+// waves take H neighbouring heads: lanes over the dims, wave w the parts w, w + W, ...,
+// four of each head in flight; the waves' sums meet in LDS.  Bound by the latency of
+// the loads that lead to the parts, and with many rows by reading them.
+template <int D, bool F8, int W, int H>
 __global__ __launch_bounds__(256) void shared_join_kernel(SharedArgs s) {
     constexpr int E = D / kWave;
-    __shared__ float factors[4][128];
+    constexpr int kMost = 128;  // parts
+    __shared__ float factors[4][H][kMost];
+    __shared__ float sums[W == 1 ? 1 : 4][D];
     const AttendArgs& a = s.own;
     const sv_cache& c = a.cache;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int per = (a.k_max + 1) * a.n_heads;
-    const int64_t id = (int64_t)blockIdx.x * 4 + wave;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), w = wave % W;
+    const int runs = (a.n_heads + H - 1) / H;
+    const int per = (a.k_max + 1) * runs;
+    const int64_t id = (int64_t)blockIdx.x * (4 / W) + wave / W;
     if (id >= (int64_t)a.n_req * per) return;
-    const int r = (int)(id / per), rest = (int)(id % per);
-    const int row = rest / a.n_heads, head = rest % a.n_heads;
+    const int r = (int)(id / per), rest = (int)id - r * per;
+    const int row = rest / runs, head0 = (rest - row * runs) * H;
     const int first = s.first[r];
     const int lo = a.cu_rows[r], hi = a.cu_rows[r + 1], rows = hi - lo, ctx = a.ctx_len[r];
     if (first < 0 || lo < 0 || hi < lo || rows > a.k_max + 1 || hi > a.q_rows || row >= rows ||
         ctx < first || (int64_t)ctx + rows > (int64_t)a.max_pages * c.page_size)
         return;
-    // the parts as the two launches made them
-    int n1 = 0;
-    int64_t rec1 = 0;  // parts are kSlots records apart
+    // the parts as the launch before made them
+    int n1[H], n[H];
+    int64_t rec1[H];  // parts are kSlots records apart
+    const int len = ctx + rows - (first & ~15), plen = part_len(len, a.parts, a.part_min);
+    const int n2 = (len + plen - 1) / plen;
+#pragma unroll
+    for (int i = 0; i < H; ++i) n1[i] = 0, rec1[i] = 0;
     if (first > 0) {
         const SharedRequest at = s.request[r];
-        const int h = head / a.group;
-        const int slot = (at.row + row) * a.group + head - h * a.group;
-        const int64_t block_id = (int64_t)h * s.group[s.n_groups].block +
-                                 s.group[at.group].block + slot / SharedPlan::kSlots;
-        const SharedSpan span = s.span[block_id];
-        n1 = span.last - span.first + 1;
-        rec1 = (block_id + span.first) * SharedPlan::kSlots + slot % SharedPlan::kSlots;
+        const int head_blocks = s.group[s.n_groups].block, block0 = s.group[at.group].block;
+#pragma unroll
+        for (int i = 0; i < H; ++i) {
+            const int head = min(head0 + i, a.n_heads - 1), h = head / a.group;
+            const int slot = (at.row + row) * a.group + head - h * a.group;
+            const int64_t block_id =
+                (int64_t)h * head_blocks + block0 + slot / SharedPlan::kSlots;
+            const SharedSpan span = s.span[block_id];
+            n1[i] = span.last - span.first + 1;
+            rec1[i] = (block_id + span.first) * SharedPlan::kSlots + slot % SharedPlan::kSlots;
+        }
     }
-    const int len = ctx + rows - (first & ~15), plen = part_len(len, a.parts, a.part_min);
-    const int n = n1 + (len + plen - 1) / plen;  // at most 128
-    // attend_kernel's records: request, head, row
-    const int64_t rec2 = (((int64_t)r * a.n_heads + head) * (a.k_max + 1) + row) * a.parts;
+    int most = 0;
+    float m[H], l[H], o[H][E];
+    int64_t rec2[H];
+#pragma unroll
+    for (int i = 0; i < H; ++i) {
+        const int head = min(head0 + i, a.n_heads - 1);
+        n[i] = n1[i] + n2;  // at most kMost
+        most = max(most, n[i]);
+        // attend's records: request, head, row
+        rec2[i] = (((int64_t)r * a.n_heads + head) * (a.k_max + 1) + row) * a.parts;
+    }
     // the largest maximum and the parts' factors, two a lane
-    float mm[2] = {-kInf, -kInf}, ll[2] = {0.0f, 0.0f};
+    float mm[H][2], ll[H][2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int p = lane + 64 * i;
-        if (p >= n) continue;
-        const float* ml = p < n1 ? s.prefix_ml + (rec1 + p * SharedPlan::kSlots) * 2 : a.part_ml + (rec2 + p - n1) * 2;
-        mm[i] = ml[0];
-        ll[i] = ml[1];
+    for (int i = 0; i < H; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            mm[i][j] = -kInf;
+            ll[i][j] = 0.0f;
+            const int p = lane + 64 * j;
+            if (p >= n[i]) continue;
+            const float* ml = p < n1[i] ? s.prefix_ml + (rec1[i] + p * SharedPlan::kSlots) * 2
+                                        : a.part_ml + (rec2[i] + p - n1[i]) * 2;
+            mm[i][j] = ml[0];
+            ll[i][j] = ml[1];
+        }
+#pragma unroll
+    for (int i = 0; i < H; ++i) {
+        m[i] = wave_max(fmaxf(mm[i][0], mm[i][1]));
+        float f[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            f[j] = mm[i][j] == m[i] ? 1.0f : fast_exp2(mm[i][j] - m[i]);
+            ll[i][j] = lane + 64 * j < n[i] ? f[j] * ll[i][j] : 0.0f;
+        }
+        l[i] = wave_sum(ll[i][0] + ll[i][1]);
+        // over the whole sum before the outputs are added up: they are then shares of the
+        // mean, and stay in range
+        const float inv = l[i] == 0.0f ? 0.0f : 1.0f / l[i];
+        factors[wave][i][lane] = f[0] * inv;
+        factors[wave][i][lane + 64] = f[1] * inv;
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[i][e] = 0.0f;
     }
-    const float m = wave_max(fmaxf(mm[0], mm[1]));
-    const float f0 = mm[0] == m ? 1.0f : fast_exp2(mm[0] - m);
-    const float f1 = mm[1] == m ? 1.0f : fast_exp2(mm[1] - m);
-    const float l =
-        wave_sum((lane < n ? f0 * ll[0] : 0.0f) + (lane + 64 < n ? f1 * ll[1] : 0.0f));
-    // over the whole sum before the outputs are added up: they are then shares of the
-    // mean, and stay in range
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    float* factor = factors[wave];
-    factor[lane] = f0 * inv;
-    factor[lane + 64] = f1 * inv;
     __builtin_amdgcn_wave_barrier();
-    float o[E];
+    for (int p0 = w; p0 < most; p0 += 4 * W) {
+        float x[H][4][E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = 0.0f;
-    for (int p0 = 0; p0 < n; p0 += 4) {
-        float x[4][E];
+        for (int i = 0; i < H; ++i)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int p = min(p0 + i, n - 1);
-            const float* from =
-                (p < n1 ? s.prefix_out + (rec1 + p * SharedPlan::kSlots) * D
-                       : a.part_out + (rec2 + p - n1) * D) + lane * E;
+            for (int j = 0; j < 4; ++j) {
+                const int p = min(p0 + j * W, n[i] - 1);
+                const float* from =
+                    (p < n1[i] ? s.prefix_out + (rec1[i] + p * SharedPlan::kSlots) * D
+                               : a.part_out + (rec2[i] + p - n1[i]) * D) +
+                    lane * E;
 #pragma unroll
-            for (int e = 0; e < E; ++e) x[i][e] = from[e];
-        }
+                for (int e = 0; e < E; ++e) x[i][j][e] = from[e];
+            }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (p0 + i >= n) break;
-            const float f = factor[p0 + i];
+        for (int i = 0; i < H; ++i)
 #pragma unroll
-            for (int e = 0; e < E; ++e) o[e] += f * x[i][e];
+            for (int j = 0; j < 4; ++j) {
+                if (p0 + j * W >= n[i]) break;
+                const float f = factors[wave][i][p0 + j * W];
+#pragma unroll
+                for (int e = 0; e < E; ++e) o[i][e] += f * x[i][j][e];
+            }
+    }
+    if (W > 1) {
+        static_assert(W == 1 || H == 1, "");
+#pragma unroll
+        for (int e = 0; e < E; ++e) sums[wave][lane * E + e] = o[0][e];
+        __syncthreads();
+        if (w != 0) return;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const int i = lane * E + e;
+            o[0][e] = (sums[0][i] + sums[1][i]) + (sums[2][i] + sums[3][i]);
         }
     }
-    const float vscale = F8 && c.v_scale != nullptr ? c.v_scale[head / a.group] : 1.0f;
-    uint16_t* out = static_cast<uint16_t*>(a.out) + (int64_t)(lo + row) * a.out_ld +
-                    (int64_t)head * D + lane * E;
 #pragma unroll
-    for (int e = 0; e < E; ++e)
-        out[e] = (uint16_t)pack_bf16(l == 0.0f ? 0.0f : o[e] * vscale, 0.0f);
-    if (a.out_lse != nullptr && lane == 0) {
-        // the sum's exponent first: both terms are then of the result's size
-        int e;
-        const float f = frexpf(l, &e);
-        a.out_lse[(int64_t)(lo + row) * a.n_heads + head] =
-            l == 0.0f ? -kInf : ((m + (float)e) + log2f(f)) * kLn2;
+    for (int i = 0; i < H; ++i) {
+        const int head = head0 + i;
+        if (head >= a.n_heads) break;
+        const float vscale = F8 && c.v_scale != nullptr ? c.v_scale[head / a.group] : 1.0f;
+        uint16_t* out = static_cast<uint16_t*>(a.out) + (int64_t)(lo + row) * a.out_ld +
+                        (int64_t)head * D + lane * E;
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            out[e] = (uint16_t)pack_bf16(l[i] == 0.0f ? 0.0f : o[i][e] * vscale, 0.0f);
+        if (a.out_lse != nullptr && lane == 0) {
+            // the sum's exponent first: both terms are then of the result's size
+            int e;
+            const float f = frexpf(l[i], &e);
+            a.out_lse[(int64_t)(lo + row) * a.n_heads + head] =
+                l[i] == 0.0f ? -kInf : ((m[i] + (float)e) + log2f(f)) * kLn2;
+        }
+    }
+}
+
+template <int D, bool F8>
+void run_shared_join(const SharedArgs& s, hipStream_t stream) {
+    const int64_t rows = (int64_t)s.own.n_req * (s.own.k_max + 1);
+    // Few rows: a workgroup a head, for parts read at once.  Many: fewer, longer waves.
+    if (rows * s.own.n_heads <= 2048) {
+        shared_join_kernel<D, F8, 4, 1><<<(unsigned)(rows * s.own.n_heads), 256, 0, stream>>>(s);
+    } else {
+        const int64_t runs = rows * ((s.own.n_heads + 1) / 2);
+        shared_join_kernel<D, F8, 1, 2><<<(unsigned)((runs + 3) / 4), 256, 0, stream>>>(s);
     }
 }
 
@@ -752,7 +834,9 @@ void run_both(const SharedArgs& s, hipStream_t stream) {
 template <int D, bool F8>
 hipError_t run_shared(const SharedArgs& s, hipStream_t stream) {
     const AttendArgs& a = s.own;
-    layout_kernel<<<1, kLayoutThreads, 0, stream>>>(s);
+    if (a.n_req <= 256) layout_kernel<256, true><<<1, 256, 0, stream>>>(s);
+    else if (a.n_req <= 1024) layout_kernel<1024, true><<<1, 1024, 0, stream>>>(s);
+    else layout_kernel<1024, false><<<1, 1024, 0, stream>>>(s);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     // the plan takes slot_tiles * D <= 256
@@ -763,8 +847,7 @@ hipError_t run_shared(const SharedArgs& s, hipStream_t stream) {
     else run_both<D, F8, 4>(s, stream);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
-    const int64_t total = (int64_t)a.n_req * (a.k_max + 1) * a.n_heads;
-    shared_join_kernel<D, F8><<<(unsigned)((total + 3) / 4), 256, 0, stream>>>(s);
+    run_shared_join<D, F8>(s, stream);
     return hipGetLastError();
 }
 
