@@ -10,6 +10,7 @@ namespace sv {
 namespace {
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 // ------------------------------------------------------------------- append
 
@@ -91,7 +92,7 @@ struct Latent {
     static constexpr int kLoads = kChunks / 8;     // of a group
     static constexpr int kSteps = kDim / 32;       // products of a score
     static constexpr int kEarly = kSteps / 4;      // loads issued between them
-    static constexpr int kDims = R / 32;           // 16-dim tiles of a wave's output
+    static constexpr int kDims = R / 64;           // 32-dim tiles of a wave's output
     static constexpr int kEsize = F8 ? 1 : 2;
     static constexpr int kPlaces = 1024;           // positions whose places are in LDS
     // Weights are 2^(score - m), m kHold above the maximum of the slot's first tile.
@@ -255,27 +256,29 @@ __global__ __launch_bounds__(256, 1) void latent_kernel(LatentAttendArgs a) {
     const float scale = signed_scale == 0.0f ? 1.0f : fabsf(signed_scale);
     const float sign = signed_scale == 0.0f ? 0.0f : signed_scale < 0.0f ? -1.0f : 1.0f;
 
-    f32x4 acc[C::kDims][2];
+    f32x16 acc[C::kDims];
     float m[2], mu[2];  // m (-inf: no score in the first tile), the m used
     float far[2];       // the product whose score is kSlack above the first ones
     float l[2];         // sum
 
     // where a lane reads keys: chunks 4 st + g of its position, st = 0, 1 of 128 bytes
-    int k_at[2], v_own[4], v_other[4];
+    int k_at[2], v_own[2], v_other[2];
     {
         const int pos = half * 16 + col, at = (pos >> 3) * C::kGroup + (pos & 7) * 128;
 #pragma unroll
         for (int j = 0; j < 2; ++j) k_at[j] = at + ((4 * j + g) ^ swizzle(pos)) * 16;
     }
-    // and values: 4 positions by 16 dims for 16 lanes, tiles 0 .. 3 of 128 bytes, from
-    // the wave's half of the dims on; of its own positions and of the other wave's
+    // and values: 4 positions by 16 dims for 16 lanes, the first four of 8 and even 32
+    // dims or the second and odd ones, then the others; of the wave's half of the dims, of
+    // its own positions and of the other wave's
     {
-        const int pos = 4 * g + (col >> 2);
+        const int pos = 8 * (lane >> 5) + ((lane & 15) >> 2);
         const int at = (pos >> 3) * C::kGroup + (pos & 7) * 128 + (lane & 1) * 8 +
                        half * (R / 128) * 1024;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int x = at + ((2 * j + ((lane >> 1) & 1)) ^ swizzle(pos)) * 16;
+        for (int j = 0; j < 2; ++j) {
+            const int ch = 4 * j + 2 * ((lane >> 4) & 1) + ((lane >> 1) & 1);
+            const int x = at + (ch ^ swizzle(pos)) * 16;
             v_own[j] = x + half * 2 * C::kGroup;
             v_other[j] = x + (half ^ 1) * 2 * C::kGroup;
         }
@@ -410,16 +413,29 @@ __global__ __launch_bounds__(256, 1) void latent_kernel(LatentAttendArgs a) {
         }
         return make_uint4(w[0], w[1], w[2], w[3]);
     };
+    // Words of both slots' splits as operands: the lane's slot is lane % 32 then, its
+    // positions 8 (lane / 32) .. of 16.
+    struct Weights {
+        uint4 hi, rest;
+    };
+    auto operands = [&](const uint4& x, const uint4& y) __attribute__((always_inline)) {
+        const auto h0 = __builtin_amdgcn_permlane16_swap(x.x, y.x, false, false);
+        const auto h1 = __builtin_amdgcn_permlane16_swap(x.y, y.y, false, false);
+        const auto r0 = __builtin_amdgcn_permlane16_swap(x.z, y.z, false, false);
+        const auto r1 = __builtin_amdgcn_permlane16_swap(x.w, y.w, false, false);
+        return Weights{make_uint4(h0[0], h1[0], h0[1], h1[1]),
+                       make_uint4(r0[0], r1[0], r0[1], r1[1])};
+    };
 
     // a second time from the true maxima, if a score rose too far above the first ones
     for (bool again = false;; again = true) {
 #pragma unroll
         for (int i = 0; i < C::kDims; ++i)
 #pragma unroll
-            for (int sh = 0; sh < 2; ++sh) acc[i][sh] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            for (int e = 0; e < 16; ++e) acc[i][e] = 0.0f;
         l[0] = l[1] = 0.0f;
         if (again) place = start();
-        uint4 own[2];  // weights of the tile before: slots 0 .. 15, 16 .. 31; two terms each
+        Weights own;  // of the tile before
         {
             settle(0);
             __syncthreads();
@@ -437,12 +453,12 @@ __global__ __launch_bounds__(256, 1) void latent_kernel(LatentAttendArgs a) {
                 refer(mx);
             }
 #pragma unroll
-            for (int sh = 0; sh < 2; ++sh) {
+            for (int sh = 0; sh < 2; ++sh)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) weigh(p[sh][e], sh);
-                own[sh] = split(p[sh]);
-                weights[0][wave][sh][lane] = own[sh];
-            }
+            own = operands(split(p[0]), split(p[1]));
+            weights[0][wave][0][lane] = own.hi;
+            weights[0][wave][1][lane] = own.rest;
         }
         // a turn takes the scores of its tile (there is none in the last turn) and the
         // values of the one before
@@ -453,8 +469,8 @@ __global__ __launch_bounds__(256, 1) void latent_kernel(LatentAttendArgs a) {
             __syncthreads();
             // of the tile before: no wave is a tile further before this one has read it
             const int rose_before = risen[odd ^ 1];
-            const uint4 other[2] = {weights[odd ^ 1][wave ^ 1][0][lane],
-                                    weights[odd ^ 1][wave ^ 1][1][lane]};
+            const Weights other{weights[odd ^ 1][wave ^ 1][0][lane],
+                                weights[odd ^ 1][wave ^ 1][1][lane]};
             more = t0 < end;
             float p[2][4];
             if (more) {
@@ -471,67 +487,50 @@ __global__ __launch_bounds__(256, 1) void latent_kernel(LatentAttendArgs a) {
             }
             rose = !again && __builtin_amdgcn_readfirstlane(rose_before) != 0;
             more = more && !rose;
-            // positions 4 g .. of the wave's own 16, then of the other's
             const char* tile = tiles[buf == 0 ? 2 : buf - 1];
-            bf16x8 pb[2], pr[2];
-            uint4 next[2];
-#pragma unroll
-            for (int sh = 0; sh < 2; ++sh) {
-                const uint4 x = own[sh], y = other[sh];
-                pb[sh] = as_bf16x8(x.x, x.y, y.x, y.y);
-                pr[sh] = as_bf16x8(x.z, x.w, y.z, y.w);
-            }
+            uint4 words[2];
+            // value operand i: dims 32 (i / 2) .., the wave's own 16 positions or the other's
             auto value = [&](int i) __attribute__((always_inline)) {
+                const char* at = tile + (i >> 2) * 1024;
+                const int j = (i >> 1) & 1;
                 const s16x4 x0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
                     (__attribute__((address_space(3)))
-                     s16x4*)(tile + v_own[i & 3] + (i >> 2) * 1024));
+                     s16x4*)(at + ((i & 1) == 0 ? v_own[j] : v_other[j])));
                 const s16x4 x1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
                     (__attribute__((address_space(3)))
-                     s16x4*)(tile + v_other[i & 3] + (i >> 2) * 1024));
+                     s16x4*)(at + 512 + ((i & 1) == 0 ? v_own[j ^ 1] : v_other[j ^ 1])));
                 uint2 w0, w1;
                 __builtin_memcpy(&w0, &x0, 8);
                 __builtin_memcpy(&w1, &x1, 8);
                 return as_bf16x8(w0.x, w0.y, w1.x, w1.y);
             };
-            // Two tiles at a time: a product waits for the one before it on the same sum.
-            // Between them the values' reads, kAhead tiles ahead, this turn's weights and
-            // the rest of the next tile's loads (in the last turn weights of 0, and loads to
-            // where nothing is read any more).
-            constexpr int kAhead = 4;
+            // Between the products the values' reads, kAhead operands ahead, this turn's
+            // weights and the rest of the next tile's loads (in the last turn weights of 0,
+            // and loads to where nothing is read any more).
+            constexpr int kAhead = 4, kProducts = 4 * C::kDims;
             bf16x8 v8[kAhead];
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) v8[i] = value(i);
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int i0 = 0; i0 < C::kDims; i0 += 2) {
-#pragma unroll
-                for (int x = 0; x < 8; ++x) {
-                    const int i = i0 + ((x >> 1) & 1), sh = x & 1;
-                    acc[i][sh] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                        v8[i % kAhead], x < 4 ? pb[sh] : pr[sh], acc[i][sh], 0, 0, 0);
-                    constexpr int kEach = C::kDims >= 16 ? 1 : 2;  // weights at a time
-                    if (x == 0 || x == 2) {
-#pragma unroll
-                        for (int e = 0; e < kEach; ++e) {
-                            const int n = (i0 + x / 2) * kEach + e;
-                            if (n < 8) weigh(p[n >> 2][n & 3], n >> 2);
-                        }
-                    }
-                    if (x == 3) {
-                        const int n = (i0 / 2 - (C::kDims / 2 - 2)) ;
-                        if (n >= 0) next[n] = split(p[n]);
-                    }
-                    if (x == 4 && C::kEarly + i0 / 2 < C::kLoads) issue(C::kEarly + i0 / 2);
-                    if (x >= 6 && i0 + kAhead + (x - 6) < C::kDims)
-                        v8[(i0 + x - 6) % kAhead] = value(i0 + kAhead + (x - 6));
-                    __builtin_amdgcn_sched_barrier(0);
-                }
+            for (int k = 0; k < kProducts; ++k) {
+                const int i = k >> 1;
+                const Weights& of = (i & 1) == 0 ? own : other;
+                const uint4& w = (k & 1) == 0 ? of.hi : of.rest;
+                acc[i >> 1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                    v8[i % kAhead], as_bf16x8(w.x, w.y, w.z, w.w), acc[i >> 1], 0, 0, 0);
+                constexpr int kEvery = kProducts / 16;  // 8 weights in half of the products
+                if (k % kEvery == 0 && k / kEvery < 8)
+                    weigh(p[k / kEvery >> 2][k / kEvery & 3], k / kEvery >> 2);
+                if (k == kProducts / 2) words[0] = split(p[0]);
+                if (k == kProducts / 2 + 2) words[1] = split(p[1]);
+                if (k % 4 == 1 && C::kEarly + k / 4 < C::kLoads) issue(C::kEarly + k / 4);
+                if ((k & 1) == 1 && i + kAhead < 2 * C::kDims) v8[i % kAhead] = value(i + kAhead);
+                __builtin_amdgcn_sched_barrier(0);
             }
-#pragma unroll
-            for (int sh = 0; sh < 2; ++sh) {
-                own[sh] = next[sh];
-                weights[odd][wave][sh][lane] = own[sh];
-            }
+            own = operands(words[0], words[1]);
+            weights[odd][wave][0][lane] = own.hi;
+            weights[odd][wave][1][lane] = own.rest;
             buf = buf == 2 ? 0 : buf + 1;
             odd ^= 1;
         }
@@ -574,51 +573,58 @@ __global__ __launch_bounds__(256, 1) void latent_kernel(LatentAttendArgs a) {
         const float o = tops[wave ^ 1][sh * 16 + col];
         l[sh] = half == 0 ? l[sh] + o : o + l[sh];
     }
+    // the accumulators' slot is lane % 32: of either kind of lane the one's it is
+    const int upper = lane >> 5;
+    const bool odd16 = (lane >> 4) & 1;
+    const float l_of = odd16 ? l[1] : l[0], m_of = odd16 ? m[1] : m[0];
+    const int row_of = odd16 ? q_row[1] : q_row[0], head_of = odd16 ? head[1] : head[0];
+    const bool live_of = odd16 ? live[1] : live[0];
     const int dim0 = half * (R / 2);
     if (!whole) {
+        if (!live_of) return;
+        const int64_t rec =
+            (((int64_t)r * (a.k_max + 1) + row_of) * a.n_heads + head_of) * a.parts + part;
+        float* o = a.part_out + rec * R + dim0 + 4 * upper;
 #pragma unroll
-        for (int sh = 0; sh < 2; ++sh) {
-            if (!live[sh]) continue;
-            const int64_t rec =
-                (((int64_t)r * (a.k_max + 1) + q_row[sh]) * a.n_heads + head[sh]) * a.parts + part;
-            float* o = a.part_out + rec * R + dim0 + 4 * g;
+        for (int i = 0; i < C::kDims; ++i)
 #pragma unroll
-            for (int i = 0; i < C::kDims; ++i) *reinterpret_cast<f32x4*>(o + i * 16) = acc[i][sh];
-            if (g == 0 && half == 0) {
-                a.part_ml[rec * 2] = m[sh];
-                a.part_ml[rec * 2 + 1] = l[sh];
-            }
+            for (int e = 0; e < 4; ++e)
+                *reinterpret_cast<f32x4*>(o + i * 32 + e * 8) =
+                    f32x4{acc[i][4 * e], acc[i][4 * e + 1], acc[i][4 * e + 2], acc[i][4 * e + 3]};
+        if (upper == 0 && half == 0) {
+            a.part_ml[rec * 2] = m_of;
+            a.part_ml[rec * 2 + 1] = l_of;
         }
         return;
     }
+    // no weight at all: 0, also where 0 times a value was NaN
+    const bool nothing = l_of == 0.0f;
+    const float inv = nothing ? 0.0f : 1.0f / l_of;
+    // eight dims a lane after the exchange of halves: an even or an odd eighth
+    uint16_t* o = static_cast<uint16_t*>(a.out) + (int64_t)(lo + row_of) * a.out_ld +
+                  (int64_t)head_of * R + dim0 + 8 * upper;
 #pragma unroll
-    for (int sh = 0; sh < 2; ++sh) {
-        // no weight at all: 0, also where 0 times a value was NaN
-        const bool nothing = l[sh] == 0.0f;
-        const float inv = nothing ? 0.0f : 1.0f / l[sh];
-        // dims 8 (g / 2) .. of tile i + g % 2 after the exchange of quarters
-        uint16_t* o = static_cast<uint16_t*>(a.out) + (int64_t)(lo + q_row[sh]) * a.out_ld +
-                      (int64_t)head[sh] * R + dim0 + (g & 1) * 16 + (g >> 1) * 8;
+    for (int i = 0; i < C::kDims; ++i)
 #pragma unroll
-        for (int i = 0; i < C::kDims; i += 2) {
+        for (int e = 0; e < 4; e += 2) {
             uint32_t w[2][2];
 #pragma unroll
             for (int j = 0; j < 2; ++j)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float x = acc[i + j][sh][2 * e], y = acc[i + j][sh][2 * e + 1];
+                for (int n = 0; n < 2; ++n) {
+                    const float x = acc[i][4 * (e + j) + 2 * n], y = acc[i][4 * (e + j) + 2 * n + 1];
                     // the mean first, then its scale: only their product has to be in range
-                    w[j][e] = nothing ? 0u : pack_bf16(x * inv * kv_scale, y * inv * kv_scale);
+                    w[j][n] = nothing ? 0u : pack_bf16(x * inv * kv_scale, y * inv * kv_scale);
                 }
-            const auto s0 = __builtin_amdgcn_permlane16_swap(w[0][0], w[1][0], false, false);
-            const auto s1 = __builtin_amdgcn_permlane16_swap(w[0][1], w[1][1], false, false);
-            if (live[sh])
-                *reinterpret_cast<uint4*>(o + i * 16) = make_uint4(s0[0], s1[0], s0[1], s1[1]);
+            const auto s0 = __builtin_amdgcn_permlane32_swap(w[0][0], w[1][0], false, false);
+            const auto s1 = __builtin_amdgcn_permlane32_swap(w[0][1], w[1][1], false, false);
+            if (live_of)
+                *reinterpret_cast<uint4*>(o + i * 32 + e * 8) =
+                    make_uint4(s0[0], s1[0], s0[1], s1[1]);
         }
-        if (live[sh] && a.out_lse != nullptr && g == 0 && half == 0)
-            a.out_lse[(int64_t)(lo + q_row[sh]) * a.n_heads + head[sh]] =
-                nothing ? -kInf : ((m[sh] - C::kHold) + log2f(l[sh] * exp2f(C::kHold))) * kLn2;
-    }
+    if (live_of && a.out_lse != nullptr && upper == 0 && half == 0)
+        a.out_lse[(int64_t)(lo + row_of) * a.n_heads + head_of] =
+            nothing ? -kInf : ((m_of - C::kHold) + log2f(l_of * exp2f(C::kHold))) * kLn2;
 }
 
 // Merges the parts of a (row, head), a wave each: lanes over the dims.
