@@ -109,9 +109,11 @@ __global__ __launch_bounds__(256, 1) void latent_kernel(LatentAttendArgs a) {
     __shared__ __attribute__((aligned(16))) char tiles[3][C::kTileBytes];
     __shared__ uint4 weights[2][4][2][kWave];  // of even and odd tiles: a wave's, for the other
     __shared__ float tops[4][32];              // maxima of a wave's slots
-    __shared__ int64_t places[C::kPlaces];     // bytes to position begin + i at i % kPlaces
-    // a byte a position of the tile: it is none, or not finite
-    __shared__ __attribute__((aligned(4))) uint8_t absent[3][C::kTile], tainted[3][C::kTile];
+    // of position begin + i at i % kPlaces: where it is, and whether there is none
+    __shared__ const char* places[C::kPlaces];
+    __shared__ __attribute__((aligned(4))) uint8_t absent[C::kPlaces];
+    // a byte a position of the tile: it is not finite
+    __shared__ __attribute__((aligned(4))) uint8_t tainted[3][C::kTile];
     __shared__ int holes;     // a position before the end is none
     __shared__ int risen[2];  // a score passed its slot's m by too much, in an even or odd tile
     const sv_latent_cache& c = a.cache;
@@ -153,26 +155,30 @@ __global__ __launch_bounds__(256, 1) void latent_kernel(LatentAttendArgs a) {
     const int chunk_of = ((lane & 7) ^ swizzle(mine)) * 8 * C::kEsize;
     // The places of `n` positions from `from` on, into LDS: kPlaces at first, then half
     // as many at a time (a wait for a page id in registers would be a wait for the tile
-    // that is on its way).  -1: after the end, or on a page that is not there.
+    // that is on its way).  None: after the end, or on a page that is not there.
     bool bad = false;
     auto fetch_places = [&](int from, int n) __attribute__((always_inline)) {
-        for (int i = threadIdx.x; i < n && from + i < end + 3 * C::kTile; i += 256) {
-            const int t = from + i;
-            int64_t place = -1;
+        for (int i = threadIdx.x; i < n; i += 256) {
+            const int64_t t = (int64_t)from + i;
+            const char* at = reinterpret_cast<const char*>(kZeros);
+            bool none = true;
             if (t < end) {
-                const int in = a.page_shift >= 0 ? t >> a.page_shift
-                                                 : (int)((unsigned)t / (unsigned)c.page_size);
+                const int in = a.page_shift >= 0
+                                   ? (int)t >> a.page_shift
+                                   : (int)((unsigned)t / (unsigned)c.page_size);
                 const int page = table[in];
                 if (page >= 0 && page < c.n_pages) {
-                    place = ((int64_t)page * c.page_stride +
-                             (int64_t)(t - in * c.page_size) * c.token_stride) *
-                            C::kEsize;
+                    at = kv + ((int64_t)page * c.page_stride +
+                               (int64_t)((int)t - in * c.page_size) * c.token_stride) *
+                                  C::kEsize;
+                    none = false;
                 } else {
                     bad = true;
                     holes = 1;
                 }
             }
-            places[(t - begin) & (C::kPlaces - 1)] = place;
+            places[(int)(t - begin) & (C::kPlaces - 1)] = at;
+            absent[(int)(t - begin) & (C::kPlaces - 1)] = none;
         }
     };
     auto look_up = [&](int t0) { return places[(t0 + mine - begin) & (C::kPlaces - 1)]; };
@@ -180,9 +186,8 @@ __global__ __launch_bounds__(256, 1) void latent_kernel(LatentAttendArgs a) {
     const char* from;
     uint32_t to_lds;
     // the loads of a tile are made ready, and then issued one by one
-    auto prepare = [&](int buf, int64_t place) __attribute__((always_inline)) {
-        from = (place >= 0 ? kv + place : reinterpret_cast<const char*>(kZeros)) + chunk_of;
-        absent[buf][mine] = place < 0;
+    auto prepare = [&](int buf, const char* place) __attribute__((always_inline)) {
+        from = place + chunk_of;
         to_lds = __builtin_amdgcn_readfirstlane(lds_address(tiles[buf] + wave * C::kGroup));
     };
     auto issue = [&](int i) __attribute__((always_inline)) {
@@ -213,7 +218,7 @@ __global__ __launch_bounds__(256, 1) void latent_kernel(LatentAttendArgs a) {
     // the order of requests was read from where the tiles go
     if (threadIdx.x == 0) risen[0] = risen[1] = holes = 0;
     __syncthreads();
-    int64_t place = start();
+    const char* place = start();
 
     // ---- queries of the pair's slots, operand B of every step
     int q_row[2], head[2], last[2];  // last: the position a slot sees last
@@ -242,10 +247,10 @@ __global__ __launch_bounds__(256, 1) void latent_kernel(LatentAttendArgs a) {
         }
     __builtin_amdgcn_sched_barrier(0);
     // Waited for here, not among the loads of a tile.  512 registers a lane are 256 for
-    // any use and 256 for products alone: half of the queries go among the latter.
+    // any use and 256 for products alone: most of the queries go among the latter.
 #pragma unroll
     for (int st = 0; st < C::kSteps; ++st)
-        if (2 * st < C::kSteps) asm volatile("" : "+v"(q[st][0]), "+v"(q[st][1]));
+        if (st < 4) asm volatile("" : "+v"(q[st][0]), "+v"(q[st][1]));
         else asm volatile("" : "+a"(q[st][0]), "+a"(q[st][1]));
 
     // The scale is taken as positive (products change their sign with it), so that the
@@ -318,7 +323,8 @@ __global__ __launch_bounds__(256, 1) void latent_kernel(LatentAttendArgs a) {
     // The products of the lane's four positions and two slots.  Between two matrix
     // instructions there is time for three others: the keys' reads, kAhead steps before
     // their products, and the first of the next tile's loads.
-    auto score = [&](int t0, int buf, float (&p)[2][4]) __attribute__((always_inline)) {
+    auto score = [&](int t0, int buf, float (&p)[2][4], auto behind)
+                     __attribute__((always_inline)) {
         const char* tile = tiles[buf];
         const int any_hole = holes;
         auto key = [&](int st) __attribute__((always_inline)) {
@@ -345,6 +351,7 @@ __global__ __launch_bounds__(256, 1) void latent_kernel(LatentAttendArgs a) {
             if (st + kAhead < C::kSteps) k8[st % kAhead] = key(st + kAhead);
             __builtin_amdgcn_sched_barrier(0);
         }
+        behind();  // while the last products are on their way
 #pragma unroll
         for (int sh = 0; sh < 2; ++sh)
 #pragma unroll
@@ -352,7 +359,7 @@ __global__ __launch_bounds__(256, 1) void latent_kernel(LatentAttendArgs a) {
         const bool edge = t0 + C::kTile > ctx;
         if (edge || __builtin_amdgcn_readfirstlane(any_hole) != 0) {
             const int first = half * 16 + 4 * g;
-            const uint32_t no = *reinterpret_cast<const uint32_t*>(&absent[buf][first]);
+            const uint32_t no = *reinterpret_cast<const uint32_t*>(&absent[(t0 - begin + first) & (C::kPlaces - 1)]);
             const uint32_t nan =
                 edge ? *reinterpret_cast<const uint32_t*>(&tainted[buf][first]) : 0;
 #pragma unroll
@@ -441,7 +448,7 @@ __global__ __launch_bounds__(256, 1) void latent_kernel(LatentAttendArgs a) {
             __syncthreads();
             enter(begin, 0);
             float p[2][4];
-            score(begin, 0, p);
+            score(begin, 0, p, [] {});
 #pragma unroll
             for (int i = C::kEarly; i < C::kLoads; ++i) issue(i);
             if (!again) {
@@ -472,23 +479,7 @@ __global__ __launch_bounds__(256, 1) void latent_kernel(LatentAttendArgs a) {
             const Weights other{weights[odd ^ 1][wave ^ 1][0][lane],
                                 weights[odd ^ 1][wave ^ 1][1][lane]};
             more = t0 < end;
-            float p[2][4];
-            if (more) {
-                enter(t0, buf);
-                score(t0, buf, p);
-                bool above = false;
-#pragma unroll
-                for (int sh = 0; sh < 2; ++sh)
-                    above |= fmaxf(fmaxf(p[sh][0], p[sh][1]), fmaxf(p[sh][2], p[sh][3])) > far[sh];
-                if (__ballot(above) != 0) risen[odd] = 1;
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) p[e >> 2][e & 3] = -kInf;
-            }
-            rose = !again && __builtin_amdgcn_readfirstlane(rose_before) != 0;
-            more = more && !rose;
             const char* tile = tiles[buf == 0 ? 2 : buf - 1];
-            uint4 words[2];
             // value operand i: dims 32 (i / 2) .., the wave's own 16 positions or the other's
             auto value = [&](int i) __attribute__((always_inline)) {
                 const char* at = tile + (i >> 2) * 1024;
@@ -504,14 +495,34 @@ __global__ __launch_bounds__(256, 1) void latent_kernel(LatentAttendArgs a) {
                 __builtin_memcpy(&w1, &x1, 8);
                 return as_bf16x8(w0.x, w0.y, w1.x, w1.y);
             };
+            constexpr int kAhead = 4;
+            bf16x8 v8[kAhead];
+            auto first_values = [&]() __attribute__((always_inline)) {
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i) v8[i] = value(i);
+                __builtin_amdgcn_sched_barrier(0);
+            };
+            float p[2][4];
+            if (more) {
+                enter(t0, buf);
+                score(t0, buf, p, first_values);
+                bool above = false;
+#pragma unroll
+                for (int sh = 0; sh < 2; ++sh)
+                    above |= fmaxf(fmaxf(p[sh][0], p[sh][1]), fmaxf(p[sh][2], p[sh][3])) > far[sh];
+                if (__ballot(above) != 0) risen[odd] = 1;
+            } else {
+                first_values();
+#pragma unroll
+                for (int e = 0; e < 8; ++e) p[e >> 2][e & 3] = -kInf;
+            }
+            rose = !again && __builtin_amdgcn_readfirstlane(rose_before) != 0;
+            more = more && !rose;
+            uint4 words[2];
             // Between the products the values' reads, kAhead operands ahead, this turn's
             // weights and the rest of the next tile's loads (in the last turn weights of 0,
             // and loads to where nothing is read any more).
-            constexpr int kAhead = 4, kProducts = 4 * C::kDims;
-            bf16x8 v8[kAhead];
-#pragma unroll
-            for (int i = 0; i < kAhead; ++i) v8[i] = value(i);
-            __builtin_amdgcn_sched_barrier(0);
+            constexpr int kProducts = 4 * C::kDims;
 #pragma unroll
             for (int k = 0; k < kProducts; ++k) {
                 const int i = k >> 1;
@@ -545,7 +556,7 @@ __global__ __launch_bounds__(256, 1) void latent_kernel(LatentAttendArgs a) {
             __syncthreads();
             enter(t0, buf);
             float p[2][4];
-            score(t0, buf, p);
+            score(t0, buf, p, [] {});
 #pragma unroll
             for (int i = C::kEarly; i < C::kLoads; ++i) issue(i);
 #pragma unroll
