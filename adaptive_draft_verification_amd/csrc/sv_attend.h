@@ -79,7 +79,7 @@ __device__ __forceinline__ void load_to_lds(const char* from, uint32_t to, int i
     asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\t"
                  "global_load_lds_dwordx4 %2, off offset:%3\n\ts_mov_b32 m0, %0"
                  : "=&s"(keep)
-                 : "s"(to - i * STEP), "v"(from), "i"(i * STEP)
+                 : "s"(__builtin_amdgcn_readfirstlane(to - i * STEP)), "v"(from), "i"(i * STEP)
                  : "memory");
 }
 

@@ -53,6 +53,12 @@ struct LatentAttendArgs {
 };
 hipError_t launch_latent_attend(const LatentAttendArgs& a, hipStream_t stream);
 
+// Positions of a part: whole tiles.
+inline __host__ __device__ int latent_part_len(int len, int parts, int part_min) {
+    const int even = ((len + parts - 1) / parts + 31) / 32 * 32;
+    return even > part_min ? even : part_min;
+}
+
 // How a call is cut into workgroups: by host-known sizes alone.
 struct LatentPlan {
     int slot_blocks;  // workgroups over a request's query slots, 64 each
@@ -66,9 +72,15 @@ struct LatentPlan {
         // as two positions' keys: four positions a slot keep that below the products'
         // time, and a workgroup has two tiles at least.
         const int64_t mine = slots < block ? slots : block;
-        part_min = (int)((4 * mine + 127) / 128 * 128);
+        part_min = (int)((4 * mine + 63) / 64 * 64);
+        // A CU holds one workgroup.  Few requests: as many as there are CUs, none twice.
+        // Many: twice as many, so that short ones make room for long ones.  Measured the
+        // one way and the other: 64 x 16 slots of 4000 positions 75 and 87 us, 2 x 1024 of
+        // 100,000 639 and 678; 256 x 16 of 1 .. 2000 113 and 94, 32 x up to 512 of 1 .. 4000
+        // (latent_dim 256) 143 and 110.
         const int64_t groups = (int64_t)n_req * slot_blocks;
-        const int64_t want = groups > 0 ? (512 + groups - 1) / groups : 1;
+        const int64_t want = groups < 1 ? 1 : groups <= 64 ? 256 / groups
+                                                           : (512 + groups - 1) / groups;
         const int64_t most = (capacity + part_min - 1) / part_min;
         const int64_t p = want < most ? want : most;
         parts = (int)(p < 1 ? 1 : p > 128 ? 128 : p);

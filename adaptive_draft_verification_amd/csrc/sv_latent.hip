@@ -143,7 +143,7 @@ __global__ __launch_bounds__(256, 1) void latent_kernel(LatentAttendArgs a) {
     const int slots = rows * a.n_heads - mb * C::kSlots;  // slots of this block
     if (slots <= 0) return;
     const int len = ctx + rows;
-    const int plen = part_len(len, a.parts, a.part_min);
+    const int plen = latent_part_len(len, a.parts, a.part_min);
     const int begin = part * plen, end = min(len, begin + plen);
     if (begin >= len) return;
     const bool whole = plen >= len;  // the request's only part
@@ -655,7 +655,7 @@ __global__ __launch_bounds__(256) void latent_join_kernel(LatentAttendArgs a) {
     if (lo < 0 || hi < lo || rows > a.k_max + 1 || hi > a.q_rows || row >= rows || ctx < 0 ||
         (int64_t)ctx + rows > (int64_t)a.max_pages * c.page_size)
         return;
-    const int len = ctx + rows, plen = part_len(len, a.parts, a.part_min);
+    const int len = ctx + rows, plen = latent_part_len(len, a.parts, a.part_min);
     if (plen >= len) return;
     const int n = (len + plen - 1) / plen;  // at most 128
     const int64_t rec = id * a.parts;

@@ -60,7 +60,7 @@ hipError_t launch_latent_attend(const LatentAttendArgs& a, hipStream_t) {
     const int64_t grid = (int64_t)a.n_req * a.slot_blocks * a.parts;
     EXPECT(grid > 0 && grid * 256 < ((int64_t)1 << 32));
     EXPECT(a.slot_blocks * 64 >= (a.k_max + 1) * a.n_heads);
-    EXPECT(a.parts >= 1 && a.parts <= 128 && a.part_min % 128 == 0 && a.part_min > 0);
+    EXPECT(a.parts >= 1 && a.parts <= 128 && a.part_min % 32 == 0 && a.part_min > 0);
     const size_t records = (size_t)a.n_req * (a.k_max + 1) * a.n_heads * a.parts;
     if (a.parts > 1) {
         EXPECT(inside(a.part_out, records * a.cache.latent_dim * 4, 16));
@@ -69,7 +69,7 @@ hipError_t launch_latent_attend(const LatentAttendArgs& a, hipStream_t) {
     const int64_t capacity = (int64_t)a.max_pages * a.cache.page_size;
     for (int64_t len : {(int64_t)1, capacity / 2, capacity})
         if (len > 0 && len < (1 << 30))
-            EXPECT((int64_t)part_len((int)len, a.parts, a.part_min) * a.parts >= len);
+            EXPECT((int64_t)latent_part_len((int)len, a.parts, a.part_min) * a.parts >= len);
     return hipErrorNotSupported;
 }
 hipError_t launch_cache_attend_shared(const SharedArgs& s, hipStream_t) {
