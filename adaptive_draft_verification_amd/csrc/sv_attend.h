@@ -64,6 +64,14 @@ __device__ __forceinline__ int2 e4m3_of(const uint4& w, float s) {
     return make_int2(lo, hi);
 }
 
+// 8 bytes of device memory: a pointer kept in LDS does not tell the compiler that it is
+// one, and a load that may be of LDS waits for that too.
+__device__ __forceinline__ uint2 load_global8(const char* p) {
+    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+    const u32x2 w = *(const __attribute__((address_space(1))) u32x2*)p;
+    return make_uint2(w[0], w[1]);
+}
+
 __device__ __forceinline__ uint32_t lds_address(const void* p) {
     return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char*)p;
 }

@@ -191,7 +191,7 @@ __global__ __launch_bounds__(256, 1) void latent_kernel(LatentAttendArgs a) {
         to_lds = __builtin_amdgcn_readfirstlane(lds_address(tiles[buf] + wave * C::kGroup));
     };
     auto issue = [&](int i) __attribute__((always_inline)) {
-        if constexpr (F8) raw[i] = *reinterpret_cast<const uint2*>(from + i * 64);
+        if constexpr (F8) raw[i] = load_global8(from + i * 64);
         else load_to_lds<128>(from, to_lds + i * 1024, i);
     };
     // the first tile's

@@ -336,7 +336,7 @@ __device__ __forceinline__ void prefix(const SharedArgs& s, int id,
                          __attribute__((always_inline)) {
             from += chunk_of;
             if constexpr (F8) {
-                raw[(keys ? 0 : C::kLoads) + i] = *reinterpret_cast<const uint2*>(from + i * 64);
+                raw[(keys ? 0 : C::kLoads) + i] = load_global8(from + i * 64);
             } else {
                 const uint32_t to =
                     __builtin_amdgcn_readfirstlane(lds_address(into + wave * C::kGroup));
