@@ -638,16 +638,19 @@ __global__ __launch_bounds__(256, 1) void latent_kernel(LatentAttendArgs a) {
             nothing ? -kInf : ((m_of - C::kHold) + log2f(l_of * exp2f(C::kHold))) * kLn2;
 }
 
-// Merges the parts of a (row, head), a wave each: lanes over the dims.
-template <int R, bool F8>
+// Merges the parts of a (row, head): W waves, lanes over the dims, wave w the parts w,
+// w + W, ..., four in flight; the waves' sums meet in LDS, in a fixed order.  Bound by the
+// latency of its loads, and with many rows by reading the parts.
+template <int R, bool F8, int W>
 __global__ __launch_bounds__(256) void latent_join_kernel(LatentAttendArgs a) {
     constexpr int E = R / kWave;
     constexpr float kHold = Latent<R, F8>::kHold;
     __shared__ float factors[4][128];
+    __shared__ float sums[W == 1 ? 1 : 4][R];
     const sv_latent_cache& c = a.cache;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, w0 = wave % W;
     const int per = (a.k_max + 1) * a.n_heads;
-    const int64_t id = (int64_t)blockIdx.x * 4 + wave;
+    const int64_t id = (int64_t)blockIdx.x * (4 / W) + wave / W;  // W = 4: of the workgroup
     if (id >= (int64_t)a.n_req * per) return;
     const int r = (int)(id / per), rest = (int)(id % per);
     const int row = rest / a.n_heads, head = rest % a.n_heads;
@@ -679,18 +682,29 @@ __global__ __launch_bounds__(256) void latent_join_kernel(LatentAttendArgs a) {
     float o[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] = 0.0f;
-    for (int p0 = 0; p0 < n; p0 += 4) {
+    for (int p0 = w0; p0 < n; p0 += 4 * W) {
         float x[4][E];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int e = 0; e < E; ++e) x[i][e] = po[(int64_t)min(p0 + i, n - 1) * R + e];
+            for (int e = 0; e < E; ++e) x[i][e] = po[(int64_t)min(p0 + i * W, n - 1) * R + e];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            if (p0 + i >= n) break;
-            const float f = factor[p0 + i];
+            if (p0 + i * W >= n) break;
+            const float f = factor[p0 + i * W];
 #pragma unroll
             for (int e = 0; e < E; ++e) o[e] += f * x[i][e];
+        }
+    }
+    if (W > 1) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) sums[wave][lane * E + e] = o[e];
+        __syncthreads();
+        if (w0 != 0) return;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const int i = lane * E + e;
+            o[e] = (sums[0][i] + sums[1][i]) + (sums[2][i] + sums[3][i]);
         }
     }
     const float kv_scale = F8 && c.scale != nullptr ? *c.scale : 1.0f;
@@ -713,7 +727,9 @@ hipError_t run_latent(const LatentAttendArgs& a, hipStream_t stream) {
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.parts == 1) return e;
     const int64_t total = (int64_t)a.n_req * (a.k_max + 1) * a.n_heads;
-    latent_join_kernel<R, F8><<<(unsigned)((total + 3) / 4), 256, 0, stream>>>(a);
+    // few: a workgroup each, so that all parts are read at once
+    if (total <= 2048) latent_join_kernel<R, F8, 4><<<(unsigned)total, 256, 0, stream>>>(a);
+    else latent_join_kernel<R, F8, 1><<<(unsigned)((total + 3) / 4), 256, 0, stream>>>(a);
     return hipGetLastError();
 }
 
