@@ -59,8 +59,10 @@ hipError_t launch_cache_attend_shared(const SharedArgs& a, hipStream_t stream);
 // How the prefixes' launch is cut into workgroups: by host-known sizes alone.
 struct SharedPlan {
     static constexpr int kSlots = 128, kTile = 32;
-    // A run is four tiles at least (a segment's start costs about as much), and long
-    // enough that a block has 64 segments at most.
+    // A run is four tiles at least (a segment's start, 7000 clocks or more, costs about as
+    // much), and long enough that a block has 64 segments at most.  Equal runs instead of
+    // parts of a length a block: 256 x 1 .. 8 rows behind 8192 positions 281 -> 218 us,
+    // since 576 workgroups took turns on 512 places.
     static constexpr int kRunMin = 4, kSegments = 64;
     int64_t blocks;  // blocks of query slots over all groups and kv heads, at most
     int chunks;      // workgroups
@@ -77,7 +79,9 @@ struct SharedPlan {
         const int64_t slots = (int64_t)n_req * (k_max + 1) * (n_heads / n_kv_heads);
         blocks = n_groups == 0 ? 0 : (slots / kSlots + n_groups) * n_kv_heads;
         // As many as are on the chip at once, fewer beside a lot of workgroups over own
-        // positions; no more than there are runs.
+        // positions; no more than there are runs.  256, 384 and 512: 256 x 1 .. 8 rows
+        // behind 8192 positions with up to 500 of their own 300, 295, 308 us, of 8 bits
+        // 292, 281, 285; 256 x 1 row with one of their own 72, 80, 83.
         const bool many = own.grid(n_req, n_kv_heads) >= 512;
         chunks = head_dim == 256 ? 256 : many ? 384 : 512;
         const double runs = (double)blocks * ((capacity + kTile - 1) / kTile) / kRunMin + 8;

@@ -1,6 +1,6 @@
 // Attention of a batch whose requests share prefixes (gfx950, wave64):
-// sv_cache_attend_shared.  Four launches: the groups laid out; every group's rows over
-// its prefix, as one long block of queries; every request's rows over its own
+// sv_cache_attend_shared.  Three launches: the groups laid out; every group's rows over
+// its prefix, as one long block of queries, and every request's rows over its own
 // positions (sv_cache_attend's kernel, from the prefix's end on); the join.
 #include <type_traits>
 
@@ -29,7 +29,7 @@ __device__ __forceinline__ int64_t wave_incl_sum64(int64_t v, int lane) {
 // Checks the groups and their requests, and counts the tiles: one workgroup, so that
 // the launches behind it only read.  KEEP: at most T requests; what is read more than
 // once is kept in LDS then, and one round trip to memory is left of six (2 requests
-// 5.2 -> XX us).
+// 5.2 -> 3.6 us).
 template <int T, bool KEEP>
 __global__ __launch_bounds__(T) void layout_kernel(SharedArgs s) {
     const AttendArgs& a = s.own;
@@ -170,7 +170,10 @@ __global__ __launch_bounds__(T) void layout_kernel(SharedArgs s) {
 //   LDS reads of 4 positions by 16 dims for each 16 lanes.
 // What bounds it: at 128 dims 24 products of 32 clocks a wave and tile, and on the same
 // issue port some 105 other instructions of 4 clocks (exp2 8), beside which a product
-// takes 8 (measured; one of 16 x 16 x 32, of half the work, as many).
+// takes 8 (measured; one of 16 x 16 x 32, of half the work, as many).  A tile takes a
+// wave 1950 clocks alone on its SIMD and two waves 2400: scores 280, their maxima 180,
+// products with the values 690, the rest waits for LDS, for the other waves and for the
+// loads' issue.  Other orders of the same instructions all came out within 3 %.
 // In LDS 8 positions by 8 chunks of 16 bytes are a KB, the chunk c of position x at
 // (c ^ swizzle(x)) of its 128 bytes.  LDS has 64 banks of 4 bytes: the chunk c of 16
 // neighbouring positions, and the chunks c and c ^ 1 of 8, lie in different ones.
@@ -642,9 +645,12 @@ __device__ __forceinline__ void prefix(const SharedArgs& s, int id,
 }
 
 // Both kinds of workgroups: products keep those over the prefixes busy, loads of keys
-// and values those over the requests' own positions, so that they share the CUs well.
-// 256 x 1..8 rows (32 heads over 8, dim 128) behind 8192 shared positions and up to 500
-// of their own: XX us, one launch after the other XX.
+// and values those over the requests' own positions, so that they share the CUs well,
+// and small calls wait for one launch less.  One launch, and one after the other: 2 x 1
+// row behind 512 positions 9.5 and 16.7 us, 48 x 1 .. 8 rows behind 2000 (8 bits) 25 and
+// 36, 256 x 1 .. 8 rows (32 heads over 8, dim 128) behind 8192, up to 500 of their own,
+// 274 and 311: 115 GFLOP over the prefix (173 with the weights' second terms, 630
+// TFLOP/s) beside 290 MB read, at a clock that falls below 2 GHz under it.
 template <int D, bool F8, int MT, bool PG16>
 __global__ __launch_bounds__(256, (Prefix<D, F8>::kOccupancy)) void shared_kernel(SharedArgs s) {
     using Own = Attend<D, F8, MT, PG16>;
@@ -811,7 +817,10 @@ __global__ __launch_bounds__(256) void shared_join_kernel(SharedArgs s) {
 template <int D, bool F8>
 void run_shared_join(const SharedArgs& s, hipStream_t stream) {
     const int64_t rows = (int64_t)s.own.n_req * (s.own.k_max + 1);
-    // Few rows: a workgroup a head, for parts read at once.  Many: fewer, longer waves.
+    // Few rows: a workgroup a head, so that all parts are read at once (16 rows of 32 heads,
+    // 64 parts, 14.9 -> 6.9 us; 384 of 16 heads, a few parts, 8.9 -> 14.2).  Many: two heads
+    // a wave (one, two, four: whole calls of 256 x 1 .. 8 rows 316, 313, 310 us, of 48 x
+    // 1 .. 8 rows 41.1, 41.7, 44.2).
     if (rows * s.own.n_heads <= 2048) {
         shared_join_kernel<D, F8, 4, 1><<<(unsigned)(rows * s.own.n_heads), 256, 0, stream>>>(s);
     } else {

@@ -42,8 +42,9 @@
  *    dev_error bit for them.  Both make calls synchronous and slow; neither
  *    changes any result.  sv_verify_noalloc honours SV_FORCE_SYNC only (its
  *    contract is to allocate nothing, host memory included), and so do the
- *    calls of truncated laws and of the paged cache (their kernels check
- *    every index themselves).
+ *    calls of truncated laws, of histories and adjusted logits, of the paged
+ *    cache and of the latent cache (their kernels check every index
+ *    themselves).
  */
 #ifndef LIBSPECVERIFY_H
 #define LIBSPECVERIFY_H
@@ -845,9 +846,9 @@ sv_status sv_cache_attend(const sv_cache* cache, const int32_t* page_table, int3
  * agree bit for bit.
  * ws:      sv_cache_attend_shared_workspace_bytes(...) bytes, 16-byte aligned,
  *          uninitialised.  Calls that overlap in time must not share it.
- * Launch: four kernels: one workgroup that lays out the groups; the prefixes, four
- * waves for each kv head, 128 query slots and part of the length; the requests' own
- * positions; the join.
+ * Launch: three kernels: one workgroup that lays out the groups; workgroups over
+ * equal runs of the prefixes (128 query slots of a kv head at a time) and over the
+ * requests' own positions; the join.
  * Errors: SV_ERR_NULL; SV_ERR_DTYPE; SV_ERR_SHAPE (also n_groups outside 0 ..
  * n_req); SV_ERR_VALUE (scale not finite); SV_ERR_WORKSPACE.
  */
@@ -922,14 +923,14 @@ sv_status sv_latent_append(const sv_latent_cache* cache, const int32_t* page_tab
  * as for sv_cache_attend.  A position behind the context (one of the step's own)
  * whose vector holds NaN or infinity makes NaN of the rows that see it and does
  * not touch the others.
- * Numerics: as for sv_cache_attend, except that values below 2^-86 may lose bits
- * and weights below 2^-86 of the largest may count as 0.  Repeated calls agree
+ * Numerics: as for sv_cache_attend, except that values below 2^-46 may lose bits
+ * and weights below 2^-62 of the largest may count as 0.  Repeated calls agree
  * bit for bit.
  * ws:      sv_latent_attend_workspace_bytes(...) bytes, 16-byte aligned (0: NULL
  *          will do), uninitialised.  Calls that overlap in time must not share it.
- * Launch: one kernel of four waves for each request, block of up to 128 query
- * slots (rows times heads; 64 where there are few) and part of the length; a
- * second one merges the parts if there are several.
+ * Launch: one kernel of four waves for each request, block of 64 query slots
+ * (rows times heads) and part of the length; a second one merges the parts if
+ * there are several.
  * Errors: SV_ERR_NULL; SV_ERR_DTYPE; SV_ERR_SHAPE (SV_MAX_ATTEND_SLOTS holds
  * here too); SV_ERR_VALUE (scale not finite); SV_ERR_WORKSPACE.
  */
