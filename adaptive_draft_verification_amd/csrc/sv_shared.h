@@ -82,7 +82,9 @@ struct SharedPlan {
         // positions; no more than there are runs.  256, 384 and 512: 256 x 1 .. 8 rows
         // behind 8192 positions with up to 500 of their own 300, 295, 308 us, of 8 bits
         // 292, 281, 285; 256 x 1 row with one of their own 72, 80, 83.
-        const bool many = own.grid(n_req, n_kv_heads) >= 512;
+        // (By the plan of two-byte caches: callers ask for the workspace without a type.)
+        const bool many = AttendPlan(n_req, k_max, n_heads, n_kv_heads, head_dim, 2, capacity)
+                              .grid(n_req, n_kv_heads) >= 512;
         chunks = head_dim == 256 ? 256 : many ? 384 : 512;
         const double runs = (double)blocks * ((capacity + kTile - 1) / kTile) / kRunMin + 8;
         if (runs < chunks) chunks = (int)runs & ~7;

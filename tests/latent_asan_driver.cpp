@@ -208,6 +208,22 @@ int main() {
                             }
         }
     }
+    // the size asked for does not know the cache's type: it has to do for either
+    for (const sv_dtype dt : {SV_BF16, SV_E4M3})
+        for (const int heads : {1, 8, 16})
+            for (const int k : {0, 3, 7})
+                for (int n = 1; n < 200; n += n < 20 ? 1 : 17)
+                    for (const int pages : {16, 128, 512, 4096}) {
+                        const sv_cache c{F, F, dt, 100, 16, 1, 64, 1024, 64, 64, nullptr, nullptr};
+                        const size_t b =
+                            sv_cache_attend_shared_workspace_bytes(n, n, k, heads, 1, 64, pages, 16);
+                        g_ws = reinterpret_cast<const char*>((uintptr_t)1 << 40);
+                        g_ws_bytes = b;
+                        EXPECT(sv_cache_attend_shared(&c, ci, pages, F, heads * 64, 1000, heads, ci,
+                                                      ci, n, k, ci, ci, n, 0.1f, F, heads * 64,
+                                                      nullptr, nullptr, const_cast<char*>(g_ws), b,
+                                                      nullptr) == SV_ERR_LAUNCH);
+                    }
     EXPECT(sv_latent_attend_workspace_bytes(2147483647, 64, 2147483647, 512, 2147483647,
                                             2147483647) == 0);
     EXPECT(sv_cache_attend_shared_workspace_bytes(2147483647, 2147483647, 64, 2147483647, 1, 64,
