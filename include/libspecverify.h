@@ -849,8 +849,9 @@ sv_status sv_cache_attend(const sv_cache* cache, const int32_t* page_table, int3
  * Launch: three kernels: one workgroup that lays out the groups; workgroups over
  * equal runs of the prefixes (128 query slots of a kv head at a time) and over the
  * requests' own positions; the join.
- * Errors: SV_ERR_NULL; SV_ERR_DTYPE; SV_ERR_SHAPE (also n_groups outside 0 ..
- * n_req); SV_ERR_VALUE (scale not finite); SV_ERR_WORKSPACE.
+ * Errors: SV_ERR_NULL; SV_ERR_DTYPE; SV_ERR_SHAPE (SV_MAX_ATTEND_SLOTS, less 512,
+ * holds here too; n_groups outside 0 .. n_req); SV_ERR_VALUE (scale not finite);
+ * SV_ERR_WORKSPACE.
  */
 size_t sv_cache_attend_shared_workspace_bytes(int32_t n_req, int32_t n_groups, int32_t k_max,
                                               int32_t n_heads, int32_t n_kv_heads,

@@ -183,6 +183,13 @@ def test_a_prefix_in_parts(dtype, dim):
     Batch(4, [(20000, [(1, 300)]), (1100, [(3, 1)])], 2, 1, dim, 32, dtype, extra=0).device().check()
 
 
+@pytest.mark.parametrize("dtype", [BF, F8])
+def test_small_calls_with_long_tables(dtype):
+    """The workspace does not depend on the type; few slots, a table of 8192 positions."""
+    Batch(24, [(1000, [(2, i)]) for i in range(8)], 1, 1, 64, 16, dtype, k_max=3,
+          extra=448).device().check()
+
+
 def test_a_part_longer_than_the_places_kept():
     """Room for many rows, so few parts, each of more than 1024 positions."""
     Batch(5, [(4100, [(1 + i % 2, i) for i in range(11)])], 64, 8, 64, 64, extra=0,
