@@ -634,7 +634,7 @@ sv_status sv_history_clear(const sv_history* history, const int32_t* slots, int3
  *          [0, n_slots) too (SV_DEV_BAD_SLOT).
  * slots:   as above; rows of one slot in one call add up.
  * in_prompt: 0: emitted (each occurrence counts), else: the prompt's.
- * Launch: one kernel, one thread an id.
+ * Launch: one kernel, one thread an id, or four ids where there are many.
  * Errors: SV_ERR_NULL; SV_ERR_SHAPE.
  */
 sv_status sv_history_add(const sv_history* history, const int32_t* slots, const int32_t* tokens,
