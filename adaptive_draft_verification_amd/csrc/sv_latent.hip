@@ -402,7 +402,8 @@ __global__ __launch_bounds__(256, 1) void latent_kernel(LatentAttendArgs a) {
         for (int sh = 0; sh < 2; ++sh) {
             m[sh] = top[sh] * scale + C::kHold;
             mu[sh] = m[sh] == -kInf ? 0.0f : m[sh];
-            far[sh] = top[sh] + C::kSlack / scale;
+            // (-inf also where a scale near zero makes the distance infinite)
+            far[sh] = top[sh] == -kInf ? -kInf : top[sh] + C::kSlack / scale;
         }
     };
     // Weights go into the product as two bf16 terms, the upper half of the fp32 weight
