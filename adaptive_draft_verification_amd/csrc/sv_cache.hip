@@ -162,8 +162,10 @@ void run_join(const AttendArgs& a, hipStream_t stream) {
 template <int D, bool F8, int MT, bool PG16>
 __global__ __launch_bounds__(256, (Attend<D, F8, MT, PG16>::kOccupancy))
 void attend_kernel(AttendArgs a) {
+    constexpr bool OWN = false;
+    const unsigned block = blockIdx.x, blocks = gridDim.x;
     __shared__ typename Attend<D, F8, MT, PG16>::Smem sm;
-    attend<D, F8, MT, PG16, false>(a, blockIdx.x, gridDim.x, sm);
+#include "sv_attend_body.h"
 }
 
 template <int D, bool F8, int MT>

@@ -662,7 +662,7 @@ __global__ __launch_bounds__(256, (Prefix<D, F8>::kOccupancy)) void shared_kerne
     if ((int)blockIdx.x < s.chunks)
         prefix<D, F8>(s, blockIdx.x, sm.prefix);
     else
-        attend<D, F8, MT, PG16, true>(s.own, blockIdx.x - s.chunks, gridDim.x - s.chunks, sm.own);
+        attend_own<D, F8, MT, PG16>(s.own, blockIdx.x - s.chunks, gridDim.x - s.chunks, sm.own);
 }
 
 // --------------------------------------------------------------------- join
