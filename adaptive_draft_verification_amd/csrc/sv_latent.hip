@@ -163,7 +163,6 @@ __global__ __launch_bounds__(256, 1) void latent_kernel(LatentAttendArgs a) {
     // The places of `n` positions from `from` on, into LDS: kPlaces at first, then half
     // as many at a time (a wait for a page id in registers would be a wait for the tile
     // that is on its way).  None: after the end, or on a page that is not there.
-    bool bad = false;
     auto fetch_places = [&](int from, int n) __attribute__((always_inline)) {
         for (int i = threadIdx.x; i < n; i += 256) {
             const int64_t t = (int64_t)from + i;
@@ -180,7 +179,6 @@ __global__ __launch_bounds__(256, 1) void latent_kernel(LatentAttendArgs a) {
                                   C::kEsize;
                     none = false;
                 } else {
-                    bad = true;
                     holes = 1;
                 }
             }
@@ -577,7 +575,9 @@ __global__ __launch_bounds__(256, 1) void latent_kernel(LatentAttendArgs a) {
         refer(mx);
         __syncthreads();
     }
-    if (bad && lane == 0) raise_error(a.dev_error, SV_DEV_BAD_PAGE);
+
+    // whichever thread found it: barriers lie between
+    if (threadIdx.x == 0 && holes != 0) raise_error(a.dev_error, SV_DEV_BAD_PAGE);
 
     // sums over the positions of a slot's lanes, and of the other wave
 #pragma unroll
