@@ -58,9 +58,10 @@ __global__ void append_kernel(AppendArgs a) {
 
 // ------------------------------------------------------------------- attend
 
-// Merges the parts of a (row, head): W waves, wave w the parts w, w + W, ...
-// (eight loads in flight each), lanes over the dims; the waves' sums meet in
-// LDS, in a fixed order.  A request of one part wrote its outputs itself.
+// Merges the parts of a (row, head): W waves, wave w the parts w, w + W, ..., lanes
+// over the dims; the waves' sums meet in LDS, in a fixed order.  hipcc puts a part's load
+// behind the test that ends the sum, so that a wave has one on its way at a time.  A
+// request of one part wrote its outputs itself.
 template <int D, bool F8, int W>
 __global__ __launch_bounds__(256) void join_kernel(AttendArgs a) {
     constexpr int E = D / 64, kEach = 4 / W;  // (row, head)s a workgroup takes at once
@@ -150,7 +151,7 @@ __global__ __launch_bounds__(256) void join_kernel(AttendArgs a) {
 template <int D, bool F8>
 void run_join(const AttendArgs& a, hipStream_t stream) {
     const int64_t total = (int64_t)a.n_req * (a.k_max + 1) * a.n_heads;
-    // up to 16 parts one wave keeps them all in flight in two goes
+    // up to 16 parts are one wave's
     if (a.parts <= 16) {
         const int64_t grid = (total + 3) / 4;
         join_kernel<D, F8, 1><<<(unsigned)(grid < 4096 ? grid : 4096), 256, 0, stream>>>(a);

@@ -75,9 +75,11 @@ struct LatentPlan {
         part_min = (int)((4 * mine + 63) / 64 * 64);
         // A CU holds one workgroup.  Few requests: as many as there are CUs, none twice.
         // Many: twice as many, so that short ones make room for long ones.  Measured the
-        // one way and the other: 64 x 16 slots of 4000 positions 75 and 87 us, 2 x 1024 of
-        // 100,000 639 and 678; 256 x 16 of 1 .. 2000 113 and 94, 32 x up to 512 of 1 .. 4000
-        // (latent_dim 256) 143 and 110.
+        // one way and the other, n x 64 slots of 0 .. 4000 positions: n = 48 62 and 72 us, 64 70
+        // and 90, 96 121 and 118, 128 135 and 139, 160 219 and 161, 192 222 and 187, 256 231 and
+        // 200; n x 16 slots: 96 108 and 92, 192 219 and 165.  Where all have 4000 the first
+        // is the better one up to 256 (64 93 and 116, 128 162 and 186, 192 250 and 307), but
+        // lengths are not known here, and a server's differ.
         const int64_t groups = (int64_t)n_req * slot_blocks;
         const int64_t want = groups < 1 ? 1 : groups <= 64 ? 256 / groups
                                                            : (512 + groups - 1) / groups;

@@ -62,6 +62,9 @@ __global__ void latent_append_kernel(LatentAppendArgs a) {
 // of 16 positions over all dims and half of the output's dims over all 32 positions,
 // so that the accumulators are R / 4 registers a lane beside R / 4 + 16 of queries;
 // the weights of the other 16 positions come from the other wave through LDS.
+// At 512 dims a few values that only the ends of a part need do not fit beside them and go
+// to scratch (16 bytes a lane; 56 with 8-bit tiles, which pass registers): none is read
+// back within a turn.
 // Operands:
 //   S^T = K Q^T, v_mfma_f32_16x16x32_bf16: A holds 16 positions (lane % 16) by 32 dims
 //   (8 for each g = lane / 16), B 16 slots by the same dims, so a lane ends with the
@@ -81,7 +84,7 @@ __global__ void latent_append_kernel(LatentAppendArgs a) {
 // Bound by the products and what stands between them: a turn of 32 positions takes a wave
 // some 3500 clocks, 1600 of them products (scores 1080 with their keys' way from LDS,
 // values 1250, the next tile's addresses, maxima, exchange and barriers the rest).  128
-// x 1 .. 8 rows of 128 heads on up to 4096 positions 709 us, 2 x 8 rows on 100,000 620 us:
+// x 1 .. 8 rows of 128 heads on up to 4096 positions 718 us, 2 x 8 rows on 100,000 620 us:
 // 720 TFLOP/s, 1060 with the weights' second terms, where a large product of this card's
 // library reaches 1230.
 
@@ -647,8 +650,9 @@ __global__ __launch_bounds__(256, 1) void latent_kernel(LatentAttendArgs a) {
 }
 
 // Merges the parts of a (row, head): W waves, lanes over the dims, wave w the parts w,
-// w + W, ..., four in flight; the waves' sums meet in LDS, in a fixed order.  Bound by the
-// latency of its loads, and with many rows by reading the parts.
+// w + W, ...; the waves' sums meet in LDS, in a fixed order.  Bound by the latency of its
+// loads: hipcc puts a part's behind the test that ends the sum, so that a wave has one on
+// its way at a time (64 x 128 heads, 64 MB of parts: 13 us).
 template <int R, bool F8, int W>
 __global__ __launch_bounds__(256) void latent_join_kernel(LatentAttendArgs a) {
     constexpr int E = R / kWave;
@@ -735,7 +739,7 @@ hipError_t run_latent(const LatentAttendArgs& a, hipStream_t stream) {
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.parts == 1) return e;
     const int64_t total = (int64_t)a.n_req * (a.k_max + 1) * a.n_heads;
-    // few: a workgroup each, so that all parts are read at once
+    // few: a workgroup each, so that four parts are read at once
     if (total <= 2048) latent_join_kernel<R, F8, 4><<<(unsigned)total, 256, 0, stream>>>(a);
     else latent_join_kernel<R, F8, 1><<<(unsigned)((total + 3) / 4), 256, 0, stream>>>(a);
     return hipGetLastError();

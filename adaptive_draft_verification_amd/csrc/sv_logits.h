@@ -52,8 +52,8 @@ hipError_t launch_adjust(const AdjustArgs& a, hipStream_t stream);
 constexpr int kAdjustTile = 512;         // ids
 constexpr int kAdjustPartBytes = 32768;  // of a row, at most
 
-// Workgroups a row: the power of two that makes some 8192 of them, with 4096 ids
-// each at least, and no more ids than LDS holds.
+// Workgroups a row: the power of two that makes some 8192 of them, with more than 2048
+// ids each (a row of 4096 or fewer is one's), and no more ids than LDS holds.
 inline int adjust_parts(int n_rows, int vocab, int esize) {
     const int tiles = (vocab + kAdjustTile - 1) / kAdjustTile;
     int p = 1;

@@ -87,8 +87,10 @@ __global__ __launch_bounds__(256) void add_kernel(HistoryAddArgs a, int blocks_a
 // ------------------------------------------------------------------- adjust
 //
 // Bound by the rows, read and written once: 256 x 1 .. 8 rows of 129,280 bf16 with
-// penalties, biases and masks 151 us (3.9 TB/s; the rows alone copied 113), in place 105,
-// 1 row of 128,255 fp32 5.6.  One workgroup takes a part of a row.
+// penalties, biases and masks 156 us (4.0 TB/s; the rows alone copied 114), in place 105,
+// fp32 269 (231) and 163, 1 row of 128,255 fp32 5.4.  That is with 2560 ids said by each
+// request, whose list every workgroup of its rows reads; with 274 of them 123 and 43, with
+// 14,200 324 and 253.  One workgroup takes a part of a row.
 // Out of place (kStaged) the part goes through LDS: the few ids that the request
 // has said, drafted or biased are adjusted there, and the part leaves with the mask
 // applied.  In place only the masked vectors and those few ids are touched.  Each of

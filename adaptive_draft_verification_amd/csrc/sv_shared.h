@@ -78,10 +78,15 @@ struct SharedPlan {
         }
         const int64_t slots = (int64_t)n_req * (k_max + 1) * (n_heads / n_kv_heads);
         blocks = n_groups == 0 ? 0 : (slots / kSlots + n_groups) * n_kv_heads;
-        // As many as are on the chip at once, fewer beside a lot of workgroups over own
-        // positions; no more than there are runs.  256, 384 and 512: 256 x 1 .. 8 rows
-        // behind 8192 positions with up to 500 of their own 300, 295, 308 us, of 8 bits
-        // 292, 281, 285; 256 x 1 row with one of their own 72, 80, 83.
+        // Two for each CU (one at dim 256, whose workgroups need all registers of a SIMD;
+        // three would fit at dim 64 in 8 bits), fewer beside a lot of workgroups over own
+        // positions; no more than there are runs.  256, 384, 512 and 768: 256 x 1 .. 8 rows
+        // behind 8192 positions with up to 500 of their own 327, 314, 327, 326 us, of 8 bits
+        // 329, 327, 318, 320; 256 x 1 row with one of their own 70, 77, 84, 87, with up to
+        // 500 126, 134, 146, 153; 48 x 1 .. 8 of dim 64 in 8 bits 38.0, 39.2, 41.9, 44.4; 64 x
+        // 1 .. 4 in eight groups, few workgroups over own positions, 29.8, 30.6, 31.8, 31.4.
+        // So 384 is right where products take most of the call, and costs up to a tenth
+        // where a request has one row.
         // (By the plan of two-byte caches: callers ask for the workspace without a type.)
         const bool many = AttendPlan(n_req, k_max, n_heads, n_kv_heads, head_dim, 2, capacity)
                               .grid(n_req, n_kv_heads) >= 512;

@@ -668,9 +668,11 @@ __global__ __launch_bounds__(256, (Prefix<D, F8>::kOccupancy)) void shared_kerne
 // --------------------------------------------------------------------- join
 
 // Merges the parts of a row's heads, those over the prefix first, in a fixed order.  W
-// waves take H neighbouring heads: lanes over the dims, wave w the parts w, w + W, ...,
-// four of each head in flight; the waves' sums meet in LDS.  Bound by the latency of
-// the loads that lead to the parts, and with many rows by reading them.
+// waves take H neighbouring heads: lanes over the dims, wave w the parts w, w + W, ...; the
+// waves' sums meet in LDS.  Bound by the latency of its loads, first of those that lead to
+// the parts, then of the parts themselves: hipcc puts a part's load behind the test that
+// ends the sum, so that of the first (or only) head one is on its way at a time, of the
+// second four (256 x 1 .. 8 rows, 32 heads of 128: 37 us for 62 MB of parts).
 template <int D, bool F8, int W, int H>
 __global__ __launch_bounds__(256) void shared_join_kernel(SharedArgs s) {
     constexpr int E = D / kWave;
@@ -817,7 +819,7 @@ __global__ __launch_bounds__(256) void shared_join_kernel(SharedArgs s) {
 template <int D, bool F8>
 void run_shared_join(const SharedArgs& s, hipStream_t stream) {
     const int64_t rows = (int64_t)s.own.n_req * (s.own.k_max + 1);
-    // Few rows: a workgroup a head, so that all parts are read at once (16 rows of 32 heads,
+    // Few rows: a workgroup a head, so that four parts are read at once (16 rows of 32 heads,
     // 64 parts, 14.9 -> 6.9 us; 384 of 16 heads, a few parts, 8.9 -> 14.2).  Many: two heads
     // a wave (one, two, four: whole calls of 256 x 1 .. 8 rows 316, 313, 310 us, of 48 x
     // 1 .. 8 rows 41.1, 41.7, 44.2).

@@ -602,7 +602,8 @@ sv_status sv_verify_truncated(const void* target_logits, int64_t target_ld, int6
  * n_seen:  [n_slots] int32: ids whose count is not 0.
  * seen:    [n_slots, cap] int32: those ids, each once, in no order.  Where there
  *          are more than cap of them, calls read the slot's whole row of counts
- *          instead: right at any cap, fast while the ids fit.
+ *          instead: right at any cap, and faster while the ids fit and are few
+ *          beside vocab.
  * Start with zeroed counts and n_seen.  Counts hold 2^30 - 1 emissions.
  */
 typedef struct {
@@ -700,7 +701,8 @@ typedef struct {
  * penalty or a bias that is not finite (-inf biases are), a bias range or a
  * mask that is not there (SV_DEV_BAD_PARAM) is filled with NaN, so that a draw
  * from it is refused.
- * Launch: one kernel, a workgroup for each 4096 ids or more of a row (up to 32 KB).
+ * Launch: one kernel, a workgroup for more than 2048 ids of a row (up to 32 KB of it).
+ * Each reads its request's whole list of seen ids.
  * Errors: SV_ERR_NULL; SV_ERR_DTYPE; SV_ERR_SHAPE (also a history of another
  * vocab).
  */

@@ -2,8 +2,9 @@
 
 FOS page, section "속도, 메모리, 정확도에 주는 영향", row 정확도: the output law is the
 target's; a request served with penalties, biases or a grammar has the adjusted
-law as its target.  The pages do not spell the adjustments out; these are the
-usual serving ones, id by id, the drafts before a row counted as said.  fp64.
+law as its target.  The pages do not spell the adjustments out: their form and
+order (repetition, frequency and presence, bias, mask) are this library's choice, id
+by id, the drafts before a row counted as said.  fp64.
 """
 
 import numpy as np
