@@ -7,14 +7,17 @@
 #include <cstdint>
 
 #include "libspecverify.h"
+#include "sv_cache_check.h"
 #include "sv_latent.h"
 #include "sv_launch.h"
 
 namespace {
 
-hipStream_t as_stream(void* s) { return static_cast<hipStream_t>(s); }
+using sv::aligned16;
+using sv::log2_exact;
+using sv::row_layout_ok;
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+hipStream_t as_stream(void* s) { return static_cast<hipStream_t>(s); }
 
 bool latent_dim_ok(int32_t d) { return d == 256 || d == 512; }
 
@@ -33,16 +36,6 @@ sv_status check_cache(const sv_latent_cache* c, int32_t max_pages) {
         return SV_ERR_SHAPE;
     if (!aligned16(c->kv)) return SV_ERR_SHAPE;
     return SV_OK;
-}
-
-int log2_exact(int32_t n) {
-    for (int i = 0; i < 31; ++i)
-        if (n == (int32_t)1 << i) return i;
-    return -1;
-}
-
-bool row_layout_ok(const void* p, int64_t ld, int64_t width) {
-    return ld >= width && ld % 8 == 0 && aligned16(p);
 }
 
 sv_status check_attend_sizes(int32_t n_req, int32_t k_max, int32_t n_heads, int32_t latent_dim,
