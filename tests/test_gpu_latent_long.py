@@ -84,3 +84,38 @@ def test_sums_that_start_again(dtype, rank):
         # the kernel starts again from 2^32 on
         assert (s[-1] - s[:32].max()) / np.log(2.0) > 40
     b.device().check()
+
+
+@pytest.mark.parametrize("dtype", [BF, F8])
+def test_offsets_past_32_bits(dtype):
+    """A cache of more than 2^32 values, the pages in use at its ends: written and attended to."""
+    pages, page, rank = 120000, 64, 512
+    b = Batch(45, [2, 1], [130, 200], 5, rank, page, dtype, extra=0).device()
+    kv = torch.zeros(pages, page, rank + 64, dtype=dtype, device="cuda")
+    table = b.table.clone()
+    for i, p in enumerate(b.table.unique().tolist()):
+        to = pages - 1 - i if i % 2 else i
+        kv[to] = b.kv[p].cuda()
+        table[b.table == p] = to
+    assert int(table.max()) * page * (rank + 64) > 2 ** 32
+    cache = sv.LatentCache(kv, rank, b.cache.scale)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    # the first row of either request appended anew, as the same values
+    at = [(int(table[r, c // page]), c % page) for r, c in enumerate((130, 200))]
+    s = 1.0 if b.kv_scale is None else b.kv_scale.item()
+    rows = torch.stack([kv[p, j].float() for p, j in at])
+    for p, j in at:
+        kv[p, j] = 0
+    sv.sv_latent_append(cache, table.cuda(), (rows * s).to(BF)[:, :rank], (rows * s).to(BF)[:, rank:],
+                        i32([0, 1]), i32([0, 0]), b.ctx.cuda())
+    back = torch.stack([kv[p, j].float() for p, j in at])
+    # bf16 of the product (2^-8), then e4m3 (2^-4) of it: one step of e4m3 at most
+    assert bool(((back - rows).abs() <= rows.abs() * (0 if dtype == BF else 2.0 ** -3)).all())
+    for (p, j), row in zip(at, rows):
+        kv[p, j] = row.to(dtype)
+    b.cache, b.table, small = cache, table, b.table
+    out, lse, err = b.attend()
+    b.cache, b.table = sv.LatentCache(b.kvd, rank, b.cache.scale), small
+    want, want_lse, _ = b.attend()
+    assert err == 0 and torch.equal(out, want) and torch.equal(lse, want_lse)
+    b.check()
